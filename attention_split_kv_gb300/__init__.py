@@ -21,7 +21,8 @@ __all__ = [
     "attn_version", "attn_last_error", "attn_decode_workspace_size", "attn_decode",
     "attn_decode_ring", "attn_decode_ex", "attn_decode_tiered", "attn_decode_tiered_workspace_size",
     "attn_decode_noalloc", "attn_prefill", "attn_prefill_paged", "attn_decode_validate", "attn_device_status",
-    "attn_testing_set_waits", "decode", "decode_tiered", "prefill", "prefill_paged",
+    "attn_testing_set_waits", "attn_prefill_paged_ex", "attn_prefill_paged_workspace_size", "attn_append",
+    "attn_kv_read", "decode", "decode_tiered", "prefill", "prefill_paged", "append", "kv_read",
 ]
 
 ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED, ATTN_ECUDA, ATTN_EBOUNDS, ATTN_ETIMEOUT = range(6)
@@ -38,7 +39,8 @@ _lib = None
 exported_symbols = ("attn_version", "attn_last_error", "attn_decode_workspace_size", "attn_decode",
                     "attn_decode_ring", "attn_decode_ex", "attn_decode_tiered", "attn_decode_tiered_workspace_size",
                     "attn_decode_noalloc", "attn_prefill", "attn_prefill_paged", "attn_decode_validate",
-                    "attn_device_status", "attn_testing_set_waits")
+                    "attn_device_status", "attn_testing_set_waits", "attn_prefill_paged_ex",
+                    "attn_prefill_paged_workspace_size", "attn_append", "attn_kv_read")
 
 
 class AttnLibraryMissing(RuntimeError):
@@ -91,6 +93,17 @@ def load():
     lib.attn_prefill.restype = I
     lib.attn_prefill_paged.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, F, P, P, P]
     lib.attn_prefill_paged.restype = I
+    LL = ctypes.c_longlong
+    lib.attn_prefill_paged_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.attn_prefill_paged_workspace_size.restype = SZ
+    lib.attn_prefill_paged_ex.argtypes = [P, P, P, P, P, P, I, I, I, P, P, I, I, I, I, I, I, I, I, F, F, P, P, P, SZ,
+                                          P]
+    lib.attn_prefill_paged_ex.restype = I
+    lib.attn_append.argtypes = [P, P, P, I, LL, LL, LL, P, P, F, F, P, P, I, I, I, P, P, P, P, P, I, I, I, I, I, P, P,
+                                I, I, I, I, I, I, P, I, P]
+    lib.attn_append.restype = I
+    lib.attn_kv_read.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, I, I, I, I, I, P, P, I, P]
+    lib.attn_kv_read.restype = I
     lib.attn_decode_validate.argtypes = [P, P, I, I, I, I, I, ctypes.POINTER(ctypes.c_int), P]
     lib.attn_decode_validate.restype = I
     lib.attn_device_status.argtypes = [P]
@@ -317,12 +330,118 @@ def attn_prefill_paged(q, k_cache, v_cache, q_start, kv_len, page_table, page_si
                                      _stream(stream)))
 
 
-def prefill_paged(case, out=None, lse_out=None, stream=None):
-    """attn_prefill_paged on a ChunkCase-like object (tensors already on the GPU)."""
+def attn_prefill_paged_workspace_size(batch, max_q, n_heads, n_kv_heads, head_dim, kv_dtype) -> int:
+    return int(load().attn_prefill_paged_workspace_size(batch, max_q, n_heads, n_kv_heads, head_dim, kv_dtype))
+
+
+def attn_prefill_paged_ex(q, k_cache, v_cache, q_start, kv_len, page_table, page_size, max_pages, n_pages, k_scales,
+                          v_scales, kv_dtype, batch, total_q, max_q, n_heads, n_kv_heads, head_dim, window, softcap,
+                          scale, out, lse_out, workspace, workspace_bytes, stream=None) -> None:
+    _check(load().attn_prefill_paged_ex(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(q_start), _ptr(kv_len),
+                                        _ptr(page_table), int(page_size), int(max_pages), int(n_pages),
+                                        _ptr(k_scales), _ptr(v_scales), int(kv_dtype), int(batch), int(total_q),
+                                        int(max_q), int(n_heads), int(n_kv_heads), int(head_dim), int(window),
+                                        float(softcap), float(scale), _ptr(out), _ptr(lse_out), _ptr(workspace),
+                                        int(workspace_bytes), _stream(stream)))
+
+
+def attn_append(q, k, v, in_dtype, q_stride, k_stride, v_stride, q_norm, k_norm, norm_eps, norm_offset, rope_cos,
+                rope_sin, rope_positions, rope_dim, rope_interleaved, q_start, kv_len, k_cache, v_cache, page_table,
+                page_size, max_pages, n_pages, max_kv, ring_size, k_scales, v_scales, kv_dtype, batch, total_q,
+                n_heads, n_kv_heads, head_dim, q_out, q_out_dtype, stream=None) -> None:
+    _check(load().attn_append(_ptr(q), _ptr(k), _ptr(v), int(in_dtype), int(q_stride), int(k_stride), int(v_stride),
+                              _ptr(q_norm), _ptr(k_norm), float(norm_eps), float(norm_offset), _ptr(rope_cos),
+                              _ptr(rope_sin), int(rope_positions), int(rope_dim), int(bool(rope_interleaved)),
+                              _ptr(q_start), _ptr(kv_len), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
+                              int(page_size), int(max_pages), int(n_pages), int(max_kv), int(ring_size),
+                              _ptr(k_scales), _ptr(v_scales), int(kv_dtype), int(batch), int(total_q), int(n_heads),
+                              int(n_kv_heads), int(head_dim), _ptr(q_out), int(q_out_dtype), _stream(stream)))
+
+
+def attn_kv_read(k_cache, v_cache, kv_len, first, out_start, page_table, page_size, max_pages, n_pages, max_kv,
+                 ring_size, k_scales, v_scales, kv_dtype, batch, total, n_kv_heads, head_dim, k_out, v_out, out_dtype,
+                 stream=None) -> None:
+    _check(load().attn_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(kv_len), _ptr(first), _ptr(out_start),
+                               _ptr(page_table), int(page_size), int(max_pages), int(n_pages), int(max_kv),
+                               int(ring_size), _ptr(k_scales), _ptr(v_scales), int(kv_dtype), int(batch), int(total),
+                               int(n_kv_heads), int(head_dim), _ptr(k_out), _ptr(v_out), int(out_dtype),
+                               _stream(stream)))
+
+
+def prefill_paged(case, out=None, lse_out=None, stream=None, workspace=None):
+    """attn_prefill_paged on a ChunkCase-like object (tensors already on the GPU);
+    attn_prefill_paged_ex over int8 pages when its cache holds int8 codes."""
     import torch
     if out is None:
         out = torch.empty_like(case.q)
+    if case.k.dtype == torch.int8:
+        if workspace is None:
+            size = attn_prefill_paged_workspace_size(case.batch, case.max_q, case.n_heads, case.n_kv_heads,
+                                                     case.head_dim, ATTN_KV_INT8)
+            if size == 0:
+                raise AttnError(ATTN_EINVAL, "invalid sizes for the chunked prefill workspace")
+            workspace = torch.empty(size, dtype=torch.uint8, device=case.q.device)
+        attn_prefill_paged_ex(case.q, case.k, case.v, case.q_start, case.kv_len, case.page_table, case.page_size,
+                              case.max_pages, int(case.k.shape[0]), case.k_scales, case.v_scales, ATTN_KV_INT8,
+                              case.batch, case.total_q, case.max_q, case.n_heads, case.n_kv_heads, case.head_dim,
+                              case.window, case.softcap, case.scale, out, lse_out, workspace, workspace.numel(),
+                              stream)
+        return out
     attn_prefill_paged(case.q, case.k, case.v, case.q_start, case.kv_len, case.page_table, case.page_size,
                        case.max_pages, int(case.k.shape[0]), case.batch, case.total_q, case.max_q, case.n_heads,
                        case.n_kv_heads, case.head_dim, case.window, case.softcap, case.scale, out, lse_out, stream)
     return out
+
+
+def _cache_args(case):
+    """page_size, max_pages, n_pages, max_kv and ring_size of a DecodeCase- or ChunkCase-like cache."""
+    ring = int(getattr(case, "ring", 0) or 0)
+    if case.page_table is not None:
+        return int(case.page_size), int(case.max_pages), int(case.k.shape[0]), 0, 0
+    return 0, 0, 0, 0 if ring else int(case.k.shape[1]), ring
+
+
+def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_eps=1e-6, norm_offset=0.0,
+           rope_cos=None, rope_sin=None, rope_interleaved=False, q_out=None, stream=None):
+    """attn_append of packed token rows (q [T, Hq, D] or None; k, v [T, Hkv, D], f16
+    or f32, the heads of a token together) to the cache that a DecodeCase- or
+    ChunkCase-like object holds; ``kv_len`` (default: the case's) counts each
+    sequence's tokens with the new ones.  Returns q_out (f16 unless given)."""
+    import torch
+
+    def stride(x):
+        if x is None:
+            return 0
+        if x.dtype != k.dtype or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+            raise AttnError(ATTN_EINVAL, "q, k and v rows must have one type and their heads side by side")
+        return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+    int8 = case.k.dtype == torch.int8
+    P, max_pages, n_pages, max_kv, ring = _cache_args(case)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+    rows = 0 if rope_cos is None else rope_cos.shape[0]
+    rot = 0 if rope_cos is None else 2 * rope_cos.shape[1]
+    attn_append(q, k, v, _dtype_of(k), stride(q), stride(k), stride(v), q_norm, k_norm, norm_eps, norm_offset,
+                rope_cos, rope_sin, rows, rot, rope_interleaved, q_start, case.kv_len if kv_len is None else kv_len,
+                case.k, case.v, case.page_table, P, max_pages, n_pages, max_kv, ring,
+                case.k_scales if int8 else None, case.v_scales if int8 else None,
+                ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, k.shape[0], 0 if q is None else q.shape[1],
+                k.shape[1], k.shape[2], q_out, ATTN_F16 if q_out is None else _dtype_of(q_out), stream)
+    return q_out
+
+
+def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stream=None):
+    """attn_kv_read of a DecodeCase- or ChunkCase-like object's cache: (k, v) rows
+    [total, Hkv, D], f16 or f32; rows past out_start[B] are not written."""
+    import torch
+    int8 = case.k.dtype == torch.int8
+    P, max_pages, n_pages, max_kv, ring = _cache_args(case)
+    shape = (total, case.n_kv_heads, case.head_dim)
+    dt = torch.float32 if out_f32 else torch.float16
+    k, v = torch.empty(shape, dtype=dt, device=case.k.device), torch.empty(shape, dtype=dt, device=case.k.device)
+    attn_kv_read(case.k, case.v, case.kv_len if kv_len is None else kv_len, first, out_start, case.page_table, P,
+                 max_pages, n_pages, max_kv, ring, case.k_scales if int8 else None, case.v_scales if int8 else None,
+                 ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, total, case.n_kv_heads, case.head_dim, k, v,
+                 _dtype_of(k), stream)
+    return k, v

@@ -455,39 +455,78 @@ attn_status attn_prefill(const void* q, const void* k, const void* v, int seq_le
     return launch_prefill(L);
 }
 
-attn_status attn_prefill_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* q_start,
-                               const int32_t* kv_len, const int32_t* page_table, int page_size,
-                               int max_pages_per_seq, int n_pages, int batch, int total_q, int max_q, int n_heads,
-                               int n_kv_heads, int head_dim, int window, float softcap, float scale, void* out,
-                               float* lse_out, void* stream) {
+// attn_prefill_paged and attn_prefill_paged_ex
+static attn_status prefill_paged_entry(const char* fn, const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                       int page_size, int max_pages_per_seq, int n_pages, const void* k_scales,
+                                       const void* v_scales, attn_kv_dtype kv_dtype, int batch, int total_q,
+                                       int max_q, int n_heads, int n_kv_heads, int head_dim, int window,
+                                       float softcap, float scale, void* out, float* lse_out, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
     if (!q || !k_cache || !v_cache || !q_start || !kv_len || !page_table || !out)
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: q, caches, q_start, kv_len, page_table and out must be "
-                                      "non-null");
+        return set_error(ATTN_EINVAL, "%s: q, caches, q_start, kv_len, page_table and out must be non-null", fn);
     if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || total_q < 0 || max_q < 0)
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: positive batch and head counts, total_q/max_q >= 0 "
-                                      "required");
+        return set_error(ATTN_EINVAL, "%s: positive batch and head counts, total_q/max_q >= 0 required", fn);
     if (n_heads % n_kv_heads != 0)
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: n_heads (%d) must be a multiple of n_kv_heads (%d)",
-                         n_heads, n_kv_heads);
+        return set_error(ATTN_EINVAL, "%s: n_heads (%d) must be a multiple of n_kv_heads (%d)", fn, n_heads,
+                         n_kv_heads);
     if (n_heads > 65535 || batch > 65535)
-        return set_error(ATTN_EUNSUPPORTED, "attn_prefill_paged: n_heads and batch must be at most 65535");
+        return set_error(ATTN_EUNSUPPORTED, "%s: n_heads and batch must be at most 65535", fn);
     if (head_dim != 64 && head_dim != 128 && head_dim != 256)
-        return set_error(ATTN_EUNSUPPORTED, "attn_prefill_paged: head_dim %d not supported (64, 128, 256)",
-                         head_dim);
+        return set_error(ATTN_EUNSUPPORTED, "%s: head_dim %d not supported (64, 128, 256)", fn, head_dim);
+    if (kv_dtype != ATTN_KV_F16 && kv_dtype != ATTN_KV_INT8)
+        return set_error(ATTN_EINVAL, "%s: unknown kv_dtype %d", fn, (int)kv_dtype);
+    const bool int8 = kv_dtype == ATTN_KV_INT8;
+    if (int8 && (!k_scales || !v_scales))
+        return set_error(ATTN_EINVAL, "%s: int8 caches need k_scales and v_scales", fn);
     if (page_size < 8 || (page_size & (page_size - 1)) != 0)
-        return set_error(ATTN_EUNSUPPORTED, "attn_prefill_paged: page_size %d must be a power of two >= 8",
-                         page_size);
+        return set_error(ATTN_EUNSUPPORTED, "%s: page_size %d must be a power of two >= 8", fn, page_size);
     if (max_pages_per_seq <= 0 || n_pages <= 0)
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: max_pages_per_seq and n_pages must be positive");
-    if (window < 0) return set_error(ATTN_EINVAL, "attn_prefill_paged: window must be >= 0 (0 = off)");
+        return set_error(ATTN_EINVAL, "%s: max_pages_per_seq and n_pages must be positive", fn);
+    if (window < 0) return set_error(ATTN_EINVAL, "%s: window must be >= 0 (0 = off)", fn);
     if (!(softcap >= 0.f) || !std::isfinite(softcap))
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: softcap must be finite and >= 0 (0 = off)");
-    if (!std::isfinite(scale)) return set_error(ATTN_EINVAL, "attn_prefill_paged: scale must be finite");
-    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
-        return set_error(ATTN_EINVAL, "attn_prefill_paged: q, caches and out must be 16-byte aligned");
+        return set_error(ATTN_EINVAL, "%s: softcap must be finite and >= 0 (0 = off)", fn);
+    if (!std::isfinite(scale)) return set_error(ATTN_EINVAL, "%s: scale must be finite", fn);
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        (int8 && (!aligned(k_scales, 16) || !aligned(v_scales, 16))))
+        return set_error(ATTN_EINVAL, "%s: q, caches, scales and out must be 16-byte aligned", fn);
     if (total_q == 0 || max_q == 0) return ATTN_OK;
+    if (int8) {
+        const size_t need = prefill8_workspace(max_q, n_heads, n_kv_heads, head_dim);
+        const attn_status st = check_workspace(fn, workspace, workspace_bytes, need);
+        if (st != ATTN_OK) return st;
+    }
     int* err = device_error_word();
-    if (!err) return set_error(ATTN_ECUDA, "attn_prefill_paged: no CUDA device / error word");
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    if (int8) {
+        Prefill8Launch L;
+        L.q = q;
+        L.k = k_cache;
+        L.v = v_cache;
+        L.k_scales = k_scales;
+        L.v_scales = v_scales;
+        L.q_start = q_start;
+        L.kv_len = kv_len;
+        L.page_table = page_table;
+        L.page_size = page_size;
+        L.max_pages = max_pages_per_seq;
+        L.n_pages = n_pages;
+        L.B = batch;
+        L.total_q = total_q;
+        L.max_q = max_q;
+        L.Hq = n_heads;
+        L.Hkv = n_kv_heads;
+        L.D = head_dim;
+        L.window = window;
+        L.softcap = softcap;
+        L.scale = scale;
+        L.out = out;
+        L.lse = lse_out;
+        L.workspace = workspace;
+        L.err_word = err;
+        L.stream = static_cast<cudaStream_t>(stream);
+        return launch_prefill8(L);
+    }
     PrefillLaunch L;
     L.q = q;
     L.k = k_cache;
@@ -515,6 +554,205 @@ attn_status attn_prefill_paged(const void* q, const void* k_cache, const void* v
     L.total_q = total_q;
     L.max_q = max_q;
     return launch_prefill(L);
+}
+
+attn_status attn_prefill_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* q_start,
+                               const int32_t* kv_len, const int32_t* page_table, int page_size,
+                               int max_pages_per_seq, int n_pages, int batch, int total_q, int max_q, int n_heads,
+                               int n_kv_heads, int head_dim, int window, float softcap, float scale, void* out,
+                               float* lse_out, void* stream) {
+    return prefill_paged_entry("attn_prefill_paged", q, k_cache, v_cache, q_start, kv_len, page_table, page_size,
+                               max_pages_per_seq, n_pages, nullptr, nullptr, ATTN_KV_F16, batch, total_q, max_q,
+                               n_heads, n_kv_heads, head_dim, window, softcap, scale, out, lse_out, nullptr, 0,
+                               stream);
+}
+
+attn_status attn_prefill_paged_ex(const void* q, const void* k_cache, const void* v_cache, const int32_t* q_start,
+                                  const int32_t* kv_len, const int32_t* page_table, int page_size,
+                                  int max_pages_per_seq, int n_pages, const void* k_scales, const void* v_scales,
+                                  attn_kv_dtype kv_dtype, int batch, int total_q, int max_q, int n_heads,
+                                  int n_kv_heads, int head_dim, int window, float softcap, float scale, void* out,
+                                  float* lse_out, void* workspace, size_t workspace_bytes, void* stream) {
+    return prefill_paged_entry("attn_prefill_paged_ex", q, k_cache, v_cache, q_start, kv_len, page_table, page_size,
+                               max_pages_per_seq, n_pages, k_scales, v_scales, kv_dtype, batch, total_q, max_q,
+                               n_heads, n_kv_heads, head_dim, window, softcap, scale, out, lse_out, workspace,
+                               workspace_bytes, stream);
+}
+
+size_t attn_prefill_paged_workspace_size(int batch, int max_q, int n_heads, int n_kv_heads, int head_dim,
+                                         attn_kv_dtype kv_dtype) {
+    if (batch <= 0 || max_q <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0) return 0;
+    if (batch > 65535 || n_heads > 65535) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    if (kv_dtype == ATTN_KV_F16) return 256;   // unused
+    if (kv_dtype != ATTN_KV_INT8) return 0;
+    return prefill8_workspace(max_q, n_heads, n_kv_heads, head_dim);
+}
+
+// The cache layout of attn_append and attn_kv_read, checked.
+static attn_status cache_layout(const char* fn, const int32_t* page_table, int page_size, int max_pages_per_seq,
+                                int n_pages, int max_kv, int ring_size, const void* k_cache, const void* v_cache,
+                                const void* k_scales, const void* v_scales, attn_kv_dtype kv_dtype,
+                                int n_kv_heads, int head_dim, CacheLayout* c) {
+    if (!k_cache || !v_cache) return set_error(ATTN_EINVAL, "%s: k_cache and v_cache must be non-null", fn);
+    if (n_kv_heads <= 0) return set_error(ATTN_EINVAL, "%s: n_kv_heads must be positive", fn);
+    if (n_kv_heads > 65535) return set_error(ATTN_EUNSUPPORTED, "%s: n_kv_heads above 65535", fn);
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return set_error(ATTN_EUNSUPPORTED, "%s: head_dim %d not supported (64, 128, 256)", fn, head_dim);
+    if (kv_dtype != ATTN_KV_F16 && kv_dtype != ATTN_KV_INT8)
+        return set_error(ATTN_EINVAL, "%s: unknown kv_dtype %d", fn, (int)kv_dtype);
+    const bool int8 = kv_dtype == ATTN_KV_INT8;
+    if (int8 && (!k_scales || !v_scales))
+        return set_error(ATTN_EINVAL, "%s: int8 caches need k_scales and v_scales", fn);
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        (int8 && (!aligned(k_scales, 16) || !aligned(v_scales, 16))))
+        return set_error(ATTN_EINVAL, "%s: caches and scales must be 16-byte aligned", fn);
+    c->page_table = page_table;
+    c->log2P = 0;
+    c->max_pages = max_pages_per_seq;
+    c->n_pages = n_pages;
+    c->ring = ring_size;
+    if (ring_size != 0) {
+        if (page_table) return set_error(ATTN_EINVAL, "%s: a ring cache takes no page table", fn);
+        if (ring_size < 16 || ring_size % 16 != 0)
+            return set_error(ATTN_EUNSUPPORTED, "%s: ring_size %d must be a positive multiple of 16", fn, ring_size);
+        c->rows = ring_size;
+        c->capacity = 1ll << 31;   // every position an int32 length can give
+    } else if (page_table) {
+        if (!pow2(page_size) || page_size > 1024)
+            return set_error(ATTN_EUNSUPPORTED, "%s: page_size %d must be a power of two <= 1024", fn, page_size);
+        if (int8 && page_size < 8) return set_error(ATTN_EUNSUPPORTED, "%s: int8 caches need page_size >= 8", fn);
+        if (max_pages_per_seq <= 0 || n_pages <= 0)
+            return set_error(ATTN_EINVAL, "%s: max_pages_per_seq and n_pages must be positive", fn);
+        c->rows = page_size;
+        while ((1 << c->log2P) < page_size) ++c->log2P;
+        c->capacity = static_cast<long long>(max_pages_per_seq) * page_size;
+    } else {
+        if (max_kv <= 0) return set_error(ATTN_EINVAL, "%s: max_kv must be positive", fn);
+        if (int8 && max_kv % 8 != 0)
+            return set_error(ATTN_EUNSUPPORTED, "%s: contiguous int8 caches need max_kv %% 8 == 0", fn);
+        c->rows = max_kv;
+        c->capacity = max_kv;
+    }
+    return ATTN_OK;
+}
+
+attn_status attn_append(const void* q, const void* k, const void* v, attn_dtype in_dtype, long long q_stride,
+                        long long k_stride, long long v_stride, const float* q_norm, const float* k_norm,
+                        float norm_eps, float norm_offset, const float* rope_cos, const float* rope_sin,
+                        int rope_positions, int rope_dim, int rope_interleaved, const int32_t* q_start,
+                        const int32_t* kv_len, void* k_cache, void* v_cache, const int32_t* page_table,
+                        int page_size, int max_pages_per_seq, int n_pages, int max_kv, int ring_size,
+                        void* k_scales, void* v_scales, attn_kv_dtype kv_dtype, int batch, int total_q, int n_heads,
+                        int n_kv_heads, int head_dim, void* q_out, attn_dtype q_out_dtype, void* stream) {
+    const char* fn = "attn_append";
+    if (!k || !v || !q_start || !kv_len)
+        return set_error(ATTN_EINVAL, "%s: k, v, q_start and kv_len must be non-null", fn);
+    if ((q == nullptr) != (q_out == nullptr))
+        return set_error(ATTN_EINVAL, "%s: q and q_out go together (both NULL: k and v only)", fn);
+    if ((in_dtype != ATTN_F16 && in_dtype != ATTN_F32) || (q_out_dtype != ATTN_F16 && q_out_dtype != ATTN_F32))
+        return set_error(ATTN_EINVAL, "%s: in_dtype and q_out_dtype must be ATTN_F16 or ATTN_F32", fn);
+    if (batch <= 0 || total_q < 0 || (q && n_heads <= 0))
+        return set_error(ATTN_EINVAL, "%s: positive batch and head counts, total_q >= 0 required", fn);
+    if (q && n_heads > 65535) return set_error(ATTN_EUNSUPPORTED, "%s: n_heads above 65535", fn);
+    AppendLaunch L;
+    AppendArgs& a = L.args;
+    attn_status st = cache_layout(fn, page_table, page_size, max_pages_per_seq, n_pages, max_kv, ring_size, k_cache,
+                                  v_cache, k_scales, v_scales, kv_dtype, n_kv_heads, head_dim, &a.cache);
+    if (st != ATTN_OK) return st;
+    const int per16 = in_dtype == ATTN_F32 ? 4 : 8;   // elements in 16 bytes
+    const long long kv_row = static_cast<long long>(n_kv_heads) * head_dim;
+    if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < static_cast<long long>(n_heads) * head_dim))
+        return set_error(ATTN_EINVAL, "%s: a token stride is smaller than its heads * head_dim", fn);
+    if (k_stride % per16 || v_stride % per16 || (q && q_stride % per16))
+        return set_error(ATTN_EUNSUPPORTED, "%s: token strides must be multiples of 16 bytes", fn);
+    if ((q_norm || k_norm) && (!(norm_eps >= 0.f) || !std::isfinite(norm_eps) || !std::isfinite(norm_offset)))
+        return set_error(ATTN_EINVAL, "%s: norm_eps must be finite and >= 0, norm_offset finite", fn);
+    if (rope_dim < 0 || rope_dim > head_dim)
+        return set_error(ATTN_EINVAL, "%s: rope_dim %d must be in [0, head_dim]", fn, rope_dim);
+    if (rope_dim % 16) return set_error(ATTN_EUNSUPPORTED, "%s: rope_dim %d must be a multiple of 16", fn, rope_dim);
+    if (rope_dim > 0 && (!rope_cos || !rope_sin || rope_positions <= 0))
+        return set_error(ATTN_EINVAL, "%s: a rotation needs rope_cos, rope_sin and rope_positions > 0", fn);
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(q_norm, 16) ||
+        !aligned(k_norm, 16) || (rope_dim > 0 && (!aligned(rope_cos, 16) || !aligned(rope_sin, 16))))
+        return set_error(ATTN_EINVAL, "%s: q, k, v, q_out, norm weights and tables must be 16-byte aligned", fn);
+    if (total_q == 0) return ATTN_OK;
+    int* err = device_error_word();
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_norm = q ? q_norm : nullptr;
+    a.k_norm = k_norm;
+    a.eps = norm_eps;
+    a.offset = norm_offset;
+    a.cos = rope_cos;
+    a.sin = rope_sin;
+    a.n_pos = rope_positions;
+    a.rot = rope_dim;
+    a.interleaved = rope_interleaved != 0;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.B = batch;
+    a.total_q = total_q;
+    a.Hq = q ? n_heads : 0;
+    a.Hkv = n_kv_heads;
+    a.q_out = q_out;
+    a.err = err;
+    L.D = head_dim;
+    L.in_f32 = in_dtype == ATTN_F32;
+    L.q_out_f32 = q_out_dtype == ATTN_F32;
+    L.int8 = kv_dtype == ATTN_KV_INT8;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_append(L);
+}
+
+attn_status attn_kv_read(const void* k_cache, const void* v_cache, const int32_t* kv_len, const int32_t* first,
+                         const int32_t* out_start, const int32_t* page_table, int page_size, int max_pages_per_seq,
+                         int n_pages, int max_kv, int ring_size, const void* k_scales, const void* v_scales,
+                         attn_kv_dtype kv_dtype, int batch, int total, int n_kv_heads, int head_dim, void* k_out,
+                         void* v_out, attn_dtype out_dtype, void* stream) {
+    const char* fn = "attn_kv_read";
+    if (!kv_len || !out_start || !k_out || !v_out)
+        return set_error(ATTN_EINVAL, "%s: kv_len, out_start, k_out and v_out must be non-null", fn);
+    if (out_dtype != ATTN_F16 && out_dtype != ATTN_F32)
+        return set_error(ATTN_EINVAL, "%s: out_dtype must be ATTN_F16 or ATTN_F32", fn);
+    if (batch <= 0 || total < 0) return set_error(ATTN_EINVAL, "%s: batch > 0 and total >= 0 required", fn);
+    KvReadLaunch L;
+    KvReadArgs& a = L.args;
+    attn_status st = cache_layout(fn, page_table, page_size, max_pages_per_seq, n_pages, max_kv, ring_size, k_cache,
+                                  v_cache, k_scales, v_scales, kv_dtype, n_kv_heads, head_dim, &a.cache);
+    if (st != ATTN_OK) return st;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+        return set_error(ATTN_EINVAL, "%s: k_out and v_out must be 16-byte aligned", fn);
+    if (total == 0) return ATTN_OK;
+    int* err = device_error_word();
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.kv_len = kv_len;
+    a.first = first;
+    a.out_start = out_start;
+    a.B = batch;
+    a.total = total;
+    a.Hkv = n_kv_heads;
+    a.D = head_dim;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = err;
+    L.out_f32 = out_dtype == ATTN_F32;
+    L.int8 = kv_dtype == ATTN_KV_INT8;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_kv_read(L);
 }
 
 attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_table, int batch, int page_size,
@@ -562,6 +800,12 @@ attn_status attn_device_status(void* stream) {
         return set_error(ATTN_ECUDA, "attn_device_status: %s", cudaGetErrorString(cudaGetLastError()));
     if (v == kErrBadPage)
         return set_error(ATTN_EBOUNDS, "attn_decode read a page id outside the pool (page 0 was used instead)");
+    if (v == kErrCachePage)
+        return set_error(ATTN_EBOUNDS, "attn_append or attn_kv_read met a page id outside the pool (the token was not "
+                                       "written, or read as zeros)");
+    if (v == kErrAppendRange)
+        return set_error(ATTN_EBOUNDS, "attn_append met a position outside the cache or the cos/sin tables (the token "
+                                       "was left out)");
     if (v) return set_error(ATTN_ETIMEOUT, "a kernel abandoned a pipeline wait (code %d)", v);
     return ATTN_OK;
 }

@@ -19,6 +19,8 @@ enum : int {
     kErrTimeoutMma = 3,      // a wait on a tensor-core result timed out
     kErrTimeoutSoftmax = 4,  // the MMA issuer waited too long for P
     kErrBadPage = 5,         // a page-table entry in use was outside the page pool
+    kErrCachePage = 6,       // the same, met by attn_append or attn_kv_read
+    kErrAppendRange = 7,     // a new token's position outside the cache or the cos/sin tables
 };
 
 // Records a message for attn_last_error() (thread-local) and returns `st`.
@@ -120,6 +122,68 @@ bool direct_decode_fits(const DecodeLaunch& L);
 attn_status launch_direct(const DecodeLaunch& L);
 attn_status launch_decode_tiered(const DecodeLaunch& cold, const DecodePlan& cold_plan, const DecodeLaunch& hot,
                                  const DecodePlan& hot_plan);
+
+// ---- cache writes and reads (cache.cu)
+// One sequence-addressed cache: contiguous [B, rows, Hkv, D], ring (the same with
+// token t in row t % ring) or a page pool [n_pages, rows, Hkv, D].
+struct CacheLayout {
+    const int32_t* page_table;   // NULL: contiguous or ring
+    int rows;                    // tokens a slot (page or sequence) holds
+    int log2P, max_pages, n_pages;
+    int ring;                    // > 0: ring of this many rows
+    long long capacity;          // positions at or above it are not in the cache
+};
+struct AppendArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;   // elements between tokens
+    const float *q_norm, *k_norm;
+    float eps, offset;
+    const float *cos, *sin;
+    int n_pos, rot, interleaved;
+    const int32_t *q_start, *kv_len;
+    CacheLayout cache;
+    void *k_cache, *v_cache, *k_scales, *v_scales;
+    int B, total_q, Hq, Hkv;
+    void* q_out;
+    int* err;
+};
+struct AppendLaunch {
+    AppendArgs args;
+    int D, in_f32, q_out_f32, int8;
+    cudaStream_t stream;
+};
+attn_status launch_append(const AppendLaunch& L);
+
+struct KvReadArgs {
+    const void *k_cache, *v_cache, *k_scales, *v_scales;
+    const int32_t *kv_len, *first, *out_start;
+    CacheLayout cache;
+    int B, total, Hkv, D;
+    void *k_out, *v_out;
+    int* err;
+};
+struct KvReadLaunch {
+    KvReadArgs args;
+    int out_f32, int8;
+    cudaStream_t stream;
+};
+attn_status launch_kv_read(const KvReadLaunch& L);
+
+// ---- chunks over an int8 paged cache (prefill_int8.cu)
+struct Prefill8Launch {
+    const void *q, *k, *v, *k_scales, *v_scales;
+    const int32_t *q_start, *kv_len, *page_table;
+    int page_size, max_pages, n_pages;
+    int B, total_q, max_q, Hq, Hkv, D, window;
+    float softcap, scale;
+    void* out;
+    float* lse;
+    void* workspace;
+    int* err_word;
+    cudaStream_t stream;
+};
+size_t prefill8_workspace(int max_q, int Hq, int Hkv, int D);
+attn_status launch_prefill8(const Prefill8Launch& L);
 
 // Test controls of the prefill and decode translation units: the time limit
 // of pipeline waits (ns) and the first-tile stall (see ptx.cuh).

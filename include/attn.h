@@ -349,6 +349,121 @@ attn_status attn_prefill_paged(const void* q, const void* k_cache, const void* v
                                void* out, float* lse_out, void* stream);
 
 /*
+ * attn_prefill_paged_ex -- attn_prefill_paged with the cache's element type as
+ * an argument.
+ *
+ *  kv_dtype  ATTN_KV_F16: attn_prefill_paged bit for bit (scales and workspace
+ *            are not used and may be NULL).  ATTN_KV_INT8: k_cache, v_cache are
+ *            int8 codes [n_pages, P, Hkv, D] with f16 scales [n_pages, Hkv, P],
+ *            as attn_decode takes them and attn_append writes them.  Keys and
+ *            values are used as they are: logits are q . code in f32 times the
+ *            key's scale, and a value's scale goes into its weight.
+ *  max_q     an upper bound of q_len; rows of a longer chunk past it are not
+ *            computed.
+ *  workspace ATTN_KV_INT8: device scratch of workspace_bytes >=
+ *            attn_prefill_paged_workspace_size(...) bytes, 256-byte aligned,
+ *            contents need no initialisation.  Calls that may overlap on the
+ *            GPU each need their own.
+ *  The other arguments, the masks, rows that keep no key (out = 0, lse = -inf)
+ *  and the errors are attn_prefill_paged's.  Keys that no query of a call may
+ *  keep are never used for the result, whatever their codes and scales.  A
+ *  scale that is not finite makes the rows that keep its key NaN.
+ */
+size_t attn_prefill_paged_workspace_size(int batch, int max_q, int n_heads, int n_kv_heads, int head_dim,
+                                         attn_kv_dtype kv_dtype);
+attn_status attn_prefill_paged_ex(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                                  int page_size, int max_pages_per_seq, int n_pages,
+                                  const void* k_scales, const void* v_scales, attn_kv_dtype kv_dtype,
+                                  int batch, int total_q, int max_q,
+                                  int n_heads, int n_kv_heads, int head_dim,
+                                  int window, float softcap, float scale,
+                                  void* out, float* lse_out,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_append -- what stands between the projections and the attention calls:
+ * the new tokens' q and k heads are RMS-normed and rotated to their positions,
+ * q is written packed for attn_decode_ex / attn_prefill_paged(_ex), and k and v
+ * go into the cache, as f16 or quantised to int8, in one pass.  (doppler run.js,
+ * runLayerAttentionGPU: per-head q/k norm, RoPE from cos/sin tables, then
+ * kvCache.updateFromGPU; attention.js D1: the cache layouts.)
+ *
+ *  q, k, v     device, in_dtype (f16 or f32): packed token rows; row t of q holds
+ *                Hq heads of D values from q + t * q_stride (elements), k and v
+ *                Hkv heads.  Strides are multiples of 16 bytes, so the three may
+ *                be slices of one projection's rows.  q and q_out may both be NULL
+ *                (k and v only; Hq is then ignored).
+ *  q_norm,     device f32 [D] or NULL (no norm): y = x * rsqrt(mean(x^2) +
+ *  k_norm        norm_eps) * (w + norm_offset) over each head (norm_offset 1 for
+ *                weights stored as w - 1).
+ *  rope_cos,   device f32 [rope_positions, rope_dim / 2]: row p turns the heads of
+ *  rope_sin      a token at position p.  rope_dim R (a multiple of 16, at most D;
+ *                0: no rotation): the pairs (e, e + R/2), or (2e, 2e + 1) if
+ *                rope_interleaved, e < R/2, become (a cos - b sin, b cos + a sin);
+ *                the other D - R values stay.
+ *  q_start,    device i32 [B+1] and [B], as attn_prefill_paged takes them: rows
+ *  kv_len        q_start[b] .. q_start[b+1]-1 are sequence b's new tokens, and
+ *                kv_len[b] counts its tokens with them, so token i of q_len sits
+ *                at position kv_len[b] - q_len + i.  (A decode step is q_start =
+ *                0, 1, .., B.)  Rows from q_start[B] on are left alone.
+ *  k_cache, v_cache, page_table, page_size, max_pages_per_seq, n_pages, max_kv,
+ *  k_scales, v_scales, kv_dtype  the cache exactly as attn_decode takes it (max_kv
+ *                is the contiguous capacity, unused for pages).
+ *  ring_size   > 0: the ring of attn_decode_ring (page_table NULL, max_kv unused).
+ *                Of a chunk only a sequence's newest ring_size tokens are written.
+ *  int8        s = f16(max|y| / 127) of each (token, head), code = y / s rounded to
+ *                nearest even and clamped to [-127, 127], 0 where s is 0.  Division
+ *                and rounding are exact, so without norm and rotation the codes are
+ *                those of the definition bit for bit.  A head with an infinity or a
+ *                NaN gets it as its scale and reads back as NaN.
+ *  q_out       device, q_out_dtype, [total_q, Hq, D].  It may be q itself where type
+ *                and stride agree.
+ *  All arithmetic is f32, with one rounding at the end.  A token whose position is
+ *  negative, at or above the cache's capacity or the tables' rows is left out
+ *  (neither q_out nor the cache is written), and a token whose page id lies
+ *  outside the pool is not written to the cache; both are reported through
+ *  attn_device_status (ATTN_EBOUNDS).  Sequences must not share the pages that the
+ *  call writes.
+ */
+attn_status attn_append(const void* q, const void* k, const void* v, attn_dtype in_dtype,
+                        long long q_stride, long long k_stride, long long v_stride,
+                        const float* q_norm, const float* k_norm, float norm_eps, float norm_offset,
+                        const float* rope_cos, const float* rope_sin, int rope_positions, int rope_dim,
+                        int rope_interleaved,
+                        const int32_t* q_start, const int32_t* kv_len,
+                        void* k_cache, void* v_cache, const int32_t* page_table,
+                        int page_size, int max_pages_per_seq, int n_pages, int max_kv, int ring_size,
+                        void* k_scales, void* v_scales, attn_kv_dtype kv_dtype,
+                        int batch, int total_q, int n_heads, int n_kv_heads, int head_dim,
+                        void* q_out, attn_dtype q_out_dtype, void* stream);
+
+/*
+ * attn_kv_read -- cached tokens back as packed rows: to move them to another
+ * tier or layout (attn_append takes the rows as its k and v), to attend with
+ * attn_prefill, or to save them.
+ *
+ *  k_cache .. ring_size, k_scales, v_scales, kv_dtype  the cache as attn_append
+ *                takes it; kv_len (device i32 [B]) its tokens.
+ *  first       device i32 [B] or NULL (all 0): the first token to read.
+ *  out_start   device i32 [B+1], non-decreasing, out_start[0] = 0: rows
+ *                out_start[b] .. out_start[b+1]-1 receive tokens first[b], first[b]
+ *                + 1, ... of sequence b.  Rows from out_start[B] on are left alone.
+ *  total       rows of k_out and v_out (>= out_start[B]).
+ *  k_out,      device, out_dtype (f16 or f32) [total, Hkv, D]: the f16 values, or
+ *  v_out         code * scale in f32 (rounded once where out_dtype is f16).
+ *  A token that the cache does not hold (below 0, at or above kv_len or the
+ *  capacity, or overwritten in a ring) is a row of zeros; one whose page id lies
+ *  outside the pool too, and is reported through attn_device_status (ATTN_EBOUNDS).
+ */
+attn_status attn_kv_read(const void* k_cache, const void* v_cache, const int32_t* kv_len,
+                         const int32_t* first, const int32_t* out_start, const int32_t* page_table,
+                         int page_size, int max_pages_per_seq, int n_pages, int max_kv, int ring_size,
+                         const void* k_scales, const void* v_scales, attn_kv_dtype kv_dtype,
+                         int batch, int total, int n_kv_heads, int head_dim,
+                         void* k_out, void* v_out, attn_dtype out_dtype, void* stream);
+
+/*
  * attn_decode_validate -- synchronous check of the device-side decode inputs:
  * every kv_len[b] in [1, capacity] and every page id a sequence uses in
  * [0, n_pages).  Launches one small kernel on stream and waits for it.
@@ -366,8 +481,9 @@ attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_tabl
 /*
  * attn_device_status -- synchronises stream, then reads and clears the
  * library's device error word.  Returns ATTN_ETIMEOUT if a kernel abandoned a
- * pipeline wait (its output is then invalid), ATTN_EBOUNDS if attn_decode met
- * a page id outside the pool, else ATTN_OK.
+ * pipeline wait (its output is then invalid), ATTN_EBOUNDS if a call met a page
+ * id outside the pool or attn_append a position outside the cache or its
+ * tables, else ATTN_OK.
  */
 attn_status attn_device_status(void* stream);
 

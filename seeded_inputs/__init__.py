@@ -207,6 +207,7 @@ class ChunkCase:
                    q_start[b] .. q_start[b+1]-1
       k, v         f16 pool [n_pages, P, Hkv, D]; the new tokens' K/V are already
                    the last q_len[b] of sequence b's kv_len[b] cache tokens
+                   (int8 codes when k_scales, v_scales f16 [n_pages, Hkv, P] are given)
       q_start      int32 [B+1]; kv_len int32 [B]; page_table int32 [B, max_pages]
     """
     q: torch.Tensor
@@ -227,6 +228,8 @@ class ChunkCase:
     scale: float = 0.0
     q_lens: list = field(default_factory=list)
     kv_lens: list = field(default_factory=list)
+    k_scales: Optional[torch.Tensor] = None
+    v_scales: Optional[torch.Tensor] = None
 
     @property
     def total_q(self) -> int:
@@ -234,8 +237,10 @@ class ChunkCase:
 
     def to(self, device: str) -> "ChunkCase":
         kw = dict(self.__dict__)
-        for name in ("q", "k", "v", "q_start", "kv_len", "page_table"):
-            kw[name] = kw[name].to(device)
+        for name in ("q", "k", "v", "q_start", "kv_len", "page_table", "k_scales", "v_scales"):
+            t = kw[name]
+            if t is not None:
+                kw[name] = t.to(device)
         return ChunkCase(**kw)
 
 
@@ -417,7 +422,7 @@ def paged_from_contiguous(case: DecodeCase, page_size: int, seed: int,
 def make_chunked_case(batch: int, n_heads: int, n_kv_heads: int, head_dim: int, q_lens, ctx_lens,
                       seed: int, *, page_size: int, n_pages: Optional[int] = None, window: int = 0,
                       softcap: float = 0.0, scale: Optional[float] = None,
-                      device: str = "cpu") -> ChunkCase:
+                      device: str = "cpu", int8: bool = False) -> ChunkCase:
     """Build a chunked-prefill case: sequence b has ctx_lens[b] cached tokens
     before a chunk of q_lens[b] new ones (kv_len = ctx + q_len).  Either list may
     be a (lo, hi) tuple for seeded uniform lengths.  Pages as in make_decode_case.
@@ -449,12 +454,18 @@ def make_chunked_case(batch: int, n_heads: int, n_kv_heads: int, head_dim: int, 
         pos += need[b]
     k = f16_normal((n_pages, P, n_kv_heads, head_dim), seed * 1000 + 22, device)
     v = f16_normal((n_pages, P, n_kv_heads, head_dim), seed * 1000 + 23, device)
+    ks = vs = None
+    if int8:
+        k, ks = quantize_int8_rows(k)
+        v, vs = quantize_int8_rows(v)
+        ks = ks.permute(0, 2, 1).contiguous()        # [n_pages, Hkv, P]
+        vs = vs.permute(0, 2, 1).contiguous()
     return ChunkCase(q=q, k=k, v=v, q_start=q_start,
                      kv_len=torch.tensor(kv_lens, dtype=torch.int32, device=device),
                      page_table=pt.to(device), batch=batch, n_heads=n_heads, n_kv_heads=n_kv_heads,
                      head_dim=head_dim, page_size=P, max_pages=max_pages, max_q=max(max(q_lens), 1),
                      window=window, softcap=softcap, scale=float(scale), q_lens=q_lens,
-                     kv_lens=kv_lens)
+                     kv_lens=kv_lens, k_scales=ks, v_scales=vs)
 
 
 def make_prefill_case(seq_len: int, n_heads: int, n_kv_heads: int, head_dim: int, seed: int, *,

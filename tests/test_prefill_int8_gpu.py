@@ -1,0 +1,252 @@
+"""GPU parity of attn_prefill_paged_ex over int8 pages against the plain 64-bit
+form on code * scale: one token to several tiles, ragged and empty chunks, splits
+over long caches, head groups of every size, masks that leave rows or tiles empty."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_split_kv_gb300 as attn
+import seeded_inputs as si
+from cache_util import chunk_reference
+from parity_util import INT8_MAX_ABS, INT8_REL_L2, LSE_MAX_ABS, errors
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    attn.build()
+    attn.load()
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    yield
+    assert attn.attn_device_status() == attn.ATTN_OK
+
+
+def _run(case, extra=0):
+    """out, lse with `extra` rows behind the last sequence that the call must leave alone."""
+    g = case.to("cuda")
+    T = case.q.shape[0]
+    g.q = torch.cat((g.q, torch.zeros((extra,) + tuple(g.q.shape[1:]), dtype=torch.float16, device="cuda")))
+    g.q_lens = [T + extra]
+    lse = torch.full((T + extra, case.n_heads), 7.0, dtype=torch.float32, device="cuda")
+    out = torch.full((T + extra, case.n_heads, case.head_dim), 7.0, dtype=torch.float16, device="cuda")
+    attn.prefill_paged(g, out=out, lse_out=lse)
+    torch.cuda.synchronize()
+    assert bool((out[T:] == 7).all()) and bool((lse[T:] == 7).all())
+    return out[:T].float().cpu(), lse[:T].cpu()
+
+
+def _check(case, what, extra=0):
+    ref, ref_lse = chunk_reference(case)
+    T = int(case.q_start[-1])
+    out, lse = _run(case, extra)
+    out, lse, ref, ref_lse = out[:T], lse[:T], ref[:T], ref_lse[:T]
+    assert bool(torch.isfinite(out).all()), what
+    mx, rel = errors(out.numpy(), ref.numpy())
+    assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2, "%s: max-abs %.3g rel-L2 %.3g" % (what, mx, rel)
+    empty = torch.isneginf(ref_lse)
+    assert torch.equal(torch.isneginf(lse), empty), what
+    assert bool((out[empty] == 0).all()), what
+    if not bool(empty.all()):
+        assert float((lse.double() - ref_lse)[~empty].abs().max()) <= LSE_MAX_ABS, what
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page_size", [8, 16, 64, 256, 1024])
+def test_chunks(D, page_size):
+    case = si.make_chunked_case(4, 4, 2, D, [130, 0, 1, 37], [300, 50, 777, 0], seed=D + page_size,
+                                page_size=page_size, int8=True)
+    _check(case, "D=%d P=%d" % (D, page_size), extra=3)
+
+
+@pytest.mark.parametrize("G,Hkv", [(1, 1), (1, 8), (2, 3), (3, 2), (4, 8), (5, 1), (7, 2), (8, 2), (12, 1), (16, 1),
+                                   (33, 1), (71, 1), (128, 1), (150, 1)])
+def test_head_groups(G, Hkv):
+    case = si.make_chunked_case(3, G * Hkv, Hkv, 64, [3, 40, 1], [200, 11, 0], seed=G * 10 + Hkv, page_size=16,
+                                int8=True)
+    _check(case, "G=%d Hkv=%d" % (G, Hkv))
+
+
+@pytest.mark.parametrize("D,G", [(128, 3), (128, 20), (256, 4), (256, 7), (256, 130)])
+def test_head_groups_of_wide_heads(D, G):
+    case = si.make_chunked_case(2, G, 1, D, [50, 9], [90, 300], seed=G, page_size=16, int8=True)
+    _check(case, "D=%d G=%d" % (D, G))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 2, 5])
+def test_few_rows_over_a_long_cache(D, n):
+    # one sequence, few rows: the keys are split over every CTA
+    case = si.make_chunked_case(1, 8, 2, D, [n], [20011], seed=D + n, page_size=32, int8=True)
+    _check(case, "D=%d n=%d" % (D, n))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_steps_of_ragged_lengths(D):
+    ctx = [0, 1, 126, 127, 128, 129, 255, 256, 1000, 4095, 33, 7]
+    case = si.make_chunked_case(12, 8, 2, D, [1] * 12, ctx, seed=D, page_size=8, int8=True)
+    _check(case, "D=%d" % D)
+
+
+def test_mixed_steps():
+    # prompts, chunks and single tokens in one call
+    case = si.make_chunked_case(6, 8, 2, 128, [300, 1, 1, 65, 1, 129], [0, 3000, 17, 500, 127, 1], seed=9,
+                                page_size=16, int8=True)
+    _check(case, "mixed")
+
+
+def test_many_sequences():
+    rng = np.random.default_rng(3)
+    q = [int(x) for x in rng.integers(0, 9, 700)]
+    ctx = [int(x) for x in rng.integers(0, 60, 700)]
+    case = si.make_chunked_case(700, 2, 1, 64, q, ctx, seed=7, page_size=8, int8=True)
+    _check(case, "700 sequences")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window,softcap,scale", [(1, 0.0, 0.1), (50, 0.0, 0.1), (300, 5.0, 0.1), (0, 30.0, 0.3),
+                                                  (0, 0.0, -0.1), (0, 0.0, 0.0), (129, 0.0, 0.1)])
+def test_masks_and_caps(D, window, softcap, scale):
+    case = si.make_chunked_case(3, 8, 2, D, [90, 1, 260], [400, 99, 1000], seed=window + D, page_size=32,
+                                window=window, softcap=softcap, scale=scale, int8=True)
+    _check(case, "D=%d window %d softcap %g scale %g" % (D, window, softcap, scale))
+
+
+def test_saturated_cap_and_large_logits():
+    case = si.make_chunked_case(2, 4, 2, 64, [20, 3], [100, 300], seed=3, page_size=16, softcap=1.0, scale=8.0,
+                                int8=True)
+    _check(case, "saturated")
+    case = si.make_chunked_case(2, 4, 2, 128, [20, 3], [100, 300], seed=4, page_size=16, scale=3.0, int8=True)
+    _check(case, "peaked softmax")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_growing_logits_rescale(D):
+    # key j's scale grows along the cache, so every tile moves the running maximum
+    case = si.make_chunked_case(1, 4, 2, D, [70], [1200], seed=D, page_size=16, int8=True)
+    n = case.max_pages * 16
+    grow = torch.linspace(0.2, 40.0, n)
+    for i in range(case.max_pages):
+        case.k_scales[int(case.page_table[0, i])] *= grow[i * 16:(i + 1) * 16].half()[None]
+    _check(case, "D=%d" % D)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_that_keep_no_key(D):
+    # chunks longer than their caches: rows at negative positions; a sequence without tokens
+    case = si.make_chunked_case(3, 4, 2, D, [40, 10, 200], [0, 5, 0], seed=29, page_size=16, int8=True)
+    case.kv_len = torch.tensor([25, 0, 7], dtype=torch.int32)
+    _check(case, "negative positions")
+    out, lse = _run(case)
+    assert bool((out[:15] == 0).all()) and bool(torch.isneginf(lse[:15]).all())
+
+
+def test_lengths_past_the_table_are_clamped():
+    case = si.make_chunked_case(2, 4, 2, 64, [8, 4], [56, 20], seed=30, page_size=16, int8=True)
+    case.kv_len = torch.tensor([70, 24], dtype=torch.int32)   # the table holds 64: rows at 62 .. 69 keep keys below 64
+    _check(case, "clamped")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("what", ["inf", "nan"])
+def test_scales_behind_the_mask_are_not_used(D, what):
+    # everything no row keeps is poisoned: pages' ends, tokens before the window, unused pages
+    case = si.make_chunked_case(3, 4, 2, D, [20, 1, 3], [300, 40, 0], seed=D, page_size=32, window=64, int8=True)
+    clean = chunk_reference(case)
+    poison = math.inf if what == "inf" else math.nan
+    used = torch.zeros(case.k.shape[0], 32, dtype=torch.bool)
+    for b in range(3):
+        L, n = case.kv_lens[b], case.q_lens[b]
+        for p in range(max(0, L - n - 63), L):
+            used[int(case.page_table[b, p // 32]), p % 32] = True
+    for s in (case.k_scales, case.v_scales):
+        s.copy_(torch.where(used[:, None, :], s, torch.tensor(poison).half()))
+    case.k[~used], case.v[~used] = 127, -127
+    out, lse = _run(case)
+    mx, rel = errors(out.numpy(), clean[0].numpy())
+    assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
+    assert float((lse.double() - clean[1]).abs().max()) <= LSE_MAX_ABS
+
+
+@pytest.mark.parametrize("name", ["k_scales", "v_scales"])
+@pytest.mark.parametrize("what", [math.inf, -math.inf, math.nan])
+def test_a_key_that_is_not_finite_spoils_its_own_rows_only(name, what):
+    # position 110 of 130, chunk 90 .. 129: rows from 110 on keep it
+    case = si.make_chunked_case(1, 4, 2, 128, [40], [90], seed=6, page_size=16, int8=True)
+    ref, _ = chunk_reference(case)
+    getattr(case, name)[int(case.page_table[0, 110 // 16]), 0, 110 % 16] = what
+    out, _ = _run(case)
+    assert bool(out[20:, :2].isnan().all())
+    clean = torch.ones(40, 4, dtype=torch.bool)
+    clean[20:, :2] = False
+    mx, rel = errors(out[clean].numpy(), ref[clean].numpy())
+    assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
+
+
+def test_one_key_gives_its_value():
+    case = si.make_chunked_case(1, 4, 2, 128, [1], [0], seed=5, page_size=8, int8=True)
+    out, _ = _run(case)
+    page = int(case.page_table[0, 0])
+    v = (case.v[page, 0].double() * case.v_scales[page, :, 0].double()[:, None]).repeat_interleave(2, 0)
+    # the weight is p / p: a few f32 roundings, then the output's own
+    assert bool(((out[0].double() - v).abs() <= (2.0 ** -11 + 8 * 2.0 ** -24) * v.abs() + 2.0 ** -25).all())
+
+
+def test_invalid_page_id_reads_as_zeros_and_is_reported():
+    case = si.make_chunked_case(2, 4, 2, 64, [20, 20], [100, 100], seed=31, page_size=16, int8=True)
+    ref, _ = chunk_reference(case)
+    case.page_table[0, 2] = 10_000_000
+    out, _ = _run(case)
+    assert bool(torch.isfinite(out).all())
+    assert attn.attn_device_status() == attn.ATTN_EBOUNDS
+    assert attn.attn_device_status() == attn.ATTN_OK
+    mx, rel = errors(out[20:].numpy(), ref[20:].numpy())
+    assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
+    zero = case.to("cpu")
+    zero.page_table = zero.page_table.clone()
+    zero.k, zero.v = torch.cat((zero.k, torch.zeros_like(zero.k[:1]))), torch.cat((zero.v, torch.zeros_like(zero.v[:1])))
+    zero.k_scales = torch.cat((zero.k_scales, torch.zeros_like(zero.k_scales[:1])))
+    zero.v_scales = torch.cat((zero.v_scales, torch.zeros_like(zero.v_scales[:1])))
+    zero.page_table[0, 2] = zero.k.shape[0] - 1
+    ref, _ = chunk_reference(zero)
+    mx, rel = errors(out[:20].numpy(), ref[:20].numpy())
+    assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_f16_caches_are_attn_prefill_paged_bit_for_bit(D):
+    case = si.make_chunked_case(2, 4, 2, D, [64, 130], [200, 3], seed=D, page_size=16).to("cuda")
+    a = attn.prefill_paged(case)
+    b = torch.empty_like(a)
+    attn.attn_prefill_paged_ex(case.q, case.k, case.v, case.q_start, case.kv_len, case.page_table, 16, case.max_pages,
+                               int(case.k.shape[0]), None, None, attn.ATTN_KV_F16, 2, case.total_q, case.max_q, 4, 2, D,
+                               0, 0.0, case.scale, b, None, None, 0)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
+def test_repeated_calls_give_the_same_bits():
+    case = si.make_chunked_case(5, 8, 2, 128, [3, 140, 1, 0, 260], [5000, 20, 777, 4, 300], seed=41, page_size=16,
+                                int8=True)
+    a, la = _run(case)
+    for _ in range(3):
+        b, lb = _run(case)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_two_streams_with_their_own_workspaces():
+    cases = [si.make_chunked_case(2, 8, 2, 128, [3, 70], [9000, 100], seed=s, page_size=16, int8=True) for s in (1, 2)]
+    alone = [_run(c)[0] for c in cases]
+    g = [c.to("cuda") for c in cases]
+    streams = [torch.cuda.Stream() for _ in g]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(5):
+        for c, s in zip(g, streams):
+            with torch.cuda.stream(s):
+                outs.append(attn.prefill_paged(c, stream=s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o.float().cpu(), alone[i % 2])
