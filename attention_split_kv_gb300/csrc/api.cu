@@ -787,6 +787,7 @@ attn_status attn_testing_set_waits(unsigned long long wait_limit_ns, int stall_f
     const unsigned long long limit = wait_limit_ns ? wait_limit_ns : 4000000000ull;
     attn_status st = set_test_controls_prefill(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_decode(limit, stall_first_tile);
+    if (st == ATTN_OK) st = set_test_controls_prefill8(limit, stall_first_tile);
     return st;
 }
 

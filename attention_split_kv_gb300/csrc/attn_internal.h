@@ -189,6 +189,7 @@ attn_status launch_prefill8(const Prefill8Launch& L);
 // of pipeline waits (ns) and the first-tile stall (see ptx.cuh).
 attn_status set_test_controls_prefill(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_decode(unsigned long long wait_limit_ns, int stall);
+attn_status set_test_controls_prefill8(unsigned long long wait_limit_ns, int stall);
 
 constexpr int kDecodeMaxBatch = 4096;
 constexpr int kDecodeMaxFix = 256;    // most CTAs the balanced decode kernel launches (>= SMs)

@@ -1,131 +1,1080 @@
 // prefill_int8.cu -- a chunk of new tokens of every sequence over its int8 paged
-// cache (attn_prefill_paged_ex with ATTN_KV_INT8).
+// cache (attn_prefill_paged_ex with ATTN_KV_INT8) on the sm_103a tensor cores.
 //
-//   o_i = sum_j softmax_j(cap(scale * ks_j * q_i . kcode_j)) f16(vcode_j * vs_j)
+//   o_i = sum_j softmax_j(cap(scale ks_j q_i . kc_j)) vs_j vc_j
 //
-// over the keys j <= pos_i (and pos_i - j < W).  One CTA a (packed query, head),
-// a thread a key of a 128-key tile for the logits and a column for the sum, in
-// f32 with a running maximum and sum.
+// over the keys j <= pos_i (and pos_i - j < W), with codes kc, vc and one scale
+// ks_j, vs_j a (token, kv head).  Codes are integers of at most 8 bits, so they are
+// exact as f16 operands and neither K nor V is rounded:
+//
+//   S   = Q Kc^T                                 (tcgen05.mma, f32 in TMEM)
+//   y_j = S_j (ks_j scale log2e) + log2 vs_j     (one packed fma)
+//   P_j = f16(2^(y_j - m)),  m the running maximum of y
+//   O  += P Vc,   l += 2^(y_j - m) / vs_j        (tcgen05.mma; f32)
+//
+// so the value's scale sits in its weight, and the weight is rounded once, relative
+// to the row's largest weighted scale.  out = O / l, lse = (m + log2 l) / log2e.
+//
+// Rows are packed: the query heads that share a kv head are rows of one tile beside
+// its queries (row r is query r / HG, head r % HG), so a decode step or a few draft
+// tokens read their cache once.  A group of rows is one 128-row tile, or two.
+//
+// Persistent CTAs: the key tiles of all (sequence, row group, head) items, in that
+// order, are cut into equal runs, one a CTA.  An item inside one run is written
+// directly; one that runs over a boundary leaves unnormalised partial rows in the
+// workspace, which a second kernel joins.  Long caches with few rows and short ones
+// with many are balanced by the same cut, without the host knowing any length.
+//
+// Roles (16 warps): a TMA warp brings code tiles and scales into a ring of stages; 4
+// or 8 converter warps turn them into f16 operands (128-byte swizzle) in a ring of 3
+// and write the per-key factors; one thread issues the MMAs; 4 or 8 softmax warps.
+// D = 64/128 keep two streams, each with its S (P overwrites it) and O in TMEM and
+// its own softmax warps, which take turns on the tensor cores: the two row tiles of
+// a group, or for a single tile the even and the odd key tiles, joined at the end.
+// D = 256 has one O (its 256 columns) and two S buffers.
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int BM = 128;                     // rows of a tile (TMEM lanes)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
+constexpr int kMaxCtas = 152;               // one CTA an SM
+constexpr int kMinTiles = 2;                // least key tiles of a run
+constexpr int kThreads = 512;
 
-struct Args8 {
-    Prefill8Launch L;
-    int log2P;
+// Per-key factors of a key tile, laid out as the softmax threads read them (a pair
+// of keys a time), and the sign of the value's scale for the converters.
+template <int BN>
+struct KeyFactors {
+    float4 a[BN / 2];      // {ks, ks', log2 vs, log2 vs'}: ks times scale (and log2e, or 1 / cap)
+    float2 b[BN / 2];      // {1 / vs, 1 / vs'}
+    uint32_t sign[BN];     // f16x2 of 1, -1, or 0 for a value that counts as zero
 };
 
-__device__ __forceinline__ float dequant(int8_t c, __half s) {
-    return __half2float(__float2half_rn(static_cast<float>(c) * __half2float(s)));
+template <int D, int NT>
+struct Cfg {
+    static constexpr int BN = D == 256 ? 64 : 128;       // keys a tile
+    static constexpr int NCH = D / 64;                   // 128-byte chunks of a row of f16
+    static constexpr int NS = D == 256 ? 1 : 2;          // streams (O accumulators)
+    static constexpr int NSM = 4 * NS;                   // softmax warps
+    static constexpr int NCV = 12 - NSM;                 // converter warps
+    static constexpr int PROD_WARP = 12, MMA_WARP = 13, Q_WARP = 14;
+    static constexpr int RING = 3;                       // f16 operand tiles
+    // staged code tiles: what shared memory leaves beside Q and the operand ring
+    static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
+    static constexpr int NTAB = 4;                       // key-factor tables
+    static constexpr uint32_t Q_TILE = NCH * BM * 128;
+    static constexpr uint32_t OP_CHUNK = BN * 128, OP_BYTES = NCH * OP_CHUNK;
+    static constexpr uint32_t CODE_BYTES = BN * D, SCALE_BYTES = 2 * BN * 2;
+    static constexpr uint32_t OFF_Q = 0;
+    static constexpr uint32_t OFF_OP = OFF_Q + NT * Q_TILE;
+    static constexpr uint32_t OFF_CODE = OFF_OP + RING * OP_BYTES;
+    static constexpr uint32_t OFF_SCALE = OFF_CODE + NST * CODE_BYTES;
+    static constexpr uint32_t OFF_TAB = OFF_SCALE + NST * SCALE_BYTES;
+    static constexpr uint32_t OFF_ML = OFF_TAB + NTAB * sizeof(KeyFactors<BN>);
+    static constexpr uint32_t OFF_BAR = OFF_ML + 2 * BM * 8;
+    enum : int {
+        B_SFULL_ST = 0,                    // stage: codes and scales are there
+        B_SEMPTY_ST = B_SFULL_ST + NST,    // stage: converted
+        B_OPFULL = B_SEMPTY_ST + NST,      // operand tile: converted
+        B_OPEMPTY = B_OPFULL + RING,       // operand tile: its MMAs are done
+        B_TAB = B_OPEMPTY + RING,          // key factors are there
+        B_QFULL = B_TAB + NTAB,
+        B_QEMPTY,
+        B_S,                               // S of buffer 0, 1
+        B_P = B_S + 2,                     // P of buffer 0, 1
+        B_DONE = B_P + 2,                  // a segment's last PV is done
+        B_OFREE,                           // its O has been read
+        B_ML,                              // its row statistics are in shared memory
+        B_PV,                              // each PV (one stream only)
+        B_TEARDOWN,
+        N_BARS
+    };
+    static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag, start
+    static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 64 + 1024;
+    static constexpr uint32_t COL_O = 2 * BN;            // S buffers first
+    static constexpr uint32_t TMEM_COLS = 512;
+    static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+    static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
+    static_assert(COL_O + NS * D <= TMEM_COLS, "TMEM budget");
+    static_assert(D != 256 || NT == 1, "one O");
+};
+
+struct Args8 {
+    const int32_t *q_start, *kv_len, *page_table;
+    const __half *k_scales, *v_scales;
+    __half* out;
+    float* lse;
+    float* part_o;       // [CTA][2][rows][D]
+    float2* part_ml;     // [CTA][2][rows]
+    int* meta;           // [CTA][8]
+    int* err;
+    int B, total_q, max_q, Hq, Hkv, G, HG, n_hg, QT1, QTG;   // QT1 queries a row tile, QTG a group
+    int P, log2P, max_pages, n_pages, box_rows, window, slot_rows;
+    long long capacity;
+    int max_rg;
+    float scale, softcap;
+};
+
+// One sequence's chunk, and one of its row groups.
+struct Chunk {
+    int q_base, n_rows, pos0, L;   // first packed row, rows computed, position of query 0, cached keys
+};
+__device__ __forceinline__ Chunk load_chunk(const Args8& a, int b) {
+    Chunk c;
+    c.q_base = a.q_start[b];
+    const int n_q = max(a.q_start[b + 1] - c.q_base, 0), len = a.kv_len[b];
+    c.n_rows = min(n_q, a.max_q);
+    c.pos0 = len - n_q;
+    c.L = static_cast<int>(min(static_cast<long long>(max(len, 0)), a.capacity));
+    return c;
+}
+struct Span {
+    int lo, hi, jt0, tiles;   // keys some row of the group keeps lie in [lo, hi); its key tiles (at least one)
+};
+template <int BN>
+__device__ __forceinline__ Span group_span(const Args8& a, const Chunk& c, int rg) {
+    const long long first = static_cast<long long>(c.pos0) + rg * a.QTG;
+    const long long last = static_cast<long long>(c.pos0) + min(rg * a.QTG + a.QTG, c.n_rows) - 1;
+    Span s;
+    s.hi = static_cast<int>(max(min(static_cast<long long>(c.L), last + 1), 0ll));
+    s.lo = a.window > 0 ? static_cast<int>(max(0ll, first - a.window + 1)) : 0;
+    if (s.lo >= s.hi) s.lo = s.hi = 0;   // no row keeps a key: one tile, all masked
+    s.jt0 = s.lo / BN;
+    s.tiles = max((s.hi + BN - 1) / BN - s.jt0, 1);
+    return s;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kTile) prefill8_kernel(const Args8 a) {
-    __shared__ float q[D];
-    __shared__ float pr[kTile];
-    __shared__ int page[kTile];
-    __shared__ float red[8];
-    const Prefill8Launch& L = a.L;
-    const int t = blockIdx.x, h = blockIdx.y, g = h / (L.Hq / L.Hkv), tid = threadIdx.x;
-    int b = 0;
-    while (b < L.B && L.q_start[b + 1] <= t) ++b;
-    if (b >= L.B || t < L.q_start[b]) return;
-    const long long pos = static_cast<long long>(L.kv_len[b]) - L.q_start[b + 1] + t;
-    const long long cap = static_cast<long long>(L.max_pages) * L.page_size;
-    const long long hi = min(min(pos + 1, cap), static_cast<long long>(max(L.kv_len[b], 0)));
-    const long long lo = L.window > 0 ? max(0ll, pos - L.window + 1) : 0;
-    const size_t row = static_cast<size_t>(t) * L.Hq + h;
-    for (int i = tid; i < D; i += kTile) q[i] = __half2float(static_cast<const __half*>(L.q)[row * D + i]);
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, o[D / kTile > 0 ? D / kTile : 1] = {};
-    for (long long j0 = lo; j0 < hi; j0 += kTile) {
-        const long long j = j0 + tid;
-        float s = -INFINITY;
-        int pg = -1;
-        if (j < hi) {
-            pg = L.page_table[static_cast<size_t>(b) * L.max_pages + (j >> a.log2P)];
-            if (pg < 0 || pg >= L.n_pages) {
-                atomicExch(L.err_word, kErrBadPage);
-                pg = -1;
-            }
-            float d = 0.f;
-            if (pg >= 0) {
-                const int r = static_cast<int>(j & (L.page_size - 1));
-                const int8_t* kp = static_cast<const int8_t*>(L.k) +
-                                   ((static_cast<size_t>(pg) * L.page_size + r) * L.Hkv + g) * D;
-                const __half ks = static_cast<const __half*>(L.k_scales)[(static_cast<size_t>(pg) * L.Hkv + g) * L.page_size + r];
-                for (int i = 0; i < D; ++i) d = fmaf(q[i], static_cast<float>(kp[i]), d);
-                // a scale that is not finite makes the logit, and so the row, NaN
-                const float vs = __half2float(static_cast<const __half*>(
-                    L.v_scales)[(static_cast<size_t>(pg) * L.Hkv + g) * L.page_size + r]);
-                d = isfinite(__half2float(ks)) && isfinite(vs) ? d * __half2float(ks) : NAN;
-            }
-            s = d * L.scale;
-            if (L.softcap > 0.f) s = L.softcap * tanhf(s / L.softcap);
+// A CTA's run of key tiles as segments, each of one item.  Every role walks it alike.
+struct Start {
+    int b, rg, head, off;
+    long long rem;
+};
+template <int BN>
+struct Walk {
+    int b, rg, head, off, n, n_rg;
+    long long rem;
+    Chunk c;
+    Span s;
+    __device__ __forceinline__ Walk(const Args8& a, const Start& st)
+        : b(st.b), rg(st.rg), head(st.head), off(st.off), n(0), n_rg(0), rem(st.rem) {
+        if (rem > 0) {
+            c = load_chunk(a, b);
+            n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
+            s = group_span<BN>(a, c, rg);
+            n = static_cast<int>(min(static_cast<long long>(s.tiles - off), rem));
         }
-        page[tid] = pg;
-        float mx = s;
-        for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-        const float off = mn == -INFINITY ? 0.f : mn;
-        const float p = expf(s - off);
-        pr[tid] = p;
-        float sum = p;
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        if ((tid & 31) == 0) red[4 + (tid >> 5)] = sum;
-        __syncthreads();
-        const float alpha = m == -INFINITY ? 0.f : expf(m - off);
-        l = l * alpha + ((red[4] + red[5]) + (red[6] + red[7]));
-        m = mn;
-        const int n = static_cast<int>(min(hi - j0, static_cast<long long>(kTile)));
-        for (int c = 0; c * kTile < D; ++c) {
-            const int col = c * kTile + tid;
-            float acc = o[c] * alpha;
-            if (col < D)
-                for (int x = 0; x < n; ++x) {
-                    const int pgx = page[x];
-                    if (pgx < 0) continue;
-                    const int r = static_cast<int>((j0 + x) & (L.page_size - 1));
-                    const int8_t cv = static_cast<const int8_t*>(
-                        L.v)[((static_cast<size_t>(pgx) * L.page_size + r) * L.Hkv + g) * D + col];
-                    acc = fmaf(pr[x], dequant(cv, static_cast<const __half*>(L.v_scales)[(static_cast<size_t>(pgx) * L.Hkv + g) *
-                                                                                    L.page_size + r]), acc);
+    }
+    __device__ __forceinline__ void next(const Args8& a) {
+        rem -= n;
+        off = 0;
+        if (rem <= 0) return;
+        if (++head == a.Hkv * a.n_hg) {
+            head = 0;
+            ++rg;
+            while (rg >= n_rg) {
+                if (++b >= a.B) {
+                    rem = 0;
+                    return;
                 }
-            o[c] = acc;
+                c = load_chunk(a, b);
+                n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
+                rg = 0;
+            }
+            s = group_span<BN>(a, c, rg);
         }
+        n = static_cast<int>(min(static_cast<long long>(s.tiles), rem));
+    }
+    __device__ __forceinline__ bool whole() const { return off == 0 && n == s.tiles; }
+    // two row tiles (every key tile twice), or one
+    __device__ __forceinline__ bool two(const Args8& a) const { return a.QTG > a.QT1 && c.n_rows - rg * a.QTG > a.QT1; }
+};
+
+// The order in which a segment of n key tiles loads them, which is the order the
+// MMAs first need them in: with two row tiles K0 V0 K1 V1 ..; with one, S of the next
+// tile runs before PV of this one: K0 K1 V0 K2 V1 .. .
+__device__ __forceinline__ int item_k(bool two, int j) { return two ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int item_v(bool two, int j, int n) { return two ? 2 * j + 1 : j == n - 1 ? 2 * n - 1 : 2 * j + 2; }
+__device__ __forceinline__ bool item_of(bool two, int i, int n, int& j) {   // true: K
+    if (two) {
+        j = i >> 1;
+        return (i & 1) == 0;
+    }
+    if (i == 0) {
+        j = 0;
+        return true;
+    }
+    if (i == 2 * n - 1) {
+        j = n - 1;
+        return false;
+    }
+    j = (i & 1) ? (i + 1) >> 1 : (i >> 1) - 1;
+    return (i & 1) != 0;
+}
+
+// Four int8 codes to two f16 pairs: a code's byte with its sign bit flipped is code +
+// 128, the low byte of the f16 number 1024 + 128 + code; fma(x, s, -1152 s) is then
+// s * code exactly for s = 1, -1 or 0.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, __half2 s, __half2 off, uint32_t& lo, uint32_t& hi) {
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 x = __hfma2(*reinterpret_cast<const __half2*>(&a), s, off);
+    const __half2 y = __hfma2(*reinterpret_cast<const __half2*>(&b), s, off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+template <int D, int NT, bool CAP>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const Args8 a) {
+    using C = Cfg<D, NT>;
+    constexpr int BN = C::BN, NCH = C::NCH, NST = C::NST, RING = C::RING;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    Start* start_s = reinterpret_cast<Start*>(smem + C::OFF_MISC + 16);
+    KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [stream][row]
+    auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- this CTA's run: sum the key tiles of every (sequence, row group), then find
+    // where the run starts
+    {
+        long long* sums = reinterpret_cast<long long*>(smem + C::OFF_CODE);   // before any copy
+        const long long pairs = static_cast<long long>(a.B) * a.max_rg;
+        const long long per = (pairs + kThreads - 1) / kThreads;
+        const long long f0 = min(pairs, tid * per), f1 = min(pairs, f0 + per);
+        // visits this thread's pairs in order until fn says stop
+        auto visit = [&](auto fn) {
+            Chunk c;
+            int bb = -1, n_rg = 0;
+            for (long long f = f0; f < f1;) {
+                const int b = static_cast<int>(f / a.max_rg), rg = static_cast<int>(f % a.max_rg);
+                if (b != bb) {
+                    c = load_chunk(a, b);
+                    n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
+                    bb = b;
+                }
+                if (rg >= n_rg) {
+                    f = static_cast<long long>(b + 1) * a.max_rg;
+                    continue;
+                }
+                if (!fn(b, rg, group_span<BN>(a, c, rg).tiles)) break;
+                ++f;
+            }
+        };
+        long long mine = 0;
+        visit([&](int, int, int t) {
+            mine += t;
+            return true;
+        });
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) sums[warp] = incl;
+        if (tid == 0) {
+            start_s->rem = 0;
+            for (int i = 0; i < NST; ++i) {
+                mbar_init(bar(C::B_SFULL_ST + i), 1);
+                mbar_init(bar(C::B_SEMPTY_ST + i), C::NCV * 32);
+            }
+            for (int i = 0; i < RING; ++i) {
+                mbar_init(bar(C::B_OPFULL + i), C::NCV * 32);
+                mbar_init(bar(C::B_OPEMPTY + i), 1);
+            }
+            for (int i = 0; i < C::NTAB; ++i) mbar_init(bar(C::B_TAB + i), C::NCV * 32);
+            mbar_init(bar(C::B_QFULL), 1);
+            mbar_init(bar(C::B_QEMPTY), 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(bar(C::B_S + i), 1);
+                mbar_init(bar(C::B_P + i), 128);
+            }
+            mbar_init(bar(C::B_DONE), 1);
+            mbar_init(bar(C::B_OFREE), C::NSM * 32);
+            mbar_init(bar(C::B_ML), C::NSM * 32);
+            mbar_init(bar(C::B_PV), 1);
+            mbar_init(bar(C::B_TEARDOWN), 1);
+            *abort_flag = 0;
+            fence_barrier_init();
+        }
+        if (warp == C::MMA_WARP) {
+            tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sums[w];
+            total += sums[w];
+        }
+        before += incl - mine;
+        const int heads = a.Hkv * a.n_hg;
+        const long long all = total * heads;
+        // as many runs as CTAs, or fewer of kMinTiles
+        const long long runs = max(1ll, min(static_cast<long long>(gridDim.x), all / kMinTiles));
+        const long long t0 = blockIdx.x < runs ? all * blockIdx.x / runs : all;
+        const long long t1 = blockIdx.x < runs ? all * (blockIdx.x + 1) / runs : all;
+        if (t0 < t1 && before * heads <= t0 && t0 < (before + mine) * heads) {   // one thread
+            long long acc = before;
+            visit([&](int b, int rg, int t) {
+                if ((acc + t) * heads <= t0) {
+                    acc += t;
+                    return true;
+                }
+                const long long in = t0 - acc * heads;
+                start_s->b = b;
+                start_s->rg = rg;
+                start_s->head = static_cast<int>(in / t);
+                start_s->off = static_cast<int>(in % t);
+                start_s->rem = t1 - t0;
+                return false;
+            });
+        }
+        fence_proxy_async_smem();   // the scratch is where codes land
         __syncthreads();
     }
-    for (int c = 0; c * kTile < D; ++c) {
-        const int col = c * kTile + tid;
-        if (col < D) static_cast<__half*>(L.out)[row * D + col] = __float2half_rn(hi > lo ? o[c] / l : 0.f);
+    const uint32_t tmem = *tmem_holder;
+    const Start start = *start_s;
+    Walk<BN> w(a, start);
+    if (tid == 0) {
+        int* m = a.meta + blockIdx.x * 8;
+        m[0] = w.rem > 0 && w.off > 0;          // begins inside an item
+        m[1] = w.rem > 0 && w.n == w.s.tiles - w.off;   // and ends it
+        m[2] = 0;                               // ends inside another (set below)
     }
-    if (L.lse && tid == 0) L.lse[row] = hi > lo ? m + logf(l) : -INFINITY;
+
+    if (warp == C::PROD_WARP) {
+        // ------------------------------------------------------------ codes and scales
+        // lanes 0-15, lane i the box of the tile's i-th page (one box inside a page that
+        // is longer than the tile); lane 0 waits for the stage and posts the byte count
+        if (lane < 16) {
+            const unsigned gmask = 0x0000ffffu;
+            const bool leader = lane == 0;
+            if (leader) {
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+            }
+            const int R = a.box_rows;
+            const bool has_box = lane * R < BN;
+            uint32_t gi = 0;   // tiles loaded by this CTA so far
+            int ok = 1;
+            for (; ok && w.rem > 0; w.next(a)) {
+                const bool two = w.two(a);
+                const int g = w.head / a.n_hg;
+                const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+                // page id of this lane's box in item i
+                auto fetch = [&](int i) {
+                    int j;
+                    if (i >= 2 * w.n) return 0;
+                    item_of(two, i, w.n, j);
+                    const int kk = (w.s.jt0 + w.off + j) * BN + lane * R;
+                    return has_box && kk >= w.s.lo - R + 1 && kk < w.s.hi ? __ldg(&table[kk >> a.log2P]) : 0;
+                };
+                int pg = fetch(0);
+                for (int i = 0; i < 2 * w.n; ++i, ++gi) {
+                    const uint32_t st = gi % NST;
+                    if (gi >= NST) {
+                        if (leader)
+                            ok = mbar_wait(bar(C::B_SEMPTY_ST + st), ((gi / NST) - 1) & 1, abort_flag, a.err,
+                                           kErrTimeoutSlot);
+                        ok = __shfl_sync(gmask, ok, 0);
+                        if (!ok) break;
+                    }
+                    int j;
+                    const bool is_k = item_of(two, i, w.n, j);
+                    const int kk = (w.s.jt0 + w.off + j) * BN + lane * R;
+                    // boxes without a key of [lo, hi), and pages outside the pool, take the page
+                    // coordinate n_pages, so that the copy fills zeros, and zero scales
+                    int page = a.n_pages, row = 0;
+                    if (has_box && kk >= w.s.lo - R + 1 && kk < w.s.hi) {
+                        if (pg >= 0 && pg < a.n_pages) {
+                            page = pg;
+                            row = kk & (a.P - 1);
+                        } else {
+                            atomicExch(a.err, kErrBadPage);
+                        }
+                    }
+                    const bool live = page < a.n_pages;
+                    const uint32_t sc = C::OFF_SCALE + st * C::SCALE_BYTES + lane * R * 2;
+                    if (is_k && has_box && !live) {
+                        for (int x = 0; x < R * 2; x += 16) {
+                            *reinterpret_cast<uint4*>(smem + sc + x) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(smem + sc + BN * 2 + x) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    const unsigned lives = __ballot_sync(gmask, live);
+                    __syncwarp(gmask);   // the zeros before the leader's arrival
+                    if (leader)
+                        mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st),
+                                              C::CODE_BYTES + (is_k ? __popc(lives) * R * 4 : 0));
+                    __syncwarp(gmask);
+                    if (has_box) {
+                        tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + lane * R * D, is_k ? &tm_k : &tm_v,
+                                    bar(C::B_SFULL_ST + st), 0, g, row, page);
+                        if (is_k && live) {
+                            const size_t at = (static_cast<size_t>(page) * a.Hkv + g) * a.P + row;
+                            bulk_load(sbase + sc, a.k_scales + at, R * 2, bar(C::B_SFULL_ST + st));
+                            bulk_load(sbase + sc + BN * 2, a.v_scales + at, R * 2, bar(C::B_SFULL_ST + st));
+                        }
+                    }
+                    pg = fetch(i + 1);
+                }
+            }
+            if (leader && *abort_flag) {
+                // copies in flight land before the CTA's shared memory goes away
+                for (uint32_t i = gi > NST ? gi - NST : 0; i < gi; ++i)
+                    mbar_wait_drain(bar(C::B_SFULL_ST + i % NST), (i / NST) & 1, a.err, kErrTimeoutLoad);
+            }
+        }
+    } else if (warp == C::Q_WARP) {
+        // ------------------------------------------------------------ Q
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_q);
+            uint32_t seg = 0;
+            for (; w.rem > 0; w.next(a), ++seg) {
+                if (seg > 0 &&
+                    !mbar_wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot)) break;
+                const int nt = w.two(a) ? 2 : 1;
+                const int h0 = (w.head / a.n_hg) * a.G + (w.head % a.n_hg) * a.HG;
+                mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
+                for (int t = 0; t < nt; ++t)
+                    for (int c = 0; c < NCH; ++c)
+                        tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64, h0,
+                                    w.c.q_base + w.rg * a.QTG + t * a.QT1);
+            }
+            if (*abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
+        }
+    } else if (warp == C::MMA_WARP) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, false);
+            constexpr uint32_t idesc_o = idesc_f16_f32(BM, D, true);
+            const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(sbase + C::OFF_OP, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(sbase + C::OFF_OP, C::OP_CHUNK, 1024);
+            // testing hook: hold back the signal of the first S tile
+            const bool stall = stall_first_tile();
+            uint32_t base = 0, u0 = 0, seg = 0;   // tiles and units before this segment
+            bool ok = true;
+            for (; ok && w.rem > 0; w.next(a), ++seg) {
+                const bool two = NT == 2 && w.two(a);
+                const int n = w.n, U = two ? 2 * n : n;
+                ok = mbar_wait(bar(C::B_QFULL), seg & 1, abort_flag, a.err, kErrTimeoutLoad);
+                auto issue_s = [&](int u) -> bool {
+                    const int j = two ? u >> 1 : u;
+                    const uint32_t gi = base + item_k(two, j), slot = gi % RING, buf = (u0 + u) & 1;
+                    if (!mbar_wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t kd = desc_advance(k_desc, slot * C::OP_BYTES);
+                    const uint64_t qd = desc_advance(q_desc, two ? (u & 1) * C::Q_TILE : 0);
+#pragma unroll
+                    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_f16_ss(tmem + buf * BN, desc_advance(qd, c * (BM * 128) + kk * 32),
+                                          desc_advance(kd, c * C::OP_CHUNK + kk * 32), idesc_s, (c | kk) != 0);
+                    if (!(stall && u0 + u == 0)) tc_commit(bar(C::B_S + buf));
+                    if (!two || (u & 1)) tc_commit(bar(C::B_OPEMPTY + slot));
+                    if (u == U - 1) tc_commit(bar(C::B_QEMPTY));
+                    return true;
+                };
+                ok = ok && issue_s(0);
+                for (int u = 0; ok && u < U; ++u) {
+                    // S of the next unit overwrites P of the unit before this one, whose PV was
+                    // issued earlier: MMAs of one thread run in the order of their issue
+                    if (u + 1 < U && !(ok = issue_s(u + 1))) break;
+                    const uint32_t buf = (u0 + u) & 1;
+                    const int j = two ? u >> 1 : u;
+                    const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
+                    ok = mbar_wait(bar(C::B_P + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax) &&
+                         mbar_wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                    // O still holds the segment before until its rows have been read
+                    if (ok && u == 0 && seg > 0)
+                        ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = desc_advance(v_desc, slot * C::OP_BYTES);
+                    const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        tc_mma_f16_ts(o_tmem, tmem + buf * BN + kk * 8, desc_advance(vd, kk * 16 * 128), idesc_o,
+                                      u >= C::NS || kk > 0 ? 1u : 0u);
+                    if (C::NS == 1) tc_commit(bar(C::B_PV));
+                    if (!two || (u & 1)) tc_commit(bar(C::B_OPEMPTY + slot));
+                }
+                if (ok) tc_commit(bar(C::B_DONE));
+                base += 2 * n;
+                u0 += U;
+            }
+            tc_commit(bar(C::B_TEARDOWN));   // all MMAs retire before TMEM is released
+            mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
+        }
+    } else if (warp >= C::NSM && warp < 12) {
+        // ------------------------------------------------------------ converters
+        constexpr int CT = C::NCV * 32;               // threads
+        constexpr int CH = BN * D / 16 / CT;          // 16-code pieces a thread
+        static_assert(CH % 4 == 0 && CT >= BN, "converter split");
+        const int ct = tid - C::NSM * 32;
+        const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
+        uint32_t gi = 0, jt = 0;    // tiles converted; key tiles before this segment
+        bool ok = true;
+        for (; ok && w.rem > 0; w.next(a)) {
+            const bool two = NT == 2 && w.two(a);
+            for (int i = 0; i < 2 * w.n; ++i, ++gi) {
+                int j;
+                const bool is_k = item_of(two, i, w.n, j);
+                const uint32_t st = gi % NST, slot = gi % RING, tb = (jt + j) % C::NTAB;
+                ok = mbar_wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                if (ok && gi >= RING)
+                    ok = mbar_wait(bar(C::B_OPEMPTY + slot), ((gi / RING) - 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                if (ok && !is_k)   // the signs of this tile's value scales
+                    ok = mbar_wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                if (!ok) break;
+                KeyFactors<BN>& t = tab[tb];
+                if (is_k) {
+                    if (ct < BN) {
+                        const __half* sc = reinterpret_cast<const __half*>(smem + C::OFF_SCALE + st * C::SCALE_BYTES);
+                        const int key = (w.s.jt0 + w.off + j) * BN + ct;
+                        const bool in = key >= w.s.lo && key < w.s.hi;
+                        const float ks = __half2float(sc[ct]), vs = __half2float(sc[BN + ct]);
+                        const bool fin = isfinite(ks) && isfinite(vs);
+                        // a value scale of 0 counts as the smallest f16 with codes of 0; a scale
+                        // that is not finite makes the logit NaN, which only rows that keep the
+                        // key take; keys outside [lo, hi) get factors that cannot spoil anything
+                        const float av = in && fin ? fmaxf(fabsf(vs), 0x1p-24f) : 1.f;
+                        float* fa = reinterpret_cast<float*>(&t.a[ct >> 1]);
+                        fa[ct & 1] = !in ? 0.f : fin ? ks * kf : __int_as_float(0x7fc00000);
+                        fa[2 + (ct & 1)] = log2f(av);
+                        reinterpret_cast<float*>(&t.b[ct >> 1])[ct & 1] = 1.f / av;
+                        t.sign[ct] = !in || !fin || vs == 0.f ? 0u : vs > 0.f ? 0x3c003c00u : 0xbc00bc00u;
+                    }
+                    mbar_arrive(bar(C::B_TAB + tb));
+                }
+                const uint8_t* src = smem + C::OFF_CODE + st * C::CODE_BYTES;
+                uint8_t* dst = smem + C::OFF_OP + slot * C::OP_BYTES;
+                const __half2 one = __float2half2_rn(1.f), shift = __float2half2_rn(-1152.f);
+#pragma unroll
+                for (int c0 = 0; c0 < CH; c0 += 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((c0 + c) * CT + ct) * 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int piece = (c0 + c) * CT + ct;
+                        const int row = piece / (D / 16), part = piece % (D / 16);
+                        __half2 s = one, off = shift;
+                        if (!is_k) {
+                            const uint32_t sg = t.sign[row];
+                            s = *reinterpret_cast<const __half2*>(&sg);
+                            off = __hmul2(s, shift);
+                        }
+                        uint4 x, y;
+                        codes_to_f16(v[c].x, s, off, x.x, x.y);
+                        codes_to_f16(v[c].y, s, off, x.z, x.w);
+                        codes_to_f16(v[c].z, s, off, y.x, y.y);
+                        codes_to_f16(v[c].w, s, off, y.z, y.w);
+                        // two 16-byte units of the row's 128-byte line; the lanes of the second
+                        // line store them the other way round, so that no two lanes of a store
+                        // meet in a bank
+                        uint8_t* line = dst + (part >> 2) * C::OP_CHUNK + row * 128;
+                        const int u = (part & 3) * 2, sw = row & 7;
+                        const bool flip = (part & 4) != 0;
+                        *reinterpret_cast<uint4*>(line + (((u + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
+                        *reinterpret_cast<uint4*>(line + (((u + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(C::B_OPFULL + slot));
+                mbar_arrive(bar(C::B_SEMPTY_ST + st));
+            }
+            jt += w.n;
+        }
+    } else if (warp < C::NSM) {
+        // ------------------------------------------------------------ softmax
+        const int ws = warp >> 2;                  // stream
+        const int quarter = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const float cap_log2 = a.softcap * kLog2e;
+        uint32_t u0 = 0, jt = 0, seg = 0;
+        bool ok = true;
+        for (; ok && w.rem > 0; w.next(a), ++seg) {
+            const bool two = NT == 2 && w.two(a);
+            const int n = w.n, U = two ? 2 * n : n;
+            // this warpgroup's units: those of its stream (all, if there is one)
+            const int first_u = C::NS == 1 ? 0 : static_cast<int>((ws ^ u0) & 1);
+            const int rt = two ? first_u : 0;      // row tile
+            const int q0 = w.rg * a.QTG + rt * a.QT1;
+            // a thread holds rows quarter*32 + 16 x + lane / 4 (+ 8), x = 0, 1, and of every 8
+            // columns the pair 2 (lane % 4): the per-key factors are then one 16- and one
+            // 8-byte load for 4 rows and 2 keys
+            int pos[4];
+            float m[4], l[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                pos[x] = w.c.pos0 + q0 + (quarter * 32 + x * 8 + (lane >> 2)) / a.HG;
+                m[x] = -INFINITY;
+                l[x] = 0.f;
+            }
+            for (int u = first_u; ok && u < U; u += C::NS) {
+                const int j = two ? u >> 1 : u;
+                const uint32_t buf = (u0 + u) & 1, tb = (jt + j) % C::NTAB;
+                ok = mbar_wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
+                     mbar_wait(bar(C::B_S + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                ok = __all_sync(0xffffffffu, ok);   // tcgen05 loads and stores need whole warps
+                if (!ok) break;
+                tc_fence_after();
+                const KeyFactors<BN>& t = tab[tb];
+                const int key0 = (w.s.jt0 + w.off + j) * BN;
+#pragma unroll
+                for (int hlf = 0; hlf < 2; ++hlf) {
+                    const uint32_t rows = lanes + (static_cast<uint32_t>(hlf * 16) << 16);
+                    const uint32_t s_addr = rows + buf * BN;
+                    float2 y[2][BN / 8];           // [row of the half][8-column group]
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) {
+                        uint32_t r[32];
+                        tc_ld_16x256b_x8(s_addr + c * 64, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            y[0][c * 8 + i] = make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
+                            y[1][c * 8 + i] = make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                        }
+                    }
+                    if constexpr (CAP) {
+                        // c tanh(x) in log2 units: an odd polynomial for |x| <= 1/4 (the dropped
+                        // x^9 term is below 8.4e-8), else the exponential form for the whole half
+                        const float k1 = cap_log2 * (-1.0f / 3.0f), k2 = cap_log2 * (2.0f / 15.0f),
+                                    k3 = cap_log2 * (-17.0f / 315.0f);
+                        float ax = 0.f;
+#pragma unroll
+                        for (int i = 0; i < BN / 8; ++i) {
+                            const float4 f = t.a[4 * i + (lane & 3)];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                y[x][i] = fmul2(y[x][i], make_float2(f.x, f.y));
+                                ax = fmaxf(ax, fmaxf(fabsf(y[x][i].x), fabsf(y[x][i].y)));
+                            }
+                        }
+                        const bool small = __all_sync(0xffffffffu, ax <= 0.25f);
+#pragma unroll
+                        for (int i = 0; i < BN / 8; ++i) {
+                            const float4 f = t.a[4 * i + (lane & 3)];
+                            const float2 lv = make_float2(f.z, f.w);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float2 v = y[x][i];
+                                if (small) {
+                                    const float2 z = fmul2(v, v);
+                                    float2 q = ffma2(z, make_float2(k3, k3), make_float2(k2, k2));
+                                    q = ffma2(q, z, make_float2(k1, k1));
+                                    q = ffma2(q, z, make_float2(cap_log2, cap_log2));
+                                    y[x][i] = ffma2(v, q, lv);
+                                } else {
+                                    y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(v.x), lv.x),
+                                                          fmaf(cap_log2, tanh_abs_accurate(v.y), lv.y));
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BN / 8; ++i) {
+                            const float4 f = t.a[4 * i + (lane & 3)];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                y[x][i] = ffma2(y[x][i], make_float2(f.x, f.y), make_float2(f.z, f.w));
+                        }
+                    }
+                    const int pa = pos[2 * hlf], pb = pos[2 * hlf + 1];
+                    const int key_last = key0 + BN - 1;
+                    bool full = key_last < w.s.hi && key_last <= pa && key_last <= pb;
+                    if (a.window > 0) full = full && pa - key0 < a.window && pb - key0 < a.window;
+                    if (!full) {
+#pragma unroll
+                        for (int i = 0; i < BN / 8; ++i) {
+                            const int kj = key0 + 8 * i + 2 * (lane & 3);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int p = x ? pb : pa;
+                                bool k0 = kj < w.s.hi && kj <= p, k1 = kj + 1 < w.s.hi && kj + 1 <= p;
+                                if (a.window > 0) {
+                                    k0 = k0 && p - kj < a.window;
+                                    k1 = k1 && p - kj - 1 < a.window;
+                                }
+                                if (!k0) y[x][i].x = -INFINITY;
+                                if (!k1) y[x][i].y = -INFINITY;
+                            }
+                        }
+                    }
+                    // running maxima of the two rows (their 4 lanes agree on them)
+                    float alpha[2] = {1.f, 1.f}, m_off[2];
+                    bool need = false;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < BN / 8; ++i) mx = fmaxf(mx, fmaxf(y[x][i].x, y[x][i].y));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        float& mu = m[2 * hlf + x];
+                        if (mx > mu + kRescaleThreshold || (mu == -INFINITY && mx > -INFINITY)) {
+                            alpha[x] = mu == -INFINITY ? 0.f : ex2_approx(mu - mx);
+                            l[2 * hlf + x] *= alpha[x];
+                            mu = mx;
+                            need = true;
+                        }
+                        m_off[x] = mu == -INFINITY ? 0.f : mu;
+                    }
+                    // exponentials: P = f16(2^(y - m)), l += 2^(y - m) / vs
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) {
+                        uint32_t packed[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 iv = t.b[4 * (c * 8 + i) + (lane & 3)];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float2 d = fadd2(y[x][c * 8 + i], make_float2(-m_off[x], -m_off[x]));
+                                const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                                ls[x] = ffma2(p, iv, ls[x]);
+                                const __half2 hp = __floats2half2_rn(p.x, p.y);
+                                packed[2 * i + x] = *reinterpret_cast<const uint32_t*>(&hp);
+                            }
+                        }
+                        tc_st_16x128b_x8(s_addr + c * 32, packed);
+                    }
+                    l[2 * hlf] += ls[0].x + ls[0].y;
+                    l[2 * hlf + 1] += ls[1].x + ls[1].y;
+                    // the stream's O is rescaled when a maximum moved.  Its last PV has retired:
+                    // S was issued after it (one stream: PV of the unit before is waited for)
+                    if (u >= C::NS && __any_sync(0xffffffffu, need)) {
+                        if (C::NS == 1) {
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
+                                                                   kErrTimeoutMma));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        const uint32_t o_addr = rows + C::COL_O + (C::NS == 2 ? buf * D : 0);
+#pragma unroll 1
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint32_t r[32];
+                            tc_ld_16x256b_x8(o_addr + c * 64, r);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha[(i >> 1) & 1]);
+                            tc_st_16x256b_x8(o_addr + c * 64, r);
+                        }
+                    }
+                }
+                if (!ok) break;
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(C::B_P + buf));
+            }
+            // -------------------------------------------------------- the segment's rows
+            if (ok) ok = mbar_wait(bar(C::B_DONE), seg & 1, abort_flag, a.err, kErrTimeoutMma);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float s = l[x];
+                s += __shfl_xor_sync(0xffffffffu, s, 1);
+                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                if ((lane & 3) == 0) ml[ws * BM + quarter * 32 + x * 8 + (lane >> 2)] = make_float2(m[x], s);
+            }
+            mbar_arrive(bar(C::B_ML));
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
+            if (!ok) break;
+            {
+                // one row a lane now.  Two streams of one row tile are joined here, each
+                // warpgroup half of the columns
+                const bool join = C::NS == 2 && !two;
+                const int row = quarter * 32 + lane;
+                const int cols = join ? D / 2 : D, c0 = join ? ws * (D / 2) : 0;
+                const int s0 = join ? static_cast<int>(u0 & 1) : ws;    // stream of the first unit
+                const bool both = join && n > 1;
+                const float2 x0 = ml[s0 * BM + row];
+                float mx = x0.x, sum = x0.y, w0 = 1.f, w1 = 0.f;
+                if (both) {
+                    const float2 x1 = ml[(s0 ^ 1) * BM + row];
+                    mx = fmaxf(x0.x, x1.x);
+                    w0 = x0.x == -INFINITY ? 0.f : ex2_approx(x0.x - mx);
+                    w1 = x1.x == -INFINITY ? 0.f : ex2_approx(x1.x - mx);
+                    sum = w0 * x0.y + w1 * x1.y;
+                }
+                const int i = row / a.HG, gh = (w.head % a.n_hg) * a.HG + row % a.HG;
+                const int qi = q0 + i, orow = w.c.q_base + qi;
+                const bool live = row < a.QT1 * a.HG && qi < w.c.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
+                const bool whole = w.whole();
+                // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
+                const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+                if (whole) {
+                    w0 *= inv;
+                    w1 *= inv;
+                }
+                const size_t at = static_cast<size_t>(orow) * a.Hq + (w.head / a.n_hg) * a.G + gh;
+                const int slot = blockIdx.x * 2 + (w.off > 0 ? 0 : 1);
+                const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + row;
+                const uint32_t o0 = lanes + C::COL_O + (C::NS == 2 ? s0 * D : 0) + c0;
+                const uint32_t o1 = lanes + C::COL_O + (C::NS == 2 ? (s0 ^ 1) * D : 0) + c0;
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32) {
+                    __syncwarp();
+                    uint32_t r[32];
+                    tc_ld_32x32b_x32(o0 + c, r);
+                    tc_wait_ld();
+                    float o[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
+                    if (both) {
+                        tc_ld_32x32b_x32(o1 + c, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), w1, o[e]);
+                    }
+                    if (live && whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + c0 + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t hv[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const __half2 h2 = __floats2half2_rn(o[8 * e + 2 * x], o[8 * e + 2 * x + 1]);
+                                hv[x] = *reinterpret_cast<const uint32_t*>(&h2);
+                            }
+                            dst[e] = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+                        }
+                    } else if (live) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c0 + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                if (live && c0 == 0) {
+                    if (!whole) a.part_ml[part] = make_float2(mx, sum);
+                    else if (a.lse)
+                        a.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
+                }
+                if (tid == 0 && w.off == 0 && !whole) {
+                    int* meta = a.meta + blockIdx.x * 8;
+                    meta[2] = 1;
+                    meta[3] = w.b;
+                    meta[4] = w.rg;
+                    meta[5] = w.head;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(C::B_OFREE));
+            u0 += U;
+            jt += n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == C::MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partial rows of the items that run over a CTA boundary: block (c, y) takes
+// the item that CTA c leaves unfinished, and of its rows those of chunk y, a warp a row.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Args8 a, int n_ctas) {
+    const int* meta = a.meta + blockIdx.x * 8;
+    if (!meta[2]) return;
+    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Chunk c = load_chunk(a, meta[3]);
+    const int rg = meta[4], head = meta[5];
+    const int per = a.QT1 * a.HG;
+    const int qi = rg * a.QTG + (row / per) * a.QT1 + (row % per) / a.HG;
+    const int gh = (head % a.n_hg) * a.HG + (row % per) % a.HG, orow = c.q_base + qi;
+    if (qi >= c.n_rows || qi >= (rg + 1) * a.QTG || gh >= a.G || orow < 0 || orow >= a.total_q) return;
+    // the parts: the end of CTA c's run, whole runs, the beginning of the last
+    float mx = a.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + 1) * a.slot_rows + row].x;
+    int last = blockIdx.x;
+    do {
+        ++last;
+        mx = fmaxf(mx, a.part_ml[static_cast<size_t>(last) * 2 * a.slot_rows + row].x);
+    } while (!a.meta[last * 8 + 1] && last + 1 < n_ctas);
+    float o[D / 32], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    for (int i = blockIdx.x; i <= last; ++i) {
+        const size_t at = (static_cast<size_t>(i) * 2 + (i == blockIdx.x ? 1 : 0)) * a.slot_rows + row;
+        const float2 x = a.part_ml[at];
+        const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - mx);
+        sum = fmaf(w, x.y, sum);
+        const float* src = a.part_o + at * D + lane * (D / 32);
+#pragma unroll
+        for (int e = 0; e < D / 32; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + e);
+            o[e] = fmaf(w, v.x, o[e]);
+            o[e + 1] = fmaf(w, v.y, o[e + 1]);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    const size_t at = static_cast<size_t>(orow) * a.Hq + (head / a.n_hg) * a.G + gh;
+    __half2* dst = reinterpret_cast<__half2*>(a.out + at * D + lane * (D / 32));
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2) dst[e / 2] = __floats2half2_rn(o[e] * inv, o[e + 1] * inv);
+    if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
+}
+
+// Row packing and the workspace: partial rows, their statistics, a description a CTA.
+struct Plan {
+    int G, HG, n_hg, QT1, NT, QTG, slot_rows;
+    size_t off_ml, off_meta, bytes;
+};
+Plan make_plan(int max_q, int Hq, int Hkv, int D) {
+    Plan p;
+    p.G = Hq / Hkv;
+    p.HG = p.G < BM ? p.G : BM;
+    p.n_hg = (p.G + p.HG - 1) / p.HG;
+    p.QT1 = BM / p.HG;
+    p.NT = D <= 128 && max_q > p.QT1 ? 2 : 1;   // D = 256: one O fills TMEM
+    p.QTG = p.NT * p.QT1;
+    p.slot_rows = (max_q < p.QTG ? max_q : p.QTG) * p.HG;
+    const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * p.slot_rows;
+    p.off_ml = (rows * D * 4 + 255) / 256 * 256;
+    p.off_meta = (p.off_ml + rows * 8 + 255) / 256 * 256;
+    p.bytes = p.off_meta + kMaxCtas * 32;
+    return p;
+}
+
+template <int D, int NT, bool CAP>
+attn_status launch(const Prefill8Launch& L, const Plan& p) {
+    using C = Cfg<D, NT>;
+    CUtensorMap tq, tk, tv;
+    Args8 a;
+    a.box_rows = L.page_size < C::BN ? L.page_size : C::BN;
+    attn_status st;
+    {
+        // q [total_q, Hq, D]: boxes of HG heads of QT1 queries, packed rows in row order
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)L.Hq, (uint64_t)L.total_q};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * L.Hq};
+        const uint32_t box[3] = {64u, (uint32_t)p.HG, (uint32_t)p.QT1};
+        if ((st = encode_tmap_sw128(&tq, L.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, strides, box)) != ATTN_OK)
+            return st;
+    }
+    {
+        const uint64_t dims[4] = {(uint64_t)D, (uint64_t)L.Hkv, (uint64_t)L.page_size, (uint64_t)L.n_pages};
+        const uint64_t strides[3] = {(uint64_t)D, (uint64_t)D * L.Hkv, (uint64_t)D * L.Hkv * L.page_size};
+        const uint32_t box[4] = {(uint32_t)D, 1u, (uint32_t)a.box_rows, 1u};
+        if ((st = encode_tmap_plain(&tk, L.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK)
+            return st;
+        if ((st = encode_tmap_plain(&tv, L.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK)
+            return st;
+    }
+    auto kernel = prefill8_kernel<D, NT, CAP>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC) != cudaSuccess)
+            return set_error(ATTN_ECUDA, "cudaFuncSetAttribute(prefill int8 smem) failed");
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(L.workspace);
+    a.q_start = L.q_start;
+    a.kv_len = L.kv_len;
+    a.page_table = L.page_table;
+    a.k_scales = static_cast<const __half*>(L.k_scales);
+    a.v_scales = static_cast<const __half*>(L.v_scales);
+    a.out = static_cast<__half*>(L.out);
+    a.lse = L.lse;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
+    a.meta = reinterpret_cast<int*>(ws + p.off_meta);
+    a.err = L.err_word;
+    a.B = L.B;
+    a.total_q = L.total_q;
+    a.max_q = L.max_q;
+    a.Hq = L.Hq;
+    a.Hkv = L.Hkv;
+    a.G = p.G;
+    a.HG = p.HG;
+    a.n_hg = p.n_hg;
+    a.QT1 = p.QT1;
+    a.QTG = p.QTG;
+    a.P = L.page_size;
+    a.log2P = 0;
+    while ((1 << a.log2P) < L.page_size) ++a.log2P;
+    a.max_pages = L.max_pages;
+    a.n_pages = L.n_pages;
+    a.window = L.window;
+    a.slot_rows = p.slot_rows;
+    const long long cap = static_cast<long long>(L.max_pages) * L.page_size;
+    a.capacity = cap < 0x7ffff000ll ? cap : 0x7ffff000ll;
+    a.max_rg = (L.max_q - 1) / p.QTG + 1;
+    a.scale = L.scale;
+    a.softcap = L.softcap;
+    const int sms = sm_count();
+    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    const dim3 join(grid, (p.slot_rows + kJoinWarps - 1) / kJoinWarps);
+    if (trace_enabled())
+        trace("prefill8_kernel<D=%d,row_tiles=%d,cap=%d> grid=%d block=%d smem=%u key_tile=%d stages=%d heads_per_row_tile=%d "
+              "queries_per_group=%d B=%d total_q=%d Hq=%d Hkv=%d page=%d window=%d, then prefill8_join_kernel grid=(%u,%u)",
+              D, NT, (int)CAP, grid, kThreads, C::SMEM_ALLOC, C::BN, C::NST, p.HG, p.QTG, L.B, L.total_q, L.Hq, L.Hkv,
+              L.page_size, L.window, join.x, join.y);
+    kernel<<<grid, kThreads, C::SMEM_ALLOC, L.stream>>>(tq, tk, tv, a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        prefill8_join_kernel<D><<<join, kJoinWarps * 32, 0, L.stream>>>(a, grid);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return set_error(ATTN_ECUDA, "prefill (int8) launch failed: %s", cudaGetErrorString(e));
+    return ATTN_OK;
+}
+
+template <int D, int NT>
+attn_status launch_cap(const Prefill8Launch& L, const Plan& p) {
+    return L.softcap > 0.f ? launch<D, NT, true>(L, p) : launch<D, NT, false>(L, p);
 }
 
 }  // namespace
 
-size_t prefill8_workspace(int, int, int, int) { return 256; }
+size_t prefill8_workspace(int max_q, int Hq, int Hkv, int D) { return make_plan(max_q, Hq, Hkv, D).bytes; }
 
 attn_status launch_prefill8(const Prefill8Launch& L) {
-    Args8 a;
-    a.L = L;
-    a.log2P = 0;
-    while ((1 << a.log2P) < L.page_size) ++a.log2P;
-    const dim3 grid(L.total_q, L.Hq);
-    if (trace_enabled()) trace("prefill8_kernel<D=%d> grid=(%u,%u) block=%d", L.D, grid.x, grid.y, kTile);
-    if (L.D == 64) prefill8_kernel<64><<<grid, kTile, 0, L.stream>>>(a);
-    else if (L.D == 128) prefill8_kernel<128><<<grid, kTile, 0, L.stream>>>(a);
-    else prefill8_kernel<256><<<grid, kTile, 0, L.stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return set_error(ATTN_ECUDA, "prefill (int8) launch failed: %s", cudaGetErrorString(e));
+    const Plan p = make_plan(L.max_q, L.Hq, L.Hkv, L.D);
+    switch (L.D) {
+        case 64: return p.NT == 2 ? launch_cap<64, 2>(L, p) : launch_cap<64, 1>(L, p);
+        case 128: return p.NT == 2 ? launch_cap<128, 2>(L, p) : launch_cap<128, 1>(L, p);
+        default: return launch_cap<256, 1>(L, p);
+    }
+}
+
+// Sets this translation unit's test controls (see ptx.cuh).
+attn_status set_test_controls_prefill8(unsigned long long wait_limit_ns, int stall) {
+    if (cudaMemcpyToSymbol(g_wait_limit_ns, &wait_limit_ns, sizeof(wait_limit_ns)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_stall_first_tile, &stall, sizeof(stall)) != cudaSuccess)
+        return set_error(ATTN_ECUDA, "test controls (prefill int8): %s", cudaGetErrorString(cudaGetLastError()));
     return ATTN_OK;
 }
 
