@@ -25,13 +25,13 @@
 // workspace, which a second kernel joins.  Long caches with few rows and short ones
 // with many are balanced by the same cut, without the host knowing any length.
 //
-// Roles (16 warps): a TMA warp brings code tiles and scales into a ring of stages; 4
-// or 8 converter warps turn them into f16 operands (128-byte swizzle) in a ring of 3
-// and write the per-key factors; one thread issues the MMAs; 4 or 8 softmax warps.
-// D = 64/128 keep two streams, each with its S (P overwrites it) and O in TMEM and
-// its own softmax warps, which take turns on the tensor cores: the two row tiles of
-// a group, or for a single tile the even and the odd key tiles, joined at the end.
-// D = 256 has one O (its 256 columns) and two S buffers.
+// Roles (20 warps): a TMA warp brings code tiles and scales into a ring of stages; 8
+// converter warps turn codes into f16 operands (128-byte swizzle) in a ring of 3, and
+// one writes the per-key factors; one thread issues the MMAs; 8 softmax warps.
+// D = 64/128 keep two streams, each with its S (P overwrites it) and O in TMEM and 4
+// softmax warps, which take turns on the tensor cores: the two row tiles of a group,
+// or for a single tile the even and the odd key tiles, joined at the end.  D = 256 has
+// one O (its 256 columns) and two S buffers, each read by all 8 softmax warps.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,7 +47,38 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
 constexpr int kMaxCtas = 152;               // one CTA an SM
 constexpr int kMinTiles = 2;                // least key tiles of a run
-constexpr int kThreads = 512;
+// 5 warpgroups.  Registers at launch: 640 x 96; the softmax warpgroups then take
+// theirs from the last one's and the converters'.
+constexpr int kThreads = 640;
+constexpr int kRegSoftmax = 136, kRegConvert = 72, kRegOther = 64;
+static_assert(2 * kRegSoftmax + 2 * kRegConvert + kRegOther == 5 * 96, "register split");
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// The bounded wait of ptx.cuh with its loop out of line: this kernel's roles together
+// run close to the instruction caches' size, and waits are in all of them.
+__device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    return mbar_wait(bar, parity, abort_flag, err, code);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    return mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort_flag, err, code);
+}
+// One arrival of a whole warp: its lanes' earlier writes are ordered before it.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 
 // Per-key factors of a key tile, laid out as the softmax threads read them (a pair
 // of keys a time), and the sign of the value's scale for the converters.
@@ -63,9 +94,8 @@ struct Cfg {
     static constexpr int BN = D == 256 ? 64 : 128;       // keys a tile
     static constexpr int NCH = D / 64;                   // 128-byte chunks of a row of f16
     static constexpr int NS = D == 256 ? 1 : 2;          // streams (O accumulators)
-    static constexpr int NSM = 4 * NS;                   // softmax warps
-    static constexpr int NCV = 12 - NSM;                 // converter warps
-    static constexpr int PROD_WARP = 12, MMA_WARP = 13, Q_WARP = 14;
+    static constexpr int NSM = 8, NCV = 8;               // softmax and converter warps
+    static constexpr int PROD_WARP = 16, MMA_WARP = 17, Q_WARP = 18;   // 19: per-key factors
     static constexpr int RING = 3;                       // f16 operand tiles
     // staged code tiles: what shared memory leaves beside Q and the operand ring
     static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
@@ -86,7 +116,8 @@ struct Cfg {
         B_OPFULL = B_SEMPTY_ST + NST,      // operand tile: converted
         B_OPEMPTY = B_OPFULL + RING,       // operand tile: its MMAs are done
         B_TAB = B_OPEMPTY + RING,          // key factors are there
-        B_QFULL = B_TAB + NTAB,
+        B_TABEMPTY = B_TAB + NTAB,         // their tile's P are done, and its V is converted
+        B_QFULL = B_TABEMPTY + NTAB,
         B_QEMPTY,
         B_S,                               // S of buffer 0, 1
         B_P = B_S + 2,                     // P of buffer 0, 1
@@ -98,9 +129,11 @@ struct Cfg {
         N_BARS
     };
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag, start
-    static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 64 + 1024;
+    static constexpr uint32_t OFF_SEG = OFF_MISC + 16;
+    static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (kThreads / 32 + 1) * 72 + 1024;   // 72: sizeof(Seg)
     static constexpr uint32_t COL_O = 2 * BN;            // S buffers first
     static constexpr uint32_t TMEM_COLS = 512;
+    static_assert(OFF_SEG % 8 == 0, "alignment");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
     static_assert(COL_O + NS * D <= TMEM_COLS, "TMEM budget");
@@ -117,6 +150,7 @@ struct Args8 {
     int* meta;           // [CTA][8]
     int* err;
     int B, total_q, max_q, Hq, Hkv, G, HG, n_hg, QT1, QTG;   // QT1 queries a row tile, QTG a group
+    int hp, n_hb;        // heads (kv heads x head groups) taken side by side, batches of them
     int P, log2P, max_pages, n_pages, box_rows, window, slot_rows;
     long long capacity;
     int max_rg;
@@ -152,50 +186,66 @@ __device__ __forceinline__ Span group_span(const Args8& a, const Chunk& c, int r
     return s;
 }
 
-// A CTA's run of key tiles as segments, each of one item.  Every role walks it alike.
-struct Start {
-    int b, rg, head, off;
-    long long rem;
+// A CTA's run of key tiles as segments, each of one item; every warp walks it alike,
+// with its state in shared memory (segments are long, and the code of a step is kept
+// out of the roles).
+struct Seg {
+    int b, rg, hb, off, n_rg;
+    int head;                 // kv head and head group
+    int n, tiles;             // key tiles of this segment and of its item
+    int lo, hi, key0;         // keys some row keeps; the segment's first key
+    int q_base, n_rows, pos0;
+    int two;                  // two row tiles (every key tile is used twice), or one
+    long long rem;            // key tiles of the run from this segment on; 0: the end
 };
+static_assert(sizeof(Seg) == 72, "shared memory budget");
 template <int BN>
-struct Walk {
-    int b, rg, head, off, n, n_rg;
-    long long rem;
-    Chunk c;
-    Span s;
-    __device__ __forceinline__ Walk(const Args8& a, const Start& st)
-        : b(st.b), rg(st.rg), head(st.head), off(st.off), n(0), n_rg(0), rem(st.rem) {
-        if (rem > 0) {
-            c = load_chunk(a, b);
-            n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
-            s = group_span<BN>(a, c, rg);
-            n = static_cast<int>(min(static_cast<long long>(s.tiles - off), rem));
-        }
-    }
-    __device__ __forceinline__ void next(const Args8& a) {
-        rem -= n;
-        off = 0;
-        if (rem <= 0) return;
-        if (++head == a.Hkv * a.n_hg) {
-            head = 0;
-            ++rg;
-            while (rg >= n_rg) {
-                if (++b >= a.B) {
-                    rem = 0;
-                    return;
+__device__ __forceinline__ void seg_item(const Args8& a, Seg& s) {
+    const Chunk c = load_chunk(a, s.b);
+    const Span sp = group_span<BN>(a, c, s.rg);
+    s.n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
+    s.tiles = sp.tiles;
+    s.lo = sp.lo;
+    s.hi = sp.hi;
+    s.key0 = (sp.jt0 + s.off) * BN;
+    s.q_base = c.q_base;
+    s.n_rows = c.n_rows;
+    s.pos0 = c.pos0;
+    s.two = a.QTG > a.QT1 && c.n_rows - s.rg * a.QTG > a.QT1;
+    s.n = static_cast<int>(min(static_cast<long long>(s.tiles - s.off), s.rem));
+}
+// The first segment (b, rg, hb, off and rem are set), or the next one.  Returns false
+// at the end of the run.
+template <int BN>
+__device__ __forceinline__ void seg_step(const Args8& a, Seg& s, bool first) {
+    for (;; first = false) {
+        if (!first) {
+            s.rem -= s.n;
+            s.off = 0;
+            if (s.rem > 0 && ++s.hb == a.n_hb) {
+                s.hb = 0;
+                if (++s.rg >= s.n_rg) {
+                    s.rg = 0;
+                    do {
+                        if (++s.b >= a.B) s.rem = 0;   // (q_start changed under the call)
+                    } while (s.rem > 0 && load_chunk(a, s.b).n_rows == 0);
                 }
-                c = load_chunk(a, b);
-                n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
-                rg = 0;
             }
-            s = group_span<BN>(a, c, rg);
         }
-        n = static_cast<int>(min(static_cast<long long>(s.tiles), rem));
+        if (s.rem <= 0) return;
+        seg_item<BN>(a, s);
+        s.head = s.hb * a.hp + static_cast<int>(blockIdx.x) % a.hp;
+        if (s.head < a.Hkv * a.n_hg) return;   // the last batch may have fewer heads
     }
-    __device__ __forceinline__ bool whole() const { return off == 0 && n == s.tiles; }
-    // two row tiles (every key tile twice), or one
-    __device__ __forceinline__ bool two(const Args8& a) const { return a.QTG > a.QT1 && c.n_rows - rg * a.QTG > a.QT1; }
-};
+}
+// `lanes` of a warp, all of which call it, move to its first or next segment.
+template <int BN>
+__device__ __forceinline__ bool seg_next(const Args8& a, Seg& s, bool first, int lane, unsigned lanes) {
+    __syncwarp(lanes);
+    if (lane == 0) seg_step<BN>(a, s, first);
+    __syncwarp(lanes);
+    return s.rem > 0;
+}
 
 // The order in which a segment of n key tiles loads them, which is the order the
 // MMAs first need them in: with two row tiles K0 V0 K1 V1 ..; with one, S of the next
@@ -242,7 +292,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const uint32_t sbase = smem_u32(smem);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    Start* start_s = reinterpret_cast<Start*>(smem + C::OFF_MISC + 16);
+    Seg* segs = reinterpret_cast<Seg*>(smem + C::OFF_SEG);   // one a warp
+    Seg& first_seg = segs[kThreads / 32];
     KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [stream][row]
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
@@ -257,21 +308,18 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const long long f0 = min(pairs, tid * per), f1 = min(pairs, f0 + per);
         // visits this thread's pairs in order until fn says stop
         auto visit = [&](auto fn) {
-            Chunk c;
-            int bb = -1, n_rg = 0;
-            for (long long f = f0; f < f1;) {
-                const int b = static_cast<int>(f / a.max_rg), rg = static_cast<int>(f % a.max_rg);
-                if (b != bb) {
-                    c = load_chunk(a, b);
-                    n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
-                    bb = b;
-                }
-                if (rg >= n_rg) {
-                    f = static_cast<long long>(b + 1) * a.max_rg;
-                    continue;
-                }
-                if (!fn(b, rg, group_span<BN>(a, c, rg).tiles)) break;
-                ++f;
+            if (f0 >= f1) return;
+            int b = static_cast<int>(f0 / a.max_rg), rg = static_cast<int>(f0 - static_cast<long long>(b) * a.max_rg);
+            long long left = f1 - f0;
+            while (left > 0) {
+                const Chunk c = load_chunk(a, b);
+                const int n_rg = (c.n_rows + a.QTG - 1) / a.QTG;
+                const int end = static_cast<int>(min(static_cast<long long>(n_rg), rg + left));
+                for (int r = rg; r < end; ++r)
+                    if (!fn(b, r, group_span<BN>(a, c, r).tiles)) return;
+                left -= a.max_rg - rg;
+                rg = 0;
+                ++b;
             }
         };
         long long mine = 0;
@@ -287,25 +335,27 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         if (lane == 31) sums[warp] = incl;
         if (tid == 0) {
-            start_s->rem = 0;
             for (int i = 0; i < NST; ++i) {
                 mbar_init(bar(C::B_SFULL_ST + i), 1);
-                mbar_init(bar(C::B_SEMPTY_ST + i), C::NCV * 32);
+                mbar_init(bar(C::B_SEMPTY_ST + i), C::NCV + 1);
             }
             for (int i = 0; i < RING; ++i) {
-                mbar_init(bar(C::B_OPFULL + i), C::NCV * 32);
+                mbar_init(bar(C::B_OPFULL + i), C::NCV);
                 mbar_init(bar(C::B_OPEMPTY + i), 1);
             }
-            for (int i = 0; i < C::NTAB; ++i) mbar_init(bar(C::B_TAB + i), C::NCV * 32);
+            for (int i = 0; i < C::NTAB; ++i) {
+                mbar_init(bar(C::B_TAB + i), 1);
+                mbar_init(bar(C::B_TABEMPTY + i), 1);
+            }
             mbar_init(bar(C::B_QFULL), 1);
             mbar_init(bar(C::B_QEMPTY), 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(bar(C::B_S + i), 1);
-                mbar_init(bar(C::B_P + i), 128);
+                mbar_init(bar(C::B_P + i), C::NSM / C::NS);
             }
             mbar_init(bar(C::B_DONE), 1);
-            mbar_init(bar(C::B_OFREE), C::NSM * 32);
-            mbar_init(bar(C::B_ML), C::NSM * 32);
+            mbar_init(bar(C::B_OFREE), C::NSM);
+            mbar_init(bar(C::B_ML), C::NSM);
             mbar_init(bar(C::B_PV), 1);
             mbar_init(bar(C::B_TEARDOWN), 1);
             *abort_flag = 0;
@@ -316,6 +366,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tmem_relinquish();
         }
         tc_fence_before();
+        if (tid == 0) first_seg.rem = 0;   // an empty run, unless a thread finds its start
         __syncthreads();
         tc_fence_after();
         long long before = 0, total = 0;
@@ -325,25 +376,25 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             total += sums[w];
         }
         before += incl - mine;
-        const int heads = a.Hkv * a.n_hg;
-        const long long all = total * heads;
-        // as many runs as CTAs, or fewer of kMinTiles
-        const long long runs = max(1ll, min(static_cast<long long>(gridDim.x), all / kMinTiles));
-        const long long t0 = blockIdx.x < runs ? all * blockIdx.x / runs : all;
-        const long long t1 = blockIdx.x < runs ? all * (blockIdx.x + 1) / runs : all;
-        if (t0 < t1 && before * heads <= t0 && t0 < (before + mine) * heads) {   // one thread
+        // as many runs as CTAs for each of the hp heads, or fewer of kMinTiles
+        const long long all = total * a.n_hb;
+        const int rank = static_cast<int>(blockIdx.x) / a.hp;
+        const long long runs = max(1ll, min(static_cast<long long>(gridDim.x / a.hp), all / kMinTiles));
+        const long long t0 = rank < runs ? all * rank / runs : all;
+        const long long t1 = rank < runs ? all * (rank + 1) / runs : all;
+        if (t0 < t1 && before * a.n_hb <= t0 && t0 < (before + mine) * a.n_hb) {   // one thread
             long long acc = before;
             visit([&](int b, int rg, int t) {
-                if ((acc + t) * heads <= t0) {
+                if ((acc + t) * a.n_hb <= t0) {
                     acc += t;
                     return true;
                 }
-                const long long in = t0 - acc * heads;
-                start_s->b = b;
-                start_s->rg = rg;
-                start_s->head = static_cast<int>(in / t);
-                start_s->off = static_cast<int>(in % t);
-                start_s->rem = t1 - t0;
+                const long long in = t0 - acc * a.n_hb;
+                first_seg.b = b;
+                first_seg.rg = rg;
+                first_seg.hb = static_cast<int>(in / t);
+                first_seg.off = static_cast<int>(in - static_cast<long long>(first_seg.hb) * t);
+                first_seg.rem = t1 - t0;
                 return false;
             });
         }
@@ -351,15 +402,20 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         __syncthreads();
     }
     const uint32_t tmem = *tmem_holder;
-    const Start start = *start_s;
-    Walk<BN> w(a, start);
+    Seg& w = segs[warp];
+    if (lane == 0) w = first_seg;
     if (tid == 0) {
+        Seg s = first_seg;
+        seg_step<BN>(a, s, true);
         int* m = a.meta + blockIdx.x * 8;
-        m[0] = w.rem > 0 && w.off > 0;          // begins inside an item
-        m[1] = w.rem > 0 && w.n == w.s.tiles - w.off;   // and ends it
-        m[2] = 0;                               // ends inside another (set below)
+        m[0] = s.rem > 0 && s.off > 0;                  // begins inside an item
+        m[1] = s.rem > 0 && s.n == s.tiles - s.off;     // and ends it
+        m[2] = 0;                                       // ends inside another (set below)
     }
 
+    // (setmaxnreg is executed by all four warps of a warpgroup)
+    if (warp >= C::PROD_WARP) {
+    regs_dec<kRegOther>();
     if (warp == C::PROD_WARP) {
         // ------------------------------------------------------------ codes and scales
         // lanes 0-15, lane i the box of the tile's i-th page (one box inside a page that
@@ -375,35 +431,37 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const bool has_box = lane * R < BN;
             uint32_t gi = 0;   // tiles loaded by this CTA so far
             int ok = 1;
-            for (; ok && w.rem > 0; w.next(a)) {
-                const bool two = w.two(a);
+            for (bool more = seg_next<BN>(a, w, true, lane, gmask); ok && more;
+                 more = seg_next<BN>(a, w, false, lane, gmask)) {
+                const bool two = NT == 2 && w.two;
+                const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0 + lane * R;
                 const int g = w.head / a.n_hg;
                 const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
                 // page id of this lane's box in item i
                 auto fetch = [&](int i) {
                     int j;
-                    if (i >= 2 * w.n) return 0;
-                    item_of(two, i, w.n, j);
-                    const int kk = (w.s.jt0 + w.off + j) * BN + lane * R;
-                    return has_box && kk >= w.s.lo - R + 1 && kk < w.s.hi ? __ldg(&table[kk >> a.log2P]) : 0;
+                    if (i >= 2 * n) return 0;
+                    item_of(two, i, n, j);
+                    const int kk = k0 + j * BN;
+                    return has_box && kk >= lo - R + 1 && kk < hi ? __ldg(&table[kk >> a.log2P]) : 0;
                 };
                 int pg = fetch(0);
-                for (int i = 0; i < 2 * w.n; ++i, ++gi) {
+                for (int i = 0; i < 2 * n; ++i, ++gi) {
                     const uint32_t st = gi % NST;
                     if (gi >= NST) {
                         if (leader)
-                            ok = mbar_wait(bar(C::B_SEMPTY_ST + st), ((gi / NST) - 1) & 1, abort_flag, a.err,
+                            ok = wait(bar(C::B_SEMPTY_ST + st), ((gi / NST) - 1) & 1, abort_flag, a.err,
                                            kErrTimeoutSlot);
                         ok = __shfl_sync(gmask, ok, 0);
                         if (!ok) break;
                     }
                     int j;
-                    const bool is_k = item_of(two, i, w.n, j);
-                    const int kk = (w.s.jt0 + w.off + j) * BN + lane * R;
+                    const bool is_k = item_of(two, i, n, j);
+                    const int kk = k0 + j * BN;
                     // boxes without a key of [lo, hi), and pages outside the pool, take the page
                     // coordinate n_pages, so that the copy fills zeros, and zero scales
                     int page = a.n_pages, row = 0;
-                    if (has_box && kk >= w.s.lo - R + 1 && kk < w.s.hi) {
+                    if (has_box && kk >= lo - R + 1 && kk < hi) {
                         if (pg >= 0 && pg < a.n_pages) {
                             page = pg;
                             row = kk & (a.P - 1);
@@ -449,16 +507,16 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (lane == 0) {
             tma_prefetch_desc(&tm_q);
             uint32_t seg = 0;
-            for (; w.rem > 0; w.next(a), ++seg) {
+            for (bool more = seg_next<BN>(a, w, true, 0, 1u); more; more = seg_next<BN>(a, w, false, 0, 1u), ++seg) {
                 if (seg > 0 &&
-                    !mbar_wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot)) break;
-                const int nt = w.two(a) ? 2 : 1;
+                    !wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot)) break;
+                const int nt = w.two ? 2 : 1;
                 const int h0 = (w.head / a.n_hg) * a.G + (w.head % a.n_hg) * a.HG;
                 mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
                 for (int t = 0; t < nt; ++t)
                     for (int c = 0; c < NCH; ++c)
                         tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64, h0,
-                                    w.c.q_base + w.rg * a.QTG + t * a.QT1);
+                                    w.q_base + w.rg * a.QTG + t * a.QT1);
             }
             if (*abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
         }
@@ -472,16 +530,17 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const uint64_t v_desc = smem_desc_sw128(sbase + C::OFF_OP, C::OP_CHUNK, 1024);
             // testing hook: hold back the signal of the first S tile
             const bool stall = stall_first_tile();
-            uint32_t base = 0, u0 = 0, seg = 0;   // tiles and units before this segment
+            uint32_t base = 0, jt = 0, u0 = 0, seg = 0;   // items, key tiles and units before this segment
             bool ok = true;
-            for (; ok && w.rem > 0; w.next(a), ++seg) {
-                const bool two = NT == 2 && w.two(a);
+            for (bool more = seg_next<BN>(a, w, true, 0, 1u); ok && more;
+                 more = seg_next<BN>(a, w, false, 0, 1u), ++seg) {
+                const bool two = NT == 2 && w.two;
                 const int n = w.n, U = two ? 2 * n : n;
-                ok = mbar_wait(bar(C::B_QFULL), seg & 1, abort_flag, a.err, kErrTimeoutLoad);
+                ok = wait(bar(C::B_QFULL), seg & 1, abort_flag, a.err, kErrTimeoutLoad);
                 auto issue_s = [&](int u) -> bool {
                     const int j = two ? u >> 1 : u;
                     const uint32_t gi = base + item_k(two, j), slot = gi % RING, buf = (u0 + u) & 1;
-                    if (!mbar_wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad))
+                    if (!wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad))
                         return false;
                     tc_fence_after();
                     const uint64_t kd = desc_advance(k_desc, slot * C::OP_BYTES);
@@ -505,13 +564,14 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     const uint32_t buf = (u0 + u) & 1;
                     const int j = two ? u >> 1 : u;
                     const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
-                    ok = mbar_wait(bar(C::B_P + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax) &&
-                         mbar_wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                    ok = wait(bar(C::B_P + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax) &&
+                         wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad);
                     // O still holds the segment before until its rows have been read
                     if (ok && u == 0 && seg > 0)
-                        ok = mbar_wait(bar(C::B_OFREE), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax);
+                        ok = wait(bar(C::B_OFREE), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax);
                     if (!ok) break;
                     tc_fence_after();
+                    if (!two || (u & 1)) mbar_arrive(bar(C::B_TABEMPTY + (jt + j) % C::NTAB));
                     const uint64_t vd = desc_advance(v_desc, slot * C::OP_BYTES);
                     const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll
@@ -523,141 +583,190 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 if (ok) tc_commit(bar(C::B_DONE));
                 base += 2 * n;
+                jt += n;
                 u0 += U;
             }
             tc_commit(bar(C::B_TEARDOWN));   // all MMAs retire before TMEM is released
             mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
         }
-    } else if (warp >= C::NSM && warp < 12) {
+    } else {
+        // ------------------------------------------------------------ per-key factors
+        const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
+        uint32_t gi = 0, jt = 0;    // tiles and key tiles before this one
+        bool ok = true;
+        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
+             more = seg_next<BN>(a, w, false, lane, 0xffffffffu)) {
+            const bool two = NT == 2 && w.two;
+            const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0;
+            for (int i = 0; i < 2 * n; ++i, ++gi) {
+                int j;
+                const bool is_k = item_of(two, i, n, j);
+                const uint32_t st = gi % NST, tb = (jt + j) % C::NTAB;
+                ok = wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                if (ok && is_k && jt + j >= C::NTAB)
+                    ok = wait(bar(C::B_TABEMPTY + tb), ((jt + j) / C::NTAB - 1) & 1, abort_flag, a.err,
+                                   kErrTimeoutSoftmax);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (is_k) {
+                    KeyFactors<BN>& t = tab[tb];
+                    const __half* sc = reinterpret_cast<const __half*>(smem + C::OFF_SCALE + st * C::SCALE_BYTES);
+                    const int key0 = k0 + j * BN;
+#pragma unroll 1
+                    for (int x = 0; x < BN / 64; ++x) {
+                        const int pr = x * 32 + lane;   // a pair of keys
+                        const float2 ks2 = __half22float2(*reinterpret_cast<const __half2*>(sc + 2 * pr));
+                        const float2 vs2 = __half22float2(*reinterpret_cast<const __half2*>(sc + BN + 2 * pr));
+                        float f[2], lv[2], iv[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + 2 * pr + e;
+                            const float ks = e ? ks2.y : ks2.x, vs = e ? vs2.y : vs2.x;
+                            const bool in = key >= lo && key < hi;
+                            const bool fin = isfinite(ks) && isfinite(vs);
+                            // a value scale of 0 counts as the smallest f16 with codes of 0; a scale
+                            // that is not finite makes the logit NaN, which only rows that keep the
+                            // key take; keys outside [lo, hi) get factors that cannot spoil anything
+                            const float av = in && fin ? fmaxf(fabsf(vs), 0x1p-24f) : 1.f;
+                            f[e] = !in ? 0.f : fin ? ks * kf : __int_as_float(0x7fc00000);
+                            lv[e] = log2f(av);
+                            iv[e] = 1.f / av;
+                            t.sign[2 * pr + e] = !in || !fin || vs == 0.f ? 0u : vs > 0.f ? 0x3c003c00u : 0xbc00bc00u;
+                        }
+                        t.a[pr] = make_float4(f[0], f[1], lv[0], lv[1]);
+                        t.b[pr] = make_float2(iv[0], iv[1]);
+                    }
+                    warp_arrive(bar(C::B_TAB + tb), lane);
+                }
+                warp_arrive(bar(C::B_SEMPTY_ST + st), lane);
+            }
+            jt += n;
+        }
+    }
+    } else if (warp >= C::NSM) {
         // ------------------------------------------------------------ converters
+        regs_dec<kRegConvert>();
         constexpr int CT = C::NCV * 32;               // threads
         constexpr int CH = BN * D / 16 / CT;          // 16-code pieces a thread
-        static_assert(CH % 4 == 0 && CT >= BN, "converter split");
         const int ct = tid - C::NSM * 32;
-        const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
         uint32_t gi = 0, jt = 0;    // tiles converted; key tiles before this segment
         bool ok = true;
-        for (; ok && w.rem > 0; w.next(a)) {
-            const bool two = NT == 2 && w.two(a);
-            for (int i = 0; i < 2 * w.n; ++i, ++gi) {
+        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
+             more = seg_next<BN>(a, w, false, lane, 0xffffffffu)) {
+            const bool two = NT == 2 && w.two;
+            const int n = w.n;
+            for (int i = 0; i < 2 * n; ++i, ++gi) {
                 int j;
-                const bool is_k = item_of(two, i, w.n, j);
+                const bool is_k = item_of(two, i, n, j);
                 const uint32_t st = gi % NST, slot = gi % RING, tb = (jt + j) % C::NTAB;
-                ok = mbar_wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
-                if (ok && gi >= RING)
-                    ok = mbar_wait(bar(C::B_OPEMPTY + slot), ((gi / RING) - 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                ok = wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
                 if (ok && !is_k)   // the signs of this tile's value scales
-                    ok = mbar_wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                    ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad);
                 if (!ok) break;
-                KeyFactors<BN>& t = tab[tb];
-                if (is_k) {
-                    if (ct < BN) {
-                        const __half* sc = reinterpret_cast<const __half*>(smem + C::OFF_SCALE + st * C::SCALE_BYTES);
-                        const int key = (w.s.jt0 + w.off + j) * BN + ct;
-                        const bool in = key >= w.s.lo && key < w.s.hi;
-                        const float ks = __half2float(sc[ct]), vs = __half2float(sc[BN + ct]);
-                        const bool fin = isfinite(ks) && isfinite(vs);
-                        // a value scale of 0 counts as the smallest f16 with codes of 0; a scale
-                        // that is not finite makes the logit NaN, which only rows that keep the
-                        // key take; keys outside [lo, hi) get factors that cannot spoil anything
-                        const float av = in && fin ? fmaxf(fabsf(vs), 0x1p-24f) : 1.f;
-                        float* fa = reinterpret_cast<float*>(&t.a[ct >> 1]);
-                        fa[ct & 1] = !in ? 0.f : fin ? ks * kf : __int_as_float(0x7fc00000);
-                        fa[2 + (ct & 1)] = log2f(av);
-                        reinterpret_cast<float*>(&t.b[ct >> 1])[ct & 1] = 1.f / av;
-                        t.sign[ct] = !in || !fin || vs == 0.f ? 0u : vs > 0.f ? 0x3c003c00u : 0xbc00bc00u;
-                    }
-                    mbar_arrive(bar(C::B_TAB + tb));
-                }
                 const uint8_t* src = smem + C::OFF_CODE + st * C::CODE_BYTES;
                 uint8_t* dst = smem + C::OFF_OP + slot * C::OP_BYTES;
                 const __half2 one = __float2half2_rn(1.f), shift = __float2half2_rn(-1152.f);
+                uint4 v[CH];
+                uint32_t sg[CH];
 #pragma unroll
-                for (int c0 = 0; c0 < CH; c0 += 4) {
-                    uint4 v[4];
+                for (int c = 0; c < CH; ++c) {
+                    v[c] = *reinterpret_cast<const uint4*>(src + (c * CT + ct) * 16);
+                    if (!is_k) sg[c] = tab[tb].sign[(c * CT + ct) / (D / 16)];
+                }
+                if (gi >= RING)
+                    ok = wait(bar(C::B_OPEMPTY + slot), ((gi / RING) - 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                if (!ok) break;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(src + ((c0 + c) * CT + ct) * 16);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int piece = (c0 + c) * CT + ct;
-                        const int row = piece / (D / 16), part = piece % (D / 16);
-                        __half2 s = one, off = shift;
-                        if (!is_k) {
-                            const uint32_t sg = t.sign[row];
-                            s = *reinterpret_cast<const __half2*>(&sg);
-                            off = __hmul2(s, shift);
-                        }
-                        uint4 x, y;
-                        codes_to_f16(v[c].x, s, off, x.x, x.y);
-                        codes_to_f16(v[c].y, s, off, x.z, x.w);
-                        codes_to_f16(v[c].z, s, off, y.x, y.y);
-                        codes_to_f16(v[c].w, s, off, y.z, y.w);
-                        // two 16-byte units of the row's 128-byte line; the lanes of the second
-                        // line store them the other way round, so that no two lanes of a store
-                        // meet in a bank
-                        uint8_t* line = dst + (part >> 2) * C::OP_CHUNK + row * 128;
-                        const int u = (part & 3) * 2, sw = row & 7;
-                        const bool flip = (part & 4) != 0;
-                        *reinterpret_cast<uint4*>(line + (((u + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
-                        *reinterpret_cast<uint4*>(line + (((u + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
+                for (int c = 0; c < CH; ++c) {
+                    const int piece = c * CT + ct;
+                    const int row = piece / (D / 16), part = piece % (D / 16);
+                    __half2 s = one, off = shift;
+                    if (!is_k) {
+                        s = *reinterpret_cast<const __half2*>(&sg[c]);
+                        off = __hmul2(s, shift);
                     }
+                    uint4 x, y;
+                    codes_to_f16(v[c].x, s, off, x.x, x.y);
+                    codes_to_f16(v[c].y, s, off, x.z, x.w);
+                    codes_to_f16(v[c].z, s, off, y.x, y.y);
+                    codes_to_f16(v[c].w, s, off, y.z, y.w);
+                    // two 16-byte units of the row's 128-byte line; the lanes of the second
+                    // line store them the other way round, so that no two lanes of a store
+                    // meet in a bank
+                    uint8_t* line = dst + (part >> 2) * C::OP_CHUNK + row * 128;
+                    const int u = (part & 3) * 2, sw = row & 7;
+                    const bool flip = (part & 4) != 0;
+                    *reinterpret_cast<uint4*>(line + (((u + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
+                    *reinterpret_cast<uint4*>(line + (((u + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(bar(C::B_OPFULL + slot));
-                mbar_arrive(bar(C::B_SEMPTY_ST + st));
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_OPFULL + slot));
+                    mbar_arrive(bar(C::B_SEMPTY_ST + st));
+                }
             }
-            jt += w.n;
+            jt += n;
         }
-    } else if (warp < C::NSM) {
+    } else {
         // ------------------------------------------------------------ softmax
-        const int ws = warp >> 2;                  // stream
+        regs_inc<kRegSoftmax>();
+        const int ws = warp >> 2;                  // stream; one stream: the half of each quarter's rows
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const float cap_log2 = a.softcap * kLog2e;
         uint32_t u0 = 0, jt = 0, seg = 0;
         bool ok = true;
-        for (; ok && w.rem > 0; w.next(a), ++seg) {
-            const bool two = NT == 2 && w.two(a);
-            const int n = w.n, U = two ? 2 * n : n;
+        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
+             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
+            const bool two = NT == 2 && w.two;
+            const int n = w.n, U = two ? 2 * n : n, k0 = w.key0;
             // this warpgroup's units: those of its stream (all, if there is one)
             const int first_u = C::NS == 1 ? 0 : static_cast<int>((ws ^ u0) & 1);
+            constexpr int XN = C::NS == 1 ? 2 : 4;   // rows of a thread
+            const int half0 = C::NS == 1 ? ws : 0;   // its first 16-row half
             const int rt = two ? first_u : 0;      // row tile
             const int q0 = w.rg * a.QTG + rt * a.QT1;
-            // a thread holds rows quarter*32 + 16 x + lane / 4 (+ 8), x = 0, 1, and of every 8
+            // of each 16-row half a thread holds rows lane / 4 and lane / 4 + 8, and of every 8
             // columns the pair 2 (lane % 4): the per-key factors are then one 16- and one
             // 8-byte load for 4 rows and 2 keys
-            int pos[4];
-            float m[4], l[4];
+            // a row keeps the keys [klo, khi)
+            int klo[XN], khi[XN];
+            float m[XN], l[XN];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                pos[x] = w.c.pos0 + q0 + (quarter * 32 + x * 8 + (lane >> 2)) / a.HG;
+            for (int x = 0; x < XN; ++x) {
+                const int pos = w.pos0 + q0 + (quarter * 32 + half0 * 16 + x * 8 + (lane >> 2)) / a.HG;
+                khi[x] = min(w.hi, pos + 1);
+                klo[x] = a.window > 0 ? max(0, pos - min(a.window, 0x3fffffff) + 1) : 0;
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
             for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t buf = (u0 + u) & 1, tb = (jt + j) % C::NTAB;
-                ok = mbar_wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
-                     mbar_wait(bar(C::B_S + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
+                     wait(bar(C::B_S + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
                 ok = __all_sync(0xffffffffu, ok);   // tcgen05 loads and stores need whole warps
                 if (!ok) break;
                 tc_fence_after();
                 const KeyFactors<BN>& t = tab[tb];
-                const int key0 = (w.s.jt0 + w.off + j) * BN;
-#pragma unroll
-                for (int hlf = 0; hlf < 2; ++hlf) {
-                    const uint32_t rows = lanes + (static_cast<uint32_t>(hlf * 16) << 16);
+                const int key0 = k0 + j * BN;
+                // (one copy of the code; the rows' state changes places after each half)
+#pragma unroll 1
+                for (int hlf = 0; hlf < XN / 2; ++hlf) {
+                    const uint32_t rows = lanes + (static_cast<uint32_t>((half0 + hlf) * 16) << 16);
                     const uint32_t s_addr = rows + buf * BN;
                     float2 y[2][BN / 8];           // [row of the half][8-column group]
+                    {
+                        uint32_t r[BN / 64][32];
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) {
-                        uint32_t r[32];
-                        tc_ld_16x256b_x8(s_addr + c * 64, r);
+                        for (int c = 0; c < BN / 64; ++c) tc_ld_16x256b_x8(s_addr + c * 64, r[c]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            y[0][c * 8 + i] = make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]));
-                            y[1][c * 8 + i] = make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                        for (int i = 0; i < BN / 8; ++i) {
+                            const uint32_t* q = &r[i / 8][4 * (i % 8)];
+                            y[0][i] = make_float2(__uint_as_float(q[0]), __uint_as_float(q[1]));
+                            y[1][i] = make_float2(__uint_as_float(q[2]), __uint_as_float(q[3]));
                         }
                     }
                     if constexpr (CAP) {
@@ -704,72 +813,89 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                 y[x][i] = ffma2(y[x][i], make_float2(f.x, f.y), make_float2(f.z, f.w));
                         }
                     }
-                    const int pa = pos[2 * hlf], pb = pos[2 * hlf + 1];
-                    const int key_last = key0 + BN - 1;
-                    bool full = key_last < w.s.hi && key_last <= pa && key_last <= pb;
-                    if (a.window > 0) full = full && pa - key0 < a.window && pb - key0 < a.window;
-                    if (!full) {
+                    const bool full = key0 >= max(klo[0], klo[1]) && key0 + BN <= min(khi[0], khi[1]);
+                    if (!__all_sync(0xffffffffu, full)) {
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const int kj = key0 + 8 * i + 2 * (lane & 3);
+                        for (int x = 0; x < 2; ++x) {
+                            const int from = klo[x] - key0 - 2 * (lane & 3);
+                            const unsigned count = max(khi[x] - klo[x], 0);
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int p = x ? pb : pa;
-                                bool k0 = kj < w.s.hi && kj <= p, k1 = kj + 1 < w.s.hi && kj + 1 <= p;
-                                if (a.window > 0) {
-                                    k0 = k0 && p - kj < a.window;
-                                    k1 = k1 && p - kj - 1 < a.window;
-                                }
-                                if (!k0) y[x][i].x = -INFINITY;
-                                if (!k1) y[x][i].y = -INFINITY;
+                            for (int i = 0; i < BN / 8; ++i) {
+                                if (static_cast<unsigned>(8 * i - from) >= count) y[x][i].x = -INFINITY;
+                                if (static_cast<unsigned>(8 * i + 1 - from) >= count) y[x][i].y = -INFINITY;
                             }
                         }
                     }
-                    // running maxima of the two rows (their 4 lanes agree on them)
-                    float alpha[2] = {1.f, 1.f}, m_off[2];
-                    bool need = false;
+                    // P = f16(2^(y - m)), sums of 2^(y - m) / vs.  A row keeps its m while no y
+                    // exceeds it by more than the threshold (P stays at most 2^8), so that the
+                    // lanes of a row need not agree on the tile's maximum
+                    auto exps = [&](float (&sum)[2]) {
+                        float2 ls[2][2] = {};
+                        float2 nm[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float mu = m[x] == -INFINITY ? 0.f : -m[x];
+                            nm[x] = make_float2(mu, mu);
+                        }
+#pragma unroll
+                        for (int c = 0; c < BN / 64; ++c) {
+                            uint32_t packed[16];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 iv = t.b[4 * (c * 8 + i) + (lane & 3)];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const float2 d = fadd2(y[x][c * 8 + i], nm[x]);
+                                    const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                                    ls[x][i & 1] = ffma2(p, iv, ls[x][i & 1]);
+                                    const __half2 hp = __floats2half2_rn(p.x, p.y);
+                                    packed[2 * i + x] = *reinterpret_cast<const uint32_t*>(&hp);
+                                }
+                            }
+                            tc_st_16x128b_x8(s_addr + c * 32, packed);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 z = fadd2(ls[x][0], ls[x][1]);
+                            sum[x] = z.x + z.y;
+                        }
+                    };
+                    float sum[2], mx[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float mx = -INFINITY;
+                        float q[4];
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) mx = fmaxf(mx, fmaxf(y[x][i].x, y[x][i].y));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        float& mu = m[2 * hlf + x];
-                        if (mx > mu + kRescaleThreshold || (mu == -INFINITY && mx > -INFINITY)) {
-                            alpha[x] = mu == -INFINITY ? 0.f : ex2_approx(mu - mx);
-                            l[2 * hlf + x] *= alpha[x];
-                            mu = mx;
-                            need = true;
-                        }
-                        m_off[x] = mu == -INFINITY ? 0.f : mu;
+                        for (int e = 0; e < 4; ++e) q[e] = fmaxf(y[x][e].x, y[x][e].y);
+#pragma unroll
+                        for (int i = 4; i < BN / 8; ++i) q[i & 3] = max3(q[i & 3], y[x][i].x, y[x][i].y);
+                        mx[x] = fmaxf(max3(q[0], q[1], q[2]), q[3]);
                     }
-                    // exponentials: P = f16(2^(y - m)), l += 2^(y - m) / vs
-                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const bool over = mx[0] > m[0] + kRescaleThreshold ||
+                                      mx[1] > m[1] + kRescaleThreshold;   // m = -inf: any kept key
+                    float alpha[2] = {1.f, 1.f};
+                    const bool moved = __any_sync(0xffffffffu, over);
+                    if (moved) {
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) {
-                        uint32_t packed[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 iv = t.b[4 * (c * 8 + i) + (lane & 3)];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float2 d = fadd2(y[x][c * 8 + i], make_float2(-m_off[x], -m_off[x]));
-                                const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-                                ls[x] = ffma2(p, iv, ls[x]);
-                                const __half2 hp = __floats2half2_rn(p.x, p.y);
-                                packed[2 * i + x] = *reinterpret_cast<const uint32_t*>(&hp);
+                        for (int x = 0; x < 2; ++x) {
+                            float v = mx[x];       // the row's 4 lanes agree on its maximum
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                            float& mu = m[x];
+                            if (v > mu + kRescaleThreshold) {
+                                alpha[x] = mu == -INFINITY ? 0.f : ex2_approx(mu - v);
+                                l[x] *= alpha[x];
+                                mu = v;
                             }
                         }
-                        tc_st_16x128b_x8(s_addr + c * 32, packed);
                     }
-                    l[2 * hlf] += ls[0].x + ls[0].y;
-                    l[2 * hlf + 1] += ls[1].x + ls[1].y;
+                    exps(sum);
+                    l[0] += sum[0];
+                    l[1] += sum[1];
                     // the stream's O is rescaled when a maximum moved.  Its last PV has retired:
                     // S was issued after it (one stream: PV of the unit before is waited for)
-                    if (u >= C::NS && __any_sync(0xffffffffu, need)) {
+                    if (moved && u >= C::NS) {
                         if (C::NS == 1) {
-                            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
+                            ok = __all_sync(0xffffffffu, wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
                                                                    kErrTimeoutMma));
                             if (!ok) break;
                             tc_fence_after();
@@ -786,35 +912,53 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             tc_st_16x256b_x8(o_addr + c * 64, r);
                         }
                     }
+                    if constexpr (XN == 4) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float f = m[x];
+                            m[x] = m[x + 2];
+                            m[x + 2] = f;
+                            f = l[x];
+                            l[x] = l[x + 2];
+                            l[x + 2] = f;
+                            int i = klo[x];
+                            klo[x] = klo[x + 2];
+                            klo[x + 2] = i;
+                            i = khi[x];
+                            khi[x] = khi[x + 2];
+                            khi[x + 2] = i;
+                        }
+                    }
                 }
                 if (!ok) break;
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(C::B_P + buf));
+                warp_arrive(bar(C::B_P + buf), lane);
             }
             // -------------------------------------------------------- the segment's rows
-            if (ok) ok = mbar_wait(bar(C::B_DONE), seg & 1, abort_flag, a.err, kErrTimeoutMma);
+            if (ok) ok = wait(bar(C::B_DONE), seg & 1, abort_flag, a.err, kErrTimeoutMma);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < XN; ++x) {
                 float s = l[x];
                 s += __shfl_xor_sync(0xffffffffu, s, 1);
                 s += __shfl_xor_sync(0xffffffffu, s, 2);
-                if ((lane & 3) == 0) ml[ws * BM + quarter * 32 + x * 8 + (lane >> 2)] = make_float2(m[x], s);
+                if ((lane & 3) == 0)
+                    ml[(C::NS == 2 ? ws * BM : 0) + quarter * 32 + half0 * 16 + x * 8 + (lane >> 2)] = make_float2(m[x], s);
             }
-            mbar_arrive(bar(C::B_ML));
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
+            warp_arrive(bar(C::B_ML), lane);
+            ok = __all_sync(0xffffffffu, wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
             if (!ok) break;
             {
-                // one row a lane now.  Two streams of one row tile are joined here, each
-                // warpgroup half of the columns
-                const bool join = C::NS == 2 && !two;
+                // one row a lane now.  Where both warpgroups have one row tile, each writes half
+                // of its columns, and two streams are joined
+                const bool halves = C::NS == 1 || !two;
                 const int row = quarter * 32 + lane;
-                const int cols = join ? D / 2 : D, c0 = join ? ws * (D / 2) : 0;
-                const int s0 = join ? static_cast<int>(u0 & 1) : ws;    // stream of the first unit
-                const bool both = join && n > 1;
+                const int cols = halves ? D / 2 : D, c0 = halves ? ws * (D / 2) : 0;
+                const int s0 = C::NS == 1 ? 0 : two ? ws : static_cast<int>(u0 & 1);   // stream of the first unit
+                const bool both = C::NS == 2 && !two && n > 1;
                 const float2 x0 = ml[s0 * BM + row];
                 float mx = x0.x, sum = x0.y, w0 = 1.f, w1 = 0.f;
                 if (both) {
@@ -825,9 +969,9 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     sum = w0 * x0.y + w1 * x1.y;
                 }
                 const int i = row / a.HG, gh = (w.head % a.n_hg) * a.HG + row % a.HG;
-                const int qi = q0 + i, orow = w.c.q_base + qi;
-                const bool live = row < a.QT1 * a.HG && qi < w.c.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
-                const bool whole = w.whole();
+                const int qi = q0 + i, orow = w.q_base + qi;
+                const bool live = row < a.QT1 * a.HG && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
+                const bool whole = w.off == 0 && n == w.tiles;
                 // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
                 const float inv = sum == 0.f ? 0.f : 1.0f / sum;
                 if (whole) {
@@ -887,7 +1031,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar(C::B_OFREE));
+            warp_arrive(bar(C::B_OFREE), lane);
             u0 += U;
             jt += n;
         }
@@ -915,17 +1059,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Ar
     const int qi = rg * a.QTG + (row / per) * a.QT1 + (row % per) / a.HG;
     const int gh = (head % a.n_hg) * a.HG + (row % per) % a.HG, orow = c.q_base + qi;
     if (qi >= c.n_rows || qi >= (rg + 1) * a.QTG || gh >= a.G || orow < 0 || orow >= a.total_q) return;
-    // the parts: the end of CTA c's run, whole runs, the beginning of the last
+    // the parts: the end of CTA c's run, whole runs of the same head, the beginning of the last
     float mx = a.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + 1) * a.slot_rows + row].x;
     int last = blockIdx.x;
     do {
-        ++last;
+        last += a.hp;
         mx = fmaxf(mx, a.part_ml[static_cast<size_t>(last) * 2 * a.slot_rows + row].x);
-    } while (!a.meta[last * 8 + 1] && last + 1 < n_ctas);
+    } while (!a.meta[last * 8 + 1] && last + a.hp < n_ctas);
     float o[D / 32], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    for (int i = blockIdx.x; i <= last; ++i) {
+    for (int i = blockIdx.x; i <= last; i += a.hp) {
         const size_t at = (static_cast<size_t>(i) * 2 + (i == blockIdx.x ? 1 : 0)) * a.slot_rows + row;
         const float2 x = a.part_ml[at];
         const float w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - mx);
@@ -1034,13 +1178,28 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     a.max_rg = (L.max_q - 1) / p.QTG + 1;
     a.scale = L.scale;
     a.softcap = L.softcap;
-    const int sms = sm_count();
-    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
+    // The CTAs of one run take its hp heads side by side, so that they read neighbouring
+    // rows of the same pages at the same time.  hp: the count that leaves the fewest CTAs
+    // without work (152 CTAs: 8 heads as 19 x 8, 7 as 21 x 7, 100 in 2 batches as 3 x 50)
+    const int sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    const int heads = L.Hkv * p.n_hg;
+    double best = 0.;
+    const int nb0 = (heads + sms - 1) / sms;
+    for (int nb = nb0; nb <= heads && nb < nb0 + 32; ++nb) {
+        const int hp = (heads + nb - 1) / nb;
+        const double use = static_cast<double>(sms / hp) * hp / sms * heads / (static_cast<double>(hp) * nb);
+        if (use > best * 1.02) {
+            best = use;
+            a.hp = hp;
+            a.n_hb = nb;
+        }
+    }
+    const int grid = sms / a.hp * a.hp;
     const dim3 join(grid, (p.slot_rows + kJoinWarps - 1) / kJoinWarps);
     if (trace_enabled())
-        trace("prefill8_kernel<D=%d,row_tiles=%d,cap=%d> grid=%d block=%d smem=%u key_tile=%d stages=%d heads_per_row_tile=%d "
+        trace("prefill8_kernel<D=%d,row_tiles=%d,cap=%d> grid=%d block=%d smem=%u key_tile=%d stages=%d heads_per_row_tile=%d heads_side_by_side=%d "
               "queries_per_group=%d B=%d total_q=%d Hq=%d Hkv=%d page=%d window=%d, then prefill8_join_kernel grid=(%u,%u)",
-              D, NT, (int)CAP, grid, kThreads, C::SMEM_ALLOC, C::BN, C::NST, p.HG, p.QTG, L.B, L.total_q, L.Hq, L.Hkv,
+              D, NT, (int)CAP, grid, kThreads, C::SMEM_ALLOC, C::BN, C::NST, p.HG, a.hp, p.QTG, L.B, L.total_q, L.Hq, L.Hkv,
               L.page_size, L.window, join.x, join.y);
     kernel<<<grid, kThreads, C::SMEM_ALLOC, L.stream>>>(tq, tk, tv, a);
     cudaError_t e = cudaGetLastError();
