@@ -95,23 +95,26 @@ struct Cfg {
     static constexpr int NCH = D / 64;                   // 128-byte chunks of a row of f16
     static constexpr int NS = D == 256 ? 1 : 2;          // streams (O accumulators)
     static constexpr int NSM = 8, NCV = 8;               // softmax and converter warps
-    static constexpr int PROD_WARP = 16, MMA_WARP = 17, Q_WARP = 18;   // 19: per-key factors
+    static constexpr int K_WARP = 16, MMA_WARP = 17, V_WARP = 18;   // 19: per-key factors and Q
     static constexpr int RING = 3;                       // f16 operand tiles
     // staged code tiles: what shared memory leaves beside Q and the operand ring
     static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
     static constexpr int NTAB = 4;                       // key-factor tables
     static constexpr uint32_t Q_TILE = NCH * BM * 128;
     static constexpr uint32_t OP_CHUNK = BN * 128, OP_BYTES = NCH * OP_CHUNK;
+    static constexpr int IDS = 8, SCALES = 4;            // rings of prefetched page ids and scales (tiles)
     static constexpr uint32_t CODE_BYTES = BN * D, SCALE_BYTES = 2 * BN * 2;
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_OP = OFF_Q + NT * Q_TILE;
     static constexpr uint32_t OFF_CODE = OFF_OP + RING * OP_BYTES;
     static constexpr uint32_t OFF_SCALE = OFF_CODE + NST * CODE_BYTES;
-    static constexpr uint32_t OFF_TAB = OFF_SCALE + NST * SCALE_BYTES;
+    static constexpr uint32_t OFF_IDS = OFF_SCALE + SCALES * SCALE_BYTES;      // of the factor warp: a pair of keys each
+    static constexpr uint32_t OFF_IDS_KV = OFF_IDS + IDS * (BN / 2) * 4;       // of the K and the V warp: a box each
+    static constexpr uint32_t OFF_TAB = OFF_IDS_KV + 2 * IDS * 16 * 4;
     static constexpr uint32_t OFF_ML = OFF_TAB + NTAB * sizeof(KeyFactors<BN>);
     static constexpr uint32_t OFF_BAR = OFF_ML + 2 * BM * 8;
     enum : int {
-        B_SFULL_ST = 0,                    // stage: codes and scales are there
+        B_SFULL_ST = 0,                    // stage: codes are there
         B_SEMPTY_ST = B_SFULL_ST + NST,    // stage: converted
         B_OPFULL = B_SEMPTY_ST + NST,      // operand tile: converted
         B_OPEMPTY = B_OPFULL + RING,       // operand tile: its MMAs are done
@@ -337,7 +340,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         if (tid == 0) {
             for (int i = 0; i < NST; ++i) {
                 mbar_init(bar(C::B_SFULL_ST + i), 1);
-                mbar_init(bar(C::B_SEMPTY_ST + i), C::NCV + 1);
+                mbar_init(bar(C::B_SEMPTY_ST + i), C::NCV);
             }
             for (int i = 0; i < RING; ++i) {
                 mbar_init(bar(C::B_OPFULL + i), C::NCV);
@@ -351,7 +354,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_init(bar(C::B_QEMPTY), 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(bar(C::B_S + i), 1);
-                mbar_init(bar(C::B_P + i), C::NSM / C::NS);
+                mbar_init(bar(C::B_P + i), C::NSM);
             }
             mbar_init(bar(C::B_DONE), 1);
             mbar_init(bar(C::B_OFREE), C::NSM);
@@ -414,22 +417,24 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
 
     // (setmaxnreg is executed by all four warps of a warpgroup)
-    if (warp >= C::PROD_WARP) {
+    if (warp >= C::K_WARP) {
     regs_dec<kRegOther>();
-    if (warp == C::PROD_WARP) {
-        // ------------------------------------------------------------ codes and scales
-        // lanes 0-15, lane i the box of the tile's i-th page (one box inside a page that
-        // is longer than the tile); lane 0 waits for the stage and posts the byte count
+    if (warp == C::K_WARP || warp == C::V_WARP) {
+        // ------------------------------------------------------------ codes
+        // One warp brings K tiles, one V tiles; lanes 0-15, lane i the box of the tile's
+        // i-th page (one box inside a page that is longer than the tile).  Page ids come
+        // 4 tiles ahead by asynchronous copies; lane 0 waits for the stage and posts the
+        // byte count.
         if (lane < 16) {
             const unsigned gmask = 0x0000ffffu;
-            const bool leader = lane == 0;
-            if (leader) {
-                tma_prefetch_desc(&tm_k);
-                tma_prefetch_desc(&tm_v);
-            }
+            const bool leader = lane == 0, mine_k = warp == C::K_WARP;
+            const CUtensorMap* tm = mine_k ? &tm_k : &tm_v;
+            if (leader) tma_prefetch_desc(tm);
             const int R = a.box_rows;
             const bool has_box = lane * R < BN;
-            uint32_t gi = 0;   // tiles loaded by this CTA so far
+            const uint32_t ids = C::OFF_IDS_KV + (mine_k ? 0 : C::IDS * 16 * 4) + lane * 4;
+            uint32_t base = 0;                     // items before this segment
+            uint32_t sent = 0, parity = 0;         // stages this warp filled, and their phases (one bit each)
             int ok = 1;
             for (bool more = seg_next<BN>(a, w, true, lane, gmask); ok && more;
                  more = seg_next<BN>(a, w, false, lane, gmask)) {
@@ -437,31 +442,29 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0 + lane * R;
                 const int g = w.head / a.n_hg;
                 const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
-                // page id of this lane's box in item i
-                auto fetch = [&](int i) {
-                    int j;
-                    if (i >= 2 * n) return 0;
-                    item_of(two, i, n, j);
+                auto in_use = [&](int kk) { return has_box && kk >= lo - R + 1 && kk < hi; };
+                auto fetch = [&](int j) {
                     const int kk = k0 + j * BN;
-                    return has_box && kk >= lo - R + 1 && kk < hi ? __ldg(&table[kk >> a.log2P]) : 0;
+                    if (j < n && in_use(kk)) cp_async4(sbase + ids + (j % C::IDS) * 64, &table[kk >> a.log2P]);
+                    cp_async_commit();
                 };
-                int pg = fetch(0);
-                for (int i = 0; i < 2 * n; ++i, ++gi) {
-                    const uint32_t st = gi % NST;
+                for (int j = 0; j < 4; ++j) fetch(j);
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t gi = base + (mine_k ? item_k(two, j) : item_v(two, j, n)), st = gi % NST;
+                    fetch(j + 4);
+                    cp_async_wait<4>();
                     if (gi >= NST) {
                         if (leader)
-                            ok = wait(bar(C::B_SEMPTY_ST + st), ((gi / NST) - 1) & 1, abort_flag, a.err,
-                                           kErrTimeoutSlot);
+                            ok = wait(bar(C::B_SEMPTY_ST + st), ((gi / NST) - 1) & 1, abort_flag, a.err, kErrTimeoutSlot);
                         ok = __shfl_sync(gmask, ok, 0);
                         if (!ok) break;
                     }
-                    int j;
-                    const bool is_k = item_of(two, i, n, j);
-                    const int kk = k0 + j * BN;
                     // boxes without a key of [lo, hi), and pages outside the pool, take the page
-                    // coordinate n_pages, so that the copy fills zeros, and zero scales
+                    // coordinate n_pages, so that the copy fills zeros
+                    const int kk = k0 + j * BN;
                     int page = a.n_pages, row = 0;
-                    if (has_box && kk >= lo - R + 1 && kk < hi) {
+                    if (in_use(kk)) {
+                        const int pg = *reinterpret_cast<const int*>(smem + ids + (j % C::IDS) * 64);
                         if (pg >= 0 && pg < a.n_pages) {
                             page = pg;
                             row = kk & (a.P - 1);
@@ -469,56 +472,21 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             atomicExch(a.err, kErrBadPage);
                         }
                     }
-                    const bool live = page < a.n_pages;
-                    const uint32_t sc = C::OFF_SCALE + st * C::SCALE_BYTES + lane * R * 2;
-                    if (is_k && has_box && !live) {
-                        for (int x = 0; x < R * 2; x += 16) {
-                            *reinterpret_cast<uint4*>(smem + sc + x) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4*>(smem + sc + BN * 2 + x) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    const unsigned lives = __ballot_sync(gmask, live);
-                    __syncwarp(gmask);   // the zeros before the leader's arrival
-                    if (leader)
-                        mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st),
-                                              C::CODE_BYTES + (is_k ? __popc(lives) * R * 4 : 0));
+                    if (leader) mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st), C::CODE_BYTES);
                     __syncwarp(gmask);
-                    if (has_box) {
-                        tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + lane * R * D, is_k ? &tm_k : &tm_v,
-                                    bar(C::B_SFULL_ST + st), 0, g, row, page);
-                        if (is_k && live) {
-                            const size_t at = (static_cast<size_t>(page) * a.Hkv + g) * a.P + row;
-                            bulk_load(sbase + sc, a.k_scales + at, R * 2, bar(C::B_SFULL_ST + st));
-                            bulk_load(sbase + sc + BN * 2, a.v_scales + at, R * 2, bar(C::B_SFULL_ST + st));
-                        }
-                    }
-                    pg = fetch(i + 1);
+                    if (has_box)
+                        tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + lane * R * D, tm, bar(C::B_SFULL_ST + st), 0,
+                                    g, row, page);
+                    sent |= 1u << st;
+                    parity = (parity & ~(1u << st)) | (((gi / NST) & 1) << st);
                 }
+                cp_async_wait<0>();
+                base += 2 * n;
             }
-            if (leader && *abort_flag) {
-                // copies in flight land before the CTA's shared memory goes away
-                for (uint32_t i = gi > NST ? gi - NST : 0; i < gi; ++i)
-                    mbar_wait_drain(bar(C::B_SFULL_ST + i % NST), (i / NST) & 1, a.err, kErrTimeoutLoad);
-            }
-        }
-    } else if (warp == C::Q_WARP) {
-        // ------------------------------------------------------------ Q
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            uint32_t seg = 0;
-            for (bool more = seg_next<BN>(a, w, true, 0, 1u); more; more = seg_next<BN>(a, w, false, 0, 1u), ++seg) {
-                if (seg > 0 &&
-                    !wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot)) break;
-                const int nt = w.two ? 2 : 1;
-                const int h0 = (w.head / a.n_hg) * a.G + (w.head % a.n_hg) * a.HG;
-                mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
-                for (int t = 0; t < nt; ++t)
-                    for (int c = 0; c < NCH; ++c)
-                        tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64, h0,
-                                    w.q_base + w.rg * a.QTG + t * a.QT1);
-            }
-            if (*abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
+            if (leader && *abort_flag)   // copies in flight land before the CTA's shared memory goes away
+                for (int st = 0; st < NST; ++st)
+                    if (sent >> st & 1)
+                        mbar_wait_drain(bar(C::B_SFULL_ST + st), parity >> st & 1, a.err, kErrTimeoutLoad);
         }
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
@@ -590,58 +558,109 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
         }
     } else {
-        // ------------------------------------------------------------ per-key factors
+        // ------------------------------------------------------------ per-key factors, Q
+        // A lane takes a pair of keys (D = 64/128: two).  Its page ids come 4 tiles ahead
+        // and its scales 2 tiles ahead, by asynchronous copies of its own.
+        if (lane == 0) tma_prefetch_desc(&tm_q);
         const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
-        uint32_t gi = 0, jt = 0;    // tiles and key tiles before this one
+        const uint32_t ids = C::OFF_IDS + lane * 4, scl = C::OFF_SCALE + lane * 4;
+        uint32_t jt = 0, seg = 0;    // key tiles and segments before this one
         bool ok = true;
         for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
-             more = seg_next<BN>(a, w, false, lane, 0xffffffffu)) {
-            const bool two = NT == 2 && w.two;
-            const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0;
-            for (int i = 0; i < 2 * n; ++i, ++gi) {
-                int j;
-                const bool is_k = item_of(two, i, n, j);
-                const uint32_t st = gi % NST, tb = (jt + j) % C::NTAB;
-                ok = wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
-                if (ok && is_k && jt + j >= C::NTAB)
-                    ok = wait(bar(C::B_TABEMPTY + tb), ((jt + j) / C::NTAB - 1) & 1, abort_flag, a.err,
-                                   kErrTimeoutSoftmax);
+             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
+            const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0 + 2 * lane;
+            const int g = w.head / a.n_hg;
+            const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+            if (lane == 0) {
+                if (seg > 0) ok = wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot);
+                if (ok) {
+                    const int nt = NT == 2 && w.two ? 2 : 1;
+                    const int h0 = g * a.G + (w.head % a.n_hg) * a.HG;
+                    mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
+                    for (int t = 0; t < nt; ++t)
+#pragma unroll 1
+                        for (int c = 0; c < NCH; ++c)
+                            tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64,
+                                        h0, w.q_base + w.rg * a.QTG + t * a.QT1);
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            auto in_use = [&](int j, int x) {
+                const int kk = k0 + j * BN + x * 64;
+                return j < n && kk + 1 >= lo && kk < hi;
+            };
+            auto fetch_ids = [&](int j) {
+#pragma unroll
+                for (int x = 0; x < BN / 64; ++x)
+                    if (in_use(j, x))
+                        cp_async4(sbase + ids + (j % C::IDS) * (BN * 2) + x * 128, &table[(k0 + j * BN + x * 64) >> a.log2P]);
+            };
+            auto fetch_scales = [&](int j) {
+#pragma unroll
+                for (int x = 0; x < BN / 64; ++x) {
+                    if (!in_use(j, x)) continue;
+                    const int pg = *reinterpret_cast<const int*>(smem + ids + (j % C::IDS) * (BN * 2) + x * 128);
+                    const uint32_t dst = scl + (j % C::SCALES) * C::SCALE_BYTES + x * 128;
+                    if (pg >= 0 && pg < a.n_pages) {
+                        const size_t at = (static_cast<size_t>(pg) * a.Hkv + g) * a.P + ((k0 + j * BN + x * 64) & (a.P - 1));
+                        cp_async4(sbase + dst, a.k_scales + at);
+                        cp_async4(sbase + dst + BN * 2, a.v_scales + at);
+                    } else {   // its codes are zeros too
+                        *reinterpret_cast<uint32_t*>(smem + dst) = 0u;
+                        *reinterpret_cast<uint32_t*>(smem + dst + BN * 2) = 0u;
+                    }
+                }
+            };
+            for (int j = 0; j < 4; ++j) fetch_ids(j);
+            cp_async_commit();
+            cp_async_wait<0>();
+            fetch_scales(0);
+            cp_async_commit();
+            fetch_scales(1);
+            cp_async_commit();
+            for (int j = 0; j < n; ++j) {
+                cp_async_wait<1>();       // scales of tile j, ids up to tile j + 2
+                fetch_scales(j + 2);
+                fetch_ids(j + 4);
+                cp_async_commit();
+                const uint32_t tb = (jt + j) % C::NTAB;
+                if (jt + j >= C::NTAB)
+                    ok = wait(bar(C::B_TABEMPTY + tb), ((jt + j) / C::NTAB - 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (is_k) {
-                    KeyFactors<BN>& t = tab[tb];
-                    const __half* sc = reinterpret_cast<const __half*>(smem + C::OFF_SCALE + st * C::SCALE_BYTES);
-                    const int key0 = k0 + j * BN;
+                KeyFactors<BN>& t = tab[tb];
+                const uint8_t* sc = smem + scl + (j % C::SCALES) * C::SCALE_BYTES;
 #pragma unroll 1
-                    for (int x = 0; x < BN / 64; ++x) {
-                        const int pr = x * 32 + lane;   // a pair of keys
-                        const float2 ks2 = __half22float2(*reinterpret_cast<const __half2*>(sc + 2 * pr));
-                        const float2 vs2 = __half22float2(*reinterpret_cast<const __half2*>(sc + BN + 2 * pr));
-                        float f[2], lv[2], iv[2];
+                for (int x = 0; x < BN / 64; ++x) {
+                    const int pr = x * 32 + lane;
+                    const float2 ks2 = __half22float2(*reinterpret_cast<const __half2*>(sc + x * 128));
+                    const float2 vs2 = __half22float2(*reinterpret_cast<const __half2*>(sc + x * 128 + BN * 2));
+                    float f[2], lv[2], iv[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + 2 * pr + e;
-                            const float ks = e ? ks2.y : ks2.x, vs = e ? vs2.y : vs2.x;
-                            const bool in = key >= lo && key < hi;
-                            const bool fin = isfinite(ks) && isfinite(vs);
-                            // a value scale of 0 counts as the smallest f16 with codes of 0; a scale
-                            // that is not finite makes the logit NaN, which only rows that keep the
-                            // key take; keys outside [lo, hi) get factors that cannot spoil anything
-                            const float av = in && fin ? fmaxf(fabsf(vs), 0x1p-24f) : 1.f;
-                            f[e] = !in ? 0.f : fin ? ks * kf : __int_as_float(0x7fc00000);
-                            lv[e] = log2f(av);
-                            iv[e] = 1.f / av;
-                            t.sign[2 * pr + e] = !in || !fin || vs == 0.f ? 0u : vs > 0.f ? 0x3c003c00u : 0xbc00bc00u;
-                        }
-                        t.a[pr] = make_float4(f[0], f[1], lv[0], lv[1]);
-                        t.b[pr] = make_float2(iv[0], iv[1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = k0 + j * BN + x * 64 + e;
+                        const float ks = e ? ks2.y : ks2.x, vs = e ? vs2.y : vs2.x;
+                        const bool in = key >= lo && key < hi;
+                        const bool fin = isfinite(ks) && isfinite(vs);
+                        // a value scale of 0 counts as the smallest f16 with codes of 0; a scale
+                        // that is not finite makes the logit NaN, which only rows that keep the
+                        // key take; keys outside [lo, hi) get factors that cannot spoil anything
+                        const float av = in && fin ? fmaxf(fabsf(vs), 0x1p-24f) : 1.f;
+                        f[e] = !in ? 0.f : fin ? ks * kf : __int_as_float(0x7fc00000);
+                        lv[e] = log2f(av);
+                        iv[e] = 1.f / av;
+                        t.sign[2 * pr + e] = !in || !fin || vs == 0.f ? 0u : vs > 0.f ? 0x3c003c00u : 0xbc00bc00u;
                     }
-                    warp_arrive(bar(C::B_TAB + tb), lane);
+                    t.a[pr] = make_float4(f[0], f[1], lv[0], lv[1]);
+                    t.b[pr] = make_float2(iv[0], iv[1]);
                 }
-                warp_arrive(bar(C::B_SEMPTY_ST + st), lane);
+                warp_arrive(bar(C::B_TAB + tb), lane);
             }
+            cp_async_wait<0>();
             jt += n;
         }
+        if (lane == 0 && *abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
     }
     } else if (warp >= C::NSM) {
         // ------------------------------------------------------------ converters
@@ -711,7 +730,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<kRegSoftmax>();
-        const int ws = warp >> 2;                  // stream; one stream: the half of each quarter's rows
+        // both warpgroups take every unit: warp w and w + 4 the two 16-row halves of quarter w % 4
+        const int ws = warp >> 2;
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const float cap_log2 = a.softcap * kLog2e;
@@ -721,27 +741,23 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
              more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
             const bool two = NT == 2 && w.two;
             const int n = w.n, U = two ? 2 * n : n, k0 = w.key0;
-            // this warpgroup's units: those of its stream (all, if there is one)
-            const int first_u = C::NS == 1 ? 0 : static_cast<int>((ws ^ u0) & 1);
-            constexpr int XN = C::NS == 1 ? 2 : 4;   // rows of a thread
-            const int half0 = C::NS == 1 ? ws : 0;   // its first 16-row half
-            const int rt = two ? first_u : 0;      // row tile
-            const int q0 = w.rg * a.QTG + rt * a.QT1;
-            // of each 16-row half a thread holds rows lane / 4 and lane / 4 + 8, and of every 8
-            // columns the pair 2 (lane % 4): the per-key factors are then one 16- and one
-            // 8-byte load for 4 rows and 2 keys
-            // a row keeps the keys [klo, khi)
+            // of its 16 rows a thread holds lane / 4 and lane / 4 + 8, and of every 8 columns the
+            // pair 2 (lane % 4): the per-key factors are then one 16- and one 8-byte load for
+            // 2 rows and 2 keys.  A row keeps the keys [klo, khi) and has running statistics in
+            // each stream; those of the unit's stream come first and change places after it.
+            constexpr int XN = 2 * C::NS;
             int klo[XN], khi[XN];
             float m[XN], l[XN];
 #pragma unroll
             for (int x = 0; x < XN; ++x) {
-                const int pos = w.pos0 + q0 + (quarter * 32 + half0 * 16 + x * 8 + (lane >> 2)) / a.HG;
+                const int q0 = w.rg * a.QTG + (two ? x / 2 : 0) * a.QT1;
+                const int pos = w.pos0 + q0 + (quarter * 32 + ws * 16 + (x & 1) * 8 + (lane >> 2)) / a.HG;
                 khi[x] = min(w.hi, pos + 1);
                 klo[x] = a.window > 0 ? max(0, pos - min(a.window, 0x3fffffff) + 1) : 0;
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
-            for (int u = first_u; ok && u < U; u += C::NS) {
+            for (int u = 0; ok && u < U; ++u) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t buf = (u0 + u) & 1, tb = (jt + j) % C::NTAB;
                 ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
@@ -751,12 +767,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tc_fence_after();
                 const KeyFactors<BN>& t = tab[tb];
                 const int key0 = k0 + j * BN;
-                // (one copy of the code; the rows' state changes places after each half)
-#pragma unroll 1
-                for (int hlf = 0; hlf < XN / 2; ++hlf) {
-                    const uint32_t rows = lanes + (static_cast<uint32_t>((half0 + hlf) * 16) << 16);
+                {
+                    const uint32_t rows = lanes + (static_cast<uint32_t>(ws * 16) << 16);
                     const uint32_t s_addr = rows + buf * BN;
-                    float2 y[2][BN / 8];           // [row of the half][8-column group]
+                    float2 y[2][BN / 8];           // [row][8-column group]
                     {
                         uint32_t r[BN / 64][32];
 #pragma unroll
@@ -912,7 +926,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             tc_st_16x256b_x8(o_addr + c * 64, r);
                         }
                     }
-                    if constexpr (XN == 4) {
+                    if constexpr (XN == 4) {   // the other stream's state to the front
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             float f = m[x];
@@ -942,27 +956,32 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < XN; ++x) {
-                float s = l[x];
-                s += __shfl_xor_sync(0xffffffffu, s, 1);
-                s += __shfl_xor_sync(0xffffffffu, s, 2);
+                float v = l[x];
+                v += __shfl_xor_sync(0xffffffffu, v, 1);
+                v += __shfl_xor_sync(0xffffffffu, v, 2);
+                // streams in the order of the segment's units, or the other way round after an
+                // odd number of them
+                const int first = C::NS == 2 ? (x / 2) ^ (U & 1) : 0;
                 if ((lane & 3) == 0)
-                    ml[(C::NS == 2 ? ws * BM : 0) + quarter * 32 + half0 * 16 + x * 8 + (lane >> 2)] = make_float2(m[x], s);
+                    ml[first * BM + quarter * 32 + ws * 16 + (x & 1) * 8 + (lane >> 2)] = make_float2(m[x], v);
             }
             warp_arrive(bar(C::B_ML), lane);
             ok = __all_sync(0xffffffffu, wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
             if (!ok) break;
             {
-                // one row a lane now.  Where both warpgroups have one row tile, each writes half
-                // of its columns, and two streams are joined
+                // one row a lane now.  Of two row tiles each warpgroup writes one, of a single one
+                // half of the columns, where two streams are joined
                 const bool halves = C::NS == 1 || !two;
                 const int row = quarter * 32 + lane;
                 const int cols = halves ? D / 2 : D, c0 = halves ? ws * (D / 2) : 0;
-                const int s0 = C::NS == 1 ? 0 : two ? ws : static_cast<int>(u0 & 1);   // stream of the first unit
+                const int rt = two ? ws : 0;                              // row tile
+                const int q0 = w.rg * a.QTG + rt * a.QT1;
+                const int s0 = C::NS == 1 ? 0 : static_cast<int>((u0 + rt) & 1);   // its (first) stream
                 const bool both = C::NS == 2 && !two && n > 1;
-                const float2 x0 = ml[s0 * BM + row];
+                const float2 x0 = ml[rt * BM + row];
                 float mx = x0.x, sum = x0.y, w0 = 1.f, w1 = 0.f;
                 if (both) {
-                    const float2 x1 = ml[(s0 ^ 1) * BM + row];
+                    const float2 x1 = ml[BM + row];
                     mx = fmaxf(x0.x, x1.x);
                     w0 = x0.x == -INFINITY ? 0.f : ex2_approx(x0.x - mx);
                     w1 = x1.x == -INFINITY ? 0.f : ex2_approx(x1.x - mx);

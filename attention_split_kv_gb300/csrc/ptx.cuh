@@ -335,11 +335,14 @@ __device__ __forceinline__ void tc_st_16x128b_x8(uint32_t taddr, const uint32_t 
         : "memory");
 }
 
-// Copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) without a tensor map.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-                 : "memory");
+// Asynchronous 4-byte copies of a thread, in groups that it waits for in order.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>   // all but the newest N groups have arrived
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Shared-memory matrix descriptor for tcgen05.mma (sm_100 family format):
