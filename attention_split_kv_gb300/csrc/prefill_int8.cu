@@ -108,11 +108,11 @@ struct Cfg {
     static constexpr uint32_t OFF_OP = OFF_Q + NT * Q_TILE;
     static constexpr uint32_t OFF_CODE = OFF_OP + RING * OP_BYTES;
     static constexpr uint32_t OFF_SCALE = OFF_CODE + NST * CODE_BYTES;
-    static constexpr uint32_t OFF_IDS = OFF_SCALE + SCALES * SCALE_BYTES;      // of the factor warp: a pair of keys each
-    static constexpr uint32_t OFF_IDS_KV = OFF_IDS + IDS * (BN / 2) * 4;       // of the K and the V warp: a box each
-    static constexpr uint32_t OFF_TAB = OFF_IDS_KV + 2 * IDS * 16 * 4;
+    static constexpr uint32_t OFF_IDS = OFF_SCALE + SCALES * SCALE_BYTES;
+    // (of the factor, the K and the V warp: one a box)
+    static constexpr uint32_t OFF_TAB = OFF_IDS + 3 * IDS * 16 * 4;
     static constexpr uint32_t OFF_ML = OFF_TAB + NTAB * sizeof(KeyFactors<BN>);
-    static constexpr uint32_t OFF_BAR = OFF_ML + 2 * BM * 8;
+    static constexpr uint32_t OFF_BAR = OFF_ML + 2 * BM * 8;   // row statistics [warpgroup][row]
     enum : int {
         B_SFULL_ST = 0,                    // stage: codes are there
         B_SEMPTY_ST = B_SFULL_ST + NST,    // stage: converted
@@ -298,7 +298,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     Seg* segs = reinterpret_cast<Seg*>(smem + C::OFF_SEG);   // one a warp
     Seg& first_seg = segs[kThreads / 32];
     KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
-    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [stream][row]
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [warpgroup][row]
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -354,7 +354,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_init(bar(C::B_QEMPTY), 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(bar(C::B_S + i), 1);
-                mbar_init(bar(C::B_P + i), C::NSM);
+                mbar_init(bar(C::B_P + i), 4);
             }
             mbar_init(bar(C::B_DONE), 1);
             mbar_init(bar(C::B_OFREE), C::NSM);
@@ -432,7 +432,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (leader) tma_prefetch_desc(tm);
             const int R = a.box_rows;
             const bool has_box = lane * R < BN;
-            const uint32_t ids = C::OFF_IDS_KV + (mine_k ? 0 : C::IDS * 16 * 4) + lane * 4;
+            const uint32_t ids = C::OFF_IDS + (mine_k ? 1 : 2) * (C::IDS * 16 * 4) + lane * 4;
             uint32_t base = 0;                     // items before this segment
             uint32_t sent = 0, parity = 0;         // stages this warp filled, and their phases (one bit each)
             int ok = 1;
@@ -563,7 +563,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // and its scales 2 tiles ahead, by asynchronous copies of its own.
         if (lane == 0) tma_prefetch_desc(&tm_q);
         const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
-        const uint32_t ids = C::OFF_IDS + lane * 4, scl = C::OFF_SCALE + lane * 4;
+        const uint32_t ids = C::OFF_IDS, scl = C::OFF_SCALE + lane * 4;
+        const int R = a.box_rows;
         uint32_t jt = 0, seg = 0;    // key tiles and segments before this one
         bool ok = true;
         for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
@@ -586,24 +587,22 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            auto in_use = [&](int j, int x) {
-                const int kk = k0 + j * BN + x * 64;
-                return j < n && kk + 1 >= lo && kk < hi;
-            };
+            // page ids: lane i < 16 that of the tile's i-th box
             auto fetch_ids = [&](int j) {
-#pragma unroll
-                for (int x = 0; x < BN / 64; ++x)
-                    if (in_use(j, x))
-                        cp_async4(sbase + ids + (j % C::IDS) * (BN * 2) + x * 128, &table[(k0 + j * BN + x * 64) >> a.log2P]);
+                const int kk = w.key0 + j * BN + lane * R;
+                if (j < n && lane * R < BN && kk >= lo - R + 1 && kk < hi)
+                    cp_async4(sbase + ids + (j % C::IDS) * 64 + lane * 4, &table[kk >> a.log2P]);
             };
             auto fetch_scales = [&](int j) {
+                __syncwarp();             // ids that other lanes brought
 #pragma unroll
                 for (int x = 0; x < BN / 64; ++x) {
-                    if (!in_use(j, x)) continue;
-                    const int pg = *reinterpret_cast<const int*>(smem + ids + (j % C::IDS) * (BN * 2) + x * 128);
+                    const int kk = k0 + j * BN + x * 64;
+                    if (!(j < n && kk + 1 >= lo && kk < hi)) continue;
+                    const int pg = *reinterpret_cast<const int*>(smem + ids + (j % C::IDS) * 64 + (2 * lane + x * 64) / R * 4);
                     const uint32_t dst = scl + (j % C::SCALES) * C::SCALE_BYTES + x * 128;
                     if (pg >= 0 && pg < a.n_pages) {
-                        const size_t at = (static_cast<size_t>(pg) * a.Hkv + g) * a.P + ((k0 + j * BN + x * 64) & (a.P - 1));
+                        const size_t at = (static_cast<size_t>(pg) * a.Hkv + g) * a.P + (kk & (a.P - 1));
                         cp_async4(sbase + dst, a.k_scales + at);
                         cp_async4(sbase + dst + BN * 2, a.v_scales + at);
                     } else {   // its codes are zeros too
@@ -730,7 +729,12 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<kRegSoftmax>();
-        // both warpgroups take every unit: warp w and w + 4 the two 16-row halves of quarter w % 4
+        // Each warpgroup takes the units of its stream (one stream: the first takes all), a
+        // warp 32 rows, 64 keys a time.  Of every 16-row half a thread holds rows lane / 4 and
+        // lane / 4 + 8, and of every 8 columns the pair 2 (lane % 4), so that a 16- and an
+        // 8-byte load of per-key factors serve 4 rows and 2 keys.  (For 2 rows the factors
+        // take as much of shared memory's bandwidth as the MMAs' operands; a row a thread
+        // would take 4 times as much.)
         const int ws = warp >> 2;
         const int quarter = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -741,23 +745,22 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
              more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
             const bool two = NT == 2 && w.two;
             const int n = w.n, U = two ? 2 * n : n, k0 = w.key0;
-            // of its 16 rows a thread holds lane / 4 and lane / 4 + 8, and of every 8 columns the
-            // pair 2 (lane % 4): the per-key factors are then one 16- and one 8-byte load for
-            // 2 rows and 2 keys.  A row keeps the keys [klo, khi) and has running statistics in
-            // each stream; those of the unit's stream come first and change places after it.
-            constexpr int XN = 2 * C::NS;
-            int klo[XN], khi[XN];
-            float m[XN], l[XN];
+            const int first_u = C::NS == 1 ? (ws ? U : 0) : static_cast<int>((ws ^ u0) & 1);
+            const int rt = two ? first_u : 0;      // this warpgroup's row tile
+            const int q0 = w.rg * a.QTG + rt * a.QT1;
+            // rows quarter*32 + 8 x + lane / 4, at positions that ascend
+            int pos[4];
+            float m[4], l[4];
 #pragma unroll
-            for (int x = 0; x < XN; ++x) {
-                const int q0 = w.rg * a.QTG + (two ? x / 2 : 0) * a.QT1;
-                const int pos = w.pos0 + q0 + (quarter * 32 + ws * 16 + (x & 1) * 8 + (lane >> 2)) / a.HG;
-                khi[x] = min(w.hi, pos + 1);
-                klo[x] = a.window > 0 ? max(0, pos - min(a.window, 0x3fffffff) + 1) : 0;
+            for (int x = 0; x < 4; ++x) {
+                pos[x] = w.pos0 + q0 + (quarter * 32 + x * 8 + (lane >> 2)) / a.HG;
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
-            for (int u = 0; ok && u < U; ++u) {
+            // without a query among its rows a warp only keeps step (its rows of P are what S
+            // left there: rows of the products do not mix)
+            const bool idle = w.n_rows - q0 <= quarter * 32 / a.HG;
+            for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t buf = (u0 + u) & 1, tb = (jt + j) % C::NTAB;
                 ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
@@ -766,183 +769,187 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!ok) break;
                 tc_fence_after();
                 const KeyFactors<BN>& t = tab[tb];
-                const int key0 = k0 + j * BN;
-                {
-                    const uint32_t rows = lanes + (static_cast<uint32_t>(ws * 16) << 16);
-                    const uint32_t s_addr = rows + buf * BN;
-                    float2 y[2][BN / 8];           // [row][8-column group]
+#pragma unroll 1
+                for (int c = 0; c < BN / 64 && !idle; ++c) {   // 64 keys
+                    const float4* fa = t.a + c * 32 + (lane & 3);
+                    const float2* fb = t.b + c * 32 + (lane & 3);
+                    const int key0 = k0 + j * BN + c * 64;
+                    const uint32_t s_addr = lanes + buf * BN;
+                    float2 y[4][8];                // [row][8-column group]
                     {
-                        uint32_t r[BN / 64][32];
+                        uint32_t r[2][32];
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c) tc_ld_16x256b_x8(s_addr + c * 64, r[c]);
+                        for (int hf = 0; hf < 2; ++hf)
+                            tc_ld_16x256b_x8(s_addr + c * 64 + (static_cast<uint32_t>(hf * 16) << 16), r[hf]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const uint32_t* q = &r[i / 8][4 * (i % 8)];
-                            y[0][i] = make_float2(__uint_as_float(q[0]), __uint_as_float(q[1]));
-                            y[1][i] = make_float2(__uint_as_float(q[2]), __uint_as_float(q[3]));
-                        }
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                y[x][i] = make_float2(__uint_as_float(r[x / 2][4 * i + 2 * (x & 1)]),
+                                                      __uint_as_float(r[x / 2][4 * i + 2 * (x & 1) + 1]));
                     }
                     if constexpr (CAP) {
                         // c tanh(x) in log2 units: an odd polynomial for |x| <= 1/4 (the dropped
-                        // x^9 term is below 8.4e-8), else the exponential form for the whole half
+                        // x^9 term is below 8.4e-8), else the exponential form for the whole warp
                         const float k1 = cap_log2 * (-1.0f / 3.0f), k2 = cap_log2 * (2.0f / 15.0f),
                                     k3 = cap_log2 * (-17.0f / 315.0f);
                         float ax = 0.f;
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const float4 f = t.a[4 * i + (lane & 3)];
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 f = fa[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
+                            for (int x = 0; x < 4; ++x) {
                                 y[x][i] = fmul2(y[x][i], make_float2(f.x, f.y));
-                                ax = fmaxf(ax, fmaxf(fabsf(y[x][i].x), fabsf(y[x][i].y)));
+                                ax = max3(ax, fabsf(y[x][i].x), fabsf(y[x][i].y));
                             }
                         }
-                        const bool small = __all_sync(0xffffffffu, ax <= 0.25f);
+                        if (__all_sync(0xffffffffu, ax <= 0.25f)) {
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const float4 f = t.a[4 * i + (lane & 3)];
-                            const float2 lv = make_float2(f.z, f.w);
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 f = fa[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float2 v = y[x][i];
-                                if (small) {
-                                    const float2 z = fmul2(v, v);
+                                for (int x = 0; x < 4; ++x) {
+                                    const float2 v = y[x][i], z = fmul2(v, v);
                                     float2 q = ffma2(z, make_float2(k3, k3), make_float2(k2, k2));
                                     q = ffma2(q, z, make_float2(k1, k1));
                                     q = ffma2(q, z, make_float2(cap_log2, cap_log2));
-                                    y[x][i] = ffma2(v, q, lv);
-                                } else {
-                                    y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(v.x), lv.x),
-                                                          fmaf(cap_log2, tanh_abs_accurate(v.y), lv.y));
+                                    y[x][i] = ffma2(v, q, make_float2(f.z, f.w));
                                 }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 f = fa[4 * i];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(y[x][i].x), f.z),
+                                                          fmaf(cap_log2, tanh_abs_accurate(y[x][i].y), f.w));
                             }
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < BN / 8; ++i) {
-                            const float4 f = t.a[4 * i + (lane & 3)];
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 f = fa[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x)
+                            for (int x = 0; x < 4; ++x)
                                 y[x][i] = ffma2(y[x][i], make_float2(f.x, f.y), make_float2(f.z, f.w));
                         }
                     }
-                    const bool full = key0 >= max(klo[0], klo[1]) && key0 + BN <= min(khi[0], khi[1]);
+                    // a row keeps the keys [klo, khi)
+                    const int hi = w.hi, W = a.window > 0 ? min(a.window, 0x3fffffff) : 0;
+                    bool full = key0 + 64 <= min(hi, pos[0] + 1);
+                    if (W) full = full && key0 >= pos[3] - W + 1;
                     if (!__all_sync(0xffffffffu, full)) {
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int from = klo[x] - key0 - 2 * (lane & 3);
-                            const unsigned count = max(khi[x] - klo[x], 0);
+                        for (int x = 0; x < 4; ++x) {
+                            const int khi = min(hi, pos[x] + 1), klo = W ? max(0, pos[x] - W + 1) : 0;
+                            const int from = klo - key0 - 2 * (lane & 3);
+                            const unsigned count = max(khi - klo, 0);
 #pragma unroll
-                            for (int i = 0; i < BN / 8; ++i) {
+                            for (int i = 0; i < 8; ++i) {
                                 if (static_cast<unsigned>(8 * i - from) >= count) y[x][i].x = -INFINITY;
                                 if (static_cast<unsigned>(8 * i + 1 - from) >= count) y[x][i].y = -INFINITY;
                             }
                         }
                     }
                     // P = f16(2^(y - m)), sums of 2^(y - m) / vs.  A row keeps its m while no y
-                    // exceeds it by more than the threshold (P stays at most 2^8), so that the
-                    // lanes of a row need not agree on the tile's maximum
-                    auto exps = [&](float (&sum)[2]) {
-                        float2 ls[2][2] = {};
-                        float2 nm[2];
+                    // exceeds it by more than the threshold (P stays at most 2^8), so its 4
+                    // lanes need not agree on every tile's maximum
+                    float mx[4];
+                    bool over = false;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float mu = m[x] == -INFINITY ? 0.f : -m[x];
-                            nm[x] = make_float2(mu, mu);
+                    for (int x = 0; x < 4; ++x) {
+                        float q[2] = {fmaxf(y[x][0].x, y[x][0].y), fmaxf(y[x][1].x, y[x][1].y)};
+#pragma unroll
+                        for (int i = 2; i < 8; ++i) q[i & 1] = max3(q[i & 1], y[x][i].x, y[x][i].y);
+                        mx[x] = fmaxf(q[0], q[1]);
+                        over = over || mx[x] > m[x] + kRescaleThreshold;   // m = -inf: any kept key
+                    }
+                    if (__any_sync(0xffffffffu, over)) {
+                        float alpha[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float v = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                            alpha[x] = 1.f;
+                            if (v > m[x] + kRescaleThreshold) {
+                                alpha[x] = m[x] == -INFINITY ? 0.f : ex2_approx(m[x] - v);
+                                l[x] *= alpha[x];
+                                m[x] = v;
+                            }
                         }
+                        // what was weighted with the old maxima is rescaled: P of the tile's first
+                        // 64 keys, and the stream's O.  O's last PV has retired: S was issued
+                        // after it (one stream: PV of the unit before is waited for)
+                        if (c > 0) {
 #pragma unroll
-                        for (int c = 0; c < BN / 64; ++c) {
-                            uint32_t packed[16];
+                            for (int hf = 0; hf < 2; ++hf) {
+                                const uint32_t at = s_addr + (static_cast<uint32_t>(hf * 16) << 16);
+                                uint32_t r[16];
+                                tc_wait_st();
+                                tc_ld_16x128b_x8(at, r);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 iv = t.b[4 * (c * 8 + i) + (lane & 3)];
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+                                    const float al = alpha[2 * hf + (i & 1)];
+                                    const __half2 hv = __floats2half2_rn(v.x * al, v.y * al);
+                                    r[i] = *reinterpret_cast<const uint32_t*>(&hv);
+                                }
+                                tc_st_16x128b_x8(at, r);
+                            }
+                        }
+                        if (u >= C::NS) {
+                            if (C::NS == 1) {
+                                ok = __all_sync(0xffffffffu, wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
+                                                                       kErrTimeoutMma));
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            const uint32_t o_addr = lanes + C::COL_O + (C::NS == 2 ? buf * D : 0);
+#pragma unroll 1
+                            for (int e = 0; e < D; e += 32) {
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    const float2 d = fadd2(y[x][c * 8 + i], nm[x]);
-                                    const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-                                    ls[x][i & 1] = ffma2(p, iv, ls[x][i & 1]);
-                                    const __half2 hp = __floats2half2_rn(p.x, p.y);
-                                    packed[2 * i + x] = *reinterpret_cast<const uint32_t*>(&hp);
+                                for (int hf = 0; hf < 2; ++hf) {
+                                    const uint32_t at = o_addr + e + (static_cast<uint32_t>(hf * 16) << 16);
+                                    uint32_t r[16];
+                                    tc_ld_16x256b_x4(at, r);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha[2 * hf + ((i >> 1) & 1)]);
+                                    tc_st_16x256b_x4(at, r);
                                 }
                             }
-                            tc_st_16x128b_x8(s_addr + c * 32, packed);
-                        }
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float2 z = fadd2(ls[x][0], ls[x][1]);
-                            sum[x] = z.x + z.y;
-                        }
-                    };
-                    float sum[2], mx[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float q[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) q[e] = fmaxf(y[x][e].x, y[x][e].y);
-#pragma unroll
-                        for (int i = 4; i < BN / 8; ++i) q[i & 3] = max3(q[i & 3], y[x][i].x, y[x][i].y);
-                        mx[x] = fmaxf(max3(q[0], q[1], q[2]), q[3]);
-                    }
-                    const bool over = mx[0] > m[0] + kRescaleThreshold ||
-                                      mx[1] > m[1] + kRescaleThreshold;   // m = -inf: any kept key
-                    float alpha[2] = {1.f, 1.f};
-                    const bool moved = __any_sync(0xffffffffu, over);
-                    if (moved) {
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float v = mx[x];       // the row's 4 lanes agree on its maximum
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                            float& mu = m[x];
-                            if (v > mu + kRescaleThreshold) {
-                                alpha[x] = mu == -INFINITY ? 0.f : ex2_approx(mu - v);
-                                l[x] *= alpha[x];
-                                mu = v;
-                            }
                         }
                     }
-                    exps(sum);
-                    l[0] += sum[0];
-                    l[1] += sum[1];
-                    // the stream's O is rescaled when a maximum moved.  Its last PV has retired:
-                    // S was issued after it (one stream: PV of the unit before is waited for)
-                    if (moved && u >= C::NS) {
-                        if (C::NS == 1) {
-                            ok = __all_sync(0xffffffffu, wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
-                                                                   kErrTimeoutMma));
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        const uint32_t o_addr = rows + C::COL_O + (C::NS == 2 ? buf * D : 0);
-#pragma unroll 1
-                        for (int c = 0; c < D / 64; ++c) {
-                            uint32_t r[32];
-                            tc_ld_16x256b_x8(o_addr + c * 64, r);
-                            tc_wait_ld();
+                    float2 ls[4], nm[4];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha[(i >> 1) & 1]);
-                            tc_st_16x256b_x8(o_addr + c * 64, r);
+                    for (int x = 0; x < 4; ++x) {
+                        const float mu = m[x] == -INFINITY ? 0.f : -m[x];
+                        nm[x] = make_float2(mu, mu);
+                        ls[x] = make_float2(0.f, 0.f);
+                    }
+                    uint32_t packed[2][16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 iv = fb[4 * i];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 d = fadd2(y[x][i], nm[x]);
+                            const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                            ls[x] = ffma2(p, iv, ls[x]);
+                            const __half2 hp = __floats2half2_rn(p.x, p.y);
+                            packed[x / 2][2 * i + (x & 1)] = *reinterpret_cast<const uint32_t*>(&hp);
                         }
                     }
-                    if constexpr (XN == 4) {   // the other stream's state to the front
+                    // P's 32 columns of these keys, over S columns that have been read
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            float f = m[x];
-                            m[x] = m[x + 2];
-                            m[x + 2] = f;
-                            f = l[x];
-                            l[x] = l[x + 2];
-                            l[x + 2] = f;
-                            int i = klo[x];
-                            klo[x] = klo[x + 2];
-                            klo[x + 2] = i;
-                            i = khi[x];
-                            khi[x] = khi[x + 2];
-                            khi[x + 2] = i;
-                        }
-                    }
+                    for (int hf = 0; hf < 2; ++hf)
+                        tc_st_16x128b_x8(s_addr + c * 32 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) l[x] += ls[x].x + ls[x].y;
                 }
                 if (!ok) break;
                 tc_wait_st();
@@ -955,15 +962,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < XN; ++x) {
+            for (int x = 0; x < 4; ++x) {
                 float v = l[x];
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
-                // streams in the order of the segment's units, or the other way round after an
-                // odd number of them
-                const int first = C::NS == 2 ? (x / 2) ^ (U & 1) : 0;
-                if ((lane & 3) == 0)
-                    ml[first * BM + quarter * 32 + ws * 16 + (x & 1) * 8 + (lane >> 2)] = make_float2(m[x], v);
+                if ((lane & 3) == 0) ml[ws * BM + quarter * 32 + x * 8 + (lane >> 2)] = make_float2(m[x], v);
             }
             warp_arrive(bar(C::B_ML), lane);
             ok = __all_sync(0xffffffffu, wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
@@ -974,18 +977,17 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const bool halves = C::NS == 1 || !two;
                 const int row = quarter * 32 + lane;
                 const int cols = halves ? D / 2 : D, c0 = halves ? ws * (D / 2) : 0;
-                const int rt = two ? ws : 0;                              // row tile
-                const int q0 = w.rg * a.QTG + rt * a.QT1;
-                const int s0 = C::NS == 1 ? 0 : static_cast<int>((u0 + rt) & 1);   // its (first) stream
+                // of the streams: this warpgroup's, or the one with the segment's first unit
+                const int s0 = C::NS == 1 ? 0 : two ? ws : static_cast<int>(u0 & 1);
                 const bool both = C::NS == 2 && !two && n > 1;
-                const float2 x0 = ml[rt * BM + row];
-                float mx = x0.x, sum = x0.y, w0 = 1.f, w1 = 0.f;
+                float mx = ml[s0 * BM + row].x, sum = ml[s0 * BM + row].y, w0 = 1.f, w1 = 0.f;
                 if (both) {
-                    const float2 x1 = ml[BM + row];
-                    mx = fmaxf(x0.x, x1.x);
-                    w0 = x0.x == -INFINITY ? 0.f : ex2_approx(x0.x - mx);
+                    const float2 x1 = ml[(s0 ^ 1) * BM + row];
+                    const float m0 = mx;
+                    mx = fmaxf(m0, x1.x);
+                    w0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mx);
                     w1 = x1.x == -INFINITY ? 0.f : ex2_approx(x1.x - mx);
-                    sum = w0 * x0.y + w1 * x1.y;
+                    sum = w0 * sum + w1 * x1.y;
                 }
                 const int i = row / a.HG, gh = (w.head % a.n_hg) * a.HG + row % a.HG;
                 const int qi = q0 + i, orow = w.q_base + qi;
