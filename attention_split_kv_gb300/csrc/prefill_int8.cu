@@ -300,7 +300,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [warpgroup][row]
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---- this CTA's run: sum the key tiles of every (sequence, row group), then find
     // where the run starts
@@ -475,8 +475,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (leader) mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st), C::CODE_BYTES);
                     __syncwarp(gmask);
                     if (has_box)
-                        tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + lane * R * D, tm, bar(C::B_SFULL_ST + st), 0,
-                                    g, row, page);
+#pragma unroll
+                        for (int c = 0; c < D; c += 128)   // 128-byte columns
+                            tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + c * BN + lane * R * min(D, 128), tm,
+                                        bar(C::B_SFULL_ST + st), c, g, row, page);
                     sent |= 1u << st;
                     parity = (parity & ~(1u << st)) | (((gi / NST) & 1) << st);
                 }
@@ -490,73 +492,76 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, false);
-            constexpr uint32_t idesc_o = idesc_f16_f32(BM, D, true);
-            const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
-            const uint64_t k_desc = smem_desc_sw128(sbase + C::OFF_OP, 16, 1024);
-            const uint64_t v_desc = smem_desc_sw128(sbase + C::OFF_OP, C::OP_CHUNK, 1024);
-            // testing hook: hold back the signal of the first S tile
-            const bool stall = stall_first_tile();
-            uint32_t base = 0, jt = 0, u0 = 0, seg = 0;   // items, key tiles and units before this segment
-            bool ok = true;
-            for (bool more = seg_next<BN>(a, w, true, 0, 1u); ok && more;
-                 more = seg_next<BN>(a, w, false, 0, 1u), ++seg) {
-                const bool two = NT == 2 && w.two;
-                const int n = w.n, U = two ? 2 * n : n;
-                ok = wait(bar(C::B_QFULL), seg & 1, abort_flag, a.err, kErrTimeoutLoad);
-                auto issue_s = [&](int u) -> bool {
-                    const int j = two ? u >> 1 : u;
-                    const uint32_t gi = base + item_k(two, j), slot = gi % RING, buf = (u0 + u) & 1;
-                    if (!wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad))
-                        return false;
-                    tc_fence_after();
-                    const uint64_t kd = desc_advance(k_desc, slot * C::OP_BYTES);
-                    const uint64_t qd = desc_advance(q_desc, two ? (u & 1) * C::Q_TILE : 0);
+        // The whole warp runs it, one lane issues.
+        constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, false);
+        constexpr uint32_t idesc_o = idesc_f16_f32(BM, D, true);
+        const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(sbase + C::OFF_OP, 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(sbase + C::OFF_OP, C::OP_CHUNK, 1024);
+        const uint32_t one = elect_one();
+        // testing hook: hold back the signal of the first S tile
+        const bool stall = stall_first_tile();
+        uint32_t base = 0, jt = 0, u0 = 0, seg = 0;   // items, key tiles and units before this segment
+        auto wait_all = [&](int b, uint32_t parity, int code) -> bool {
+            return __all_sync(0xffffffffu, wait(bar(b), parity & 1, abort_flag, a.err, code));
+        };
+        bool ok = true;
+        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
+             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
+            const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.two, 0);
+            const int n = __shfl_sync(0xffffffffu, w.n, 0), U = two ? 2 * n : n;
+            ok = wait_all(C::B_QFULL, seg, kErrTimeoutLoad);
+            auto issue_s = [&](int u) -> bool {
+                const int j = two ? u >> 1 : u;
+                const uint32_t gi = base + item_k(two, j), slot = gi % RING, buf = (u0 + u) & 1;
+                if (!wait_all(C::B_OPFULL + slot, gi / RING, kErrTimeoutLoad)) return false;
+                tc_fence_after();
+                const uint64_t kd = desc_advance(k_desc, slot * C::OP_BYTES);
+                const uint64_t qd = desc_advance(q_desc, two ? (u & 1) * C::Q_TILE : 0);
 #pragma unroll
-                    for (int c = 0; c < NCH; ++c)
+                for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_f16_ss(tmem + buf * BN, desc_advance(qd, c * (BM * 128) + kk * 32),
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_f16_ss_one(one, tmem + buf * BN, desc_advance(qd, c * (BM * 128) + kk * 32),
                                           desc_advance(kd, c * C::OP_CHUNK + kk * 32), idesc_s, (c | kk) != 0);
-                    if (!(stall && u0 + u == 0)) tc_commit(bar(C::B_S + buf));
-                    if (!two || (u & 1)) tc_commit(bar(C::B_OPEMPTY + slot));
-                    if (u == U - 1) tc_commit(bar(C::B_QEMPTY));
-                    return true;
-                };
-                ok = ok && issue_s(0);
-                for (int u = 0; ok && u < U; ++u) {
-                    // S of the next unit overwrites P of the unit before this one, whose PV was
-                    // issued earlier: MMAs of one thread run in the order of their issue
-                    if (u + 1 < U && !(ok = issue_s(u + 1))) break;
-                    const uint32_t buf = (u0 + u) & 1;
-                    const int j = two ? u >> 1 : u;
-                    const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
-                    ok = wait(bar(C::B_P + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax) &&
-                         wait(bar(C::B_OPFULL + slot), (gi / RING) & 1, abort_flag, a.err, kErrTimeoutLoad);
-                    // O still holds the segment before until its rows have been read
-                    if (ok && u == 0 && seg > 0)
-                        ok = wait(bar(C::B_OFREE), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSoftmax);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (!two || (u & 1)) mbar_arrive(bar(C::B_TABEMPTY + (jt + j) % C::NTAB));
-                    const uint64_t vd = desc_advance(v_desc, slot * C::OP_BYTES);
-                    const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
+                if (!(stall && u0 + u == 0)) tc_commit_one(one, bar(C::B_S + buf));
+                if (!two || (u & 1)) tc_commit_one(one, bar(C::B_OPEMPTY + slot));
+                if (u == U - 1) tc_commit_one(one, bar(C::B_QEMPTY));
+                return true;
+            };
+            ok = ok && issue_s(0);
+            for (int u = 0; ok && u < U; ++u) {
+                // S of the next unit overwrites P of the unit before this one, whose PV was
+                // issued earlier: MMAs of one thread run in the order of their issue
+                if (u + 1 < U && !(ok = issue_s(u + 1))) break;
+                const uint32_t buf = (u0 + u) & 1;
+                const int j = two ? u >> 1 : u;
+                const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
+                ok = wait_all(C::B_P + buf, (u0 + u) >> 1, kErrTimeoutSoftmax) &&
+                     wait_all(C::B_OPFULL + slot, gi / RING, kErrTimeoutLoad);
+                // O still holds the segment before until its rows have been read
+                if (ok && u == 0 && seg > 0) ok = wait_all(C::B_OFREE, seg - 1, kErrTimeoutSoftmax);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = desc_advance(v_desc, slot * C::OP_BYTES);
+                const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        tc_mma_f16_ts(o_tmem, tmem + buf * BN + kk * 8, desc_advance(vd, kk * 16 * 128), idesc_o,
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    tc_mma_f16_ts_one(one, o_tmem, tmem + buf * BN + kk * 8, desc_advance(vd, kk * 16 * 128), idesc_o,
                                       u >= C::NS || kk > 0 ? 1u : 0u);
-                    if (C::NS == 1) tc_commit(bar(C::B_PV));
-                    if (!two || (u & 1)) tc_commit(bar(C::B_OPEMPTY + slot));
+                if (C::NS == 1) tc_commit_one(one, bar(C::B_PV));
+                if (!two || (u & 1)) {
+                    tc_commit_one(one, bar(C::B_OPEMPTY + slot));
+                    if (one) mbar_arrive(bar(C::B_TABEMPTY + (jt + j) % C::NTAB));   // its P are done
                 }
-                if (ok) tc_commit(bar(C::B_DONE));
-                base += 2 * n;
-                jt += n;
-                u0 += U;
             }
-            tc_commit(bar(C::B_TEARDOWN));   // all MMAs retire before TMEM is released
-            mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
+            if (ok) tc_commit_one(one, bar(C::B_DONE));
+            base += 2 * n;
+            jt += n;
+            u0 += U;
         }
+        tc_commit_one(one, bar(C::B_TEARDOWN));   // all MMAs retire before TMEM is released
+        mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
     } else {
         // ------------------------------------------------------------ per-key factors, Q
         // A lane takes a pair of keys (D = 64/128: two).  Its page ids come 4 tiles ahead
@@ -664,58 +669,64 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else if (warp >= C::NSM) {
         // ------------------------------------------------------------ converters
         regs_dec<kRegConvert>();
-        constexpr int CT = C::NCV * 32;               // threads
-        constexpr int CH = BN * D / 16 / CT;          // 16-code pieces a thread
-        const int ct = tid - C::NSM * 32;
-        uint32_t gi = 0, jt = 0;    // tiles converted; key tiles before this segment
+        // A thread takes pieces of 16 codes: one 16-byte load, two 16-byte stores of f16.
+        // Staged rows of 128 bytes are swizzled by their TMA copy (16-byte unit u of row r at
+        // u ^ (r & 7)), operand rows by what the MMA reads; 4 lanes take a row's 64 bytes, and
+        // the 8 lanes of an access phase the rows r and r ^ 5, whose units fall into distinct
+        // banks in the load and in both stores (64-byte rows: r and r + 1, not swizzled).
+        constexpr int ROWS = BN / C::NCV;             // of a warp
+        constexpr int GROUPS = ROWS / 8;              // 8 rows, a quad of lanes each
+        constexpr int HALVES = D / 64;                // 64-byte pieces of a row
+        const int cw = warp - C::NSM, quad = lane >> 2;
+        const int r8 = D == 64 ? quad : (quad & 1) ? (quad >> 1) ^ 5 : quad >> 1;   // row of 8
+        const int row0 = cw * ROWS + r8;
+        const uint32_t src0 = D == 64 ? row0 * 64 + (lane & 3) * 16 : row0 * 128 + (((lane & 3) ^ r8) << 4);
+        const uint32_t dst0 = row0 * 128 + (((lane & 3) * 2 ^ r8) << 4);     // and dst0 ^ 16
+        uint32_t st = 0, st_par = 0, slot = 0, slot_par = 1, jt = 0;   // rings, and key tiles before this segment
         bool ok = true;
         for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
              more = seg_next<BN>(a, w, false, lane, 0xffffffffu)) {
             const bool two = NT == 2 && w.two;
             const int n = w.n;
-            for (int i = 0; i < 2 * n; ++i, ++gi) {
+            for (int i = 0; i < 2 * n; ++i) {
                 int j;
                 const bool is_k = item_of(two, i, n, j);
-                const uint32_t st = gi % NST, slot = gi % RING, tb = (jt + j) % C::NTAB;
-                ok = wait(bar(C::B_SFULL_ST + st), (gi / NST) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                const KeyFactors<BN>& t = tab[(jt + j) % C::NTAB];
+                ok = wait(bar(C::B_SFULL_ST + st), st_par, abort_flag, a.err, kErrTimeoutLoad);
                 if (ok && !is_k)   // the signs of this tile's value scales
-                    ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad);
+                    ok = wait(bar(C::B_TAB + (jt + j) % C::NTAB), ((jt + j) / C::NTAB) & 1, abort_flag, a.err,
+                              kErrTimeoutLoad);
                 if (!ok) break;
                 const uint8_t* src = smem + C::OFF_CODE + st * C::CODE_BYTES;
-                uint8_t* dst = smem + C::OFF_OP + slot * C::OP_BYTES;
-                const __half2 one = __float2half2_rn(1.f), shift = __float2half2_rn(-1152.f);
-                uint4 v[CH];
-                uint32_t sg[CH];
+                uint8_t* dst = smem + C::OFF_OP + slot * C::OP_BYTES + dst0;
+                uint4 v[GROUPS][HALVES];
+                uint32_t sg[GROUPS];
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    v[c] = *reinterpret_cast<const uint4*>(src + (c * CT + ct) * 16);
-                    if (!is_k) sg[c] = tab[tb].sign[(c * CT + ct) / (D / 16)];
+                for (int g = 0; g < GROUPS; ++g) {
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h)
+                        v[g][h] = *reinterpret_cast<const uint4*>(
+                            src + ((src0 + g * 8 * (D == 64 ? 64 : 128)) ^ ((h & 1) * 64)) + (h >> 1) * (BN * 128));
+                    sg[g] = is_k ? 0x3c003c00u : t.sign[row0 + g * 8];
                 }
-                if (gi >= RING)
-                    ok = wait(bar(C::B_OPEMPTY + slot), ((gi / RING) - 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                // (a fresh barrier's "phase before" counts as complete: the first RING waits pass)
+                ok = wait(bar(C::B_OPEMPTY + slot), slot_par, abort_flag, a.err, kErrTimeoutMma);
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const int piece = c * CT + ct;
-                    const int row = piece / (D / 16), part = piece % (D / 16);
-                    __half2 s = one, off = shift;
-                    if (!is_k) {
-                        s = *reinterpret_cast<const __half2*>(&sg[c]);
-                        off = __hmul2(s, shift);
+                for (int g = 0; g < GROUPS; ++g) {
+                    const __half2 s = *reinterpret_cast<const __half2*>(&sg[g]);
+                    const __half2 off = __hmul2(s, __float2half2_rn(-1152.f));
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        uint4 x, y;
+                        codes_to_f16(v[g][h].x, s, off, x.x, x.y);
+                        codes_to_f16(v[g][h].y, s, off, x.z, x.w);
+                        codes_to_f16(v[g][h].z, s, off, y.x, y.y);
+                        codes_to_f16(v[g][h].w, s, off, y.z, y.w);
+                        uint8_t* d = dst + g * 1024 + h * C::OP_CHUNK;
+                        *reinterpret_cast<uint4*>(d) = x;
+                        *reinterpret_cast<uint4*>(smem + ((d - smem) ^ 16)) = y;
                     }
-                    uint4 x, y;
-                    codes_to_f16(v[c].x, s, off, x.x, x.y);
-                    codes_to_f16(v[c].y, s, off, x.z, x.w);
-                    codes_to_f16(v[c].z, s, off, y.x, y.y);
-                    codes_to_f16(v[c].w, s, off, y.z, y.w);
-                    // two 16-byte units of the row's 128-byte line; the lanes of the second
-                    // line store them the other way round, so that no two lanes of a store
-                    // meet in a bank
-                    uint8_t* line = dst + (part >> 2) * C::OP_CHUNK + row * 128;
-                    const int u = (part & 3) * 2, sw = row & 7;
-                    const bool flip = (part & 4) != 0;
-                    *reinterpret_cast<uint4*>(line + (((u + (flip ? 1 : 0)) ^ sw) << 4)) = flip ? y : x;
-                    *reinterpret_cast<uint4*>(line + (((u + (flip ? 0 : 1)) ^ sw) << 4)) = flip ? x : y;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -723,6 +734,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     mbar_arrive(bar(C::B_OPFULL + slot));
                     mbar_arrive(bar(C::B_SEMPTY_ST + st));
                 }
+                if (++st == NST) st = 0, st_par ^= 1;
+                if (++slot == RING) slot = 0, slot_par ^= 1;
             }
             jt += n;
         }
@@ -931,23 +944,26 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         nm[x] = make_float2(mu, mu);
                         ls[x] = make_float2(0.f, 0.f);
                     }
-                    uint32_t packed[2][16];
+                    // (32 keys a time: P's 16 columns, over S columns that have been read)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 iv = fb[4 * i];
+                    for (int i0 = 0; i0 < 8; i0 += 4) {
+                        uint32_t packed[2][8];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float2 d = fadd2(y[x][i], nm[x]);
-                            const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-                            ls[x] = ffma2(p, iv, ls[x]);
-                            const __half2 hp = __floats2half2_rn(p.x, p.y);
-                            packed[x / 2][2 * i + (x & 1)] = *reinterpret_cast<const uint32_t*>(&hp);
+                        for (int i = i0; i < i0 + 4; ++i) {
+                            const float2 iv = fb[4 * i];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float2 d = fadd2(y[x][i], nm[x]);
+                                const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                                ls[x] = ffma2(p, iv, ls[x]);
+                                const __half2 hp = __floats2half2_rn(p.x, p.y);
+                                packed[x / 2][2 * (i - i0) + (x & 1)] = *reinterpret_cast<const uint32_t*>(&hp);
+                            }
                         }
-                    }
-                    // P's 32 columns of these keys, over S columns that have been read
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        tc_st_16x128b_x8(s_addr + c * 32 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
+                        for (int hf = 0; hf < 2; ++hf)
+                            tc_st_16x128b_x4(s_addr + c * 32 + i0 * 4 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
+                    }
 #pragma unroll
                     for (int x = 0; x < 4; ++x) l[x] += ls[x].x + ls[x].y;
                 }
@@ -1150,11 +1166,10 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     {
         const uint64_t dims[4] = {(uint64_t)D, (uint64_t)L.Hkv, (uint64_t)L.page_size, (uint64_t)L.n_pages};
         const uint64_t strides[3] = {(uint64_t)D, (uint64_t)D * L.Hkv, (uint64_t)D * L.Hkv * L.page_size};
-        const uint32_t box[4] = {(uint32_t)D, 1u, (uint32_t)a.box_rows, 1u};
-        if ((st = encode_tmap_plain(&tk, L.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK)
-            return st;
-        if ((st = encode_tmap_plain(&tv, L.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK)
-            return st;
+        const uint32_t box[4] = {(uint32_t)(D < 128 ? D : 128), 1u, (uint32_t)a.box_rows, 1u};
+        auto encode = D == 64 ? encode_tmap_plain : encode_tmap_sw128;
+        if ((st = encode(&tk, L.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK) return st;
+        if ((st = encode(&tv, L.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, dims, strides, box)) != ATTN_OK) return st;
     }
     auto kernel = prefill8_kernel<D, NT, CAP>;
     static bool attr_set[64] = {};
