@@ -50,7 +50,7 @@ constexpr int kMinTiles = 2;                // least key tiles of a run
 // 5 warpgroups.  Registers at launch: 640 x 96; the softmax warpgroups then take
 // theirs from the last one's and the converters'.
 constexpr int kThreads = 640;
-constexpr int kRegSoftmax = 136, kRegConvert = 72, kRegOther = 64;
+constexpr int kRegSoftmax = 152, kRegConvert = 56, kRegOther = 64;
 static_assert(2 * kRegSoftmax + 2 * kRegConvert + kRegOther == 5 * 96, "register split");
 
 template <int N>
