@@ -66,14 +66,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// The bounded wait of ptx.cuh with its loop out of line: this kernel's roles together
-// run close to the instruction caches' size, and waits are in all of them.
-__device__ __forceinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
-    return mbar_wait(bar, parity, abort_flag, err, code);
-}
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
-    return mbar_try_wait(bar, parity) || wait_loop(bar, parity, abort_flag, err, code);
-}
 // One arrival of a whole warp: its lanes' earlier writes are ordered before it.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
     __syncwarp();
@@ -100,6 +92,7 @@ struct Cfg {
     // staged code tiles: what shared memory leaves beside Q and the operand ring
     static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
     static constexpr int NTAB = 4;                       // key-factor tables
+    static constexpr int SEGS = 4;                       // segment descriptions
     static constexpr uint32_t Q_TILE = NCH * BM * 128;
     static constexpr uint32_t OP_CHUNK = BN * 128, OP_BYTES = NCH * OP_CHUNK;
     static constexpr int IDS = 8, SCALES = 4;            // rings of prefetched page ids and scales (tiles)
@@ -120,21 +113,27 @@ struct Cfg {
         B_OPEMPTY = B_OPFULL + RING,       // operand tile: its MMAs are done
         B_TAB = B_OPEMPTY + RING,          // key factors are there
         B_TABEMPTY = B_TAB + NTAB,         // their tile's P are done, and its V is converted
-        B_QFULL = B_TABEMPTY + NTAB,
+        B_SEG = B_TABEMPTY + NTAB,         // segment descriptions
+        B_SEGFREE = B_SEG + SEGS,          // no warp needs it any more
+        B_QFULL = B_SEGFREE + SEGS,
         B_QEMPTY,
         B_S,                               // S of buffer 0, 1
-        B_P = B_S + 2,                     // P of buffer 0, 1
-        B_DONE = B_P + 2,                  // a segment's last PV is done
+        B_SFREE = B_S + 2,                 // it has been read (D = 256)
+        B_P = B_SFREE + 2,                 // P of buffer 0, 1
+        B_PV = B_P + 2,                    // its PV is done (D = 256)
+        B_DONE = B_PV + 2,                 // a segment's last PV is done
         B_OFREE,                           // its O has been read
         B_ML,                              // its row statistics are in shared memory
-        B_PV,                              // each PV (one stream only)
         B_TEARDOWN,
         N_BARS
     };
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag, start
     static constexpr uint32_t OFF_SEG = OFF_MISC + 16;
-    static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (kThreads / 32 + 1) * 72 + 1024;   // 72: sizeof(Seg)
-    static constexpr uint32_t COL_O = 2 * BN;            // S buffers first
+    static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (SEGS + 1) * 72 + 1024;   // 72: sizeof(Seg)
+    // TMEM: S of two units, P (D = 64/128: over the S it was made from), then O
+    static constexpr bool OVER = D <= 128;
+    static constexpr uint32_t COL_P = OVER ? 0 : 2 * BN, P_STRIDE = OVER ? BN : BN / 2;
+    static constexpr uint32_t COL_O = OVER ? 2 * BN : 2 * BN + BN;
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(OFF_SEG % 8 == 0, "alignment");
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
@@ -189,9 +188,9 @@ __device__ __forceinline__ Span group_span(const Args8& a, const Chunk& c, int r
     return s;
 }
 
-// A CTA's run of key tiles as segments, each of one item; every warp walks it alike,
-// with its state in shared memory (segments are long, and the code of a step is kept
-// out of the roles).
+// A CTA's run of key tiles as segments, each of one item.  One lane walks it and leaves
+// the segments in shared memory for all warps (the walk's code in each role would push the
+// roles' own code out of the instruction caches).
 struct Seg {
     int b, rg, hb, off, n_rg;
     int head;                 // kv head and head group
@@ -241,15 +240,6 @@ __device__ __forceinline__ void seg_step(const Args8& a, Seg& s, bool first) {
         if (s.head < a.Hkv * a.n_hg) return;   // the last batch may have fewer heads
     }
 }
-// `lanes` of a warp, all of which call it, move to its first or next segment.
-template <int BN>
-__device__ __forceinline__ bool seg_next(const Args8& a, Seg& s, bool first, int lane, unsigned lanes) {
-    __syncwarp(lanes);
-    if (lane == 0) seg_step<BN>(a, s, first);
-    __syncwarp(lanes);
-    return s.rem > 0;
-}
-
 // The order in which a segment of n key tiles loads them, which is the order the
 // MMAs first need them in: with two row tiles K0 V0 K1 V1 ..; with one, S of the next
 // tile runs before PV of this one: K0 K1 V0 K2 V1 .. .
@@ -295,11 +285,28 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const uint32_t sbase = smem_u32(smem);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-    Seg* segs = reinterpret_cast<Seg*>(smem + C::OFF_SEG);   // one a warp
-    Seg& first_seg = segs[kThreads / 32];
+    Seg* segs = reinterpret_cast<Seg*>(smem + C::OFF_SEG);
+    Seg& walk = segs[C::SEGS];     // the walk's own state
     KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [warpgroup][row]
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
+    // The bounded wait of ptx.cuh (mbar_wait) in less code (it is in all of this kernel's
+    // roles, which together run close to the instruction caches' size), and suspended up to
+    // 1 ms a try: 20 warps that poll slow down the ones that work.
+    const uint32_t limit = static_cast<uint32_t>(
+        min(*static_cast<volatile unsigned long long*>(&g_wait_limit_ns), 0xffffffffull));
+    auto wait = [limit](uint32_t b, uint32_t parity, volatile int* abort_flag, int* err, int code) -> bool {
+        if (mbar_try_wait_for(b, parity, 1000000)) return true;
+        const uint32_t t0 = globaltimer_lo();
+#pragma unroll 1
+        do {
+            if (mbar_try_wait_for(b, parity, 1000000)) return true;
+            if (*abort_flag) return false;
+        } while (globaltimer_lo() - t0 < limit);
+        *abort_flag = 1;
+        atomicExch(err, code);
+        return false;
+    };
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---- this CTA's run: sum the key tiles of every (sequence, row group), then find
@@ -346,6 +353,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_init(bar(C::B_OPFULL + i), C::NCV);
                 mbar_init(bar(C::B_OPEMPTY + i), 1);
             }
+            for (int i = 0; i < C::SEGS; ++i) {
+                mbar_init(bar(C::B_SEG + i), 1);
+                mbar_init(bar(C::B_SEGFREE + i), kThreads / 32);
+            }
             for (int i = 0; i < C::NTAB; ++i) {
                 mbar_init(bar(C::B_TAB + i), 1);
                 mbar_init(bar(C::B_TABEMPTY + i), 1);
@@ -354,12 +365,13 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_init(bar(C::B_QEMPTY), 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(bar(C::B_S + i), 1);
-                mbar_init(bar(C::B_P + i), 4);
+                mbar_init(bar(C::B_SFREE + i), C::NSM / C::NS);
+                mbar_init(bar(C::B_P + i), C::NSM / C::NS);
+                mbar_init(bar(C::B_PV + i), 1);
             }
             mbar_init(bar(C::B_DONE), 1);
             mbar_init(bar(C::B_OFREE), C::NSM);
             mbar_init(bar(C::B_ML), C::NSM);
-            mbar_init(bar(C::B_PV), 1);
             mbar_init(bar(C::B_TEARDOWN), 1);
             *abort_flag = 0;
             fence_barrier_init();
@@ -369,7 +381,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tmem_relinquish();
         }
         tc_fence_before();
-        if (tid == 0) first_seg.rem = 0;   // an empty run, unless a thread finds its start
+        if (tid == 0) walk.rem = 0;   // an empty run, unless a thread finds its start
         __syncthreads();
         tc_fence_after();
         long long before = 0, total = 0;
@@ -393,28 +405,26 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     return true;
                 }
                 const long long in = t0 - acc * a.n_hb;
-                first_seg.b = b;
-                first_seg.rg = rg;
-                first_seg.hb = static_cast<int>(in / t);
-                first_seg.off = static_cast<int>(in - static_cast<long long>(first_seg.hb) * t);
-                first_seg.rem = t1 - t0;
+                walk.b = b;
+                walk.rg = rg;
+                walk.hb = static_cast<int>(in / t);
+                walk.off = static_cast<int>(in - static_cast<long long>(walk.hb) * t);
+                walk.rem = t1 - t0;
                 return false;
             });
         }
         fence_proxy_async_smem();   // the scratch is where codes land
         __syncthreads();
     }
-    const uint32_t tmem = *tmem_holder;
-    Seg& w = segs[warp];
-    if (lane == 0) w = first_seg;
-    if (tid == 0) {
-        Seg s = first_seg;
-        seg_step<BN>(a, s, true);
-        int* m = a.meta + blockIdx.x * 8;
-        m[0] = s.rem > 0 && s.off > 0;                  // begins inside an item
-        m[1] = s.rem > 0 && s.n == s.tiles - s.off;     // and ends it
-        m[2] = 0;                                       // ends inside another (set below)
-    }
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+    // Segment `seg` of the run, once it is known; false at the run's end.  leave(): this warp
+    // needs segment `seg` no more.
+    auto enter = [&](uint32_t seg, const Seg*& w) -> bool {
+        const bool known = wait(bar(C::B_SEG + seg % C::SEGS), (seg / C::SEGS) & 1, abort_flag, a.err, kErrTimeoutSlot);
+        w = &segs[seg % C::SEGS];
+        return known && w->rem > 0;
+    };
+    auto leave = [&](uint32_t seg) { mbar_arrive(bar(C::B_SEGFREE + seg % C::SEGS)); };
 
     // (setmaxnreg is executed by all four warps of a warpgroup)
     if (warp >= C::K_WARP) {
@@ -436,12 +446,14 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             uint32_t base = 0;                     // items before this segment
             uint32_t sent = 0, parity = 0;         // stages this warp filled, and their phases (one bit each)
             int ok = 1;
-            for (bool more = seg_next<BN>(a, w, true, lane, gmask); ok && more;
-                 more = seg_next<BN>(a, w, false, lane, gmask)) {
-                const bool two = NT == 2 && w.two;
-                const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0 + lane * R;
-                const int g = w.head / a.n_hg;
-                const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+            const Seg* w;
+            for (uint32_t seg = 0; ok && __any_sync(gmask, enter(seg, w)); ++seg) {
+                const bool two = NT == 2 && w->two;
+                const int n = w->n, lo = w->lo, hi = w->hi, k0 = w->key0 + lane * R;
+                const int g = w->head / a.n_hg;
+                const int32_t* table = a.page_table + static_cast<size_t>(w->b) * a.max_pages;
+                __syncwarp(gmask);
+                if (leader) leave(seg);
                 auto in_use = [&](int kk) { return has_box && kk >= lo - R + 1 && kk < hi; };
                 auto fetch = [&](int j) {
                     const int kk = k0 + j * BN;
@@ -493,6 +505,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
         // The whole warp runs it, one lane issues.
+        // Unit u of a segment is a key tile with a row tile: of two row tiles, key tile u / 2 and
+        // row tile u % 2, else key tile u.  Where P lies over S, S of unit u + 2 is issued right
+        // after PV of unit u (MMAs of one thread run in the order of their issue); else before
+        // it, as soon as S of unit u has been read.
         constexpr uint32_t idesc_s = idesc_f16_f32(BM, BN, false);
         constexpr uint32_t idesc_o = idesc_f16_f32(BM, D, true);
         const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
@@ -501,20 +517,21 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const uint32_t one = elect_one();
         // testing hook: hold back the signal of the first S tile
         const bool stall = stall_first_tile();
-        uint32_t base = 0, jt = 0, u0 = 0, seg = 0;   // items, key tiles and units before this segment
+        uint32_t base = 0, jt = 0, u0 = 0;   // items, key tiles and units before this segment
         auto wait_all = [&](int b, uint32_t parity, int code) -> bool {
             return __all_sync(0xffffffffu, wait(bar(b), parity & 1, abort_flag, a.err, code));
         };
         bool ok = true;
-        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
-             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
-            const bool two = NT == 2 && __shfl_sync(0xffffffffu, w.two, 0);
-            const int n = __shfl_sync(0xffffffffu, w.n, 0), U = two ? 2 * n : n;
+        const Seg* w;
+        for (uint32_t seg = 0; ok && __any_sync(0xffffffffu, enter(seg, w)); ++seg) {
+            const bool two = NT == 2 && __shfl_sync(0xffffffffu, w->two, 0);
+            const int n = __shfl_sync(0xffffffffu, w->n, 0), U = two ? 2 * n : n;
+            if (one) leave(seg);
             ok = wait_all(C::B_QFULL, seg, kErrTimeoutLoad);
             auto issue_s = [&](int u) -> bool {
-                const int j = two ? u >> 1 : u;
-                const uint32_t gi = base + item_k(two, j), slot = gi % RING, buf = (u0 + u) & 1;
+                const uint32_t gi = base + item_k(two, two ? u >> 1 : u), slot = gi % RING, gu = u0 + u, buf = gu & 1;
                 if (!wait_all(C::B_OPFULL + slot, gi / RING, kErrTimeoutLoad)) return false;
+                if (!C::OVER && gu >= 2 && !wait_all(C::B_SFREE + buf, (gu >> 1) - 1, kErrTimeoutSoftmax)) return false;
                 tc_fence_after();
                 const uint64_t kd = desc_advance(k_desc, slot * C::OP_BYTES);
                 const uint64_t qd = desc_advance(q_desc, two ? (u & 1) * C::Q_TILE : 0);
@@ -524,20 +541,19 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma_f16_ss_one(one, tmem + buf * BN, desc_advance(qd, c * (BM * 128) + kk * 32),
                                           desc_advance(kd, c * C::OP_CHUNK + kk * 32), idesc_s, (c | kk) != 0);
-                if (!(stall && u0 + u == 0)) tc_commit_one(one, bar(C::B_S + buf));
+                if (!(stall && gu == 0)) tc_commit_one(one, bar(C::B_S + buf));
                 if (!two || (u & 1)) tc_commit_one(one, bar(C::B_OPEMPTY + slot));
                 if (u == U - 1) tc_commit_one(one, bar(C::B_QEMPTY));
                 return true;
             };
-            ok = ok && issue_s(0);
-            for (int u = 0; ok && u < U; ++u) {
-                // S of the next unit overwrites P of the unit before this one, whose PV was
-                // issued earlier: MMAs of one thread run in the order of their issue
-                if (u + 1 < U && !(ok = issue_s(u + 1))) break;
-                const uint32_t buf = (u0 + u) & 1;
+            // (units -2 and -1 only issue S of units 0 and 1)
+            for (int u = -2; ok && u < U; ++u) {
+                if ((!C::OVER || u < 0) && u + 2 < U && !(ok = issue_s(u + 2))) break;
+                if (u < 0) continue;
+                const uint32_t gu = u0 + u, buf = gu & 1;
                 const int j = two ? u >> 1 : u;
                 const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
-                ok = wait_all(C::B_P + buf, (u0 + u) >> 1, kErrTimeoutSoftmax) &&
+                ok = wait_all(C::B_P + buf, gu >> 1, kErrTimeoutSoftmax) &&
                      wait_all(C::B_OPFULL + slot, gi / RING, kErrTimeoutLoad);
                 // O still holds the segment before until its rows have been read
                 if (ok && u == 0 && seg > 0) ok = wait_all(C::B_OFREE, seg - 1, kErrTimeoutSoftmax);
@@ -547,13 +563,14 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                    tc_mma_f16_ts_one(one, o_tmem, tmem + buf * BN + kk * 8, desc_advance(vd, kk * 16 * 128), idesc_o,
-                                      u >= C::NS || kk > 0 ? 1u : 0u);
-                if (C::NS == 1) tc_commit_one(one, bar(C::B_PV));
+                    tc_mma_f16_ts_one(one, o_tmem, tmem + C::COL_P + buf * C::P_STRIDE + kk * 8,
+                                      desc_advance(vd, kk * 16 * 128), idesc_o, u >= C::NS || kk > 0 ? 1u : 0u);
+                if (!C::OVER) tc_commit_one(one, bar(C::B_PV + buf));
                 if (!two || (u & 1)) {
                     tc_commit_one(one, bar(C::B_OPEMPTY + slot));
                     if (one) mbar_arrive(bar(C::B_TABEMPTY + (jt + j) % C::NTAB));   // its P are done
                 }
+                if (C::OVER && u + 2 < U && !(ok = issue_s(u + 2))) break;
             }
             if (ok) tc_commit_one(one, bar(C::B_DONE));
             base += 2 * n;
@@ -570,31 +587,53 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const float kf = CAP ? a.scale / a.softcap : a.scale * kLog2e;
         const uint32_t ids = C::OFF_IDS, scl = C::OFF_SCALE + lane * 4;
         const int R = a.box_rows;
-        uint32_t jt = 0, seg = 0;    // key tiles and segments before this one
+        uint32_t jt = 0, seg = 0, known = 0;   // key tiles before this segment; segments published
         bool ok = true;
-        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
-             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
-            const int n = w.n, lo = w.lo, hi = w.hi, k0 = w.key0 + 2 * lane;
-            const int g = w.head / a.n_hg;
-            const int32_t* table = a.page_table + static_cast<size_t>(w.b) * a.max_pages;
+        const Seg* w;
+        for (;; ++seg) {
+            // this warp also walks the run: two segments ahead of its own, as far as the
+            // descriptions' ring has room
+            if (lane == 0) {
+                while (ok && known <= seg + 2 && (known == 0 || walk.rem > 0)) {
+                    const uint32_t e = known % C::SEGS;
+                    if (known >= C::SEGS)
+                        ok = wait(bar(C::B_SEGFREE + e), (known / C::SEGS - 1) & 1, abort_flag, a.err, kErrTimeoutSlot);
+                    if (!ok) break;
+                    seg_step<BN>(a, walk, known == 0);
+                    segs[e] = walk;
+                    if (known == 0) {
+                        int* m = a.meta + blockIdx.x * 8;
+                        m[0] = walk.rem > 0 && walk.off > 0;                      // begins inside an item
+                        m[1] = walk.rem > 0 && walk.n == walk.tiles - walk.off;   // and ends it
+                        m[2] = 0;                                                 // ends inside another (set below)
+                    }
+                    mbar_arrive(bar(C::B_SEG + e));
+                    ++known;
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || !__any_sync(0xffffffffu, enter(seg, w))) break;
+            const int n = w->n, lo = w->lo, hi = w->hi, k0 = w->key0 + 2 * lane;
+            const int g = w->head / a.n_hg;
+            const int32_t* table = a.page_table + static_cast<size_t>(w->b) * a.max_pages;
             if (lane == 0) {
                 if (seg > 0) ok = wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot);
                 if (ok) {
-                    const int nt = NT == 2 && w.two ? 2 : 1;
-                    const int h0 = g * a.G + (w.head % a.n_hg) * a.HG;
+                    const int nt = NT == 2 && w->two ? 2 : 1;
+                    const int h0 = g * a.G + (w->head % a.n_hg) * a.HG;
                     mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
                     for (int t = 0; t < nt; ++t)
 #pragma unroll 1
                         for (int c = 0; c < NCH; ++c)
                             tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64,
-                                        h0, w.q_base + w.rg * a.QTG + t * a.QT1);
+                                        h0, w->q_base + w->rg * a.QTG + t * a.QT1);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             // page ids: lane i < 16 that of the tile's i-th box
             auto fetch_ids = [&](int j) {
-                const int kk = w.key0 + j * BN + lane * R;
+                const int kk = w->key0 + j * BN + lane * R;
                 if (j < n && lane * R < BN && kk >= lo - R + 1 && kk < hi)
                     cp_async4(sbase + ids + (j % C::IDS) * 64 + lane * 4, &table[kk >> a.log2P]);
             };
@@ -663,6 +702,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             cp_async_wait<0>();
             jt += n;
+            warp_arrive(bar(C::B_SEGFREE + seg % C::SEGS), lane);
         }
         if (lane == 0 && *abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
     }
@@ -684,10 +724,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const uint32_t dst0 = row0 * 128 + (((lane & 3) * 2 ^ r8) << 4);     // and dst0 ^ 16
         uint32_t st = 0, st_par = 0, slot = 0, slot_par = 1, jt = 0;   // rings, and key tiles before this segment
         bool ok = true;
-        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
-             more = seg_next<BN>(a, w, false, lane, 0xffffffffu)) {
-            const bool two = NT == 2 && w.two;
-            const int n = w.n;
+        const Seg* w;
+        for (uint32_t seg = 0; ok && __any_sync(0xffffffffu, enter(seg, w)); ++seg) {
+            const bool two = NT == 2 && w->two;
+            const int n = w->n;
+            warp_arrive(bar(C::B_SEGFREE + seg % C::SEGS), lane);
             for (int i = 0; i < 2 * n; ++i) {
                 int j;
                 const bool is_k = item_of(two, i, n, j);
@@ -742,65 +783,84 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     } else {
         // ------------------------------------------------------------ softmax
         regs_inc<kRegSoftmax>();
-        // Each warpgroup takes the units of its stream (one stream: the first takes all), a
-        // warp 32 rows, 64 keys a time.  Of every 16-row half a thread holds rows lane / 4 and
-        // lane / 4 + 8, and of every 8 columns the pair 2 (lane % 4), so that a 16- and an
-        // 8-byte load of per-key factors serve 4 rows and 2 keys.  (For 2 rows the factors
-        // take as much of shared memory's bandwidth as the MMAs' operands; a row a thread
-        // would take 4 times as much.)
+        // Each warpgroup takes the units of its stream, a warp 32 rows (one stream: both take
+        // every unit, a warp 16 rows), 64 keys a time.  Of every 16-row half a thread holds
+        // rows lane / 4 and lane / 4 + 8, and of every 8 columns the pair 2 (lane % 4), so that
+        // a 16- and an 8-byte load of per-key factors serve 4 rows and 2 keys.  (For 2 rows the
+        // factors take as much of shared memory's bandwidth as the MMAs' operands; a row a
+        // thread would take 4 times as much.)
+        constexpr int HN = C::NS;                  // 16-row halves of a warp
         const int ws = warp >> 2;
         const int quarter = warp & 3;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int row0 = quarter * 32 + (HN == 1 ? ws * 16 : 0);   // the warp's first row
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(row0) << 16);
         const float cap_log2 = a.softcap * kLog2e;
+        const int W = a.window > 0 ? min(a.window, 0x3fffffff) : 0;
         uint32_t u0 = 0, jt = 0, seg = 0;
         bool ok = true;
-        for (bool more = seg_next<BN>(a, w, true, lane, 0xffffffffu); ok && more;
-             more = seg_next<BN>(a, w, false, lane, 0xffffffffu), ++seg) {
+        const Seg* wp;
+        for (; ok && __any_sync(0xffffffffu, enter(seg, wp)); ++seg) {
+            const Seg& w = *wp;
             const bool two = NT == 2 && w.two;
-            const int n = w.n, U = two ? 2 * n : n, k0 = w.key0;
-            const int first_u = C::NS == 1 ? (ws ? U : 0) : static_cast<int>((ws ^ u0) & 1);
+            const int n = w.n, U = two ? 2 * n : n, k0 = w.key0, hi = w.hi;
+            const int first_u = C::NS == 1 ? 0 : static_cast<int>((ws ^ u0) & 1);
             const int rt = two ? first_u : 0;      // this warpgroup's row tile
             const int q0 = w.rg * a.QTG + rt * a.QT1;
-            // rows quarter*32 + 8 x + lane / 4, at positions that ascend
-            int pos[4];
-            float m[4], l[4];
+            // rows row0 + 8 x + lane / 4, at positions that ascend
+            int pos[2 * HN];
+            float m[2 * HN], l[2 * HN];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                pos[x] = w.pos0 + q0 + (quarter * 32 + x * 8 + (lane >> 2)) / a.HG;
+            for (int x = 0; x < 2 * HN; ++x) {
+                pos[x] = w.pos0 + q0 + (row0 + x * 8 + (lane >> 2)) / a.HG;
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
-            // without a query among its rows a warp only keeps step (its rows of P are what S
-            // left there: rows of the products do not mix)
-            const bool idle = w.n_rows - q0 <= quarter * 32 / a.HG;
+            // keys in [all_lo, all_hi) are kept by each of the warp's rows
+            const int all_hi = min(hi, w.pos0 + q0 + row0 / a.HG + 1);
+            const int all_lo = W ? w.pos0 + q0 + (row0 + 16 * HN - 1) / a.HG - W + 1 : 0;
+            // without a query among its rows a warp only keeps step (its rows of P are what TMEM
+            // holds: rows of the products do not mix)
+            const bool idle = w.n_rows - q0 <= row0 / a.HG;
             for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
-                const uint32_t buf = (u0 + u) & 1, tb = (jt + j) % C::NTAB;
+                const uint32_t gu = u0 + u, buf = gu & 1, tb = (jt + j) % C::NTAB;
                 ok = wait(bar(C::B_TAB + tb), ((jt + j) / C::NTAB) & 1, abort_flag, a.err, kErrTimeoutLoad) &&
-                     wait(bar(C::B_S + buf), ((u0 + u) >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                     wait(bar(C::B_S + buf), (gu >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
                 ok = __all_sync(0xffffffffu, ok);   // tcgen05 loads and stores need whole warps
                 if (!ok) break;
                 tc_fence_after();
-                const KeyFactors<BN>& t = tab[tb];
+                // PV of unit g is done: its P may be overwritten, its O rescaled.  (Where P lies
+                // over S, S of unit g + 2 was issued after it.)
+                auto pv_done = [&](uint32_t g) -> bool {
+                    const bool done = wait(bar(C::B_PV + (g & 1)), (g >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
+                    tc_fence_after();
+                    return __all_sync(0xffffffffu, done);
+                };
+                if (!C::OVER && idle) warp_arrive(bar(C::B_SFREE + buf), lane);
+                if (!C::OVER && gu >= 2 && !(ok = pv_done(gu - 2))) break;
 #pragma unroll 1
                 for (int c = 0; c < BN / 64 && !idle; ++c) {   // 64 keys
-                    const float4* fa = t.a + c * 32 + (lane & 3);
-                    const float2* fb = t.b + c * 32 + (lane & 3);
+                    const float4* fa = tab[tb].a + c * 32 + (lane & 3);
+                    const float2* fb = tab[tb].b + c * 32 + (lane & 3);
                     const int key0 = k0 + j * BN + c * 64;
-                    const uint32_t s_addr = lanes + buf * BN;
-                    float2 y[4][8];                // [row][8-column group]
+                    const uint32_t p_addr = lanes + C::COL_P + buf * C::P_STRIDE;
+                    float2 y[2 * HN][8];           // [row][8-column group]
                     {
-                        uint32_t r[2][32];
+                        uint32_t r[HN][32];
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-                            tc_ld_16x256b_x8(s_addr + c * 64 + (static_cast<uint32_t>(hf * 16) << 16), r[hf]);
+                        for (int hf = 0; hf < HN; ++hf)
+                            tc_ld_16x256b_x8(lanes + buf * BN + c * 64 + (static_cast<uint32_t>(hf * 16) << 16), r[hf]);
                         tc_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                        for (int x = 0; x < 2 * HN; ++x)
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 y[x][i] = make_float2(__uint_as_float(r[x / 2][4 * i + 2 * (x & 1)]),
                                                       __uint_as_float(r[x / 2][4 * i + 2 * (x & 1) + 1]));
+                    }
+                    if (!C::OVER) {
+                        tc_fence_before();
+                        warp_arrive(bar(C::B_SFREE + buf), lane);
                     }
                     if constexpr (CAP) {
                         // c tanh(x) in log2 units: an odd polynomial for |x| <= 1/4 (the dropped
@@ -812,7 +872,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = fa[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
+                            for (int x = 0; x < 2 * HN; ++x) {
                                 y[x][i] = fmul2(y[x][i], make_float2(f.x, f.y));
                                 ax = max3(ax, fabsf(y[x][i].x), fabsf(y[x][i].y));
                             }
@@ -822,7 +882,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             for (int i = 0; i < 8; ++i) {
                                 const float4 f = fa[4 * i];
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
+                                for (int x = 0; x < 2 * HN; ++x) {
                                     const float2 v = y[x][i], z = fmul2(v, v);
                                     float2 q = ffma2(z, make_float2(k3, k3), make_float2(k2, k2));
                                     q = ffma2(q, z, make_float2(k1, k1));
@@ -835,7 +895,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             for (int i = 0; i < 8; ++i) {
                                 const float4 f = fa[4 * i];
 #pragma unroll
-                                for (int x = 0; x < 4; ++x)
+                                for (int x = 0; x < 2 * HN; ++x)
                                     y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(y[x][i].x), f.z),
                                                           fmaf(cap_log2, tanh_abs_accurate(y[x][i].y), f.w));
                             }
@@ -845,17 +905,13 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = fa[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
+                            for (int x = 0; x < 2 * HN; ++x)
                                 y[x][i] = ffma2(y[x][i], make_float2(f.x, f.y), make_float2(f.z, f.w));
                         }
                     }
-                    // a row keeps the keys [klo, khi)
-                    const int hi = w.hi, W = a.window > 0 ? min(a.window, 0x3fffffff) : 0;
-                    bool full = key0 + 64 <= min(hi, pos[0] + 1);
-                    if (W) full = full && key0 >= pos[3] - W + 1;
-                    if (!__all_sync(0xffffffffu, full)) {
+                    if (key0 < all_lo || key0 + 64 > all_hi) {   // a row keeps the keys [klo, khi)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
+                        for (int x = 0; x < 2 * HN; ++x) {
                             const int khi = min(hi, pos[x] + 1), klo = W ? max(0, pos[x] - W + 1) : 0;
                             const int from = klo - key0 - 2 * (lane & 3);
                             const unsigned count = max(khi - klo, 0);
@@ -869,10 +925,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     // P = f16(2^(y - m)), sums of 2^(y - m) / vs.  A row keeps its m while no y
                     // exceeds it by more than the threshold (P stays at most 2^8), so its 4
                     // lanes need not agree on every tile's maximum
-                    float mx[4];
+                    float mx[2 * HN];
                     bool over = false;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2 * HN; ++x) {
                         float q[2] = {fmaxf(y[x][0].x, y[x][0].y), fmaxf(y[x][1].x, y[x][1].y)};
 #pragma unroll
                         for (int i = 2; i < 8; ++i) q[i & 1] = max3(q[i & 1], y[x][i].x, y[x][i].y);
@@ -880,9 +936,9 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         over = over || mx[x] > m[x] + kRescaleThreshold;   // m = -inf: any kept key
                     }
                     if (__any_sync(0xffffffffu, over)) {
-                        float alpha[4];
+                        float alpha[2 * HN];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
+                        for (int x = 0; x < 2 * HN; ++x) {
                             float v = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
                             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                             alpha[x] = 1.f;
@@ -893,12 +949,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             }
                         }
                         // what was weighted with the old maxima is rescaled: P of the tile's first
-                        // 64 keys, and the stream's O.  O's last PV has retired: S was issued
-                        // after it (one stream: PV of the unit before is waited for)
-                        if (c > 0) {
+                        // 64 keys, and the stream's O (one stream: after PV of the unit before)
+                        if (BN > 64 && c > 0) {
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                const uint32_t at = s_addr + (static_cast<uint32_t>(hf * 16) << 16);
+                            for (int hf = 0; hf < HN; ++hf) {
+                                const uint32_t at = p_addr + (static_cast<uint32_t>(hf * 16) << 16);
                                 uint32_t r[16];
                                 tc_wait_st();
                                 tc_ld_16x128b_x8(at, r);
@@ -910,21 +965,17 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                     const __half2 hv = __floats2half2_rn(v.x * al, v.y * al);
                                     r[i] = *reinterpret_cast<const uint32_t*>(&hv);
                                 }
-                                tc_st_16x128b_x8(at, r);
+                                tc_st_16x128b_x4(at, *reinterpret_cast<const uint32_t(*)[8]>(r));
+                                tc_st_16x128b_x4(at + 16, *reinterpret_cast<const uint32_t(*)[8]>(r + 8));
                             }
                         }
                         if (u >= C::NS) {
-                            if (C::NS == 1) {
-                                ok = __all_sync(0xffffffffu, wait(bar(C::B_PV), (u0 + u - 1) & 1, abort_flag, a.err,
-                                                                       kErrTimeoutMma));
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
+                            if (C::NS == 1 && !(ok = pv_done(gu - 1))) break;
                             const uint32_t o_addr = lanes + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll 1
                             for (int e = 0; e < D; e += 32) {
 #pragma unroll
-                                for (int hf = 0; hf < 2; ++hf) {
+                                for (int hf = 0; hf < HN; ++hf) {
                                     const uint32_t at = o_addr + e + (static_cast<uint32_t>(hf * 16) << 16);
                                     uint32_t r[16];
                                     tc_ld_16x256b_x4(at, r);
@@ -937,22 +988,22 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             }
                         }
                     }
-                    float2 ls[4], nm[4];
+                    float2 ls[2 * HN], nm[2 * HN];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
+                    for (int x = 0; x < 2 * HN; ++x) {
                         const float mu = m[x] == -INFINITY ? 0.f : -m[x];
                         nm[x] = make_float2(mu, mu);
                         ls[x] = make_float2(0.f, 0.f);
                     }
-                    // (32 keys a time: P's 16 columns, over S columns that have been read)
+                    // (32 keys a time: 16 columns of P)
 #pragma unroll
                     for (int i0 = 0; i0 < 8; i0 += 4) {
-                        uint32_t packed[2][8];
+                        uint32_t packed[HN][8];
 #pragma unroll
                         for (int i = i0; i < i0 + 4; ++i) {
                             const float2 iv = fb[4 * i];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
+                            for (int x = 0; x < 2 * HN; ++x) {
                                 const float2 d = fadd2(y[x][i], nm[x]);
                                 const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
                                 ls[x] = ffma2(p, iv, ls[x]);
@@ -961,11 +1012,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             }
                         }
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-                            tc_st_16x128b_x4(s_addr + c * 32 + i0 * 4 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
+                        for (int hf = 0; hf < HN; ++hf)
+                            tc_st_16x128b_x4(p_addr + c * 32 + i0 * 4 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
                     }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) l[x] += ls[x].x + ls[x].y;
+                    for (int x = 0; x < 2 * HN; ++x) l[x] += ls[x].x + ls[x].y;
                 }
                 if (!ok) break;
                 tc_wait_st();
@@ -978,86 +1029,117 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+            for (int x = 0; x < 2 * HN; ++x) {
                 float v = l[x];
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
-                if ((lane & 3) == 0) ml[ws * BM + quarter * 32 + x * 8 + (lane >> 2)] = make_float2(m[x], v);
+                if ((lane & 3) == 0) ml[(HN == 2 ? ws * BM : 0) + row0 + x * 8 + (lane >> 2)] = make_float2(m[x], v);
             }
             warp_arrive(bar(C::B_ML), lane);
             ok = __all_sync(0xffffffffu, wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
             if (!ok) break;
             {
-                // one row a lane now.  Of two row tiles each warpgroup writes one, of a single one
-                // half of the columns, where two streams are joined
-                const bool halves = C::NS == 1 || !two;
-                const int row = quarter * 32 + lane;
-                const int cols = halves ? D / 2 : D, c0 = halves ? ws * (D / 2) : 0;
-                // of the streams: this warpgroup's, or the one with the segment's first unit
+                // A warp writes its quarter's 32 rows: of two row tiles each warpgroup one, of a
+                // single one half of the columns, where the two streams are joined.
+                const bool join = C::NS == 2 && !two && n > 1, whole = w.off == 0 && n == w.tiles;
+                const int cols = two ? D : D / 2, c0 = two ? 0 : ws * (D / 2);
+                // stream of this row tile, or of the segment's first unit; the other one
                 const int s0 = C::NS == 1 ? 0 : two ? ws : static_cast<int>(u0 & 1);
-                const bool both = C::NS == 2 && !two && n > 1;
-                float mx = ml[s0 * BM + row].x, sum = ml[s0 * BM + row].y, w0 = 1.f, w1 = 0.f;
-                if (both) {
-                    const float2 x1 = ml[(s0 ^ 1) * BM + row];
-                    const float m0 = mx;
-                    mx = fmaxf(m0, x1.x);
-                    w0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - mx);
-                    w1 = x1.x == -INFINITY ? 0.f : ex2_approx(x1.x - mx);
-                    sum = w0 * sum + w1 * x1.y;
-                }
-                const int i = row / a.HG, gh = (w.head % a.n_hg) * a.HG + row % a.HG;
-                const int qi = q0 + i, orow = w.q_base + qi;
-                const bool live = row < a.QT1 * a.HG && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
-                const bool whole = w.off == 0 && n == w.tiles;
-                // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
-                const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-                if (whole) {
-                    w0 *= inv;
-                    w1 *= inv;
-                }
-                const size_t at = static_cast<size_t>(orow) * a.Hq + (w.head / a.n_hg) * a.G + gh;
+                const uint32_t o_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::COL_O + c0;
+                const uint32_t o0 = o_tmem + s0 * D, o1 = o_tmem + (C::NS == 2 ? (s0 ^ 1) * D : 0);
+                const int kv = w.head / a.n_hg, hg0 = (w.head % a.n_hg) * a.HG;
                 const int slot = blockIdx.x * 2 + (w.off > 0 ? 0 : 1);
-                const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + row;
-                const uint32_t o0 = lanes + C::COL_O + (C::NS == 2 ? s0 * D : 0) + c0;
-                const uint32_t o1 = lanes + C::COL_O + (C::NS == 2 ? (s0 ^ 1) * D : 0) + c0;
+                float w0[4], w1[4];
+                char* dst[4];                      // of this lane's part of each row; null: not a row of the call
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = quarter * 32 + x * 8 + (lane >> 2);
+                    const float2 a0 = ml[s0 * BM + row];
+                    float mx = a0.x, sum = a0.y;
+                    w0[x] = 1.f;
+                    w1[x] = 0.f;
+                    if (join) {
+                        const float2 a1 = ml[(s0 ^ 1) * BM + row];
+                        mx = fmaxf(a0.x, a1.x);
+                        w0[x] = a0.x == -INFINITY ? 0.f : ex2_approx(a0.x - mx);
+                        w1[x] = a1.x == -INFINITY ? 0.f : ex2_approx(a1.x - mx);
+                        sum = w0[x] * a0.y + w1[x] * a1.y;
+                    }
+                    const int qi = q0 + row / a.HG, gh = hg0 + row % a.HG, orow = w.q_base + qi;
+                    const bool live = row < a.QT1 * a.HG && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
+                    const size_t at = static_cast<size_t>(orow) * a.Hq + kv * a.G + gh;
+                    const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + row;
+                    if (whole) {
+                        // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
+                        const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+                        w0[x] *= inv;
+                        w1[x] *= inv;
+                    }
+                    dst[x] = !live ? nullptr
+                             : whole ? reinterpret_cast<char*>(a.out + at * D + c0 + 8 * (lane & 3))
+                                     : reinterpret_cast<char*>(a.part_o + part * D + c0 + 2 * (lane & 3));
+                    if (live && c0 == 0 && (lane & 3) == 0) {
+                        if (!whole) a.part_ml[part] = make_float2(mx, sum);
+                        else if (a.lse)
+                            a.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
+                    }
+                }
 #pragma unroll 1
                 for (int c = 0; c < cols; c += 32) {
                     __syncwarp();
-                    uint32_t r[32];
-                    tc_ld_32x32b_x32(o0 + c, r);
-                    tc_wait_ld();
-                    float o[32];
+                    float o[2][16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
-                    if (both) {
-                        tc_ld_32x32b_x32(o1 + c, r);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t r[16];
+                        tc_ld_16x256b_x4(o0 + c + (static_cast<uint32_t>(hf * 16) << 16), r);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(r[e]), w1, o[e]);
-                    }
-                    if (live && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + c0 + c);
+                        for (int e = 0; e < 16; ++e) o[hf][e] = __uint_as_float(r[e]) * w0[2 * hf + ((e >> 1) & 1)];
+                        if (join) {
+                            tc_ld_16x256b_x4(o1 + c + (static_cast<uint32_t>(hf * 16) << 16), r);
+                            tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t hv[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const __half2 h2 = __floats2half2_rn(o[8 * e + 2 * x], o[8 * e + 2 * x + 1]);
-                                hv[x] = *reinterpret_cast<const uint32_t*>(&h2);
-                            }
-                            dst[e] = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+                            for (int e = 0; e < 16; ++e)
+                                o[hf][e] = fmaf(__uint_as_float(r[e]), w1[2 * hf + ((e >> 1) & 1)], o[hf][e]);
                         }
-                    } else if (live) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + c0 + c);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     }
-                }
-                if (live && c0 == 0) {
-                    if (!whole) a.part_ml[part] = make_float2(mx, sum);
-                    else if (a.lse)
-                        a.lse[at] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
+                    if (whole) {
+                        // the 4 lanes of a row hold 2 of every 8 columns: after a 4 x 4 transpose a
+                        // lane has 8 in a row, and the row's store is 64 bytes
+                        const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __half2 h2 = __floats2half2_rn(o[x / 2][4 * i + 2 * (x & 1)],
+                                                                     o[x / 2][4 * i + 2 * (x & 1) + 1]);
+                                v[i] = *reinterpret_cast<const uint32_t*>(&h2);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2) {
+                                const uint32_t g = __shfl_xor_sync(0xffffffffu, b0 ? v[i] : v[i + 1], 1);
+                                if (b0) v[i] = g;
+                                else v[i + 1] = g;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t g = __shfl_xor_sync(0xffffffffu, b1 ? v[i] : v[i + 2], 2);
+                                if (b1) v[i] = g;
+                                else v[i + 2] = g;
+                            }
+                            if (dst[x]) *reinterpret_cast<uint4*>(dst[x] + c * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (dst[x]) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<float2*>(dst[x] + (c + 8 * i) * 4) =
+                                        make_float2(o[x / 2][4 * i + 2 * (x & 1)], o[x / 2][4 * i + 2 * (x & 1) + 1]);
+                            }
+                    }
                 }
                 if (tid == 0 && w.off == 0 && !whole) {
                     int* meta = a.meta + blockIdx.x * 8;
@@ -1068,7 +1150,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             tc_fence_before();
-            warp_arrive(bar(C::B_OFREE), lane);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::B_OFREE));
+                leave(seg);
+            }
             u0 += U;
             jt += n;
         }
