@@ -443,6 +443,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int R = a.box_rows;
             const bool has_box = lane * R < BN;
             const uint32_t ids = C::OFF_IDS + (mine_k ? 1 : 2) * (C::IDS * 16 * 4) + lane * 4;
+            // (A parity wait is right only for a barrier at most one phase behind.  This warp's
+            // own items are at most 3 apart, and the converters free stages in item order, so
+            // the one it waited for last vouches for every earlier phase of any stage.)
+            static_assert(NST >= 3, "stage waits");
             uint32_t base = 0;                     // items before this segment
             uint32_t sent = 0, parity = 0;         // stages this warp filled, and their phases (one bit each)
             int ok = 1;
@@ -786,13 +790,15 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         // Each warpgroup takes the units of its stream, a warp 32 rows (one stream: both take
         // every unit, a warp 16 rows), 64 keys a time.  Of every 16-row half a thread holds
         // rows lane / 4 and lane / 4 + 8, and of every 8 columns the pair 2 (lane % 4), so that
-        // a 16- and an 8-byte load of per-key factors serve 4 rows and 2 keys.  (For 2 rows the
-        // factors take as much of shared memory's bandwidth as the MMAs' operands; a row a
-        // thread would take 4 times as much.)
-        constexpr int HN = C::NS;                  // 16-row halves of a warp
+        // a 16- and an 8-byte load of per-key factors serve 2 keys of 4 rows; a row a thread
+        // would take 4 times the loads.  Where row groups have one row tile the halves go one
+        // after the other, so that the second one, often without rows, can be left out.
+        constexpr int HL = C::NS;                  // 16-row halves of a warp
+        constexpr int HN = NT == 2 ? 2 : 1;        // taken at once
+        static_assert(HN <= HL, "halves");
         const int ws = warp >> 2;
         const int quarter = warp & 3;
-        const int row0 = quarter * 32 + (HN == 1 ? ws * 16 : 0);   // the warp's first row
+        const int row0 = quarter * 32 + (HL == 1 ? ws * 16 : 0);   // the warp's first row
         const uint32_t lanes = tmem + (static_cast<uint32_t>(row0) << 16);
         const float cap_log2 = a.softcap * kLog2e;
         const int W = a.window > 0 ? min(a.window, 0x3fffffff) : 0;
@@ -807,20 +813,21 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int rt = two ? first_u : 0;      // this warpgroup's row tile
             const int q0 = w.rg * a.QTG + rt * a.QT1;
             // rows row0 + 8 x + lane / 4, at positions that ascend
-            int pos[2 * HN];
-            float m[2 * HN], l[2 * HN];
+            int pos[2 * HL];
+            float m[2 * HL], l[2 * HL];
 #pragma unroll
-            for (int x = 0; x < 2 * HN; ++x) {
+            for (int x = 0; x < 2 * HL; ++x) {
                 pos[x] = w.pos0 + q0 + (row0 + x * 8 + (lane >> 2)) / a.HG;
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
             // keys in [all_lo, all_hi) are kept by each of the warp's rows
             const int all_hi = min(hi, w.pos0 + q0 + row0 / a.HG + 1);
-            const int all_lo = W ? w.pos0 + q0 + (row0 + 16 * HN - 1) / a.HG - W + 1 : 0;
+            const int all_lo = W ? w.pos0 + q0 + (row0 + 16 * HL - 1) / a.HG - W + 1 : 0;
             // without a query among its rows a warp only keeps step (its rows of P are what TMEM
             // holds: rows of the products do not mix)
             const bool idle = w.n_rows - q0 <= row0 / a.HG;
+            const int nh = HL == HN ? 1 : w.n_rows - q0 <= (row0 + 16) / a.HG ? 1 : 2;   // halves in turn
             for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t gu = u0 + u, buf = gu & 1, tb = (jt + j) % C::NTAB;
@@ -839,17 +846,19 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (!C::OVER && idle) warp_arrive(bar(C::B_SFREE + buf), lane);
                 if (!C::OVER && gu >= 2 && !(ok = pv_done(gu - 2))) break;
 #pragma unroll 1
-                for (int c = 0; c < BN / 64 && !idle; ++c) {   // 64 keys
+                for (int it = 0; it < BN / 64 * nh && !idle; ++it) {   // 64 keys, a half or both
+                    const int c = nh == 2 ? it >> 1 : it;
+                    const uint32_t half = nh == 2 ? static_cast<uint32_t>((it & 1) * 16) << 16 : 0u;
                     const float4* fa = tab[tb].a + c * 32 + (lane & 3);
                     const float2* fb = tab[tb].b + c * 32 + (lane & 3);
                     const int key0 = k0 + j * BN + c * 64;
-                    const uint32_t p_addr = lanes + C::COL_P + buf * C::P_STRIDE;
+                    const uint32_t p_addr = lanes + half + C::COL_P + buf * C::P_STRIDE;
                     float2 y[2 * HN][8];           // [row][8-column group]
                     {
                         uint32_t r[HN][32];
 #pragma unroll
                         for (int hf = 0; hf < HN; ++hf)
-                            tc_ld_16x256b_x8(lanes + buf * BN + c * 64 + (static_cast<uint32_t>(hf * 16) << 16), r[hf]);
+                            tc_ld_16x256b_x8(lanes + half + buf * BN + c * 64 + (static_cast<uint32_t>(hf * 16) << 16), r[hf]);
                         tc_wait_ld();
 #pragma unroll
                         for (int x = 0; x < 2 * HN; ++x)
@@ -971,7 +980,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         }
                         if (u >= C::NS) {
                             if (C::NS == 1 && !(ok = pv_done(gu - 1))) break;
-                            const uint32_t o_addr = lanes + C::COL_O + (C::NS == 2 ? buf * D : 0);
+                            const uint32_t o_addr = lanes + half + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll 1
                             for (int e = 0; e < D; e += 32) {
 #pragma unroll
@@ -1017,6 +1026,21 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
 #pragma unroll
                     for (int x = 0; x < 2 * HN; ++x) l[x] += ls[x].x + ls[x].y;
+                    if constexpr (HL > HN) {
+                        if (nh == 2) {   // the other half's state to the front
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float fm = m[x], fl = l[x];
+                                const int ip = pos[x];
+                                m[x] = m[x + 2];
+                                l[x] = l[x + 2];
+                                pos[x] = pos[x + 2];
+                                m[x + 2] = fm;
+                                l[x + 2] = fl;
+                                pos[x + 2] = ip;
+                            }
+                        }
+                    }
                 }
                 if (!ok) break;
                 tc_wait_st();
@@ -1029,11 +1053,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 2 * HN; ++x) {
+            for (int x = 0; x < 2 * HL; ++x) {
                 float v = l[x];
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
-                if ((lane & 3) == 0) ml[(HN == 2 ? ws * BM : 0) + row0 + x * 8 + (lane >> 2)] = make_float2(m[x], v);
+                if ((lane & 3) == 0) ml[(HL == 2 ? ws * BM : 0) + row0 + x * 8 + (lane >> 2)] = make_float2(m[x], v);
             }
             warp_arrive(bar(C::B_ML), lane);
             ok = __all_sync(0xffffffffu, wait(bar(C::B_ML), seg & 1, abort_flag, a.err, kErrTimeoutSoftmax));
