@@ -92,6 +92,10 @@ struct Cfg {
     // staged code tiles: what shared memory leaves beside Q and the operand ring
     static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
     static constexpr int NTAB = 4;                       // key-factor tables
+    // what a segment costs beside its key tiles (filling the pipeline, writing its rows), in
+    // key tiles: 12 to 16 thousand cycles, where a tile takes 2.7 (one row tile), 5 (two) or
+    // 1.5 thousand (D = 256).  8 x 512 chunks: 337 us unweighted, 306 weighted
+    static constexpr int SEG_TILES = D == 256 ? 6 : 3;
     static constexpr int SEGS = 4;                       // segment descriptions
     static constexpr uint32_t Q_TILE = NCH * BM * 128;
     static constexpr uint32_t OP_CHUNK = BN * 128, OP_BYTES = NCH * OP_CHUNK;
@@ -332,18 +336,25 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 ++b;
             }
         };
-        long long mine = 0;
+        long long mine = 0, tiles = 0;         // weights, and key tiles alone
         visit([&](int, int, int t) {
-            mine += t;
+            mine += t + C::SEG_TILES;
+            tiles += t;
             return true;
         });
-        long long incl = mine;
+        long long incl = mine, incl_t = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, incl_t, o);
+            if (lane >= o) {
+                incl += x;
+                incl_t += y;
+            }
         }
-        if (lane == 31) sums[warp] = incl;
+        if (lane == 31) {
+            sums[warp] = incl;
+            sums[32 + warp] = incl_t;
+        }
         if (tid == 0) {
             for (int i = 0; i < NST; ++i) {
                 mbar_init(bar(C::B_SFULL_ST + i), 1);
@@ -381,38 +392,61 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             tmem_relinquish();
         }
         tc_fence_before();
-        if (tid == 0) walk.rem = 0;   // an empty run, unless a thread finds its start
         __syncthreads();
         tc_fence_after();
-        long long before = 0, total = 0;
-#pragma unroll
+        long long before = incl - mine, before_t = incl_t - tiles, total = 0, total_t = 0;
+#pragma unroll 4
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sums[w];
+            if (w < warp) {
+                before += sums[w];
+                before_t += sums[32 + w];
+            }
             total += sums[w];
+            total_t += sums[32 + w];
         }
-        before += incl - mine;
-        // as many runs as CTAs for each of the hp heads, or fewer of kMinTiles
+        // as many runs as CTAs for each of the hp heads, or fewer of kMinTiles.  A run's weight is
+        // more than SEG_TILES, so it has a key tile at least.
         const long long all = total * a.n_hb;
         const int rank = static_cast<int>(blockIdx.x) / a.hp;
-        const long long runs = max(1ll, min(static_cast<long long>(gridDim.x / a.hp), all / kMinTiles));
-        const long long t0 = rank < runs ? all * rank / runs : all;
-        const long long t1 = rank < runs ? all * (rank + 1) / runs : all;
-        if (t0 < t1 && before * a.n_hb <= t0 && t0 < (before + mine) * a.n_hb) {   // one thread
-            long long acc = before;
-            visit([&](int b, int rg, int t) {
-                if ((acc + t) * a.n_hb <= t0) {
-                    acc += t;
+        const long long runs =
+            max(1ll, min(static_cast<long long>(gridDim.x / a.hp), all / (C::SEG_TILES + kMinTiles)));
+        // where weight t lies: the thread that has it leaves the key tiles before it, and for the
+        // run's start the item
+        auto locate = [&](long long t, long long* pos, bool start) {
+            if (before * a.n_hb > t || t >= (before + mine) * a.n_hb) return;
+            long long acc = before, acc_t = before_t;
+            visit([&](int b, int rg, int n) {
+                const int weight = n + C::SEG_TILES;
+                if ((acc + weight) * a.n_hb <= t) {
+                    acc += weight;
+                    acc_t += n;
                     return true;
                 }
-                const long long in = t0 - acc * a.n_hb;
-                walk.b = b;
-                walk.rg = rg;
-                walk.hb = static_cast<int>(in / t);
-                walk.off = static_cast<int>(in - static_cast<long long>(walk.hb) * t);
-                walk.rem = t1 - t0;
+                const long long in = t - acc * a.n_hb;
+                const int hb = static_cast<int>(in / weight);
+                const int off = max(static_cast<int>(in - static_cast<long long>(hb) * weight) - C::SEG_TILES, 0);
+                *pos = acc_t * a.n_hb + static_cast<long long>(hb) * n + off;
+                if (start) {
+                    walk.b = b;
+                    walk.rg = rg;
+                    walk.hb = hb;
+                    walk.off = off;
+                }
                 return false;
             });
+        };
+        if (rank < runs) {
+#pragma unroll 1
+            for (int e = 0; e < 2; ++e) {
+                const long long t = all * (rank + e) / runs;
+                if (t < all) locate(t, &sums[64 + e], e == 0);
+                else if (tid == 0) sums[64 + e] = total_t * a.n_hb;
+            }
+        } else if (tid == 0) {
+            sums[64] = sums[65] = 0;
         }
+        __syncthreads();
+        if (tid == 0) walk.rem = sums[65] - sums[64];   // 0: no run
         fence_proxy_async_smem();   // the scratch is where codes land
         __syncthreads();
     }
