@@ -65,20 +65,40 @@ __device__ __forceinline__ Where find_row(const int32_t* __restrict__ start, con
     return w;
 }
 
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// 8 elements as they lie in memory, and as f32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__half> {
+    uint4 r;
+    __device__ __forceinline__ void load(const __half* p) { r = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
     }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    Raw8<T> r;
+    r.load(p);
+    r.get(x);
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -120,18 +140,34 @@ __device__ __forceinline__ bool find_slot(const CacheLayout& c, int b, long long
 }
 
 // ------------------------------------------------------------------ append
-// One CTA a token, one group of D/8 lanes a head at a time (8 elements a lane,
-// 16-byte accesses): the norm, the largest magnitude and the half-split partner
-// are shuffles inside the group.
+// A CTA takes a token (blockIdx.x), or of few tokens a part of its heads (blockIdx.y of
+// gridDim.y); a group of D/8 lanes a head at a time, 8 elements a lane (16-byte accesses).
+// The norm, the largest magnitude and the half-split partner are shuffles inside the group.
+// A lane's first two loads are issued before the search for the token's sequence, each
+// later one before the head two back is worked on, so that the chain of dependent loads
+// (sequence, page, table row) lies under them.
 template <int D, typename T, typename TQ, bool INT8>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     constexpr int LPR = D / 8;          // lanes a head
     constexpr int RPW = 32 / LPR;       // heads a warp
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31;
     const int t = blockIdx.x;
     const int sub = lane & (LPR - 1);   // lane within its head
     const int e0 = sub * 8;             // its first element
     const int n_heads = a.Hq + 2 * a.Hkv;
+    const int step = static_cast<int>(gridDim.y * (blockDim.x >> 5)) * RPW;
+    int h0 = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * RPW;
+    auto fetch = [&](int h, Raw8<T>& r) {
+        if (h >= n_heads) return;
+        const T* p = h < a.Hq            ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
+                     : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_stride + (h - a.Hq) * D
+                                        : static_cast<const T*>(a.v) + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
+        r.load(p + e0);
+    };
+    Raw8<T> raw[2];
+    fetch(h0 + lane / LPR, raw[0]);
+    fetch(h0 + step + lane / LPR, raw[1]);
+
     const Where w = find_row(a.q_start, a.kv_len, a.B, t, lane);
     if (w.b < 0) return;
     const long long p = static_cast<long long>(w.len) - w.end + t;   // kv_len - q_len + i
@@ -164,18 +200,15 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         }
     }
 
-    for (int h0 = warp * RPW; h0 < n_heads; h0 += n_warps * RPW) {   // uniform in the warp
+    for (; h0 < n_heads; h0 += step) {   // uniform in the warp
         const int h = h0 + lane / LPR;
         const bool live = h < n_heads;
         const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;    // q, k, v
         const int hh = kind == 0 ? h : kind == 1 ? h - a.Hq : h - a.Hq - a.Hkv;
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) {
-            const T* src = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                           static_cast<size_t>(t) * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
-                           hh * D + e0;
-            load8(src, x);
-        }
+        if (live) raw[0].get(x);
+        raw[0] = raw[1];
+        fetch(h + 2 * step, raw[1]);
         const float* nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
         if (a.q_norm || a.k_norm) {
             float ss = 0.f;
@@ -236,10 +269,15 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         if constexpr (INT8) {
             uint32_t c[2] = {0, 0};
             if (scale > 0.f && scale < INFINITY) {
+                // x times 1 / scale is within 2^-23 * 127.1 < 2e-5 of x / scale, so it rounds
+                // alike unless it lies that near to a tie: then the division decides
+                const float inv = __fdiv_rn(1.0f, scale);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float q = fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.f), 127.f);
-                    c[i / 4] |= (static_cast<uint32_t>(static_cast<int>(q)) & 0xffu) << (8 * (i & 3));
+                    float q = x[i] * inv, r = rintf(q);
+                    if (fabsf(q - r) > 0.4999f) r = rintf(__fdiv_rn(x[i], scale));
+                    r = fminf(fmaxf(r, -127.f), 127.f);
+                    c[i / 4] |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * (i & 3));
                 }
             }
             *reinterpret_cast<uint2*>(static_cast<int8_t*>(kind == 1 ? a.k_cache : a.v_cache) + at) =
@@ -254,70 +292,89 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 }
 
 template <int D, typename T, typename TQ>
-void append_dispatch(const AppendArgs& a, bool int8, int threads, cudaStream_t s) {
-    if (int8) append_kernel<D, T, TQ, true><<<a.total_q, threads, 0, s>>>(a);
-    else append_kernel<D, T, TQ, false><<<a.total_q, threads, 0, s>>>(a);
+void append_dispatch(const AppendArgs& a, bool int8, dim3 grid, int threads, cudaStream_t s) {
+    if (int8) append_kernel<D, T, TQ, true><<<grid, threads, 0, s>>>(a);
+    else append_kernel<D, T, TQ, false><<<grid, threads, 0, s>>>(a);
 }
 template <int D>
-void append_types(const AppendLaunch& L, int threads) {
+void append_types(const AppendLaunch& L, dim3 grid, int threads) {
     if (L.in_f32) {
-        if (L.q_out_f32) append_dispatch<D, float, float>(L.args, L.int8, threads, L.stream);
-        else append_dispatch<D, float, __half>(L.args, L.int8, threads, L.stream);
+        if (L.q_out_f32) append_dispatch<D, float, float>(L.args, L.int8, grid, threads, L.stream);
+        else append_dispatch<D, float, __half>(L.args, L.int8, grid, threads, L.stream);
     } else {
-        if (L.q_out_f32) append_dispatch<D, __half, float>(L.args, L.int8, threads, L.stream);
-        else append_dispatch<D, __half, __half>(L.args, L.int8, threads, L.stream);
+        if (L.q_out_f32) append_dispatch<D, __half, float>(L.args, L.int8, grid, threads, L.stream);
+        else append_dispatch<D, __half, __half>(L.args, L.int8, grid, threads, L.stream);
     }
 }
 
 // ------------------------------------------------------------------ read back
-// A warp takes 4 consecutive rows; a lane 16 elements at a time (one 16-byte load
-// of codes, or two of f16).
-constexpr int kReadRows = 4, kReadWarps = 8;
+// A warp takes a row; a lane pieces of 16 elements (one 16-byte load of codes, two of f16),
+// four at a time, all loads before the first store.
+constexpr int kReadWarps = 8;
 
 template <typename TO, bool INT8>
 __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long t0 = (static_cast<long long>(blockIdx.x) * kReadWarps + warp) * kReadRows;
-    const int per = a.Hkv * (a.D / 16);   // 16-element pieces of a token's K (or V)
-    for (int r = 0; r < kReadRows; ++r) {
-        if (t0 + r >= a.total) return;
-        const int t = static_cast<int>(t0 + r);
-        const Where w = find_row(a.out_start, a.kv_len, a.B, t, lane);
-        if (w.b < 0) return;
-        const long long p = (a.first ? static_cast<long long>(a.first[w.b]) : 0ll) + (t - w.start);
-        bool held = p >= 0 && p < w.len && p < a.cache.capacity &&
-                    (a.cache.ring == 0 || p >= static_cast<long long>(w.len) - a.cache.ring);
-        Slot slot{0, 0};
-        if (held) held = find_slot(a.cache, w.b, p, slot, a.err);
-        const size_t row = slot.slot * a.cache.rows + slot.row;
-        for (int c = lane; c < 2 * per; c += 32) {
+    const int lane = threadIdx.x & 31;
+    const long long t = static_cast<long long>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
+    if (t >= a.total) return;
+    const int log_d = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;   // log2 of a head's pieces
+    const int per = a.Hkv << log_d;                          // pieces of a token's K (or V)
+    const Where w = find_row(a.out_start, a.kv_len, a.B, static_cast<int>(t), lane);
+    if (w.b < 0) return;
+    const long long p = (a.first ? static_cast<long long>(a.first[w.b]) : 0ll) + (t - w.start);
+    bool held = p >= 0 && p < w.len && p < a.cache.capacity &&
+                (a.cache.ring == 0 || p >= static_cast<long long>(w.len) - a.cache.ring);
+    Slot slot{0, 0};
+    if (held) held = find_slot(a.cache, w.b, p, slot, a.err);
+    const size_t src = (slot.slot * a.cache.rows + slot.row) * a.Hkv * a.D;
+    const size_t dst = static_cast<size_t>(t) * a.Hkv * a.D;
+    for (int c0 = lane; c0 < 2 * per; c0 += 128) {
+        uint4 raw[4][INT8 ? 1 : 2];
+        __half sc[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + 32 * u;
             const bool is_k = c < per;
             const int cc = is_k ? c : c - per;
-            const int hh = cc / (a.D / 16);
+            if (c >= 2 * per || !held) {
+#pragma unroll
+                for (int i = 0; i < (INT8 ? 1 : 2); ++i) raw[u][i] = make_uint4(0u, 0u, 0u, 0u);
+                sc[u] = __float2half_rn(0.f);
+            } else if constexpr (INT8) {
+                raw[u][0] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(is_k ? a.k_cache : a.v_cache) +
+                                                            src + static_cast<size_t>(cc) * 16);
+                sc[u] = static_cast<const __half*>(
+                    is_k ? a.k_scales : a.v_scales)[(slot.slot * a.Hkv + (cc >> log_d)) * a.cache.rows + slot.row];
+            } else {
+                const uint4* s = reinterpret_cast<const uint4*>(
+                    static_cast<const __half*>(is_k ? a.k_cache : a.v_cache) + src + static_cast<size_t>(cc) * 16);
+                raw[u][0] = s[0];
+                raw[u][1] = s[1];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + 32 * u;
+            if (c >= 2 * per) break;
+            const bool is_k = c < per;
+            TO* out = static_cast<TO*>(is_k ? a.k_out : a.v_out) + dst + static_cast<size_t>(is_k ? c : c - per) * 16;
             float x[2][8];
+            if constexpr (INT8) {
+                const float s = __half2float(sc[u]);
+                const uint32_t wd[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[0][i] = x[1][i] = 0.f;
-            if (held) {
-                const size_t at = row * a.Hkv * a.D + static_cast<size_t>(cc) * 16;
-                if constexpr (INT8) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(
-                        static_cast<const int8_t*>(is_k ? a.k_cache : a.v_cache) + at);
-                    const float s = __half2float(static_cast<const __half*>(
-                        is_k ? a.k_scales : a.v_scales)[(slot.slot * a.Hkv + hh) * a.cache.rows + slot.row]);
-                    const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
+                for (int i = 0; i < 16; ++i)
+                    x[i / 8][i % 8] = static_cast<float>(static_cast<int8_t>(wd[i / 4] >> (8 * (i & 3)))) * s;
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        x[i / 8][i % 8] = static_cast<float>(static_cast<int8_t>(wd[i / 4] >> (8 * (i & 3)))) * s;
-                } else {
-                    const __half* src = static_cast<const __half*>(is_k ? a.k_cache : a.v_cache) + at;
-                    load8(src, x[0]);
-                    load8(src + 8, x[1]);
+                for (int i = 0; i < 2; ++i) {
+                    Raw8<__half> r;
+                    r.r = raw[u][i];
+                    r.get(x[i]);
                 }
             }
-            TO* dst = static_cast<TO*>(is_k ? a.k_out : a.v_out) + static_cast<size_t>(t) * a.Hkv * a.D +
-                      static_cast<size_t>(cc) * 16;
-            store8(dst, x[0]);
-            store8(dst + 8, x[1]);
+            store8(out, x[0]);
+            store8(out + 8, x[1]);
         }
     }
 }
@@ -326,17 +383,20 @@ __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadAr
 
 attn_status launch_append(const AppendLaunch& L) {
     const AppendArgs& a = L.args;
-    // one pass over the token's heads where 256 threads hold them
+    // One CTA a token.  A call with fewer tokens than two an SM spreads each token's heads over
+    // CTAs of one pass.
     const int lanes = (a.Hq + 2 * a.Hkv) * (L.D / 8);
     const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
+    const int parts = a.total_q >= 2 * sm_count() ? 1 : (lanes + threads - 1) / threads;
+    const dim3 grid(a.total_q, parts);
     if (trace_enabled())
-        trace("append_kernel<D=%d,in=%s,q_out=%s,int8=%d> grid=%d block=%d B=%d Hq=%d Hkv=%d rot=%d", L.D,
-              L.in_f32 ? "f32" : "f16", L.q_out_f32 ? "f32" : "f16", (int)L.int8, a.total_q, threads, a.B, a.Hq,
+        trace("append_kernel<D=%d,in=%s,q_out=%s,int8=%d> grid=(%d,%d) block=%d B=%d Hq=%d Hkv=%d rot=%d", L.D,
+              L.in_f32 ? "f32" : "f16", L.q_out_f32 ? "f32" : "f16", (int)L.int8, a.total_q, parts, threads, a.B, a.Hq,
               a.Hkv, a.rot);
     switch (L.D) {
-        case 64: append_types<64>(L, threads); break;
-        case 128: append_types<128>(L, threads); break;
-        default: append_types<256>(L, threads); break;
+        case 64: append_types<64>(L, grid, threads); break;
+        case 128: append_types<128>(L, grid, threads); break;
+        default: append_types<256>(L, grid, threads); break;
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "append launch failed: %s", cudaGetErrorString(e));
@@ -345,8 +405,7 @@ attn_status launch_append(const AppendLaunch& L) {
 
 attn_status launch_kv_read(const KvReadLaunch& L) {
     const KvReadArgs& a = L.args;
-    const int rows = kReadRows * kReadWarps;
-    const int grid = static_cast<int>((static_cast<long long>(a.total) + rows - 1) / rows);
+    const int grid = (a.total - 1) / kReadWarps + 1;
     if (trace_enabled())
         trace("kv_read_kernel<out=%s,int8=%d> grid=%d block=%d B=%d Hkv=%d D=%d", L.out_f32 ? "f32" : "f16",
               (int)L.int8, grid, kReadWarps * 32, a.B, a.Hkv, a.D);

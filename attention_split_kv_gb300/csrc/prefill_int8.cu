@@ -311,6 +311,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         atomicExch(err, code);
         return false;
     };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be set up meanwhile
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     // ---- this CTA's run: sum the key tiles of every (sequence, row group), then find
@@ -1231,6 +1232,7 @@ constexpr int kJoinWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Args8 a, int n_ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the whole of prefill8_kernel
     const int* meta = a.meta + blockIdx.x * 8;
     if (!meta[2]) return;
     const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -1384,8 +1386,17 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     kernel<<<grid, kThreads, C::SMEM_ALLOC, L.stream>>>(tq, tk, tv, a);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) {
-        prefill8_join_kernel<D><<<join, kJoinWarps * 32, 0, L.stream>>>(a, grid);
-        e = cudaGetLastError();
+        // set up while prefill8_kernel runs: the join waits for its end itself
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = join;
+        cfg.blockDim = dim3(kJoinWarps * 32);
+        cfg.stream = L.stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, prefill8_join_kernel<D>, a, grid);
     }
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "prefill (int8) launch failed: %s", cudaGetErrorString(e));
     return ATTN_OK;
