@@ -65,44 +65,39 @@ __device__ __forceinline__ Where find_row(const int32_t* __restrict__ start, con
     return w;
 }
 
-// 8 elements as they lie in memory, and as f32.
+// 4 elements as they lie in memory, and as f32.
 template <typename T>
-struct Raw8;
+struct Raw4;
 template <>
-struct Raw8<__half> {
-    uint4 r;
-    __device__ __forceinline__ void load(const __half* p) { r = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+struct Raw4<__half> {
+    uint2 r;
+    __device__ __forceinline__ void load(const __half* p) { r = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void get(float* x) const {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
     }
 };
 template <>
-struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    }
+struct Raw4<float> {
+    float4 r;
+    __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void get(float* x) const { x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w; }
 };
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    Raw8<T> r;
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    Raw4<float> r;
     r.load(p);
     r.get(x);
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store4(__half* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 __device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
@@ -140,33 +135,78 @@ __device__ __forceinline__ bool find_slot(const CacheLayout& c, int b, long long
 }
 
 // ------------------------------------------------------------------ append
+// max(a, |b|, |c|), NaN if any is
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return d;
+}
+
+// Four codes of r = x / scale: rint(x * inv) sits in the low bits of x * inv + 1.5 * 2^23.
+// x * inv is within 2^-24 * 127.1 < 1e-5 of x / scale, so it rounds alike unless it is that
+// near to a tie; `tie` collects the distances from the integers.
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv, float& tie) {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float r = fmaf(x[i], inv, kMagic);
+        tie = fmaxf(tie, fabsf(fmaf(x[i], inv, kMagic - r)));
+        b[i] = __float_as_uint(r);
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+// The same by division, clamped (near a tie, or under a scale too small to be accurate).
+__device__ __forceinline__ uint32_t codes4_exact(const float* x, float scale) {
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float r = fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.f), 127.f);
+        c |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * i);
+    }
+    return c;
+}
+
 // A CTA takes a token (blockIdx.x), or of few tokens a part of its heads (blockIdx.y of
-// gridDim.y); a group of D/8 lanes a head at a time, 8 elements a lane (16-byte accesses).
-// The norm, the largest magnitude and the half-split partner are shuffles inside the group.
-// A lane's first two loads are issued before the search for the token's sequence, each
-// later one before the head two back is worked on, so that the chain of dependent loads
-// (sequence, page, table row) lies under them.
+// gridDim.y); a group of D/8 lanes a head at a time, a warp heads of one kind (q, k or v).
+// A lane has two quads of 4 elements: those that half-split rotation pairs, or neighbours,
+// so that a rotation stays inside a lane; the norm and the largest magnitude are shuffles
+// inside the group.  A lane's first loads are issued before the search for the token's
+// sequence, each later one before the head two back is worked on, so that the chain of
+// dependent loads (sequence, page, table row) lies under them.
 template <int D, typename T, typename TQ, bool INT8>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     constexpr int LPR = D / 8;          // lanes a head
     constexpr int RPW = 32 / LPR;       // heads a warp
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
-    const int sub = lane & (LPR - 1);   // lane within its head
-    const int e0 = sub * 8;             // its first element
-    const int n_heads = a.Hq + 2 * a.Hkv;
-    const int step = static_cast<int>(gridDim.y * (blockDim.x >> 5)) * RPW;
-    int h0 = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * RPW;
-    auto fetch = [&](int h, Raw8<T>& r) {
-        if (h >= n_heads) return;
-        const T* p = h < a.Hq            ? static_cast<const T*>(a.q) + t * a.q_stride + h * D
-                     : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_stride + (h - a.Hq) * D
-                                        : static_cast<const T*>(a.v) + t * a.v_stride + (h - a.Hq - a.Hkv) * D;
-        r.load(p + e0);
+    const int lane = threadIdx.x & 31, t = blockIdx.x;
+    const int sub = lane & (LPR - 1), hsub = lane / LPR;
+    const int half = a.rot / 2;
+    const bool rotates = sub * 8 < a.rot;
+    // elements of the two quads: (e, e + R/2) for the first R/8 lanes of a half-split
+    // rotation, else 8 in a row
+    const bool split = !a.interleaved && rotates;
+    const int ea = split ? sub * 4 : sub * 8, eb = split ? half + sub * 4 : sub * 8 + 4;
+
+    const int nq = (a.Hq + RPW - 1) / RPW, nk = (a.Hkv + RPW - 1) / RPW, n_slots = nq + 2 * nk;
+    const int step = gridDim.y * (blockDim.x >> 5);
+    int slot_i = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const T* const qt = static_cast<const T*>(a.q) + t * a.q_stride;
+    const T* const kt = static_cast<const T*>(a.k) + t * a.k_stride;
+    const T* const vt = static_cast<const T*>(a.v) + t * a.v_stride;
+    struct Pair {
+        Raw4<T> a, b;
     };
-    Raw8<T> raw[2];
-    fetch(h0 + lane / LPR, raw[0]);
-    fetch(h0 + step + lane / LPR, raw[1]);
+    auto fetch = [&](int s, Pair& r) {
+        const int kind = s < nq ? 0 : s < nq + nk ? 1 : 2;
+        const int h = (s - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + hsub;
+        if (s >= n_slots || h >= (kind == 0 ? a.Hq : a.Hkv)) return;
+        const T* p = (kind == 0 ? qt : kind == 1 ? kt : vt) + h * D;
+        r.a.load(p + ea);
+        r.b.load(p + eb);
+    };
+    Pair raw[2];
+    fetch(slot_i, raw[0]);
+    fetch(slot_i + step, raw[1]);
 
     const Where w = find_row(a.q_start, a.kv_len, a.B, t, lane);
     if (w.b < 0) return;
@@ -176,117 +216,109 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         if (threadIdx.x == 0) atomicExch(a.err, kErrAppendRange);
         return;
     }
+    float cs[4], sn[4];
+    if (rotates) {
+        const size_t at = static_cast<size_t>(p) * half + sub * 4;
+        load4(a.cos + at, cs);
+        load4(a.sin + at, sn);
+    }
     // a ring holds a sequence's newest tokens; what a longer chunk overwrites is not
     // written at all, so no two tokens of a call share a slot
     bool write = a.cache.ring == 0 || p >= static_cast<long long>(w.len) - a.cache.ring;
     Slot slot{0, 0};
     if (write) write = find_slot(a.cache, w.b, p, slot, a.err);
+    const size_t row = (slot.slot * a.cache.rows + slot.row) * a.Hkv;        // in heads
+    const size_t srow = slot.slot * a.Hkv * a.cache.rows + slot.row;         // of scales, head 0
 
-    float cs[8], sn[8];
-    const int half = a.rot / 2;
-    const bool rotates = e0 < a.rot;
-    if (rotates) {
-        const float* ct = a.cos + static_cast<size_t>(p) * half;
-        const float* st = a.sin + static_cast<size_t>(p) * half;
-        if (a.interleaved) {
-            const float4 c4 = *reinterpret_cast<const float4*>(ct + e0 / 2);
-            const float4 s4 = *reinterpret_cast<const float4*>(st + e0 / 2);
-            cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
-            sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
-        } else {
-            const int e = e0 < half ? e0 : e0 - half;
-            load8(ct + e, cs);
-            load8(st + e, sn);
-        }
-    }
-
-    for (; h0 < n_heads; h0 += step) {   // uniform in the warp
-        const int h = h0 + lane / LPR;
-        const bool live = h < n_heads;
-        const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;    // q, k, v
-        const int hh = kind == 0 ? h : kind == 1 ? h - a.Hq : h - a.Hq - a.Hkv;
+    int g_kind = 2;
+    float g[8];                          // the norm's weights, where g_kind has any
+    for (; slot_i < n_slots; slot_i += step) {   // uniform in the warp, kind too
+        const int kind = slot_i < nq ? 0 : slot_i < nq + nk ? 1 : 2;
+        const int h = (slot_i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + hsub;
+        const bool live = h < (kind == 0 ? a.Hq : a.Hkv);
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (live) raw[0].get(x);
+        if (live) {
+            raw[0].a.get(x);
+            raw[0].b.get(x + 4);
+        }
         raw[0] = raw[1];
-        fetch(h + 2 * step, raw[1]);
+        fetch(slot_i + 2 * step, raw[1]);
         const float* nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-        if (a.q_norm || a.k_norm) {
+        if (nw) {
+            if (g_kind != kind) {
+                load4(nw + ea, g);
+                load4(nw + eb, g + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] += a.offset;
+                g_kind = kind;
+            }
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-            if (nw) {
-                const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-                float g[8];
-                load8(nw + e0, g);
+            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (g[i] + a.offset);
-            }
+            for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
         }
-        if (a.rot) {
-            if (a.interleaved) {
-                if (rotates && kind < 2) {
+        if (kind < 2 && rotates) {
+            if (split) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = x[2 * i], v = x[2 * i + 1];
-                        x[2 * i] = u * cs[i] - v * sn[i];
-                        x[2 * i + 1] = v * cs[i] + u * sn[i];
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float u = x[i], v = x[4 + i];
+                    x[i] = u * cs[i] - v * sn[i];
+                    x[4 + i] = v * cs[i] + u * sn[i];
                 }
             } else {
-                // the partner's 8 elements sit half / 8 lanes on (or back)
-                const bool low = e0 < half;
-                const int from = rotates ? lane + (low ? half / 8 : -(half / 8)) : lane;
-                float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(kFull, x[i], from);
-                if (rotates && kind < 2) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = low ? x[i] * cs[i] - y[i] * sn[i] : x[i] * cs[i] + y[i] * sn[i];
+                for (int i = 0; i < 4; ++i) {
+                    const float u = x[2 * i], v = x[2 * i + 1];
+                    x[2 * i] = u * cs[i] - v * sn[i];
+                    x[2 * i + 1] = v * cs[i] + u * sn[i];
                 }
             }
         }
-        float scale = 0.f;
-        if constexpr (INT8) {
-            // largest magnitude by its bits, which order NaN above infinity: a row with
-            // either gets it as its scale
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-            scale = __half2float(__float2half_rn(__fdiv_rn(__uint_as_float(m), 127.0f)));
-        }
-        if (!live) continue;
         if (kind == 0) {
-            store8(static_cast<TQ*>(a.q_out) + (static_cast<size_t>(t) * a.Hq + hh) * D + e0, x);
+            if (live) {
+                TQ* out = static_cast<TQ*>(a.q_out) + (static_cast<size_t>(t) * a.Hq + h) * D;
+                store4(out + ea, x);
+                store4(out + eb, x + 4);
+            }
             continue;
         }
-        if (!write) continue;
-        const size_t row = slot.slot * a.cache.rows + slot.row;
-        const size_t at = (row * a.Hkv + hh) * D + e0;
         if constexpr (INT8) {
-            uint32_t c[2] = {0, 0};
-            if (scale > 0.f && scale < INFINITY) {
-                // x times 1 / scale is within 2^-23 * 127.1 < 2e-5 of x / scale, so it rounds
-                // alike unless it lies that near to a tie: then the division decides
-                const float inv = __fdiv_rn(1.0f, scale);
+            // a head with an infinity or a NaN gets it as its scale
+            float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float q = x[i] * inv, r = rintf(q);
-                    if (fabsf(q - r) > 0.4999f) r = rintf(__fdiv_rn(x[i], scale));
-                    r = fminf(fmaxf(r, -127.f), 127.f);
-                    c[i / 4] |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * (i & 3));
+            for (int i = 0; i < 8; i += 2) m = max3_abs_nan(m, x[i], x[i + 1]);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = max3_abs_nan(m, __shfl_xor_sync(kFull, m, o), 0.f);
+            const __half hs = __float2half_rn(__fdiv_rn(m, 127.0f));
+            const float scale = __half2float(hs);
+            uint32_t c0 = 0, c1 = 0;
+            if (scale > 0.f && scale < INFINITY) {
+                // an f16 scale with all its bits puts every code within 127.1
+                float tie = 0.f;
+                const float inv = __fdiv_rn(1.0f, scale);
+                c0 = codes4(x, inv, tie);
+                c1 = codes4(x + 4, inv, tie);
+                if (tie > 0.4999f || scale < 0x1p-14f) {
+                    c0 = codes4_exact(x, scale);
+                    c1 = codes4_exact(x + 4, scale);
                 }
             }
-            *reinterpret_cast<uint2*>(static_cast<int8_t*>(kind == 1 ? a.k_cache : a.v_cache) + at) =
-                make_uint2(c[0], c[1]);
-            if (sub == 0)
-                static_cast<__half*>(kind == 1 ? a.k_scales : a.v_scales)[(slot.slot * a.Hkv + hh) * a.cache.rows +
-                                                                           slot.row] = __float2half_rn(scale);
-        } else {
-            store8(static_cast<__half*>(kind == 1 ? a.k_cache : a.v_cache) + at, x);
+            if (live && write) {
+                int8_t* out = static_cast<int8_t*>(kind == 1 ? a.k_cache : a.v_cache) + (row + h) * D;
+                *reinterpret_cast<uint32_t*>(out + ea) = c0;
+                *reinterpret_cast<uint32_t*>(out + eb) = c1;
+                if (sub == 0)
+                    static_cast<__half*>(kind == 1 ? a.k_scales : a.v_scales)[srow + static_cast<size_t>(h) * a.cache.rows] =
+                        hs;
+            }
+        } else if (live && write) {
+            __half* out = static_cast<__half*>(kind == 1 ? a.k_cache : a.v_cache) + (row + h) * D;
+            store4(out + ea, x);
+            store4(out + eb, x + 4);
         }
     }
 }
@@ -367,10 +399,11 @@ __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadAr
                     x[i / 8][i % 8] = static_cast<float>(static_cast<int8_t>(wd[i / 4] >> (8 * (i & 3)))) * s;
             } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    Raw8<__half> r;
-                    r.r = raw[u][i];
-                    r.get(x[i]);
+                for (int i = 0; i < 4; ++i) {
+                    Raw4<__half> r;
+                    r.r = (i & 1) ? make_uint2(raw[u][i / 2].z, raw[u][i / 2].w)
+                                  : make_uint2(raw[u][i / 2].x, raw[u][i / 2].y);
+                    r.get(&x[i / 2][4 * (i & 1)]);
                 }
             }
             store8(out, x[0]);
@@ -385,9 +418,10 @@ attn_status launch_append(const AppendLaunch& L) {
     const AppendArgs& a = L.args;
     // One CTA a token.  A call with fewer tokens than two an SM spreads each token's heads over
     // CTAs of one pass.
-    const int lanes = (a.Hq + 2 * a.Hkv) * (L.D / 8);
-    const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-    const int parts = a.total_q >= 2 * sm_count() ? 1 : (lanes + threads - 1) / threads;
+    const int rpw = 256 / L.D;
+    const int slots = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);   // warps' worth of heads
+    const int warps = slots < 8 ? slots : 8, threads = warps * 32;
+    const int parts = a.total_q >= 2 * sm_count() ? 1 : (slots + warps - 1) / warps;
     const dim3 grid(a.total_q, parts);
     if (trace_enabled())
         trace("append_kernel<D=%d,in=%s,q_out=%s,int8=%d> grid=(%d,%d) block=%d B=%d Hq=%d Hkv=%d rot=%d", L.D,
