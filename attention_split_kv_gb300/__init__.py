@@ -402,6 +402,11 @@ def _cache_args(case):
     return 0, 0, 0, 0 if ring else int(case.k.shape[1]), ring
 
 
+def _dense(what, x, dtype):
+    if x is not None and (x.dtype != dtype or not x.is_contiguous()):
+        raise AttnError(ATTN_EINVAL, "%s must be a contiguous %s tensor" % (what, dtype))
+
+
 def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_eps=1e-6, norm_offset=0.0,
            rope_cos=None, rope_sin=None, rope_interleaved=False, q_out=None, stream=None):
     """attn_append of packed token rows (q [T, Hq, D] or None; k, v [T, Hkv, D], f16
@@ -417,6 +422,10 @@ def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_e
             raise AttnError(ATTN_EINVAL, "q, k and v rows must have one type and their heads side by side")
         return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
 
+    for what, x in (("q_norm", q_norm), ("k_norm", k_norm), ("rope_cos", rope_cos), ("rope_sin", rope_sin)):
+        _dense(what, x, torch.float32)
+    for what, x in (("q_start", q_start), ("kv_len", kv_len)):
+        _dense(what, x, torch.int32)
     int8 = case.k.dtype == torch.int8
     P, max_pages, n_pages, max_kv, ring = _cache_args(case)
     if q is not None and q_out is None:
@@ -436,6 +445,8 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
     """attn_kv_read of a DecodeCase- or ChunkCase-like object's cache: (k, v) rows
     [total, Hkv, D], f16 or f32; rows past out_start[B] are not written."""
     import torch
+    for what, x in (("out_start", out_start), ("first", first), ("kv_len", kv_len)):
+        _dense(what, x, torch.int32)
     int8 = case.k.dtype == torch.int8
     P, max_pages, n_pages, max_kv, ring = _cache_args(case)
     shape = (total, case.n_kv_heads, case.head_dim)

@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     const Where w = find_row(a.q_start, a.kv_len, a.B, t, lane);
     if (w.b < 0) return;
     const long long p = static_cast<long long>(w.len) - w.end + t;   // kv_len - q_len + i
-    const bool in_range = p >= 0 && p < a.cache.capacity && (a.rot == 0 || p < a.n_pos);
-    if (!in_range) {
+    if (p < 0) return;                   // no token: a padded batch's row
+    if (p >= a.cache.capacity || (a.rot > 0 && p >= a.n_pos)) {
         if (threadIdx.x == 0) atomicExch(a.err, kErrAppendRange);
         return;
     }
@@ -416,12 +416,16 @@ __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadAr
 
 attn_status launch_append(const AppendLaunch& L) {
     const AppendArgs& a = L.args;
-    // One CTA a token.  A call with fewer tokens than two an SM spreads each token's heads over
-    // CTAs of one pass.
+    // One CTA a token, of warps with 8 turns each: what a warp does once (the search, the
+    // addresses) costs it as much as a turn and a half.  Ragged chunks of 48 heads: 25 us with 8
+    // warps, 22 with 3; 4096 tokens of 16 wide f32 heads: 27 with 8, 20 with 2.  A call with
+    // fewer tokens than two an SM has latency to lose instead: CTAs of at most 8 warps, a turn
+    // each.
     const int rpw = 256 / L.D;
-    const int slots = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);   // warps' worth of heads
-    const int warps = slots < 8 ? slots : 8, threads = warps * 32;
-    const int parts = a.total_q >= 2 * sm_count() ? 1 : (slots + warps - 1) / warps;
+    const int turns = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);   // warps' worth of heads
+    const bool many = a.total_q >= 2 * sm_count();
+    const int most = many ? (turns + 7) / 8 : turns, warps = most < 8 ? most : 8, threads = warps * 32;
+    const int parts = many ? 1 : (turns + warps - 1) / warps;
     const dim3 grid(a.total_q, parts);
     if (trace_enabled())
         trace("append_kernel<D=%d,in=%s,q_out=%s,int8=%d> grid=(%d,%d) block=%d B=%d Hq=%d Hkv=%d rot=%d", L.D,

@@ -132,7 +132,8 @@ struct Cfg {
         N_BARS
     };
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag, start
-    static constexpr uint32_t OFF_SEG = OFF_MISC + 16;
+    static constexpr uint32_t OFF_FILLS = OFF_MISC + 8;
+    static constexpr uint32_t OFF_SEG = (OFF_FILLS + NST * 4 + 7) / 8 * 8;
     static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (SEGS + 1) * 72 + 1024;   // 72: sizeof(Seg)
     // TMEM: S of two units, P (D = 64/128: over the S it was made from), then O
     static constexpr bool OVER = D <= 128;
@@ -289,6 +290,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const uint32_t sbase = smem_u32(smem);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+    volatile uint32_t* fills = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_FILLS);   // of each stage
     Seg* segs = reinterpret_cast<Seg*>(smem + C::OFF_SEG);
     Seg& walk = segs[C::SEGS];     // the walk's own state
     KeyFactors<BN>* tab = reinterpret_cast<KeyFactors<BN>*>(smem + C::OFF_TAB);
@@ -386,6 +388,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             mbar_init(bar(C::B_ML), C::NSM);
             mbar_init(bar(C::B_TEARDOWN), 1);
             *abort_flag = 0;
+            for (int i = 0; i < NST; ++i) fills[i] = 0;
             fence_barrier_init();
         }
         if (warp == C::MMA_WARP) {
@@ -483,7 +486,6 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // the one it waited for last vouches for every earlier phase of any stage.)
             static_assert(NST >= 3, "stage waits");
             uint32_t base = 0;                     // items before this segment
-            uint32_t sent = 0, parity = 0;         // stages this warp filled, and their phases (one bit each)
             int ok = 1;
             const Seg* w;
             for (uint32_t seg = 0; ok && __any_sync(gmask, enter(seg, w)); ++seg) {
@@ -523,23 +525,25 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             atomicExch(a.err, kErrBadPage);
                         }
                     }
-                    if (leader) mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st), C::CODE_BYTES);
+                    if (leader) {
+                        fills[st] = gi / NST + 1;
+                        mbar_arrive_expect_tx(bar(C::B_SFULL_ST + st), C::CODE_BYTES);
+                    }
                     __syncwarp(gmask);
                     if (has_box)
 #pragma unroll
                         for (int c = 0; c < D; c += 128)   // 128-byte columns
                             tma_load_4d(sbase + C::OFF_CODE + st * C::CODE_BYTES + c * BN + lane * R * min(D, 128), tm,
                                         bar(C::B_SFULL_ST + st), c, g, row, page);
-                    sent |= 1u << st;
-                    parity = (parity & ~(1u << st)) | (((gi / NST) & 1) << st);
                 }
                 cp_async_wait<0>();
                 base += 2 * n;
             }
+            cp_async_wait<0>();
             if (leader && *abort_flag)   // copies in flight land before the CTA's shared memory goes away
-                for (int st = 0; st < NST; ++st)
-                    if (sent >> st & 1)
-                        mbar_wait_drain(bar(C::B_SFULL_ST + st), parity >> st & 1, a.err, kErrTimeoutLoad);
+                for (int i = 0; i < NST; ++i)
+                    if (const uint32_t f = fills[i])
+                        mbar_wait_drain(bar(C::B_SFULL_ST + i), (f - 1) & 1, a.err, kErrTimeoutLoad);
         }
     } else if (warp == C::MMA_WARP) {
         // ------------------------------------------------------------ MMA issuer
@@ -743,6 +747,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             jt += n;
             warp_arrive(bar(C::B_SEGFREE + seg % C::SEGS), lane);
         }
+        cp_async_wait<0>();
         if (lane == 0 && *abort_flag && seg > 0) mbar_wait_drain(bar(C::B_QFULL), (seg - 1) & 1, a.err, kErrTimeoutLoad);
     }
     } else if (warp >= C::NSM) {

@@ -419,12 +419,12 @@ attn_status attn_prefill_paged_ex(const void* q, const void* k_cache, const void
  *                NaN gets it as its scale and reads back as NaN.
  *  q_out       device, q_out_dtype, [total_q, Hq, D].  It may be q itself where type
  *                and stride agree.
- *  All arithmetic is f32, with one rounding at the end.  A token whose position is
- *  negative, at or above the cache's capacity or the tables' rows is left out
- *  (neither q_out nor the cache is written), and a token whose page id lies
- *  outside the pool is not written to the cache; both are reported through
- *  attn_device_status (ATTN_EBOUNDS).  Sequences must not share the pages that the
- *  call writes.
+ *  All arithmetic is f32, with one rounding at the end.  A row whose position is
+ *  negative is no token (a padded batch's sequence of kv_len 0) and is left out:
+ *  neither q_out nor the cache is written.  So is a token at or above the cache's
+ *  capacity or the tables' rows, and a token whose page id lies outside the pool is
+ *  not written to the cache; these two are reported through attn_device_status
+ *  (ATTN_EBOUNDS).  Sequences must not share the pages that the call writes.
  */
 attn_status attn_append(const void* q, const void* k, const void* v, attn_dtype in_dtype,
                         long long q_stride, long long k_stride, long long v_stride,

@@ -201,6 +201,44 @@ def test_append_leaves_out_positions_outside():
     assert torch.equal(g.v.cpu(), want)
 
 
+def test_padded_batches_are_no_error():
+    # decode steps of 5 slots, two of them without a sequence (kv_len 0), and a padded chunk
+    D, kv = 64, [3, 0, 16, 0, 1]
+    cache = Cache("paged", 5, 1, D, 16, int8=True, page_size=8, seed=7)
+    cache.page_table[1], cache.page_table[3] = -1, -1
+    g = cache.to("cuda")
+    x = si.f16_normal((5, 1, D), 9).cuda()
+    cos, sin = (t.cuda() for t in tables(16, D))
+    n = torch.tensor(kv, dtype=torch.int32).cuda()
+    start = torch.arange(6, dtype=torch.int32).cuda()
+    q = torch.full((5, 1, D), 55.0, dtype=torch.float16, device="cuda")
+    attn.append(g, x, x, x, start, n, rope_cos=cos, rope_sin=sin, q_out=q)
+    k, _ = attn.kv_read(g, start, 5, first=n - 1, kv_len=n)
+    assert attn.attn_device_status() == attn.ATTN_OK
+    assert bool((q[[1, 3]] == 55).all()) and bool((k[[1, 3]] == 0).all())
+    assert bool((q[[0, 2, 4]] != 55).any()) and bool((k[[0, 2, 4]] != 0).any(2).all())
+    start = torch.tensor([0, 4, 5, 5, 5, 5], dtype=torch.int32).cuda()    # 4 rows for the 3 tokens of sequence 0
+    attn.append(g, x, x, x, start, n, rope_cos=cos, rope_sin=sin, q_out=q)
+    assert attn.attn_device_status() == attn.ATTN_OK
+
+
+def test_the_binding_refuses_other_types_and_strides():
+    g = Cache("plain", 1, 1, 64, 8).to("cuda")
+    x = si.f16_normal((2, 1, 64), 9).cuda()
+    start, n = torch.tensor([0, 2], dtype=torch.int32).cuda(), torch.tensor([2], dtype=torch.int32).cuda()
+    cos, sin = (t.cuda() for t in tables(8, 64))
+    for kw in (dict(q_norm=torch.ones(64, device="cuda").half()), dict(kv_len=n.long()),
+               dict(rope_cos=cos.half(), rope_sin=sin), dict(rope_cos=cos.t().contiguous().t(), rope_sin=sin)):
+        with pytest.raises(attn.AttnError):
+            attn.append(g, x, x, x, start, **{**dict(kv_len=n), **kw})
+    with pytest.raises(attn.AttnError):
+        attn.append(g, x.float(), x, x, start, n)
+    with pytest.raises(attn.AttnError):
+        attn.append(g, x, x.transpose(0, 2), x, start, n)
+    with pytest.raises(attn.AttnError):
+        attn.kv_read(g, start.long(), 2, kv_len=n)
+
+
 @pytest.mark.parametrize("bad", [-1, 10_000_000])
 def test_append_and_read_of_page_ids_outside_the_pool(bad):
     cache = Cache("paged", 1, 2, 64, 32, int8=True, page_size=8, seed=5)

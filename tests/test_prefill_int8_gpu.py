@@ -2,6 +2,9 @@
 form on code * scale: one token to several tiles, ragged and empty chunks, splits
 over long caches, head groups of every size, masks that leave rows or tiles empty."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -250,3 +253,53 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert torch.equal(o.float().cpu(), alone[i % 2])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [3, 300])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(D, n):
+    # the testing hook holds back the first S tile's signal for 20 ms waits: every role leaves
+    # its loop, copies and MMAs in flight land, and the tensor memory is free again
+    case = si.make_chunked_case(2, 8, 2, D, [n, 5], [700, 2000], seed=n + D, page_size=16, int8=True)
+    g = case.to("cuda")
+    assert attn.attn_testing_set_waits(20_000_000, 1) == attn.ATTN_OK
+    try:
+        attn.prefill_paged(g)
+        status = attn.attn_device_status()
+    finally:
+        assert attn.attn_testing_set_waits(0, 0) == attn.ATTN_OK
+    assert status == attn.ATTN_ETIMEOUT
+    assert attn.attn_device_status() == attn.ATTN_OK
+    _check(case, "after a timeout, D=%d n=%d" % (D, n))
+
+
+TRACED = """
+import torch
+import attention_split_kv_gb300 as attn
+import seeded_inputs as si
+import sys
+sys.path.insert(0, "tests")
+from cache_util import Cache
+attn.load()
+attn.prefill_paged(si.make_chunked_case(2, 8, 2, 128, [3, 2], [70, 20], seed=1, page_size=16, int8=True).to("cuda"))
+attn.prefill_paged(si.make_chunked_case(2, 8, 2, 128, [300, 2], [70, 20], seed=1, page_size=16, int8=True).to("cuda"))
+g = Cache("paged", 1, 2, 64, 32, int8=True).to("cuda")
+x = si.f16_normal((20, 2, 64), 3).cuda()
+start, n = torch.tensor([0, 20], dtype=torch.int32).cuda(), torch.tensor([20], dtype=torch.int32).cuda()
+attn.append(g, x, x, x, start, n)
+attn.kv_read(g, start, 20, kv_len=n)
+torch.cuda.synchronize()
+"""
+
+
+def test_launches_are_traced():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", TRACED], cwd=root, env=dict(os.environ, ATTN_TRACE="1"),
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [ln for ln in r.stderr.splitlines() if ln.startswith("[libattn]")]
+    assert len(lines) == 4, r.stderr
+    assert "prefill8_kernel<D=128,row_tiles=1,cap=0>" in lines[0]      # 3 queries: a row tile holds 32
+    assert "prefill8_kernel<D=128,row_tiles=2,cap=0>" in lines[1]
+    assert "append_kernel<D=64,in=f16,q_out=f16,int8=1>" in lines[2]
+    assert "kv_read_kernel<out=f16,int8=1>" in lines[3]
