@@ -25,13 +25,26 @@
 // workspace, which a second kernel joins.  Long caches with few rows and short ones
 // with many are balanced by the same cut, without the host knowing any length.
 //
-// Roles (20 warps): a TMA warp brings code tiles and scales into a ring of stages; 8
-// converter warps turn codes into f16 operands (128-byte swizzle) in a ring of 3, and
-// one writes the per-key factors; one thread issues the MMAs; 8 softmax warps.
-// D = 64/128 keep two streams, each with its S (P overwrites it) and O in TMEM and 4
-// softmax warps, which take turns on the tensor cores: the two row tiles of a group,
-// or for a single tile the even and the odd key tiles, joined at the end.  D = 256 has
-// one O (its 256 columns) and two S buffers, each read by all 8 softmax warps.
+// Roles (20 warps): a K and a V warp bring code tiles into a ring of stages (TMA, a box a
+// page); 8 converter warps turn codes into f16 operands (128-byte swizzle) in a ring of 3;
+// one warp issues the MMAs; one walks the run, loads Q and writes the per-key factors; 8
+// softmax warps.  D = 64/128 keep two streams, each with its S (P overwrites it) and O in
+// TMEM and 4 softmax warps, which take turns on the tensor cores: the two row tiles of a
+// group, or for a single tile the even and the odd key tiles, joined at the end.  D = 256
+// has one O (its 256 columns) and tiles of 64 keys, with two S and P buffers beside it; all
+// 8 softmax warps, 16 rows each, take every tile.
+//
+// What bounds it: shared memory.  Codes are written by TMA, read, stored at twice the size
+// and read by the MMA, so a 128-key tile of one row tile (D = 128) takes 2170 wavefronts of
+// 128 bytes (LSU 1150, MMA operands 768, TMA 256) in 2650 to 2790 cycles: 524288 cached
+// tokens of 8 kv heads and 4 new ones of 32 heads take 305 us, 3.6 TB/s (HBM alone: 161 us).
+// With two row tiles one conversion serves both and the softmax's chain (S, 3500 cycles of
+// softmax, PV, the next S) comes to the front: 8 chunks of 512 tokens on 512 to 7680 cached
+// ones (32/8 heads) take 305 us, 778 TFLOP/s, tensor pipe 34%, issue slots 49%, shared memory
+// 65%.  16 softmax warps of 16 rows do not shorten it (307 us): a 16-byte factor load of 4
+// distinct addresses takes 4 wavefronts, and with half the rows a load serves half as much.
+// D = 256 with a softcap and a window of 1024 keys: 78 us, 387 TFLOP/s, a third of it each
+// segment's fixed part (filling the pipeline, writing its rows).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1250,10 +1263,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Ar
     // the parts: the end of CTA c's run, whole runs of the same head, the beginning of the last
     float mx = a.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + 1) * a.slot_rows + row].x;
     int last = blockIdx.x;
-    do {
+    while (last + a.hp < n_ctas) {
         last += a.hp;
         mx = fmaxf(mx, a.part_ml[static_cast<size_t>(last) * 2 * a.slot_rows + row].x);
-    } while (!a.meta[last * 8 + 1] && last + a.hp < n_ctas);
+        if (a.meta[last * 8 + 1]) break;
+    }
     float o[D / 32], sum = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
