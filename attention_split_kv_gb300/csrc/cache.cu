@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_internal.h"
+#include "ptx.cuh"
 
 namespace attn {
 namespace {
@@ -72,40 +73,41 @@ template <>
 struct Raw4<__half> {
     uint2 r;
     __device__ __forceinline__ void load(const __half* p) { r = *reinterpret_cast<const uint2*>(p); }
-    __device__ __forceinline__ void get(float* x) const {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    __device__ __forceinline__ void get(float2* x) const {
+        x[0] = __half22float2(*reinterpret_cast<const __half2*>(&r.x));
+        x[1] = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
     }
 };
 template <>
 struct Raw4<float> {
     float4 r;
     __device__ __forceinline__ void load(const float* p) { r = *reinterpret_cast<const float4*>(p); }
-    __device__ __forceinline__ void get(float* x) const { x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w; }
+    __device__ __forceinline__ void get(float2* x) const {
+        x[0] = make_float2(r.x, r.y);
+        x[1] = make_float2(r.z, r.w);
+    }
 };
-__device__ __forceinline__ void load4(const float* p, float* x) {
+__device__ __forceinline__ void load4(const float* p, float2* x) {
     Raw4<float> r;
     r.load(p);
     r.get(x);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 a) {
+    const __half2 h = __floats2half2_rn(a.x, a.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store4(__half* p, const float* x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+__device__ __forceinline__ void store4(__half* p, const float2* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0]), pack2(x[1]));
 }
-__device__ __forceinline__ void store4(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ void store4(float* p, const float2* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
 }
-__device__ __forceinline__ void store8(__half* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]),
-                                              pack2(x[6], x[7]));
+__device__ __forceinline__ void store8(__half* p, const float2 (&x)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(float* p, const float2 (&x)[4]) {
+    store4(p, x);
+    store4(p + 4, x + 2);
 }
 
 // Where the cache keeps position p; false if its page id is outside the pool.
@@ -142,26 +144,30 @@ __device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // Four codes of r = x / scale: rint(x * inv) sits in the low bits of x * inv + 1.5 * 2^23.
 // x * inv is within 2^-24 * 127.1 < 1e-5 of x / scale, so it rounds alike unless it is that
 // near to a tie; `tie` collects the distances from the integers.
-__device__ __forceinline__ uint32_t codes4(const float* x, float inv, float& tie) {
+__device__ __forceinline__ uint32_t codes4(const float2* x, float inv, float& tie) {
     constexpr float kMagic = 12582912.0f;
-    uint32_t b[4];
+    float2 r[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float r = fmaf(x[i], inv, kMagic);
-        tie = fmaxf(tie, fabsf(fmaf(x[i], inv, kMagic - r)));
-        b[i] = __float_as_uint(r);
+    for (int i = 0; i < 2; ++i) {
+        r[i] = ffma2(x[i], both(inv), both(kMagic));
+        const float2 d = ffma2(x[i], both(inv), ffma2(r[i], both(-1.f), both(kMagic)));
+        tie = fmaxf(tie, fmaxf(fabsf(d.x), fabsf(d.y)));
     }
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    return __byte_perm(__byte_perm(__float_as_uint(r[0].x), __float_as_uint(r[0].y), 0x0040),
+                       __byte_perm(__float_as_uint(r[1].x), __float_as_uint(r[1].y), 0x0040), 0x5410);
 }
 // The same by division, clamped (near a tie, or under a scale too small to be accurate).
-__device__ __forceinline__ uint32_t codes4_exact(const float* x, float scale) {
+__device__ __forceinline__ uint32_t codes4_exact(const float2* x, float scale) {
     uint32_t c = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float r = fminf(fmaxf(rintf(__fdiv_rn(x[i], scale)), -127.f), 127.f);
+        const float v = (i & 1) ? x[i / 2].y : x[i / 2].x;
+        const float r = fminf(fmaxf(rintf(__fdiv_rn(v, scale)), -127.f), 127.f);
         c |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * i);
     }
     return c;
@@ -172,8 +178,14 @@ __device__ __forceinline__ uint32_t codes4_exact(const float* x, float scale) {
 // A lane has two quads of 4 elements: those that half-split rotation pairs, or neighbours,
 // so that a rotation stays inside a lane; the norm and the largest magnitude are shuffles
 // inside the group.  A lane's first loads are issued before the search for the token's
-// sequence, each later one before the head two back is worked on, so that the chain of
-// dependent loads (sequence, page, table row) lies under them.
+// sequence, each later one before the head before is worked on, so that the chain of
+// dependent loads (sequence, page, table row) lies under them (two heads ahead: no faster).
+//
+// Bound by instructions and by each warp's chain (load, two reductions over the lanes, two
+// divisions, store): 2853 tokens of 32 + 2 x 8 heads (D = 128, f16 to int8 pages) take 22 us,
+// 3.0 TB/s, with 217 instructions a warp's turn, issue slots 63% and DRAM 20% (half of the
+// bytes stay in L2); 4096 tokens of 8 + 2 x 4 heads (D = 256, f32, ring) 20 us, 4.5 TB/s.
+// With 48 registers (more warps, some spills) 24 and 24 us.
 template <int D, typename T, typename TQ, bool INT8>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     constexpr int LPR = D / 8;          // lanes a head
@@ -204,9 +216,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         r.a.load(p + ea);
         r.b.load(p + eb);
     };
-    Pair raw[2];
-    fetch(slot_i, raw[0]);
-    fetch(slot_i + step, raw[1]);
+    Pair raw;
+    fetch(slot_i, raw);
 
     const Where w = find_row(a.q_start, a.kv_len, a.B, t, lane);
     if (w.b < 0) return;
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         if (threadIdx.x == 0) atomicExch(a.err, kErrAppendRange);
         return;
     }
-    float cs[4], sn[4];
+    float2 cs[2], sn[2];
     if (rotates) {
         const size_t at = static_cast<size_t>(p) * half + sub * 4;
         load4(a.cos + at, cs);
@@ -231,50 +242,49 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     const size_t srow = slot.slot * a.Hkv * a.cache.rows + slot.row;         // of scales, head 0
 
     int g_kind = 2;
-    float g[8];                          // the norm's weights, where g_kind has any
+    float2 g[4];                         // the norm's weights, where g_kind has any
     for (; slot_i < n_slots; slot_i += step) {   // uniform in the warp, kind too
         const int kind = slot_i < nq ? 0 : slot_i < nq + nk ? 1 : 2;
         const int h = (slot_i - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * RPW + hsub;
         const bool live = h < (kind == 0 ? a.Hq : a.Hkv);
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float2 x[4] = {};
         if (live) {
-            raw[0].a.get(x);
-            raw[0].b.get(x + 4);
+            raw.a.get(x);
+            raw.b.get(x + 2);
         }
-        raw[0] = raw[1];
-        fetch(slot_i + 2 * step, raw[1]);
+        fetch(slot_i + step, raw);
         const float* nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
         if (nw) {
             if (g_kind != kind) {
                 load4(nw + ea, g);
-                load4(nw + eb, g + 4);
+                load4(nw + eb, g + 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] += a.offset;
+                for (int i = 0; i < 4; ++i) g[i] = fadd2(g[i], both(a.offset));
                 g_kind = kind;
             }
-            float ss = 0.f;
+            float2 s2 = fmul2(x[0], x[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 1; i < 4; ++i) s2 = ffma2(x[i], x[i], s2);
+            float ss = s2.x + s2.y;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
             const float r = rsqrtf(ss * (1.0f / D) + a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
+            for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], fmul2(g[i], both(r)));
         }
         if (kind < 2 && rotates) {
             if (split) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = x[i], v = x[4 + i];
-                    x[i] = u * cs[i] - v * sn[i];
-                    x[4 + i] = v * cs[i] + u * sn[i];
+                for (int i = 0; i < 2; ++i) {
+                    const float2 u = x[i], v = x[2 + i], n = fmul2(v, sn[i]);
+                    x[i] = ffma2(u, cs[i], make_float2(-n.x, -n.y));
+                    x[2 + i] = ffma2(v, cs[i], fmul2(u, sn[i]));
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float u = x[2 * i], v = x[2 * i + 1];
-                    x[2 * i] = u * cs[i] - v * sn[i];
-                    x[2 * i + 1] = v * cs[i] + u * sn[i];
+                    const float c = (i & 1) ? cs[i / 2].y : cs[i / 2].x, n = (i & 1) ? sn[i / 2].y : sn[i / 2].x;
+                    x[i] = ffma2(x[i], both(c), fmul2(make_float2(x[i].y, x[i].x), make_float2(-n, n)));
                 }
             }
         }
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
             if (live) {
                 TQ* out = static_cast<TQ*>(a.q_out) + (static_cast<size_t>(t) * a.Hq + h) * D;
                 store4(out + ea, x);
-                store4(out + eb, x + 4);
+                store4(out + eb, x + 2);
             }
             continue;
         }
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
             // a head with an infinity or a NaN gets it as its scale
             float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) m = max3_abs_nan(m, x[i], x[i + 1]);
+            for (int i = 0; i < 4; ++i) m = max3_abs_nan(m, x[i].x, x[i].y);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) m = max3_abs_nan(m, __shfl_xor_sync(kFull, m, o), 0.f);
             const __half hs = __float2half_rn(__fdiv_rn(m, 127.0f));
@@ -299,12 +309,12 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
             if (scale > 0.f && scale < INFINITY) {
                 // an f16 scale with all its bits puts every code within 127.1
                 float tie = 0.f;
-                const float inv = __fdiv_rn(1.0f, scale);
+                const float inv = __frcp_rn(scale);
                 c0 = codes4(x, inv, tie);
-                c1 = codes4(x + 4, inv, tie);
+                c1 = codes4(x + 2, inv, tie);
                 if (tie > 0.4999f || scale < 0x1p-14f) {
                     c0 = codes4_exact(x, scale);
-                    c1 = codes4_exact(x + 4, scale);
+                    c1 = codes4_exact(x + 2, scale);
                 }
             }
             if (live && write) {
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         } else if (live && write) {
             __half* out = static_cast<__half*>(kind == 1 ? a.k_cache : a.v_cache) + (row + h) * D;
             store4(out + ea, x);
-            store4(out + eb, x + 4);
+            store4(out + eb, x + 2);
         }
     }
 }
@@ -341,7 +351,9 @@ void append_types(const AppendLaunch& L, dim3 grid, int threads) {
 
 // ------------------------------------------------------------------ read back
 // A warp takes a row; a lane pieces of 16 elements (one 16-byte load of codes, two of f16),
-// four at a time, all loads before the first store.
+// four at a time, all loads before the first store.  Bound by DRAM: 16 x 32768 int8 tokens of
+// 8 heads to f16 take 474 us, 6.8 TB/s, what a copy takes; 4158 ring tokens of 4 heads
+// (D = 256) to f32 take 13 us, 3.9 TB/s, the launch and the search included.
 constexpr int kReadWarps = 8;
 
 template <typename TO, bool INT8>
@@ -390,20 +402,23 @@ __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadAr
             if (c >= 2 * per) break;
             const bool is_k = c < per;
             TO* out = static_cast<TO*>(is_k ? a.k_out : a.v_out) + dst + static_cast<size_t>(is_k ? c : c - per) * 16;
-            float x[2][8];
+            float2 x[2][4];
             if constexpr (INT8) {
-                const float s = __half2float(sc[u]);
+                const float2 s = both(__half2float(sc[u]));
                 const uint32_t wd[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[i / 8][i % 8] = static_cast<float>(static_cast<int8_t>(wd[i / 4] >> (8 * (i & 3)))) * s;
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t w2 = wd[i / 2] >> (16 * (i & 1));
+                    x[i / 4][i % 4] = fmul2(make_float2(static_cast<float>(static_cast<int8_t>(w2)),
+                                                        static_cast<float>(static_cast<int8_t>(w2 >> 8))), s);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     Raw4<__half> r;
                     r.r = (i & 1) ? make_uint2(raw[u][i / 2].z, raw[u][i / 2].w)
                                   : make_uint2(raw[u][i / 2].x, raw[u][i / 2].y);
-                    r.get(&x[i / 2][4 * (i & 1)]);
+                    r.get(&x[i / 2][2 * (i & 1)]);
                 }
             }
             store8(out, x[0]);
