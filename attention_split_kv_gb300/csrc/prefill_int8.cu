@@ -147,7 +147,7 @@ struct Cfg {
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag, start
     static constexpr uint32_t OFF_FILLS = OFF_MISC + 8;
     static constexpr uint32_t OFF_SEG = (OFF_FILLS + NST * 4 + 7) / 8 * 8;
-    static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (SEGS + 1) * 72 + 1024;   // 72: sizeof(Seg)
+    static constexpr uint32_t SMEM_ALLOC = OFF_SEG + (SEGS + 1) * 80 + 1024;   // 80: sizeof(Seg)
     // TMEM: S of two units, P (D = 64/128: over the S it was made from), then O
     static constexpr bool OVER = D <= 128;
     static constexpr uint32_t COL_P = OVER ? 0 : 2 * BN, P_STRIDE = OVER ? BN : BN / 2;
@@ -170,12 +170,16 @@ struct Args8 {
     int* meta;           // [CTA][8]
     int* err;
     int B, total_q, max_q, Hq, Hkv, G, HG, n_hg, QT1, QTG;   // QT1 queries a row tile, QTG a group
+    int hg_mul;          // 2^22 / HG, up
     int hp, n_hb;        // heads (kv heads x head groups) taken side by side, batches of them
     int P, log2P, max_pages, n_pages, box_rows, window, slot_rows;
     long long capacity;
     int max_rg;
     float scale, softcap;
 };
+
+// row / HG of a row of a tile: exact for rows and HG up to 143 (row * HG < 2^22)
+__device__ __forceinline__ int query_of(const Args8& a, int row) { return (row * a.hg_mul) >> 22; }
 
 // One sequence's chunk, and one of its row groups.
 struct Chunk {
@@ -211,14 +215,14 @@ __device__ __forceinline__ Span group_span(const Args8& a, const Chunk& c, int r
 // roles' own code out of the instruction caches).
 struct Seg {
     int b, rg, hb, off, n_rg;
-    int head;                 // kv head and head group
+    int head, kv, hg0;        // kv head and head group; kv head; the group's first query head of it
     int n, tiles;             // key tiles of this segment and of its item
     int lo, hi, key0;         // keys some row keeps; the segment's first key
     int q_base, n_rows, pos0;
     int two;                  // two row tiles (every key tile is used twice), or one
     long long rem;            // key tiles of the run from this segment on; 0: the end
 };
-static_assert(sizeof(Seg) == 72, "shared memory budget");
+static_assert(sizeof(Seg) == 80, "shared memory budget");
 template <int BN>
 __device__ __forceinline__ void seg_item(const Args8& a, Seg& s) {
     const Chunk c = load_chunk(a, s.b);
@@ -255,7 +259,9 @@ __device__ __forceinline__ void seg_step(const Args8& a, Seg& s, bool first) {
         if (s.rem <= 0) return;
         seg_item<BN>(a, s);
         s.head = s.hb * a.hp + static_cast<int>(blockIdx.x) % a.hp;
-        if (s.head < a.Hkv * a.n_hg) return;   // the last batch may have fewer heads
+        s.kv = s.head / a.n_hg;
+        s.hg0 = (s.head - s.kv * a.n_hg) * a.HG;
+        if (s.kv < a.Hkv) return;   // the last batch may have fewer heads
     }
 }
 // The order in which a segment of n key tiles loads them, which is the order the
@@ -332,7 +338,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     // ---- this CTA's run: sum the key tiles of every (sequence, row group), then find
     // where the run starts
     {
-        long long* sums = reinterpret_cast<long long*>(smem + C::OFF_CODE);   // before any copy
+        long long* sums = reinterpret_cast<long long*>(tab);   // before any table
+        static_assert(sizeof(KeyFactors<BN>) >= 66 * 8, "scratch");
         const long long pairs = static_cast<long long>(a.B) * a.max_rg;
         const long long per = (pairs + kThreads - 1) / kThreads;
         const long long f0 = min(pairs, tid * per), f1 = min(pairs, f0 + per);
@@ -411,16 +418,20 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        long long before = incl - mine, before_t = incl_t - tiles, total = 0, total_t = 0;
-#pragma unroll 4
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) {
-                before += sums[w];
-                before_t += sums[32 + w];
+        long long sw = lane < kThreads / 32 ? sums[lane] : 0, sw_t = lane < kThreads / 32 ? sums[32 + lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, sw, o), y = __shfl_up_sync(0xffffffffu, sw_t, o);
+            if (lane >= o) {
+                sw += x;
+                sw_t += y;
             }
-            total += sums[w];
-            total_t += sums[32 + w];
         }
+        const long long total = __shfl_sync(0xffffffffu, sw, 31), total_t = __shfl_sync(0xffffffffu, sw_t, 31);
+        long long before = __shfl_sync(0xffffffffu, sw, max(warp - 1, 0)), before_t = __shfl_sync(0xffffffffu, sw_t, max(warp - 1, 0));
+        if (warp == 0) before = before_t = 0;
+        before += incl - mine;
+        before_t += incl_t - tiles;
         // as many runs as CTAs for each of the hp heads, or fewer of kMinTiles.  A run's weight is
         // more than SEG_TILES, so it has a key tile at least.
         const long long all = total * a.n_hb;
@@ -453,19 +464,20 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             });
         };
         if (rank < runs) {
+            const long long mine_t = all * (rank + (lane & 1)) / runs;   // the run's start and end
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
-                const long long t = all * (rank + e) / runs;
+                const long long t = __shfl_sync(0xffffffffu, mine_t, e);
                 if (t < all) locate(t, &sums[64 + e], e == 0);
                 else if (tid == 0) sums[64 + e] = total_t * a.n_hb;
+                __syncwarp();
             }
         } else if (tid == 0) {
             sums[64] = sums[65] = 0;
         }
         __syncthreads();
-        if (tid == 0) walk.rem = sums[65] - sums[64];   // 0: no run
-        fence_proxy_async_smem();   // the scratch is where codes land
-        __syncthreads();
+        // (the walking warp, which is also the one that writes the tables; 0: no run)
+        if (warp == C::V_WARP + 1 && lane == 0) walk.rem = sums[65] - sums[64];
     }
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     // Segment `seg` of the run, once it is known; false at the run's end.  leave(): this warp
@@ -504,7 +516,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             for (uint32_t seg = 0; ok && __any_sync(gmask, enter(seg, w)); ++seg) {
                 const bool two = NT == 2 && w->two;
                 const int n = w->n, lo = w->lo, hi = w->hi, k0 = w->key0 + lane * R;
-                const int g = w->head / a.n_hg;
+                const int g = w->kv;
                 const int32_t* table = a.page_table + static_cast<size_t>(w->b) * a.max_pages;
                 __syncwarp(gmask);
                 if (leader) leave(seg);
@@ -670,13 +682,13 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             ok = __all_sync(0xffffffffu, ok);
             if (!ok || !__any_sync(0xffffffffu, enter(seg, w))) break;
             const int n = w->n, lo = w->lo, hi = w->hi, k0 = w->key0 + 2 * lane;
-            const int g = w->head / a.n_hg;
+            const int g = w->kv;
             const int32_t* table = a.page_table + static_cast<size_t>(w->b) * a.max_pages;
             if (lane == 0) {
                 if (seg > 0) ok = wait(bar(C::B_QEMPTY), (seg - 1) & 1, abort_flag, a.err, kErrTimeoutSlot);
                 if (ok) {
                     const int nt = NT == 2 && w->two ? 2 : 1;
-                    const int h0 = g * a.G + (w->head % a.n_hg) * a.HG;
+                    const int h0 = g * a.G + w->hg0;
                     mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
                     for (int t = 0; t < nt; ++t)
 #pragma unroll 1
@@ -870,17 +882,17 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             float m[2 * HL], l[2 * HL];
 #pragma unroll
             for (int x = 0; x < 2 * HL; ++x) {
-                pos[x] = w.pos0 + q0 + (row0 + x * 8 + (lane >> 2)) / a.HG;
+                pos[x] = w.pos0 + q0 + query_of(a, row0 + x * 8 + (lane >> 2));
                 m[x] = -INFINITY;
                 l[x] = 0.f;
             }
             // keys in [all_lo, all_hi) are kept by each of the warp's rows
-            const int all_hi = min(hi, w.pos0 + q0 + row0 / a.HG + 1);
-            const int all_lo = W ? w.pos0 + q0 + (row0 + 16 * HL - 1) / a.HG - W + 1 : 0;
+            const int all_hi = min(hi, w.pos0 + q0 + query_of(a, row0) + 1);
+            const int all_lo = W ? w.pos0 + q0 + query_of(a, row0 + 16 * HL - 1) - W + 1 : 0;
             // without a query among its rows a warp only keeps step (its rows of P are what TMEM
             // holds: rows of the products do not mix)
-            const bool idle = w.n_rows - q0 <= row0 / a.HG;
-            const int nh = HL == HN ? 1 : w.n_rows - q0 <= (row0 + 16) / a.HG ? 1 : 2;   // halves in turn
+            const bool idle = w.n_rows - q0 <= query_of(a, row0);
+            const int nh = HL == HN ? 1 : w.n_rows - q0 <= query_of(a, row0 + 16) ? 1 : 2;   // halves in turn
             for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t gu = u0 + u, buf = gu & 1, tb = (jt + j) % C::NTAB;
@@ -1124,7 +1136,6 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int s0 = C::NS == 1 ? 0 : two ? ws : static_cast<int>(u0 & 1);
                 const uint32_t o_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + C::COL_O + c0;
                 const uint32_t o0 = o_tmem + s0 * D, o1 = o_tmem + (C::NS == 2 ? (s0 ^ 1) * D : 0);
-                const int kv = w.head / a.n_hg, hg0 = (w.head % a.n_hg) * a.HG;
                 const int slot = blockIdx.x * 2 + (w.off > 0 ? 0 : 1);
                 float w0[4], w1[4];
                 char* dst[4];                      // of this lane's part of each row; null: not a row of the call
@@ -1142,9 +1153,9 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         w1[x] = a1.x == -INFINITY ? 0.f : ex2_approx(a1.x - mx);
                         sum = w0[x] * a0.y + w1[x] * a1.y;
                     }
-                    const int qi = q0 + row / a.HG, gh = hg0 + row % a.HG, orow = w.q_base + qi;
+                    const int qr = query_of(a, row), qi = q0 + qr, gh = w.hg0 + row - qr * a.HG, orow = w.q_base + qi;
                     const bool live = row < a.QT1 * a.HG && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
-                    const size_t at = static_cast<size_t>(orow) * a.Hq + kv * a.G + gh;
+                    const size_t at = static_cast<size_t>(orow) * a.Hq + w.kv * a.G + gh;
                     const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + row;
                     if (whole) {
                         // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
@@ -1365,6 +1376,7 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     a.G = p.G;
     a.HG = p.HG;
     a.n_hg = p.n_hg;
+    a.hg_mul = (1 << 22) / p.HG + 1;
     a.QT1 = p.QT1;
     a.QTG = p.QTG;
     a.P = L.page_size;
