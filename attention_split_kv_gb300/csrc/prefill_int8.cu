@@ -942,9 +942,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         const float k1 = cap_log2 * (-1.0f / 3.0f), k2 = cap_log2 * (2.0f / 15.0f),
                                     k3 = cap_log2 * (-17.0f / 315.0f);
                         float ax = 0.f;
+                        float2 lv[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 f = fa[4 * i];
+                            lv[i] = make_float2(f.z, f.w);
 #pragma unroll
                             for (int x = 0; x < 2 * HN; ++x) {
                                 y[x][i] = fmul2(y[x][i], make_float2(f.x, f.y));
@@ -954,24 +956,22 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         if (__all_sync(0xffffffffu, ax <= 0.25f)) {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 f = fa[4 * i];
 #pragma unroll
                                 for (int x = 0; x < 2 * HN; ++x) {
                                     const float2 v = y[x][i], z = fmul2(v, v);
                                     float2 q = ffma2(z, make_float2(k3, k3), make_float2(k2, k2));
                                     q = ffma2(q, z, make_float2(k1, k1));
                                     q = ffma2(q, z, make_float2(cap_log2, cap_log2));
-                                    y[x][i] = ffma2(v, q, make_float2(f.z, f.w));
+                                    y[x][i] = ffma2(v, q, lv[i]);
                                 }
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 f = fa[4 * i];
 #pragma unroll
                                 for (int x = 0; x < 2 * HN; ++x)
-                                    y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(y[x][i].x), f.z),
-                                                          fmaf(cap_log2, tanh_abs_accurate(y[x][i].y), f.w));
+                                    y[x][i] = make_float2(fmaf(cap_log2, tanh_abs_accurate(y[x][i].x), lv[i].x),
+                                                          fmaf(cap_log2, tanh_abs_accurate(y[x][i].y), lv[i].y));
                             }
                         }
                     } else {
