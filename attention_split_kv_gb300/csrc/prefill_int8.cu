@@ -137,8 +137,9 @@ struct Cfg {
         B_S,                               // S of buffer 0, 1
         B_SFREE = B_S + 2,                 // it has been read (D = 256)
         B_P = B_SFREE + 2,                 // P of buffer 0, 1
-        B_PV = B_P + 2,                    // its PV is done (D = 256)
-        B_DONE = B_PV + 2,                 // a segment's last PV is done
+        B_PV = B_P + 2,                    // its PV is done (D = 64/128: of the tile's first 64 keys)
+        B_PH = B_PV + 2,                   // P of the first 64 keys (D = 64/128)
+        B_DONE = B_PH + 2,                 // a segment's last PV is done
         B_OFREE,                           // its O has been read
         B_ML,                              // its row statistics are in shared memory
         B_TEARDOWN,
@@ -402,6 +403,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 mbar_init(bar(C::B_SFREE + i), C::NSM / C::NS);
                 mbar_init(bar(C::B_P + i), C::NSM / C::NS);
                 mbar_init(bar(C::B_PV + i), 1);
+                mbar_init(bar(C::B_PH + i), C::NSM / C::NS);
             }
             mbar_init(bar(C::B_DONE), 1);
             mbar_init(bar(C::B_OFREE), C::NSM);
@@ -621,7 +623,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const uint32_t gu = u0 + u, buf = gu & 1;
                 const int j = two ? u >> 1 : u;
                 const uint32_t gi = base + item_v(two, j, n), slot = gi % RING;
-                ok = wait_all(C::B_P + buf, gu >> 1, kErrTimeoutSoftmax) &&
+                ok = wait_all(C::OVER ? C::B_PH + buf : C::B_P + buf, gu >> 1, kErrTimeoutSoftmax) &&
                      wait_all(C::B_OPFULL + slot, gi / RING, kErrTimeoutLoad);
                 // O still holds the segment before until its rows have been read
                 if (ok && u == 0 && seg > 0) ok = wait_all(C::B_OFREE, seg - 1, kErrTimeoutSoftmax);
@@ -629,10 +631,18 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tc_fence_after();
                 const uint64_t vd = desc_advance(v_desc, slot * C::OP_BYTES);
                 const uint32_t o_tmem = tmem + C::COL_O + (C::NS == 2 ? buf * D : 0);
+                // (D = 64/128: the first half's products run while the second's P are made)
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
+                for (int kk = 0; kk < BN / 16; ++kk) {
+                    if (C::OVER && kk == BN / 32) {
+                        tc_commit_one(one, bar(C::B_PV + buf));
+                        if (!(ok = wait_all(C::B_P + buf, gu >> 1, kErrTimeoutSoftmax))) break;
+                        tc_fence_after();
+                    }
                     tc_mma_f16_ts_one(one, o_tmem, tmem + C::COL_P + buf * C::P_STRIDE + kk * 8,
                                       desc_advance(vd, kk * 16 * 128), idesc_o, u >= C::NS || kk > 0 ? 1u : 0u);
+                }
+                if (!ok) break;
                 if (!C::OVER) tc_commit_one(one, bar(C::B_PV + buf));
                 if (!two || (u & 1)) {
                     tc_commit_one(one, bar(C::B_OPEMPTY + slot));
@@ -908,7 +918,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     tc_fence_after();
                     return __all_sync(0xffffffffu, done);
                 };
-                if (!C::OVER && idle) warp_arrive(bar(C::B_SFREE + buf), lane);
+                if (idle) warp_arrive(bar((C::OVER ? C::B_PH : C::B_SFREE) + buf), lane);
                 if (!C::OVER && gu >= 2 && !(ok = pv_done(gu - 2))) break;
 #pragma unroll 1
                 for (int it = 0; it < BN / 64 * nh && !idle; ++it) {   // 64 keys, a half or both
@@ -1022,29 +1032,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                                 m[x] = v;
                             }
                         }
-                        // what was weighted with the old maxima is rescaled: P of the tile's first
-                        // 64 keys, and the stream's O (one stream: after PV of the unit before)
-                        if (BN > 64 && c > 0) {
-#pragma unroll
-                            for (int hf = 0; hf < HN; ++hf) {
-                                const uint32_t at = p_addr + (static_cast<uint32_t>(hf * 16) << 16);
-                                uint32_t r[16];
-                                tc_wait_st();
-                                tc_ld_16x128b_x8(at, r);
-                                tc_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
-                                    const float al = alpha[2 * hf + (i & 1)];
-                                    const __half2 hv = __floats2half2_rn(v.x * al, v.y * al);
-                                    r[i] = *reinterpret_cast<const uint32_t*>(&hv);
-                                }
-                                tc_st_16x128b_x4(at, *reinterpret_cast<const uint32_t(*)[8]>(r));
-                                tc_st_16x128b_x4(at + 16, *reinterpret_cast<const uint32_t(*)[8]>(r + 8));
-                            }
-                        }
-                        if (u >= C::NS) {
-                            if (C::NS == 1 && !(ok = pv_done(gu - 1))) break;
+                        // what O holds was weighted with the old maxima: one stream: after PV of the
+                        // unit before; two: after PV of the tile's first 64 keys, for the second
+                        if (u >= C::NS || c > 0) {
+                            if ((C::NS == 1 || c > 0) && !(ok = pv_done(C::NS == 1 ? gu - 1 : gu))) break;
                             const uint32_t o_addr = lanes + half + C::COL_O + (C::NS == 2 ? buf * D : 0);
 #pragma unroll 1
                             for (int e = 0; e < D; e += 32) {
@@ -1091,6 +1082,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
 #pragma unroll
                     for (int x = 0; x < 2 * HN; ++x) l[x] += ls[x].x + ls[x].y;
+                    if (C::OVER && c == 0 && (nh == 1 || it == 1)) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        warp_arrive(bar(C::B_PH + buf), lane);
+                    }
                     if constexpr (HL > HN) {
                         if (nh == 2) {   // the other half's state to the front
 #pragma unroll
