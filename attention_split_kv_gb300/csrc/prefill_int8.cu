@@ -172,6 +172,7 @@ struct Args8 {
     int* err;
     int B, total_q, max_q, Hq, Hkv, G, HG, n_hg, QT1, QTG;   // QT1 queries a row tile, QTG a group
     int hg_mul;          // 2^22 / HG, up
+    int QQ;              // queries a quarter of the tile's rows (32 of them), or 0: rows one after the other
     int hp, n_hb;        // heads (kv heads x head groups) taken side by side, batches of them
     int P, log2P, max_pages, n_pages, box_rows, window, slot_rows;
     long long capacity;
@@ -179,8 +180,15 @@ struct Args8 {
     float scale, softcap;
 };
 
-// row / HG of a row of a tile: exact for rows and HG up to 143 (row * HG < 2^22)
-__device__ __forceinline__ int query_of(const Args8& a, int row) { return (row * a.hg_mul) >> 22; }
+// The query of a tile's row (row / HG, exact for rows and HG up to 143: row * HG < 2^22), and
+// its packed row, query * HG + head; -1 where the tile has none.
+__device__ __forceinline__ int query_of(const Args8& a, int row) {
+    return a.QQ ? (row >> 5) * a.QQ + (((row & 31) * a.hg_mul) >> 22) : (row * a.hg_mul) >> 22;
+}
+__device__ __forceinline__ int packed_row(const Args8& a, int row) {
+    if (!a.QQ) return row < a.QT1 * a.HG ? row : -1;
+    return (row & 31) < a.QQ * a.HG ? (row >> 5) * a.QQ * a.HG + (row & 31) : -1;
+}
 
 // One sequence's chunk, and one of its row groups.
 struct Chunk {
@@ -699,12 +707,16 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (ok) {
                     const int nt = NT == 2 && w->two ? 2 : 1;
                     const int h0 = g * a.G + w->hg0;
+                    const int q0 = w->q_base + w->rg * a.QTG;
                     mbar_arrive_expect_tx(bar(C::B_QFULL), nt * NCH * a.HG * a.QT1 * 128);
-                    for (int t = 0; t < nt; ++t)
+                    // a box a row tile, or a quarter of one, and 64 columns
+                    const int boxes = a.QQ ? 4 : nt, queries = a.QQ ? a.QQ : a.QT1;
+                    const uint32_t apart = a.QQ ? 32 * 128 : C::Q_TILE;
+                    for (int t = 0; t < boxes; ++t)
 #pragma unroll 1
                         for (int c = 0; c < NCH; ++c)
-                            tma_load_3d(sbase + C::OFF_Q + t * C::Q_TILE + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64,
-                                        h0, w->q_base + w->rg * a.QTG + t * a.QT1);
+                            tma_load_3d(sbase + C::OFF_Q + t * apart + c * (BM * 128), &tm_q, bar(C::B_QFULL), c * 64, h0,
+                                        q0 + t * queries);
                 }
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -902,7 +914,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // without a query among its rows a warp only keeps step (its rows of P are what TMEM
             // holds: rows of the products do not mix)
             const bool idle = w.n_rows - q0 <= query_of(a, row0);
-            const int nh = HL == HN ? 1 : w.n_rows - q0 <= query_of(a, row0 + 16) ? 1 : 2;   // halves in turn
+            const int nh = HL == HN || a.QQ ? 1 : w.n_rows - q0 <= query_of(a, row0 + 16) ? 1 : 2;   // halves in turn
             for (int u = first_u; ok && u < U; u += C::NS) {
                 const int j = two ? u >> 1 : u;
                 const uint32_t gu = u0 + u, buf = gu & 1, tb = (jt + j) % C::NTAB;
@@ -1149,10 +1161,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         w1[x] = a1.x == -INFINITY ? 0.f : ex2_approx(a1.x - mx);
                         sum = w0[x] * a0.y + w1[x] * a1.y;
                     }
-                    const int qr = query_of(a, row), qi = q0 + qr, gh = w.hg0 + row - qr * a.HG, orow = w.q_base + qi;
-                    const bool live = row < a.QT1 * a.HG && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
+                    const int pr = packed_row(a, row), qr = query_of(a, row), qi = q0 + qr, gh = w.hg0 + pr - qr * a.HG;
+                    const int orow = w.q_base + qi;
+                    const bool live = pr >= 0 && qi < w.n_rows && gh < a.G && orow >= 0 && orow < a.total_q;
                     const size_t at = static_cast<size_t>(orow) * a.Hq + w.kv * a.G + gh;
-                    const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + row;
+                    const size_t part = static_cast<size_t>(slot) * a.slot_rows + rt * a.QT1 * a.HG + pr;
                     if (whole) {
                         // a sum of 0 is a row without keys (0, -inf); NaN stays NaN
                         const float inv = sum == 0.f ? 0.f : 1.0f / sum;
@@ -1301,7 +1314,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Ar
 
 // Row packing and the workspace: partial rows, their statistics, a description a CTA.
 struct Plan {
-    int G, HG, n_hg, QT1, NT, QTG, slot_rows;
+    int G, HG, n_hg, QT1, NT, QTG, QQ, slot_rows;
     size_t off_ml, off_meta, bytes;
 };
 Plan make_plan(int max_q, int Hq, int Hkv, int D) {
@@ -1311,6 +1324,12 @@ Plan make_plan(int max_q, int Hq, int Hkv, int D) {
     p.n_hg = (p.G + p.HG - 1) / p.HG;
     p.QT1 = BM / p.HG;
     p.NT = D <= 128 && max_q > p.QT1 ? 2 : 1;   // D = 256: one O fills TMEM
+    // A few queries fill the 16-row halves of the tile's quarters first, so that a softmax warp
+    // has one of them and not two in turn (1 to 8 drafts of 32 sequences, up to 32 rows: 112 us
+    // one after the other, 96 by quarters)
+    const int half = 16 / p.HG;   // queries
+    p.QQ = D <= 128 && max_q > half && max_q <= 4 * half ? half : 0;
+    if (p.QQ) p.QT1 = 4 * p.QQ;
     p.QTG = p.NT * p.QT1;
     p.slot_rows = (max_q < p.QTG ? max_q : p.QTG) * p.HG;
     const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * p.slot_rows;
@@ -1331,7 +1350,7 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
         // q [total_q, Hq, D]: boxes of HG heads of QT1 queries, packed rows in row order
         const uint64_t dims[3] = {(uint64_t)D, (uint64_t)L.Hq, (uint64_t)L.total_q};
         const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)D * 2 * L.Hq};
-        const uint32_t box[3] = {64u, (uint32_t)p.HG, (uint32_t)p.QT1};
+        const uint32_t box[3] = {64u, (uint32_t)p.HG, (uint32_t)(p.QQ ? p.QQ : p.QT1)};
         if ((st = encode_tmap_sw128(&tq, L.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, strides, box)) != ATTN_OK)
             return st;
     }
@@ -1373,6 +1392,7 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     a.HG = p.HG;
     a.n_hg = p.n_hg;
     a.hg_mul = (1 << 22) / p.HG + 1;
+    a.QQ = p.QQ;
     a.QT1 = p.QT1;
     a.QTG = p.QTG;
     a.P = L.page_size;

@@ -137,6 +137,29 @@ def test_growing_logits_rescale(D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [2, 30, 100])
+def test_logits_that_step_up_every_64_keys(D, n):
+    # the running maximum moves in the second half of a tile too, by more than any threshold
+    case = si.make_chunked_case(2, 4, 2, D, [n, 1], [900, 411], seed=D + n, page_size=16, scale=3.2 / math.sqrt(D),
+                                int8=True)
+    for b in range(2):
+        for i in range(-(-int(case.kv_len[b]) // 16)):   # (table entries behind them are -1)
+            case.k_scales[int(case.page_table[b, i])] *= 1 + i // 4
+    _check(case, "D=%d n=%d" % (D, n))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 16), (1, 17), (1, 64), (1, 65), (2, 9), (3, 5), (3, 6), (3, 20), (3, 21), (4, 5),
+                                 (4, 8), (4, 16), (4, 17), (5, 4), (5, 13), (7, 8), (7, 9), (8, 2), (8, 3), (8, 9),
+                                 (11, 2), (11, 4), (11, 5), (16, 1), (16, 2), (16, 4), (16, 5), (17, 2)])
+def test_few_queries_by_quarters(D, G, n):
+    # row counts around those that the quarters of a tile take; shorter chunks beside the longest
+    case = si.make_chunked_case(4, 2 * G, 2, D, [n, 1, max(n // 2, 1), 0], [500, 130, 0, 9], seed=16 * G + n,
+                                page_size=16, int8=True)
+    _check(case, "D=%d G=%d n=%d" % (D, G, n), extra=2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_rows_that_keep_no_key(D):
     # chunks longer than their caches: rows at negative positions; a sequence without tokens
     case = si.make_chunked_case(3, 4, 2, D, [40, 10, 200], [0, 5, 0], seed=29, page_size=16, int8=True)
