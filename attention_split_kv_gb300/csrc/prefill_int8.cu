@@ -37,14 +37,15 @@
 // What bounds it: shared memory.  Codes are written by TMA, read, stored at twice the size
 // and read by the MMA, so a 128-key tile of one row tile (D = 128) takes 2170 wavefronts of
 // 128 bytes (LSU 1150, MMA operands 768, TMA 256) in 2650 to 2790 cycles: 524288 cached
-// tokens of 8 kv heads and 4 new ones of 32 heads take 305 us, 3.6 TB/s (HBM alone: 161 us).
-// With two row tiles one conversion serves both and the softmax's chain (S, 3500 cycles of
-// softmax, PV, the next S) comes to the front: 8 chunks of 512 tokens on 512 to 7680 cached
-// ones (32/8 heads) take 305 us, 778 TFLOP/s, tensor pipe 34%, issue slots 49%, shared memory
-// 65%.  16 softmax warps of 16 rows do not shorten it (307 us): a 16-byte factor load of 4
-// distinct addresses takes 4 wavefronts, and with half the rows a load serves half as much.
-// D = 256 with a softcap and a window of 1024 keys: 78 us, 387 TFLOP/s, a third of it each
-// segment's fixed part (filling the pipeline, writing its rows).
+// tokens of 8 kv heads and 4 new ones of 32 heads take 300 us, 3.6 TB/s (HBM alone: 161 us);
+// 1 to 8 new tokens of 32 sequences of 512 to 8192, 96 us, 3.0 TB/s.  With two row tiles one
+// conversion serves both, and the softmax's chain (S, 3500 cycles of softmax, PV, the next S)
+// comes to the front: 8 chunks of 512 tokens on 1 to 7680 cached ones (32/8 heads) take
+// 302 us, 786 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
+// of 16 rows do not shorten it (307 us): a 16-byte factor load takes 4 wavefronts, and with
+// half the rows a load serves half as much.  D = 256 with a softcap and a window of 1024
+// keys: 71 us, 422 TFLOP/s: shared memory (3200 wavefronts a 64-key tile: Q is read anew for
+// each) and each segment's fixed part.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -106,9 +107,10 @@ struct Cfg {
     static constexpr int NST = D == 64 ? 8 : D == 128 ? (NT == 1 ? 5 : 3) : 3;
     static constexpr int NTAB = 4;                       // key-factor tables
     // what a segment costs beside its key tiles (filling the pipeline, writing its rows), in
-    // key tiles: 12 to 16 thousand cycles, where a tile takes 2.7 (one row tile), 5 (two) or
-    // 1.5 thousand (D = 256).  8 x 512 chunks: 337 us unweighted, 306 weighted
-    static constexpr int SEG_TILES = D == 256 ? 6 : 3;
+    // key tiles.  8 x 512 chunks (D = 128): 337 us unweighted, 304 with 2, 302 with 3, 305 with
+    // 4; the sum of eight D = 256 calls (prompts, chunks, drafts): 620, 611, 616, 620 and 631 us
+    // with 1, 2, 3, 4 and 6
+    static constexpr int SEG_TILES = D == 256 ? 2 : 3;
     static constexpr int SEGS = 4;                       // segment descriptions
     static constexpr uint32_t Q_TILE = NCH * BM * 128;
     static constexpr uint32_t OP_CHUNK = BN * 128, OP_BYTES = NCH * OP_CHUNK;
