@@ -20,6 +20,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_internal.h"
 #include "ptx.cuh"
 
@@ -350,19 +352,28 @@ void append_types(const AppendLaunch& L, dim3 grid, int threads) {
 }
 
 // ------------------------------------------------------------------ read back
-// A warp takes a row; a lane pieces of 16 elements (one 16-byte load of codes, two of f16),
-// four at a time, all loads before the first store.  Bound by DRAM: 16 x 32768 int8 tokens of
-// 8 heads to f16 take 474 us, 6.8 TB/s, what a copy takes; 4158 ring tokens of 4 heads
-// (D = 256) to f32 take 13 us, 3.9 TB/s, the launch and the search included.
+// A warp takes a row, or 32 U pieces of one (ONE: no more than those); a lane pieces of E
+// elements, one load each, U at a time, all loads before the first store.  Pieces of 16 codes
+// become 32 bytes of f16, those of 8 codes or f16 values 16 or 32 bytes, so neighbouring lanes
+// fill whole sectors.  Bound by DRAM: 16 x 32768 int8 tokens of 8 heads to f16 take 473 us,
+// 6.8 TB/s, what a copy takes; 8 x 32768 f16 tokens to f32 478 us (555 with 64 bytes a lane);
+// 4158 ring tokens of 4 heads (D = 256) to f32 12 us, the launch and the search included.
 constexpr int kReadWarps = 8;
+constexpr int kReadPieces = 4;   // U
 
-template <typename TO, bool INT8>
+template <bool INT8, typename TO>
+constexpr int read_piece() { return INT8 && sizeof(TO) == 2 ? 16 : 8; }   // E
+
+template <typename TO, bool INT8, bool ONE>
 __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadArgs a) {
+    constexpr int E = read_piece<INT8, TO>(), U = kReadPieces;
+    constexpr int W = INT8 ? E / 4 : E / 2;   // words of a piece
+    using Raw = typename std::conditional<W == 4, uint4, uint2>::type;
     const int lane = threadIdx.x & 31;
     const long long t = static_cast<long long>(blockIdx.x) * kReadWarps + (threadIdx.x >> 5);
     if (t >= a.total) return;
-    const int log_d = a.D == 64 ? 2 : a.D == 128 ? 3 : 4;   // log2 of a head's pieces
-    const int per = a.Hkv << log_d;                          // pieces of a token's K (or V)
+    const int log_d = (a.D == 64 ? 6 : a.D == 128 ? 7 : 8) - (E == 16 ? 4 : 3);   // log2 of a head's pieces
+    const int per = a.Hkv << log_d;                                               // pieces of a token's K (or V)
     const Where w = find_row(a.out_start, a.kv_len, a.B, static_cast<int>(t), lane);
     if (w.b < 0) return;
     const long long p = (a.first ? static_cast<long long>(a.first[w.b]) : 0ll) + (t - w.start);
@@ -372,59 +383,74 @@ __global__ void __launch_bounds__(kReadWarps * 32) kv_read_kernel(const KvReadAr
     if (held) held = find_slot(a.cache, w.b, p, slot, a.err);
     const size_t src = (slot.slot * a.cache.rows + slot.row) * a.Hkv * a.D;
     const size_t dst = static_cast<size_t>(t) * a.Hkv * a.D;
-    for (int c0 = lane; c0 < 2 * per; c0 += 128) {
-        uint4 raw[4][INT8 ? 1 : 2];
-        __half sc[4];
+    for (int c0 = blockIdx.y * 32 * U + lane; c0 < 2 * per; c0 += 32 * U) {
+        union {
+            Raw v;
+            uint32_t w[W];
+        } raw[U];
+        __half sc[U];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int c = c0 + 32 * u;
             const bool is_k = c < per;
             const int cc = is_k ? c : c - per;
+            sc[u] = __float2half_rn(0.f);
             if (c >= 2 * per || !held) {
-#pragma unroll
-                for (int i = 0; i < (INT8 ? 1 : 2); ++i) raw[u][i] = make_uint4(0u, 0u, 0u, 0u);
-                sc[u] = __float2half_rn(0.f);
+                raw[u].v = Raw{};
             } else if constexpr (INT8) {
-                raw[u][0] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(is_k ? a.k_cache : a.v_cache) +
-                                                            src + static_cast<size_t>(cc) * 16);
+                raw[u].v = *reinterpret_cast<const Raw*>(static_cast<const int8_t*>(is_k ? a.k_cache : a.v_cache) + src +
+                                                         static_cast<size_t>(cc) * E);
                 sc[u] = static_cast<const __half*>(
                     is_k ? a.k_scales : a.v_scales)[(slot.slot * a.Hkv + (cc >> log_d)) * a.cache.rows + slot.row];
             } else {
-                const uint4* s = reinterpret_cast<const uint4*>(
-                    static_cast<const __half*>(is_k ? a.k_cache : a.v_cache) + src + static_cast<size_t>(cc) * 16);
-                raw[u][0] = s[0];
-                raw[u][1] = s[1];
+                raw[u].v = *reinterpret_cast<const Raw*>(static_cast<const __half*>(is_k ? a.k_cache : a.v_cache) + src +
+                                                         static_cast<size_t>(cc) * E);
             }
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int c = c0 + 32 * u;
             if (c >= 2 * per) break;
             const bool is_k = c < per;
-            TO* out = static_cast<TO*>(is_k ? a.k_out : a.v_out) + dst + static_cast<size_t>(is_k ? c : c - per) * 16;
-            float2 x[2][4];
-            if constexpr (INT8) {
-                const float2 s = both(__half2float(sc[u]));
-                const uint32_t wd[4] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w};
+            TO* out = static_cast<TO*>(is_k ? a.k_out : a.v_out) + dst + static_cast<size_t>(is_k ? c : c - per) * E;
+            const float2 s = both(__half2float(sc[u]));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t w2 = wd[i / 2] >> (16 * (i & 1));
-                    x[i / 4][i % 4] = fmul2(make_float2(static_cast<float>(static_cast<int8_t>(w2)),
-                                                        static_cast<float>(static_cast<int8_t>(w2 >> 8))), s);
-                }
-            } else {
+            for (int e = 0; e < E; e += 8) {
+                float2 x[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    Raw4<__half> r;
-                    r.r = (i & 1) ? make_uint2(raw[u][i / 2].z, raw[u][i / 2].w)
-                                  : make_uint2(raw[u][i / 2].x, raw[u][i / 2].y);
-                    r.get(&x[i / 2][2 * (i & 1)]);
+                    if constexpr (INT8) {
+                        const uint32_t w2 = raw[u].w[(e + 2 * i) / 4] >> (16 * (i & 1));
+                        x[i] = fmul2(make_float2(static_cast<float>(static_cast<int8_t>(w2)),
+                                                 static_cast<float>(static_cast<int8_t>(w2 >> 8))), s);
+                    } else {
+                        x[i] = __half22float2(*reinterpret_cast<const __half2*>(&raw[u].w[i]));
+                    }
                 }
+                store8(out + e, x);
             }
-            store8(out, x[0]);
-            store8(out + 8, x[1]);
         }
+        if (ONE) break;
     }
+}
+
+template <typename TO, bool INT8>
+void read_dispatch(const KvReadLaunch& L) {
+    const KvReadArgs& a = L.args;
+    // Few rows (less than two waves of warps) are shared by warps that load all of their pieces
+    // at once: 13.5 us with a warp a row, 12.0 shared, for 4158 rows of 2 x 1024 f16 values to
+    // f32; of 262144 rows of that size 478 and 517.  Rows of at most a piece a lane take the
+    // form without a loop too, for its registers (more warps): 524288 rows of 32 pieces 200 us
+    // with the loop, 167 without; of 64 pieces 277 and 288, of 128 pieces 473 and 540.
+    const int pieces = 2 * a.Hkv * a.D / read_piece<INT8, TO>();
+    const int passes = (pieces + 32 * kReadPieces - 1) / (32 * kReadPieces);
+    const bool one = pieces <= 32 || a.total < 64 * sm_count();
+    const dim3 grid((a.total - 1) / kReadWarps + 1, one ? passes : 1);
+    if (trace_enabled())
+        trace("kv_read_kernel<out=%s,int8=%d> one_pass=%d grid=(%u,%u) block=%d B=%d Hkv=%d D=%d", L.out_f32 ? "f32" : "f16",
+              (int)INT8, (int)one, grid.x, grid.y, kReadWarps * 32, a.B, a.Hkv, a.D);
+    if (one) kv_read_kernel<TO, INT8, true><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
+    else kv_read_kernel<TO, INT8, false><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
 }
 
 }  // namespace
@@ -457,17 +483,12 @@ attn_status launch_append(const AppendLaunch& L) {
 }
 
 attn_status launch_kv_read(const KvReadLaunch& L) {
-    const KvReadArgs& a = L.args;
-    const int grid = (a.total - 1) / kReadWarps + 1;
-    if (trace_enabled())
-        trace("kv_read_kernel<out=%s,int8=%d> grid=%d block=%d B=%d Hkv=%d D=%d", L.out_f32 ? "f32" : "f16",
-              (int)L.int8, grid, kReadWarps * 32, a.B, a.Hkv, a.D);
     if (L.int8) {
-        if (L.out_f32) kv_read_kernel<float, true><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
-        else kv_read_kernel<__half, true><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
+        if (L.out_f32) read_dispatch<float, true>(L);
+        else read_dispatch<__half, true>(L);
     } else {
-        if (L.out_f32) kv_read_kernel<float, false><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
-        else kv_read_kernel<__half, false><<<grid, kReadWarps * 32, 0, L.stream>>>(a);
+        if (L.out_f32) read_dispatch<float, false>(L);
+        else read_dispatch<__half, false>(L);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "kv_read launch failed: %s", cudaGetErrorString(e));

@@ -313,6 +313,26 @@ def test_read_from_the_start_by_default():
     assert bool((k[6] == 0).all())
 
 
+@pytest.mark.parametrize("n", [5, 3400])
+@pytest.mark.parametrize("Hkv,D", [(1, 64), (5, 128), (7, 256)])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("out_f32", [False, True])
+def test_read_of_few_and_of_many_rows(n, Hkv, D, int8, out_f32):
+    # rows of one and of several passes, shared by warps or not
+    cache = Cache("plain", 3, Hkv, D, 3500, int8=int8, fill=True, seed=Hkv)
+    g = cache.to("cuda")
+    start = torch.arange(0, 3 * n + 1, n, dtype=torch.int32).cuda()
+    first = torch.tensor([0, 1, 99], dtype=torch.int32).cuda()
+    k, v = attn.kv_read(g, start, 3 * n, first=first, kv_len=torch.full((3,), 3500, dtype=torch.int32).cuda(),
+                        out_f32=out_f32)
+    for x, name in ((k, "k"), (v, "v")):
+        want = getattr(g, name).float()
+        if int8:
+            want = want * getattr(g, name + "_scales").float().transpose(1, 2)[..., None]
+        want = torch.cat([want[b, f:f + n] for b, f in enumerate((0, 1, 99))])
+        assert torch.equal(x, want if out_f32 else want.half()), name
+
+
 def test_read_offsets_past_32_bits():
     # 5.4e9 codes of one sequence: the last tokens' offsets need more than 32 bits
     Hkv, D, cap = 8, 256, 1 << 20
