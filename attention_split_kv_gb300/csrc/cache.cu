@@ -444,7 +444,7 @@ void read_dispatch(const KvReadLaunch& L) {
     // with the loop, 167 without; of 64 pieces 277 and 288, of 128 pieces 473 and 540.
     const int pieces = 2 * a.Hkv * a.D / read_piece<INT8, TO>();
     const int passes = (pieces + 32 * kReadPieces - 1) / (32 * kReadPieces);
-    const bool one = pieces <= 32 || a.total < 64 * sm_count();
+    const bool one = passes <= 65535 && (pieces <= 32 || a.total < 64 * sm_count());   // (gridDim.y)
     const dim3 grid((a.total - 1) / kReadWarps + 1, one ? passes : 1);
     if (trace_enabled())
         trace("kv_read_kernel<out=%s,int8=%d> one_pass=%d grid=(%u,%u) block=%d B=%d Hkv=%d D=%d", L.out_f32 ? "f32" : "f16",
@@ -466,7 +466,7 @@ attn_status launch_append(const AppendLaunch& L) {
     const int turns = (a.Hq + rpw - 1) / rpw + 2 * ((a.Hkv + rpw - 1) / rpw);   // warps' worth of heads
     const bool many = a.total_q >= 2 * sm_count();
     const int most = many ? (turns + 7) / 8 : turns, warps = most < 8 ? most : 8, threads = warps * 32;
-    const int parts = many ? 1 : (turns + warps - 1) / warps;
+    const int parts = many ? 1 : min((turns + warps - 1) / warps, 65535);   // (gridDim.y; the rest in turn)
     const dim3 grid(a.total_q, parts);
     if (trace_enabled())
         trace("append_kernel<D=%d,in=%s,q_out=%s,int8=%d> grid=(%d,%d) block=%d B=%d Hq=%d Hkv=%d rot=%d", L.D,
