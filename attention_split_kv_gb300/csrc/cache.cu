@@ -185,7 +185,7 @@ __device__ __forceinline__ uint32_t codes4_exact(const float2* x, float scale) {
 //
 // Bound by instructions and by each warp's chain (load, two reductions over the lanes, two
 // divisions, store): 2853 tokens of 32 + 2 x 8 heads (D = 128, f16 to int8 pages) take 22 us,
-// 3.0 TB/s, with 217 instructions a warp's turn, issue slots 63% and DRAM 20% (half of the
+// 3.0 TB/s, with 217 instructions a warp's turn, issue slots 67% and DRAM 20% (half of the
 // bytes stay in L2); 4096 tokens of 8 + 2 x 4 heads (D = 256, f32, ring) 20 us, 4.5 TB/s.
 // With 48 registers (more warps, some spills) 24 and 24 us.
 template <int D, typename T, typename TQ, bool INT8>

@@ -925,8 +925,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 ok = __all_sync(0xffffffffu, ok);   // tcgen05 loads and stores need whole warps
                 if (!ok) break;
                 tc_fence_after();
-                // PV of unit g is done: its P may be overwritten, its O rescaled.  (Where P lies
-                // over S, S of unit g + 2 was issued after it.)
+                // PV of unit g is done (D = 64/128: that of its first 64 keys): its P may be
+                // overwritten, its O rescaled.  Where P lies over S, S of unit g + 2 came after all of it.
                 auto pv_done = [&](uint32_t g) -> bool {
                     const bool done = wait(bar(C::B_PV + (g & 1)), (g >> 1) & 1, abort_flag, a.err, kErrTimeoutMma);
                     tc_fence_after();
