@@ -10,10 +10,16 @@
 //   S   = Q Kc^T                                 (tcgen05.mma, f32 in TMEM)
 //   y_j = S_j (ks_j scale log2e) + log2 vs_j     (one packed fma)
 //   P_j = f16(2^(y_j - m)),  m the running maximum of y
-//   O  += P Vc,   l += 2^(y_j - m) / vs_j        (tcgen05.mma; f32)
+//   O  += P Vc,   l += r(2^(y_j - m)) / vs_j     (tcgen05.mma; f32)
 //
 // so the value's scale sits in its weight, and the weight is rounded once, relative
 // to the row's largest weighted scale.  out = O / l, lse = (m + log2 l) / log2e.
+// r rounds to the 11 bits that f16 keeps, with f32's exponents: the sum is then over the
+// weights that the product uses, so out is a convex combination of values and a dominant
+// key gives its value exactly (with the unrounded weights: off by up to 2^-11 of it).  f16
+// itself will not do for the sum, because a key of a small value scale can have a weight
+// far below f16's normal range and still most of the row's mass.  The rounding costs 8
+// chunks of 512 tokens 8% (303 us without it) and calls of few rows at most 1%.
 //
 // Rows are packed: the query heads that share a kv head are rows of one tile beside
 // its queries (row r is query r / HG, head r % HG), so a decode step or a few draft
@@ -41,7 +47,7 @@
 // 1 to 8 new tokens of 32 sequences of 512 to 8192, 96 us, 3.0 TB/s.  With two row tiles one
 // conversion serves both, and the softmax's chain (S, 3500 cycles of softmax, PV, the next S)
 // comes to the front: 8 chunks of 512 tokens on 1 to 7680 cached ones (32/8 heads) take
-// 302 us, 786 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
+// 327 us, 726 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
 // of 16 rows do not shorten it (307 us): a 16-byte factor load takes 4 wavefronts, and with
 // half the rows a load serves half as much.  D = 256 with a softcap and a window of 1024
 // keys: 71 us, 422 TFLOP/s: shared memory (3200 wavefronts a 64-key tile: Q is read anew for
@@ -79,6 +85,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+// x rounded to 11 significant bits (to nearest even, as f16 rounds in its normal range).
+__device__ __forceinline__ float2 round11(float2 x) {
+    uint32_t a, b;
+    asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(a) : "f"(x.x));
+    asm("cvt.rn.tf32.f32 %0, %1;" : "=r"(b) : "f"(x.y));
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 // One arrival of a whole warp: its lanes' earlier writes are ordered before it.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
@@ -1020,7 +1033,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             }
                         }
                     }
-                    // P = f16(2^(y - m)), sums of 2^(y - m) / vs.  A row keeps its m while no y
+                    // P = f16(2^(y - m)), sums of it / vs.  A row keeps its m while no y
                     // exceeds it by more than the threshold (P stays at most 2^8), so its 4
                     // lanes need not agree on every tile's maximum
                     float mx[2 * HN];
@@ -1067,12 +1080,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             }
                         }
                     }
-                    float2 ls[2 * HN], nm[2 * HN];
+                    float2 nm[2 * HN];
 #pragma unroll
                     for (int x = 0; x < 2 * HN; ++x) {
                         const float mu = m[x] == -INFINITY ? 0.f : -m[x];
                         nm[x] = make_float2(mu, mu);
-                        ls[x] = make_float2(0.f, 0.f);
                     }
                     // (32 keys a time: 16 columns of P)
 #pragma unroll
@@ -1080,13 +1092,11 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         uint32_t packed[HN][8];
 #pragma unroll
                         for (int i = i0; i < i0 + 4; ++i) {
-                            const float2 iv = fb[4 * i];
 #pragma unroll
                             for (int x = 0; x < 2 * HN; ++x) {
                                 const float2 d = fadd2(y[x][i], nm[x]);
-                                const float2 p = make_float2(ex2_approx(d.x), ex2_approx(d.y));
-                                ls[x] = ffma2(p, iv, ls[x]);
-                                const __half2 hp = __floats2half2_rn(p.x, p.y);
+                                y[x][i] = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                                const __half2 hp = __floats2half2_rn(y[x][i].x, y[x][i].y);
                                 packed[x / 2][2 * (i - i0) + (x & 1)] = *reinterpret_cast<const uint32_t*>(&hp);
                             }
                         }
@@ -1094,12 +1104,23 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         for (int hf = 0; hf < HN; ++hf)
                             tc_st_16x128b_x4(p_addr + c * 32 + i0 * 4 + (static_cast<uint32_t>(hf * 16) << 16), packed[hf]);
                     }
+                    // P goes off before the sums are taken; their factors are read first, since
+                    // the tile's last P frees its table
+                    float2 iv[8];
 #pragma unroll
-                    for (int x = 0; x < 2 * HN; ++x) l[x] += ls[x].x + ls[x].y;
-                    if (C::OVER && c == 0 && (nh == 1 || it == 1)) {
+                    for (int i = 0; i < 8; ++i) iv[i] = fb[4 * i];
+                    const bool last = c == BN / 64 - 1;
+                    if ((C::OVER || last) && (nh == 1 || (it & 1))) {
                         tc_wait_st();
                         tc_fence_before();
-                        warp_arrive(bar(C::B_PH + buf), lane);
+                        warp_arrive(bar((last ? C::B_P : C::B_PH) + buf), lane);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2 * HN; ++x) {
+                        float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ls = ffma2(round11(y[x][i]), iv[i], ls);
+                        l[x] += ls.x + ls.y;
                     }
                     if constexpr (HL > HN) {
                         if (nh == 2) {   // the other half's state to the front
@@ -1118,9 +1139,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                 }
                 if (!ok) break;
-                tc_wait_st();
-                tc_fence_before();
-                warp_arrive(bar(C::B_P + buf), lane);
+                if (idle) warp_arrive(bar(C::B_P + buf), lane);
             }
             // -------------------------------------------------------- the segment's rows
             if (ok) ok = wait(bar(C::B_DONE), seg & 1, abort_flag, a.err, kErrTimeoutMma);

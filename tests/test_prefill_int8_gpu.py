@@ -220,6 +220,66 @@ def test_one_key_gives_its_value():
     assert bool(((out[0].double() - v).abs() <= (2.0 ** -11 + 8 * 2.0 ** -24) * v.abs() + 2.0 ** -25).all())
 
 
+def _two_keys(D, n, ctx, ia, ib, gap, vs_a, vs_b, seed):
+    """Every key but ia and ib has a logit of -200 or less (log2 units), ia 0 and ib `gap` times a
+    query's own factor of 0.75 to 1."""
+    case = si.make_chunked_case(1, 16, 2, D, [n], [ctx], seed=seed, page_size=16, int8=True)
+    f = 0.75 + 0.25 * torch.rand(n, 16, generator=torch.Generator().manual_seed(seed))
+    case.q.zero_()
+    case.q[:, :, 0] = f.half()
+    case.scale = 1.0 / (127 * 1.4426950408889634)
+    case.k.zero_()
+    case.k[..., 0] = 127
+    case.k_scales.fill_(-300.0)
+    for i, logit, vs in ((ia, 0.0, vs_a), (ib, gap, vs_b)):
+        page = int(case.page_table[0, i // 16])
+        case.k_scales[page, :, i % 16] = logit
+        case.v_scales[page, :, i % 16] = vs
+    return case
+
+
+def _check_two_keys(case, ia, ib, what):
+    """The weight of each key is rounded to f16 (2^-11 of itself) and their sum is taken over the
+    rounded weights, so an output is off by at most w_a w_b 2^-10 |v_a - v_b|, a few f32 roundings
+    and its own rounding."""
+    ref, ref_lse = chunk_reference(case)
+    out, lse = _run(case)
+    L, r = case.kv_lens[0], 127 * case.scale
+    w = torch.empty(case.q.shape[0], 16, 2, dtype=torch.float64)
+    v = []
+    for e, i in enumerate((ia, ib)):
+        page = int(case.page_table[0, i // 16])
+        w[..., e] = r * case.q[:, :, 0].double() * case.k_scales[page, :, i % 16].double().repeat_interleave(8)
+        v.append((case.v[page, i % 16].double() * case.v_scales[page, :, i % 16].double()[:, None]).repeat_interleave(8, 0))
+    w = torch.softmax(w, -1)
+    f32 = 2.0 ** -20   # the exponents' (6.5 log2 units in f32, ex2) and the quotient's roundings
+    tol = (2.0 ** -11 + f32) * ref.abs() + 2.0 ** -25 + \
+        ((2.0 ** -10 + f32) * w.prod(-1))[..., None] * (v[0] - v[1]).abs()[None]
+    worst = ((out.double() - ref).abs() / tol).max()
+    assert L > max(ia, ib) and float(worst) <= 1, "%s: %.3f of its tolerance" % (what, float(worst))
+    # the sum's weights are off by 2^-11 each, and log2 by a few f32 roundings
+    assert float((lse.double() - ref_lse).abs().max()) <= 2.0 ** -11 + 2.0 ** -18, what
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3, 300])
+@pytest.mark.parametrize("ib", [70, 130, 300, 391])
+def test_a_dominant_key_gives_its_value(D, n, ib):
+    # key 5 sets the running maximum, and ib lies less than 2^8 above it, so its weight is no power of two
+    case = _two_keys(D, n, 400, 5, ib, 6.5, 0.03, 0.03, seed=D + n + ib)
+    _check_two_keys(case, 5, ib, "D=%d n=%d key %d" % (D, n, ib))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 300])
+@pytest.mark.parametrize("vs", [0.0, 2.0 ** -24, -2.0 ** -24, 7 * 2.0 ** -24, 2.0 ** -18, 2.0 ** -13])
+def test_a_key_of_a_tiny_value_keeps_its_mass(D, n, vs):
+    # its weight for the values is far below the other key's, its share of the sum is not
+    for ia, ib in ((5, 6), (5, 300), (300, 5)):
+        case = _two_keys(D, n, 400, ia, ib, 0.0, vs, 0.03, seed=D + n)
+        _check_two_keys(case, ia, ib, "D=%d n=%d keys %d, %d" % (D, n, ia, ib))
+
+
 def test_invalid_page_id_reads_as_zeros_and_is_reported():
     case = si.make_chunked_case(2, 4, 2, 64, [20, 20], [100, 100], seed=31, page_size=16, int8=True)
     ref, _ = chunk_reference(case)
