@@ -43,14 +43,14 @@
 // What bounds it: shared memory.  Codes are written by TMA, read, stored at twice the size
 // and read by the MMA, so a 128-key tile of one row tile (D = 128) takes 2170 wavefronts of
 // 128 bytes (LSU 1150, MMA operands 768, TMA 256) in 2650 to 2790 cycles: 524288 cached
-// tokens of 8 kv heads and 4 new ones of 32 heads take 300 us, 3.6 TB/s (HBM alone: 161 us);
-// 1 to 8 new tokens of 32 sequences of 512 to 8192, 96 us, 3.0 TB/s.  With two row tiles one
+// tokens of 8 kv heads and 4 new ones of 32 heads take 304 us, 3.6 TB/s (HBM alone: 161 us);
+// 1 to 8 new tokens of 32 sequences of 512 to 8192, 98 us, 3.0 TB/s.  With two row tiles one
 // conversion serves both, and the softmax's chain (S, 3500 cycles of softmax, PV, the next S)
 // comes to the front: 8 chunks of 512 tokens on 1 to 7680 cached ones (32/8 heads) take
-// 327 us, 726 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
+// 319 us, 744 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
 // of 16 rows do not shorten it (307 us): a 16-byte factor load takes 4 wavefronts, and with
 // half the rows a load serves half as much.  D = 256 with a softcap and a window of 1024
-// keys: 71 us, 422 TFLOP/s: shared memory (3200 wavefronts a 64-key tile: Q is read anew for
+// keys: 70 us, 432 TFLOP/s: shared memory (3200 wavefronts a 64-key tile: Q is read anew for
 // each) and each segment's fixed part.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -356,6 +356,23 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         atomicExch(err, code);
         return false;
     };
+    // The same for a whole warp, with one answer for all of its lanes, so that a warp whose loop
+    // has warp-wide steps leaves it as a whole: a lane that gave up alone would never meet the
+    // others there.  (A vote on the answers of separate waits instead: 300 -> 316 to 326 us for 4
+    // tokens of 16 long contexts; in this form 304, and 8 chunks of 512 tokens 328 -> 319, since
+    // no lanes have to be brought together after a wait.  Slower for the softmax warps: 312.)
+    auto wait_warp = [limit](uint32_t b, uint32_t parity, volatile int* abort_flag, int* err, int code) -> bool {
+        if (__all_sync(0xffffffffu, mbar_try_wait_for(b, parity, 1000000))) return true;
+        const uint32_t t0 = globaltimer_lo();
+#pragma unroll 1
+        do {
+            if (__all_sync(0xffffffffu, mbar_try_wait_for(b, parity, 1000000))) return true;
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
+        } while (__any_sync(0xffffffffu, globaltimer_lo() - t0 < limit));
+        *abort_flag = 1;
+        atomicExch(err, code);
+        return false;
+    };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be set up meanwhile
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -612,7 +629,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const bool stall = stall_first_tile();
         uint32_t base = 0, jt = 0, u0 = 0;   // items, key tiles and units before this segment
         auto wait_all = [&](int b, uint32_t parity, int code) -> bool {
-            return __all_sync(0xffffffffu, wait(bar(b), parity & 1, abort_flag, a.err, code));
+            return wait_warp(bar(b), parity & 1, abort_flag, a.err, code);
         };
         bool ok = true;
         const Seg* w;
@@ -839,9 +856,9 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 int j;
                 const bool is_k = item_of(two, i, n, j);
                 const KeyFactors<BN>& t = tab[(jt + j) % C::NTAB];
-                ok = wait(bar(C::B_SFULL_ST + st), st_par, abort_flag, a.err, kErrTimeoutLoad);
+                ok = wait_warp(bar(C::B_SFULL_ST + st), st_par, abort_flag, a.err, kErrTimeoutLoad);
                 if (ok && !is_k)   // the signs of this tile's value scales
-                    ok = wait(bar(C::B_TAB + (jt + j) % C::NTAB), ((jt + j) / C::NTAB) & 1, abort_flag, a.err,
+                    ok = wait_warp(bar(C::B_TAB + (jt + j) % C::NTAB), ((jt + j) / C::NTAB) & 1, abort_flag, a.err,
                               kErrTimeoutLoad);
                 if (!ok) break;
                 const uint8_t* src = smem + C::OFF_CODE + st * C::CODE_BYTES;
@@ -857,7 +874,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     sg[g] = is_k ? 0x3c003c00u : t.sign[row0 + g * 8];
                 }
                 // (a fresh barrier's "phase before" counts as complete: the first RING waits pass)
-                ok = wait(bar(C::B_OPEMPTY + slot), slot_par, abort_flag, a.err, kErrTimeoutMma);
+                ok = wait_warp(bar(C::B_OPEMPTY + slot), slot_par, abort_flag, a.err, kErrTimeoutMma);
                 if (!ok) break;
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g) {

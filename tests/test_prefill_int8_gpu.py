@@ -356,6 +356,26 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(D, n):
     _check(case, "after a timeout, D=%d n=%d" % (D, n))
 
 
+@pytest.mark.parametrize("limit_ns", [20_000, 300_000, 5_000_000])
+def test_waits_that_run_out_anywhere_end_every_role(limit_ns):
+    # with limits this short any role's wait may be the first to run out, in any segment; every warp
+    # still leaves its loops as a whole, and the next call is right
+    cases = [si.make_chunked_case(3, 2 * Hkv, Hkv, D, [n, 1, 40], [900, 3000, 70], seed=n + D, page_size=16, int8=True)
+             for D, Hkv, n in ((64, 3, 200), (128, 2, 5), (128, 8, 300), (256, 2, 90))]
+    g = [c.to("cuda") for c in cases]
+    for _ in range(3):
+        assert attn.attn_testing_set_waits(limit_ns, 1) == attn.ATTN_OK
+        try:
+            for x in g:
+                attn.prefill_paged(x)
+            status = attn.attn_device_status()
+        finally:
+            assert attn.attn_testing_set_waits(0, 0) == attn.ATTN_OK
+        assert status == attn.ATTN_ETIMEOUT
+    for c in cases:
+        _check(c, "after short limits, D=%d" % c.head_dim)
+
+
 TRACED = """
 import torch
 import attention_split_kv_gb300 as attn
