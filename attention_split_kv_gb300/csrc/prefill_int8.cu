@@ -1447,7 +1447,8 @@ attn_status launch(const Prefill8Launch& L, const Plan& p) {
     a.softcap = L.softcap;
     // The CTAs of one run take its hp heads side by side, so that they read neighbouring
     // rows of the same pages at the same time.  hp: the count that leaves the fewest CTAs
-    // without work (152 CTAs: 8 heads as 19 x 8, 7 as 21 x 7, 100 in 2 batches as 3 x 50)
+    // without work (152 CTAs: 8 heads as 19 x 8, 16 as the same in 2 batches, 100 in 2 batches as
+    // 3 x 50; 7 one after the other, since 21 x 7 would leave 5 CTAs idle)
     const int sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     const int heads = L.Hkv * p.n_hg;
     double best = 0.;

@@ -280,6 +280,22 @@ def test_a_key_of_a_tiny_value_keeps_its_mass(D, n, vs):
         _check_two_keys(case, ia, ib, "D=%d n=%d keys %d, %d" % (D, n, ia, ib))
 
 
+@pytest.mark.parametrize("Hkv", [7, 9, 12, 13, 16, 20])
+def test_heads_in_several_batches(Hkv):
+    # head counts that 152 CTAs take in 2 to 13 batches; runs that end inside items of any of them
+    case = si.make_chunked_case(3, 2 * Hkv, Hkv, 64, [3, 70, 1], [2500, 300, 0], seed=Hkv, page_size=16, int8=True)
+    _check(case, "Hkv=%d" % Hkv)
+    case = si.make_chunked_case(2, Hkv, Hkv, 128, [300, 1], [1500, 6000], seed=Hkv, page_size=32, window=900, int8=True)
+    _check(case, "Hkv=%d, two row tiles" % Hkv)
+
+
+@pytest.mark.parametrize("Hkv,G,D", [(153, 1, 64), (160, 1, 64), (305, 2, 64), (20, 130, 64), (13, 1, 256),
+                                     (153, 1, 256)])
+def test_more_heads_than_ctas_and_a_partial_last_batch(Hkv, G, D):
+    case = si.make_chunked_case(2, G * Hkv, Hkv, D, [5, 1], [200, 700], seed=Hkv, page_size=16, int8=True)
+    _check(case, "Hkv=%d G=%d D=%d" % (Hkv, G, D))
+
+
 def test_invalid_page_id_reads_as_zeros_and_is_reported():
     case = si.make_chunked_case(2, 4, 2, 64, [20, 20], [100, 100], seed=31, page_size=16, int8=True)
     ref, _ = chunk_reference(case)
