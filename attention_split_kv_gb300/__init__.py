@@ -132,6 +132,26 @@ def _stream(s) -> Optional[int]:
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, scratch=False):
+    """torch.empty for a call on ``stream``.  Memory that torch hands out belongs to its
+    current stream: what that stream freed may still be in use there, and what a call drops
+    may be handed out again at once.  So with another stream the memory is that stream's
+    own, and what the caller gets back (not ``scratch``) is kept for the current one too."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if _stream(stream) == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    if not scratch:
+        x.record_stream(current)
+    return x
+
+
 def _check(status: int):
     if status != ATTN_OK:
         raise AttnError(status, load().attn_last_error().decode())
@@ -217,12 +237,12 @@ def decode_tiered(case, out=None, lse_out=None, workspace=None, split_keys: int 
     dev = case.q.device
     B, Hq, Hkv, D = case.batch, case.n_heads, case.n_kv_heads, case.head_dim
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32 if out_f32 else torch.float16, device=dev)
+        out = _empty((B, Hq, D), torch.float32 if out_f32 else torch.float16, dev, stream)
     ws_bytes = attn_decode_tiered_workspace_size(B, Hq, Hkv, D, case.cap, case.hot_ring, split_keys)
     if ws_bytes == 0:
         raise AttnError(ATTN_EINVAL, "invalid sizes for the tiered decode workspace")
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream, scratch=True)
     attn_decode_tiered(case.q, _dtype_of(case.q), case.k, case.v, case.k_scales, case.v_scales,
                        ATTN_KV_INT8 if case.int8 else ATTN_KV_F16, case.kv_len, case.page_table, case.page_size,
                        case.max_pages, case.n_pages, case.cap, case.hot_k, case.hot_v, case.hot_len,
@@ -286,12 +306,12 @@ def decode(case, out=None, lse_out=None, workspace=None, split_keys: int = 0, ma
     if max_kv is None:
         max_kv = ring if ring else case.cap
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32 if out_f32 else torch.float16, device=dev)
+        out = _empty((B, Hq, D), torch.float32 if out_f32 else torch.float16, dev, stream)
     ws_bytes = attn_decode_workspace_size(B, Hq, Hkv, D, max_kv, split_keys)
     if ws_bytes == 0:
         raise AttnError(ATTN_EINVAL, "invalid sizes for the decode workspace")
     if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream, scratch=True)
     qt, ot = _dtype_of(case.q), _dtype_of(out)
     if qt != ATTN_F16 or ot != ATTN_F16:
         attn_decode_ex(case.q, qt, case.k, case.v, case.kv_len, case.page_table, case.page_size, case.max_pages,
@@ -313,9 +333,8 @@ def decode(case, out=None, lse_out=None, workspace=None, split_keys: int = 0, ma
 
 def prefill(case, out=None, lse_out=None, stream=None):
     """attn_prefill on a PrefillCase-like object (tensors already on the GPU)."""
-    import torch
     if out is None:
-        out = torch.empty_like(case.q)
+        out = _empty(case.q.shape, case.q.dtype, case.q.device, stream)
     attn_prefill(case.q, case.k, case.v, case.seq_len, case.n_heads, case.n_kv_heads, case.head_dim,
                  case.causal, case.window, case.softcap, case.scale, out, lse_out, stream)
     return out
@@ -374,14 +393,14 @@ def prefill_paged(case, out=None, lse_out=None, stream=None, workspace=None):
     attn_prefill_paged_ex over int8 pages when its cache holds int8 codes."""
     import torch
     if out is None:
-        out = torch.empty_like(case.q)
+        out = _empty(case.q.shape, case.q.dtype, case.q.device, stream)
     if case.k.dtype == torch.int8:
         if workspace is None:
             size = attn_prefill_paged_workspace_size(case.batch, case.max_q, case.n_heads, case.n_kv_heads,
                                                      case.head_dim, ATTN_KV_INT8)
             if size == 0:
                 raise AttnError(ATTN_EINVAL, "invalid sizes for the chunked prefill workspace")
-            workspace = torch.empty(size, dtype=torch.uint8, device=case.q.device)
+            workspace = _empty(size, torch.uint8, case.q.device, stream, scratch=True)
         attn_prefill_paged_ex(case.q, case.k, case.v, case.q_start, case.kv_len, case.page_table, case.page_size,
                               case.max_pages, int(case.k.shape[0]), case.k_scales, case.v_scales, ATTN_KV_INT8,
                               case.batch, case.total_q, case.max_q, case.n_heads, case.n_kv_heads, case.head_dim,
@@ -429,7 +448,7 @@ def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_e
     int8 = case.k.dtype == torch.int8
     P, max_pages, n_pages, max_kv, ring = _cache_args(case)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        q_out = _empty(q.shape, torch.float16, q.device, stream)
     rows = 0 if rope_cos is None else rope_cos.shape[0]
     rot = 0 if rope_cos is None else 2 * rope_cos.shape[1]
     attn_append(q, k, v, _dtype_of(k), stride(q), stride(k), stride(v), q_norm, k_norm, norm_eps, norm_offset,
@@ -451,7 +470,7 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
     P, max_pages, n_pages, max_kv, ring = _cache_args(case)
     shape = (total, case.n_kv_heads, case.head_dim)
     dt = torch.float32 if out_f32 else torch.float16
-    k, v = torch.empty(shape, dtype=dt, device=case.k.device), torch.empty(shape, dtype=dt, device=case.k.device)
+    k, v = (_empty(shape, dt, case.k.device, stream) for _ in range(2))
     attn_kv_read(case.k, case.v, case.kv_len if kv_len is None else kv_len, first, out_start, case.page_table, P,
                  max_pages, n_pages, max_kv, ring, case.k_scales if int8 else None, case.v_scales if int8 else None,
                  ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, total, case.n_kv_heads, case.head_dim, k, v,
