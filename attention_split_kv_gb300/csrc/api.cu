@@ -677,6 +677,10 @@ attn_status attn_append(const void* q, const void* k, const void* v, attn_dtype 
         !aligned(k_norm, 16) || (rope_dim > 0 && (!aligned(rope_cos, 16) || !aligned(rope_sin, 16))))
         return set_error(ATTN_EINVAL, "%s: q, k, v, q_out, norm weights and tables must be 16-byte aligned", fn);
     if (total_q == 0) return ATTN_OK;
+    // rows are written where they were read, or beside all of them
+    if (q && q == q_out &&
+        (in_dtype != q_out_dtype || (total_q > 1 && q_stride != static_cast<long long>(n_heads) * head_dim)))
+        return set_error(ATTN_EINVAL, "%s: q_out may be q only if q has its type and packed rows", fn);
     int* err = device_error_word();
     if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
     a.q = q;

@@ -417,8 +417,9 @@ attn_status attn_prefill_paged_ex(const void* q, const void* k_cache, const void
  *                and rounding are exact, so without norm and rotation the codes are
  *                those of the definition bit for bit.  A head with an infinity or a
  *                NaN gets it as its scale and reads back as NaN.
- *  q_out       device, q_out_dtype, [total_q, Hq, D].  It may be q itself where type
- *                and stride agree.
+ *  q_out       device, q_out_dtype, [total_q, Hq, D].  It may be q itself where the
+ *                type agrees and q's rows are packed too (q_stride Hq * D, or one row;
+ *                else ATTN_EINVAL).  Otherwise it must not overlap q, k or v.
  *  All arithmetic is f32, with one rounding at the end.  A row whose position is
  *  negative is no token (a padded batch's sequence of kv_len 0) and is left out:
  *  neither q_out nor the cache is written.  So is a token at or above the cache's

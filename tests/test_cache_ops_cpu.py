@@ -134,6 +134,22 @@ def test_chunk_refuses_on_host(kw, status):
     _refused(attn.attn_prefill_paged_ex, CHUNK, kw, status)
 
 
+@pytest.mark.parametrize("kw", [dict(q_stride=512), dict(q_stride=256, k_stride=512, q_out_dtype=attn.ATTN_F32),
+                                dict(q_stride=256, in_dtype=attn.ATTN_F32), dict(total_q=1, q_out_dtype=attn.ATTN_F32)],
+                         ids=str)
+def test_the_entry_point_refuses_q_out_over_other_rows(kw):
+    _refused(attn.attn_append, APPEND, {**dict(q=1 << 21, q_out=1 << 21), **kw}, attn.ATTN_EINVAL)
+
+
+@pytest.mark.parametrize("kw", [dict(q_stride=256), dict(total_q=1, q_stride=512), dict(q_out=1 << 22, q_stride=512)],
+                         ids=str)
+def test_the_entry_point_takes_q_out_over_the_rows_it_read(kw):
+    if torch.cuda.is_available():
+        pytest.skip("would launch on made-up addresses")
+    # every check passes: what remains is the missing GPU
+    _refused(attn.attn_append, APPEND, {**dict(q=1 << 21, q_out=1 << 21), **kw}, attn.ATTN_ECUDA)
+
+
 def test_no_rows_is_a_call_that_does_nothing():
     attn.attn_append(**{**APPEND, "total_q": 0})
     attn.attn_kv_read(**{**READ, "total": 0})
