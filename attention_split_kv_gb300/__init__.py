@@ -395,6 +395,14 @@ def prefill_paged(case, out=None, lse_out=None, stream=None, workspace=None):
     if out is None:
         out = _empty(case.q.shape, case.q.dtype, case.q.device, stream)
     if case.k.dtype == torch.int8:
+        _cache_args(case)
+        _lengths(case, None, q_start=case.q_start)
+        rows = case.total_q * case.n_heads
+        for what, x, dtype, n in (("q", case.q, torch.float16, rows * case.head_dim),
+                                  ("out", out, torch.float16, rows * case.head_dim),
+                                  ("lse_out", lse_out, torch.float32, rows)):
+            if x is not None:
+                _dense(what, x, dtype, case.k, least=n)
         if workspace is None:
             size = attn_prefill_paged_workspace_size(case.batch, case.max_q, case.n_heads, case.n_kv_heads,
                                                      case.head_dim, ATTN_KV_INT8)
@@ -413,17 +421,57 @@ def prefill_paged(case, out=None, lse_out=None, stream=None, workspace=None):
     return out
 
 
+def _need(ok, message, *values):
+    if not ok:
+        raise AttnError(ATTN_EINVAL, message % values)
+
+
+def _dense(what, x, dtype, like, shape=None, least=0):
+    """A contiguous tensor of dtype beside the cache ``like``, of the given shape or with at least
+    ``least`` elements: the kernels address all of them from their first element."""
+    _need(x.dtype == dtype and x.is_contiguous(), "%s must be a contiguous %s tensor", what, dtype)
+    _need(x.device == like.device, "%s must be on the cache's device", what)
+    if shape is not None:
+        _need(tuple(x.shape) == shape, "%s must have the shape %s, not %s", what, shape, tuple(x.shape))
+    _need(x.numel() >= least, "%s must have at least %d elements", what, least)
+
+
 def _cache_args(case):
-    """page_size, max_pages, n_pages, max_kv and ring_size of a DecodeCase- or ChunkCase-like cache."""
-    ring = int(getattr(case, "ring", 0) or 0)
+    """page_size, max_pages, n_pages, max_kv and ring_size of a DecodeCase- or ChunkCase-like
+    cache, whose tensors agree with its sizes."""
+    import torch
+    k, B, ring = case.k, int(case.batch), int(getattr(case, "ring", 0) or 0)
+    _need(k.dim() == 4 and k.dtype in (torch.float16, torch.int8),
+          "the cache must be a float16 or int8 tensor [B or pages, tokens, Hkv, D]")
+    slots, rows, Hkv, D = k.shape
+    _need((Hkv, D) == (case.n_kv_heads, case.head_dim),
+          "the cache's heads must be n_kv_heads of head_dim, not %d of %d", Hkv, D)
+    _dense("k", k, k.dtype, k)
+    _dense("v", case.v, k.dtype, k, (slots, rows, Hkv, D))
+    if k.dtype == torch.int8:
+        for what in ("k_scales", "v_scales"):
+            x = getattr(case, what)
+            _need(x is not None, "an int8 cache needs %s", what)
+            _dense(what, x, torch.float16, k, (slots, Hkv, rows))
     if case.page_table is not None:
-        return int(case.page_size), int(case.max_pages), int(case.k.shape[0]), 0, 0
-    return 0, 0, 0, 0 if ring else int(case.k.shape[1]), ring
+        _need(int(case.page_size) == rows, "page_size must be the pages' tokens (%d)", rows)
+        _dense("page_table", case.page_table, torch.int32, k, least=B * int(case.max_pages))
+        _need(case.page_table.shape[-1] == int(case.max_pages), "page_table must have max_pages columns")
+        return rows, int(case.max_pages), slots, 0, 0
+    _need(slots >= B, "the cache must hold a slot for each of %d sequences", B)
+    _need(ring in (0, rows), "ring must be the cache's tokens (%d)", rows)
+    return 0, 0, 0, 0 if ring else rows, ring
 
 
-def _dense(what, x, dtype):
-    if x is not None and (x.dtype != dtype or not x.is_contiguous()):
-        raise AttnError(ATTN_EINVAL, "%s must be a contiguous %s tensor" % (what, dtype))
+def _lengths(case, kv_len, **others):
+    """The per-sequence lengths and starts of a call; returns kv_len (default: the case's)."""
+    import torch
+    kv_len = case.kv_len if kv_len is None else kv_len
+    _dense("kv_len", kv_len, torch.int32, case.k, least=case.batch)
+    for what, x in others.items():
+        if x is not None:
+            _dense(what, x, torch.int32, case.k, least=case.batch + (what != "first"))
+    return kv_len
 
 
 def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_eps=1e-6, norm_offset=0.0,
@@ -431,28 +479,42 @@ def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_e
     """attn_append of packed token rows (q [T, Hq, D] or None; k, v [T, Hkv, D], f16
     or f32, the heads of a token together) to the cache that a DecodeCase- or
     ChunkCase-like object holds; ``kv_len`` (default: the case's) counts each
-    sequence's tokens with the new ones.  Returns q_out (f16 unless given)."""
+    sequence's tokens with the new ones.  Returns q_out (f16 unless given; it may be q
+    where q is contiguous and of its type)."""
     import torch
+    P, max_pages, n_pages, max_kv, ring = _cache_args(case)
+    int8 = case.k.dtype == torch.int8
+    D = case.k.shape[3]
+    _need(k.dim() == 3 and k.shape[1:] == case.k.shape[2:], "k must be [T, Hkv, D] rows of the cache's heads")
+    _need(v.shape == k.shape, "v must have k's shape")
+    _need(q is None or (q.dim() == 3 and q.shape[0] == k.shape[0] and q.shape[2] == D),
+          "q must be [T, Hq, D] with k's T and D")
 
     def stride(x):
         if x is None:
             return 0
-        if x.dtype != k.dtype or x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+        if x.dtype != k.dtype or x.stride(2) != 1 or x.stride(1) != D:
             raise AttnError(ATTN_EINVAL, "q, k and v rows must have one type and their heads side by side")
-        return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+        _need(x.device == case.k.device, "q, k and v must be on the cache's device")
+        return x.stride(0) if x.shape[0] > 1 else x.shape[1] * D
 
-    for what, x in (("q_norm", q_norm), ("k_norm", k_norm), ("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-        _dense(what, x, torch.float32)
-    for what, x in (("q_start", q_start), ("kv_len", kv_len)):
-        _dense(what, x, torch.int32)
-    int8 = case.k.dtype == torch.int8
-    P, max_pages, n_pages, max_kv, ring = _cache_args(case)
+    kv_len = _lengths(case, kv_len, q_start=q_start)
+    for what, x in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if x is not None:
+            _dense(what, x, torch.float32, case.k, (D,))
+    _need((rope_cos is None) == (rope_sin is None), "rope_cos and rope_sin go together")
+    if rope_cos is not None:
+        _need(rope_cos.dim() == 2, "rope_cos must be [positions, rope_dim / 2]")
+        _dense("rope_cos", rope_cos, torch.float32, case.k)
+        _dense("rope_sin", rope_sin, torch.float32, case.k, tuple(rope_cos.shape))
+    if q is not None and q_out is not None:
+        _dense("q_out", q_out, q_out.dtype, case.k, tuple(q.shape))
     if q is not None and q_out is None:
         q_out = _empty(q.shape, torch.float16, q.device, stream)
     rows = 0 if rope_cos is None else rope_cos.shape[0]
     rot = 0 if rope_cos is None else 2 * rope_cos.shape[1]
     attn_append(q, k, v, _dtype_of(k), stride(q), stride(k), stride(v), q_norm, k_norm, norm_eps, norm_offset,
-                rope_cos, rope_sin, rows, rot, rope_interleaved, q_start, case.kv_len if kv_len is None else kv_len,
+                rope_cos, rope_sin, rows, rot, rope_interleaved, q_start, kv_len,
                 case.k, case.v, case.page_table, P, max_pages, n_pages, max_kv, ring,
                 case.k_scales if int8 else None, case.v_scales if int8 else None,
                 ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, k.shape[0], 0 if q is None else q.shape[1],
@@ -464,14 +526,13 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
     """attn_kv_read of a DecodeCase- or ChunkCase-like object's cache: (k, v) rows
     [total, Hkv, D], f16 or f32; rows past out_start[B] are not written."""
     import torch
-    for what, x in (("out_start", out_start), ("first", first), ("kv_len", kv_len)):
-        _dense(what, x, torch.int32)
-    int8 = case.k.dtype == torch.int8
     P, max_pages, n_pages, max_kv, ring = _cache_args(case)
+    int8 = case.k.dtype == torch.int8
+    kv_len = _lengths(case, kv_len, out_start=out_start, first=first)
     shape = (total, case.n_kv_heads, case.head_dim)
     dt = torch.float32 if out_f32 else torch.float16
     k, v = (_empty(shape, dt, case.k.device, stream) for _ in range(2))
-    attn_kv_read(case.k, case.v, case.kv_len if kv_len is None else kv_len, first, out_start, case.page_table, P,
+    attn_kv_read(case.k, case.v, kv_len, first, out_start, case.page_table, P,
                  max_pages, n_pages, max_kv, ring, case.k_scales if int8 else None, case.v_scales if int8 else None,
                  ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, total, case.n_kv_heads, case.head_dim, k, v,
                  _dtype_of(k), stream)
