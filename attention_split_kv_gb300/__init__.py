@@ -394,6 +394,8 @@ def prefill_paged(case, out=None, lse_out=None, stream=None, workspace=None):
     import torch
     if out is None:
         out = _empty(case.q.shape, case.q.dtype, case.q.device, stream)
+    if case.total_q == 0 or case.max_q == 0:   # (empty tensors have no address to pass on)
+        return out
     if case.k.dtype == torch.int8:
         _cache_args(case)
         _lengths(case, None, q_start=case.q_start)
@@ -511,6 +513,8 @@ def append(case, q, k, v, q_start, kv_len=None, q_norm=None, k_norm=None, norm_e
         _dense("q_out", q_out, q_out.dtype, case.k, tuple(q.shape))
     if q is not None and q_out is None:
         q_out = _empty(q.shape, torch.float16, q.device, stream)
+    if k.shape[0] == 0:
+        return q_out
     rows = 0 if rope_cos is None else rope_cos.shape[0]
     rot = 0 if rope_cos is None else 2 * rope_cos.shape[1]
     attn_append(q, k, v, _dtype_of(k), stride(q), stride(k), stride(v), q_norm, k_norm, norm_eps, norm_offset,
@@ -532,6 +536,8 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
     shape = (total, case.n_kv_heads, case.head_dim)
     dt = torch.float32 if out_f32 else torch.float16
     k, v = (_empty(shape, dt, case.k.device, stream) for _ in range(2))
+    if total == 0:
+        return k, v
     attn_kv_read(case.k, case.v, kv_len, first, out_start, case.page_table, P,
                  max_pages, n_pages, max_kv, ring, case.k_scales if int8 else None, case.v_scales if int8 else None,
                  ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, total, case.n_kv_heads, case.head_dim, k, v,

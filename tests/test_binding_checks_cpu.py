@@ -135,3 +135,25 @@ def test_int8_chunks_refuse_tensors_that_do_not_agree(kw, called):
     _refuses(lambda: attn.prefill_paged(case, lse_out=_f16(11, 4)), called)
     case.__dict__.update(kw)
     _refuses(lambda: attn.prefill_paged(case), called)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("max_q", [0, 7])
+def test_a_step_without_new_tokens_does_nothing(int8, max_q, monkeypatch):
+    # a server's step in which no sequence has a new token, with max_q as counted or as a fixed bound
+    monkeypatch.undo()
+    attn.build()
+    case = si.make_chunked_case(2, 4, 2, 64, [0, 0], [9, 30], seed=1, page_size=16, int8=int8)
+    case.max_q = max_q
+    out, lse = _f16(3, 4, 64) + 5, torch.full((3, 4), 5.0)
+    assert attn.prefill_paged(case).shape == (0, 4, 64)
+    assert attn.prefill_paged(case, out=out, lse_out=lse) is out
+    assert bool((out == 5).all()) and bool((lse == 5).all())
+    for layout in CACHES:
+        cache = Cache(B=2, Hkv=2, D=64, cap=40, int8=int8, **layout)
+        q, k = _f16(0, 4, 64), _f16(0, 2, 64)
+        got = attn.append(cache, q, k, k, _i32(3), _i32(2), rope_cos=tables(40, 64)[0], rope_sin=tables(40, 64)[1])
+        assert got.shape == (0, 4, 64) and got.dtype == torch.float16
+        assert attn.append(cache, None, k, k, _i32(3), _i32(2)) is None
+        k, v = attn.kv_read(cache, _i32(3), 0, kv_len=_i32(2), out_f32=True)
+        assert k.shape == v.shape == (0, 2, 64) and k.dtype == torch.float32
