@@ -144,7 +144,7 @@ def test_a_step_without_new_tokens_does_nothing(int8, max_q, monkeypatch):
     monkeypatch.undo()
     attn.build()
     case = si.make_chunked_case(2, 4, 2, 64, [0, 0], [9, 30], seed=1, page_size=16, int8=int8)
-    case.max_q = max_q
+    case.q, case.max_q = _f16(0, 4, 64), max_q
     out, lse = _f16(3, 4, 64) + 5, torch.full((3, 4), 5.0)
     assert attn.prefill_paged(case).shape == (0, 4, 64)
     assert attn.prefill_paged(case, out=out, lse_out=lse) is out
