@@ -805,6 +805,9 @@ attn_status attn_device_status(void* stream) {
         return set_error(ATTN_ECUDA, "attn_device_status: %s", cudaGetErrorString(cudaGetLastError()));
     if (v == kErrBadPage)
         return set_error(ATTN_EBOUNDS, "attn_decode read a page id outside the pool (page 0 was used instead)");
+    if (v == kErrChunkPage)
+        return set_error(ATTN_EBOUNDS, "attn_prefill_paged or attn_prefill_paged_ex met a page id outside the pool (its "
+                                       "keys and values were read as zeros)");
     if (v == kErrCachePage)
         return set_error(ATTN_EBOUNDS, "attn_append or attn_kv_read met a page id outside the pool (the token was not "
                                        "written, or read as zeros)");

@@ -18,9 +18,10 @@ enum : int {
     kErrTimeoutSlot = 2,     // the producer waited too long for a free slot
     kErrTimeoutMma = 3,      // a wait on a tensor-core result timed out
     kErrTimeoutSoftmax = 4,  // the MMA issuer waited too long for P
-    kErrBadPage = 5,         // a page-table entry in use was outside the page pool
+    kErrBadPage = 5,         // a page-table entry in use was outside the page pool (decode)
     kErrCachePage = 6,       // the same, met by attn_append or attn_kv_read
     kErrAppendRange = 7,     // a new token's position outside the cache or the cos/sin tables
+    kErrChunkPage = 8,       // a page-table entry in use outside the pool, met by attn_prefill_paged(_ex)
 };
 
 // Records a message for attn_last_error() (thread-local) and returns `st`.

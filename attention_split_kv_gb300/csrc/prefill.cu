@@ -362,7 +362,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                             int page = args.n_pages, row = 0;
                             if (kk < L) {
                                 if (pg >= 0 && pg < args.n_pages) page = pg;
-                                else atomicExch(args.err, kErrBadPage);   // never read: reported
+                                else atomicExch(args.err, kErrChunkPage);   // never read: reported
                                 row = kk & (args.P - 1);
                             }
                             for (int c = 0; c < NCH; ++c)

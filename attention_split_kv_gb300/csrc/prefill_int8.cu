@@ -589,7 +589,7 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                             page = pg;
                             row = kk & (a.P - 1);
                         } else {
-                            atomicExch(a.err, kErrBadPage);
+                            atomicExch(a.err, kErrChunkPage);
                         }
                     }
                     if (leader) {

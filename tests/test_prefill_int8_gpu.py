@@ -317,6 +317,16 @@ def test_invalid_page_id_reads_as_zeros_and_is_reported():
     assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
 
 
+@pytest.mark.parametrize("int8", [False, True])
+def test_an_invalid_page_is_reported_as_the_chunk_call_s(int8):
+    case = si.make_chunked_case(1, 4, 2, 64, [20], [100], seed=31, page_size=16, int8=int8)
+    case.page_table[0, 2] = -5
+    attn.prefill_paged(case.to("cuda"))
+    assert attn.attn_device_status() == attn.ATTN_EBOUNDS
+    message = attn.attn_last_error()
+    assert "attn_prefill_paged" in message and "zeros" in message and "attn_decode" not in message
+
+
 @pytest.mark.parametrize("D", [64, 256])
 def test_f16_caches_are_attn_prefill_paged_bit_for_bit(D):
     case = si.make_chunked_case(2, 4, 2, D, [64, 130], [200, 3], seed=D, page_size=16).to("cuda")
