@@ -788,6 +788,9 @@ attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_tabl
 attn_status attn_testing_set_waits(unsigned long long wait_limit_ns, int stall_first_tile) {
     if (stall_first_tile != 0 && stall_first_tile != 1)
         return set_error(ATTN_EINVAL, "attn_testing_set_waits: stall_first_tile must be 0 or 1");
+    // (the int8 chunk kernel times its waits in 32 bits of nanoseconds)
+    if (wait_limit_ns > 4000000000ull)
+        return set_error(ATTN_EINVAL, "attn_testing_set_waits: wait_limit_ns must be at most 4000000000 (the default)");
     const unsigned long long limit = wait_limit_ns ? wait_limit_ns : 4000000000ull;
     attn_status st = set_test_controls_prefill(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_decode(limit, stall_first_tile);

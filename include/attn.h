@@ -498,8 +498,8 @@ attn_status attn_device_status(void* stream);
  * leaves its loop, waits (with the full limit) for its own copies and
  * tensor-core work already in flight, frees its tensor memory and returns.
  *
- *  wait_limit_ns     the time limit of pipeline waits in ns; 0 restores the
- *                      default (4 s).  Waits for work already in flight keep
+ *  wait_limit_ns     the time limit of pipeline waits in ns, at most the default
+ *                      (4 s), which 0 restores.  Waits for work already in flight keep
  *                      the default.
  *  stall_first_tile  1: from now on every CTA of the prefill and tensor-core
  *                      decode kernels holds back the signal that its first
@@ -508,7 +508,8 @@ attn_status attn_device_status(void* stream);
  *                      the call's output is invalid and attn_device_status
  *                      then returns ATTN_ETIMEOUT.  0: normal operation.
  *  The settings apply to the current device and to every later launch; the
- *  call is synchronous.  Returns ATTN_EINVAL for another stall value.
+ *  call is synchronous.  Returns ATTN_EINVAL for a longer limit or another stall
+ *  value.
  */
 attn_status attn_testing_set_waits(unsigned long long wait_limit_ns, int stall_first_tile);
 

@@ -262,3 +262,10 @@ def test_prefill_paged_rejects_bad_arguments_on_the_host(lib, kw, status):
 def test_prefill_paged_with_no_queries_is_a_no_op(lib):
     assert _prefill_paged(total_q=0) == attn.ATTN_OK
     assert _prefill_paged(max_q=0) == attn.ATTN_OK
+
+
+@pytest.mark.parametrize("limit", [4_000_000_001, 1 << 32, (1 << 32) + 20_000_000, (1 << 64) - 1])
+def test_wait_limits_above_the_default_are_refused(lib, limit):
+    # a limit of 2^32 ns or more would never run out in a kernel that counts 32 bits of them
+    assert attn.attn_testing_set_waits(limit, 0) == attn.ATTN_EINVAL
+    assert "wait_limit_ns" in attn.attn_last_error()
