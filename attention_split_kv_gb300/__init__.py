@@ -123,9 +123,9 @@ def _ptr(x) -> Optional[int]:
 def _stream(s) -> Optional[int]:
     if s is None:
         import torch
-        if torch.cuda.is_initialized():
-            # torch.cuda.current_stream().cuda_stream without its Stream object (2.8 us)
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if raw and device and torch.cuda.is_initialized():
+            return raw(device())   # without a Stream object, which takes 2.8 us
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s

@@ -157,3 +157,16 @@ def test_a_step_without_new_tokens_does_nothing(int8, max_q, monkeypatch):
         assert attn.append(cache, None, k, k, _i32(3), _i32(2)) is None
         k, v = attn.kv_read(cache, _i32(3), 0, kv_len=_i32(2), out_f32=True)
         assert k.shape == v.shape == (0, 2, 64) and k.dtype == torch.float32
+
+
+@pytest.mark.parametrize("missing", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_the_current_stream_without_torch_s_short_cut(missing, monkeypatch):
+    # torch's own way to a raw stream is used where it is there, and not needed
+    class Now:
+        cuda_stream = 12345
+
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Now)
+    monkeypatch.delattr(torch._C, missing, raising=False)
+    assert attn._stream(None) == 12345
+    assert attn._stream(77) == 77 and attn._stream(Now) == 12345
