@@ -356,6 +356,33 @@ def test_read_offsets_past_32_bits():
     assert torch.equal(g.k[0, -3:].cpu(), c) and int(g.k[0, :-3].abs().max()) == 0
 
 
+@pytest.mark.parametrize("layout", ["plain", "paged"])
+def test_append_and_read_past_unsigned_32_bits(layout):
+    # 4.3e9 codes of one sequence: the last tokens' offsets have more than 32 bits, signed or not
+    Hkv, D, cap, P = 8, 256, (1 << 21) + 64, 64
+    n = cap * Hkv * D
+    assert (cap - 3) * Hkv * D > 1 << 32
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("needs 17 GB free")
+    g = Cache("plain", 1, Hkv, D, 8, int8=True)
+    shape = (1, cap, Hkv, D)
+    if layout == "paged":
+        shape = (cap // P, P, Hkv, D)
+        g.page_size, g.max_pages = P, cap // P
+        g.page_table = torch.arange(cap // P, dtype=torch.int32, device="cuda").view(1, -1)
+    g.k, g.v = (torch.zeros(shape, dtype=torch.int8, device="cuda") for _ in range(2))
+    g.k_scales, g.v_scales = (torch.zeros((shape[0], Hkv, shape[1]), dtype=torch.float16, device="cuda") for _ in range(2))
+    x, y = (si.f16_normal((3, Hkv, D), s).cuda() for s in (8, 9))
+    start, kv = torch.tensor([0, 3], dtype=torch.int32).cuda(), torch.tensor([cap], dtype=torch.int32).cuda()
+    attn.append(g, None, x, y, start, kv)
+    k, v = attn.kv_read(g, start, 3, first=kv - 3, kv_len=kv)
+    for got, cache, z in ((k, g.k, x), (v, g.v, y)):
+        c, s = si.quantize_int8_rows(z.cpu())
+        assert torch.equal(got.cpu(), (c.float() * s.float()[..., None]).half())
+        flat = cache.view(cap, Hkv, D)
+        assert torch.equal(flat[-3:].cpu(), c) and not bool(flat[:-3].any())
+
+
 # ------------------------------------------------------------------ together
 def _serve(stream_of=lambda: None):
     """A prompt chunk, then three decode tokens, appended to int8 pages and attended;

@@ -317,6 +317,25 @@ def test_invalid_page_id_reads_as_zeros_and_is_reported():
     assert mx <= INT8_MAX_ABS and rel <= INT8_REL_L2
 
 
+def test_pages_past_unsigned_32_bits():
+    # the last pages of a pool of 4.3e9 codes give what the same pages give in a small pool
+    Hkv, D, P = 8, 256, 64
+    case = si.make_chunked_case(2, 16, Hkv, D, [5, 70], [300, 100], seed=3, page_size=P, int8=True)
+    small, n = case.to("cuda"), case.k.shape[0]
+    want = attn.prefill_paged(small)
+    pages = (1 << 32) // (P * Hkv * D) + n
+    if torch.cuda.mem_get_info()[0] < 2 * pages * P * Hkv * D + (8 << 30):
+        pytest.skip("needs 17 GB free")
+    big = case.to("cuda")
+    for name in ("k", "v", "k_scales", "v_scales"):
+        x = getattr(small, name)
+        pool = torch.zeros((pages,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda")
+        pool[pages - n:] = x
+        setattr(big, name, pool)
+    big.page_table = torch.where(small.page_table >= 0, small.page_table + (pages - n), small.page_table)
+    assert torch.equal(attn.prefill_paged(big), want)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_an_invalid_page_is_reported_as_the_chunk_call_s(int8):
     case = si.make_chunked_case(1, 4, 2, 64, [20], [100], seed=31, page_size=16, int8=int8)
