@@ -721,9 +721,8 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     segs[e] = walk;
                     if (known == 0) {
                         int* m = a.meta + blockIdx.x * 8;
-                        m[0] = walk.rem > 0 && walk.off > 0;                      // begins inside an item
-                        m[1] = walk.rem > 0 && walk.n == walk.tiles - walk.off;   // and ends it
-                        m[2] = 0;                                                 // ends inside another (set below)
+                        m[0] = walk.rem > 0 && walk.n == walk.tiles - walk.off;   // ends the item it begins in
+                        m[1] = 0;                                                 // ends inside another (set below)
                     }
                     mbar_arrive(bar(C::B_SEG + e));
                     ++known;
@@ -1278,10 +1277,10 @@ prefill8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 if (tid == 0 && w.off == 0 && !whole) {
                     int* meta = a.meta + blockIdx.x * 8;
-                    meta[2] = 1;
-                    meta[3] = w.b;
-                    meta[4] = w.rg;
-                    meta[5] = w.head;
+                    meta[1] = 1;
+                    meta[2] = w.b;
+                    meta[3] = w.rg;
+                    meta[4] = w.head;
                 }
             }
             tc_fence_before();
@@ -1310,10 +1309,10 @@ template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Args8 a, int n_ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // for the whole of prefill8_kernel
     const int* meta = a.meta + blockIdx.x * 8;
-    if (!meta[2]) return;
+    if (!meta[1]) return;
     const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const Chunk c = load_chunk(a, meta[3]);
-    const int rg = meta[4], head = meta[5];
+    const Chunk c = load_chunk(a, meta[2]);
+    const int rg = meta[3], head = meta[4];
     const int per = a.QT1 * a.HG;
     const int qi = rg * a.QTG + (row / per) * a.QT1 + (row % per) / a.HG;
     const int gh = (head % a.n_hg) * a.HG + (row % per) % a.HG, orow = c.q_base + qi;
@@ -1324,7 +1323,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefill8_join_kernel(const Ar
     while (last + a.hp < n_ctas) {
         last += a.hp;
         mx = fmaxf(mx, a.part_ml[static_cast<size_t>(last) * 2 * a.slot_rows + row].x);
-        if (a.meta[last * 8 + 1]) break;
+        if (a.meta[last * 8]) break;
     }
     float o[D / 32], sum = 0.f;
 #pragma unroll
