@@ -411,12 +411,20 @@ attn_status attn_prefill_paged_ex(const void* q, const void* k_cache, const void
  *  k_scales, v_scales, kv_dtype  the cache exactly as attn_decode takes it (max_kv
  *                is the contiguous capacity, unused for pages).
  *  ring_size   > 0: the ring of attn_decode_ring (page_table NULL, max_kv unused).
- *                Of a chunk only a sequence's newest ring_size tokens are written.
+ *                Of a chunk only a sequence's newest ring_size tokens are written, and
+ *                a chunk's tokens may overwrite keys that its first ones still need, so
+ *                attend a chunk before it enters the ring: append it to pages (then
+ *                attn_prefill_paged_ex) or, one whole prompt, to a contiguous f16 cache of
+ *                its length, whose rows attn_prefill takes; then append its k and v to the
+ *                ring too, or move the newest tokens there with attn_kv_read and attn_append.
+ *                A single new token is appended to the ring and attended with
+ *                attn_decode_ring.
  *  int8        s = f16(max|y| / 127) of each (token, head), code = y / s rounded to
  *                nearest even and clamped to [-127, 127], 0 where s is 0.  Division
  *                and rounding are exact, so without norm and rotation the codes are
  *                those of the definition bit for bit.  A head with an infinity or a
- *                NaN gets it as its scale and reads back as NaN.
+ *                NaN gets it as its scale and reads back as NaN; so does an f32 head with a
+ *                value above 127 * 65504 (8.3e6), since f16 does not hold its scale.
  *  q_out       device, q_out_dtype, [total_q, Hq, D].  It may be q itself where the
  *                type agrees and q's rows are packed too (q_stride Hq * D, or one row;
  *                else ATTN_EINVAL).  Otherwise it must not overlap q, k or v.

@@ -6,9 +6,10 @@ import pytest
 import torch
 
 import attention_split_kv_gb300 as attn
+import oracle
 import seeded_inputs as si
 from cache_util import F16_HALF, F16_TINY, F32_CHAIN, Cache, chunk_reference, norm_rotate, tables
-from parity_util import INT8_MAX_ABS, INT8_REL_L2, errors
+from parity_util import INT8_MAX_ABS, INT8_REL_L2, assert_close, errors
 
 pytestmark = pytest.mark.gpu
 
@@ -459,6 +460,81 @@ def test_migration_between_caches_keeps_the_values():
     attn.append(dst, None, k, v, start, kv)
     k2, v2 = attn.kv_read(dst, start, 95, kv_len=kv)
     assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+def test_a_prompt_longer_than_its_ring_is_attended_first():
+    # a sliding-window model: the prompt goes to a contiguous cache, whose rows attn_prefill takes, and
+    # to the ring, whose window the next tokens decode over
+    S, Hq, Hkv, D, W = 200, 4, 2, 128, 64
+    x = si.f16_normal((S + 3, Hq + 2 * Hkv, D), 41).cuda()
+    cos, sin = (t.cuda() for t in tables(S + 3, D))
+    flat = Cache("plain", 1, Hkv, D, S, seed=1).to("cuda")
+    ring = Cache("ring", 1, Hkv, D, S, ring=W, seed=2).to("cuda")
+
+    def rows(a, b):
+        return x[a:b, :Hq], x[a:b, Hq:Hq + Hkv], x[a:b, Hq + Hkv:]
+
+    start, n = torch.tensor([0, S], dtype=torch.int32).cuda(), torch.tensor([S], dtype=torch.int32).cuda()
+    q, k, v = rows(0, S)
+    q = attn.append(flat, q, k, v, start, n, rope_cos=cos, rope_sin=sin)
+    attn.append(ring, None, k, v, start, n, rope_cos=cos, rope_sin=sin)
+    pc = si.PrefillCase(q=q, k=flat.k[0], v=flat.v[0], seq_len=S, n_heads=Hq, n_kv_heads=Hkv, head_dim=D, causal=True,
+                        window=W, scale=D ** -0.5)
+    out = attn.prefill(pc)
+    ref, _ = oracle.prefill(pc.to("cpu"))
+    assert_close(out.float().cpu().numpy().reshape(ref.shape), ref, what="prompt")
+    for i in range(W):   # the ring holds what the contiguous cache does
+        assert torch.equal(ring.k[0, (S - W + i) % W], flat.k[0, S - W + i])
+    start = torch.tensor([0, 1], dtype=torch.int32).cuda()
+    for p in range(S, S + 3):
+        n = torch.tensor([p + 1], dtype=torch.int32).cuda()
+        q = attn.append(ring, *rows(p, p + 1), start, n, rope_cos=cos, rope_sin=sin)
+        dc = si.DecodeCase(q=q, k=ring.k, v=ring.v, kv_len=n, batch=1, n_heads=Hq, n_kv_heads=Hkv, head_dim=D, cap=W,
+                           ring=W, window=W, scale=D ** -0.5)
+        out = attn.decode(dc)
+        ref, _ = oracle.decode(dc.to("cpu"))
+        assert_close(out.float().cpu().numpy().reshape(ref.shape), ref, what="token at %d" % p)
+
+
+def test_ragged_prompts_move_from_pages_to_a_ring():
+    # chunks attended over int8 pages; their newest tokens then move to an f16 ring
+    B, Hq, Hkv, D, P, W = 2, 4, 2, 64, 16, 48
+    lens = [150, 20]
+    pages = Cache("paged", B, Hkv, D, 160, int8=True, page_size=P, seed=3).to("cuda")
+    ring = Cache("ring", B, Hkv, D, 160, ring=W, seed=4).to("cuda")
+    x = si.f16_normal((sum(lens), Hq + 2 * Hkv, D), 42).cuda()
+    start, n = _starts(lens).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    q = attn.append(pages, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], start, n)
+    case = si.ChunkCase(q=q, k=pages.k, v=pages.v, q_start=start, kv_len=n, page_table=pages.page_table, batch=B,
+                        n_heads=Hq, n_kv_heads=Hkv, head_dim=D, page_size=P, max_pages=pages.max_pages, max_q=150,
+                        window=W, scale=0.125, q_lens=lens, kv_lens=lens, k_scales=pages.k_scales, v_scales=pages.v_scales)
+    _close(attn.prefill_paged(case).float().cpu(), chunk_reference(case.to("cpu"))[0], "chunks")
+    keep = [min(L, W) for L in lens]
+    start = _starts(keep).cuda()
+    k, v = attn.kv_read(pages, start, sum(keep), first=n - torch.tensor(keep, dtype=torch.int32).cuda(), kv_len=n)
+    attn.append(ring, None, k, v, start, n)
+    k2, v2 = attn.kv_read(ring, start, sum(keep), first=n - torch.tensor(keep, dtype=torch.int32).cuda(), kv_len=n)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    q = si.f16_normal((B, Hq, D), 43).cuda()
+    dc = si.DecodeCase(q=q, k=ring.k, v=ring.v, kv_len=n, batch=B, n_heads=Hq, n_kv_heads=Hkv, head_dim=D, cap=W, ring=W,
+                       window=W, scale=0.125)
+    out = attn.decode(dc)
+    ref, _ = oracle.decode(dc.to("cpu"))
+    assert_close(out.float().cpu().numpy().reshape(ref.shape), ref, what="decode over the ring")
+
+
+def test_append_of_f32_values_that_no_f16_scale_holds():
+    D = 64
+    x = torch.ones(3, 1, D)
+    x[0, 0, 5], x[1, 0, 5], x[2, 0, 5] = 127 * 65504.0, -8.4e6, 1e30
+    g = Cache("plain", 1, 1, D, 8, int8=True).to("cuda")
+    start, n = torch.tensor([0, 3], dtype=torch.int32).cuda(), torch.tensor([3], dtype=torch.int32).cuda()
+    attn.append(g, None, x.cuda(), x.cuda(), start, n)
+    k, v = attn.kv_read(g, start, 3, kv_len=n, out_f32=True)
+    want = torch.zeros(D)
+    want[5] = 127 * 65504.0
+    for y in (k.cpu(), v.cpu()):
+        assert torch.equal(y[0, 0], want) and bool(y[1:].isnan().all())
 
 
 def test_captured_step_replays_on_new_inputs():
