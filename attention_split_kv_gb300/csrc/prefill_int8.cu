@@ -47,9 +47,9 @@
 // 1 to 8 new tokens of 32 sequences of 512 to 8192, 98 us, 3.0 TB/s.  With two row tiles one
 // conversion serves both, and the softmax's chain (S, 3500 cycles of softmax, PV, the next S)
 // comes to the front: 8 chunks of 512 tokens on 1 to 7680 cached ones (32/8 heads) take
-// 319 us, 744 TFLOP/s, tensor pipe 34%, issue slots 50%, shared memory 65%.  16 softmax warps
-// of 16 rows do not shorten it (307 us): a 16-byte factor load takes 4 wavefronts, and with
-// half the rows a load serves half as much.  D = 256 with a softcap and a window of 1024
+// 319 us, 744 TFLOP/s, tensor pipe 33%, issue slots 53%, shared memory 61%.  16 softmax warps
+// of 16 rows do not shorten it (305 to 307 us): a 16-byte factor load takes 4 wavefronts, and
+// with half the rows a load serves half as much.  D = 256 with a softcap and a window of 1024
 // keys: 70 us, 432 TFLOP/s: shared memory (3200 wavefronts a 64-key tile: Q is read anew for
 // each) and each segment's fixed part.
 #include <cuda.h>
