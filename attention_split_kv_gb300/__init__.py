@@ -23,6 +23,8 @@ __all__ = [
     "attn_decode_noalloc", "attn_prefill", "attn_prefill_paged", "attn_decode_validate", "attn_device_status",
     "attn_testing_set_waits", "attn_prefill_paged_ex", "attn_prefill_paged_workspace_size", "attn_append",
     "attn_kv_read", "decode", "decode_tiered", "prefill", "prefill_paged", "append", "kv_read",
+    "attn_latent_append", "attn_latent_read", "attn_latent_workspace_size", "attn_latent_attend",
+    "attn_latent_prefill", "latent_append", "latent_read", "latent_attend", "latent_prefill",
 ]
 
 ATTN_OK, ATTN_EINVAL, ATTN_EUNSUPPORTED, ATTN_ECUDA, ATTN_EBOUNDS, ATTN_ETIMEOUT = range(6)
@@ -40,7 +42,8 @@ exported_symbols = ("attn_version", "attn_last_error", "attn_decode_workspace_si
                     "attn_decode_ring", "attn_decode_ex", "attn_decode_tiered", "attn_decode_tiered_workspace_size",
                     "attn_decode_noalloc", "attn_prefill", "attn_prefill_paged", "attn_decode_validate",
                     "attn_device_status", "attn_testing_set_waits", "attn_prefill_paged_ex",
-                    "attn_prefill_paged_workspace_size", "attn_append", "attn_kv_read")
+                    "attn_prefill_paged_workspace_size", "attn_append", "attn_kv_read", "attn_latent_append",
+                    "attn_latent_read", "attn_latent_workspace_size", "attn_latent_attend", "attn_latent_prefill")
 
 
 class AttnLibraryMissing(RuntimeError):
@@ -104,6 +107,17 @@ def load():
     lib.attn_append.restype = I
     lib.attn_kv_read.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P, I, I, I, I, I, P, P, I, P]
     lib.attn_kv_read.restype = I
+    lib.attn_latent_append.argtypes = [P, P, P, I, LL, LL, LL, LL, P, F, F, P, P, I, I, P, P, P, P, I, I, I, I, I, I,
+                                       I, I, I, P, LL, LL, P]
+    lib.attn_latent_append.restype = I
+    lib.attn_latent_read.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, I, P]
+    lib.attn_latent_read.restype = I
+    lib.attn_latent_workspace_size.argtypes = [I, I, I, I]
+    lib.attn_latent_workspace_size.restype = SZ
+    lib.attn_latent_attend.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P]
+    lib.attn_latent_attend.restype = I
+    lib.attn_latent_prefill.argtypes = [P, P, P, P, LL, LL, LL, LL, LL, LL, P, P, I, I, I, I, I, I, I, I, F, P, P, P]
+    lib.attn_latent_prefill.restype = I
     lib.attn_decode_validate.argtypes = [P, P, I, I, I, I, I, ctypes.POINTER(ctypes.c_int), P]
     lib.attn_decode_validate.restype = I
     lib.attn_device_status.argtypes = [P]
@@ -543,3 +557,205 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
                  ATTN_KV_INT8 if int8 else ATTN_KV_F16, case.batch, total, case.n_kv_heads, case.head_dim, k, v,
                  _dtype_of(k), stream)
     return k, v
+
+
+# ---------------------------------------------------------------- latent attention
+def attn_latent_append(c, k_rope, q_rope, in_dtype, c_stride, k_rope_stride, q_stride, q_head_stride, c_norm, norm_eps,
+                       norm_offset, rope_cos, rope_sin, rope_positions, rope_interleaved, q_start, kv_len, cache,
+                       page_table, page_size, max_pages, n_pages, max_kv, batch, total_q, n_heads, latent_dim,
+                       rope_dim, q_out, q_out_stride, q_out_head_stride, stream=None) -> None:
+    _check(load().attn_latent_append(_ptr(c), _ptr(k_rope), _ptr(q_rope), int(in_dtype), int(c_stride),
+                                     int(k_rope_stride), int(q_stride), int(q_head_stride), _ptr(c_norm),
+                                     float(norm_eps), float(norm_offset), _ptr(rope_cos), _ptr(rope_sin),
+                                     int(rope_positions), int(bool(rope_interleaved)), _ptr(q_start), _ptr(kv_len),
+                                     _ptr(cache), _ptr(page_table), int(page_size), int(max_pages), int(n_pages),
+                                     int(max_kv), int(batch), int(total_q), int(n_heads), int(latent_dim),
+                                     int(rope_dim), _ptr(q_out), int(q_out_stride), int(q_out_head_stride),
+                                     _stream(stream)))
+
+
+def attn_latent_read(cache, kv_len, first, out_start, page_table, page_size, max_pages, n_pages, max_kv, batch, total,
+                     latent_dim, rope_dim, c_out, k_rope_out, out_dtype, stream=None) -> None:
+    _check(load().attn_latent_read(_ptr(cache), _ptr(kv_len), _ptr(first), _ptr(out_start), _ptr(page_table),
+                                   int(page_size), int(max_pages), int(n_pages), int(max_kv), int(batch), int(total),
+                                   int(latent_dim), int(rope_dim), _ptr(c_out), _ptr(k_rope_out), int(out_dtype),
+                                   _stream(stream)))
+
+
+def attn_latent_workspace_size(batch, max_q, n_heads, latent_dim) -> int:
+    return int(load().attn_latent_workspace_size(int(batch), int(max_q), int(n_heads), int(latent_dim)))
+
+
+def attn_latent_attend(q, cache, q_start, kv_len, page_table, page_size, max_pages, n_pages, max_kv, batch, total_q,
+                       max_q, n_heads, latent_dim, rope_dim, scale, out, lse_out, workspace, workspace_bytes,
+                       stream=None) -> None:
+    _check(load().attn_latent_attend(_ptr(q), _ptr(cache), _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                     int(page_size), int(max_pages), int(n_pages), int(max_kv), int(batch),
+                                     int(total_q), int(max_q), int(n_heads), int(latent_dim), int(rope_dim),
+                                     float(scale), _ptr(out), _ptr(lse_out), _ptr(workspace), int(workspace_bytes),
+                                     _stream(stream)))
+
+
+def attn_latent_prefill(q, k, v, k_rope, q_stride, k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride,
+                        q_start, kv_start, batch, total_q, total_kv, max_q, n_heads, head_dim, rope_dim, causal, scale,
+                        out, lse_out=None, stream=None) -> None:
+    _check(load().attn_latent_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(k_rope), int(q_stride), int(k_stride),
+                                      int(k_head_stride), int(v_stride), int(v_head_stride), int(k_rope_stride),
+                                      _ptr(q_start), _ptr(kv_start), int(batch), int(total_q), int(total_kv),
+                                      int(max_q), int(n_heads), int(head_dim), int(rope_dim), int(bool(causal)),
+                                      float(scale), _ptr(out), _ptr(lse_out), _stream(stream)))
+
+
+_ROPE = 64   # values of the rotated part of a latent cache's rows
+
+
+def _latent_args(case):
+    """page_size, max_pages, n_pages, max_kv and R of a LatentCase-like cache, whose tensors
+    agree with its sizes."""
+    import torch
+    x = case.cache
+    _need(x.dim() == 3 and x.dtype == torch.float16, "the cache must be a float16 tensor [B or pages, tokens, R + 64]")
+    slots, rows, width = x.shape
+    _dense("cache", x, torch.float16, x)
+    if case.page_table is not None:
+        _need(int(case.page_size) == rows, "page_size must be the pages' tokens (%d)", rows)
+        _dense("page_table", case.page_table, torch.int32, x, least=int(case.batch) * int(case.max_pages))
+        _need(case.page_table.shape[-1] == int(case.max_pages), "page_table must have max_pages columns")
+        return rows, int(case.max_pages), slots, 0, width - _ROPE
+    _need(slots >= int(case.batch), "the cache must hold a slot for each of %d sequences", int(case.batch))
+    return 0, 0, 0, rows, width - _ROPE
+
+
+def _latent_lengths(case, kv_len, **others):
+    import torch
+    kv_len = case.kv_len if kv_len is None else kv_len
+    _dense("kv_len", kv_len, torch.int32, case.cache, least=case.batch)
+    for what, x in others.items():
+        if x is not None:
+            _dense(what, x, torch.int32, case.cache, least=case.batch + (what != "first"))
+    return kv_len
+
+
+def _rows(what, x, width, like, dtype=None):
+    """Token rows (2-D) or heads of token rows (3-D) of ``width`` values, neighbours in memory;
+    returns their strides."""
+    _need(x.shape[-1] == width and x.stride(-1) == 1, "%s must have rows of %d neighbouring values", what, width)
+    _need(dtype is None or x.dtype == dtype, "%s must be %s", what, dtype)
+    _need(x.device == like.device, "%s must be on the cache's device", what)
+    head = 0
+    if x.dim() == 3:
+        head = x.stride(1) if x.shape[1] > 1 else max(width, x.stride(1))
+    least = width if x.dim() == 2 else (x.shape[1] - 1) * head + width
+    if x.shape[0] > 1:
+        return x.stride(0), head
+    return -(-least // 8) * 8, head   # (a single row's stride is not used)
+
+
+def latent_append(case, c, k_rope, q_start, kv_len=None, q_rope=None, c_norm=None, norm_eps=1e-6, norm_offset=0.0,
+                  rope_cos=None, rope_sin=None, rope_interleaved=True, q_out=None, stream=None):
+    """attn_latent_append of token rows (c [T, R], k_rope [T, 64], q_rope [T, Hq, 64] or None,
+    f16 or f32; slices of wider rows are fine) to the cache that a LatentCase-like object
+    holds; ``kv_len`` (default: the case's) counts each sequence's tokens with the new ones.
+    Returns q_out (f16, packed unless given)."""
+    import torch
+    P, max_pages, n_pages, max_kv, R = _latent_args(case)
+    x = case.cache
+    _need(c.dim() == 2 and k_rope.dim() == 2 and k_rope.shape[0] == c.shape[0], "c and k_rope must be [T, R] and [T, 64]")
+    T, dt = c.shape[0], c.dtype
+    c_stride, _ = _rows("c", c, R, x)
+    k_stride, _ = _rows("k_rope", k_rope, _ROPE, x, dt)
+    kv_len = _latent_lengths(case, kv_len, q_start=q_start)
+    if c_norm is not None:
+        _dense("c_norm", c_norm, torch.float32, x, (R,))
+    _need((rope_cos is None) == (rope_sin is None), "rope_cos and rope_sin go together")
+    if rope_cos is not None:
+        _need(rope_cos.dim() == 2 and rope_cos.shape[1] == _ROPE // 2, "rope_cos must be [positions, 32]")
+        _dense("rope_cos", rope_cos, torch.float32, x)
+        _dense("rope_sin", rope_sin, torch.float32, x, tuple(rope_cos.shape))
+    q_strides = out_strides = (0, 0)
+    H = 0
+    if q_rope is not None:
+        _need(q_rope.dim() == 3 and q_rope.shape[0] == T, "q_rope must be [T, Hq, 64] with c's T")
+        H = q_rope.shape[1]
+        q_strides = _rows("q_rope", q_rope, _ROPE, x, dt)
+        if q_out is None:
+            q_out = _empty(q_rope.shape, torch.float16, q_rope.device, stream)
+        _need(q_out.shape == q_rope.shape, "q_out must have q_rope's shape")
+        out_strides = _rows("q_out", q_out, _ROPE, x, torch.float16)
+    if T == 0:
+        return q_out
+    attn_latent_append(c, k_rope, q_rope, _dtype_of(c), c_stride, k_stride, *q_strides, c_norm, norm_eps, norm_offset,
+                       rope_cos, rope_sin, 0 if rope_cos is None else rope_cos.shape[0], rope_interleaved, q_start,
+                       kv_len, x, case.page_table, P, max_pages, n_pages, max_kv, case.batch, T, H, R, _ROPE,
+                       None if q_rope is None else q_out, *out_strides, stream)
+    return q_out
+
+
+def latent_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stream=None):
+    """attn_latent_read of a LatentCase-like object's cache: (c [total, R], k_rope [total, 64]),
+    f16 or f32; rows past out_start[B] are not written."""
+    import torch
+    P, max_pages, n_pages, max_kv, R = _latent_args(case)
+    kv_len = _latent_lengths(case, kv_len, out_start=out_start, first=first)
+    dt = torch.float32 if out_f32 else torch.float16
+    c, k = (_empty((total, n), dt, case.cache.device, stream) for n in (R, _ROPE))
+    if total:
+        attn_latent_read(case.cache, kv_len, first, out_start, case.page_table, P, max_pages, n_pages, max_kv,
+                         case.batch, total, R, _ROPE, c, k, _dtype_of(c), stream)
+    return c, k
+
+
+def latent_attend(case, q, q_start, max_q, kv_len=None, out=None, lse_out=None, workspace=None, stream=None):
+    """attn_latent_attend of q [T, Hq, R + 64] (f16, packed) over a LatentCase-like object's cache
+    with its ``scale``; ``max_q`` bounds the sequences' new tokens.  Returns out [T, Hq, R]."""
+    import torch
+    P, max_pages, n_pages, max_kv, R = _latent_args(case)
+    x = case.cache
+    _need(q.dim() == 3 and q.shape[2] == R + _ROPE, "q must be [T, Hq, %d]", R + _ROPE)
+    T, H = q.shape[:2]
+    _dense("q", q, torch.float16, x)
+    kv_len = _latent_lengths(case, kv_len, q_start=q_start)
+    if out is None:
+        out = _empty((T, H, R), torch.float16, q.device, stream)
+    _dense("out", out, torch.float16, x, (T, H, R))
+    if lse_out is not None:
+        _dense("lse_out", lse_out, torch.float32, x, least=T * H)
+    if T == 0 or max_q == 0:
+        return out
+    if workspace is None:
+        size = attn_latent_workspace_size(case.batch, max_q, H, R)
+        if size == 0:
+            raise AttnError(ATTN_EINVAL, "invalid sizes for the latent attention workspace")
+        workspace = _empty(size, torch.uint8, q.device, stream, scratch=True)
+    attn_latent_attend(q, x, q_start, kv_len, case.page_table, P, max_pages, n_pages, max_kv, case.batch, T, max_q, H,
+                       R, _ROPE, case.scale, out, lse_out, workspace, workspace.numel(), stream)
+    return out
+
+
+def latent_prefill(q, k, v, k_rope, q_start, kv_start, max_q, scale, causal=True, out=None, lse_out=None, stream=None):
+    """attn_latent_prefill of packed q [Tq, Hq, 192], k and v [Tk, Hq, 128] (slices of wider rows
+    are fine) and k_rope [Tk, 64], all f16; ``max_q`` bounds the sequences' queries.  Returns
+    out [Tq, Hq, 128]."""
+    import torch
+    HD = 128
+    _need(q.dim() == 3 and k.dim() == 3 and v.shape == k.shape and k.shape[1] == q.shape[1] and k_rope.dim() == 2
+          and k_rope.shape[0] == k.shape[0], "q, k, v and k_rope must be [Tq, Hq, 192], [Tk, Hq, 128] twice and [Tk, 64]")
+    T, H = q.shape[:2]
+    q_stride, q_head = _rows("q", q, HD + _ROPE, q, torch.float16)
+    _need(q_head == HD + _ROPE, "q's heads must lie side by side")
+    k_strides, v_strides = (_rows(what, t, HD, q, torch.float16) for what, t in (("k", k), ("v", v)))
+    r_stride, _ = _rows("k_rope", k_rope, _ROPE, q, torch.float16)
+    B = q_start.numel() - 1
+    _need(B > 0, "q_start must have an element more than there are sequences")
+    _dense("q_start", q_start, torch.int32, q)
+    _dense("kv_start", kv_start, torch.int32, q, tuple(q_start.shape))
+    if out is None:
+        out = _empty((T, H, HD), torch.float16, q.device, stream)
+    _dense("out", out, torch.float16, q, (T, H, HD))
+    if lse_out is not None:
+        _dense("lse_out", lse_out, torch.float32, q, least=T * H)
+    if T == 0 or max_q == 0:
+        return out
+    attn_latent_prefill(q, k, v, k_rope, q_stride, *k_strides, *v_strides, r_stride, q_start, kv_start, B, T,
+                        k.shape[0], max_q, H, HD, _ROPE, causal, scale, out, lse_out, stream)
+    return out

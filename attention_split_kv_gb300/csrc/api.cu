@@ -759,6 +759,259 @@ attn_status attn_kv_read(const void* k_cache, const void* v_cache, const int32_t
     return launch_kv_read(L);
 }
 
+// The latent cache's layout, checked.
+static attn_status latent_layout(const char* fn, const void* cache, const int32_t* page_table, int page_size,
+                                 int max_pages_per_seq, int n_pages, int max_kv, int batch, int latent_dim, int rope_dim,
+                                 CacheLayout* c) {
+    if (!cache) return set_error(ATTN_EINVAL, "%s: cache must be non-null", fn);
+    if (!aligned(cache, 16)) return set_error(ATTN_EINVAL, "%s: cache must be 16-byte aligned", fn);
+    if (batch <= 0) return set_error(ATTN_EINVAL, "%s: batch must be positive", fn);
+    if (batch > 65535) return set_error(ATTN_EUNSUPPORTED, "%s: batch above 65535", fn);
+    if (latent_dim != 256 && latent_dim != 512)
+        return set_error(ATTN_EUNSUPPORTED, "%s: latent_dim %d not supported (256, 512)", fn, latent_dim);
+    if (rope_dim != 64) return set_error(ATTN_EUNSUPPORTED, "%s: rope_dim %d not supported (64)", fn, rope_dim);
+    c->page_table = page_table;
+    c->log2P = 0;
+    c->max_pages = max_pages_per_seq;
+    c->n_pages = n_pages;
+    c->ring = 0;
+    if (page_table) {
+        if (!pow2(page_size) || page_size < 8 || page_size > 1024)
+            return set_error(ATTN_EUNSUPPORTED, "%s: page_size %d must be a power of two in 8 .. 1024", fn, page_size);
+        if (max_pages_per_seq <= 0 || n_pages <= 0)
+            return set_error(ATTN_EINVAL, "%s: max_pages_per_seq and n_pages must be positive", fn);
+        c->rows = page_size;
+        while ((1 << c->log2P) < page_size) ++c->log2P;
+        c->capacity = static_cast<long long>(max_pages_per_seq) * page_size;
+    } else {
+        if (max_kv <= 0) return set_error(ATTN_EINVAL, "%s: max_kv must be positive", fn);
+        c->rows = max_kv;
+        c->capacity = max_kv;
+    }
+    return ATTN_OK;
+}
+
+attn_status attn_latent_append(const void* c, const void* k_rope, const void* q_rope, attn_dtype in_dtype,
+                               long long c_stride, long long k_rope_stride, long long q_stride,
+                               long long q_head_stride, const float* c_norm, float norm_eps, float norm_offset,
+                               const float* rope_cos, const float* rope_sin, int rope_positions, int rope_interleaved,
+                               const int32_t* q_start, const int32_t* kv_len, void* cache, const int32_t* page_table,
+                               int page_size, int max_pages_per_seq, int n_pages, int max_kv, int batch, int total_q,
+                               int n_heads, int latent_dim, int rope_dim, void* q_out, long long q_out_stride,
+                               long long q_out_head_stride, void* stream) {
+    const char* fn = "attn_latent_append";
+    if (!c || !k_rope || !q_start || !kv_len)
+        return set_error(ATTN_EINVAL, "%s: c, k_rope, q_start and kv_len must be non-null", fn);
+    if ((q_rope == nullptr) != (q_out == nullptr))
+        return set_error(ATTN_EINVAL, "%s: q_rope and q_out go together (both NULL: the cache only)", fn);
+    if (in_dtype != ATTN_F16 && in_dtype != ATTN_F32)
+        return set_error(ATTN_EINVAL, "%s: in_dtype must be ATTN_F16 or ATTN_F32", fn);
+    if (total_q < 0 || (q_rope && n_heads <= 0))
+        return set_error(ATTN_EINVAL, "%s: a positive head count and total_q >= 0 required", fn);
+    if (q_rope && n_heads > 65535) return set_error(ATTN_EUNSUPPORTED, "%s: n_heads above 65535", fn);
+    LatentAppendLaunch L;
+    LatentAppendArgs& a = L.args;
+    attn_status st = latent_layout(fn, cache, page_table, page_size, max_pages_per_seq, n_pages, max_kv, batch,
+                                   latent_dim, rope_dim, &a.cache);
+    if (st != ATTN_OK) return st;
+    const int per16 = in_dtype == ATTN_F32 ? 4 : 8;   // elements in 16 bytes
+    if (c_stride < latent_dim || k_rope_stride < rope_dim)
+        return set_error(ATTN_EINVAL, "%s: a token stride is smaller than its row", fn);
+    if (c_stride % per16 || k_rope_stride % per16)
+        return set_error(ATTN_EUNSUPPORTED, "%s: token strides must be multiples of 16 bytes", fn);
+    if (q_rope) {
+        const long long last = static_cast<long long>(n_heads - 1);
+        if (q_head_stride < rope_dim || q_out_head_stride < rope_dim || q_stride < last * q_head_stride + rope_dim ||
+            q_out_stride < last * q_out_head_stride + rope_dim)
+            return set_error(ATTN_EINVAL, "%s: q's head strides must hold rope_dim values, its token strides all heads", fn);
+        if (q_stride % per16 || q_head_stride % per16 || q_out_stride % 8 || q_out_head_stride % 8)
+            return set_error(ATTN_EUNSUPPORTED, "%s: q's strides must be multiples of 16 bytes", fn);
+        if (q_rope == q_out &&
+            (in_dtype != ATTN_F16 || q_stride != q_out_stride || q_head_stride != q_out_head_stride))
+            return set_error(ATTN_EINVAL, "%s: q_out may be q_rope only if that is f16 and has its strides", fn);
+    }
+    if (c_norm && (!(norm_eps >= 0.f) || !std::isfinite(norm_eps) || !std::isfinite(norm_offset)))
+        return set_error(ATTN_EINVAL, "%s: norm_eps must be finite and >= 0, norm_offset finite", fn);
+    if ((rope_cos == nullptr) != (rope_sin == nullptr) || (rope_cos && rope_positions <= 0))
+        return set_error(ATTN_EINVAL, "%s: a rotation needs rope_cos, rope_sin and rope_positions > 0", fn);
+    if (!aligned(c, 16) || !aligned(k_rope, 16) || !aligned(q_rope, 16) || !aligned(q_out, 16) || !aligned(c_norm, 16) ||
+        !aligned(rope_cos, 16) || !aligned(rope_sin, 16))
+        return set_error(ATTN_EINVAL, "%s: c, k_rope, q_rope, q_out, c_norm and tables must be 16-byte aligned", fn);
+    if (total_q == 0) return ATTN_OK;
+    int* err = device_error_word();
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    a.c = c;
+    a.k_rope = k_rope;
+    a.q_rope = q_rope;
+    a.c_stride = c_stride;
+    a.k_stride = k_rope_stride;
+    a.q_stride = q_rope ? q_stride : 0;
+    a.q_head_stride = q_rope ? q_head_stride : 0;
+    a.c_norm = c_norm;
+    a.eps = norm_eps;
+    a.offset = norm_offset;
+    a.cos = rope_cos;
+    a.sin = rope_sin;
+    a.n_pos = rope_positions;
+    a.interleaved = rope_interleaved != 0;
+    a.q_start = q_start;
+    a.kv_len = kv_len;
+    a.x = cache;
+    a.B = batch;
+    a.total_q = total_q;
+    a.H = q_rope ? n_heads : 0;
+    a.q_out = q_out;
+    a.q_out_stride = q_rope ? q_out_stride : 0;
+    a.q_out_head_stride = q_rope ? q_out_head_stride : 0;
+    a.err = err;
+    L.R = latent_dim;
+    L.in_f32 = in_dtype == ATTN_F32;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_latent_append(L);
+}
+
+attn_status attn_latent_read(const void* cache, const int32_t* kv_len, const int32_t* first, const int32_t* out_start,
+                             const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
+                             int batch, int total, int latent_dim, int rope_dim, void* c_out, void* k_rope_out,
+                             attn_dtype out_dtype, void* stream) {
+    const char* fn = "attn_latent_read";
+    if (!kv_len || !out_start || !c_out || !k_rope_out)
+        return set_error(ATTN_EINVAL, "%s: kv_len, out_start, c_out and k_rope_out must be non-null", fn);
+    if (out_dtype != ATTN_F16 && out_dtype != ATTN_F32)
+        return set_error(ATTN_EINVAL, "%s: out_dtype must be ATTN_F16 or ATTN_F32", fn);
+    if (total < 0) return set_error(ATTN_EINVAL, "%s: total >= 0 required", fn);
+    LatentReadLaunch L;
+    LatentReadArgs& a = L.args;
+    attn_status st = latent_layout(fn, cache, page_table, page_size, max_pages_per_seq, n_pages, max_kv, batch,
+                                   latent_dim, rope_dim, &a.cache);
+    if (st != ATTN_OK) return st;
+    if (!aligned(c_out, 16) || !aligned(k_rope_out, 16))
+        return set_error(ATTN_EINVAL, "%s: c_out and k_rope_out must be 16-byte aligned", fn);
+    if (total == 0) return ATTN_OK;
+    int* err = device_error_word();
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    a.x = cache;
+    a.kv_len = kv_len;
+    a.first = first;
+    a.out_start = out_start;
+    a.B = batch;
+    a.total = total;
+    a.c_out = c_out;
+    a.k_out = k_rope_out;
+    a.err = err;
+    L.R = latent_dim;
+    L.out_f32 = out_dtype == ATTN_F32;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_latent_read(L);
+}
+
+size_t attn_latent_workspace_size(int batch, int max_q, int n_heads, int latent_dim) {
+    if (batch <= 0 || batch > 65535 || max_q <= 0 || n_heads <= 0 || n_heads > 65535) return 0;
+    if (latent_dim != 256 && latent_dim != 512) return 0;
+    if (static_cast<long long>(max_q) * n_heads >= 1ll << 31) return 0;
+    return latent_attend_workspace(max_q, n_heads, latent_dim);
+}
+
+attn_status attn_latent_attend(const void* q, const void* cache, const int32_t* q_start, const int32_t* kv_len,
+                               const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
+                               int batch, int total_q, int max_q, int n_heads, int latent_dim, int rope_dim, float scale,
+                               void* out, float* lse_out, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "attn_latent_attend";
+    if (!q || !q_start || !kv_len || !out || !workspace)
+        return set_error(ATTN_EINVAL, "%s: q, q_start, kv_len, out and workspace must be non-null", fn);
+    if (total_q < 0 || max_q < 0 || n_heads <= 0)
+        return set_error(ATTN_EINVAL, "%s: a positive head count, total_q >= 0 and max_q >= 0 required", fn);
+    if (n_heads > 65535) return set_error(ATTN_EUNSUPPORTED, "%s: n_heads above 65535", fn);
+    if (!std::isfinite(scale)) return set_error(ATTN_EINVAL, "%s: scale must be finite", fn);
+    LatentAttendLaunch L;
+    attn_status st = latent_layout(fn, cache, page_table, page_size, max_pages_per_seq, n_pages, max_kv, batch,
+                                   latent_dim, rope_dim, &L.cache);
+    if (st != ATTN_OK) return st;
+    if (static_cast<long long>(total_q) * n_heads >= 1ll << 31 || static_cast<long long>(max_q) * n_heads >= 1ll << 31)
+        return set_error(ATTN_EUNSUPPORTED, "%s: 2^31 rows (tokens x heads) or more", fn);
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || (lse_out && !aligned(lse_out, 4)))
+        return set_error(ATTN_EINVAL, "%s: q and out must be 16-byte, the workspace 256-byte aligned", fn);
+    if (total_q == 0 || max_q == 0) return ATTN_OK;
+    const size_t need = latent_attend_workspace(max_q, n_heads, latent_dim);
+    if (workspace_bytes < need)
+        return set_error(ATTN_EINVAL, "%s: the workspace has %zu bytes, %zu needed", fn, workspace_bytes, need);
+    int* err = device_error_word();
+    if (!err) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    L.q = q;
+    L.x = cache;
+    L.q_start = q_start;
+    L.kv_len = kv_len;
+    L.B = batch;
+    L.total_q = total_q;
+    L.max_q = max_q;
+    L.H = n_heads;
+    L.R = latent_dim;
+    L.scale = scale;
+    L.out = out;
+    L.lse = lse_out;
+    L.workspace = workspace;
+    L.err_word = err;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_latent_attend(L);
+}
+
+attn_status attn_latent_prefill(const void* q, const void* k, const void* v, const void* k_rope, long long q_stride,
+                                long long k_stride, long long k_head_stride, long long v_stride,
+                                long long v_head_stride, long long k_rope_stride, const int32_t* q_start,
+                                const int32_t* kv_start, int batch, int total_q, int total_kv, int max_q, int n_heads,
+                                int head_dim, int rope_dim, int causal, float scale, void* out, float* lse_out,
+                                void* stream) {
+    const char* fn = "attn_latent_prefill";
+    if (!q || !k || !v || !k_rope || !q_start || !kv_start || !out)
+        return set_error(ATTN_EINVAL, "%s: q, k, v, k_rope, q_start, kv_start and out must be non-null", fn);
+    if (batch <= 0 || total_q < 0 || total_kv <= 0 || max_q < 0 || n_heads <= 0)
+        return set_error(ATTN_EINVAL, "%s: positive batch, total_kv and head counts, total_q and max_q >= 0 required", fn);
+    if (batch > 65535 || n_heads > 65535)
+        return set_error(ATTN_EUNSUPPORTED, "%s: batch or n_heads above 65535", fn);
+    if (head_dim != 128) return set_error(ATTN_EUNSUPPORTED, "%s: head_dim %d not supported (128)", fn, head_dim);
+    if (rope_dim != 64) return set_error(ATTN_EUNSUPPORTED, "%s: rope_dim %d not supported (64)", fn, rope_dim);
+    if (causal != 0 && causal != 1) return set_error(ATTN_EINVAL, "%s: causal must be 0 or 1", fn);
+    if (!std::isfinite(scale)) return set_error(ATTN_EINVAL, "%s: scale must be finite", fn);
+    const long long last = n_heads - 1, most = 1ll << 38;   // (of a tensor map's strides, in elements)
+    if (k_head_stride < head_dim || v_head_stride < head_dim || k_stride < last * k_head_stride + head_dim ||
+        v_stride < last * v_head_stride + head_dim || q_stride < (last + 1) * (head_dim + rope_dim) ||
+        k_rope_stride < rope_dim)
+        return set_error(ATTN_EINVAL, "%s: a head stride is smaller than head_dim, or a token stride than its row", fn);
+    if (q_stride % 8 || k_stride % 8 || k_head_stride % 8 || v_stride % 8 || v_head_stride % 8 || k_rope_stride % 8 ||
+        q_stride >= most || k_stride >= most || v_stride >= most || k_rope_stride >= most)
+        return set_error(ATTN_EUNSUPPORTED, "%s: strides must be multiples of 16 bytes below 2^39", fn);
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_rope, 16) || !aligned(out, 16))
+        return set_error(ATTN_EINVAL, "%s: q, k, v, k_rope and out must be 16-byte aligned", fn);
+    if (max_q > 65535 * 256) return set_error(ATTN_EUNSUPPORTED, "%s: max_q above 65535 * 256", fn);
+    if (total_q == 0 || max_q == 0) return ATTN_OK;
+    LatentPrefillLaunch L;
+    L.err_word = device_error_word();
+    if (!L.err_word) return set_error(ATTN_ECUDA, "%s: no CUDA device / error word", fn);
+    L.q = q;
+    L.k = k;
+    L.v = v;
+    L.k_rope = k_rope;
+    L.q_stride = q_stride;
+    L.k_stride = k_stride;
+    L.k_head_stride = k_head_stride;
+    L.v_stride = v_stride;
+    L.v_head_stride = v_head_stride;
+    L.k_rope_stride = k_rope_stride;
+    L.q_start = q_start;
+    L.kv_start = kv_start;
+    L.B = batch;
+    L.total_q = total_q;
+    L.total_kv = total_kv;
+    L.max_q = max_q;
+    L.H = n_heads;
+    L.causal = causal;
+    L.scale = scale;
+    L.out = out;
+    L.lse = lse_out;
+    L.stream = static_cast<cudaStream_t>(stream);
+    return launch_latent_prefill(L);
+}
+
 attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_table, int batch, int page_size,
                                  int max_pages_per_seq, int n_pages, int max_kv, int* bad_seq, void* stream) {
     if (!kv_len || batch <= 0 || max_kv <= 0)
@@ -795,6 +1048,8 @@ attn_status attn_testing_set_waits(unsigned long long wait_limit_ns, int stall_f
     attn_status st = set_test_controls_prefill(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_decode(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_prefill8(limit, stall_first_tile);
+    if (st == ATTN_OK) st = set_test_controls_latent_attend(limit, stall_first_tile);
+    if (st == ATTN_OK) st = set_test_controls_latent_prefill(limit, stall_first_tile);
     return st;
 }
 
@@ -812,10 +1067,12 @@ attn_status attn_device_status(void* stream) {
         return set_error(ATTN_EBOUNDS, "attn_prefill_paged or attn_prefill_paged_ex met a page id outside the pool (its "
                                        "keys and values were read as zeros)");
     if (v == kErrCachePage)
-        return set_error(ATTN_EBOUNDS, "attn_append or attn_kv_read met a page id outside the pool (the token was not "
-                                       "written, or read as zeros)");
+        return set_error(ATTN_EBOUNDS, "attn_append or attn_kv_read (or their latent forms) met a page id outside the pool "
+                                       "(the token was not written, or read as zeros)");
+    if (v == kErrLatentPage)
+        return set_error(ATTN_EBOUNDS, "attn_latent_attend met a page id outside the pool (its tokens were read as zeros)");
     if (v == kErrAppendRange)
-        return set_error(ATTN_EBOUNDS, "attn_append met a position outside the cache or the cos/sin tables (the token "
+        return set_error(ATTN_EBOUNDS, "attn_append or attn_latent_append met a position outside the cache or the cos/sin tables (the token "
                                        "was left out)");
     if (v) return set_error(ATTN_ETIMEOUT, "a kernel abandoned a pipeline wait (code %d)", v);
     return ATTN_OK;

@@ -19,9 +19,10 @@ enum : int {
     kErrTimeoutMma = 3,      // a wait on a tensor-core result timed out
     kErrTimeoutSoftmax = 4,  // the MMA issuer waited too long for P
     kErrBadPage = 5,         // a page-table entry in use was outside the page pool (decode)
-    kErrCachePage = 6,       // the same, met by attn_append or attn_kv_read
+    kErrCachePage = 6,       // the same, met by attn_append or attn_kv_read, or their latent forms
     kErrAppendRange = 7,     // a new token's position outside the cache or the cos/sin tables
     kErrChunkPage = 8,       // a page-table entry in use outside the pool, met by attn_prefill_paged(_ex)
+    kErrLatentPage = 9,      // the same, met by attn_latent_attend
 };
 
 // Records a message for attn_last_error() (thread-local) and returns `st`.
@@ -186,11 +187,79 @@ struct Prefill8Launch {
 size_t prefill8_workspace(int max_q, int Hq, int Hkv, int D);
 attn_status launch_prefill8(const Prefill8Launch& L);
 
+// ---- latent attention: a token's cached row is [c (R values) | rotated key part (64)]
+struct LatentAppendArgs {
+    const void *c, *k_rope, *q_rope;
+    long long c_stride, k_stride, q_stride, q_head_stride;   // elements
+    const float* c_norm;
+    float eps, offset;
+    const float *cos, *sin;
+    int n_pos, interleaved;
+    const int32_t *q_start, *kv_len;
+    CacheLayout cache;
+    void* x;
+    int B, total_q, H;
+    void* q_out;
+    long long q_out_stride, q_out_head_stride;
+    int* err;
+};
+struct LatentAppendLaunch {
+    LatentAppendArgs args;
+    int R, in_f32;
+    cudaStream_t stream;
+};
+attn_status launch_latent_append(const LatentAppendLaunch& L);
+
+struct LatentReadArgs {
+    const void* x;
+    const int32_t *kv_len, *first, *out_start;
+    CacheLayout cache;
+    int B, total;
+    void *c_out, *k_out;
+    int* err;
+};
+struct LatentReadLaunch {
+    LatentReadArgs args;
+    int R, out_f32;
+    cudaStream_t stream;
+};
+attn_status launch_latent_read(const LatentReadLaunch& L);
+
+struct LatentAttendLaunch {
+    const void *q, *x;
+    const int32_t *q_start, *kv_len;
+    CacheLayout cache;
+    int B, total_q, max_q, H, R;
+    float scale;
+    void* out;
+    float* lse;
+    void* workspace;
+    int* err_word;
+    cudaStream_t stream;
+};
+size_t latent_attend_workspace(int max_q, int H, int R);
+attn_status launch_latent_attend(const LatentAttendLaunch& L);
+
+struct LatentPrefillLaunch {
+    const void *q, *k, *v, *k_rope;
+    long long q_stride, k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride;   // elements
+    const int32_t *q_start, *kv_start;
+    int B, total_q, total_kv, max_q, H, causal;
+    float scale;
+    void* out;
+    float* lse;
+    int* err_word;
+    cudaStream_t stream;
+};
+attn_status launch_latent_prefill(const LatentPrefillLaunch& L);
+
 // Test controls of the prefill and decode translation units: the time limit
 // of pipeline waits (ns) and the first-tile stall (see ptx.cuh).
 attn_status set_test_controls_prefill(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_decode(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_prefill8(unsigned long long wait_limit_ns, int stall);
+attn_status set_test_controls_latent_attend(unsigned long long wait_limit_ns, int stall);
+attn_status set_test_controls_latent_prefill(unsigned long long wait_limit_ns, int stall);
 
 constexpr int kDecodeMaxBatch = 4096;
 constexpr int kDecodeMaxFix = 256;    // most CTAs the balanced decode kernel launches (>= SMs)

@@ -1,0 +1,455 @@
+// latent_prefill.cu -- the expanded form of latent attention (attn_latent_prefill) on the
+// sm_103a tensor cores: packed sequences whose keys have a part of their own a head (128
+// values) and a rotated part that all heads share (64), and values of 128.
+//
+//   o_ih = sum_j softmax_j(scale (q_ih[0:128] . k_jh + q_ih[128:192] . r_j)) v_jh
+//
+// over the keys j <= L - n + i (causal: the n queries are the last of the sequence's L
+// tokens) or all of them.  The two parts are one product of depth 192 in the operands'
+// chunks; the key is never put together in memory.
+//
+//   S  = Q K^T      128 queries x 128 keys, f32 in TMEM    (tcgen05.mma, 12 steps of 16)
+//   P  = 2^(S scale log2e - m)     f16, over S in TMEM
+//   O += P V        128 x 128, f32 in TMEM                 (P from TMEM, V MN-major)
+//
+// A CTA takes 256 queries of a head as two row tiles, each with its S/P and O (all 512 TMEM
+// columns) and a softmax warpgroup; the two take turns on the tensor cores,
+//
+//   S0(0) S1(0) | PV0(j) S0(j+1) | PV1(j) S1(j+1) | ...
+//
+// so that one tile's softmax runs under the other's products (1280 cycles a turn at the
+// tensor peak), and a key tile is read from shared memory's ring by both.  K and V lie in one
+// ring of 16 KB chunks (64 values of 128 keys) in the order of their first use, which is also
+// the order in which they are released: K(j) after S1(j), V(j) after PV1(j).
+//
+// Roles (12 warps): 8 softmax warps (row tile w / 4), a TMA warp, an MMA warp, 2 idle.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int BM = 128, BN = 128;           // rows of a row tile, keys of a key tile
+constexpr int HD = 128, RD = 64;            // a head's values, the rotated part's
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
+constexpr float kFastSumLimit = 256.0f;     // a row whose p sum to at most this has every p <= 2^8
+constexpr int kSoftmaxWarps = 8;
+// 3 warpgroups: 8 softmax warps, then the TMA warp, the MMA warp and two that only make up the
+// third, which leaves registers to the others (launch: 384 x 168)
+constexpr int kThreads = 384;
+constexpr int kRegSoftmax = 208, kRegOther = 88;
+static_assert(2 * kRegSoftmax + kRegOther == 3 * 168, "register split");
+constexpr int RING = 8, K_CHUNKS = 3, V_CHUNKS = 2, CHUNKS = K_CHUNKS + V_CHUNKS;
+constexpr uint32_t kChunk = BN * 128;       // 64 values of 128 keys (or queries)
+constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * K_CHUNKS * kChunk, OFF_BAR = OFF_RING + RING * kChunk;
+enum : int { B_Q, B_FULL = B_Q + 2, B_EMPTY = B_FULL + RING, B_S = B_EMPTY + RING, B_P = B_S + 2, B_DONE = B_P + 2,
+             B_TEARDOWN = B_DONE + 2, N_BARS };
+constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8, SMEM_ALLOC = OFF_MISC + 8 + 1024;
+constexpr uint32_t COL_O = 2 * BN, TMEM_COLS = 512;
+static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
+static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
+
+struct Args {
+    __half* out;
+    float* lse;
+    const int32_t *q_start, *kv_start;
+    int total_q, total_kv, max_q, H, causal;
+    float scale;
+    int* err;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float row_max(const float (&t)[BN]) {
+    float a[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = t[k];
+#pragma unroll
+    for (int i = 8; i + 16 <= BN; i += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) a[k] = max3(a[k], t[i + k], t[i + 8 + k]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) a[k] = fmaxf(a[k], t[BN - 8 + k]);
+    return fmaxf(max3(a[0], a[1], a[2]), max3(a[3], a[4], max3(a[5], a[6], a[7])));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+    auto bar = [&](int i) { return sbase + OFF_BAR + i * 8; };
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    // heads fastest, then blocks of 256 queries from the last (the longest when causal)
+    const int h = blockIdx.x, b = blockIdx.z;
+    const int q_base = a.q_start[b], k_base = a.kv_start[b];
+    const int n_all = max(a.q_start[b + 1] - q_base, 0), L = max(a.kv_start[b + 1] - k_base, 0);
+    const int n_q = min(n_all, a.max_q);
+    const int q0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 2 * BM;
+    if (q0 >= n_q) return;                       // a shorter sequence: no queries for this CTA
+    const int pos0 = L - n_all;                  // position of query 0
+    // key tiles of each row tile (at least one where it has rows)
+    int n_tiles[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = q0 + t * BM, last = min(first + BM, n_q) - 1;
+        const int hi = a.causal ? max(min(L, pos0 + last + 1), 0) : L;
+        n_tiles[t] = first < n_q ? max((hi + BN - 1) / BN, 1) : 0;
+    }
+    const int n = max(n_tiles[0], n_tiles[1]);
+
+    // A wait of a whole warp, with one answer for all of its lanes.
+    auto wait = [&](int i, uint32_t parity, int code) -> bool {
+        if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(i), parity, 1000000))) return true;
+        const uint64_t t0 = globaltimer();
+        const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+#pragma unroll 1
+        do {
+            if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(i), parity, 1000000))) return true;
+            if (__any_sync(0xffffffffu, *abort_flag)) return false;
+        } while (__any_sync(0xffffffffu, globaltimer() - t0 < limit));
+        *abort_flag = 1;
+        atomicExch(a.err, code);
+        return false;
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < N_BARS; ++i) mbar_init(bar(i), i == B_P || i == B_P + 1 ? 4 : 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kSoftmaxWarps + 1) {
+        tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
+
+    if (warp >= kSoftmaxWarps) {
+    // (setmaxnreg is executed by all four warps of a warpgroup)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+    if (warp == kSoftmaxWarps) {
+        // ------------------------------------------------------------ TMA
+        uint32_t issued = 0;
+        bool ok = true;
+        const int n_q_tiles = n_tiles[1] > 0 ? 2 : 1;
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_r);
+            tma_prefetch_desc(&tm_v);
+            for (int t = 0; t < n_q_tiles; ++t) {
+                mbar_arrive_expect_tx(bar(B_Q + t), K_CHUNKS * kChunk);
+                for (int c = 0; c < K_CHUNKS; ++c)
+                    tma_load_3d(sbase + OFF_Q + (t * K_CHUNKS + c) * kChunk, &tm_q, bar(B_Q + t), c * 64, h,
+                                q_base + q0 + t * BM);
+            }
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const int row = k_base + j * BN;
+            for (int c = 0; c < CHUNKS; ++c) {
+                const uint32_t s = issued % RING, round = issued / RING;
+                if (round > 0 && !(ok = wait(B_EMPTY + s, (round - 1) & 1, kErrTimeoutSlot))) break;
+                if (lane == 0) {
+                    const uint32_t dst = sbase + OFF_RING + s * kChunk;
+                    mbar_arrive_expect_tx(bar(B_FULL + s), kChunk);
+                    if (c < 2) tma_load_3d(dst, &tm_k, bar(B_FULL + s), c * 64, h, row);
+                    else if (c == 2) tma_load_2d(dst, &tm_r, bar(B_FULL + s), 0, row);
+                    else tma_load_3d(dst, &tm_v, bar(B_FULL + s), (c - K_CHUNKS) * 64, h, row);
+                }
+                __syncwarp();
+                ++issued;
+            }
+        }
+        if (!ok || __any_sync(0xffffffffu, *abort_flag)) {
+            // let copies already in flight land before the CTA's shared memory goes away
+            if (lane == 0) {
+                for (int t = 0; t < n_q_tiles; ++t) mbar_wait_drain(bar(B_Q + t), 0, a.err, kErrTimeoutLoad);
+                for (uint32_t i = issued > RING ? issued - RING : 0; i < issued; ++i)
+                    mbar_wait_drain(bar(B_FULL + i % RING), (i / RING) & 1, a.err, kErrTimeoutLoad);
+            }
+        }
+    } else if (warp == kSoftmaxWarps + 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // (the whole warp runs the code; one lane issues)
+        const uint32_t one = elect_one();
+        constexpr uint32_t id_s = idesc_f16_f32(BM, BN, false), id_o = idesc_f16_f32(BM, 64, true);
+        const uint64_t q_desc = smem_desc_sw128(sbase + OFF_Q, 16, 1024);
+        const uint64_t x_desc = smem_desc_sw128(sbase + OFF_RING, 16, 1024);
+        const bool stall = stall_first_tile();
+        bool ok = true;
+        // chunk i is there (the first row tile to use it waits; the second finds it so)
+        auto chunk = [&](uint32_t i) { return wait(B_FULL + i % RING, (i / RING) & 1, kErrTimeoutLoad); };
+        auto issue_s = [&](int t, int j) -> bool {
+            if (j >= n_tiles[t]) return true;
+            if (j == 0 && !wait(B_Q + t, 0, kErrTimeoutLoad)) return false;
+#pragma unroll
+            for (int c = 0; c < K_CHUNKS; ++c) {
+                const uint32_t i = j * CHUNKS + c;
+                if (!chunk(i)) return false;
+                tc_fence_after();
+                const uint64_t kd = desc_advance(x_desc, (i % RING) * kChunk);
+                const uint64_t qd = desc_advance(q_desc, (t * K_CHUNKS + c) * kChunk);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_f16_ss_one(one, tmem + t * BN, desc_advance(qd, kk * 32), desc_advance(kd, kk * 32), id_s,
+                                      (c | kk) != 0);
+            }
+            if (!(stall && j == 0)) tc_commit_one(one, bar(B_S + t));
+            return true;
+        };
+        auto issue_pv = [&](int t, int j) -> bool {
+            if (j >= n_tiles[t]) return true;
+            if (!wait(B_P + t, j & 1, kErrTimeoutSoftmax)) return false;
+#pragma unroll
+            for (int c = 0; c < V_CHUNKS; ++c) {
+                const uint32_t i = j * CHUNKS + K_CHUNKS + c;
+                if (!chunk(i)) return false;
+                tc_fence_after();
+                const uint64_t vd = desc_advance(x_desc, (i % RING) * kChunk);
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 8 columns of P, 16 lines of V
+                    tc_mma_f16_ts_one(one, tmem + COL_O + t * HD + c * 64, tmem + t * BN + kk * 8,
+                                      desc_advance(vd, kk * 2048), id_o, (j | kk) != 0);
+            }
+            if (j == n_tiles[t] - 1) tc_commit_one(one, bar(B_DONE + t));
+            return true;
+        };
+        auto release = [&](uint32_t i, int count) {
+            for (int c = 0; c < count; ++c) tc_commit_one(one, bar(B_EMPTY + (i + c) % RING));
+        };
+        if ((ok = issue_s(0, 0) && issue_s(1, 0))) release(0, K_CHUNKS);
+        for (int j = 0; ok && j < n; ++j) {
+            if (!(ok = issue_pv(0, j) && issue_s(0, j + 1))) break;
+            if (!(ok = issue_pv(1, j))) break;
+            release(j * CHUNKS + K_CHUNKS, V_CHUNKS);
+            if (j + 1 < n) {
+                if (!(ok = issue_s(1, j + 1))) break;
+                release((j + 1) * CHUNKS, K_CHUNKS);
+            }
+        }
+        // all issued MMAs must retire before TMEM is released
+        tc_commit_one(one, bar(B_TEARDOWN));
+        if (lane == 0) mbar_wait_drain(bar(B_TEARDOWN), 0, a.err, kErrTimeoutMma);
+        __syncwarp();
+    }
+    } else {
+        // ------------------------------------------------------------ softmax, and the rows out
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
+        const int t = warp >> 2, quarter = warp & 3;
+        const int qi = q0 + t * BM + quarter * 32 + lane;     // this thread's query
+        const int keep = a.causal ? min(L, pos0 + qi + 1) : L;   // it keeps the keys below this
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t s_addr = lanes + t * BN, o_addr = lanes + COL_O + t * HD;
+        const int my_tiles = n_tiles[t];
+        // logits are raw products times scale > 0 in the exponent; another scale goes in first
+        const bool raw = a.scale > 0.f;
+        const float to_log2 = raw ? a.scale * kLog2e : 1.f;
+        float m = -INFINITY, l = 0.f;      // m: of the products times to_log2
+        bool ok = true;
+        for (int j = 0; j < my_tiles; ++j) {
+            if (!(ok = wait(B_S + t, j & 1, kErrTimeoutMma))) break;
+            tc_fence_after();
+            float x[BN];
+            {
+                uint32_t r[BN];
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c)
+                    tc_ld_32x32b_x32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(r + c * 32));
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < BN; ++i) x[i] = __uint_as_float(r[i]);
+            }
+            if (!raw) {
+#pragma unroll
+                for (int i = 0; i < BN; ++i) x[i] *= a.scale * kLog2e;
+            }
+            const int key0 = j * BN;
+            if (key0 + BN > keep) {
+#pragma unroll
+                for (int i = 0; i < BN; ++i)
+                    if (key0 + i >= keep) x[i] = -INFINITY;
+            }
+            // weights against the offset m_off, rounded to f16 and stored over S; returns their sum
+            // (of the rounded ones, so that a row stays a convex combination of values)
+            auto exps = [&](float m_off) -> float {
+                float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                const float2 f2 = make_float2(to_log2, to_log2), nm2 = make_float2(-m_off, -m_off);
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = ffma2(make_float2(x[c * 32 + i], x[c * 32 + i + 1]), f2, nm2);
+                        const __half2 hp = __floats2half2_rn(ex2_approx(y.x), ex2_approx(y.y));
+                        packed[i / 2] = *reinterpret_cast<const uint32_t*>(&hp);
+                        const int k = (i / 2) & 3;
+                        ls[2 * k] = add_f16_lo(ls[2 * k], packed[i / 2]);
+                        ls[2 * k + 1] = add_f16_hi(ls[2 * k + 1], packed[i / 2]);
+                    }
+                    tc_st_32x32b_x16(s_addr + c * 16, packed);
+                }
+                return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+            };
+            // First against the running maximum, without the tile's: a warp with a row whose
+            // weights sum to more than 2^8 (or a NaN, or no key so far) takes the tile's maximum.
+            bool fast = false;
+            if (__all_sync(0xffffffffu, m != -INFINITY)) {
+                const float s = exps(m);
+                fast = __all_sync(0xffffffffu, s <= kFastSumLimit);
+                if (fast) l += s;
+            }
+            if (!fast) {
+                const float top = row_max(x) * to_log2;
+                const bool need = top > m + kRescaleThreshold || (m == -INFINITY && top > -INFINITY);
+                const bool rescale = __any_sync(0xffffffffu, need) && j > 0;
+                float alpha = 1.f;
+                if (need) {
+                    alpha = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                    l *= alpha;
+                    m = top;
+                }
+                l += exps(m == -INFINITY ? 0.f : m);
+                if (rescale) {
+                    // (PV of the tile before is done: S of this one was issued after it)
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tc_ld_32x32b_x32(o_addr + c * 32, r);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                        tc_st_32x32b_x32(o_addr + c * 32, r);
+                    }
+                }
+            }
+            if (key0 + BN > L) {
+                // rows behind the sequence's keys are another's, or nothing: their values are zeroed,
+                // since a weight of 0 must not meet a NaN.  (Both row tiles do it, each before its PV.)
+                const int r0 = max(L - key0, 0), units = (BN - r0) * 8;   // 16 bytes each
+                for (int c = 0; c < V_CHUNKS; ++c) {
+                    const uint32_t i = j * CHUNKS + K_CHUNKS + c;
+                    if (!(ok = wait(B_FULL + i % RING, (i / RING) & 1, kErrTimeoutLoad))) break;
+                    uint8_t* at = smem + OFF_RING + (i % RING) * kChunk + r0 * 128;
+                    for (int u = tid & 127; u < units; u += 128) *reinterpret_cast<uint4*>(at + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                if (!ok) break;
+                fence_proxy_async_smem();
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_P + t));
+        }
+        if (ok && my_tiles > 0) ok = wait(B_DONE + t, 0, kErrTimeoutMma);
+        if (ok && my_tiles > 0) {
+            tc_fence_after();
+            const float inv = l == 0.f ? 0.f : 1.0f / l;   // no key: zeros; NaN stays NaN
+            const int orow = q_base + qi;
+            const bool live = qi < n_q && orow >= 0 && orow < a.total_q;
+            __half* dst = a.out + (static_cast<size_t>(live ? orow : 0) * a.H + h) * HD;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t r[32];
+                tc_ld_32x32b_x32(o_addr + c * 32, r);
+                tc_wait_ld();
+                uint32_t hv[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const __half2 p2 = __floats2half2_rn(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+                    hv[i] = *reinterpret_cast<const uint32_t*>(&p2);
+                }
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4*>(dst + c * 32)[i] = make_uint4(hv[4 * i], hv[4 * i + 1], hv[4 * i + 2], hv[4 * i + 3]);
+                }
+            }
+            if (a.lse && live)
+                a.lse[static_cast<size_t>(orow) * a.H + h] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftmaxWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// f16 rows [rows, H, n] with strides in elements, in boxes of 64 values of 128 rows of a head.
+attn_status rows_map(CUtensorMap* m, const void* base, int n, int H, int rows, long long head_stride, long long stride) {
+    const uint64_t dims[3] = {(uint64_t)n, (uint64_t)H, (uint64_t)rows};
+    const uint64_t strides[2] = {(uint64_t)head_stride * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64u, 1u, (uint32_t)BN};
+    return encode_tmap_sw128(m, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, strides, box);
+}
+
+}  // namespace
+
+attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
+    CUtensorMap tq, tk, tr, tv;
+    attn_status st;
+    if ((st = rows_map(&tq, L.q, HD + RD, L.H, L.total_q, HD + RD, L.q_stride)) != ATTN_OK) return st;
+    if ((st = rows_map(&tk, L.k, HD, L.H, L.total_kv, L.k_head_stride, L.k_stride)) != ATTN_OK) return st;
+    if ((st = rows_map(&tv, L.v, HD, L.H, L.total_kv, L.v_head_stride, L.v_stride)) != ATTN_OK) return st;
+    {
+        const uint64_t dims[2] = {(uint64_t)RD, (uint64_t)L.total_kv};
+        const uint64_t strides[1] = {(uint64_t)L.k_rope_stride * 2};
+        const uint32_t box[2] = {64u, (uint32_t)BN};
+        if ((st = encode_tmap_sw128(&tr, L.k_rope, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, dims, strides, box)) != ATTN_OK)
+            return st;
+    }
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
+        if (cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_ALLOC) !=
+            cudaSuccess)
+            return set_error(ATTN_ECUDA, "cudaFuncSetAttribute(latent prefill smem) failed");
+        if (dev >= 0 && dev < 64) attr_set[dev] = true;
+    }
+    Args a;
+    a.out = static_cast<__half*>(L.out);
+    a.lse = L.lse;
+    a.q_start = L.q_start;
+    a.kv_start = L.kv_start;
+    a.total_q = L.total_q;
+    a.total_kv = L.total_kv;
+    a.max_q = L.max_q;
+    a.H = L.H;
+    a.causal = L.causal;
+    a.scale = L.scale;
+    a.err = L.err_word;
+    const dim3 grid(L.H, (L.max_q - 1) / (2 * BM) + 1, L.B);
+    if (trace_enabled())
+        trace("latent_prefill_kernel grid=(%u,%u,%u) block=%d smem=%u tmem_cols=%u total_q=%d total_kv=%d H=%d causal=%d",
+              grid.x, grid.y, grid.z, kThreads, SMEM_ALLOC, TMEM_COLS, L.total_q, L.total_kv, L.H, L.causal);
+    latent_prefill_kernel<<<grid, kThreads, SMEM_ALLOC, L.stream>>>(tq, tk, tr, tv, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent prefill launch failed: %s", cudaGetErrorString(e));
+    return ATTN_OK;
+}
+
+// Sets this translation unit's test controls (see ptx.cuh).
+attn_status set_test_controls_latent_prefill(unsigned long long wait_limit_ns, int stall) {
+    if (cudaMemcpyToSymbol(g_wait_limit_ns, &wait_limit_ns, sizeof(wait_limit_ns)) != cudaSuccess ||
+        cudaMemcpyToSymbol(g_stall_first_tile, &stall, sizeof(stall)) != cudaSuccess)
+        return set_error(ATTN_ECUDA, "test controls (latent prefill): %s", cudaGetErrorString(cudaGetLastError()));
+    return ATTN_OK;
+}
+
+}  // namespace attn

@@ -473,6 +473,134 @@ attn_status attn_kv_read(const void* k_cache, const void* v_cache, const int32_t
                          void* k_out, void* v_out, attn_dtype out_dtype, void* stream);
 
 /*
+ * Latent attention: one cached row a token serves as key and value of every head.
+ * The row of the token at position p is x_p = [c_p | r_p], f16: its latent vector c
+ * (R = latent_dim values, 256 or 512, as the norm left them) and the key part r
+ * (rope_dim = 64 values) turned to p.  Layouts, row-major:
+ *   contiguous (page_table == NULL)  [B, max_kv, R + 64]; token t of sequence b at [b, t];
+ *   paged  a pool [n_pages, P, R + 64]; token t at [page_table[b, t / P], t % P], P =
+ *          page_size a power of two in 8 .. 1024, page_table i32 [B, max_pages_per_seq].
+ * With c_p, a head's key is k_ph = [W_uk,h c_p | r_p] and its value W_uv,h c_p.  There
+ * are two forms of the same attention:
+ *   absorbed  q_h^T W_uk,h goes into the query (R values beside its rotated part of 64)
+ *             and W_uv,h into what follows: attn_latent_attend reads the cache as it is.
+ *             It reads least: single tokens, drafts, short chunks.
+ *   expanded  attn_latent_read (or the projection itself) gives the rows, one product with
+ *             W_uk, W_uv the heads' key parts and values, and attn_latent_prefill attends:
+ *             a third of the operations a (query, key) pair.  Prompts and long chunks.
+ * (The source pages have no counterpart: attention.js caches keys and values a kv head.)
+ */
+
+/*
+ * attn_latent_append -- new tokens into the latent cache in one pass: c RMS-normed, the
+ * key part and the query heads' parts rotated to the tokens' positions.
+ *
+ *  c, k_rope   device, in_dtype (f16 or f32): row t of c holds R values at c + t * c_stride
+ *                (elements), k_rope 64 at k_rope + t * k_rope_stride.  Strides are multiples
+ *                of 16 bytes, so both may be slices of one projection's rows.
+ *  q_rope      device, in_dtype, or NULL (the cache only): the query heads' 64 values to be
+ *                rotated, head h of token t at q_rope + t * q_stride + h * q_head_stride (a
+ *                slice of [total_q, Hq, 128 + 64] queries, for instance).
+ *  c_norm      device f32 [R] or NULL (no norm): c rsqrt(mean(c^2) + norm_eps) (w + norm_offset).
+ *  rope_cos,   device f32 [rope_positions, 32], both or neither (no rotation): the pairs
+ *  rope_sin      (e, e + 32), or (2e, 2e + 1) if rope_interleaved, e < 32, become
+ *                (a cos - b sin, b cos + a sin).
+ *  q_start, kv_len  device i32 [B+1] and [B], as attn_append takes them: rows q_start[b] ..
+ *                q_start[b+1]-1 are sequence b's newest tokens, kv_len[b] counts them too.
+ *  cache .. max_kv  the cache, as above (max_kv is unused for pages).
+ *  q_out       device f16: the rotated parts, at q_out + t * q_out_stride + h *
+ *                q_out_head_stride: the last 64 values of [total_q, Hq, R + 64] rows for the
+ *                absorbed form, say.  It may be q_rope itself where that is f16 and the strides
+ *                agree (else ATTN_EINVAL); otherwise it must not overlap the inputs.
+ *  Arithmetic is f32 with one rounding to f16 at the end.  Rows of a negative position (a padded
+ *  batch's) and rows behind the last sequence are left alone, in q_out and in the cache.  A
+ *  token at or above the cache's capacity or the tables' rows is left out too, and one whose
+ *  page id lies outside the pool is not written to the cache; both are reported through
+ *  attn_device_status (ATTN_EBOUNDS).  Sequences must not share the pages that the call writes.
+ */
+attn_status attn_latent_append(const void* c, const void* k_rope, const void* q_rope, attn_dtype in_dtype,
+                               long long c_stride, long long k_rope_stride, long long q_stride,
+                               long long q_head_stride, const float* c_norm, float norm_eps, float norm_offset,
+                               const float* rope_cos, const float* rope_sin, int rope_positions, int rope_interleaved,
+                               const int32_t* q_start, const int32_t* kv_len, void* cache, const int32_t* page_table,
+                               int page_size, int max_pages_per_seq, int n_pages, int max_kv, int batch, int total_q,
+                               int n_heads, int latent_dim, int rope_dim, void* q_out, long long q_out_stride,
+                               long long q_out_head_stride, void* stream);
+
+/*
+ * attn_latent_read -- cached rows back as packed c and key-part rows.
+ *
+ *  first, out_start, total  as attn_kv_read takes them: rows out_start[b] ..
+ *                out_start[b+1]-1 receive tokens first[b], first[b] + 1, ... of sequence b
+ *                (first NULL: 0); rows from out_start[B] on are left alone.
+ *  c_out, k_rope_out  device, out_dtype (f16 or f32), [total, R] and [total, 64].
+ *  A token that the cache does not hold (below 0, at or above kv_len or the capacity) is a
+ *  row of zeros; one whose page id lies outside the pool too, and is reported through
+ *  attn_device_status (ATTN_EBOUNDS).
+ */
+attn_status attn_latent_read(const void* cache, const int32_t* kv_len, const int32_t* first, const int32_t* out_start,
+                             const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
+                             int batch, int total, int latent_dim, int rope_dim, void* c_out, void* k_rope_out,
+                             attn_dtype out_dtype, void* stream);
+
+/*
+ * attn_latent_attend -- the absorbed form: the newest tokens of every sequence attend to
+ * their latent cache, o_ih = sum_j softmax_j(scale q_ih . x_j) c_j over j <= kv_len - q_len + i.
+ * One call from single tokens over long contexts to whole prompts.
+ *
+ *  q           device f16 [total_q, Hq, R + 64].
+ *  q_start, kv_len, max_q  as attn_prefill_paged_ex takes them (the new tokens are in the
+ *                cache); rows of a chunk past max_q are not computed.
+ *  cache .. max_kv  the cache, as above.
+ *  scale       of the logits, finite (that of the expanded heads: 1 / sqrt(128 + 64), say).
+ *  out         device f16 [total_q, Hq, R]; lse_out device f32 [total_q, Hq] or NULL.
+ *                Rows behind the last sequence are left alone.
+ *  workspace   device, 256-byte aligned, >= attn_latent_workspace_size(...) bytes (0 for invalid
+ *                sizes); contents need no initialisation.  Calls that may overlap on the GPU
+ *                each need their own.
+ *  A query that keeps no key is a row of zeros, lse -inf.  Cached rows at or above a sequence's
+ *  kv_len are never used, whatever they hold; a NaN or an infinity in a chunk's own token may
+ *  reach the rows of the tokens before it.  The tokens of a page id outside the pool are zeros,
+ *  and it is reported through attn_device_status (ATTN_EBOUNDS).  The weights are rounded to
+ *  f16, relative to about their row's largest, and summed as rounded.
+ */
+size_t attn_latent_workspace_size(int batch, int max_q, int n_heads, int latent_dim);
+attn_status attn_latent_attend(const void* q, const void* cache, const int32_t* q_start, const int32_t* kv_len,
+                               const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
+                               int batch, int total_q, int max_q, int n_heads, int latent_dim, int rope_dim, float scale,
+                               void* out, float* lse_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_latent_prefill -- the expanded form over packed sequences: the n_b queries of sequence b
+ * are the last of its L_b tokens (causal), o_ih = sum_j softmax_j(scale (q_ih[0:128] . k_jh +
+ * q_ih[128:192] . r_j)) v_jh over j <= L_b - n_b + i, or over all L_b keys (causal 0).
+ *
+ *  q           device f16: heads of head_dim + rope_dim (128 + 64) values side by side, token t
+ *                at q + t * q_stride (elements).
+ *  k, v        device f16: the heads' key parts and values, 128 each, head h of token t at
+ *                k + t * k_stride + h * k_head_stride (one product's output of [total_kv, Hq,
+ *                128 + 128], say, is k and v of head stride 256).
+ *  k_rope      device f16: the part all heads share, token t at k_rope + t * k_rope_stride.
+ *  Strides are multiples of 8 elements, addresses 16-byte aligned.
+ *  q_start, kv_start  device i32 [B+1], non-decreasing from 0: sequence b's queries are rows
+ *                q_start[b] .. q_start[b+1]-1, its keys rows kv_start[b] .. kv_start[b+1]-1.
+ *  total_q, total_kv  rows of q, and of k, v and k_rope (total_kv > 0); max_q an upper bound of
+ *                n_b (rows of a longer chunk past it are not computed).
+ *  out         device f16 [total_q, Hq, 128]; lse_out device f32 [total_q, Hq] or NULL (what
+ *                joins this with attention over other keys).  Rows behind the last sequence are
+ *                left alone.
+ *  A query that keeps no key is a row of zeros, lse -inf.  Rows behind a sequence's keys are
+ *  never used for it, whatever they hold; a NaN or an infinity in a token may reach the rows of
+ *  the tokens before it.
+ */
+attn_status attn_latent_prefill(const void* q, const void* k, const void* v, const void* k_rope, long long q_stride,
+                                long long k_stride, long long k_head_stride, long long v_stride,
+                                long long v_head_stride, long long k_rope_stride, const int32_t* q_start,
+                                const int32_t* kv_start, int batch, int total_q, int total_kv, int max_q, int n_heads,
+                                int head_dim, int rope_dim, int causal, float scale, void* out, float* lse_out,
+                                void* stream);
+
+/*
  * attn_decode_validate -- synchronous check of the device-side decode inputs:
  * every kv_len[b] in [1, capacity] and every page id a sequence uses in
  * [0, n_pages).  Launches one small kernel on stream and waits for it.
@@ -491,8 +619,8 @@ attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_tabl
  * attn_device_status -- synchronises stream, then reads and clears the
  * library's device error word.  Returns ATTN_ETIMEOUT if a kernel abandoned a
  * pipeline wait (its output is then invalid), ATTN_EBOUNDS if a call met a page
- * id outside the pool or attn_append a position outside the cache or its
- * tables, else ATTN_OK.
+ * id outside the pool or attn_append or attn_latent_append a position outside the
+ * cache or its tables, else ATTN_OK.
  */
 attn_status attn_device_status(void* stream);
 

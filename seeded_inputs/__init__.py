@@ -42,6 +42,8 @@ __all__ = [
     "make_tiered_case",
     "ChunkCase",
     "make_chunked_case",
+    "LatentCase",
+    "make_latent_case",
     "WORKLOADS",
 ]
 
@@ -242,6 +244,55 @@ class ChunkCase:
             if t is not None:
                 kw[name] = t.to(device)
         return ChunkCase(**kw)
+
+
+@dataclass
+class LatentCase:
+    """A latent cache (attn_latent_*): f16 rows [c (R values) | rotated key part (64)].
+
+    Layouts: cache [B, max_kv, R + 64], or a page pool [n_pages, P, R + 64] with page_table
+    int32 [B, max_pages]; kv_len int32 [B].
+    """
+    cache: torch.Tensor
+    kv_len: torch.Tensor
+    batch: int
+    page_table: Optional[torch.Tensor] = None
+    page_size: int = 0
+    max_pages: int = 0
+    scale: float = 0.0
+
+    def to(self, device: str) -> "LatentCase":
+        kw = dict(self.__dict__)
+        for name in ("cache", "kv_len", "page_table"):
+            if kw[name] is not None:
+                kw[name] = kw[name].to(device)
+        return LatentCase(**kw)
+
+
+def make_latent_case(kv_lens, latent_dim: int, seed: int, *, page_size: int = 0, cap: int = 0, fill: Optional[float] = None,
+                     spare_pages: int = 2, device: str = "cpu") -> LatentCase:
+    """A latent cache for sequences of kv_lens tokens (N(0, 1) rows, or all of one value), with room
+    for ``cap`` tokens each (default: the longest); unused page-table slots hold -1."""
+    B, W = len(kv_lens), latent_dim + 64
+    cap = max(cap, max(kv_lens), 1)
+    table, max_pages = None, 0
+    if page_size:
+        max_pages = -(-cap // page_size)
+        need = [-(-max(n, 0) // page_size) for n in kv_lens]
+        n_pages = sum(need) + spare_pages
+        perm = torch.randperm(n_pages, generator=_gen(seed + 7, "cpu")).to(torch.int32)
+        table, at = torch.full((B, max_pages), -1, dtype=torch.int32), 0
+        for b, n in enumerate(need):
+            table[b, :n] = perm[at:at + n]
+            at += n
+        shape = (n_pages, page_size, W)
+    else:
+        shape = (B, cap, W)
+    cache = (f16_normal(shape, seed, device) if fill is None
+             else torch.full(shape, fill, dtype=torch.float16, device=device))
+    return LatentCase(cache=cache, kv_len=torch.tensor(kv_lens, dtype=torch.int32, device=device), batch=B,
+                      page_table=None if table is None else table.to(device), page_size=page_size,
+                      max_pages=max_pages, scale=1.0 / math.sqrt(192.0))
 
 
 def _lengths(batch: int, lo: int, hi: int, seed: int) -> list:
