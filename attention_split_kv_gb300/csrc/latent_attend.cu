@@ -7,28 +7,27 @@
 // The heads of a sequence's new tokens share the cache's rows, so (token, head) pairs are
 // simply rows of one matrix, token-major as q lies in memory, cut into blocks of NR.
 //
-// The keys are the MMA's M side, the rows its N side:
+//   S = Q X^T      rows x 64 keys     (tcgen05.mma, M = 64: rows past NR are not looked at)
+//   P = 2^(S scale log2e - m)         f16, to shared memory
+//   O^T += C^T P^T   R x NR           (C^T: the tile of X as it lies, read MN-major, 128 values a
+//                                      block; N = NR)
 //
-//   S^T = X Q^T      128 keys x NR     (tcgen05.mma, X as it lies: K-major)
-//   P^T = 2^(S^T scale log2e - m)      f16, to shared memory: a key's NR weights are one line
-//   O^T += C^T P^T   R x NR            (C^T as X's same tile read MN-major, 128 values a block)
+// so a tile of 64 keys comes from memory once and serves both products, few rows (one token of
+// 16 heads) cost products of N = 16 and not of 128 padded rows, and O^T of 512 values fits TMEM
+// for up to 64 rows (4 x 64 columns) beside two S.  A row's logits lie in four threads, so its
+// maximum and sum stay there; O is rescaled lazily (m within 2^8 of the row's maximum), a
+// column a row, by all softmax warps.
 //
-// so a tile of 128 keys comes from memory once and serves both products, few rows (one
-// token of 16 heads) cost MMAs of N = 16 and not of 128 padded rows, and O^T of 512 values
-// fits TMEM beside S^T for up to 64 rows (4 x 64 columns + 64).
-//
-// A row's weights lie along the lanes, so its maximum would be a reduction over 128 threads
-// for every tile.  The running maximum m only has to be within 2^8 of the true one: a tile
-// whose logits all stay below m + 8 (one vote) keeps m; the first tile of a segment and the
-// rare others take the reduction and rescale O.  The row sums stay in the threads, over the
-// rounded weights, and are reduced once a segment.
+// The S of a tile is made while the one before is in the softmax, and tiles lie in a ring of
+// 128-value parts that holds two or three of them: a tile stays until its second product is
+// done, so with tiles of 128 keys the ring held one and the copies stood still meanwhile.
 //
 // Persistent CTAs: the key tiles of all (sequence, row block) items, in that order, are cut
 // into equal runs, one a CTA; rows of items cut by a run's end go to the workspace and are
 // joined by a second kernel.
 //
-// Roles (10 warps): 8 softmax warps (warp w: keys 32 (w % 4) .. + 31, the rows' half w / 4),
-// a TMA warp, an MMA warp.
+// Roles (6 warps): 4 softmax warps (warp w: rows 16 w .. + 15; all four zero what a tile has
+// too much, rescale O and write the rows out, 32 of O^T's lanes each), a TMA warp, an MMA warp.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,52 +38,59 @@
 namespace attn {
 namespace {
 
-constexpr int BN = 128;                     // keys of a tile (TMEM lanes)
+constexpr int BN = 64;                      // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
 constexpr int kMaxCtas = 152;               // one CTA an SM
-constexpr int kSegTiles = 1;                // a segment's fixed cost, in key tiles
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSegTiles = 2;                // a segment's fixed cost, in key tiles
+constexpr int kSoftmaxWarps = 4;
 constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
 constexpr uint32_t kPair = 2 * BN * 128;    // bytes of 128 values of a tile: two 64-value chunks
-constexpr uint32_t kRope = BN * 128;        // of its rotated part, and of P
+constexpr uint32_t kRope = BN * 128;        // of its rotated part
 
-// instruction descriptors: f16 operands, f32 accumulation; A and B majors (1: MN)
-__host__ __device__ constexpr uint32_t idesc(uint32_t N, uint32_t a_mn, uint32_t b_mn) {
-    return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((128u >> 4) << 24);
+// instruction descriptor: f16 operands, f32 accumulation; A's major (1: MN), B K-major
+__host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_mn) {
+    return (1u << 4) | (a_mn << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 // NP: blocks of 128 latent values; NR: rows of a block.
 template <int NP, int NR>
 struct Cfg {
     static constexpr int R = NP * 128, W = R + 64, NCH = 2 * NP + 1;
-    static constexpr int NH = NR / 2;                      // rows of a softmax thread
     static constexpr uint32_t Q_CHUNK = NR * 128, Q_BYTES = NCH * Q_CHUNK;
-    // where shared memory is short P takes the place of the tile's rotated part, which only S needs
-    static constexpr bool ALIAS = NP == 4 && NR >= 32;
-    static constexpr int NPS = NR == 64 ? 4 : 5;           // 128-value slots
+    // 64 rows of 512 values: P takes the place of its tile's rotated part, which only S needs
+    static constexpr bool ALIAS = NP == 4 && NR == 64;
+    static constexpr int NPS = NP == 2 || NR == 64 ? 8 : NR == 32 ? 10 : 11;   // 128-value parts
+    static constexpr int NRS = NP == 2 ? 4 : NR == 16 ? 3 : 2;                 // rotated parts
+    static constexpr uint32_t P_BYTES = NR * 128;
     static constexpr uint32_t OFF_Q = 0;
     static constexpr uint32_t OFF_PAIR = (Q_BYTES + 1023) / 1024 * 1024;
     static constexpr uint32_t OFF_ROPE = OFF_PAIR + NPS * kPair;
-    static constexpr uint32_t OFF_P = ALIAS ? OFF_ROPE : OFF_ROPE + kRope;
-    static constexpr uint32_t OFF_ROWS = OFF_P + kRope;    // lim, m, alpha, wmax[4], wl[4]: NR words each
-    enum : int { A_LIM, A_M, A_ALPHA, A_WMAX, A_WL = A_WMAX + 4, N_ROWS = A_WL + 4 };
-    static constexpr uint32_t OFF_FLAGS = OFF_ROWS + N_ROWS * NR * 4;   // [2][8] words
-    static constexpr uint32_t OFF_SUMS = OFF_FLAGS + 64;   // the run's search
+    static constexpr uint32_t OFF_P = ALIAS ? OFF_ROPE : OFF_ROPE + NRS * kRope;
+    static constexpr uint32_t OFF_ROWS = OFF_ROPE + NRS * kRope + (ALIAS ? 0 : 2 * P_BYTES);
+    // words of the rows: rescale factors of two tiles, then 1 / sum of two segments
+    static constexpr uint32_t OFF_FLAGS = OFF_ROWS + 4 * NR * 4;   // [2][4] words
+    static constexpr uint32_t OFF_SUMS = OFF_FLAGS + 32;           // the run's search
     enum : int {
-        B_QFULL, B_QEMPTY, B_PAIR, B_PAIRFREE = B_PAIR + NPS, B_ROPE = B_PAIRFREE + NPS, B_ROPEFREE, B_S, B_P,
-        B_DONE,      // a segment's last product is done
-        B_GROUP,     // the softmax warps met
+        B_QFULL, B_QEMPTY, B_PAIR, B_PAIRFREE = B_PAIR + NPS, B_ROPE = B_PAIRFREE + NPS, B_ROPEFREE = B_ROPE + NRS,
+        B_S = B_ROPEFREE + NRS,
+        B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
+        B_PV = B_P + 2,            // a tile's second product is done
+        B_DONE,            // a segment's last one is
+        B_FIX,             // O is rescaled
+        B_MEET,            // the softmax warps met
         B_TEARDOWN, N_BARS
     };
-    static constexpr uint32_t OFF_BAR = OFF_SUMS + 24 * 8 + 32;
+    static constexpr uint32_t OFF_BAR = OFF_SUMS + 24 * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
-    static constexpr uint32_t COL_O = NR, COLS = NR + NP * NR;
-    static constexpr uint32_t TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static constexpr uint32_t COL_O = 2 * BN, COLS = COL_O + NP * NR;
+    static constexpr uint32_t TMEM_COLS = COLS <= 256 ? 256 : 512;
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
     static_assert(OFF_SUMS % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
+    // S's A operand is read as 64 rows: past NR those are whatever follows Q's chunk
+    static_assert(OFF_Q + (NCH - 1) * Q_CHUNK + 64 * 128 <= OFF_ROWS, "Q's rows past NR");
 };
 
 struct Args {
@@ -99,11 +105,11 @@ struct Args {
     int log2P, max_pages, n_slots, box_rows;   // pages, or the contiguous cache's sequences
     int n_rb;            // row blocks of the longest chunk
     int side;            // row blocks of a sequence that neighbouring CTAs take side by side
-    long long capacity;
+    int capacity;
     float scale;
 };
 
-// One sequence's new tokens.
+// One sequence's new tokens.  (Rows, tokens x heads, stay below 2^31: the host checks.)
 struct Chunk {
     int q_base, n, pos0, L;   // first token row, tokens computed, position of token 0, cached keys
 };
@@ -113,23 +119,24 @@ __device__ __forceinline__ Chunk load_chunk(const Args& a, int b) {
     const int n_q = max(a.q_start[b + 1] - c.q_base, 0), len = a.kv_len[b];
     c.n = min(n_q, a.max_q);
     c.pos0 = len - n_q;
-    c.L = static_cast<int>(min(static_cast<long long>(max(len, 0)), a.capacity));
+    c.L = min(max(len, 0), a.capacity);
     return c;
 }
-// groups of row blocks that are taken side by side
+// groups of row blocks that are taken side by side (more than one block only where every chunk
+// is one token: one group)
 template <int NR>
 __device__ __forceinline__ int groups_of(const Args& a, const Chunk& c) {
-    const long long blocks = (static_cast<long long>(c.n) * a.H + NR - 1) / NR;
-    return static_cast<int>((blocks + a.side - 1) / a.side);
+    return a.side > 1 ? min(c.n, 1) : static_cast<int>((static_cast<uint32_t>(c.n * a.H) + NR - 1) / NR);
 }
 // keys that some row of the rows up to `end` (not included) keeps lie below this
-__device__ __forceinline__ int key_end(const Args& a, const Chunk& c, long long end) {
-    const long long last = min(end, static_cast<long long>(c.n) * a.H) - 1;
-    return static_cast<int>(max(0ll, min(static_cast<long long>(c.L), c.pos0 + last / a.H + 1)));
+__device__ __forceinline__ int key_end(const Args& a, const Chunk& c, uint32_t end) {
+    const uint32_t last = min(end, static_cast<uint32_t>(c.n * a.H)) - 1;
+    const long long token = c.n > 1 ? last / static_cast<uint32_t>(a.H) : 0;
+    return static_cast<int>(max(0ll, min(static_cast<long long>(c.L), c.pos0 + token + 1)));
 }
 template <int NR>
 __device__ __forceinline__ int group_tiles(const Args& a, const Chunk& c, int g) {
-    return max((key_end(a, c, static_cast<long long>(g + 1) * a.side * NR) + BN - 1) / BN, 1);
+    return max((key_end(a, c, static_cast<uint32_t>(g + 1) * (a.side * NR)) + BN - 1) / BN, 1);
 }
 
 // A CTA's run of key tiles, walked a segment (part of one item) at a time.  Every warp walks
@@ -163,64 +170,19 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
     return walk_item<NR>(a, w);
 }
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[N]) {
-    if constexpr (N == 32) {
-        tc_ld_32x32b_x32(addr, r);
-    } else if constexpr (N == 16) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-            : "r"(addr));
-    } else {
-        static_assert(N == 8, "columns");
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(addr));
-    }
-}
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t (&r)[N]) {
-    if constexpr (N == 32) {
-        tc_st_32x32b_x32(addr, r);
-    } else if constexpr (N == 16) {
-        tc_st_32x32b_x16(addr, r);
-    } else {
-        static_assert(N == 8, "columns");
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]),
-                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                     : "memory");
-    }
-}
-
-// N values of each lane reduced over the warp's lanes: lane l ends up with that of value
-// l / (32 / N), in N - 1 + log2(32 / N) shuffles.
-template <int N, typename Op>
-__device__ __forceinline__ float reduce_lanes(const float (&x)[N], int lane, Op op) {
-    float v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = x[i];
-    int o = 16;
-#pragma unroll
-    for (int w = N / 2; w > 0; w >>= 1, o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-            const float keep = up ? v[i + w] : v[i], send = up ? v[i] : v[i + w];
-            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-    }
-#pragma unroll
-    for (; o > 0; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-    return v[0];
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
 }
 
 template <int NP, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x, const Args a) {
     using C = Cfg<NP, NR>;
-    constexpr int NH = C::NH, NPS = C::NPS;
+    constexpr int NPS = C::NPS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -229,6 +191,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be set up meanwhile
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    if (tid == kSoftmaxWarps * 32) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_x);
+    }
     // A wait of a whole warp, with one answer for all of its lanes.
     auto wait = [&](int b, uint32_t parity, int code) -> bool {
         if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(b), parity, 1000000))) return true;
@@ -249,8 +215,9 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     Walk run;
     {
         constexpr int kWarps = kThreads / 32;
+        static_assert(2 * kWarps <= 20, "scratch");
         long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);   // [2][warps], then the run's ends
-        int* first = reinterpret_cast<int*>(sums + 24);
+        int* first = reinterpret_cast<int*>(sums + 22);
         const int max_g = (a.n_rb + a.side - 1) / a.side;
         const long long pairs = static_cast<long long>(a.B) * max_g;
         const long long per = (pairs + kThreads - 1) / kThreads;
@@ -291,9 +258,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         if (tid == 0) {
             for (int i = 0; i < C::N_BARS; ++i)
-                mbar_init(bar(i), i == C::B_P || i == C::B_GROUP ? kSoftmaxWarps : 1);
+                mbar_init(bar(i), (i >= C::B_P && i < C::B_P + 2) || i == C::B_FIX || i == C::B_MEET ? kSoftmaxWarps : 1);
             *abort_flag = 0;
-            first[3] = 0;
             fence_barrier_init();
         }
         if (warp == kSoftmaxWarps + 1) {
@@ -315,13 +281,17 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         // as many runs as CTAs, or fewer of a key tile at least (a run's weight is above kSegTiles)
         const int rank = static_cast<int>(blockIdx.x) / a.side;
-        const long long runs = max(1ll, min(static_cast<long long>(gridDim.x / a.side), total / (kSegTiles + 1)));
+        const int most = static_cast<int>(gridDim.x) / a.side;
+        const int runs = total >= static_cast<long long>(most) * (kSegTiles + 1) ? most : max(1, static_cast<int>(total) / (kSegTiles + 1));
+        const long long each = total < (1ll << 31) ? static_cast<uint32_t>(total) / static_cast<uint32_t>(runs) : total / runs;
+        const long long more = total - each * runs;
         if (tid == 0) sums[20] = sums[21] = total_t;
         __syncthreads();
         if (rank < runs) {
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
-                const long long t = total * (rank + e) / runs;
+                // (the first total % runs runs have one more)
+                const long long t = each * (rank + e) + min(static_cast<long long>(rank + e), more);
                 if (before > t || t >= before + mine) continue;
                 long long acc = before, acc_t = before_t;
                 visit([&](int b, int g, int n) {
@@ -356,19 +326,15 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // 128-value pair; the boxes of the rotated part are lanes 0 .. nb - 1.
         const int nb = BN / a.box_rows, bx = lane & (nb - 1), P = 1 << a.log2P;
         uint32_t n_pair = 0, n_tile = 0, n_seg = 0, n_q = 0;   // (copies posted)
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            tma_prefetch_desc(&tm_x);
-        }
         bool ok = true;
         Walk w = run;
         for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
-            const long long row0 = (static_cast<long long>(w.g) * a.side + rb_in) * NR;
+            const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int hi = key_end(a, w.c, row0 + NR);
             if (n_seg > 0 && !(ok = wait(C::B_QEMPTY, (n_seg - 1) & 1, kErrTimeoutSlot))) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(C::B_QFULL), C::Q_BYTES);
-                const int q_row = static_cast<int>(static_cast<long long>(w.c.q_base) * a.H + row0);
+                const int q_row = static_cast<int>(w.c.q_base * static_cast<uint32_t>(a.H) + row0);
                 for (int c = 0; c < C::NCH; ++c)
                     tma_load_2d(sbase + C::OFF_Q + c * C::Q_CHUNK, &tm_q, bar(C::B_QFULL), c * 64, q_row);
             }
@@ -410,12 +376,14 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                 }
                 if (!ok) break;
-                if (n_tile > 0 && !(ok = wait(C::B_ROPEFREE, (n_tile - 1) & 1, kErrTimeoutSlot))) break;
+                const uint32_t rs = n_tile % C::NRS, round = n_tile / C::NRS;
+                if (round > 0 && !(ok = wait(C::B_ROPEFREE + rs, (round - 1) & 1, kErrTimeoutSlot))) break;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(bar(C::B_ROPE), static_cast<uint32_t>(boxes * a.box_rows) * 128);
+                    mbar_arrive_expect_tx(bar(C::B_ROPE + rs), static_cast<uint32_t>(boxes * a.box_rows) * 128);
                 __syncwarp();
                 if (has && lane < nb)
-                    tma_load_3d(sbase + C::OFF_ROPE + bx * a.box_rows * 128, &tm_x, bar(C::B_ROPE), C::R, row, cur);
+                    tma_load_3d(sbase + C::OFF_ROPE + rs * kRope + bx * a.box_rows * 128, &tm_x, bar(C::B_ROPE + rs), C::R,
+                                row, cur);
             }
         }
         if (!ok || __any_sync(0xffffffffu, *abort_flag)) {
@@ -424,62 +392,104 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (n_q > 0) mbar_wait_drain(bar(C::B_QFULL), (n_q - 1) & 1, a.err, kErrTimeoutLoad);
                 for (uint32_t i = n_pair > NPS ? n_pair - NPS : 0; i < n_pair; ++i)
                     mbar_wait_drain(bar(C::B_PAIR + i % NPS), (i / NPS) & 1, a.err, kErrTimeoutLoad);
-                if (n_tile > 0) mbar_wait_drain(bar(C::B_ROPE), (n_tile - 1) & 1, a.err, kErrTimeoutLoad);
+                for (uint32_t i = n_tile > C::NRS ? n_tile - C::NRS : 0; i < n_tile; ++i)
+                    mbar_wait_drain(bar(C::B_ROPE + i % C::NRS), (i / C::NRS) & 1, a.err, kErrTimeoutLoad);
             }
         }
     } else if (warp == kSoftmaxWarps + 1) {
         // ------------------------------------------------------------ MMA issuer
         // (the whole warp runs the code; one lane issues)
         const uint32_t one = elect_one();
-        constexpr uint32_t id_s = idesc(NR, 0, 0), id_o = idesc(NR, 1, 1);
+        constexpr uint32_t id_s = idesc(64, BN, 0), id_o = idesc(128, NR, 1);
         const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
         const uint64_t x_desc = smem_desc_sw128(sbase + C::OFF_PAIR, 16, 1024);
         const uint64_t r_desc = smem_desc_sw128(sbase + C::OFF_ROPE, 16, 1024);
         const uint64_t c_desc = smem_desc_sw128(sbase + C::OFF_PAIR, BN * 128, 1024);   // MN-major: next 64 values
         const uint64_t p_desc = smem_desc_sw128(sbase + C::OFF_P, 16, 1024);
-        bool stall = stall_first_tile(), ok = true;
-        uint32_t n_tile = 0, n_seg = 0;
+        const int* flags = reinterpret_cast<const int*>(smem + C::OFF_FLAGS);
+        const bool stall = stall_first_tile();
+        bool ok = true;
+        uint32_t n_tile = 0, n_seg = 0, n_fix = 0;
+        auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity)) != 0; };
         Walk w = run;
         for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
             if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
-            for (int j = 0; j < w.n; ++j, ++n_tile) {
-                const uint32_t pair0 = n_tile * NP;
-                for (int p = 0; p < NP; ++p) {
-                    const uint32_t s = (pair0 + p) % NPS;
-                    if (!(ok = wait(C::B_PAIR + s, ((pair0 + p) / NPS) & 1, kErrTimeoutLoad))) break;
+            // What is ready is issued: the second product of tile v, which gives its place in the
+            // ring free, else the next part of S of tile s (at most one tile ahead: of two S).
+            // Waiting for a part before a second product held up the copies that it would have
+            // given room.
+            int js = 0, part = 0, jv = 0;
+            uint32_t spins = 0;
+            uint64_t t0 = 0;
+            while (jv < w.n) {
+                const uint32_t iv = n_tile + jv, is = n_tile + js;
+                if (jv < js && ready(C::B_P + (iv & 1), (iv >> 1) & 1)) {
+                    if (jv > 0) {
+                        const int* f = flags + (iv & 1) * kSoftmaxWarps;
+                        if ((f[0] | f[1] | f[2] | f[3]) && !(ok = wait(C::B_FIX, n_fix++ & 1, kErrTimeoutSoftmax))) break;
+                    }
                     tc_fence_after();
-                    const uint64_t xd = desc_advance(x_desc, s * kPair), qd = desc_advance(q_desc, p * 2 * C::Q_CHUNK);
+                    const uint64_t pd = desc_advance(p_desc, C::ALIAS ? (iv % C::NRS) * kRope : (iv & 1) * C::P_BYTES);
+                    for (int p = 0; p < NP; ++p) {
+                        const uint32_t s = (iv * NP + p) % NPS;
+                        const uint64_t cd = desc_advance(c_desc, s * kPair);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                        for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of X, 32 bytes of P's
+                            tc_mma_f16_ss_one(one, tmem + C::COL_O + p * NR, desc_advance(cd, kk * 2048),
+                                              desc_advance(pd, kk * 32), id_o, (jv | kk) != 0);
+                        tc_commit_one(one, bar(C::B_PAIRFREE + s));
+                    }
+                    if (C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + iv % C::NRS));
+                    tc_commit_one(one, bar(C::B_PV));
+                    if (++jv == w.n) tc_commit_one(one, bar(C::B_DONE));
+                    spins = 0;
+                    continue;
+                }
+                const uint32_t k = is * NP + part, rs = is % C::NRS;
+                if (js < w.n && js <= jv + 1 &&
+                    (part < NP ? ready(C::B_PAIR + k % NPS, (k / NPS) & 1) : ready(C::B_ROPE + rs, (is / C::NRS) & 1))) {
+                    tc_fence_after();
+                    const uint32_t s_tmem = tmem + (is & 1) * BN;
+                    const uint64_t qd = desc_advance(q_desc, part * 2 * C::Q_CHUNK);
+                    if (part < NP) {
+                        const uint64_t xd = desc_advance(x_desc, (k % NPS) * kPair);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, c * C::Q_CHUNK + kk * 32),
+                                                  desc_advance(xd, c * (BN * 128) + kk * 32), id_s, (part | c | kk) != 0);
+                        ++part;
+                    } else {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_f16_ss_one(one, tmem, desc_advance(xd, c * (BN * 128) + kk * 32),
-                                              desc_advance(qd, c * C::Q_CHUNK + kk * 32), id_s, (p | c | kk) != 0);
+                            tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, kk * 32), desc_advance(r_desc, rs * kRope + kk * 32),
+                                              id_s, 1);
+                        if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + rs));
+                        if (!(stall && is == 0)) tc_commit_one(one, bar(C::B_S + (is & 1)));
+                        part = 0;
+                        if (++js == w.n) tc_commit_one(one, bar(C::B_QEMPTY));
+                    }
+                    spins = 0;
+                    continue;
                 }
-                if (!ok || !(ok = wait(C::B_ROPE, n_tile & 1, kErrTimeoutLoad))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_f16_ss_one(one, tmem, desc_advance(r_desc, kk * 32),
-                                      desc_advance(q_desc, 2 * NP * C::Q_CHUNK + kk * 32), id_s, 1);
-                if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE));
-                if (j == w.n - 1) tc_commit_one(one, bar(C::B_QEMPTY));
-                if (!stall) tc_commit_one(one, bar(C::B_S));
-                stall = false;
-                if (!(ok = wait(C::B_P, n_tile & 1, kErrTimeoutSoftmax))) break;
-                tc_fence_after();
-                for (int p = 0; p < NP; ++p) {
-                    const uint32_t s = (pair0 + p) % NPS;
-                    const uint64_t cd = desc_advance(c_desc, s * kPair);
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of 128 bytes
-                        tc_mma_f16_ss_one(one, tmem + C::COL_O + p * NR, desc_advance(cd, kk * 2048),
-                                          desc_advance(p_desc, kk * 2048), id_o, (j | kk) != 0);
-                    tc_commit_one(one, bar(C::B_PAIRFREE + s));
+                // neither: the bounded wait of ptx.cuh
+                if (spins++ == 0) {
+                    t0 = globaltimer();
+                } else if ((spins & 63) == 0) {
+                    if (__any_sync(0xffffffffu, *abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (__any_sync(0xffffffffu, globaltimer() - t0 > *static_cast<volatile unsigned long long*>(&g_wait_limit_ns))) {
+                        *abort_flag = 1;
+                        atomicExch(a.err, kErrTimeoutSoftmax);
+                        ok = false;
+                        break;
+                    }
                 }
-                if (C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE));
-                if (j == w.n - 1) tc_commit_one(one, bar(C::B_DONE));
             }
+            n_tile += w.n;
         }
         // all issued MMAs must retire before TMEM is released
         tc_commit_one(one, bar(C::B_TEARDOWN));
@@ -487,138 +497,136 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax, and the rows out
-        const int quarter = warp & 3, half = warp >> 2;
-        const int key_in = quarter * 32 + lane;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        float* rows = reinterpret_cast<float*>(smem + C::OFF_ROWS);
-        int* lim = reinterpret_cast<int*>(rows + C::A_LIM * NR) + half * NH;   // this half's rows
-        float* m = rows + C::A_M * NR + half * NH;
-        float* alpha = rows + C::A_ALPHA * NR + half * NH;
-        float* wmax = rows + C::A_WMAX * NR + half * NH;
-        float* wl = rows + C::A_WL * NR + half * NH;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const bool has_rows = warp * 16 < NR;
+        const int ra = warp * 16 + (lane >> 2), rb = ra + 8;   // this thread's rows of the block
+        float* factors = reinterpret_cast<float*>(smem + C::OFF_ROWS);   // [2][NR]
         volatile int* flags = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS);
         const float scale_log2 = a.scale * kLog2e;
-        uint32_t n_meet = 0, n_tile = 0, n_seg = 0;
-        // the 8 warps meet; writes to shared memory before it are seen after it
+        uint32_t n_tile = 0, n_meet = 0, n_seg = 0;
+        // the 4 warps meet; writes to shared memory before it are seen after it
         auto meet = [&]() -> bool {
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_GROUP));
-            return wait(C::B_GROUP, n_meet++ & 1, kErrTimeoutSoftmax);
+            if (lane == 0) mbar_arrive(bar(C::B_MEET));
+            return wait(C::B_MEET, n_meet++ & 1, kErrTimeoutSoftmax);
+        };
+        // After tile i (not a segment's first): once all warps have written their weights, if a row
+        // moved its maximum, every warp rescales its lanes of O before the tile's second product.
+        auto fix = [&](uint32_t i) -> bool {
+            if (!wait(C::B_P + (i & 1), (i >> 1) & 1, kErrTimeoutSoftmax)) return false;
+            const int f = lane < kSoftmaxWarps ? flags[(i & 1) * kSoftmaxWarps + lane] : 0;
+            if (!__any_sync(0xffffffffu, f)) return true;
+            // (S of tile i came after the product of i - 2, and that of i waits for this: i - 1 is the
+            // one phase that may be open)
+            if (!wait(C::B_PV, (i - 1) & 1, kErrTimeoutMma)) return false;
+            tc_fence_after();
+            const float* at = factors + (i & 1) * NR;
+#pragma unroll 1
+            for (int p = 0; p < NP * NR / 16; ++p) {
+                uint32_t r[16];
+                tmem_load16(lanes + C::COL_O + p * 16, r);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(at + (p * 16) % NR + e);
+                    r[e] = __float_as_uint(__uint_as_float(r[e]) * x.x);
+                    r[e + 1] = __float_as_uint(__uint_as_float(r[e + 1]) * x.y);
+                    r[e + 2] = __float_as_uint(__uint_as_float(r[e + 2]) * x.z);
+                    r[e + 3] = __float_as_uint(__uint_as_float(r[e + 3]) * x.w);
+                }
+                tc_st_32x32b_x16(lanes + C::COL_O + p * 16, r);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_FIX));
+            return true;
         };
         if (tid == 0) a.meta[blockIdx.x * 4] = a.meta[blockIdx.x * 4 + 1] = 0;
         bool ok = true;
         Walk w = run;
         for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
-            const long long row0 = (static_cast<long long>(w.g) * a.side + rb_in) * NR;
+            const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int live = static_cast<int>(max(0ll, min(static_cast<long long>(NR), static_cast<long long>(w.c.n) * a.H - row0)));
             const int hi = key_end(a, w.c, row0 + NR);
-            // keys below this are kept by every row of the block
-            const int all_keep = live > 0 ? key_end(a, w.c, row0 + 1) : 0;
-            if (tid < NR) reinterpret_cast<int*>(rows)[tid] = tid < live ? key_end(a, w.c, row0 + tid + 1) : 0;
-            float l[NH];
-#pragma unroll
-            for (int i = 0; i < NH; ++i) l[i] = 0.f;
-            if (!(ok = meet())) break;
+            // rows keep the keys below lim; no row of the warp drops a key below all_keep
+            const int lim_a = key_end(a, w.c, row0 + ra + 1), lim_b = key_end(a, w.c, row0 + rb + 1);
+            const int all_keep = key_end(a, w.c, row0 + warp * 16 + 1);
+            // maxima in log2 units; +inf for what is not a row of the block: no weight
+            float m_a = ra < live ? -INFINITY : INFINITY, m_b = rb < live ? -INFINITY : INFINITY;
+            float2 l_a = make_float2(0.f, 0.f), l_b = make_float2(0.f, 0.f);
             for (int j = 0; j < w.n; ++j, ++n_tile) {
-                if (!(ok = wait(C::B_S, n_tile & 1, kErrTimeoutMma))) break;
+                if (j > 1 && !(ok = fix(n_tile - 1))) break;
+                if (!(ok = wait(C::B_S + (n_tile & 1), (n_tile >> 1) & 1, kErrTimeoutMma))) break;
                 tc_fence_after();
-                float x[NH];
-                {
-                    uint32_t r[NH];
-                    tmem_load<NH>(lanes + half * NH, r);
-                    tc_wait_ld();
+                const int key0 = (w.off + j) * BN;
+                if (has_rows) {
+                    // columns 8 i + 2 (lane % 4), + 1: row a in x[4 i], x[4 i + 1], row b in the next two
+                    float x[32];
+                    {
+                        uint32_t r[32];
+                        tc_ld_16x256b_x8(lanes + (n_tile & 1) * BN, r);
+                        tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < NH; ++i) x[i] = __uint_as_float(r[i]) * scale_log2;
-                }
-                const int key0 = (w.off + j) * BN, key = key0 + key_in;
-                if (key0 + BN > all_keep) {
-#pragma unroll
-                    for (int i = 0; i < NH; i += 4) {
-                        const int4 e = *reinterpret_cast<const int4*>(lim + i);
-                        x[i] = key < e.x ? x[i] : -INFINITY;
-                        x[i + 1] = key < e.y ? x[i + 1] : -INFINITY;
-                        x[i + 2] = key < e.z ? x[i + 2] : -INFINITY;
-                        x[i + 3] = key < e.w ? x[i + 3] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]) * scale_log2;
                     }
-                }
-                bool above = j == 0;
-                if (j > 0) {
-                    float over = -INFINITY;
+                    if (key0 + BN > all_keep) {
+                        const int k0 = key0 + 2 * (lane & 3);
 #pragma unroll
-                    for (int i = 0; i < NH; i += 4) {
-                        const float4 e = *reinterpret_cast<const float4*>(m + i);
-                        over = fmaxf(fmaxf(over, x[i] - e.x), x[i + 1] - e.y);
-                        over = fmaxf(fmaxf(over, x[i + 2] - e.z), x[i + 3] - e.w);
+                        for (int i = 0; i < 32; ++i)
+                            if (k0 + (i >> 2) * 8 + (i & 1) >= ((i & 2) ? lim_b : lim_a)) x[i] = -INFINITY;
                     }
-                    const int any = __any_sync(0xffffffffu, over > kRescaleThreshold);
+                    float ta = fmaxf(x[0], x[1]), tb = fmaxf(x[2], x[3]);
+#pragma unroll
+                    for (int i = 4; i < 32; i += 4) {
+                        ta = fmaxf(ta, fmaxf(x[i], x[i + 1]));
+                        tb = fmaxf(tb, fmaxf(x[i + 2], x[i + 3]));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
+                        tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
+                    }
+                    float f_a = 1.f, f_b = 1.f;
+                    const bool need_a = ta > m_a + kRescaleThreshold, need_b = tb > m_b + kRescaleThreshold;
+                    if (need_a) {
+                        f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - ta);
+                        l_a = fmul2(l_a, make_float2(f_a, f_a));
+                        m_a = ta;
+                    }
+                    if (need_b) {
+                        f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - tb);
+                        l_b = fmul2(l_b, make_float2(f_b, f_b));
+                        m_b = tb;
+                    }
+                    if ((lane & 3) == 0) {
+                        factors[(n_tile & 1) * NR + ra] = f_a;
+                        factors[(n_tile & 1) * NR + rb] = f_b;
+                    }
+                    const int any = __any_sync(0xffffffffu, need_a || need_b);
                     if (lane == 0) flags[(n_tile & 1) * kSoftmaxWarps + warp] = any;
-                    if (!(ok = meet())) break;
-                    above = __any_sync(0xffffffffu, lane < kSoftmaxWarps && flags[(n_tile & 1) * kSoftmaxWarps + lane]);
-                }
-                if (above) {
-                    // the rows' maxima over the tile: over the warp's lanes, then over the quarters
-                    const float top = reduce_lanes<NH>(x, lane, [](float p, float q) { return fmaxf(p, q); });
-                    if (lane % (32 / NH) == 0) wmax[quarter * NR + lane / (32 / NH)] = top;
-                    if (!(ok = meet())) break;
-                    if (quarter == 0 && lane < NH) {
-                        const float t = fmaxf(fmaxf(wmax[lane], wmax[NR + lane]), fmaxf(wmax[2 * NR + lane], wmax[3 * NR + lane]));
-                        const float old = j == 0 ? -INFINITY : m[lane];
-                        float now = old, f = 1.f;
-                        if (half * NH + lane >= live) {
-                            now = INFINITY;   // not a row: no weight
-                        } else if (t > old + kRescaleThreshold) {
-                            now = t;
-                            f = old == -INFINITY ? 0.f : ex2_approx(old - t);
-                        }
-                        m[lane] = now;
-                        alpha[lane] = f;
+                    // (a row that has kept no key yet: all of its x are -inf)
+                    const float o_a = m_a == -INFINITY ? 0.f : m_a, o_b = m_b == -INFINITY ? 0.f : m_b;
+                    // a row's line of P is its 64 weights, swizzled as the MMA reads it (both rows alike,
+                    // ra % 8 == rb % 8)
+                    uint8_t* line = smem + C::OFF_P + (C::ALIAS ? (n_tile % C::NRS) * kRope : (n_tile & 1) * C::P_BYTES) +
+                                    ra * 128 + (lane & 3) * 4;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __half2 ha = __floats2half2_rn(ex2_approx(x[4 * i] - o_a), ex2_approx(x[4 * i + 1] - o_a));
+                        const __half2 hb = __floats2half2_rn(ex2_approx(x[4 * i + 2] - o_b), ex2_approx(x[4 * i + 3] - o_b));
+                        const uint32_t pa = *reinterpret_cast<const uint32_t*>(&ha), pb = *reinterpret_cast<const uint32_t*>(&hb);
+                        l_a.x = add_f16_lo(l_a.x, pa);
+                        l_a.y = add_f16_hi(l_a.y, pa);
+                        l_b.x = add_f16_lo(l_b.x, pb);
+                        l_b.y = add_f16_hi(l_b.y, pb);
+                        const int u = (i ^ (ra & 7)) << 4;
+                        *reinterpret_cast<uint32_t*>(line + u) = pa;
+                        *reinterpret_cast<uint32_t*>(line + u + 8 * 128) = pb;
                     }
-                    if (!(ok = meet())) break;
-                    if (j > 0) {
-                        // (the product of the tile before is done: S of this one was issued after it)
-                        float f[NH];
-#pragma unroll
-                        for (int i = 0; i < NH; ++i) {
-                            f[i] = alpha[i];
-                            l[i] *= f[i];
-                        }
-#pragma unroll 1
-                        for (int p = 0; p < NP; ++p) {
-                            uint32_t r[NH];
-                            const uint32_t at = lanes + C::COL_O + p * NR + half * NH;
-                            tmem_load<NH>(at, r);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < NH; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f[i]);
-                            tmem_store<NH>(at, r);
-                        }
-                        tc_wait_st();
-                    }
+                } else if (lane == 0) {
+                    flags[(n_tile & 1) * kSoftmaxWarps + warp] = 0;
                 }
-                // weights: a key's line of P, swizzled as the MMA reads it
-                uint32_t packed[NH / 2];
-#pragma unroll
-                for (int i = 0; i < NH; i += 4) {
-                    float4 e = *reinterpret_cast<const float4*>(m + i);
-                    // (a row that has kept no key yet: all of x is -inf)
-                    e.x = e.x == -INFINITY ? 0.f : e.x;
-                    e.y = e.y == -INFINITY ? 0.f : e.y;
-                    e.z = e.z == -INFINITY ? 0.f : e.z;
-                    e.w = e.w == -INFINITY ? 0.f : e.w;
-                    const __half2 h0 = __floats2half2_rn(ex2_approx(x[i] - e.x), ex2_approx(x[i + 1] - e.y));
-                    const __half2 h1 = __floats2half2_rn(ex2_approx(x[i + 2] - e.z), ex2_approx(x[i + 3] - e.w));
-                    packed[i / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                    packed[i / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                    l[i] = add_f16_lo(l[i], packed[i / 2]);
-                    l[i + 1] = add_f16_hi(l[i + 1], packed[i / 2]);
-                    l[i + 2] = add_f16_lo(l[i + 2], packed[i / 2 + 1]);
-                    l[i + 3] = add_f16_hi(l[i + 3], packed[i / 2 + 1]);
-                }
-                uint8_t* line = smem + C::OFF_P + key_in * 128;
-#pragma unroll
-                for (int u = 0; u < NH / 8; ++u)
-                    *reinterpret_cast<uint4*>(line + (((half * (NH / 8) + u) ^ (key_in & 7)) << 4)) =
-                        make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
                 if (key0 + BN > hi) {
                     // keys that no row of the block keeps: their values are zeroed, since memory may
                     // hold anything there (or nothing was copied) and a weight of 0 must not meet a NaN
@@ -637,62 +645,76 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::B_P));
+                if (lane == 0) mbar_arrive(bar(C::B_P + (n_tile & 1)));
             }
-            if (!ok) break;
-            // the rows' sums
-            const float sum = reduce_lanes<NH>(l, lane, [](float p, float q) { return p + q; });
-            if (lane % (32 / NH) == 0) wl[quarter * NR + lane / (32 / NH)] = sum;
-            if (!(ok = meet()) || !(ok = wait(C::B_DONE, n_seg & 1, kErrTimeoutMma))) break;
-            tc_fence_after();
+            if (!ok || (w.n > 1 && !(ok = fix(n_tile - 1)))) break;
+            // the rows' sums, out of the threads that have them (two segments' in turn: another warp may
+            // still read the last one's)
+            float* inv_sum = factors + (2 + (n_seg & 1)) * NR;
             const bool whole = w.n == w.tiles;
             const int part = static_cast<int>(blockIdx.x) * 2 + (w.off > 0 ? 0 : 1);
-            const long long out0 = static_cast<long long>(w.c.q_base) * a.H + row0 + half * NH;
+            const long long out0 = static_cast<long long>(w.c.q_base) * a.H + row0;
             const long long out_end = static_cast<long long>(a.total_q) * a.H;
-            // this lane's row (the first lanes): its sum and maximum
-            float my_inv = 0.f;
-            if (lane < NH) {
-                const float s = (wl[lane] + wl[NR + lane]) + (wl[2 * NR + lane] + wl[3 * NR + lane]);
-                my_inv = !whole ? 1.f : s == 0.f ? 0.f : 1.0f / s;   // a row without keys: zeros; NaN stays NaN
-                const bool mine = half * NH + lane < live && out0 + lane >= 0 && out0 + lane < out_end;
-                if (quarter == 0 && mine) {
-                    const float mx = m[lane];
-                    if (!whole) a.part_ml[static_cast<size_t>(part) * NR + half * NH + lane] = make_float2(mx, s);
-                    else if (a.lse)
-                        a.lse[out0 + lane] = s == 0.f ? -INFINITY : (mx + __log2f(s)) * 0.6931471805599453f;
+            // rows below this are written
+            const int n_out = out0 < 0 ? 0 : static_cast<int>(max(0ll, min(static_cast<long long>(live), out_end - out0)));
+            if (has_rows) {
+                float s_a = l_a.x + l_a.y, s_b = l_b.x + l_b.y;
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    s_a += __shfl_xor_sync(0xffffffffu, s_a, o);
+                    s_b += __shfl_xor_sync(0xffffffffu, s_b, o);
+                }
+                if ((lane & 3) < 2) {
+                    const bool first = (lane & 3) == 0;
+                    const int row = first ? ra : rb;
+                    const float s = first ? s_a : s_b, mx = first ? m_a : m_b;
+                    inv_sum[row] = s == 0.f ? 0.f : 1.0f / s;   // a row without keys: zeros; NaN stays NaN
+                    if (row < n_out) {
+                        if (!whole) a.part_ml[static_cast<size_t>(part) * NR + row] = make_float2(mx, s);
+                        else if (a.lse)
+                            a.lse[out0 + row] = s == 0.f ? -INFINITY : (mx + __log2f(s)) * 0.6931471805599453f;
+                    }
                 }
             }
-            // rows below this are written
-            const int n_out = static_cast<int>(max(0ll, min(static_cast<long long>(live - half * NH), out_end - out0)));
-            const bool in_out = out0 >= 0;
+            if (!(ok = meet()) || !(ok = wait(C::B_DONE, n_seg & 1, kErrTimeoutMma))) break;
+            tc_fence_after();
+            constexpr int EC = NR < 32 ? 16 : 32;   // columns (rows of the block) at a time
 #pragma unroll 1
-            for (int p = 0; p < NP; ++p) {
-                uint32_t r[NH];
-                tmem_load<NH>(lanes + C::COL_O + p * NR + half * NH, r);
+            for (int q = 0; q < NP * NR / EC; ++q) {
+                const int c0 = (q * EC) % NR;       // the first of these rows
+                if (c0 >= n_out) continue;
+                uint32_t r[EC];
+                if constexpr (EC == 32) tc_ld_32x32b_x32(lanes + C::COL_O + q * EC, r);
+                else tmem_load16(lanes + C::COL_O + q * EC, r);
                 tc_wait_ld();
-                const int d0 = p * 128 + quarter * 32;
+                const int d0 = q * EC / NR * 128 + warp * 32;
                 if (whole) {
                     // two lanes swap halves of two rows, so that a lane has two values of one row
+                    __half* dst = a.out + static_cast<size_t>(out0 + c0 + (lane & 1)) * C::R + d0 + (lane & ~1);
 #pragma unroll
-                    for (int i = 0; i < NH; i += 2) {
-                        const float v0 = __uint_as_float(r[i]) * __shfl_sync(0xffffffffu, my_inv, i);
-                        const float v1 = __uint_as_float(r[i + 1]) * __shfl_sync(0xffffffffu, my_inv, i + 1);
+                    for (int i = 0; i < EC; i += 2) {
+                        const float2 f = *reinterpret_cast<const float2*>(inv_sum + c0 + i);
+                        const float v0 = __uint_as_float(r[i]) * f.x, v1 = __uint_as_float(r[i + 1]) * f.y;
                         const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
                         const __half2 h = (lane & 1) ? __floats2half2_rn(other, v1) : __floats2half2_rn(v0, other);
-                        const int row = i + (lane & 1);
-                        if (in_out && row < n_out)
-                            *reinterpret_cast<__half2*>(a.out + static_cast<size_t>(out0 + row) * C::R + d0 + (lane & ~1)) = h;
+                        if (c0 + i + (lane & 1) < n_out) *reinterpret_cast<__half2*>(dst + i * C::R) = h;
                     }
                 } else {
-                    float* dst = a.part_o + (static_cast<size_t>(part) * NR + half * NH) * C::R + d0 + lane;
+                    float* dst = a.part_o + (static_cast<size_t>(part) * NR + c0) * C::R + d0 + lane;
+                    const int n_here = n_out - c0;
+                    if (n_here >= EC) {
 #pragma unroll
-                    for (int i = 0; i < NH; ++i)
-                        if (i < n_out) dst[static_cast<size_t>(i) * C::R] = __uint_as_float(r[i]);
+                        for (int i = 0; i < EC; ++i) dst[i * C::R] = __uint_as_float(r[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < EC; ++i)
+                            if (i < n_here) dst[i * C::R] = __uint_as_float(r[i]);
+                    }
                 }
             }
             if (tid == 0) {
-                // what the join needs of this CTA: [0] its run goes on after its first part (or
-                // ends with it), [1] it leaves an item open, [2], [3] that item
+                // what the join needs of this CTA: [0] the item its run goes on with ends in it, [1] it
+                // leaves an item open, [2], [3] that item
                 int* meta = a.meta + blockIdx.x * 4;
                 if (w.off > 0) meta[0] = w.off + w.n == w.tiles;
                 else if (!whole) {
@@ -830,7 +852,7 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     a.H = L.H;
     a.log2P = L.cache.log2P;
     a.max_pages = L.cache.max_pages;
-    a.capacity = L.cache.capacity < 0x7ffff000ll ? L.cache.capacity : 0x7ffff000ll;
+    a.capacity = static_cast<int>(L.cache.capacity < 0x7ffff000ll ? L.cache.capacity : 0x7ffff000ll);
     a.n_rb = static_cast<int>(p.n_rb);
     // One token of many heads: neighbouring CTAs take its row blocks side by side, so that the
     // second one finds the cache's rows in L2
