@@ -26,8 +26,10 @@
 // into equal runs, one a CTA; rows of items cut by a run's end go to the workspace and are
 // joined by a second kernel.
 //
-// Roles (6 warps): 4 softmax warps (warp w: rows 16 w .. + 15; all four zero what a tile has
-// too much, rescale O and write the rows out, 32 of O^T's lanes each), a TMA warp, an MMA warp.
+// Roles (7 warps): 4 softmax warps (warp w: rows 16 w .. + 15; all four zero what a tile has
+// too much, rescale O and write the rows out, 32 of O^T's lanes each), a TMA warp, a warp that
+// issues the S products and one that issues the others: each waits for its own operands only.
+// (One warp for both, polling what is ready: 150 cycles a poll, 4500 a tile whatever its rows.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -44,7 +46,8 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
 constexpr int kMaxCtas = 152;               // one CTA an SM
 constexpr int kSegTiles = 2;                // a segment's fixed cost, in key tiles
 constexpr int kSoftmaxWarps = 4;
-constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kTmaWarp = kSoftmaxWarps, kSWarp = kTmaWarp + 1;   // and the PV warp
+constexpr int kThreads = (kSoftmaxWarps + 3) * 32;
 constexpr uint32_t kPair = 2 * BN * 128;    // bytes of 128 values of a tile: two 64-value chunks
 constexpr uint32_t kRope = BN * 128;        // of its rotated part
 
@@ -71,15 +74,19 @@ struct Cfg {
     // words of the rows: rescale factors of two tiles, then 1 / sum of two segments
     static constexpr uint32_t OFF_FLAGS = OFF_ROWS + 4 * NR * 4;   // [2][4] words
     static constexpr uint32_t OFF_SUMS = OFF_FLAGS + 32;           // the run's search
+    static constexpr int NTB = 4;      // tiles that the ring can hold parts of, at most
+    static_assert(NTB * NP >= NPS, "a tile's barrier is free when its first part's place is");
     enum : int {
-        B_QFULL, B_QEMPTY, B_PAIR, B_PAIRFREE = B_PAIR + NPS, B_ROPE = B_PAIRFREE + NPS, B_ROPEFREE = B_ROPE + NRS,
+        B_QFULL, B_QEMPTY,
+        B_TILE,                        // all of a tile is there
+        B_PAIRFREE = B_TILE + NTB, B_ROPEFREE = B_PAIRFREE + NPS,
         B_S = B_ROPEFREE + NRS,
         B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
         B_PV = B_P + 2,            // a tile's second product is done
-        B_DONE,            // a segment's last one is
-        B_FIX,             // O is rescaled
+        B_FIX = B_PV + 2,  // O is rescaled
         B_MEET,            // the softmax warps met
-        B_TEARDOWN, N_BARS
+        B_TEARDOWN,                    // of both issuers
+        N_BARS = B_TEARDOWN + 2
     };
     static constexpr uint32_t OFF_BAR = OFF_SUMS + 24 * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
@@ -262,7 +269,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             *abort_flag = 0;
             fence_barrier_init();
         }
-        if (warp == kSoftmaxWarps + 1) {
+        if (warp == kSWarp) {
             tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
             tmem_relinquish();
         }
@@ -320,7 +327,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int rb_in = static_cast<int>(blockIdx.x) % a.side;   // of the group's row blocks, this CTA's
 
-    if (warp == kSoftmaxWarps) {
+    if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA: Q, then the tiles
         // Lane l brings box l % nb (a page, or a tile's part of one) of chunk l / nb of a
         // 128-value pair; the boxes of the rotated part are lanes 0 .. nb - 1.
@@ -362,138 +369,120 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                 }
                 const int cur = slot;
+                const uint32_t full = bar(C::B_TILE + n_tile % C::NTB);
                 fetch(j + 1);
                 for (int p = 0; p < NP; ++p, ++n_pair) {
                     const uint32_t s = n_pair % NPS, round = n_pair / NPS;
                     if (round > 0 && !(ok = wait(C::B_PAIRFREE + s, (round - 1) & 1, kErrTimeoutSlot))) break;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(bar(C::B_PAIR + s), static_cast<uint32_t>(2 * boxes * a.box_rows) * 128);
+                    if (lane == 0) mbar_expect_tx(full, static_cast<uint32_t>(2 * boxes * a.box_rows) * 128);
                     __syncwarp();
                     if (has && lane < 2 * nb) {
                         const int c = lane / nb;
-                        tma_load_3d(sbase + C::OFF_PAIR + s * kPair + c * (BN * 128) + bx * a.box_rows * 128, &tm_x,
-                                    bar(C::B_PAIR + s), p * 128 + c * 64, row, cur);
+                        tma_load_3d(sbase + C::OFF_PAIR + s * kPair + c * (BN * 128) + bx * a.box_rows * 128, &tm_x, full,
+                                    p * 128 + c * 64, row, cur);
                     }
                 }
-                if (!ok) break;
                 const uint32_t rs = n_tile % C::NRS, round = n_tile / C::NRS;
-                if (round > 0 && !(ok = wait(C::B_ROPEFREE + rs, (round - 1) & 1, kErrTimeoutSlot))) break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar(C::B_ROPE + rs), static_cast<uint32_t>(boxes * a.box_rows) * 128);
+                if (ok && round > 0) ok = wait(C::B_ROPEFREE + rs, (round - 1) & 1, kErrTimeoutSlot);
+                // (the tile's one arrival, also if it was given up: its copies are waited for below)
+                if (lane == 0) mbar_arrive_expect_tx(full, ok ? static_cast<uint32_t>(boxes * a.box_rows) * 128 : 0);
                 __syncwarp();
-                if (has && lane < nb)
-                    tma_load_3d(sbase + C::OFF_ROPE + rs * kRope + bx * a.box_rows * 128, &tm_x, bar(C::B_ROPE + rs), C::R,
-                                row, cur);
+                if (ok && has && lane < nb)
+                    tma_load_3d(sbase + C::OFF_ROPE + rs * kRope + bx * a.box_rows * 128, &tm_x, full, C::R, row, cur);
+                if (!ok) {
+                    ++n_tile;
+                    break;
+                }
             }
         }
         if (!ok || __any_sync(0xffffffffu, *abort_flag)) {
             // let copies already in flight land before the CTA's shared memory goes away
             if (lane == 0) {
                 if (n_q > 0) mbar_wait_drain(bar(C::B_QFULL), (n_q - 1) & 1, a.err, kErrTimeoutLoad);
-                for (uint32_t i = n_pair > NPS ? n_pair - NPS : 0; i < n_pair; ++i)
-                    mbar_wait_drain(bar(C::B_PAIR + i % NPS), (i / NPS) & 1, a.err, kErrTimeoutLoad);
-                for (uint32_t i = n_tile > C::NRS ? n_tile - C::NRS : 0; i < n_tile; ++i)
-                    mbar_wait_drain(bar(C::B_ROPE + i % C::NRS), (i / C::NRS) & 1, a.err, kErrTimeoutLoad);
+                for (uint32_t i = n_tile > C::NTB ? n_tile - C::NTB : 0; i < n_tile; ++i)
+                    mbar_wait_drain(bar(C::B_TILE + i % C::NTB), (i / C::NTB) & 1, a.err, kErrTimeoutLoad);
             }
         }
-    } else if (warp == kSoftmaxWarps + 1) {
-        // ------------------------------------------------------------ MMA issuer
+    } else if (warp >= kSWarp) {
+        // ------------------------------------------------------------ MMA issuers
         // (the whole warp runs the code; one lane issues)
         const uint32_t one = elect_one();
-        constexpr uint32_t id_s = idesc(64, BN, 0), id_o = idesc(128, NR, 1);
-        const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
         const uint64_t x_desc = smem_desc_sw128(sbase + C::OFF_PAIR, 16, 1024);
-        const uint64_t r_desc = smem_desc_sw128(sbase + C::OFF_ROPE, 16, 1024);
-        const uint64_t c_desc = smem_desc_sw128(sbase + C::OFF_PAIR, BN * 128, 1024);   // MN-major: next 64 values
-        const uint64_t p_desc = smem_desc_sw128(sbase + C::OFF_P, 16, 1024);
-        const int* flags = reinterpret_cast<const int*>(smem + C::OFF_FLAGS);
-        const bool stall = stall_first_tile();
         bool ok = true;
-        uint32_t n_tile = 0, n_seg = 0, n_fix = 0;
-        auto ready = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test_wait(bar(i), parity)) != 0; };
+        uint32_t n_tile = 0, n_seg = 0;
         Walk w = run;
-        for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
-            if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
-            // What is ready is issued: the second product of tile v, which gives its place in the
-            // ring free, else the next part of S of tile s (at most one tile ahead: of two S).
-            // Waiting for a part before a second product held up the copies that it would have
-            // given room.
-            int js = 0, part = 0, jv = 0;
-            uint32_t spins = 0;
-            uint64_t t0 = 0;
-            while (jv < w.n) {
-                const uint32_t iv = n_tile + jv, is = n_tile + js;
-                if (jv < js && ready(C::B_P + (iv & 1), (iv >> 1) & 1)) {
-                    if (jv > 0) {
-                        const int* f = flags + (iv & 1) * kSoftmaxWarps;
-                        if ((f[0] | f[1] | f[2] | f[3]) && !(ok = wait(C::B_FIX, n_fix++ & 1, kErrTimeoutSoftmax))) break;
-                    }
+        if (warp == kSWarp) {
+            constexpr uint32_t id_s = idesc(64, BN, 0);
+            const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
+            const uint64_t r_desc = smem_desc_sw128(sbase + C::OFF_ROPE, 16, 1024);
+            const bool stall = stall_first_tile();
+            for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
+                if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
+                for (int j = 0; j < w.n; ++j, ++n_tile) {
+                    if (!(ok = wait(C::B_TILE + n_tile % C::NTB, (n_tile / C::NTB) & 1, kErrTimeoutLoad))) break;
+                    // (the S of two tiles before has been read once its weights are written)
+                    if (n_tile > 1 && !(ok = wait(C::B_P + (n_tile & 1), ((n_tile >> 1) - 1) & 1, kErrTimeoutSoftmax))) break;
                     tc_fence_after();
-                    const uint64_t pd = desc_advance(p_desc, C::ALIAS ? (iv % C::NRS) * kRope : (iv & 1) * C::P_BYTES);
-                    for (int p = 0; p < NP; ++p) {
-                        const uint32_t s = (iv * NP + p) % NPS;
-                        const uint64_t cd = desc_advance(c_desc, s * kPair);
+                    const uint32_t s_tmem = tmem + (n_tile & 1) * BN;
+                    uint32_t s = n_tile * NP % NPS;
+                    uint64_t qd = q_desc;
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of X, 32 bytes of P's
-                            tc_mma_f16_ss_one(one, tmem + C::COL_O + p * NR, desc_advance(cd, kk * 2048),
-                                              desc_advance(pd, kk * 32), id_o, (jv | kk) != 0);
-                        tc_commit_one(one, bar(C::B_PAIRFREE + s));
-                    }
-                    if (C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + iv % C::NRS));
-                    tc_commit_one(one, bar(C::B_PV));
-                    if (++jv == w.n) tc_commit_one(one, bar(C::B_DONE));
-                    spins = 0;
-                    continue;
-                }
-                const uint32_t k = is * NP + part, rs = is % C::NRS;
-                if (js < w.n && js <= jv + 1 &&
-                    (part < NP ? ready(C::B_PAIR + k % NPS, (k / NPS) & 1) : ready(C::B_ROPE + rs, (is / C::NRS) & 1))) {
-                    tc_fence_after();
-                    const uint32_t s_tmem = tmem + (is & 1) * BN;
-                    const uint64_t qd = desc_advance(q_desc, part * 2 * C::Q_CHUNK);
-                    if (part < NP) {
-                        const uint64_t xd = desc_advance(x_desc, (k % NPS) * kPair);
+                    for (int p = 0; p < NP; ++p) {
+                        const uint64_t xd = desc_advance(x_desc, s * kPair);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, c * C::Q_CHUNK + kk * 32),
-                                                  desc_advance(xd, c * (BN * 128) + kk * 32), id_s, (part | c | kk) != 0);
-                        ++part;
-                    } else {
+                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, (2 * p + c) * C::Q_CHUNK + kk * 32),
+                                                  desc_advance(xd, c * (BN * 128) + kk * 32), id_s, (p | c | kk) != 0);
+                        s = s + 1 == NPS ? 0 : s + 1;
+                    }
+                    const uint32_t rs = n_tile % C::NRS;
+                    const uint64_t rd = desc_advance(r_desc, rs * kRope);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, kk * 32), desc_advance(r_desc, rs * kRope + kk * 32),
-                                              id_s, 1);
-                        if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + rs));
-                        if (!(stall && is == 0)) tc_commit_one(one, bar(C::B_S + (is & 1)));
-                        part = 0;
-                        if (++js == w.n) tc_commit_one(one, bar(C::B_QEMPTY));
-                    }
-                    spins = 0;
-                    continue;
-                }
-                // neither: the bounded wait of ptx.cuh
-                if (spins++ == 0) {
-                    t0 = globaltimer();
-                } else if ((spins & 63) == 0) {
-                    if (__any_sync(0xffffffffu, *abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    if (__any_sync(0xffffffffu, globaltimer() - t0 > *static_cast<volatile unsigned long long*>(&g_wait_limit_ns))) {
-                        *abort_flag = 1;
-                        atomicExch(a.err, kErrTimeoutSoftmax);
-                        ok = false;
-                        break;
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, 2 * NP * C::Q_CHUNK + kk * 32), desc_advance(rd, kk * 32),
+                                          id_s, 1);
+                    if (!(stall && n_tile == 0)) tc_commit_one(one, bar(C::B_S + (n_tile & 1)));
+                    if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + rs));
+                    if (j == w.n - 1) tc_commit_one(one, bar(C::B_QEMPTY));
                 }
             }
-            n_tile += w.n;
+        } else {
+            constexpr uint32_t id_o = idesc(128, NR, 1);
+            const uint64_t c_desc = smem_desc_sw128(sbase + C::OFF_PAIR, BN * 128, 1024);   // MN-major: next 64 values
+            const uint64_t p_desc = smem_desc_sw128(sbase + C::OFF_P, 16, 1024);
+            const int* flags = reinterpret_cast<const int*>(smem + C::OFF_FLAGS);
+            uint32_t n_fix = 0;
+            for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w)) {
+                for (int j = 0; j < w.n; ++j, ++n_tile) {
+                    if (!(ok = wait(C::B_P + (n_tile & 1), (n_tile >> 1) & 1, kErrTimeoutSoftmax))) break;
+                    if (j > 0) {
+                        const int* f = flags + (n_tile & 1) * kSoftmaxWarps;
+                        if ((f[0] | f[1] | f[2] | f[3]) && !(ok = wait(C::B_FIX, n_fix++ & 1, kErrTimeoutSoftmax))) break;
+                    }
+                    tc_fence_after();
+                    const uint64_t pd = desc_advance(p_desc, C::ALIAS ? (n_tile % C::NRS) * kRope : (n_tile & 1) * C::P_BYTES);
+                    uint32_t s = n_tile * NP % NPS;
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) {
+                        const uint64_t cd = desc_advance(c_desc, s * kPair);
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of X, 32 bytes of P's
+                            tc_mma_f16_ss_one(one, tmem + C::COL_O + p * NR, desc_advance(cd, kk * 2048),
+                                              desc_advance(pd, kk * 32), id_o, (j | kk) != 0);
+                        tc_commit_one(one, bar(C::B_PAIRFREE + s));
+                        s = s + 1 == NPS ? 0 : s + 1;
+                    }
+                    if (C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + n_tile % C::NRS));
+                    tc_commit_one(one, bar(C::B_PV + (n_tile & 1)));
+                }
+            }
         }
         // all issued MMAs must retire before TMEM is released
-        tc_commit_one(one, bar(C::B_TEARDOWN));
-        if (lane == 0) mbar_wait_drain(bar(C::B_TEARDOWN), 0, a.err, kErrTimeoutMma);
+        const int done = C::B_TEARDOWN + (warp - kSWarp);
+        tc_commit_one(one, bar(done));
+        if (lane == 0) mbar_wait_drain(bar(done), 0, a.err, kErrTimeoutMma);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax, and the rows out
@@ -516,9 +505,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!wait(C::B_P + (i & 1), (i >> 1) & 1, kErrTimeoutSoftmax)) return false;
             const int f = lane < kSoftmaxWarps ? flags[(i & 1) * kSoftmaxWarps + lane] : 0;
             if (!__any_sync(0xffffffffu, f)) return true;
-            // (S of tile i came after the product of i - 2, and that of i waits for this: i - 1 is the
-            // one phase that may be open)
-            if (!wait(C::B_PV, (i - 1) & 1, kErrTimeoutMma)) return false;
+            if (!wait(C::B_PV + ((i - 1) & 1), ((i - 1) >> 1) & 1, kErrTimeoutMma)) return false;
             tc_fence_after();
             const float* at = factors + (i & 1) * NR;
 #pragma unroll 1
@@ -559,6 +546,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (j > 1 && !(ok = fix(n_tile - 1))) break;
                 if (!(ok = wait(C::B_S + (n_tile & 1), (n_tile >> 1) & 1, kErrTimeoutMma))) break;
                 tc_fence_after();
+                // (P of two tiles before must have been read)
+                if (n_tile > 1 && !(ok = wait(C::B_PV + (n_tile & 1), ((n_tile >> 1) - 1) & 1, kErrTimeoutMma))) break;
                 const int key0 = (w.off + j) * BN;
                 if (has_rows) {
                     // columns 8 i + 2 (lane % 4), + 1: row a in x[4 i], x[4 i + 1], row b in the next two
@@ -631,16 +620,16 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     // keys that no row of the block keeps: their values are zeroed, since memory may
                     // hold anything there (or nothing was copied) and a weight of 0 must not meet a NaN
                     const int r0 = max(hi - key0, 0), per_chunk = (BN - r0) * 8;   // 16-byte units
+                    // (the wait, long over, orders these writes after the copies)
+                    if (!(ok = wait(C::B_TILE + n_tile % C::NTB, (n_tile / C::NTB) & 1, kErrTimeoutLoad))) break;
                     for (int p = 0; p < NP; ++p) {
-                        const uint32_t pr = n_tile * NP + p, s = pr % NPS;
-                        if (!(ok = wait(C::B_PAIR + s, (pr / NPS) & 1, kErrTimeoutLoad))) break;
+                        const uint32_t s = (n_tile * NP + p) % NPS;
                         uint8_t* at = smem + C::OFF_PAIR + s * kPair;
                         for (int u = tid; u < 2 * per_chunk; u += kSoftmaxWarps * 32) {
                             const int c = u >= per_chunk, v = u - c * per_chunk;
                             *reinterpret_cast<uint4*>(at + c * (BN * 128) + r0 * 128 + v * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
-                    if (!ok) break;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -676,7 +665,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     }
                 }
             }
-            if (!(ok = meet()) || !(ok = wait(C::B_DONE, n_seg & 1, kErrTimeoutMma))) break;
+            if (!(ok = meet()) || !(ok = wait(C::B_PV + ((n_tile - 1) & 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
             tc_fence_after();
             constexpr int EC = NR < 32 ? 16 : 32;   // columns (rows of the block) at a time
 #pragma unroll 1
@@ -728,7 +717,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kSoftmaxWarps + 1) {
+    if (warp == kSWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
