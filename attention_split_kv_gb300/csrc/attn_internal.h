@@ -187,6 +187,23 @@ struct Prefill8Launch {
 size_t prefill8_workspace(int max_q, int Hq, int Hkv, int D);
 attn_status launch_prefill8(const Prefill8Launch& L);
 
+// A launch that may start before the kernel before it in the stream has ended: the kernel waits
+// for that (griddepcontrol.wait) before it reads or writes device memory.
+template <typename... K, typename... A>
+cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- latent attention: a token's cached row is [c (R values) | rotated key part (64)]
 struct LatentAppendArgs {
     const void *c, *k_rope, *q_rope;

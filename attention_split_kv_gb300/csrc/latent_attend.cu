@@ -43,6 +43,7 @@ namespace {
 constexpr int BN = 64;                      // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
+constexpr float kFastSumLimit = 256.0f;
 constexpr int kMaxCtas = 152;               // one CTA an SM
 constexpr int kSegTiles = 2;                // a segment's fixed cost, in key tiles
 constexpr int kSoftmaxWarps = 4;
@@ -74,12 +75,12 @@ struct Cfg {
     // words of the rows: rescale factors of two tiles, then 1 / sum of two segments
     static constexpr uint32_t OFF_FLAGS = OFF_ROWS + 4 * NR * 4;   // [2][4] words
     static constexpr uint32_t OFF_SUMS = OFF_FLAGS + 32;           // the run's search
-    static constexpr int NTB = 4;      // tiles that the ring can hold parts of, at most
-    static_assert(NTB * NP >= NPS, "a tile's barrier is free when its first part's place is");
+    static constexpr int NHB = 8;      // halves of tiles that the ring can hold parts of, at most
+    static_assert(NHB * NP / 2 >= NPS, "a half's barrier is free when its first part's place is");
     enum : int {
         B_QFULL, B_QEMPTY,
-        B_TILE,                        // all of a tile is there
-        B_PAIRFREE = B_TILE + NTB, B_ROPEFREE = B_PAIRFREE + NPS,
+        B_HALF,                        // half a tile is there (the second one with the rotated part)
+        B_PAIRFREE = B_HALF + NHB, B_ROPEFREE = B_PAIRFREE + NPS,
         B_S = B_ROPEFREE + NRS,
         B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
         B_PV = B_P + 2,            // a tile's second product is done
@@ -88,7 +89,7 @@ struct Cfg {
         B_TEARDOWN,                    // of both issuers
         N_BARS = B_TEARDOWN + 2
     };
-    static constexpr uint32_t OFF_BAR = OFF_SUMS + 24 * 8;
+    static constexpr uint32_t OFF_BAR = OFF_SUMS + 10 * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
     static constexpr uint32_t COL_O = 2 * BN, COLS = COL_O + NP * NR;
@@ -109,7 +110,7 @@ struct Args {
     int* meta;           // [CTA][4]
     int* err;
     int B, total_q, max_q, H;
-    int log2P, max_pages, n_slots, box_rows;   // pages, or the contiguous cache's sequences
+    int log2P, max_pages, n_slots, box_rows;   // slots: pages, or the contiguous cache's sequences
     int n_rb;            // row blocks of the longest chunk
     int side;            // row blocks of a sequence that neighbouring CTAs take side by side
     int capacity;
@@ -146,29 +147,29 @@ __device__ __forceinline__ int group_tiles(const Args& a, const Chunk& c, int g)
     return max((key_end(a, c, static_cast<uint32_t>(g + 1) * (a.side * NR)) + BN - 1) / BN, 1);
 }
 
-// A CTA's run of key tiles, walked a segment (part of one item) at a time.  Every warp walks
-// for itself.
+// A CTA's run, walked a segment (part of one item) at a time; every warp walks for itself.  A run
+// is a range of weights: an item weighs its key tiles and kSegTiles before them.
 struct Walk {
-    int b, g, off;       // sequence, group of row blocks, first key tile
-    int n_g, n, tiles;   // groups of the sequence; key tiles of the segment and of the item
-    long long rem;       // key tiles of the run from this segment on
+    int b, g;            // sequence, group of row blocks
+    long long in, rem;   // where the run enters the item; its weight from there on
+    int off, n, tiles;   // first key tile and key tiles of the segment; key tiles of the item
     Chunk c;
 };
 template <int NR>
 __device__ __forceinline__ bool walk_item(const Args& a, Walk& w) {
     if (w.rem <= 0) return false;
     w.c = load_chunk(a, w.b);
-    w.n_g = groups_of<NR>(a, w.c);
     w.tiles = group_tiles<NR>(a, w.c, w.g);
-    w.n = static_cast<int>(min(static_cast<long long>(w.tiles - w.off), w.rem));
-    return w.n > 0;      // (lengths that changed under the call)
+    w.off = max(static_cast<int>(w.in) - kSegTiles, 0);
+    w.n = static_cast<int>(min(static_cast<long long>(w.tiles), w.in + w.rem - kSegTiles)) - w.off;
+    return w.n > 0;
 }
 template <int NR>
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
-    w.rem -= w.n;
-    w.off = 0;
+    w.rem -= w.tiles + kSegTiles - w.in;
+    w.in = 0;
     if (w.rem <= 0) return false;
-    if (++w.g >= w.n_g) {
+    if (++w.g >= groups_of<NR>(a, w.c)) {
         w.g = 0;
         do {
             if (++w.b >= a.B) return false;
@@ -187,7 +188,8 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
 
 template <int NP, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x, const Args a) {
+latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x2,
+                     const __grid_constant__ CUtensorMap tm_x1, const Args a) {
     using C = Cfg<NP, NR>;
     constexpr int NPS = C::NPS;
     extern __shared__ uint8_t smem_raw[];
@@ -200,7 +202,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == kSoftmaxWarps * 32) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_x2);
+        tma_prefetch_desc(&tm_x1);
     }
     // A wait of a whole warp, with one answer for all of its lanes.
     auto wait = [&](int b, uint32_t parity, int code) -> bool {
@@ -217,122 +220,101 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         return false;
     };
 
-    // ---- this CTA's run: sum the key tiles of every (sequence, group), then find where the
-    // run starts
+    if (warp == 0) {
+        for (int i = lane; i < C::N_BARS; i += 32)
+            mbar_init(bar(i), (i >= C::B_P && i < C::B_P + 2) || i == C::B_FIX || i == C::B_MEET ? kSoftmaxWarps : 1);
+        if (lane == 0) *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kSWarp) {
+        tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for what earlier calls wrote or still read
+
+    // ---- this CTA's run: sum the weights of all items, then find where the run starts
     Walk run;
     {
         constexpr int kWarps = kThreads / 32;
-        static_assert(2 * kWarps <= 20, "scratch");
-        long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);   // [2][warps], then the run's ends
-        int* first = reinterpret_cast<int*>(sums + 22);
-        const int max_g = (a.n_rb + a.side - 1) / a.side;
-        const long long pairs = static_cast<long long>(a.B) * max_g;
-        const long long per = (pairs + kThreads - 1) / kThreads;
-        const long long f0 = min(pairs, tid * per), f1 = min(pairs, f0 + per);
+        long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);   // of the warps, then the run's start
+        int* first = reinterpret_cast<int*>(sums + kWarps + 1);
+        static_assert(kWarps + 2 <= 10, "scratch");
+        const int max_g = a.side > 1 ? 1 : a.n_rb;
+        const long long items = static_cast<long long>(a.B) * max_g, per = (items + kThreads - 1) / kThreads;
+        const long long f0 = min(items, tid * per), f1 = min(items, f0 + per);
         // visits this thread's items in order until fn says stop
         auto visit = [&](auto fn) {
             if (f0 >= f1) return;
-            int b = static_cast<int>(f0 / max_g), g = static_cast<int>(f0 - static_cast<long long>(b) * max_g);
-            long long left = f1 - f0;
-            while (left > 0) {
+            int b = static_cast<int>(max_g == 1 ? f0 : f0 / max_g);
+            int g = max_g == 1 ? 0 : static_cast<int>(f0 - static_cast<long long>(b) * max_g);
+#pragma unroll 1
+            for (long long left = f1 - f0; left > 0; ++b) {
                 const Chunk c = load_chunk(a, b);
                 const int end = static_cast<int>(min(static_cast<long long>(groups_of<NR>(a, c)), g + left));
+#pragma unroll 1
                 for (int i = g; i < end; ++i)
-                    if (!fn(b, i, group_tiles<NR>(a, c, i))) return;
+                    if (!fn(b, i, group_tiles<NR>(a, c, i) + kSegTiles)) return;
                 left -= max_g - g;
                 g = 0;
-                ++b;
             }
         };
-        long long mine = 0, tiles = 0;         // weights, and key tiles alone
-        visit([&](int, int, int t) {
-            mine += t + kSegTiles;
-            tiles += t;
+        long long mine = 0;
+        visit([&](int, int, int weight) {
+            mine += weight;
             return true;
         });
-        long long incl = mine, incl_t = tiles;
+        long long before = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, o), y = __shfl_up_sync(0xffffffffu, incl_t, o);
-            if (lane >= o) {
-                incl += x;
-                incl_t += y;
-            }
+            const long long x = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += x;
         }
-        if (lane == 31) {
-            sums[warp] = incl;
-            sums[kWarps + warp] = incl_t;
-        }
-        if (tid == 0) {
-            for (int i = 0; i < C::N_BARS; ++i)
-                mbar_init(bar(i), (i >= C::B_P && i < C::B_P + 2) || i == C::B_FIX || i == C::B_MEET ? kSoftmaxWarps : 1);
-            *abort_flag = 0;
-            fence_barrier_init();
-        }
-        if (warp == kSWarp) {
-            tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
-            tmem_relinquish();
-        }
+        if (lane == 31) sums[warp] = before;
+        before -= mine;
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        long long before = incl - mine, before_t = incl_t - tiles, total = 0, total_t = 0;
+        long long total = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) {
-                before += sums[i];
-                before_t += sums[kWarps + i];
-            }
+            if (i < warp) before += sums[i];
             total += sums[i];
-            total_t += sums[kWarps + i];
         }
         // as many runs as CTAs, or fewer of a key tile at least (a run's weight is above kSegTiles)
-        const int rank = static_cast<int>(blockIdx.x) / a.side;
-        const int most = static_cast<int>(gridDim.x) / a.side;
+        const int rank = static_cast<int>(blockIdx.x) / a.side, most = static_cast<int>(gridDim.x) / a.side;
         const int runs = total >= static_cast<long long>(most) * (kSegTiles + 1) ? most : max(1, static_cast<int>(total) / (kSegTiles + 1));
         const long long each = total < (1ll << 31) ? static_cast<uint32_t>(total) / static_cast<uint32_t>(runs) : total / runs;
-        const long long more = total - each * runs;
-        if (tid == 0) sums[20] = sums[21] = total_t;
-        __syncthreads();
-        if (rank < runs) {
-#pragma unroll 1
-            for (int e = 0; e < 2; ++e) {
-                // (the first total % runs runs have one more)
-                const long long t = each * (rank + e) + min(static_cast<long long>(rank + e), more);
-                if (before > t || t >= before + mine) continue;
-                long long acc = before, acc_t = before_t;
-                visit([&](int b, int g, int n) {
-                    if (acc + n + kSegTiles <= t) {
-                        acc += n + kSegTiles;
-                        acc_t += n;
-                        return true;
-                    }
-                    const int off = max(static_cast<int>(t - acc) - kSegTiles, 0);
-                    sums[20 + e] = acc_t + off;
-                    if (e == 0) {
-                        first[0] = b;
-                        first[1] = g;
-                        first[2] = off;
-                    }
-                    return false;
-                });
-            }
+        const int more = static_cast<int>(total - each * runs);   // the first ones have one more
+        const long long t = each * rank + min(rank, more);
+        if (rank < runs && before <= t && t < before + mine) {
+            long long at = before;
+            visit([&](int b, int g, int weight) {
+                if (at + weight <= t) {
+                    at += weight;
+                    return true;
+                }
+                sums[kWarps] = t - at;
+                first[0] = b;
+                first[1] = g;
+                return false;
+            });
         }
         __syncthreads();
         run.b = first[0];
         run.g = first[1];
-        run.off = first[2];
-        run.rem = rank < runs ? sums[21] - sums[20] : 0;
+        run.in = sums[kWarps];
+        run.rem = rank < runs && total > 0 ? each + (rank < more) : 0;
     }
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const int rb_in = static_cast<int>(blockIdx.x) % a.side;   // of the group's row blocks, this CTA's
 
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA: Q, then the tiles
-        // Lane l brings box l % nb (a page, or a tile's part of one) of chunk l / nb of a
-        // 128-value pair; the boxes of the rotated part are lanes 0 .. nb - 1.
+        // A 128-value part is one box of two chunks where the tile lies in one page (or none), else
+        // a box a page and chunk: lane l brings page l % nb of chunk l / nb.
         const int nb = BN / a.box_rows, bx = lane & (nb - 1), P = 1 << a.log2P;
-        uint32_t n_pair = 0, n_tile = 0, n_seg = 0, n_q = 0;   // (copies posted)
+        uint32_t n_pair = 0, n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
+        uint32_t s_pair = 0, s_rope = 0, free_phase = 0, rope_phase = 0;   // places in the rings, phases of their barriers
         bool ok = true;
         Walk w = run;
         for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
@@ -346,61 +328,79 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     tma_load_2d(sbase + C::OFF_Q + c * C::Q_CHUNK, &tm_q, bar(C::B_QFULL), c * 64, q_row);
             }
             ++n_q;
-            // the place of this lane's box in tile j: page id (or sequence) and row
-            int slot = 0;
+            // the place of this lane's box in tile j, page id or sequence: read a tile before its copies
             auto fetch = [&](int j) {
                 const int kk = (w.off + j) * BN + bx * a.box_rows;
-                slot = w.b;
-                if (a.page_table)
-                    slot = j < w.n && kk < hi
-                               ? __ldg(&a.page_table[static_cast<size_t>(w.b) * a.max_pages + (kk >> a.log2P)]) : 0;
+                if (!a.page_table) return w.b;
+                return j < w.n && kk < hi ? __ldg(&a.page_table[static_cast<size_t>(w.b) * a.max_pages + (kk >> a.log2P)]) : 0;
             };
-            fetch(0);
-            for (int j = 0; j < w.n; ++j, ++n_tile) {
+            int slot = fetch(0);
+#pragma unroll 1
+            for (int j = 0; j < w.n; ++j) {
                 const int key0 = (w.off + j) * BN, kk = key0 + bx * a.box_rows;
                 const int boxes = hi > key0 ? min(nb, (hi - key0 + a.box_rows - 1) / a.box_rows) : 0;
                 const bool has = kk < hi;
-                int row = kk;
+                int row = kk, cur = slot;
                 if (a.page_table) {
                     row = kk & (P - 1);
-                    if (has && (slot < 0 || slot >= a.n_slots)) {
+                    if (has && (cur < 0 || cur >= a.n_slots)) {
                         atomicExch(a.err, kErrLatentPage);   // never read: its keys are zeros
-                        slot = a.n_slots;
+                        cur = a.n_slots;
                     }
                 }
-                const int cur = slot;
-                const uint32_t full = bar(C::B_TILE + n_tile % C::NTB);
-                fetch(j + 1);
-                for (int p = 0; p < NP; ++p, ++n_pair) {
-                    const uint32_t s = n_pair % NPS, round = n_pair / NPS;
-                    if (round > 0 && !(ok = wait(C::B_PAIRFREE + s, (round - 1) & 1, kErrTimeoutSlot))) break;
-                    if (lane == 0) mbar_expect_tx(full, static_cast<uint32_t>(2 * boxes * a.box_rows) * 128);
+                slot = fetch(j + 1);
+                // The halves' byte counts are posted after their copies: a half given up in between
+                // then has the bytes that are on their way.
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t full = bar(C::B_HALF + n_half % C::NHB);
+                    uint32_t bytes = 0;
+                    for (int p = 0; p < NP / 2 && ok; ++p) {
+                        if (n_pair >= NPS && !(ok = wait(C::B_PAIRFREE + s_pair, free_phase, kErrTimeoutSlot))) break;
+                        const uint32_t dst = sbase + C::OFF_PAIR + s_pair * kPair + bx * a.box_rows * 128;
+                        const int x0 = (h * (NP / 2) + p) * 2;   // the part's first chunk
+                        if (has) {
+                            if (nb == 1) {
+                                if (lane == 0) tma_load_4d(dst, &tm_x2, full, 0, row, x0, cur);
+                            } else if (lane < 2 * nb) {
+                                const int c = lane / nb;
+                                tma_load_4d(dst + c * (BN * 128), &tm_x1, full, 0, row, x0 + c, cur);
+                            }
+                        }
+                        bytes += 2 * boxes * a.box_rows * 128;
+                        ++n_pair;
+                        if (++s_pair == NPS) {
+                            s_pair = 0;
+                            if (n_pair > NPS) free_phase ^= 1;
+                        }
+                    }
+                    if (h == 1 && ok) {
+                        if (n_half >= 2 * C::NRS && !(ok = wait(C::B_ROPEFREE + s_rope, rope_phase, kErrTimeoutSlot))) {
+                        } else {
+                            if (has && lane < nb)
+                                tma_load_4d(sbase + C::OFF_ROPE + s_rope * kRope + bx * a.box_rows * 128, &tm_x1, full, 0, row,
+                                            2 * NP, cur);
+                            bytes += boxes * a.box_rows * 128;
+                            if (++s_rope == C::NRS) {
+                                s_rope = 0;
+                                if (n_half > 2 * C::NRS) rope_phase ^= 1;
+                            }
+                        }
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                     __syncwarp();
-                    if (has && lane < 2 * nb) {
-                        const int c = lane / nb;
-                        tma_load_3d(sbase + C::OFF_PAIR + s * kPair + c * (BN * 128) + bx * a.box_rows * 128, &tm_x, full,
-                                    p * 128 + c * 64, row, cur);
-                    }
+                    ++n_half;
+                    if (!ok) break;
                 }
-                const uint32_t rs = n_tile % C::NRS, round = n_tile / C::NRS;
-                if (ok && round > 0) ok = wait(C::B_ROPEFREE + rs, (round - 1) & 1, kErrTimeoutSlot);
-                // (the tile's one arrival, also if it was given up: its copies are waited for below)
-                if (lane == 0) mbar_arrive_expect_tx(full, ok ? static_cast<uint32_t>(boxes * a.box_rows) * 128 : 0);
-                __syncwarp();
-                if (ok && has && lane < nb)
-                    tma_load_3d(sbase + C::OFF_ROPE + rs * kRope + bx * a.box_rows * 128, &tm_x, full, C::R, row, cur);
-                if (!ok) {
-                    ++n_tile;
-                    break;
-                }
+                if (!ok) break;
             }
         }
         if (!ok || __any_sync(0xffffffffu, *abort_flag)) {
             // let copies already in flight land before the CTA's shared memory goes away
             if (lane == 0) {
                 if (n_q > 0) mbar_wait_drain(bar(C::B_QFULL), (n_q - 1) & 1, a.err, kErrTimeoutLoad);
-                for (uint32_t i = n_tile > C::NTB ? n_tile - C::NTB : 0; i < n_tile; ++i)
-                    mbar_wait_drain(bar(C::B_TILE + i % C::NTB), (i / C::NTB) & 1, a.err, kErrTimeoutLoad);
+                for (uint32_t i = n_half > C::NHB ? n_half - C::NHB : 0; i < n_half; ++i)
+                    mbar_wait_drain(bar(C::B_HALF + i % C::NHB), (i / C::NHB) & 1, a.err, kErrTimeoutLoad);
             }
         }
     } else if (warp >= kSWarp) {
@@ -419,29 +419,32 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
                 if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
-                    if (!(ok = wait(C::B_TILE + n_tile % C::NTB, (n_tile / C::NTB) & 1, kErrTimeoutLoad))) break;
                     // (the S of two tiles before has been read once its weights are written)
                     if (n_tile > 1 && !(ok = wait(C::B_P + (n_tile & 1), ((n_tile >> 1) - 1) & 1, kErrTimeoutSoftmax))) break;
-                    tc_fence_after();
                     const uint32_t s_tmem = tmem + (n_tile & 1) * BN;
                     uint32_t s = n_tile * NP % NPS;
-                    uint64_t qd = q_desc;
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
+                        if (p % (NP / 2) == 0) {
+                            const uint32_t i = 2 * n_tile + p / (NP / 2);
+                            if (!(ok = wait(C::B_HALF + i % C::NHB, (i / C::NHB) & 1, kErrTimeoutLoad))) break;
+                            tc_fence_after();
+                        }
                         const uint64_t xd = desc_advance(x_desc, s * kPair);
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, (2 * p + c) * C::Q_CHUNK + kk * 32),
+                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(q_desc, (2 * p + c) * C::Q_CHUNK + kk * 32),
                                                   desc_advance(xd, c * (BN * 128) + kk * 32), id_s, (p | c | kk) != 0);
                         s = s + 1 == NPS ? 0 : s + 1;
                     }
+                    if (!ok) break;
                     const uint32_t rs = n_tile % C::NRS;
                     const uint64_t rd = desc_advance(r_desc, rs * kRope);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f16_ss_one(one, s_tmem, desc_advance(qd, 2 * NP * C::Q_CHUNK + kk * 32), desc_advance(rd, kk * 32),
+                        tc_mma_f16_ss_one(one, s_tmem, desc_advance(q_desc, 2 * NP * C::Q_CHUNK + kk * 32), desc_advance(rd, kk * 32),
                                           id_s, 1);
                     if (!(stall && n_tile == 0)) tc_commit_one(one, bar(C::B_S + (n_tile & 1)));
                     if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + rs));
@@ -557,62 +560,93 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         tc_ld_16x256b_x8(lanes + (n_tile & 1) * BN, r);
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]) * scale_log2;
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
                     }
-                    if (key0 + BN > all_keep) {
-                        const int k0 = key0 + 2 * (lane & 3);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (k0 + (i >> 2) * 8 + (i & 1) >= ((i & 2) ? lim_b : lim_a)) x[i] = -INFINITY;
-                    }
-                    float ta = fmaxf(x[0], x[1]), tb = fmaxf(x[2], x[3]);
-#pragma unroll
-                    for (int i = 4; i < 32; i += 4) {
-                        ta = fmaxf(ta, fmaxf(x[i], x[i + 1]));
-                        tb = fmaxf(tb, fmaxf(x[i + 2], x[i + 3]));
-                    }
-#pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) {
-                        ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
-                        tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
-                    }
-                    float f_a = 1.f, f_b = 1.f;
-                    const bool need_a = ta > m_a + kRescaleThreshold, need_b = tb > m_b + kRescaleThreshold;
-                    if (need_a) {
-                        f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - ta);
-                        l_a = fmul2(l_a, make_float2(f_a, f_a));
-                        m_a = ta;
-                    }
-                    if (need_b) {
-                        f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - tb);
-                        l_b = fmul2(l_b, make_float2(f_b, f_b));
-                        m_b = tb;
-                    }
-                    if ((lane & 3) == 0) {
-                        factors[(n_tile & 1) * NR + ra] = f_a;
-                        factors[(n_tile & 1) * NR + rb] = f_b;
-                    }
-                    const int any = __any_sync(0xffffffffu, need_a || need_b);
-                    if (lane == 0) flags[(n_tile & 1) * kSoftmaxWarps + warp] = any;
-                    // (a row that has kept no key yet: all of its x are -inf)
-                    const float o_a = m_a == -INFINITY ? 0.f : m_a, o_b = m_b == -INFINITY ? 0.f : m_b;
+                    const bool masked = key0 + BN > all_keep;
+                    const int drop_a = lim_a - key0 - 2 * (lane & 3), drop_b = lim_b - key0 - 2 * (lane & 3);
                     // a row's line of P is its 64 weights, swizzled as the MMA reads it (both rows alike,
                     // ra % 8 == rb % 8)
                     uint8_t* line = smem + C::OFF_P + (C::ALIAS ? (n_tile % C::NRS) * kRope : (n_tile & 1) * C::P_BYTES) +
                                     ra * 128 + (lane & 3) * 4;
+                    const float2 f2 = make_float2(scale_log2, scale_log2);
+                    // weights against the offsets; returns their sums (of the rounded ones, so that an
+                    // output is a convex combination of values)
+                    auto weights = [&](float o_a, float o_b, float2& s_a, float2& s_b) {
+                        s_a = s_b = make_float2(0.f, 0.f);
+                        const float2 na = make_float2(-o_a, -o_a), nb2 = make_float2(-o_b, -o_b);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const __half2 ha = __floats2half2_rn(ex2_approx(x[4 * i] - o_a), ex2_approx(x[4 * i + 1] - o_a));
-                        const __half2 hb = __floats2half2_rn(ex2_approx(x[4 * i + 2] - o_b), ex2_approx(x[4 * i + 3] - o_b));
-                        const uint32_t pa = *reinterpret_cast<const uint32_t*>(&ha), pb = *reinterpret_cast<const uint32_t*>(&hb);
-                        l_a.x = add_f16_lo(l_a.x, pa);
-                        l_a.y = add_f16_hi(l_a.y, pa);
-                        l_b.x = add_f16_lo(l_b.x, pb);
-                        l_b.y = add_f16_hi(l_b.y, pb);
-                        const int u = (i ^ (ra & 7)) << 4;
-                        *reinterpret_cast<uint32_t*>(line + u) = pa;
-                        *reinterpret_cast<uint32_t*>(line + u + 8 * 128) = pb;
+                        for (int i = 0; i < 8; ++i) {
+                            float2 ya = ffma2(make_float2(x[4 * i], x[4 * i + 1]), f2, na);
+                            float2 yb = ffma2(make_float2(x[4 * i + 2], x[4 * i + 3]), f2, nb2);
+                            if (masked) {
+                                if (8 * i >= drop_a) ya.x = -INFINITY;
+                                if (8 * i + 1 >= drop_a) ya.y = -INFINITY;
+                                if (8 * i >= drop_b) yb.x = -INFINITY;
+                                if (8 * i + 1 >= drop_b) yb.y = -INFINITY;
+                            }
+                            const __half2 ha = __floats2half2_rn(ex2_approx(ya.x), ex2_approx(ya.y));
+                            const __half2 hb = __floats2half2_rn(ex2_approx(yb.x), ex2_approx(yb.y));
+                            const uint32_t pa = *reinterpret_cast<const uint32_t*>(&ha), pb = *reinterpret_cast<const uint32_t*>(&hb);
+                            s_a.x = add_f16_lo(s_a.x, pa);
+                            s_a.y = add_f16_hi(s_a.y, pa);
+                            s_b.x = add_f16_lo(s_b.x, pb);
+                            s_b.y = add_f16_hi(s_b.y, pb);
+                            const int u = (i ^ (ra & 7)) << 4;
+                            *reinterpret_cast<uint32_t*>(line + u) = pa;
+                            *reinterpret_cast<uint32_t*>(line + u + 8 * 128) = pb;
+                        }
+                    };
+                    // First against the running maxima, without the tile's: weights of a thread that sum to
+                    // at most 2^8 are each at most that.  A warp with any other (or a NaN, or a row that
+                    // has kept no key so far) takes the tile's maxima.
+                    float2 s_a, s_b;
+                    bool fast = __all_sync(0xffffffffu, m_a != -INFINITY && m_b != -INFINITY);
+                    if (fast) {
+                        weights(m_a, m_b, s_a, s_b);
+                        fast = __all_sync(0xffffffffu, s_a.x + s_a.y <= kFastSumLimit && s_b.x + s_b.y <= kFastSumLimit);
                     }
+                    int moved = 0;
+                    if (!fast) {
+                        float ta = -INFINITY, tb = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float ya = x[4 * i + e] * scale_log2, yb = x[4 * i + 2 + e] * scale_log2;
+                                ta = fmaxf(ta, masked && 8 * i + e >= drop_a ? -INFINITY : ya);
+                                tb = fmaxf(tb, masked && 8 * i + e >= drop_b ? -INFINITY : yb);
+                            }
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
+                            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
+                        }
+                        float f_a = 1.f, f_b = 1.f;
+                        const bool need_a = ta > m_a + kRescaleThreshold, need_b = tb > m_b + kRescaleThreshold;
+                        if (need_a) {
+                            f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - ta);
+                            l_a = fmul2(l_a, make_float2(f_a, f_a));
+                            m_a = ta;
+                        }
+                        if (need_b) {
+                            f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - tb);
+                            l_b = fmul2(l_b, make_float2(f_b, f_b));
+                            m_b = tb;
+                        }
+                        if ((lane & 3) == 0) {
+                            factors[(n_tile & 1) * NR + ra] = f_a;
+                            factors[(n_tile & 1) * NR + rb] = f_b;
+                        }
+                        moved = __any_sync(0xffffffffu, need_a || need_b);
+                        // (a row that has kept no key yet: all of its weights are 0)
+                        weights(m_a == -INFINITY ? 0.f : m_a, m_b == -INFINITY ? 0.f : m_b, s_a, s_b);
+                    } else if ((lane & 3) == 0) {
+                        factors[(n_tile & 1) * NR + ra] = 1.f;
+                        factors[(n_tile & 1) * NR + rb] = 1.f;
+                    }
+                    l_a = fadd2(l_a, s_a);
+                    l_b = fadd2(l_b, s_b);
+                    if (lane == 0) flags[(n_tile & 1) * kSoftmaxWarps + warp] = moved;
                 } else if (lane == 0) {
                     flags[(n_tile & 1) * kSoftmaxWarps + warp] = 0;
                 }
@@ -620,8 +654,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     // keys that no row of the block keeps: their values are zeroed, since memory may
                     // hold anything there (or nothing was copied) and a weight of 0 must not meet a NaN
                     const int r0 = max(hi - key0, 0), per_chunk = (BN - r0) * 8;   // 16-byte units
-                    // (the wait, long over, orders these writes after the copies)
-                    if (!(ok = wait(C::B_TILE + n_tile % C::NTB, (n_tile / C::NTB) & 1, kErrTimeoutLoad))) break;
+                    // (the waits, long over, order these writes after the copies)
+                    for (uint32_t i = 2 * n_tile; ok && i < 2 * n_tile + 2; ++i)
+                        ok = wait(C::B_HALF + i % C::NHB, (i / C::NHB) & 1, kErrTimeoutLoad);
+                    if (!ok) break;
                     for (int p = 0; p < NP; ++p) {
                         const uint32_t s = (n_tile * NP + p) % NPS;
                         uint8_t* at = smem + C::OFF_PAIR + s * kPair;
@@ -668,48 +704,53 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!(ok = meet()) || !(ok = wait(C::B_PV + ((n_tile - 1) & 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
             tc_fence_after();
             constexpr int EC = NR < 32 ? 16 : 32;   // columns (rows of the block) at a time
-#pragma unroll 1
-            for (int q = 0; q < NP * NR / EC; ++q) {
+            uint32_t r[2][EC];
+            auto load = [&](int q, uint32_t (&to)[EC]) {
+                if constexpr (EC == 32) tc_ld_32x32b_x32(lanes + C::COL_O + q * EC, to);
+                else tmem_load16(lanes + C::COL_O + q * EC, to);
+            };
+            auto write = [&](int q, const uint32_t (&v)[EC]) {
                 const int c0 = (q * EC) % NR;       // the first of these rows
-                if (c0 >= n_out) continue;
-                uint32_t r[EC];
-                if constexpr (EC == 32) tc_ld_32x32b_x32(lanes + C::COL_O + q * EC, r);
-                else tmem_load16(lanes + C::COL_O + q * EC, r);
-                tc_wait_ld();
-                const int d0 = q * EC / NR * 128 + warp * 32;
+                const int d0 = q * EC / NR * 128 + warp * 32, n_here = n_out - c0;
                 if (whole) {
                     // two lanes swap halves of two rows, so that a lane has two values of one row
                     __half* dst = a.out + static_cast<size_t>(out0 + c0 + (lane & 1)) * C::R + d0 + (lane & ~1);
 #pragma unroll
                     for (int i = 0; i < EC; i += 2) {
                         const float2 f = *reinterpret_cast<const float2*>(inv_sum + c0 + i);
-                        const float v0 = __uint_as_float(r[i]) * f.x, v1 = __uint_as_float(r[i + 1]) * f.y;
+                        const float v0 = __uint_as_float(v[i]) * f.x, v1 = __uint_as_float(v[i + 1]) * f.y;
                         const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
                         const __half2 h = (lane & 1) ? __floats2half2_rn(other, v1) : __floats2half2_rn(v0, other);
-                        if (c0 + i + (lane & 1) < n_out) *reinterpret_cast<__half2*>(dst + i * C::R) = h;
+                        if (i + (lane & 1) < n_here) *reinterpret_cast<__half2*>(dst + i * C::R) = h;
                     }
                 } else {
                     float* dst = a.part_o + (static_cast<size_t>(part) * NR + c0) * C::R + d0 + lane;
-                    const int n_here = n_out - c0;
-                    if (n_here >= EC) {
 #pragma unroll
-                        for (int i = 0; i < EC; ++i) dst[i * C::R] = __uint_as_float(r[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < EC; ++i)
-                            if (i < n_here) dst[i * C::R] = __uint_as_float(r[i]);
-                    }
+                    for (int i = 0; i < EC; ++i)
+                        if (i < n_here) dst[i * C::R] = __uint_as_float(v[i]);
                 }
+            };
+            constexpr int NQ = NP * NR / EC;
+            static_assert(NQ % 2 == 0, "two at a time");
+            load(0, r[0]);
+#pragma unroll 1
+            for (int q = 0; q < NQ; q += 2) {
+                tc_wait_ld();
+                load(q + 1, r[1]);
+                write(q, r[0]);
+                tc_wait_ld();
+                if (q + 2 < NQ) load(q + 2, r[0]);
+                write(q + 1, r[1]);
             }
             if (tid == 0) {
-                // what the join needs of this CTA: [0] the item its run goes on with ends in it, [1] it
-                // leaves an item open, [2], [3] that item
+                // what the join needs of this CTA: [0] the item its run goes on with ends in it; [1] the
+                // rows to write of the item that it leaves open (0: none), [2] the first of them
                 int* meta = a.meta + blockIdx.x * 4;
-                if (w.off > 0) meta[0] = w.off + w.n == w.tiles;
-                else if (!whole) {
-                    meta[1] = 1;
-                    meta[2] = w.b;
-                    meta[3] = w.g;
+                if (w.off > 0) {
+                    meta[0] = w.off + w.n == w.tiles;
+                } else if (!whole) {
+                    meta[1] = n_out;
+                    meta[2] = static_cast<int>(out0);
                 }
             }
             tc_fence_before();
@@ -730,41 +771,63 @@ constexpr int kJoinWarps = 8;
 template <int NP, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Args a, int n_ctas) {
     constexpr int R = NP * 128;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the next call's attention waits for this kernel)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // for the whole of latent_attend_kernel
-    const int* meta = a.meta + blockIdx.x * 4;
-    if (!meta[1]) return;
     const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const Chunk c = load_chunk(a, meta[2]);
-    const long long at = (static_cast<long long>(meta[3]) * a.side + blockIdx.x % a.side) * NR + row;
-    const long long orow = static_cast<long long>(c.q_base) * a.H + at;
-    if (at >= static_cast<long long>(c.n) * a.H || orow < 0 || orow >= static_cast<long long>(a.total_q) * a.H) return;
-    // the parts: the end of CTA c's run, whole runs of the same item, the beginning of the last
-    float mx = a.part_ml[(static_cast<size_t>(blockIdx.x) * 2 + 1) * NR + row].x;
-    int last = blockIdx.x;
-    while (last + a.side < n_ctas) {
-        last += a.side;
-        mx = fmaxf(mx, a.part_ml[static_cast<size_t>(last) * 2 * NR + row].x);
-        if (a.meta[last * 4]) break;
-    }
+    const int4 meta = *reinterpret_cast<const int4*>(a.meta + blockIdx.x * 4);
+    const size_t orow = static_cast<size_t>(static_cast<uint32_t>(meta.z)) + row;
+    // The parts: the end of CTA c's run, whole runs of the same item, the beginning of the last.  A
+    // lane each reads their statistics (32 at a time), then all read their values.
     float2 o[NP * 2];
-    float sum = 0.f;
+    float sum = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < NP * 2; ++e) o[e] = make_float2(0.f, 0.f);
-    for (int i = blockIdx.x; i <= last; i += a.side) {
-        const size_t p = (static_cast<size_t>(i) * 2 + (i == static_cast<int>(blockIdx.x) ? 1 : 0)) * NR + row;
-        const float2 x = a.part_ml[p];
-        const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - mx);
-        sum = fmaf(f, x.y, sum);
-        const float4* src = reinterpret_cast<const float4*>(a.part_o + p * R) + lane;
+    for (int c0 = blockIdx.x, ended = 0; !ended && c0 < n_ctas; c0 += 32 * a.side) {
+        const int i = c0 + lane * a.side;
+        const bool first = i == static_cast<int>(blockIdx.x);
+        float2 x = make_float2(-INFINITY, 0.f);
+        int end = 0;
+        if (i < n_ctas) {
+            x = a.part_ml[(static_cast<size_t>(i) * 2 + first) * NR + row];
+            end = !first && a.meta[i * 4];
+        }
+        if (row >= meta.y) return;   // (looked at beside the first loads, whose addresses do not need it)
+        const unsigned ends = __ballot_sync(0xffffffffu, end);
+        int n = min(32, (n_ctas - c0 + a.side - 1) / a.side);
+        if (ends) {
+            n = min(n, __ffs(ends));
+            ended = 1;
+        }
+        if (lane >= n) x = make_float2(-INFINITY, 0.f);
+        float top = x.x;
 #pragma unroll
-        for (int e = 0; e < NP; ++e) {
-            const float4 v = src[e * 32];
-            o[2 * e] = ffma2(make_float2(v.x, v.y), make_float2(f, f), o[2 * e]);
-            o[2 * e + 1] = ffma2(make_float2(v.z, v.w), make_float2(f, f), o[2 * e + 1]);
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        top = fmaxf(top, mx);
+        const float old = mx == -INFINITY ? 0.f : ex2_approx(mx - top);
+        const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+        mx = top;
+        float part = f * x.y;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xffffffffu, part, s);
+        sum = fmaf(sum, old, part);
+#pragma unroll
+        for (int e = 0; e < NP * 2; ++e) o[e] = fmul2(o[e], make_float2(old, old));
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const int j = c0 + k * a.side;
+            const float g = __shfl_sync(0xffffffffu, f, k);
+            const float4* src = reinterpret_cast<const float4*>(
+                                    a.part_o + ((static_cast<size_t>(j) * 2 + (j == static_cast<int>(blockIdx.x))) * NR + row) * R) + lane;
+#pragma unroll
+            for (int e = 0; e < NP; ++e) {
+                const float4 v = src[e * 32];
+                o[2 * e] = ffma2(make_float2(v.x, v.y), make_float2(g, g), o[2 * e]);
+                o[2 * e + 1] = ffma2(make_float2(v.z, v.w), make_float2(g, g), o[2 * e + 1]);
+            }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    uint2* dst = reinterpret_cast<uint2*>(a.out + static_cast<size_t>(orow) * R) + lane;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + orow * R) + lane;
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
         const __half2 h0 = __floats2half2_rn(o[2 * e].x * inv, o[2 * e].y * inv);
@@ -796,7 +859,7 @@ Plan make_plan(int max_q, int H, int R) {
 template <int NP, int NR>
 attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     using C = Cfg<NP, NR>;
-    CUtensorMap tq, tx;
+    CUtensorMap tq, tx1, tx2;
     Args a;
     attn_status st;
     {
@@ -810,10 +873,12 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     a.n_slots = L.cache.page_table ? L.cache.n_pages : L.B;
     a.box_rows = L.cache.page_table && rows < BN ? rows : BN;
     {
-        const uint64_t dims[3] = {(uint64_t)C::W, (uint64_t)rows, (uint64_t)a.n_slots};
-        const uint64_t strides[2] = {(uint64_t)C::W * 2, (uint64_t)C::W * 2 * rows};
-        const uint32_t box[3] = {64u, (uint32_t)a.box_rows, 1u};
-        if ((st = encode_tmap_sw128(&tx, L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, strides, box)) != ATTN_OK)
+        // rows of 9 (5) chunks of 64 values: boxes of one chunk of some rows, or of two of a tile's
+        const uint64_t dims[4] = {64u, (uint64_t)rows, (uint64_t)C::NCH, (uint64_t)a.n_slots};
+        const uint64_t strides[3] = {(uint64_t)C::W * 2, 128u, (uint64_t)C::W * 2 * rows};
+        const uint32_t box1[4] = {64u, (uint32_t)a.box_rows, 1u, 1u}, box2[4] = {64u, (uint32_t)a.box_rows, 2u, 1u};
+        if ((st = encode_tmap_sw128(&tx1, L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims, strides, box1)) != ATTN_OK ||
+            (st = encode_tmap_sw128(&tx2, L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims, strides, box2)) != ATTN_OK)
             return st;
     }
     auto kernel = latent_attend_kernel<NP, NR>;
@@ -855,21 +920,10 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
               "total_q=%d H=%d box_rows=%d, then latent_join_kernel grid=(%u,%u)",
               C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, a.box_rows,
               join.x, join.y);
-    kernel<<<grid, kThreads, C::SMEM_ALLOC, L.stream>>>(tq, tx, a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) {
-        // set up while latent_attend_kernel runs: the join waits for its end itself
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = join;
-        cfg.blockDim = dim3(kJoinWarps * 32);
-        cfg.stream = L.stream;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, latent_join_kernel<NP, NR>, a, grid);
-    }
+    // both are set up while the kernel before runs, and wait for its end themselves
+    cudaError_t e = launch_dependent(kernel, dim3(grid), kThreads, C::SMEM_ALLOC, L.stream, tq, tx2, tx1, a);
+    if (e == cudaSuccess)
+        e = launch_dependent(latent_join_kernel<NP, NR>, join, kJoinWarps * 32, 0, L.stream, a, grid);
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent attend launch failed: %s", cudaGetErrorString(e));
     return ATTN_OK;
 }
