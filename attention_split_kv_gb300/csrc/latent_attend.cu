@@ -49,8 +49,7 @@ constexpr int kSegTiles = 2;                // a segment's fixed cost, in key ti
 constexpr int kSoftmaxWarps = 4;
 constexpr int kTmaWarp = kSoftmaxWarps, kSWarp = kTmaWarp + 1;   // and the PV warp
 constexpr int kThreads = (kSoftmaxWarps + 3) * 32;
-constexpr uint32_t kPair = 2 * BN * 128;    // bytes of 128 values of a tile: two 64-value chunks
-constexpr uint32_t kRope = BN * 128;        // of its rotated part
+constexpr uint32_t kChunk = BN * 128;       // bytes of 64 values of a tile
 
 // instruction descriptor: f16 operands, f32 accumulation; A's major (1: MN), B K-major
 __host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_mn) {
@@ -62,26 +61,34 @@ template <int NP, int NR>
 struct Cfg {
     static constexpr int R = NP * 128, W = R + 64, NCH = 2 * NP + 1;
     static constexpr uint32_t Q_CHUNK = NR * 128, Q_BYTES = NCH * Q_CHUNK;
+    // The ring's places hold half a tile each: NP chunks of 64 values, the second half's with the
+    // rotated part behind them.  An even number is packed as tiles.
+    static constexpr int NHS = NP == 2 ? 8 : NR == 16 ? 5 : 4;
+    static constexpr uint32_t H0 = NP * kChunk, H1 = H0 + kChunk;
+    static constexpr uint32_t RING_BYTES = NHS % 2 ? NHS * H1 : NHS / 2 * (H0 + H1);
     // 64 rows of 512 values: P takes the place of its tile's rotated part, which only S needs
     static constexpr bool ALIAS = NP == 4 && NR == 64;
-    static constexpr int NPS = NP == 2 || NR == 64 ? 8 : NR == 32 ? 10 : 11;   // 128-value parts
-    static constexpr int NRS = NP == 2 ? 4 : NR == 16 ? 3 : 2;                 // rotated parts
     static constexpr uint32_t P_BYTES = NR * 128;
     static constexpr uint32_t OFF_Q = 0;
-    static constexpr uint32_t OFF_PAIR = (Q_BYTES + 1023) / 1024 * 1024;
-    static constexpr uint32_t OFF_ROPE = OFF_PAIR + NPS * kPair;
-    static constexpr uint32_t OFF_P = ALIAS ? OFF_ROPE : OFF_ROPE + NRS * kRope;
-    static constexpr uint32_t OFF_ROWS = OFF_ROPE + NRS * kRope + (ALIAS ? 0 : 2 * P_BYTES);
+    static constexpr uint32_t OFF_RING = (Q_BYTES + 1023) / 1024 * 1024;
+    static constexpr uint32_t OFF_P = OFF_RING + RING_BYTES;
+    static constexpr uint32_t OFF_ROWS = OFF_P + (ALIAS ? 0 : 2 * P_BYTES);
     // words of the rows: rescale factors of two tiles, then 1 / sum of two segments
     static constexpr uint32_t OFF_FLAGS = OFF_ROWS + 4 * NR * 4;   // [2][4] words
     static constexpr uint32_t OFF_SUMS = OFF_FLAGS + 32;           // the run's search
-    static constexpr int NHB = 8;      // halves of tiles that the ring can hold parts of, at most
-    static_assert(NHB * NP / 2 >= NPS, "a half's barrier is free when its first part's place is");
+    // of place s, from the ring's start
+    __device__ static __forceinline__ uint32_t place(uint32_t s) {
+        return NHS % 2 ? s * H1 : (s >> 1) * (H0 + H1) + (s & 1) * H0;
+    }
+    // P of tile i, from shared memory's start
+    __device__ static __forceinline__ uint32_t p_of(uint32_t i) {
+        return ALIAS ? OFF_RING + (i & 1) * (H0 + H1) + 2 * H0 : OFF_P + (i & 1) * P_BYTES;
+    }
+    static_assert(!ALIAS || NHS == 4, "P of tile i in place 2 i + 1");
     enum : int {
         B_QFULL, B_QEMPTY,
-        B_HALF,                        // half a tile is there (the second one with the rotated part)
-        B_PAIRFREE = B_HALF + NHB, B_ROPEFREE = B_PAIRFREE + NPS,
-        B_S = B_ROPEFREE + NRS,
+        B_FULL, B_FREE = B_FULL + NHS,   // of the ring's places
+        B_S = B_FREE + NHS,
         B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
         B_PV = B_P + 2,            // a tile's second product is done
         B_FIX = B_PV + 2,  // O is rescaled
@@ -99,6 +106,7 @@ struct Cfg {
     static_assert(OFF_SUMS % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
     // S's A operand is read as 64 rows: past NR those are whatever follows Q's chunk
     static_assert(OFF_Q + (NCH - 1) * Q_CHUNK + 64 * 128 <= OFF_ROWS, "Q's rows past NR");
+    static_assert(NP % 2 == 0, "halves of whole blocks");
 };
 
 struct Args {
@@ -110,7 +118,7 @@ struct Args {
     int* meta;           // [CTA][4]
     int* err;
     int B, total_q, max_q, H;
-    int log2P, max_pages, n_slots, box_rows;   // slots: pages, or the contiguous cache's sequences
+    int log2P, max_pages, n_slots, log_nb;   // 2^log_nb boxes a tile; slots: pages, or the contiguous cache's sequences
     int n_rb;            // row blocks of the longest chunk
     int side;            // row blocks of a sequence that neighbouring CTAs take side by side
     int capacity;
@@ -188,10 +196,10 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
 
 template <int NP, int NR>
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x2,
-                     const __grid_constant__ CUtensorMap tm_x1, const Args a) {
+latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_h0,
+                     const __grid_constant__ CUtensorMap tm_h1, const __grid_constant__ CUtensorMap tm_box, const Args a) {
     using C = Cfg<NP, NR>;
-    constexpr int NPS = C::NPS;
+    constexpr int NHS = C::NHS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -202,8 +210,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == kSoftmaxWarps * 32) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_x2);
-        tma_prefetch_desc(&tm_x1);
+        tma_prefetch_desc(a.log_nb ? &tm_box : &tm_h0);
+        tma_prefetch_desc(a.log_nb ? &tm_box : &tm_h1);
     }
     // A wait of a whole warp, with one answer for all of its lanes.
     auto wait = [&](int b, uint32_t parity, int code) -> bool {
@@ -310,87 +318,62 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA: Q, then the tiles
-        // A 128-value part is one box of two chunks where the tile lies in one page (or none), else
-        // a box a page and chunk: lane l brings page l % nb of chunk l / nb.
-        const int nb = BN / a.box_rows, bx = lane & (nb - 1), P = 1 << a.log2P;
-        uint32_t n_pair = 0, n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
-        uint32_t s_pair = 0, s_rope = 0, free_phase = 0, rope_phase = 0;   // places in the rings, phases of their barriers
+        // Half a tile is one box where the tile lies in one page (or none), else a box a page and
+        // chunk.  (The whole warp runs the code and one lane issues.)
+        const uint32_t one = elect_one();
+        const int log_nb = a.log_nb, nb = 1 << log_nb, box_rows = BN >> log_nb, P = 1 << a.log2P;
+        uint32_t n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
+        uint32_t s = 0, phase = 1;                 // place, and the phase of its release (the first round waits for none)
         bool ok = true;
         Walk w = run;
         for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
             const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int hi = key_end(a, w.c, row0 + NR);
-            if (n_seg > 0 && !(ok = wait(C::B_QEMPTY, (n_seg - 1) & 1, kErrTimeoutSlot))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(C::B_QFULL), C::Q_BYTES);
-                const int q_row = static_cast<int>(w.c.q_base * static_cast<uint32_t>(a.H) + row0);
-                for (int c = 0; c < C::NCH; ++c)
-                    tma_load_2d(sbase + C::OFF_Q + c * C::Q_CHUNK, &tm_q, bar(C::B_QFULL), c * 64, q_row);
-            }
-            ++n_q;
-            // the place of this lane's box in tile j, page id or sequence: read a tile before its copies
+            // the page of box `lane` of tile j, or the sequence: read a tile before its copies
             auto fetch = [&](int j) {
-                const int kk = (w.off + j) * BN + bx * a.box_rows;
+                const int kk = (w.off + j) * BN + lane * box_rows;
                 if (!a.page_table) return w.b;
-                return j < w.n && kk < hi ? __ldg(&a.page_table[static_cast<size_t>(w.b) * a.max_pages + (kk >> a.log2P)]) : 0;
+                return lane < nb && j < w.n && kk < hi
+                           ? __ldg(&a.page_table[static_cast<size_t>(w.b) * a.max_pages + (kk >> a.log2P)]) : 0;
             };
             int slot = fetch(0);
+            if (n_seg > 0 && !(ok = wait(C::B_QEMPTY, (n_seg - 1) & 1, kErrTimeoutSlot))) break;
+            mbar_arrive_expect_tx_one(one, bar(C::B_QFULL), C::Q_BYTES);
+            tma_load_3d_one(one, sbase + C::OFF_Q, &tm_q, bar(C::B_QFULL), 0,
+                            static_cast<int>(w.c.q_base * static_cast<uint32_t>(a.H) + row0), 0);
+            ++n_q;
+            int key0 = w.off * BN;
 #pragma unroll 1
-            for (int j = 0; j < w.n; ++j) {
-                const int key0 = (w.off + j) * BN, kk = key0 + bx * a.box_rows;
-                const int boxes = hi > key0 ? min(nb, (hi - key0 + a.box_rows - 1) / a.box_rows) : 0;
-                const bool has = kk < hi;
-                int row = kk, cur = slot;
-                if (a.page_table) {
-                    row = kk & (P - 1);
-                    if (has && (cur < 0 || cur >= a.n_slots)) {
-                        atomicExch(a.err, kErrLatentPage);   // never read: its keys are zeros
-                        cur = a.n_slots;
-                    }
+            for (int j = 0; j < w.n; ++j, key0 += BN) {
+                const int boxes = hi > key0 ? min(nb, (hi - key0 + box_rows - 1) >> (6 - log_nb)) : 0;
+                const int row = a.page_table ? key0 & (P - 1) : key0;   // (0 where a tile has several pages)
+                if (a.page_table && (slot < 0 || slot >= a.n_slots)) {
+                    atomicExch(a.err, kErrLatentPage);   // never read: its keys are zeros
+                    slot = a.n_slots;
                 }
+                const int cur = slot;
                 slot = fetch(j + 1);
-                // The halves' byte counts are posted after their copies: a half given up in between
-                // then has the bytes that are on their way.
-#pragma unroll 1
+#pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t full = bar(C::B_HALF + n_half % C::NHB);
-                    uint32_t bytes = 0;
-                    for (int p = 0; p < NP / 2 && ok; ++p) {
-                        if (n_pair >= NPS && !(ok = wait(C::B_PAIRFREE + s_pair, free_phase, kErrTimeoutSlot))) break;
-                        const uint32_t dst = sbase + C::OFF_PAIR + s_pair * kPair + bx * a.box_rows * 128;
-                        const int x0 = (h * (NP / 2) + p) * 2;   // the part's first chunk
-                        if (has) {
-                            if (nb == 1) {
-                                if (lane == 0) tma_load_4d(dst, &tm_x2, full, 0, row, x0, cur);
-                            } else if (lane < 2 * nb) {
-                                const int c = lane / nb;
-                                tma_load_4d(dst + c * (BN * 128), &tm_x1, full, 0, row, x0 + c, cur);
-                            }
-                        }
-                        bytes += 2 * boxes * a.box_rows * 128;
-                        ++n_pair;
-                        if (++s_pair == NPS) {
-                            s_pair = 0;
-                            if (n_pair > NPS) free_phase ^= 1;
+                    if (!(ok = wait(C::B_FREE + s, phase, kErrTimeoutSlot))) break;
+                    const uint32_t dst = sbase + C::OFF_RING + C::place(s), full = bar(C::B_FULL + s);
+                    mbar_arrive_expect_tx_one(one, full, static_cast<uint32_t>(boxes * box_rows) * 128 * (NP + h));
+                    if (log_nb == 0) {
+                        if (boxes) tma_load_4d_one(one, dst, h ? &tm_h1 : &tm_h0, full, 0, row, h * NP, __shfl_sync(0xffffffffu, cur, 0));
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < boxes; ++i) {
+                            const int page = __shfl_sync(0xffffffffu, cur, i);
+#pragma unroll
+                            for (int c = 0; c < NP + h; ++c)
+                                tma_load_4d_one(one, dst + c * kChunk + i * box_rows * 128, &tm_box, full, 0, 0, h * NP + c, page);
                         }
                     }
-                    if (h == 1 && ok) {
-                        if (n_half >= 2 * C::NRS && !(ok = wait(C::B_ROPEFREE + s_rope, rope_phase, kErrTimeoutSlot))) {
-                        } else {
-                            if (has && lane < nb)
-                                tma_load_4d(sbase + C::OFF_ROPE + s_rope * kRope + bx * a.box_rows * 128, &tm_x1, full, 0, row,
-                                            2 * NP, cur);
-                            bytes += boxes * a.box_rows * 128;
-                            if (++s_rope == C::NRS) {
-                                s_rope = 0;
-                                if (n_half > 2 * C::NRS) rope_phase ^= 1;
-                            }
-                        }
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                    __syncwarp();
                     ++n_half;
-                    if (!ok) break;
+                    if (++s == NHS) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
                 if (!ok) break;
             }
@@ -399,22 +382,21 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // let copies already in flight land before the CTA's shared memory goes away
             if (lane == 0) {
                 if (n_q > 0) mbar_wait_drain(bar(C::B_QFULL), (n_q - 1) & 1, a.err, kErrTimeoutLoad);
-                for (uint32_t i = n_half > C::NHB ? n_half - C::NHB : 0; i < n_half; ++i)
-                    mbar_wait_drain(bar(C::B_HALF + i % C::NHB), (i / C::NHB) & 1, a.err, kErrTimeoutLoad);
+                for (uint32_t i = n_half > NHS ? n_half - NHS : 0; i < n_half; ++i)
+                    mbar_wait_drain(bar(C::B_FULL + i % NHS), (i / NHS) & 1, a.err, kErrTimeoutLoad);
             }
         }
     } else if (warp >= kSWarp) {
         // ------------------------------------------------------------ MMA issuers
         // (the whole warp runs the code; one lane issues)
         const uint32_t one = elect_one();
-        const uint64_t x_desc = smem_desc_sw128(sbase + C::OFF_PAIR, 16, 1024);
         bool ok = true;
-        uint32_t n_tile = 0, n_seg = 0;
+        uint32_t n_tile = 0, n_seg = 0, s = 0, phase = 0;   // s, phase: the ring's place
         Walk w = run;
         if (warp == kSWarp) {
             constexpr uint32_t id_s = idesc(64, BN, 0);
             const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
-            const uint64_t r_desc = smem_desc_sw128(sbase + C::OFF_ROPE, 16, 1024);
+            const uint64_t x_desc = smem_desc_sw128(sbase + C::OFF_RING, 16, 1024);
             const bool stall = stall_first_tile();
             for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
                 if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
@@ -422,39 +404,31 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     // (the S of two tiles before has been read once its weights are written)
                     if (n_tile > 1 && !(ok = wait(C::B_P + (n_tile & 1), ((n_tile >> 1) - 1) & 1, kErrTimeoutSoftmax))) break;
                     const uint32_t s_tmem = tmem + (n_tile & 1) * BN;
-                    uint32_t s = n_tile * NP % NPS;
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        if (p % (NP / 2) == 0) {
-                            const uint32_t i = 2 * n_tile + p / (NP / 2);
-                            if (!(ok = wait(C::B_HALF + i % C::NHB, (i / C::NHB) & 1, kErrTimeoutLoad))) break;
-                            tc_fence_after();
-                        }
-                        const uint64_t xd = desc_advance(x_desc, s * kPair);
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(ok = wait(C::B_FULL + s, phase, kErrTimeoutLoad))) break;
+                        tc_fence_after();
+                        const uint64_t xd = desc_advance(x_desc, C::place(s));
 #pragma unroll
-                        for (int c = 0; c < 2; ++c)
+                        for (int c = 0; c < NP + h; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(q_desc, (2 * p + c) * C::Q_CHUNK + kk * 32),
-                                                  desc_advance(xd, c * (BN * 128) + kk * 32), id_s, (p | c | kk) != 0);
-                        s = s + 1 == NPS ? 0 : s + 1;
+                                tc_mma_f16_ss_one(one, s_tmem, desc_advance(q_desc, (h * NP + c) * C::Q_CHUNK + kk * 32),
+                                                  desc_advance(xd, c * kChunk + kk * 32), id_s, (h | c | kk) != 0);
+                        if (++s == NHS) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
                     if (!ok) break;
-                    const uint32_t rs = n_tile % C::NRS;
-                    const uint64_t rd = desc_advance(r_desc, rs * kRope);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f16_ss_one(one, s_tmem, desc_advance(q_desc, 2 * NP * C::Q_CHUNK + kk * 32), desc_advance(rd, kk * 32),
-                                          id_s, 1);
                     if (!(stall && n_tile == 0)) tc_commit_one(one, bar(C::B_S + (n_tile & 1)));
-                    if (!C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + rs));
                     if (j == w.n - 1) tc_commit_one(one, bar(C::B_QEMPTY));
                 }
             }
         } else {
             constexpr uint32_t id_o = idesc(128, NR, 1);
-            const uint64_t c_desc = smem_desc_sw128(sbase + C::OFF_PAIR, BN * 128, 1024);   // MN-major: next 64 values
-            const uint64_t p_desc = smem_desc_sw128(sbase + C::OFF_P, 16, 1024);
+            const uint64_t c_desc = smem_desc_sw128(sbase + C::OFF_RING, kChunk, 1024);   // MN-major: next 64 values
+            const uint64_t p_desc = smem_desc_sw128(sbase, 16, 1024);
             const int* flags = reinterpret_cast<const int*>(smem + C::OFF_FLAGS);
             uint32_t n_fix = 0;
             for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w)) {
@@ -465,19 +439,20 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         if ((f[0] | f[1] | f[2] | f[3]) && !(ok = wait(C::B_FIX, n_fix++ & 1, kErrTimeoutSoftmax))) break;
                     }
                     tc_fence_after();
-                    const uint64_t pd = desc_advance(p_desc, C::ALIAS ? (n_tile % C::NRS) * kRope : (n_tile & 1) * C::P_BYTES);
-                    uint32_t s = n_tile * NP % NPS;
+                    const uint64_t pd = desc_advance(p_desc, C::p_of(n_tile));
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        const uint64_t cd = desc_advance(c_desc, s * kPair);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t cd = desc_advance(c_desc, C::place(s));
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of X, 32 bytes of P's
-                            tc_mma_f16_ss_one(one, tmem + C::COL_O + p * NR, desc_advance(cd, kk * 2048),
-                                              desc_advance(pd, kk * 32), id_o, (j | kk) != 0);
-                        tc_commit_one(one, bar(C::B_PAIRFREE + s));
-                        s = s + 1 == NPS ? 0 : s + 1;
+                        for (int p = 0; p < NP / 2; ++p)
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 16 lines of X, 32 bytes of P's
+                                tc_mma_f16_ss_one(one, tmem + C::COL_O + (h * (NP / 2) + p) * NR,
+                                                  desc_advance(cd, p * 2 * kChunk + kk * 2048), desc_advance(pd, kk * 32), id_o,
+                                                  (j | kk) != 0);
+                        tc_commit_one(one, bar(C::B_FREE + s));
+                        s = s + 1 == NHS ? 0 : s + 1;
                     }
-                    if (C::ALIAS) tc_commit_one(one, bar(C::B_ROPEFREE + n_tile % C::NRS));
                     tc_commit_one(one, bar(C::B_PV + (n_tile & 1)));
                 }
             }
@@ -566,8 +541,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const int drop_a = lim_a - key0 - 2 * (lane & 3), drop_b = lim_b - key0 - 2 * (lane & 3);
                     // a row's line of P is its 64 weights, swizzled as the MMA reads it (both rows alike,
                     // ra % 8 == rb % 8)
-                    uint8_t* line = smem + C::OFF_P + (C::ALIAS ? (n_tile % C::NRS) * kRope : (n_tile & 1) * C::P_BYTES) +
-                                    ra * 128 + (lane & 3) * 4;
+                    uint8_t* line = smem + C::p_of(n_tile) + ra * 128 + (lane & 3) * 4;
                     const float2 f2 = make_float2(scale_log2, scale_log2);
                     // weights against the offsets; returns their sums (of the rounded ones, so that an
                     // output is a convex combination of values)
@@ -654,18 +628,16 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     // keys that no row of the block keeps: their values are zeroed, since memory may
                     // hold anything there (or nothing was copied) and a weight of 0 must not meet a NaN
                     const int r0 = max(hi - key0, 0), per_chunk = (BN - r0) * 8;   // 16-byte units
-                    // (the waits, long over, order these writes after the copies)
-                    for (uint32_t i = 2 * n_tile; ok && i < 2 * n_tile + 2; ++i)
-                        ok = wait(C::B_HALF + i % C::NHB, (i / C::NHB) & 1, kErrTimeoutLoad);
-                    if (!ok) break;
-                    for (int p = 0; p < NP; ++p) {
-                        const uint32_t s = (n_tile * NP + p) % NPS;
-                        uint8_t* at = smem + C::OFF_PAIR + s * kPair;
-                        for (int u = tid; u < 2 * per_chunk; u += kSoftmaxWarps * 32) {
-                            const int c = u >= per_chunk, v = u - c * per_chunk;
-                            *reinterpret_cast<uint4*>(at + c * (BN * 128) + r0 * 128 + v * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    for (uint32_t i = 2 * n_tile; i < 2 * n_tile + 2; ++i) {
+                        // (the wait, long over, orders these writes after the copies)
+                        if (!(ok = wait(C::B_FULL + i % NHS, (i / NHS) & 1, kErrTimeoutLoad))) break;
+                        uint8_t* at = smem + C::OFF_RING + C::place(i % NHS);
+                        for (int u = tid; u < NP * per_chunk; u += kSoftmaxWarps * 32) {
+                            const int c = u / per_chunk, v = u - c * per_chunk;
+                            *reinterpret_cast<uint4*>(at + c * kChunk + r0 * 128 + v * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
+                    if (!ok) break;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -859,27 +831,32 @@ Plan make_plan(int max_q, int H, int R) {
 template <int NP, int NR>
 attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     using C = Cfg<NP, NR>;
-    CUtensorMap tq, tx1, tx2;
+    CUtensorMap tq, tx[3];
     Args a;
     attn_status st;
     {
-        const uint64_t dims[2] = {(uint64_t)C::W, (uint64_t)L.total_q * L.H};
-        const uint64_t strides[1] = {(uint64_t)C::W * 2};
-        const uint32_t box[2] = {64u, (uint32_t)NR};
-        if ((st = encode_tmap_sw128(&tq, L.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, dims, strides, box)) != ATTN_OK)
+        // rows of 9 (5) chunks of 64 values, all chunks of a block in one box
+        const uint64_t dims[3] = {64u, (uint64_t)L.total_q * L.H, (uint64_t)C::NCH};
+        const uint64_t strides[2] = {(uint64_t)C::W * 2, 128u};
+        const uint32_t box[3] = {64u, (uint32_t)NR, (uint32_t)C::NCH};
+        if ((st = encode_tmap_sw128(&tq, L.q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, dims, strides, box)) != ATTN_OK)
             return st;
     }
     const int rows = L.cache.rows;
     a.n_slots = L.cache.page_table ? L.cache.n_pages : L.B;
-    a.box_rows = L.cache.page_table && rows < BN ? rows : BN;
+    const int box_rows = L.cache.page_table && rows < BN ? rows : BN;
+    a.log_nb = 0;
+    while ((BN >> a.log_nb) > box_rows) ++a.log_nb;
     {
-        // rows of 9 (5) chunks of 64 values: boxes of one chunk of some rows, or of two of a tile's
+        // the same: boxes of half a tile's chunks, or of one chunk of a page
         const uint64_t dims[4] = {64u, (uint64_t)rows, (uint64_t)C::NCH, (uint64_t)a.n_slots};
         const uint64_t strides[3] = {(uint64_t)C::W * 2, 128u, (uint64_t)C::W * 2 * rows};
-        const uint32_t box1[4] = {64u, (uint32_t)a.box_rows, 1u, 1u}, box2[4] = {64u, (uint32_t)a.box_rows, 2u, 1u};
-        if ((st = encode_tmap_sw128(&tx1, L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims, strides, box1)) != ATTN_OK ||
-            (st = encode_tmap_sw128(&tx2, L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims, strides, box2)) != ATTN_OK)
-            return st;
+        const uint32_t chunks[3] = {(uint32_t)NP, (uint32_t)NP + 1, 1u};
+        for (int i = 0; i < 3; ++i) {
+            const uint32_t box[4] = {64u, (uint32_t)box_rows, chunks[i], 1u};
+            if ((st = encode_tmap_sw128(&tx[i], L.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, dims, strides, box)) != ATTN_OK)
+                return st;
+        }
     }
     auto kernel = latent_attend_kernel<NP, NR>;
     static bool attr_set[64] = {};
@@ -918,10 +895,10 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     if (trace_enabled())
         trace("latent_attend_kernel<R=%d,rows=%d> grid=%d block=%d smem=%u tmem_cols=%u row_blocks=%d side=%d B=%d "
               "total_q=%d H=%d box_rows=%d, then latent_join_kernel grid=(%u,%u)",
-              C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, a.box_rows,
+              C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, box_rows,
               join.x, join.y);
     // both are set up while the kernel before runs, and wait for its end themselves
-    cudaError_t e = launch_dependent(kernel, dim3(grid), kThreads, C::SMEM_ALLOC, L.stream, tq, tx2, tx1, a);
+    cudaError_t e = launch_dependent(kernel, dim3(grid), kThreads, C::SMEM_ALLOC, L.stream, tq, tx[0], tx[1], tx[2], a);
     if (e == cudaSuccess)
         e = launch_dependent(latent_join_kernel<NP, NR>, join, kJoinWarps * 32, 0, L.stream, a, grid);
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent attend launch failed: %s", cudaGetErrorString(e));
