@@ -26,10 +26,11 @@
 // into equal runs, one a CTA; rows of items cut by a run's end go to the workspace and are
 // joined by a second kernel.
 //
-// Roles (7 warps): 4 softmax warps (warp w: rows 16 w .. + 15; all four zero what a tile has
-// too much, rescale O and write the rows out, 32 of O^T's lanes each), a TMA warp, a warp that
-// issues the S products and one that issues the others: each waits for its own operands only.
-// (One warp for both, polling what is ready: 150 cycles a poll, 4500 a tile whatever its rows.)
+// Roles (11 warps): 4 softmax warps (warp w: rows 16 w .. + 15; all four zero what a tile has
+// too much and rescale O, 32 of O^T's lanes each), a TMA warp, a warp that issues the S products
+// and one that issues the others: each waits for its own operands only (one warp for both,
+// polling what is ready: 150 cycles a poll, 4500 a tile whatever its rows).  A segment's rows are
+// written by the softmax warps and 4 that do only that.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,10 +46,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
 constexpr float kFastSumLimit = 256.0f;
 constexpr int kMaxCtas = 152;               // one CTA an SM
-constexpr int kSegTiles = 2;                // a segment's fixed cost, in key tiles
+constexpr int kWholeTiles = 4;              // items of at most this many tiles are not cut
 constexpr int kSoftmaxWarps = 4;
 constexpr int kTmaWarp = kSoftmaxWarps, kSWarp = kTmaWarp + 1;   // and the PV warp
-constexpr int kThreads = (kSoftmaxWarps + 3) * 32;
+constexpr int kOutWarp = kSWarp + 2;
+constexpr int kThreads = (kOutWarp + 4) * 32;
 constexpr uint32_t kChunk = BN * 128;       // bytes of 64 values of a tile
 
 // instruction descriptor: f16 operands, f32 accumulation; A's major (1: MN), B K-major
@@ -60,6 +62,7 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_
 template <int NP, int NR>
 struct Cfg {
     static constexpr int R = NP * 128, W = R + 64, NCH = 2 * NP + 1;
+    static constexpr int SEG = NR == 64 ? 4 : 2;           // a segment's fixed cost, in key tiles
     static constexpr uint32_t Q_CHUNK = NR * 128, Q_BYTES = NCH * Q_CHUNK;
     // The ring's places hold half a tile each: NP chunks of 64 values, the second half's with the
     // rotated part behind them.  An even number is packed as tiles.
@@ -92,11 +95,12 @@ struct Cfg {
         B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
         B_PV = B_P + 2,            // a tile's second product is done
         B_FIX = B_PV + 2,  // O is rescaled
-        B_MEET,            // the softmax warps met
+        B_MEET,            // the softmax warps have a segment's sums, and its products are done
+        B_OUT,             // the other four warps have read its O
         B_TEARDOWN,                    // of both issuers
         N_BARS = B_TEARDOWN + 2
     };
-    static constexpr uint32_t OFF_BAR = OFF_SUMS + 10 * 8;
+    static constexpr uint32_t OFF_BAR = OFF_SUMS + 14 * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
     static constexpr uint32_t COL_O = 2 * BN, COLS = COL_O + NP * NR;
@@ -122,6 +126,7 @@ struct Args {
     int n_rb;            // row blocks of the longest chunk
     int side;            // row blocks of a sequence that neighbouring CTAs take side by side
     int capacity;
+    int whole;           // items are not cut
     float scale;
 };
 
@@ -156,25 +161,25 @@ __device__ __forceinline__ int group_tiles(const Args& a, const Chunk& c, int g)
 }
 
 // A CTA's run, walked a segment (part of one item) at a time; every warp walks for itself.  A run
-// is a range of weights: an item weighs its key tiles and kSegTiles before them.
+// is a range of weights: an item weighs its key tiles and SEG before them.
 struct Walk {
     int b, g;            // sequence, group of row blocks
     long long in, rem;   // where the run enters the item; its weight from there on
     int off, n, tiles;   // first key tile and key tiles of the segment; key tiles of the item
     Chunk c;
 };
-template <int NR>
+template <int NR, int SEG>
 __device__ __forceinline__ bool walk_item(const Args& a, Walk& w) {
     if (w.rem <= 0) return false;
     w.c = load_chunk(a, w.b);
     w.tiles = group_tiles<NR>(a, w.c, w.g);
-    w.off = max(static_cast<int>(w.in) - kSegTiles, 0);
-    w.n = static_cast<int>(min(static_cast<long long>(w.tiles), w.in + w.rem - kSegTiles)) - w.off;
+    w.off = a.whole ? 0 : max(static_cast<int>(w.in) - SEG, 0);
+    w.n = (a.whole ? w.tiles : static_cast<int>(min(static_cast<long long>(w.tiles), w.in + w.rem - SEG))) - w.off;
     return w.n > 0;
 }
-template <int NR>
+template <int NR, int SEG>
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
-    w.rem -= w.tiles + kSegTiles - w.in;
+    w.rem -= w.tiles + SEG - w.in;
     w.in = 0;
     if (w.rem <= 0) return false;
     if (++w.g >= groups_of<NR>(a, w.c)) {
@@ -183,7 +188,12 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
             if (++w.b >= a.B) return false;
         } while (load_chunk(a, w.b).n == 0);
     }
-    return walk_item<NR>(a, w);
+    return walk_item<NR, SEG>(a, w);
+}
+template <int NR, int SEG>
+__device__ __forceinline__ bool walk_first(const Args& a, Walk& w) {
+    const bool on = walk_item<NR, SEG>(a, w);
+    return on && a.whole && w.in > 0 ? walk_next<NR, SEG>(a, w) : on;   // (whole items: those that start in the run)
 }
 
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
@@ -192,6 +202,58 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
+}
+
+// Where a segment's rows go: to out, or as a part to the workspace.
+struct Out {
+    long long row0;   // first row of out
+    int n, part;      // rows written; place of the part
+    bool whole;       // all of the item: to out
+};
+template <int NP, int NR>
+__device__ __forceinline__ Out out_of(const Args& a, const Walk& w, uint32_t row0) {
+    const long long live = static_cast<long long>(w.c.n) * a.H - row0, end = static_cast<long long>(a.total_q) * a.H;
+    Out o;
+    o.row0 = static_cast<long long>(w.c.q_base) * a.H + row0;
+    o.n = o.row0 < 0 ? 0 : static_cast<int>(max(0ll, min(min(live, static_cast<long long>(NR)), end - o.row0)));
+    o.part = static_cast<int>(blockIdx.x) * 2 + (w.off > 0 ? 0 : 1);
+    o.whole = w.n == w.tiles;
+    return o;
+}
+// 32 of O^T's lanes (`quarter`) of every second group of rows, from `first` on.
+template <int NP, int NR>
+__device__ __forceinline__ void write_rows(const Args& a, const Out& o, uint32_t o_tmem, int quarter, int first,
+                                           const float* inv_sum) {
+    constexpr int R = NP * 128, EC = NR < 32 ? 16 : 32, NQ = NP * NR / EC;   // columns (rows) at a time
+    const int lane = threadIdx.x & 31;
+    const uint32_t lanes = o_tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+    for (int q = first; q < NQ; q += 2) {
+        const int c0 = (q * EC) % NR;       // the first of these rows
+        const int d0 = q * EC / NR * 128 + quarter * 32, n_here = o.n - c0;
+        if (n_here <= 0) continue;
+        uint32_t v[EC];
+        if constexpr (EC == 32) tc_ld_32x32b_x32(lanes + q * EC, v);
+        else tmem_load16(lanes + q * EC, v);
+        tc_wait_ld();
+        if (o.whole) {
+            // two lanes swap halves of two rows, so that a lane has two values of one row
+            __half* dst = a.out + static_cast<size_t>(o.row0 + c0 + (lane & 1)) * R + d0 + (lane & ~1);
+#pragma unroll
+            for (int i = 0; i < EC; i += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(inv_sum + c0 + i);
+                const float v0 = __uint_as_float(v[i]) * f.x, v1 = __uint_as_float(v[i + 1]) * f.y;
+                const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
+                const __half2 h = (lane & 1) ? __floats2half2_rn(other, v1) : __floats2half2_rn(v0, other);
+                if (i + (lane & 1) < n_here) *reinterpret_cast<__half2*>(dst + i * R) = h;
+            }
+        } else {
+            float* dst = a.part_o + (static_cast<size_t>(o.part) * NR + c0) * R + d0 + lane;
+#pragma unroll
+            for (int i = 0; i < EC; ++i)
+                if (i < n_here) dst[i * R] = __uint_as_float(v[i]);
+        }
+    }
 }
 
 template <int NP, int NR>
@@ -215,12 +277,12 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     // A wait of a whole warp, with one answer for all of its lanes.
     auto wait = [&](int b, uint32_t parity, int code) -> bool {
-        if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(b), parity, 1000000))) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
         const uint64_t t0 = globaltimer();
         const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_wait_limit_ns);
 #pragma unroll 1
         do {
-            if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(b), parity, 1000000))) return true;
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar(b), parity))) return true;
             if (__any_sync(0xffffffffu, *abort_flag)) return false;
         } while (__any_sync(0xffffffffu, globaltimer() - t0 < limit));
         *abort_flag = 1;
@@ -230,7 +292,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 
     if (warp == 0) {
         for (int i = lane; i < C::N_BARS; i += 32)
-            mbar_init(bar(i), (i >= C::B_P && i < C::B_P + 2) || i == C::B_FIX || i == C::B_MEET ? kSoftmaxWarps : 1);
+            mbar_init(bar(i), (i >= C::B_P && i < C::B_P + 2) || i == C::B_FIX || i == C::B_MEET || i == C::B_OUT ? 4 : 1);
         if (lane == 0) *abort_flag = 0;
         fence_barrier_init();
     }
@@ -246,7 +308,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         constexpr int kWarps = kThreads / 32;
         long long* sums = reinterpret_cast<long long*>(smem + C::OFF_SUMS);   // of the warps, then the run's start
         int* first = reinterpret_cast<int*>(sums + kWarps + 1);
-        static_assert(kWarps + 2 <= 10, "scratch");
+        static_assert(kWarps + 2 <= 14, "scratch");
         const int max_g = a.side > 1 ? 1 : a.n_rb;
         const long long items = static_cast<long long>(a.B) * max_g, per = (items + kThreads - 1) / kThreads;
         const long long f0 = min(items, tid * per), f1 = min(items, f0 + per);
@@ -261,7 +323,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 const int end = static_cast<int>(min(static_cast<long long>(groups_of<NR>(a, c)), g + left));
 #pragma unroll 1
                 for (int i = g; i < end; ++i)
-                    if (!fn(b, i, group_tiles<NR>(a, c, i) + kSegTiles)) return;
+                    if (!fn(b, i, group_tiles<NR>(a, c, i) + C::SEG)) return;
                 left -= max_g - g;
                 g = 0;
             }
@@ -288,9 +350,9 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (i < warp) before += sums[i];
             total += sums[i];
         }
-        // as many runs as CTAs, or fewer of a key tile at least (a run's weight is above kSegTiles)
+        // as many runs as CTAs, or fewer of a key tile at least (a run's weight is above C::SEG)
         const int rank = static_cast<int>(blockIdx.x) / a.side, most = static_cast<int>(gridDim.x) / a.side;
-        const int runs = total >= static_cast<long long>(most) * (kSegTiles + 1) ? most : max(1, static_cast<int>(total) / (kSegTiles + 1));
+        const int runs = total >= static_cast<long long>(most) * (C::SEG + 1) ? most : max(1, static_cast<int>(total) / (C::SEG + 1));
         const long long each = total < (1ll << 31) ? static_cast<uint32_t>(total) / static_cast<uint32_t>(runs) : total / runs;
         const int more = static_cast<int>(total - each * runs);   // the first ones have one more
         const long long t = each * rank + min(rank, more);
@@ -326,7 +388,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         uint32_t s = 0, phase = 1;                 // place, and the phase of its release (the first round waits for none)
         bool ok = true;
         Walk w = run;
-        for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
+        for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
             const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int hi = key_end(a, w.c, row0 + NR);
             // the page of box `lane` of tile j, or the sequence: read a tile before its copies
@@ -386,7 +448,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     mbar_wait_drain(bar(C::B_FULL + i % NHS), (i / NHS) & 1, a.err, kErrTimeoutLoad);
             }
         }
-    } else if (warp >= kSWarp) {
+    } else if (warp >= kSWarp && warp < kOutWarp) {
         // ------------------------------------------------------------ MMA issuers
         // (the whole warp runs the code; one lane issues)
         const uint32_t one = elect_one();
@@ -398,7 +460,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const uint64_t q_desc = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
             const uint64_t x_desc = smem_desc_sw128(sbase + C::OFF_RING, 16, 1024);
             const bool stall = stall_first_tile();
-            for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
+            for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
                 if (!(ok = wait(C::B_QFULL, n_seg & 1, kErrTimeoutLoad))) break;
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
                     // (the S of two tiles before has been read once its weights are written)
@@ -431,7 +493,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const uint64_t p_desc = smem_desc_sw128(sbase, 16, 1024);
             const int* flags = reinterpret_cast<const int*>(smem + C::OFF_FLAGS);
             uint32_t n_fix = 0;
-            for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w)) {
+            for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
+                if (n_seg > 0 && !(ok = wait(C::B_OUT, (n_seg - 1) & 1, kErrTimeoutSoftmax))) break;
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
                     if (!(ok = wait(C::B_P + (n_tile & 1), (n_tile >> 1) & 1, kErrTimeoutSoftmax))) break;
                     if (j > 0) {
@@ -462,6 +525,21 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         tc_commit_one(one, bar(done));
         if (lane == 0) mbar_wait_drain(bar(done), 0, a.err, kErrTimeoutMma);
         __syncwarp();
+    } else if (warp >= kOutWarp) {
+        // ------------------------------------------------------------ half of the rows' values out
+        uint32_t n_seg = 0;
+        bool ok = true;
+        Walk w = run;
+        for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
+            const Out to = out_of<NP, NR>(a, w, static_cast<uint32_t>(w.g * a.side + rb_in) * NR);
+            if (!(ok = wait(C::B_MEET, n_seg & 1, kErrTimeoutSoftmax))) break;
+            tc_fence_after();
+            write_rows<NP, NR>(a, to, tmem + C::COL_O, warp & 3, 1,
+                               reinterpret_cast<const float*>(smem + C::OFF_ROWS) + (2 + (n_seg & 1)) * NR);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_OUT));
+        }
     } else {
         // ------------------------------------------------------------ softmax, and the rows out
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -510,7 +588,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         if (tid == 0) a.meta[blockIdx.x * 4] = a.meta[blockIdx.x * 4 + 1] = 0;
         bool ok = true;
         Walk w = run;
-        for (bool on = walk_item<NR>(a, w); on && ok; on = walk_next<NR>(a, w), ++n_seg) {
+        for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
             const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int live = static_cast<int>(max(0ll, min(static_cast<long long>(NR), static_cast<long long>(w.c.n) * a.H - row0)));
             const int hi = key_end(a, w.c, row0 + NR);
@@ -648,12 +726,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // the rows' sums, out of the threads that have them (two segments' in turn: another warp may
             // still read the last one's)
             float* inv_sum = factors + (2 + (n_seg & 1)) * NR;
-            const bool whole = w.n == w.tiles;
-            const int part = static_cast<int>(blockIdx.x) * 2 + (w.off > 0 ? 0 : 1);
-            const long long out0 = static_cast<long long>(w.c.q_base) * a.H + row0;
-            const long long out_end = static_cast<long long>(a.total_q) * a.H;
-            // rows below this are written
-            const int n_out = out0 < 0 ? 0 : static_cast<int>(max(0ll, min(static_cast<long long>(live), out_end - out0)));
+            const Out to = out_of<NP, NR>(a, w, row0);
             if (has_rows) {
                 float s_a = l_a.x + l_a.y, s_b = l_b.x + l_b.y;
 #pragma unroll
@@ -666,63 +739,25 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const int row = first ? ra : rb;
                     const float s = first ? s_a : s_b, mx = first ? m_a : m_b;
                     inv_sum[row] = s == 0.f ? 0.f : 1.0f / s;   // a row without keys: zeros; NaN stays NaN
-                    if (row < n_out) {
-                        if (!whole) a.part_ml[static_cast<size_t>(part) * NR + row] = make_float2(mx, s);
+                    if (row < to.n) {
+                        if (!to.whole) a.part_ml[static_cast<size_t>(to.part) * NR + row] = make_float2(mx, s);
                         else if (a.lse)
-                            a.lse[out0 + row] = s == 0.f ? -INFINITY : (mx + __log2f(s)) * 0.6931471805599453f;
+                            a.lse[to.row0 + row] = s == 0.f ? -INFINITY : (mx + __log2f(s)) * 0.6931471805599453f;
                     }
                 }
             }
-            if (!(ok = meet()) || !(ok = wait(C::B_PV + ((n_tile - 1) & 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
+            if (!(ok = wait(C::B_PV + ((n_tile - 1) & 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma)) || !(ok = meet())) break;
             tc_fence_after();
-            constexpr int EC = NR < 32 ? 16 : 32;   // columns (rows of the block) at a time
-            uint32_t r[2][EC];
-            auto load = [&](int q, uint32_t (&to)[EC]) {
-                if constexpr (EC == 32) tc_ld_32x32b_x32(lanes + C::COL_O + q * EC, to);
-                else tmem_load16(lanes + C::COL_O + q * EC, to);
-            };
-            auto write = [&](int q, const uint32_t (&v)[EC]) {
-                const int c0 = (q * EC) % NR;       // the first of these rows
-                const int d0 = q * EC / NR * 128 + warp * 32, n_here = n_out - c0;
-                if (whole) {
-                    // two lanes swap halves of two rows, so that a lane has two values of one row
-                    __half* dst = a.out + static_cast<size_t>(out0 + c0 + (lane & 1)) * C::R + d0 + (lane & ~1);
-#pragma unroll
-                    for (int i = 0; i < EC; i += 2) {
-                        const float2 f = *reinterpret_cast<const float2*>(inv_sum + c0 + i);
-                        const float v0 = __uint_as_float(v[i]) * f.x, v1 = __uint_as_float(v[i + 1]) * f.y;
-                        const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
-                        const __half2 h = (lane & 1) ? __floats2half2_rn(other, v1) : __floats2half2_rn(v0, other);
-                        if (i + (lane & 1) < n_here) *reinterpret_cast<__half2*>(dst + i * C::R) = h;
-                    }
-                } else {
-                    float* dst = a.part_o + (static_cast<size_t>(part) * NR + c0) * C::R + d0 + lane;
-#pragma unroll
-                    for (int i = 0; i < EC; ++i)
-                        if (i < n_here) dst[i * C::R] = __uint_as_float(v[i]);
-                }
-            };
-            constexpr int NQ = NP * NR / EC;
-            static_assert(NQ % 2 == 0, "two at a time");
-            load(0, r[0]);
-#pragma unroll 1
-            for (int q = 0; q < NQ; q += 2) {
-                tc_wait_ld();
-                load(q + 1, r[1]);
-                write(q, r[0]);
-                tc_wait_ld();
-                if (q + 2 < NQ) load(q + 2, r[0]);
-                write(q + 1, r[1]);
-            }
+            write_rows<NP, NR>(a, to, tmem + C::COL_O, warp, 0, inv_sum);
             if (tid == 0) {
                 // what the join needs of this CTA: [0] the item its run goes on with ends in it; [1] the
                 // rows to write of the item that it leaves open (0: none), [2] the first of them
                 int* meta = a.meta + blockIdx.x * 4;
                 if (w.off > 0) {
                     meta[0] = w.off + w.n == w.tiles;
-                } else if (!whole) {
-                    meta[1] = n_out;
-                    meta[2] = static_cast<int>(out0);
+                } else if (!to.whole) {
+                    meta[1] = to.n;
+                    meta[2] = static_cast<int>(to.row0);
                 }
             }
             tc_fence_before();
@@ -737,23 +772,33 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 }
 
 // Joins the partial rows of the items that run over a CTA boundary: block (c, y) takes the
-// item that CTA c leaves open, and of its rows those of chunk y, a warp a row.
-constexpr int kJoinWarps = 8;
+// item that CTA c leaves open, and of its rows those of chunk y.  A warp takes a row, or of few
+// rows 128 values of one (join_width); all of its parts' loads are issued before the first is used.
+constexpr int kJoinWarps = 4;
+constexpr int join_width(int NP, int NR) { return NR == 64 ? NP : 1; }   // 128-value blocks a warp
+
+// (in the order they are written in: left to the compiler, each load is waited for before the next)
+__device__ __forceinline__ float4 load_in_order(const float* p) {
+    float4 v;
+    asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
 
 template <int NP, int NR>
 __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Args a, int n_ctas) {
-    constexpr int R = NP * 128;
+    constexpr int R = NP * 128, NW = join_width(NP, NR), AT = NW == 1 ? 8 : 4;   // parts at a time
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the next call's attention waits for this kernel)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // for the whole of latent_attend_kernel
-    const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int unit = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int row = unit * NW / NP, d0 = unit * NW % NP * 128 + lane * 4;
     const int4 meta = *reinterpret_cast<const int4*>(a.meta + blockIdx.x * 4);
     const size_t orow = static_cast<size_t>(static_cast<uint32_t>(meta.z)) + row;
     // The parts: the end of CTA c's run, whole runs of the same item, the beginning of the last.  A
     // lane each reads their statistics (32 at a time), then all read their values.
-    float2 o[NP * 2];
-    float sum = 0.f, mx = -INFINITY;
+    float2 o[2 * NW];
 #pragma unroll
-    for (int e = 0; e < NP * 2; ++e) o[e] = make_float2(0.f, 0.f);
+    for (int e = 0; e < 2 * NW; ++e) o[e] = make_float2(0.f, 0.f);
+    float sum = 0.f, mx = -INFINITY;
     for (int c0 = blockIdx.x, ended = 0; !ended && c0 < n_ctas; c0 += 32 * a.side) {
         const int i = c0 + lane * a.side;
         const bool first = i == static_cast<int>(blockIdx.x);
@@ -783,30 +828,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) latent_join_kernel(const Args
         for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(0xffffffffu, part, s);
         sum = fmaf(sum, old, part);
 #pragma unroll
-        for (int e = 0; e < NP * 2; ++e) o[e] = fmul2(o[e], make_float2(old, old));
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const int j = c0 + k * a.side;
-            const float g = __shfl_sync(0xffffffffu, f, k);
-            const float4* src = reinterpret_cast<const float4*>(
-                                    a.part_o + ((static_cast<size_t>(j) * 2 + (j == static_cast<int>(blockIdx.x))) * NR + row) * R) + lane;
+        for (int e = 0; e < 2 * NW; ++e) o[e] = fmul2(o[e], make_float2(old, old));
+        for (int k0 = 0; k0 < n; k0 += AT) {
+            float4 v[AT][NW];
 #pragma unroll
-            for (int e = 0; e < NP; ++e) {
-                const float4 v = src[e * 32];
-                o[2 * e] = ffma2(make_float2(v.x, v.y), make_float2(g, g), o[2 * e]);
-                o[2 * e + 1] = ffma2(make_float2(v.z, v.w), make_float2(g, g), o[2 * e + 1]);
+            for (int k = 0; k < AT; ++k) {
+                const int j = c0 + min(k0 + k, n - 1) * a.side;   // (past the last part: the last again, times 0)
+                const float* src = a.part_o + ((static_cast<size_t>(j) * 2 + (j == static_cast<int>(blockIdx.x))) * NR + row) * R + d0;
+#pragma unroll
+                for (int e = 0; e < NW; ++e)
+                    v[k][e] = load_in_order(src + e * 128);
+            }
+#pragma unroll
+            for (int k = 0; k < AT; ++k) {
+                const float g = __shfl_sync(0xffffffffu, k0 + k < n ? f : 0.f, (k0 + k) & 31);
+#pragma unroll
+                for (int e = 0; e < NW; ++e) {
+                    o[2 * e] = ffma2(make_float2(v[k][e].x, v[k][e].y), make_float2(g, g), o[2 * e]);
+                    o[2 * e + 1] = ffma2(make_float2(v[k][e].z, v[k][e].w), make_float2(g, g), o[2 * e + 1]);
+                }
             }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-    uint2* dst = reinterpret_cast<uint2*>(a.out + orow * R) + lane;
 #pragma unroll
-    for (int e = 0; e < NP; ++e) {
+    for (int e = 0; e < NW; ++e) {
         const __half2 h0 = __floats2half2_rn(o[2 * e].x * inv, o[2 * e].y * inv);
         const __half2 h1 = __floats2half2_rn(o[2 * e + 1].x * inv, o[2 * e + 1].y * inv);
-        dst[e * 32] = make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+        *reinterpret_cast<uint2*>(a.out + orow * R + d0 + e * 128) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     }
-    if (a.lse && lane == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
+    if (a.lse && d0 == 0) a.lse[orow] = sum == 0.f ? -INFINITY : (mx + __log2f(sum)) * 0.6931471805599453f;
 }
 
 // Rows of a block, blocks of the longest chunk, and the workspace: partial rows, their
@@ -891,15 +943,18 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     a.scale = L.scale;
     const int sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
     const int grid = sms / a.side * a.side;
-    const dim3 join(grid, NR / kJoinWarps);
+    // Short caches: items of few tiles are not cut, and nothing is to be joined (one token over 128
+    // keys 9.1 us, 6.9 without the second kernel)
+    a.whole = a.capacity <= kWholeTiles * BN;
+    const dim3 join(grid, NR * NP / join_width(NP, NR) / kJoinWarps);
     if (trace_enabled())
         trace("latent_attend_kernel<R=%d,rows=%d> grid=%d block=%d smem=%u tmem_cols=%u row_blocks=%d side=%d B=%d "
-              "total_q=%d H=%d box_rows=%d, then latent_join_kernel grid=(%u,%u)",
+              "total_q=%d H=%d box_rows=%d whole=%d, then latent_join_kernel grid=(%u,%u)",
               C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, box_rows,
-              join.x, join.y);
+              a.whole, a.whole ? 0 : join.x, a.whole ? 0 : join.y);
     // both are set up while the kernel before runs, and wait for its end themselves
     cudaError_t e = launch_dependent(kernel, dim3(grid), kThreads, C::SMEM_ALLOC, L.stream, tq, tx[0], tx[1], tx[2], a);
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !a.whole)
         e = launch_dependent(latent_join_kernel<NP, NR>, join, kJoinWarps * 32, 0, L.stream, a, grid);
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent attend launch failed: %s", cudaGetErrorString(e));
     return ATTN_OK;
