@@ -44,6 +44,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = 384;
 constexpr int kRegSoftmax = 208, kRegOther = 88;
 static_assert(2 * kRegSoftmax + kRegOther == 3 * 168, "register split");
+constexpr int kMaxRanked = 128;   // most (sequence, block) pairs that are ranked
 constexpr int RING = 8, K_CHUNKS = 3, V_CHUNKS = 2, CHUNKS = K_CHUNKS + V_CHUNKS;
 constexpr uint32_t kChunk = BN * 128;       // 64 values of 128 keys (or queries)
 constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * K_CHUNKS * kChunk, OFF_BAR = OFF_RING + RING * kChunk;
@@ -59,6 +60,8 @@ struct Args {
     float* lse;
     const int32_t *q_start, *kv_start;
     int total_q, total_kv, max_q, H, causal;
+    int B, blocks;   // sequences, blocks of 256 queries of the longest
+    int ranked;      // the grid's CTAs take (sequence, block) pairs longest first
     float scale;
     int* err;
 };
@@ -92,12 +95,42 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     auto bar = [&](int i) { return sbase + OFF_BAR + i * 8; };
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
-    // heads fastest, then blocks of 256 queries from the last (the longest when causal)
-    const int h = blockIdx.x, b = blockIdx.z;
+    // Heads fastest, then blocks of 256 queries: of few sequences all of them ranked by the work
+    // they are, the most first (8 chunks of 33 to 700 tokens over 739 to 3900: 103 us in the
+    // sequences' order), else sequence by sequence from the last block (the longest when causal).
+    int h = blockIdx.x, b = blockIdx.z, block = static_cast<int>(gridDim.y - 1 - blockIdx.y);
+    if (a.ranked) {
+        int* work = reinterpret_cast<int*>(smem + OFF_Q);   // before any copy
+        const int n_pairs = a.B * a.blocks, want = static_cast<int>(blockIdx.x) / a.H;
+        int mine = -1;                           // no queries: last
+        if (tid < n_pairs) {
+            const int bb = tid / a.blocks, first = tid % a.blocks * 2 * BM;
+            const int all = max(a.q_start[bb + 1] - a.q_start[bb], 0), keys = max(a.kv_start[bb + 1] - a.kv_start[bb], 0);
+            const int nq = min(all, a.max_q);
+            if (first < nq) {
+                const int end = min(first + 2 * BM, nq);
+                const int hi = a.causal ? max(min(keys, keys - all + end), 0) : keys;
+                mine = (hi / BN + 1) * (end - first > BM ? 4 : 3);   // (a key tile for one row tile: 3/4 of the time)
+            }
+            work[tid] = mine;
+        }
+        __syncthreads();
+        if (tid < n_pairs) {
+            int rank = 0;
+            for (int i = 0; i < n_pairs; ++i) rank += work[i] > mine || (work[i] == mine && i < tid);
+            if (rank == want) work[kMaxRanked] = tid;   // (ranks are a permutation: one writer)
+        }
+        __syncthreads();
+        const int pair = work[kMaxRanked];
+        b = pair / a.blocks;
+        block = pair % a.blocks;
+        h = static_cast<int>(blockIdx.x) % a.H;
+        __syncthreads();                         // (before Q is copied over it)
+    }
     const int q_base = a.q_start[b], k_base = a.kv_start[b];
     const int n_all = max(a.q_start[b + 1] - q_base, 0), L = max(a.kv_start[b + 1] - k_base, 0);
     const int n_q = min(n_all, a.max_q);
-    const int q0 = static_cast<int>(gridDim.y - 1 - blockIdx.y) * 2 * BM;
+    const int q0 = block * 2 * BM;
     if (q0 >= n_q) return;                       // a shorter sequence: no queries for this CTA
     const int pos0 = L - n_all;                  // position of query 0
     // key tiles of each row tile (at least one where it has rows)
@@ -112,12 +145,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
     // A wait of a whole warp, with one answer for all of its lanes.
     auto wait = [&](int i, uint32_t parity, int code) -> bool {
-        if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(i), parity, 1000000))) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
         const uint64_t t0 = globaltimer();
         const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_wait_limit_ns);
 #pragma unroll 1
         do {
-            if (__all_sync(0xffffffffu, mbar_try_wait_for(bar(i), parity, 1000000))) return true;
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity))) return true;
             if (__any_sync(0xffffffffu, *abort_flag)) return false;
         } while (__any_sync(0xffffffffu, globaltimer() - t0 < limit));
         *abort_flag = 1;
@@ -434,10 +467,13 @@ attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
     a.causal = L.causal;
     a.scale = L.scale;
     a.err = L.err_word;
-    const dim3 grid(L.H, (L.max_q - 1) / (2 * BM) + 1, L.B);
+    a.B = L.B;
+    a.blocks = (L.max_q - 1) / (2 * BM) + 1;
+    a.ranked = L.B > 1 && static_cast<long long>(L.B) * a.blocks <= kMaxRanked;
+    const dim3 grid = a.ranked ? dim3(L.B * a.blocks * L.H) : dim3(L.H, a.blocks, L.B);
     if (trace_enabled())
-        trace("latent_prefill_kernel grid=(%u,%u,%u) block=%d smem=%u tmem_cols=%u total_q=%d total_kv=%d H=%d causal=%d",
-              grid.x, grid.y, grid.z, kThreads, SMEM_ALLOC, TMEM_COLS, L.total_q, L.total_kv, L.H, L.causal);
+        trace("latent_prefill_kernel grid=(%u,%u,%u) block=%d smem=%u tmem_cols=%u total_q=%d total_kv=%d H=%d causal=%d ranked=%d",
+              grid.x, grid.y, grid.z, kThreads, SMEM_ALLOC, TMEM_COLS, L.total_q, L.total_kv, L.H, L.causal, a.ranked);
     latent_prefill_kernel<<<grid, kThreads, SMEM_ALLOC, L.stream>>>(tq, tk, tr, tv, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent prefill launch failed: %s", cudaGetErrorString(e));
