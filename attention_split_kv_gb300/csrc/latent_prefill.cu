@@ -38,7 +38,7 @@ constexpr int HD = 128, RD = 64;            // a head's values, the rotated part
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
 constexpr float kFastSumLimit = 256.0f;     // a row whose p sum to at most this has every p <= 2^8
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 8, kTmaWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 // 3 warpgroups: 8 softmax warps, then the TMA warp, the MMA warp and two that only make up the
 // third, which leaves registers to the others (launch: 384 x 168)
 constexpr int kThreads = 384;
@@ -48,8 +48,9 @@ constexpr int kMaxRanked = 128;   // most (sequence, block) pairs that are ranke
 constexpr int RING = 8, K_CHUNKS = 3, V_CHUNKS = 2, CHUNKS = K_CHUNKS + V_CHUNKS;
 constexpr uint32_t kChunk = BN * 128;       // 64 values of 128 keys (or queries)
 constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * K_CHUNKS * kChunk, OFF_BAR = OFF_RING + RING * kChunk;
-enum : int { B_Q, B_FULL = B_Q + 2, B_EMPTY = B_FULL + RING, B_S = B_EMPTY + RING, B_P = B_S + 2, B_DONE = B_P + 2,
-             B_TEARDOWN = B_DONE + 2, N_BARS };
+// barriers: of K tiles (even, odd), V tiles, their release; of each row tile: S, weights, the last PV done
+enum : int { B_Q, B_K = B_Q + 2, B_V = B_K + 2, B_KFREE = B_V + 2, B_VFREE = B_KFREE + 2, B_S = B_VFREE + 2, B_P = B_S + 2,
+             B_DONE = B_P + 2, B_TEARDOWN = B_DONE + 2, N_BARS };
 constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8, SMEM_ALLOC = OFF_MISC + 8 + 1024;
 constexpr uint32_t COL_O = 2 * BN, TMEM_COLS = 512;
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
@@ -163,7 +164,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == kSoftmaxWarps + 1) {
+    if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_holder), TMEM_COLS);
         tmem_relinquish();
     }
@@ -175,47 +176,47 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (warp >= kSoftmaxWarps) {
     // (setmaxnreg is executed by all four warps of a warpgroup)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
-    if (warp == kSoftmaxWarps) {
+    if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA
-        uint32_t issued = 0;
+        // (the whole warp runs the code; one lane issues)
+        const uint32_t one = elect_one();
+        int k_posted = 0, v_posted = 0;
         bool ok = true;
         const int n_q_tiles = n_tiles[1] > 0 ? 2 : 1;
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_r);
-            tma_prefetch_desc(&tm_v);
-            for (int t = 0; t < n_q_tiles; ++t) {
-                mbar_arrive_expect_tx(bar(B_Q + t), K_CHUNKS * kChunk);
-                for (int c = 0; c < K_CHUNKS; ++c)
-                    tma_load_3d(sbase + OFF_Q + (t * K_CHUNKS + c) * kChunk, &tm_q, bar(B_Q + t), c * 64, h,
+        for (int t = 0; t < n_q_tiles; ++t) {
+            mbar_arrive_expect_tx_one(one, bar(B_Q + t), K_CHUNKS * kChunk);
+            for (int c = 0; c < K_CHUNKS; ++c)
+                tma_load_3d_one(one, sbase + OFF_Q + (t * K_CHUNKS + c) * kChunk, &tm_q, bar(B_Q + t), c * 64, h,
                                 q_base + q0 + t * BM);
-            }
         }
-        for (int j = 0; j < n && ok; ++j) {
+        // K(j) takes the places of K(j - 2)'s last chunk and V(j - 2), V(j) of K(j - 1)'s first two.
+        for (int j = 0; j < n; ++j) {
             const int row = k_base + j * BN;
-            for (int c = 0; c < CHUNKS; ++c) {
-                const uint32_t s = issued % RING, round = issued / RING;
-                if (round > 0 && !(ok = wait(B_EMPTY + s, (round - 1) & 1, kErrTimeoutSlot))) break;
-                if (lane == 0) {
-                    const uint32_t dst = sbase + OFF_RING + s * kChunk;
-                    mbar_arrive_expect_tx(bar(B_FULL + s), kChunk);
-                    if (c < 2) tma_load_3d(dst, &tm_k, bar(B_FULL + s), c * 64, h, row);
-                    else if (c == 2) tma_load_2d(dst, &tm_r, bar(B_FULL + s), 0, row);
-                    else tma_load_3d(dst, &tm_v, bar(B_FULL + s), (c - K_CHUNKS) * 64, h, row);
-                }
-                __syncwarp();
-                ++issued;
-            }
+            if (j > 1 && !(ok = wait(B_VFREE + (j & 1), ((j >> 1) - 1) & 1, kErrTimeoutSlot))) break;
+            uint32_t s = j * CHUNKS % RING;
+            mbar_arrive_expect_tx_one(one, bar(B_K + (j & 1)), K_CHUNKS * kChunk);
+            for (int c = 0; c < 2; ++c, s = (s + 1) % RING)
+                tma_load_3d_one(one, sbase + OFF_RING + s * kChunk, &tm_k, bar(B_K + (j & 1)), c * 64, h, row);
+            tma_load_3d_one(one, sbase + OFF_RING + s * kChunk, &tm_r, bar(B_K + (j & 1)), 0, 0, row);
+            s = (s + 1) % RING;
+            ++k_posted;
+            if (j > 0 && !(ok = wait(B_KFREE + ((j - 1) & 1), ((j - 1) >> 1) & 1, kErrTimeoutSlot))) break;
+            mbar_arrive_expect_tx_one(one, bar(B_V + (j & 1)), V_CHUNKS * kChunk);
+            for (int c = 0; c < V_CHUNKS; ++c, s = (s + 1) % RING)
+                tma_load_3d_one(one, sbase + OFF_RING + s * kChunk, &tm_v, bar(B_V + (j & 1)), c * 64, h, row);
+            ++v_posted;
         }
         if (!ok || __any_sync(0xffffffffu, *abort_flag)) {
             // let copies already in flight land before the CTA's shared memory goes away
             if (lane == 0) {
                 for (int t = 0; t < n_q_tiles; ++t) mbar_wait_drain(bar(B_Q + t), 0, a.err, kErrTimeoutLoad);
-                for (uint32_t i = issued > RING ? issued - RING : 0; i < issued; ++i)
-                    mbar_wait_drain(bar(B_FULL + i % RING), (i / RING) & 1, a.err, kErrTimeoutLoad);
+                for (int j = max(k_posted - 2, 0); j < k_posted; ++j)
+                    mbar_wait_drain(bar(B_K + (j & 1)), (j >> 1) & 1, a.err, kErrTimeoutLoad);
+                for (int j = max(v_posted - 2, 0); j < v_posted; ++j)
+                    mbar_wait_drain(bar(B_V + (j & 1)), (j >> 1) & 1, a.err, kErrTimeoutLoad);
             }
         }
-    } else if (warp == kSoftmaxWarps + 1) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         // (the whole warp runs the code; one lane issues)
         const uint32_t one = elect_one();
@@ -224,17 +225,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const uint64_t x_desc = smem_desc_sw128(sbase + OFF_RING, 16, 1024);
         const bool stall = stall_first_tile();
         bool ok = true;
-        // chunk i is there (the first row tile to use it waits; the second finds it so)
-        auto chunk = [&](uint32_t i) { return wait(B_FULL + i % RING, (i / RING) & 1, kErrTimeoutLoad); };
         auto issue_s = [&](int t, int j) -> bool {
             if (j >= n_tiles[t]) return true;
             if (j == 0 && !wait(B_Q + t, 0, kErrTimeoutLoad)) return false;
+            if (t == 0 && !wait(B_K + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;   // (row tile 0 takes every key
+            tc_fence_after();                                                                   //  tile that 1 takes, but the last)
+            if (t == 1 && j >= n_tiles[0] && !wait(B_K + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;
+            uint32_t s = j * CHUNKS % RING;
 #pragma unroll
-            for (int c = 0; c < K_CHUNKS; ++c) {
-                const uint32_t i = j * CHUNKS + c;
-                if (!chunk(i)) return false;
-                tc_fence_after();
-                const uint64_t kd = desc_advance(x_desc, (i % RING) * kChunk);
+            for (int c = 0; c < K_CHUNKS; ++c, s = (s + 1) % RING) {
+                const uint64_t kd = desc_advance(x_desc, s * kChunk);
                 const uint64_t qd = desc_advance(q_desc, (t * K_CHUNKS + c) * kChunk);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -247,12 +247,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         auto issue_pv = [&](int t, int j) -> bool {
             if (j >= n_tiles[t]) return true;
             if (!wait(B_P + t, j & 1, kErrTimeoutSoftmax)) return false;
+            if ((t == 0 || j >= n_tiles[0]) && !wait(B_V + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;
+            tc_fence_after();
+            uint32_t s = (j * CHUNKS + K_CHUNKS) % RING;
 #pragma unroll
-            for (int c = 0; c < V_CHUNKS; ++c) {
-                const uint32_t i = j * CHUNKS + K_CHUNKS + c;
-                if (!chunk(i)) return false;
-                tc_fence_after();
-                const uint64_t vd = desc_advance(x_desc, (i % RING) * kChunk);
+            for (int c = 0; c < V_CHUNKS; ++c, s = (s + 1) % RING) {
+                const uint64_t vd = desc_advance(x_desc, s * kChunk);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)   // 16 keys: 8 columns of P, 16 lines of V
                     tc_mma_f16_ts_one(one, tmem + COL_O + t * HD + c * 64, tmem + t * BN + kk * 8,
@@ -261,17 +261,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             if (j == n_tiles[t] - 1) tc_commit_one(one, bar(B_DONE + t));
             return true;
         };
-        auto release = [&](uint32_t i, int count) {
-            for (int c = 0; c < count; ++c) tc_commit_one(one, bar(B_EMPTY + (i + c) % RING));
-        };
-        if ((ok = issue_s(0, 0) && issue_s(1, 0))) release(0, K_CHUNKS);
+        if ((ok = issue_s(0, 0) && issue_s(1, 0))) tc_commit_one(one, bar(B_KFREE));
         for (int j = 0; ok && j < n; ++j) {
-            if (!(ok = issue_pv(0, j) && issue_s(0, j + 1))) break;
-            if (!(ok = issue_pv(1, j))) break;
-            release(j * CHUNKS + K_CHUNKS, V_CHUNKS);
+            if (!(ok = issue_pv(0, j) && issue_s(0, j + 1) && issue_pv(1, j))) break;
+            tc_commit_one(one, bar(B_VFREE + (j & 1)));
             if (j + 1 < n) {
                 if (!(ok = issue_s(1, j + 1))) break;
-                release((j + 1) * CHUNKS, K_CHUNKS);
+                tc_commit_one(one, bar(B_KFREE + ((j + 1) & 1)));
             }
         }
         // all issued MMAs must retire before TMEM is released
@@ -373,13 +369,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                 // rows behind the sequence's keys are another's, or nothing: their values are zeroed,
                 // since a weight of 0 must not meet a NaN.  (Both row tiles do it, each before its PV.)
                 const int r0 = max(L - key0, 0), units = (BN - r0) * 8;   // 16 bytes each
+                if (!(ok = wait(B_V + (j & 1), (j >> 1) & 1, kErrTimeoutLoad))) break;
                 for (int c = 0; c < V_CHUNKS; ++c) {
-                    const uint32_t i = j * CHUNKS + K_CHUNKS + c;
-                    if (!(ok = wait(B_FULL + i % RING, (i / RING) & 1, kErrTimeoutLoad))) break;
-                    uint8_t* at = smem + OFF_RING + (i % RING) * kChunk + r0 * 128;
+                    uint8_t* at = smem + OFF_RING + (j * CHUNKS + K_CHUNKS + c) % RING * kChunk + r0 * 128;
                     for (int u = tid & 127; u < units; u += 128) *reinterpret_cast<uint4*>(at + u * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (!ok) break;
                 fence_proxy_async_smem();
             }
             tc_wait_st();
@@ -417,7 +411,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kSoftmaxWarps + 1) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
     }
@@ -439,13 +433,7 @@ attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
     if ((st = rows_map(&tq, L.q, HD + RD, L.H, L.total_q, HD + RD, L.q_stride)) != ATTN_OK) return st;
     if ((st = rows_map(&tk, L.k, HD, L.H, L.total_kv, L.k_head_stride, L.k_stride)) != ATTN_OK) return st;
     if ((st = rows_map(&tv, L.v, HD, L.H, L.total_kv, L.v_head_stride, L.v_stride)) != ATTN_OK) return st;
-    {
-        const uint64_t dims[2] = {(uint64_t)RD, (uint64_t)L.total_kv};
-        const uint64_t strides[1] = {(uint64_t)L.k_rope_stride * 2};
-        const uint32_t box[2] = {64u, (uint32_t)BN};
-        if ((st = encode_tmap_sw128(&tr, L.k_rope, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, dims, strides, box)) != ATTN_OK)
-            return st;
-    }
+    if ((st = rows_map(&tr, L.k_rope, RD, 1, L.total_kv, RD, L.k_rope_stride)) != ATTN_OK) return st;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
