@@ -178,6 +178,12 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     return p;
 }
 
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1,
                                                  int c2, uint64_t policy) {
     asm volatile(
@@ -314,14 +320,14 @@ __device__ __forceinline__ void tma_load_3d_one(uint32_t one, uint32_t dst, cons
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(one)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_4d_one(uint32_t one, uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1,
-                                                int c2, int c3) {
+__device__ __forceinline__ void tma_load_4d_hint_one(uint32_t one, uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                                     int c1, int c2, int c3, uint64_t policy) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
         "setp.ne.b32 e, %7, 0;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(one)
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %8;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(one), "l"(policy)
         : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_one(uint32_t one, uint32_t bar, uint32_t bytes) {
