@@ -644,7 +644,7 @@ def _rows(what, x, width, like, dtype=None):
     _need(x.device == like.device, "%s must be on the cache's device", what)
     head = 0
     if x.dim() == 3:
-        head = x.stride(1) if x.shape[1] > 1 else max(width, x.stride(1))
+        head = x.stride(1) if x.shape[1] > 1 else width   # (one head's stride is not used)
     least = width if x.dim() == 2 else (x.shape[1] - 1) * head + width
     if x.shape[0] > 1:
         return x.stride(0), head

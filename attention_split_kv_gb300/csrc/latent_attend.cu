@@ -18,9 +18,9 @@
 // maximum and sum stay there; O is rescaled lazily (m within 2^8 of the row's maximum), a
 // column a row, by all softmax warps.
 //
-// The S of a tile is made while the one before is in the softmax, and tiles lie in a ring of
-// 128-value parts that holds two or three of them: a tile stays until its second product is
-// done, so with tiles of 128 keys the ring held one and the copies stood still meanwhile.
+// The S of a tile is made while the one before is in the softmax.  Tiles lie in a ring of halves
+// that holds two or two and a half of them: a tile stays until its second product is done, so
+// with tiles of 128 keys the ring held one and the copies stood still meanwhile.
 //
 // Persistent CTAs: the key tiles of all (sequence, row block) items, in that order, are cut
 // into equal runs, one a CTA; rows of items cut by a run's end go to the workspace and are
@@ -31,6 +31,15 @@
 // and one that issues the others: each waits for its own operands only (one warp for both,
 // polling what is ready: 150 cycles a poll, 4500 a tile whatever its rows).  A segment's rows are
 // written by the softmax warps and 4 that do only that.
+//
+// What bounds it.  Few heads: memory.  One token of 32 sequences of 512 to 8192 (137 thousand
+// tokens of 576 values, 158 MB), 16 heads: 35.4 us with the join, 4.5 TB/s (23.3 us at a copy's
+// rate); of the rest about 4 us go by before the first tile is there, 4 in the join, and the CTAs
+// end 3 apart.  64-row blocks: the tensor cores, whose M = 64 products run at half rate: a tile
+// takes 36 MMAs of 37 cycles and 16 of 47, 2080 in all, and comes by every 2600 to 3000, since
+// with 64 rows' Q the ring holds two tiles and a tile's chain (copy, S, softmax, PV) is 6000
+// long.  128 heads: 61.4 us, 620 TFLOP/s; 1 to 4 drafts of 32 heads of 16 x 32768 tokens: 140 us
+// (89 at a copy's rate), tensor pipe 54%, DRAM 61%.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -44,7 +53,7 @@ namespace {
 constexpr int BN = 64;                      // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
-constexpr float kFastSumLimit = 256.0f;
+constexpr float kFastSumLimit = 256.0f;     // weights that sum to at most this are at most 2^8
 constexpr int kMaxCtas = 152;               // one CTA an SM
 constexpr int kWholeTiles = 4;              // items of at most this many tiles are not cut
 constexpr int kSoftmaxWarps = 4;
@@ -62,7 +71,9 @@ __host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_
 template <int NP, int NR>
 struct Cfg {
     static constexpr int R = NP * 128, W = R + 64, NCH = 2 * NP + 1;
-    static constexpr int SEG = NR == 64 ? 4 : 2;           // a segment's fixed cost, in key tiles
+    // a segment's fixed cost, in key tiles (128 heads: 69.0 us with 1, 68.0 with 2, 65.2 with 4, 67.0
+    // with 6; 16 heads: 40.7, 40.6 and 40.4 with 1, 2 and 4)
+    static constexpr int SEG = NR == 64 ? 4 : 2;
     static constexpr uint32_t Q_CHUNK = NR * 128, Q_BYTES = NCH * Q_CHUNK;
     // The ring's places hold half a tile each: NP chunks of 64 values, the second half's with the
     // rotated part behind them.  An even number is packed as tiles.
@@ -93,11 +104,11 @@ struct Cfg {
         B_FULL, B_FREE = B_FULL + NHS,   // of the ring's places
         B_S = B_FREE + NHS,
         B_P = B_S + 2,     // weights are there (and flags, factors), of even and odd tiles
-        B_PV = B_P + 2,            // a tile's second product is done
+        B_PV = B_P + 2,    // a tile's second product is done
         B_FIX = B_PV + 2,  // O is rescaled
         B_MEET,            // the softmax warps have a segment's sums, and its products are done
         B_OUT,             // the other four warps have read its O
-        B_TEARDOWN,                    // of both issuers
+        B_TEARDOWN,        // of both issuers
         N_BARS = B_TEARDOWN + 2
     };
     static constexpr uint32_t OFF_BAR = OFF_SUMS + 14 * 8;
@@ -782,7 +793,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 // item that CTA c leaves open, and of its rows those of chunk y.  A warp takes a row, or of few
 // rows 128 values of one (join_width); all of its parts' loads are issued before the first is used.
 constexpr int kJoinWarps = 4;
-constexpr int join_width(int NP, int NR) { return NR == 64 ? NP : 1; }   // 128-value blocks a warp
+// 128-value blocks a warp (16 rows: 40.5 us with one, 42.5 with four; 64 rows: 70.0 and 66.0)
+constexpr int join_width(int NP, int NR) { return NR == 64 ? NP : 1; }
 
 // (in the order they are written in: left to the compiler, each load is waited for before the next)
 __device__ __forceinline__ float4 load_in_order(const float* p) {

@@ -54,6 +54,10 @@ struct Raw8<__half> {
 // gridDim.y).  A warp's turn is the latent vector (a lane R/32 values of it, the norm a sum
 // over the warp), or four rotated parts of 64 values (8 lanes each: the key's first, then the
 // query heads'); a lane has both values of each pair it turns.
+//
+// Bound by latency (launch, and each warp's chain sequence, length, page, slot, table row): 2853
+// tokens of 8 ragged chunks, 32 heads, f16: 6.8 us, 4.5 TB/s; 4096 f32 tokens of 16 heads 8.2 us,
+// 4.9 TB/s; one token 2.0 us.
 template <int R, typename T>
 __global__ void __launch_bounds__(256) latent_append_kernel(const LatentAppendArgs a) {
     constexpr int NC = R / 256;      // 8-value pieces of the latent vector a lane
@@ -172,7 +176,9 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const LatentAppendAr
 
 // ------------------------------------------------------------------ read back
 // A CTA takes `per` rows in a row: a lane each finds their places (a binary search over the
-// sequences), then all threads copy 16-byte pieces, several at a time before their stores.
+// sequences), then all threads copy 16-byte pieces, several at a time before their stores.  Bound
+// by memory: 16 x 32768 tokens of 576 values to f16 178.6 us, 6.8 TB/s, what a copy takes; 37 tokens
+// 2.5 us.  Few rows (less than 8 CTAs an SM of 32) are spread, 4 a CTA.
 constexpr int kReadThreads = 256;
 constexpr int kReadMost = 32;    // rows of a CTA
 constexpr int kReadPieces = 4;   // pieces of a thread at a time
@@ -243,11 +249,14 @@ void read_types(const LatentReadLaunch& L, int grid, int per) {
 
 attn_status launch_latent_append(const LatentAppendLaunch& L) {
     const LatentAppendArgs& a = L.args;
-    // A call of many tokens gives each a CTA of warps with 8 turns; of few tokens (fewer than two
-    // an SM) CTAs of at most 8 warps, a turn each, several a token.
-    const int turns = 1 + (a.H + 1 + 3) / 4;
+    // A call of many tokens gives each a CTA of warps with up to 16 turns, or 4 of f32 (whose loads
+    // are twice as many): 2853 f16 tokens of 10 turns take 9.2, 8.2, 7.6 and 6.8 us with up to 2, 4,
+    // 8 and 16 turns a warp, 4096 f32 tokens of 6 turns 9.2, 8.2 and 8.8 with 2, 4 and 8 (several
+    // tokens a CTA: no faster).  Of few tokens (fewer than two an SM) CTAs of at most 8 warps, a turn
+    // each, several a token.
+    const int turns = 1 + (a.H + 1 + 3) / 4, each = L.in_f32 ? 4 : 16;
     const bool many = a.total_q >= 2 * sm_count();
-    const int most = many ? (turns + 7) / 8 : turns, warps = most < 8 ? most : 8;
+    const int most = many ? (turns + each - 1) / each : turns, warps = most < 8 ? most : 8;
     const int parts = many ? 1 : (turns + warps - 1) / warps;
     const dim3 grid(a.total_q, parts < 65535 ? parts : 65535);   // (gridDim.y; the rest in turn)
     if (trace_enabled())

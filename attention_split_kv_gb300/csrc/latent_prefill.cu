@@ -22,6 +22,13 @@
 // ring of 16 KB chunks (64 values of 128 keys) in the order of their first use, which is also
 // the order in which they are released: K(j) after S1(j), V(j) after PV1(j).
 //
+// What bounds it: a row tile's chain.  From S to the next S of the same row tile (430 cycles until
+// the softmax has it, 230 to load it, 1550 for its weights, 180 until PV is issued, 540 and 680 of
+// products) is 3600, for 2560 of products of both; 8192 tokens of 16 heads take 218 us, 1577
+// TFLOP/s (83% of what a library's large product reaches here), tensor pipe 68%.  Rows shared by
+// two threads, 16 softmax warps, made it 243; a barrier a chunk instead of a tile (12 waits and 7
+// commits a turn, not 4 and 4) 231; waits with a suspend-time hint 226.
+//
 // Roles (12 warps): 8 softmax warps (row tile w / 4), a TMA warp, an MMA warp, 2 idle.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -228,9 +235,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         auto issue_s = [&](int t, int j) -> bool {
             if (j >= n_tiles[t]) return true;
             if (j == 0 && !wait(B_Q + t, 0, kErrTimeoutLoad)) return false;
-            if (t == 0 && !wait(B_K + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;   // (row tile 0 takes every key
-            tc_fence_after();                                                                   //  tile that 1 takes, but the last)
-            if (t == 1 && j >= n_tiles[0] && !wait(B_K + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;
+            // (what row tile 0 has taken is there for 1 too)
+            if ((t == 0 || j >= n_tiles[0]) && !wait(B_K + (j & 1), (j >> 1) & 1, kErrTimeoutLoad)) return false;
+            tc_fence_after();
             uint32_t s = j * CHUNKS % RING;
 #pragma unroll
             for (int c = 0; c < K_CHUNKS; ++c, s = (s + 1) % RING) {

@@ -212,3 +212,37 @@ def test_offsets_past_32_bits():
     ref, _, bound = attend_reference(case, q, [1, 2])
     case.cache, case.page_table = pool, far
     assert_within(attn.latent_attend(case, q, start, 2), ref, bound)
+
+
+TRACE = r"""
+import torch
+import attention_split_kv_gb300 as attn
+import seeded_inputs as si
+from tests.latent_util import starts
+attn.load()
+for kv, cap, H in ((100, 256, 16), (100, 257, 16), (300, 0, 40), (300, 0, 128)):
+    case = si.make_latent_case([kv], 512, 1, cap=cap, device="cuda")
+    attn.latent_attend(case, si.f16_normal((1, H, 576), 2, "cuda"), starts([1], "cuda"), 1)
+q = si.f16_normal((300, 4, 192), 3, "cuda")
+st = starts([200, 100], "cuda")
+attn.latent_prefill(q, q[..., :128], q[..., 64:], q[:, 0, :64], st, st, 200, 0.07)
+torch.cuda.synchronize()
+assert attn.attn_device_status() == attn.ATTN_OK
+"""
+
+
+def test_trace_names_the_forms():
+    # short caches are not cut (and not joined); rows choose the block; several blocks go side by side
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", TRACE], cwd=root, env=dict(os.environ, ATTN_TRACE="1"), capture_output=True,
+                       text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+    lines = [x for x in r.stderr.splitlines() if x.startswith("[libattn]")]
+    assert len(lines) == 5
+    for line, part in zip(lines, ("rows=16> ", "rows=16> ", "rows=64> ", "rows=64> ", "latent_prefill_kernel ")):
+        assert part in line, line
+    assert "whole=1" in lines[0] and all("whole=0" in x for x in lines[1:4])
+    assert "side=1" in lines[2] and "side=2" in lines[3] and "ranked=1" in lines[4]
