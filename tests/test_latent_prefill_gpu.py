@@ -140,3 +140,30 @@ def test_the_same_call_gives_the_same_bits_and_can_be_captured():
 def test_a_long_prompt():
     q, k, v, r = _inputs([3000], [3000], 2)
     _check(q, k, v, r, [3000], [3000])
+
+
+@pytest.mark.parametrize("n", [1, 5, 127, 128])
+@pytest.mark.parametrize("L", [128, 129, 256, 257, 384, 500, 1100, 2000])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_queries_over_many_keys(n, L, causal):
+    # blocks of one row tile take even and odd key tiles as two streams
+    _check(*_inputs([n, 3], [L, 200], 2, tail=1), [n, 3], [L, 200], causal=causal)
+
+
+def test_a_stream_without_a_key():
+    # 100 queries, the last of 130 keys: in the second key tile only the last two keep any; and with
+    # fewer keys than queries
+    _check(*_inputs([100, 128], [130, 140], 2), [100, 128], [130, 140])
+    _check(*_inputs([128, 100], [129, 40], 2), [128, 100], [129, 40])
+
+
+@pytest.mark.parametrize("n", [300, 100])
+def test_a_nan_query_stays_in_its_row(n):
+    q, k, v, r = _inputs([n], [700], 3)
+    ref, _, bound = prefill_reference(q, k, v, r, [n], [700], SCALE)
+    q[7, 1, 5], q[40, 2, 150] = math.nan, math.inf
+    out = attn.latent_prefill(q, k, v, r, starts([n], "cuda"), starts([700], "cuda"), n, SCALE)
+    assert bool(out[7, 1].isnan().all()) and bool(out[40, 2].isnan().all())
+    good = torch.ones(n, 3, dtype=torch.bool)
+    good[7, 1] = good[40, 2] = False
+    assert_within(out[good], ref[good], bound[good])
