@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libattn.so")
 SOURCES = ["api.cu", "cache.cu", "decode.cu", "decode_direct.cu", "prefill.cu", "prefill_int8.cu",
-           "latent_cache.cu", "latent_attend.cu", "latent_prefill.cu"]
+           "latent_cache.cu", "latent_attend.cu", "latent_pair.cu", "latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

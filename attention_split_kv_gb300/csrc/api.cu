@@ -1049,6 +1049,7 @@ attn_status attn_testing_set_waits(unsigned long long wait_limit_ns, int stall_f
     if (st == ATTN_OK) st = set_test_controls_decode(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_prefill8(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_latent_attend(limit, stall_first_tile);
+    if (st == ATTN_OK) st = set_test_controls_latent_pair(limit, stall_first_tile);
     if (st == ATTN_OK) st = set_test_controls_latent_prefill(limit, stall_first_tile);
     return st;
 }

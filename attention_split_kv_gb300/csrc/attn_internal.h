@@ -256,6 +256,7 @@ struct LatentAttendLaunch {
 };
 size_t latent_attend_workspace(int max_q, int H, int R);
 attn_status launch_latent_attend(const LatentAttendLaunch& L);
+attn_status launch_latent_pair(const LatentAttendLaunch& L);   // (of more than 64 rows a chunk)
 
 struct LatentPrefillLaunch {
     const void *q, *k, *v, *k_rope;
@@ -276,6 +277,7 @@ attn_status set_test_controls_prefill(unsigned long long wait_limit_ns, int stal
 attn_status set_test_controls_decode(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_prefill8(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_latent_attend(unsigned long long wait_limit_ns, int stall);
+attn_status set_test_controls_latent_pair(unsigned long long wait_limit_ns, int stall);
 attn_status set_test_controls_latent_prefill(unsigned long long wait_limit_ns, int stall);
 
 constexpr int kDecodeMaxBatch = 4096;
