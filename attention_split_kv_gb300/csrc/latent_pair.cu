@@ -2,7 +2,7 @@
 // (a cluster) takes blocks of 128 rows, each CTA one half of a cached row's values.
 //
 //   S_r = Q_r X_r^T    128 rows x 64 keys, over CTA r's half of the dims    (tcgen05.mma, M = 128)
-//   S = S_0 + S_1      for rows 64 r .. + 63: the peer's part comes through shared memory
+//   S = S_0 + S_1      for 64 of the rows: the peer's part comes through shared memory
 //   P = 2^(S scale log2e - m)   f16, to both CTAs' shared memory
 //   O_r += P C_r       128 rows x R / 2 values      (C_r: the half tile as it lies, MN-major)
 //
@@ -11,17 +11,17 @@
 // beside Q, whose latent part (R / 2 values of 128 rows) lies in TMEM: 512 columns are O (R / 2), two S
 // (128) and Q (R / 4).  The rotated part (64 values) of a tile is CTA 0's or CTA 1's in turn.
 //
-// A row belongs to one CTA (0: rows 0 .. 63, 1: the others) and to one of four of its warps, the owners,
-// 16 rows each; two warps send the other rows' part of S to the peer, and two take what concerns the
-// other rows' O: they wait for their P and rescale their O if their maximum moved.
+// A row belongs to one CTA: 16 of each 32 rows (of a warp's lanes of TMEM) to CTA 0, the others to CTA
+// 1, so that the four warps that own rows are on all four schedulers (on two: 2260 cycles a tile).
+// Four more send the other rows' part of S to the peer, and four take what concerns the other rows'
+// O: they wait for their P and rescale their O if their maximum moved.
 //
-// Ordering between the CTAs: an owner's P(i) follows the peer's part of S(i), which is sent after the
-// peer's second product of tile i - 2; so the peer's buffers of tile i - 2 are free by then, without a
-// message of their own.  Neither CTA ends before the other's last store to it: they meet at the end.
+// Ordering between the CTAs: tile i's part of S is sent once the peer's weights of tile i - 2 are here
+// (it has read that tile's part); P(i) is written once both CTAs' second products of tile i - 2 are done
+// (each commits to both).  Neither CTA ends before the other's last store to it: they meet at the end.
 //
-// Roles (11 warps): 2 owners and 2 senders, a TMA warp, a warp that issues S and one that issues the
-// others, 4 that load Q into TMEM, of which 2 are owners as well and 2 wait for the peer's P.  Those of
-// the same warp number mod 4 share 32 rows' lanes of TMEM, and a segment's rows are written by both.
+// Roles (15 warps): 4 owners, 4 senders, 4 that wait for the peer's P (and load Q into TMEM), a TMA warp,
+// a warp that issues S and one that issues the others.  The first 12 write a segment's rows.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,9 +32,9 @@ namespace attn {
 namespace {
 
 constexpr int NR = 128;                     // rows of a block
-constexpr int SEG = 4;                      // a segment's fixed cost, in key tiles
-constexpr int kTmaWarp = 4, kSWarp = 5, kPvWarp = 6, kAuxWarp = 7;   // and 4 owners and senders before them
-constexpr int kThreads = (kAuxWarp + 4) * 32;
+constexpr int SEG = 8;                      // a segment's fixed cost, in key tiles
+constexpr int kTmaWarp = 12, kSWarp = 13, kPvWarp = 14;   // and 4 each of owners, senders and others before them
+constexpr int kThreads = (kPvWarp + 1) * 32;
 constexpr uint32_t kRowsChunk = NR * 128;   // bytes of 64 values of a block's rows
 
 // NP: blocks of 128 latent values, NP / 2 a CTA.
@@ -59,9 +59,9 @@ struct Cfg {
         B_S = B_FREE + NS,               // S is there, of even and odd tiles
         B_READ = B_S + 2,                // S has been read
         B_X = B_READ + 2,                // the peer's part is there: [2][4 owners]
-        B_THEIRS = B_X + 8,              // the peer's weights are there: [2][rows 0 .. 31 or 32 .. 63]
-        B_P = B_THEIRS + 4,              // all weights are there, and O is rescaled
-        B_PV = B_P + 2,                  // a tile's second product is done
+        B_THEIRS = B_X + 8,              // the peer's weights are there: [2][4 owners]
+        B_P = B_THEIRS + 8,              // all weights are there, and O is rescaled
+        B_PV = B_P + 2,                  // a tile's second product is done, in both CTAs
         B_SUM = B_PV + 2,                // sums are there, and the products are done, of even and odd segments
         B_OUT = B_SUM + 2,               // a segment's O has been read
         B_TEARDOWN,                      // of both issuers
@@ -98,6 +98,16 @@ __device__ __forceinline__ void peer_store_async(uint32_t addr, uint32_t bar, fl
                  "r"(__float_as_uint(x))
                  : "memory");
 }
+// (commits to the barrier at this place in both CTAs)
+__device__ __forceinline__ void commit_both(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar),
+        "r"(one)
+        : "memory");
+}
 __device__ __forceinline__ void peer_copy(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "r"(src), "r"(bytes), "r"(bar)
@@ -118,13 +128,13 @@ __device__ __forceinline__ bool try_wait_peer(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// This thread's row of O, every second 32 values from `first` on.
+// This thread's row of O, every third 32 values from `first` on.
 template <int NP>
 __device__ __forceinline__ void write_row(const Args& a, const Out& o, uint32_t o_tmem, int row, int d0, int first, float inv) {
     constexpr int R = NP * 128;
     const bool live = row < o.n;
 #pragma unroll 1
-    for (int q = first; q < NP * 2; q += 2) {
+    for (int q = first; q < NP * 2; q += 3) {
         uint32_t v[32];
         tc_ld_32x32b_x32(o_tmem + q * 32, v);
         tc_wait_ld();
@@ -147,24 +157,9 @@ __device__ __forceinline__ void write_row(const Args& a, const Out& o, uint32_t 
     }
 }
 
-// A warp's 32 lanes of O, times a factor a row.
+// 16 lanes of O times a factor a row (a thread has values of rows lane / 4 and lane / 4 + 8).
 template <int NP>
-__device__ __forceinline__ void rescale(uint32_t o_tmem, float f) {
-#pragma unroll 1
-    for (int q = 0; q < NP * 2; ++q) {
-        uint32_t v[32];
-        tc_ld_32x32b_x32(o_tmem + q * 32, v);
-        tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-        tc_st_32x32b_x32(o_tmem + q * 32, v);
-    }
-    tc_wait_st();
-}
-
-// An owner's 16 lanes of O (a thread has values of rows lane / 4 and lane / 4 + 8).
-template <int NP>
-__device__ __forceinline__ void rescale_own(uint32_t o_tmem, float f_a, float f_b) {
+__device__ __forceinline__ void rescale(uint32_t o_tmem, float f_a, float f_b) {
 #pragma unroll 1
     for (int q = 0; q < NP * 2; ++q) {
         uint32_t v[16];
@@ -226,10 +221,11 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
         for (int i = lane; i < C::N_BARS; i += 32) {
             int n = 1;
             if (i == C::B_Q) n = 4;                                     // warps
-            if (i >= C::B_READ && i < C::B_READ + 2) n = 6;             // owners, senders
-            if (i >= C::B_P && i < C::B_P + 2) n = 6;                   // owners, and two for the peer's rows
+            if (i >= C::B_READ && i < C::B_READ + 2) n = 8;             // owners, senders
+            if (i >= C::B_P && i < C::B_P + 2) n = 8;                   // owners, and those of the peer's rows
             if (i >= C::B_SUM && i < C::B_SUM + 2) n = 4;               // owners (and the peer's bytes)
-            if (i == C::B_OUT) n = 8;
+            if (i >= C::B_PV && i < C::B_PV + 2) n = 2;                 // CTAs
+            if (i == C::B_OUT) n = 12;
             mbar_init(bar(i), n);
         }
         if (lane == 0) *abort_flag = 0;
@@ -383,7 +379,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                         tc_mma_f16_ss_one(one, tmem + C::COL_O, desc_advance(pd, kk * 32), desc_advance(cd, kk * 2048), id_o,
                                           (j | kk) != 0);
                     tc_commit_one(one, bar(C::B_FREE + s));
-                    tc_commit_one(one, bar(C::B_PV + (n_tile & 1)));
+                    commit_both(one, bar(C::B_PV + (n_tile & 1)));
                     s = s + 1 == NS ? 0 : s + 1;
                 }
             }
@@ -394,16 +390,15 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
         if (lane == 0) mbar_wait_drain(bar(done), 0, a.err, kErrTimeoutMma);
         __syncwarp();
     } else {
-        const bool aux = warp >= kAuxWarp;
-        const int quarter = warp & 3;                              // its lanes of TMEM
-        const int row = quarter * 32 + lane, half = quarter & 1;   // half: of a CTA's 64 rows
-        const bool mine = static_cast<uint32_t>(quarter >> 1) == rank;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int group = warp >> 2, unit = warp & 3;   // unit: its 32 lanes of TMEM
+        const int row = unit * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(unit * 32) << 16);
+        const uint32_t own = lanes + (rank * 16 << 16), others = lanes + ((rank ^ 1) * 16 << 16);   // 16 lanes each
         float* sums = reinterpret_cast<float*>(smem + C::OFF_SUMS);
         uint32_t n_tile = 0, n_seg = 0;
         bool ok = true;
         Walk w = run;
-        if (!aux && rank == 0 && tid == 0) a.meta[pair * 4] = a.meta[pair * 4 + 1] = 0;
+        if (rank == 0 && tid == 0) a.meta[pair * 4] = a.meta[pair * 4 + 1] = 0;
         // Q's latent part into TMEM, a row a thread
         auto load_q = [&](const Walk& v) {
             const long long at = static_cast<long long>(v.c.q_base) * a.H + row0_of(v) + row;
@@ -431,20 +426,19 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
         };
         const float scale_log2 = a.scale * kLog2e;
         bool on = walk_first<NR, SEG>(a, w);
-        if (aux && on) load_q(w);
+        if (group == 2 && on) load_q(w);
         for (; on && ok; ++n_seg) {
             const uint32_t row0 = row0_of(w);
             const int hi = key_end(a, w.c, row0 + NR);
             const Out to = out_of<NR>(a, w, row0, pair);
-            if (mine) {
+            if (group == 0) {
                 // ---------------------------------------------------- owners: 16 rows' weights
-                const int sub = aux ? 16 : 0, unit = half * 2 + aux;
-                const int ra = quarter * 32 + sub + (lane >> 2), rb = ra + 8;   // this thread's rows of the block
-                const uint32_t own = lanes + (static_cast<uint32_t>(sub) << 16);
+                const int first_row = unit * 32 + rank * 16;
+                const int ra = first_row + (lane >> 2), rb = ra + 8;   // this thread's rows of the block
                 const long long live = static_cast<long long>(w.c.n) * a.H - row0;
                 // rows keep the keys below lim; no row of the warp drops a key below all_keep
                 const int lim_a = key_end(a, w.c, row0 + ra + 1), lim_b = key_end(a, w.c, row0 + rb + 1);
-                const int all_keep = key_end(a, w.c, row0 + quarter * 32 + sub + 1);
+                const int all_keep = key_end(a, w.c, row0 + first_row + 1);
                 // maxima in log2 units; +inf for what is not a row of the block: no weight
                 float m_a = ra < live ? -INFINITY : INFINITY, m_b = rb < live ? -INFINITY : INFINITY;
                 float2 l_a = make_float2(0.f, 0.f), l_b = make_float2(0.f, 0.f);
@@ -480,7 +474,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                             x[4 * i + 3] = v.y;
                         }
                     }
-                    // (this CTA's P of two tiles before has been read)
+                    // (P of two tiles before has been read, here and at the peer)
                     if (n_tile > 1 && !(ok = wait(C::B_PV + par, ((n_tile >> 1) - 1) & 1, kErrTimeoutMma))) break;
                     const int key0 = (w.off + j) * BN;
                     const bool masked = key0 + BN > all_keep;
@@ -560,10 +554,10 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     l_b = fadd2(l_b, s_b);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    const uint32_t theirs = of_peer(bar(C::B_THEIRS + par * 2 + half), rank);
+                    const uint32_t theirs = of_peer(bar(C::B_THEIRS + par * 4 + unit), rank);
                     if (lane == 0) {
                         // 16 lines of P to the peer
-                        const uint32_t at = sbase + C::OFF_P + par * kRowsChunk + (quarter * 32 + sub) * 128;
+                        const uint32_t at = sbase + C::OFF_P + par * kRowsChunk + first_row * 128;
                         peer_copy(of_peer(at, rank), at, 16 * 128, theirs);
                     }
                     if ((lane & 3) == 0) {
@@ -574,12 +568,14 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     if (moved) {
                         if (!(ok = wait(C::B_PV + (par ^ 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
                         tc_fence_after();
-                        rescale_own<NP>(own + C::COL_O, f_a, f_b);
+                        rescale<NP>(own + C::COL_O, f_a, f_b);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_P + par));
                 }
+                // (the products of the last two tiles: no commit of the peer's is on its way at the end)
+                if (ok && n_tile > 1) ok = wait(C::B_PV + (n_tile & 1), ((n_tile >> 1) - 1) & 1, kErrTimeoutMma);
                 if (!ok || !(ok = wait(C::B_PV + ((n_tile - 1) & 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
                 float s_a = l_a.x + l_a.y, s_b = l_b.x + l_b.y;
 #pragma unroll
@@ -605,30 +601,26 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     if (unit == 0) mbar_arrive_expect_tx(bar(C::B_SUM + (n_seg & 1)), 64 * 4);
                     else mbar_arrive(bar(C::B_SUM + (n_seg & 1)));
                 }
-            } else if (!aux) {
+            } else if (group == 1) {
                 // ---------------------------------------------------- senders: the peer's rows of S
-                const uint32_t to_x = of_peer(sbase + C::OFF_X + half * (C::X_BYTES / 2) + lane * 16, rank);
-                const uint32_t to_b = of_peer(bar(C::B_X + half * 2), rank);
+                const uint32_t to_x = of_peer(sbase + C::OFF_X + unit * (C::X_BYTES / 4) + lane * 16, rank);
+                const uint32_t to_b = of_peer(bar(C::B_X + unit), rank);
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
                     const uint32_t par = n_tile & 1;
                     if (!(ok = wait(C::B_S + par, (n_tile >> 1) & 1, kErrTimeoutMma))) break;
                     tc_fence_after();
-                    uint32_t r[2][32];   // of two owners, as they hold theirs
-                    tc_ld_16x256b_x8(lanes + C::COL_S + par * BN, r[0]);
-                    tc_ld_16x256b_x8(lanes + (16u << 16) + C::COL_S + par * BN, r[1]);
+                    uint32_t r[32];   // as the owner holds its part
+                    tc_ld_16x256b_x8(others + C::COL_S + par * BN, r);
                     tc_wait_ld();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_READ + par));
-                    // (this CTA is done with tile i - 2: the peer has read that tile's part of S, and may
-                    // write tile i's weights here)
-                    if (n_tile > 1 && !(ok = wait(C::B_PV + par, ((n_tile >> 1) - 1) & 1, kErrTimeoutMma))) break;
+                    // (the peer has read its part of S of two tiles before)
+                    if (n_tile > 1 && !(ok = wait(C::B_THEIRS + par * 4 + unit, ((n_tile >> 1) - 1) & 1, kErrTimeoutSoftmax))) break;
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            peer_store4_async(to_x + par * C::X_BYTES + u * (C::X_BYTES / 4) + i * 512, to_b + (par * 4 + u) * 8,
-                                              r[u][4 * i], r[u][4 * i + 1], r[u][4 * i + 2], r[u][4 * i + 3]);
+                    for (int i = 0; i < 8; ++i)
+                        peer_store4_async(to_x + par * C::X_BYTES + i * 512, to_b + par * 32, r[4 * i], r[4 * i + 1],
+                                          r[4 * i + 2], r[4 * i + 3]);
                 }
                 if (!ok) break;
             } else {
@@ -637,7 +629,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
                     const uint32_t par = n_tile & 1;
                     const int key0 = (w.off + j) * BN;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_THEIRS + par * 2 + half), 32 * (128 + 4));
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::B_THEIRS + par * 4 + unit), 16 * (128 + 4));
                     if (key0 + BN > hi) {
                         // keys that no row of the block keeps: their values are zeroed, since memory may
                         // hold anything there (or nothing was copied) and a weight of 0 must not meet a NaN
@@ -646,16 +638,17 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                         const int r0 = max(hi - key0, 0), per_chunk = (BN - r0) * 8;   // 16-byte units
                         uint8_t* at = smem + C::OFF_RING + s * C::TILE + r0 * 128;
                         for (int c = 0; c < DC; ++c)
-                            for (int u = half * 32 + lane; u < per_chunk; u += 64)
+                            for (int u = row; u < per_chunk; u += 128)
                                 *reinterpret_cast<uint4*>(at + c * kChunk + u * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();
                     }
-                    if (!(ok = wait_peer(C::B_THEIRS + par * 2 + half, (n_tile >> 1) & 1, kErrTimeoutSoftmax))) break;
-                    const float f = factors[par * 64 + half * 32 + lane];
-                    if (__any_sync(0xffffffffu, f != 1.f) && j > 0) {
+                    if (!(ok = wait_peer(C::B_THEIRS + par * 4 + unit, (n_tile >> 1) & 1, kErrTimeoutSoftmax))) break;
+                    const float* f = factors + par * 64 + unit * 16 + (lane >> 2);
+                    const float f_a = f[0], f_b = f[8];
+                    if (__any_sync(0xffffffffu, f_a != 1.f || f_b != 1.f) && j > 0) {
                         if (!(ok = wait(C::B_PV + (par ^ 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
                         tc_fence_after();
-                        rescale<NP>(lanes + C::COL_O, f);
+                        rescale<NP>(others + C::COL_O, f_a, f_b);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -665,14 +658,14 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
             }
             const Walk cur = w;
             on = walk_next<NR, SEG>(a, w);
-            if (aux && on) {
+            if (group == 2 && on) {
                 if (!(ok = wait(C::B_QEMPTY, n_seg & 1, kErrTimeoutMma))) break;
                 tc_fence_after();
                 load_q(w);
             }
             if (!(ok = wait_peer(C::B_SUM + (n_seg & 1), (n_seg >> 1) & 1, kErrTimeoutSoftmax))) break;
             tc_fence_after();
-            write_row<NP>(a, to, lanes + C::COL_O, row, rank * C::HD, aux, sums[(n_seg & 1) * NR + row]);
+            write_row<NP>(a, to, lanes + C::COL_O, row, rank * C::HD, group, sums[(n_seg & 1) * NR + row]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_OUT));
