@@ -53,7 +53,6 @@ constexpr int kSoftmaxWarps = 4;
 constexpr int kTmaWarp = kSoftmaxWarps, kSWarp = kTmaWarp + 1;   // and the PV warp
 constexpr int kOutWarp = kSWarp + 2;
 constexpr int kThreads = (kOutWarp + 4) * 32;
-static_assert(kThreads / 32 + 2 <= 14, "scratch");
 
 // instruction descriptor: f16 operands, f32 accumulation; A's major (1: MN), B K-major
 __host__ __device__ constexpr uint32_t idesc(uint32_t M, uint32_t N, uint32_t a_mn) {
@@ -104,7 +103,7 @@ struct Cfg {
         B_TEARDOWN,        // of both issuers
         N_BARS = B_TEARDOWN + 2
     };
-    static constexpr uint32_t OFF_BAR = OFF_SUMS + 14 * 8;
+    static constexpr uint32_t OFF_BAR = OFF_SUMS + kRunWords<kThreads> * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
     static constexpr uint32_t COL_O = 2 * BN, COLS = COL_O + NP * NR;
@@ -174,6 +173,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be set up meanwhile
+    prefetch_run(a, kThreads);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (tid == kSoftmaxWarps * 32) {
         tma_prefetch_desc(&tm_q);

@@ -67,7 +67,7 @@ struct Cfg {
         B_TEARDOWN,                      // of both issuers
         N_BARS = B_TEARDOWN + 2
     };
-    static constexpr uint32_t OFF_BAR = OFF_RUN + (kThreads / 32 + 3) / 2 * 16;
+    static constexpr uint32_t OFF_BAR = OFF_RUN + kRunWords<kThreads> * 8;
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
     static constexpr uint32_t COL_O = 0, COL_S = HD, COL_Q = COL_S + 2 * BN, COLS = COL_Q + HD / 2;
@@ -75,7 +75,7 @@ struct Cfg {
     static_assert(COLS <= 512 && NS % 2 == 0);
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
-    static_assert(OFF_BAR % 8 == 0 && OFF_RUN % 16 == 0, "alignment");
+    static_assert(OFF_BAR % 8 == 0 && OFF_RUN % 8 == 0, "alignment");
 };
 
 // ---- the peer's shared memory
@@ -185,6 +185,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     auto bar = [&](int i) { return sbase + C::OFF_BAR + i * 8; };
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be set up meanwhile
+    prefetch_run(a, kThreads);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = blockIdx.x & 1;
     if (tid == kTmaWarp * 32) {
@@ -198,23 +199,23 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
         peer_store(of_peer(sbase + C::OFF_MISC + 4, rank), 1u);
         atomicExch(a.err, code);
     };
-    auto wait_by = [&](auto test, int b, uint32_t parity, int code) -> bool {
-        if (__all_sync(0xffffffffu, test(bar(b), parity))) return true;
+    auto wait_for = [&](auto test, int code) -> bool {
+        if (__all_sync(0xffffffffu, test())) return true;
         const uint64_t t0 = globaltimer();
         const uint64_t limit = *static_cast<volatile unsigned long long*>(&g_wait_limit_ns);
 #pragma unroll 1
         do {
-            if (__all_sync(0xffffffffu, test(bar(b), parity))) return true;
+            if (__all_sync(0xffffffffu, test())) return true;
             if (__any_sync(0xffffffffu, *abort_flag)) return false;
         } while (__any_sync(0xffffffffu, globaltimer() - t0 < limit));
         give_up(code);
         return false;
     };
     auto wait = [&](int b, uint32_t parity, int code) -> bool {
-        return wait_by([](uint32_t x, uint32_t y) { return mbar_try_wait(x, y); }, b, parity, code);
+        return wait_for([&] { return mbar_try_wait(bar(b), parity); }, code);
     };
     auto wait_peer = [&](int b, uint32_t parity, int code) -> bool {
-        return wait_by([](uint32_t x, uint32_t y) { return try_wait_peer(x, y); }, b, parity, code);
+        return wait_for([&] { return try_wait_peer(bar(b), parity); }, code);
     };
 
     if (warp == 0) {
@@ -435,6 +436,9 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                 // ---------------------------------------------------- owners: 16 rows' weights
                 const int first_row = unit * 32 + rank * 16;
                 const int ra = first_row + (lane >> 2), rb = ra + 8;   // this thread's rows of the block
+                const uint32_t at_p = sbase + C::OFF_P + first_row * 128, to_p = of_peer(at_p, rank);
+                const uint32_t theirs = of_peer(bar(C::B_THEIRS + unit), rank);
+                const uint32_t to_f = of_peer(sbase + C::OFF_FACTORS + (unit * 16 + (lane >> 2)) * 4, rank);
                 const long long live = static_cast<long long>(w.c.n) * a.H - row0;
                 // rows keep the keys below lim; no row of the warp drops a key below all_keep
                 const int lim_a = key_end(a, w.c, row0 + ra + 1), lim_b = key_end(a, w.c, row0 + rb + 1);
@@ -446,36 +450,37 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     const uint32_t par = n_tile & 1;
                     const int b_x = C::B_X + par * 4 + unit;
                     if (lane == 0) mbar_arrive_expect_tx(bar(b_x), C::X_BYTES / 4);
-                    if (!(ok = wait(C::B_S + par, (n_tile >> 1) & 1, kErrTimeoutMma))) break;
+                    // S of both CTAs is there, and P of two tiles before has been read, here and at the peer
+                    // (in one: each wait costs 100 cycles or more)
+                    const uint32_t now = (n_tile >> 1) & 1;
+                    if (!(ok = wait_for([&] {
+                              return mbar_try_wait(bar(C::B_S + par), now) && try_wait_peer(bar(b_x), now) &&
+                                     (n_tile < 2 || mbar_try_wait(bar(C::B_PV + par), now ^ 1));
+                          }, kErrTimeoutMma))) break;
                     tc_fence_after();
                     // columns 8 i + 2 (lane % 4), + 1: row a in x[4 i], x[4 i + 1], row b in the next two
                     float x[32];
                     {
                         uint32_t r[32];
+                        float4 y[8];
                         tc_ld_16x256b_x8(own + C::COL_S + par * BN, r);
+                        const float4* part = reinterpret_cast<const float4*>(smem + C::OFF_X + par * C::X_BYTES) + unit * 256 + lane;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = part[i * 32];
                         tc_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::B_READ + par));
-                    if (!(ok = wait_peer(b_x, (n_tile >> 1) & 1, kErrTimeoutSoftmax))) break;
-                    {
-                        const float4* theirs = reinterpret_cast<const float4*>(smem + C::OFF_X + par * C::X_BYTES) + unit * 256 + lane;
-#pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float4 y = theirs[i * 32];
-                            const float2 u = fadd2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(y.x, y.y));
-                            const float2 v = fadd2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(y.z, y.w));
+                            const float2 u = fadd2(make_float2(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1])), make_float2(y[i].x, y[i].y));
+                            const float2 v = fadd2(make_float2(__uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3])), make_float2(y[i].z, y[i].w));
                             x[4 * i] = u.x;
                             x[4 * i + 1] = u.y;
                             x[4 * i + 2] = v.x;
                             x[4 * i + 3] = v.y;
                         }
                     }
-                    // (P of two tiles before has been read, here and at the peer)
-                    if (n_tile > 1 && !(ok = wait(C::B_PV + par, ((n_tile >> 1) - 1) & 1, kErrTimeoutMma))) break;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_READ + par));
                     const int key0 = (w.off + j) * BN;
                     const bool masked = key0 + BN > all_keep;
                     const int drop_a = lim_a - key0 - 2 * (lane & 3), drop_b = lim_b - key0 - 2 * (lane & 3);
@@ -554,16 +559,11 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     l_b = fadd2(l_b, s_b);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    const uint32_t theirs = of_peer(bar(C::B_THEIRS + par * 4 + unit), rank);
-                    if (lane == 0) {
-                        // 16 lines of P to the peer
-                        const uint32_t at = sbase + C::OFF_P + par * kRowsChunk + first_row * 128;
-                        peer_copy(of_peer(at, rank), at, 16 * 128, theirs);
-                    }
+                    // 16 lines of P to the peer, and the rows' factors
+                    if (lane == 0) peer_copy(to_p + par * kRowsChunk, at_p + par * kRowsChunk, 16 * 128, theirs + par * 32);
                     if ((lane & 3) == 0) {
-                        const uint32_t to_f = of_peer(sbase + C::OFF_FACTORS + (par * 64 + unit * 16 + (lane >> 2)) * 4, rank);
-                        peer_store_async(to_f, theirs, f_a);
-                        peer_store_async(to_f + 32, theirs, f_b);
+                        peer_store_async(to_f + par * 256, theirs + par * 32, f_a);
+                        peer_store_async(to_f + par * 256 + 32, theirs + par * 32, f_b);
                     }
                     if (moved) {
                         if (!(ok = wait(C::B_PV + (par ^ 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
@@ -607,7 +607,12 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                 const uint32_t to_b = of_peer(bar(C::B_X + unit), rank);
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
                     const uint32_t par = n_tile & 1;
-                    if (!(ok = wait(C::B_S + par, (n_tile >> 1) & 1, kErrTimeoutMma))) break;
+                    // (the peer has read its part of S of two tiles before)
+                    const uint32_t now = (n_tile >> 1) & 1;
+                    if (!(ok = wait_for([&] {
+                              return mbar_try_wait(bar(C::B_S + par), now) &&
+                                     (n_tile < 2 || mbar_try_wait(bar(C::B_THEIRS + par * 4 + unit), now ^ 1));
+                          }, kErrTimeoutMma))) break;
                     tc_fence_after();
                     uint32_t r[32];   // as the owner holds its part
                     tc_ld_16x256b_x8(others + C::COL_S + par * BN, r);
@@ -615,8 +620,6 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_READ + par));
-                    // (the peer has read its part of S of two tiles before)
-                    if (n_tile > 1 && !(ok = wait(C::B_THEIRS + par * 4 + unit, ((n_tile >> 1) - 1) & 1, kErrTimeoutSoftmax))) break;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         peer_store4_async(to_x + par * C::X_BYTES + i * 512, to_b + par * 32, r[4 * i], r[4 * i + 1],

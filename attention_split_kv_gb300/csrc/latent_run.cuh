@@ -78,11 +78,10 @@ struct Walk {
     int off, n, tiles;   // first key tile and key tiles of the segment; key tiles of the item
     Chunk c;
 };
-template <int NR, int SEG>
+// (b, g, in, rem and the item's chunk and tiles are there)
+template <int SEG>
 __device__ __forceinline__ bool walk_item(const Args& a, Walk& w) {
     if (w.rem <= 0) return false;
-    w.c = load_chunk(a, w.b);
-    w.tiles = group_tiles<NR>(a, w.c, w.g);
     w.off = a.whole ? 0 : max(static_cast<int>(w.in) - SEG, 0);
     w.n = (a.whole ? w.tiles : static_cast<int>(min(static_cast<long long>(w.tiles), w.in + w.rem - SEG))) - w.off;
     return w.n > 0;
@@ -96,18 +95,33 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
         w.g = 0;
         do {
             if (++w.b >= a.B) return false;
-        } while (load_chunk(a, w.b).n == 0);
+            w.c = load_chunk(a, w.b);
+        } while (w.c.n == 0);
     }
-    return walk_item<NR, SEG>(a, w);
+    w.tiles = group_tiles<NR>(a, w.c, w.g);
+    return walk_item<SEG>(a, w);
 }
 template <int NR, int SEG>
 __device__ __forceinline__ bool walk_first(const Args& a, Walk& w) {
-    const bool on = walk_item<NR, SEG>(a, w);
+    const bool on = walk_item<SEG>(a, w);
     return on && a.whole && w.in > 0 ? walk_next<NR, SEG>(a, w) : on;   // (whole items: those that start in the run)
 }
 
+// What a run's start depends on, on its way into L2 and the address tables before the kernels before this
+// one have ended (nothing is read): a miss of those costs 2500 cycles, and three lie one behind another.
+__device__ __forceinline__ void prefetch_run(const Args& a, int threads) {
+    for (int b = threadIdx.x; b <= a.B; b += threads) {
+        prefetch_l2(a.q_start + b);
+        if (b == a.B) break;
+        prefetch_l2(a.kv_len + b);
+        if (a.page_table) prefetch_l2(a.page_table + static_cast<size_t>(b) * a.max_pages);
+    }
+}
+
 // The run of unit `unit` of `units`, found by the whole block of THREADS threads (two __syncthreads, the
-// first with the tcgen05 fences for what the caller has set up); `scratch`: THREADS / 32 + 2 words of 8 bytes.
+// first with the tcgen05 fences for what the caller has set up); `sums`: scratch of kRunWords words of 8 bytes.
+template <int THREADS>
+constexpr int kRunWords = THREADS / 32 + 5;
 template <int NR, int SEG, int THREADS>
 __device__ __forceinline__ Walk find_run(const Args& a, int unit, int units, long long* sums) {
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -168,14 +182,22 @@ __device__ __forceinline__ Walk find_run(const Args& a, int unit, int units, lon
                 return true;
             }
             sums[kWarps] = t - at;
+            const Chunk c = load_chunk(a, b);
             first[0] = b;
             first[1] = g;
+            first[2] = c.q_base;
+            first[3] = c.n;
+            first[4] = c.pos0;
+            first[5] = c.L;
+            first[6] = weight - SEG;
             return false;
         });
     }
     __syncthreads();
     run.b = first[0];
     run.g = first[1];
+    run.c = Chunk{first[2], first[3], first[4], first[5]};
+    run.tiles = first[6];
     run.in = sums[kWarps];
     run.rem = unit < runs && total > 0 ? each + (unit < more) : 0;
     return run;
