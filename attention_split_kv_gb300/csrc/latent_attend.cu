@@ -217,11 +217,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // Half a tile is one box where the tile lies in one page (or none), else a box a page and
         // chunk.  (The whole warp runs the code and one lane issues.)
         const uint32_t one = elect_one();
-        // One token a sequence reads the cache once (its row blocks side by side): the lines are the
-        // first to go, so that those of the partial rows stay, and some of the cache for the next step
-        // (32 sequences of 512 to 8192, 16 heads: 39.2 to 35.5 us; 128 heads: 65.0 to 61.8).  Row blocks
-        // that come by at other times want them longer (1 to 4 drafts of 16 x 32768: 139.5 to 141.3).
-        const uint64_t policy = a.max_q == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+        // (a chunk is one row block)  The cache is read once: its lines are the first to leave L2, so that
+        // those of the partial rows stay, and some of the cache for the next step (32 sequences of 512 to
+        // 8192, 16 heads: 39.2 to 35.5 us).
+        const uint64_t policy = l2_policy_evict_first();
         const int log_nb = a.log_nb, nb = 1 << log_nb, box_rows = BN >> log_nb, P = 1 << a.log2P;
         uint32_t n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
         uint32_t s = 0, phase = 1;                 // place, and the phase of its release (the first round waits for none)
