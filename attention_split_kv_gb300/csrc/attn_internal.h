@@ -256,7 +256,7 @@ struct LatentAttendLaunch {
 };
 size_t latent_attend_workspace(int max_q, int H, int R);
 attn_status launch_latent_attend(const LatentAttendLaunch& L);
-attn_status launch_latent_pair(const LatentAttendLaunch& L);   // (of more than 64 rows a chunk)
+attn_status launch_latent_pair(const LatentAttendLaunch& L);   // (many rows, long caches)
 
 struct LatentPrefillLaunch {
     const void *q, *k, *v, *k_rope;

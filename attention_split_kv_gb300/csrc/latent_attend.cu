@@ -33,13 +33,13 @@
 // written by the softmax warps and 4 that do only that.
 //
 // What bounds it.  Few heads: memory.  One token of 32 sequences of 512 to 8192 (137 thousand
-// tokens of 576 values, 158 MB), 16 heads: 35.4 us with the join, 4.5 TB/s (23.3 us at a copy's
+// tokens of 576 values, 158 MB), 16 heads: 34.7 us with the join, 4.6 TB/s (23.3 us at a copy's
 // rate); of the rest about 4 us go by before the first tile is there, 4 in the join, and the CTAs
 // end 3 apart.  64-row blocks: the tensor cores, whose M = 64 products run at half rate: a tile
 // takes 36 MMAs of 37 cycles and 16 of 47, 2080 in all, and comes by every 2600 to 3000, since
 // with 64 rows' Q the ring holds two tiles and a tile's chain (copy, S, softmax, PV) is 6000
-// long.  128 heads: 61.4 us, 620 TFLOP/s; 1 to 4 drafts of 32 heads of 16 x 32768 tokens: 140 us
-// (89 at a copy's rate), tensor pipe 54%, DRAM 61%.
+// long: 8 sequences of 4096, 128 heads, 27.0 us.  Many such blocks over long caches go to pairs of
+// CTAs instead (latent_pair.cu).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -207,9 +207,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");   // for what earlier calls wrote or still read
 
-    const int unit = static_cast<int>(blockIdx.x);
-    const Walk run = find_run<NR, C::SEG, kThreads>(a, unit, static_cast<int>(gridDim.x),
+    const int cta = static_cast<int>(blockIdx.x);
+    const Walk run = find_run<NR, C::SEG, kThreads>(a, cta / a.side, static_cast<int>(gridDim.x) / a.side,
                                                     reinterpret_cast<long long*>(smem + C::OFF_SUMS));
+    const int rb_in = cta % a.side;   // of the group's row blocks, this CTA's
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
 
     if (warp == kTmaWarp) {
@@ -217,17 +218,18 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // Half a tile is one box where the tile lies in one page (or none), else a box a page and
         // chunk.  (The whole warp runs the code and one lane issues.)
         const uint32_t one = elect_one();
-        // (a chunk is one row block)  The cache is read once: its lines are the first to leave L2, so that
-        // those of the partial rows stay, and some of the cache for the next step (32 sequences of 512 to
-        // 8192, 16 heads: 39.2 to 35.5 us).
-        const uint64_t policy = l2_policy_evict_first();
+        // Row blocks taken side by side, or one, read the cache once: the lines are the first to leave L2,
+        // so that those of the partial rows stay, and some of the cache for the next step (32 sequences of
+        // 512 to 8192, 16 heads: 39.2 to 35.5 us; 128 heads: 65.0 to 61.8).  Row blocks that come by at other
+        // times want them longer (1 to 4 drafts of 16 x 32768: 139.5 to 141.3).
+        const uint64_t policy = a.n_rb <= a.side ? l2_policy_evict_first() : l2_policy_evict_normal();
         const int log_nb = a.log_nb, nb = 1 << log_nb, box_rows = BN >> log_nb, P = 1 << a.log2P;
         uint32_t n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
         uint32_t s = 0, phase = 1;                 // place, and the phase of its release (the first round waits for none)
         bool ok = true;
         Walk w = run;
         for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
-            const uint32_t row0 = static_cast<uint32_t>(w.g) * NR;
+            const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int hi = key_end(a, w.c, row0 + NR);
             // the page of box `lane` of tile j, or the sequence: read a tile before its copies
             auto fetch = [&](int j) {
@@ -371,7 +373,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         bool ok = true;
         Walk w = run;
         for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
-            const Out to = out_of<NR>(a, w, static_cast<uint32_t>(w.g) * NR, unit);
+            const Out to = out_of<NR>(a, w, static_cast<uint32_t>(w.g * a.side + rb_in) * NR, cta);
             if (!(ok = wait(C::B_MEET, n_seg & 1, kErrTimeoutSoftmax))) break;
             tc_fence_after();
             write_rows<NP, NR>(a, to, tmem + C::COL_O, warp & 3, 1,
@@ -425,11 +427,11 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (lane == 0) mbar_arrive(bar(C::B_FIX));
             return true;
         };
-        if (tid == 0) a.meta[unit * 4] = a.meta[unit * 4 + 1] = 0;
+        if (tid == 0) a.meta[cta * 4] = a.meta[cta * 4 + 1] = 0;
         bool ok = true;
         Walk w = run;
         for (bool on = walk_first<NR, C::SEG>(a, w); on && ok; on = walk_next<NR, C::SEG>(a, w), ++n_seg) {
-            const uint32_t row0 = static_cast<uint32_t>(w.g) * NR;
+            const uint32_t row0 = static_cast<uint32_t>(w.g * a.side + rb_in) * NR;
             const int live = static_cast<int>(max(0ll, min(static_cast<long long>(NR), static_cast<long long>(w.c.n) * a.H - row0)));
             const int hi = key_end(a, w.c, row0 + NR);
             // rows keep the keys below lim; no row of the warp drops a key below all_keep
@@ -566,7 +568,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // the rows' sums, out of the threads that have them (two segments' in turn: another warp may
             // still read the last one's)
             float* inv_sum = factors + (2 + (n_seg & 1)) * NR;
-            const Out to = out_of<NR>(a, w, row0, unit);
+            const Out to = out_of<NR>(a, w, row0, cta);
             if (has_rows) {
                 float s_a = l_a.x + l_a.y, s_b = l_b.x + l_b.y;
 #pragma unroll
@@ -592,7 +594,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (tid == 0) {
                 // what the join needs of this CTA: [0] the item its run goes on with ends in it; [1] the
                 // rows to write of the item that it leaves open (0: none), [2] the first of them
-                int* meta = a.meta + unit * 4;
+                int* meta = a.meta + cta * 4;
                 if (w.off > 0) {
                     meta[0] = w.off + w.n == w.tiles;
                 } else if (!to.whole) {
@@ -626,7 +628,6 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
             return st;
     }
     fill_args(L, p, a);
-    a.side = 1;
     const int rows = L.cache.rows, box_rows = BN >> a.log_nb;
     {
         // the same: boxes of half a tile's chunks, or of one chunk of a page
@@ -648,12 +649,13 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
             return set_error(ATTN_ECUDA, "cudaFuncSetAttribute(latent attend smem) failed");
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    const int grid = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    const int sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+    const int grid = sms / a.side * a.side;
     const dim3 join(grid, NR * NP / join_width(NP, NR) / kJoinWarps);
     if (trace_enabled())
-        trace("latent_attend_kernel<R=%d,rows=%d> grid=%d block=%d smem=%u tmem_cols=%u B=%d "
+        trace("latent_attend_kernel<R=%d,rows=%d> grid=%d block=%d smem=%u tmem_cols=%u row_blocks=%d side=%d B=%d "
               "total_q=%d H=%d box_rows=%d whole=%d, then latent_join_kernel grid=(%u,%u)",
-              C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, L.B, L.total_q, L.H, box_rows,
+              C::R, NR, grid, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, box_rows,
               a.whole, a.whole ? 0 : join.x, a.whole ? 0 : join.y);
     // both are set up while the kernel before runs, and wait for its end themselves
     cudaError_t e = launch_dependent(kernel, dim3(grid), kThreads, C::SMEM_ALLOC, L.stream, tq, tx[0], tx[1], tx[2], a);
@@ -668,8 +670,7 @@ attn_status launch_rows(const LatentAttendLaunch& L, const Plan& p) {
     switch (p.NR) {
         case 16: return launch<NP, 16>(L, p);
         case 32: return launch<NP, 32>(L, p);
-        case 64: return launch<NP, 64>(L, p);
-        default: return launch_latent_pair(L);
+        default: return launch<NP, 64>(L, p);
     }
 }
 
@@ -679,6 +680,14 @@ size_t latent_attend_workspace(int max_q, int H, int R) { return make_plan(max_q
 
 attn_status launch_latent_attend(const LatentAttendLaunch& L) {
     const Plan p = make_plan(L.max_q, L.H, L.R);
+    // Many blocks of 64 rows over long caches go to pairs of CTAs, which are faster a tile and slower to
+    // start and to end (one GB300, blocks of 64 rows here and in pairs: 32 sequences of 512 to 8192, 128 heads,
+    // 28 tiles an SM, 61.4 and 57.2 us; 256 of 1024, 54 tiles, 124 and 110; a chunk of 512 tokens on 4096,
+    // 597 and 473; 8 sequences of 4096, 7 tiles, 27.1 and 31.6; one of 3000 20.7 and 27.7; 256 latent values,
+    // 32 sequences of 4096: 33.7 and 41.6).  What the caches hold is not known here, only what they can.
+    const long long blocks = L.B * p.n_rb;
+    if (L.R == 512 && p.n_rb > 1 && blocks >= 32 && blocks * ((L.cache.capacity + BN - 1) / BN) >= 16 * kMaxCtas)
+        return launch_latent_pair(L);
     return L.R == 256 ? launch_rows<2>(L, p) : launch_rows<4>(L, p);
 }
 

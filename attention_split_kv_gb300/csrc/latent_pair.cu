@@ -1,5 +1,5 @@
-// latent_pair.cu -- attn_latent_attend for chunks of more than 64 (token, head) rows: a pair of CTAs
-// (a cluster) takes blocks of 128 rows, each CTA one half of a cached row's values.
+// latent_pair.cu -- attn_latent_attend for many (token, head) rows over long caches, 512 latent values: a
+// pair of CTAs (a cluster) takes blocks of 128 rows, each CTA one half of a cached row's values.
 //
 //   S_r = Q_r X_r^T    128 rows x 64 keys, over CTA r's half of the dims    (tcgen05.mma, M = 128)
 //   S = S_0 + S_1      for 64 of the rows: the peer's part comes through shared memory
@@ -8,17 +8,28 @@
 //
 // Alone, a CTA has room for 64 rows of 512 values, whose M = 64 products run at half rate, and for
 // two tiles beside their Q.  Halves of the dims make both products M = 128, and four half tiles fit
-// beside Q, whose latent part (R / 2 values of 128 rows) lies in TMEM: 512 columns are O (R / 2), two S
-// (128) and Q (R / 4).  The rotated part (64 values) of a tile is CTA 0's or CTA 1's in turn.
+// beside Q, whose latent part (256 values of 128 rows) lies in TMEM: 512 columns are O (256), two S
+// (128) and Q (128).  The rotated part (64 values) of a tile is CTA 0's or CTA 1's in turn.
 //
 // A row belongs to one CTA: 16 of each 32 rows (of a warp's lanes of TMEM) to CTA 0, the others to CTA
 // 1, so that the four warps that own rows are on all four schedulers (on two: 2260 cycles a tile).
 // Four more send the other rows' part of S to the peer, and four take what concerns the other rows'
 // O: they wait for their P and rescale their O if their maximum moved.
 //
+// What crosses to the peer goes without a release (one costs 1500 to 2300 cycles): S by st.async, 16 lines
+// of P by a copy of 2 KB, both counted in bytes on the peer's barriers (a copy arrives 900 cycles later;
+// st.async of P as well, after a transpose over four lanes, was no faster).
+//
 // Ordering between the CTAs: tile i's part of S is sent once the peer's weights of tile i - 2 are here
 // (it has read that tile's part); P(i) is written once both CTAs' second products of tile i - 2 are done
 // (each commits to both).  Neither CTA ends before the other's last store to it: they meet at the end.
+//
+// What bounds it: the chain from tile to tile.  A tile comes by every 1900 to 2000 cycles, of which the tensor
+// cores work 1150; with a quarter of the products, no exponentials and a quarter of the copies it is 1700.
+// Two tiles' P and S are under way at a time, and shared memory is full.  An owner's loop takes 2000 cycles
+// for 16 rows; 8 rows an owner (19 warps) made 128 heads 57 to 61 us, owners that take every second
+// tile 67.  32 sequences of 512 to 8192, 128 heads: 57.2 us, 660 TFLOP/s; 1 to 4 drafts of 32 heads of 16 x
+// 32768 tokens: 138.7 us, 4.4 TB/s.
 //
 // Roles (15 warps): 4 owners, 4 senders, 4 that wait for the peer's P (and load Q into TMEM), a TMA warp,
 // a warp that issues S and one that issues the others.  The first 12 write a segment's rows.
@@ -31,17 +42,16 @@
 namespace attn {
 namespace {
 
+constexpr int NP = 4;                       // blocks of 128 latent values, half of them a CTA's
 constexpr int NR = 128;                     // rows of a block
-constexpr int SEG = 8;                      // a segment's fixed cost, in key tiles
+constexpr int SEG = 8;   // a segment's fixed cost, in key tiles (128 heads: 66.0 us with 2, 61.9 with 4, 58.3 with 8, 58.6 with 12)
 constexpr int kTmaWarp = 12, kSWarp = 13, kPvWarp = 14;   // and 4 each of owners, senders and others before them
 constexpr int kThreads = (kPvWarp + 1) * 32;
 constexpr uint32_t kRowsChunk = NR * 128;   // bytes of 64 values of a block's rows
 
-// NP: blocks of 128 latent values, NP / 2 a CTA.
-template <int NP>
 struct Cfg {
     static constexpr int R = NP * 128, W = R + 64, HD = R / 2, DC = NP;   // DC: chunks of 64 values of a half
-    static constexpr int NS = NP == 4 ? 4 : 6;                            // tiles in the ring
+    static constexpr int NS = 4;                                          // tiles in the ring
     static constexpr uint32_t TILE = DC * kChunk;
     static constexpr uint32_t X_BYTES = NR / 2 * BN * 4;
     static constexpr uint32_t OFF_QR = 0;                                 // rotated part of Q
@@ -71,8 +81,8 @@ struct Cfg {
     static constexpr uint32_t OFF_MISC = OFF_BAR + N_BARS * 8;   // TMEM base, abort flag
     static constexpr uint32_t SMEM_ALLOC = OFF_MISC + 8 + 1024;
     static constexpr uint32_t COL_O = 0, COL_S = HD, COL_Q = COL_S + 2 * BN, COLS = COL_Q + HD / 2;
-    static constexpr uint32_t TMEM_COLS = COLS <= 256 ? 256 : 512;
-    static_assert(COLS <= 512 && NS % 2 == 0);
+    static constexpr uint32_t TMEM_COLS = 512;
+    static_assert(COLS <= TMEM_COLS && NS % 2 == 0);
     static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
     static_assert(2 * (SMEM_ALLOC + 1024) > 233472, "one CTA an SM: its TMEM allocation never waits");
     static_assert(OFF_BAR % 8 == 0 && OFF_RUN % 8 == 0, "alignment");
@@ -129,7 +139,6 @@ __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // This thread's row of O, every third 32 values from `first` on.
-template <int NP>
 __device__ __forceinline__ void write_row(const Args& a, const Out& o, uint32_t o_tmem, int row, int d0, int first, float inv) {
     constexpr int R = NP * 128;
     const bool live = row < o.n;
@@ -158,7 +167,6 @@ __device__ __forceinline__ void write_row(const Args& a, const Out& o, uint32_t 
 }
 
 // 16 lanes of O times a factor a row (a thread has values of rows lane / 4 and lane / 4 + 8).
-template <int NP>
 __device__ __forceinline__ void rescale(uint32_t o_tmem, float f_a, float f_b) {
 #pragma unroll 1
     for (int q = 0; q < NP * 2; ++q) {
@@ -172,11 +180,10 @@ __device__ __forceinline__ void rescale(uint32_t o_tmem, float f_a, float f_b) {
     tc_wait_st();
 }
 
-template <int NP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_half,
                    const __grid_constant__ CUtensorMap tm_box, const Args a) {
-    using C = Cfg<NP>;
+    using C = Cfg;
     constexpr int NS = C::NS, DC = C::DC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -220,7 +227,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
 
     if (warp == 0) {
         for (int i = lane; i < C::N_BARS; i += 32) {
-            int n = 1;
+            int n = 1;   // arrivals
             if (i == C::B_Q) n = 4;                                     // warps
             if (i >= C::B_READ && i < C::B_READ + 2) n = 8;             // owners, senders
             if (i >= C::B_P && i < C::B_P + 2) n = 8;                   // owners, and those of the peer's rows
@@ -568,7 +575,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     if (moved) {
                         if (!(ok = wait(C::B_PV + (par ^ 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
                         tc_fence_after();
-                        rescale<NP>(own + C::COL_O, f_a, f_b);
+                        rescale(own + C::COL_O, f_a, f_b);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -651,7 +658,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                     if (__any_sync(0xffffffffu, f_a != 1.f || f_b != 1.f) && j > 0) {
                         if (!(ok = wait(C::B_PV + (par ^ 1), ((n_tile - 1) >> 1) & 1, kErrTimeoutMma))) break;
                         tc_fence_after();
-                        rescale<NP>(others + C::COL_O, f_a, f_b);
+                        rescale(others + C::COL_O, f_a, f_b);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -668,7 +675,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
             }
             if (!(ok = wait_peer(C::B_SUM + (n_seg & 1), (n_seg >> 1) & 1, kErrTimeoutSoftmax))) break;
             tc_fence_after();
-            write_row<NP>(a, to, lanes + C::COL_O, row, rank * C::HD, group, sums[(n_seg & 1) * NR + row]);
+            write_row(a, to, lanes + C::COL_O, row, rank * C::HD, group, sums[(n_seg & 1) * NR + row]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_OUT));
@@ -700,16 +707,12 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
     cluster_meet();   // (the peer may still store here)
 }
 
-template <int NP>
 attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
-    using C = Cfg<NP>;
+    using C = Cfg;
     CUtensorMap tq, tx[2];
     Args a;
     attn_status st;
     fill_args(L, p, a);
-    // One token of more than 128 heads: neighbouring pairs take its row blocks side by side, so that the
-    // second one finds the cache's rows in L2
-    a.side = L.max_q == 1 && p.n_rb <= 8 ? static_cast<int>(p.n_rb) : 1;
     {
         const uint64_t dims[3] = {64u, (uint64_t)L.total_q * L.H, 2 * NP + 1};
         const uint64_t strides[2] = {(uint64_t)C::W * 2, 128u};
@@ -728,7 +731,7 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
                 return st;
         }
     }
-    auto kernel = latent_pair_kernel<NP>;
+    auto kernel = latent_pair_kernel;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -741,9 +744,9 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
     const int pairs = sms / 2 / a.side * a.side;
     const dim3 join(pairs, NR * NP / join_width(NP, NR) / kJoinWarps);
     if (trace_enabled())
-        trace("latent_pair_kernel<R=%d> grid=%d block=%d smem=%u tmem_cols=%u row_blocks=%d side=%d B=%d total_q=%d H=%d "
+        trace("latent_pair_kernel grid=%d block=%d smem=%u tmem_cols=%u row_blocks=%d side=%d B=%d total_q=%d H=%d "
               "box_rows=%d whole=%d, then latent_join_kernel grid=(%u,%u)",
-              C::R, pairs * 2, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, box_rows, a.whole,
+              pairs * 2, kThreads, C::SMEM_ALLOC, C::TMEM_COLS, a.n_rb, a.side, L.B, L.total_q, L.H, box_rows, a.whole,
               a.whole ? 0 : join.x, a.whole ? 0 : join.y);
     // both are set up while the kernel before runs, and wait for its end themselves
     cudaError_t e = launch_dependent(kernel, dim3(pairs * 2), kThreads, C::SMEM_ALLOC, L.stream, static_cast<const __half*>(L.q),
@@ -757,8 +760,10 @@ attn_status launch(const LatentAttendLaunch& L, const Plan& p) {
 }  // namespace
 
 attn_status launch_latent_pair(const LatentAttendLaunch& L) {
-    const Plan p = make_plan(L.max_q, L.H, L.R);
-    return L.R == 256 ? launch<2>(L, p) : launch<4>(L, p);
+    // (the workspace is that of blocks of 64 rows: half as many units, of twice the rows)
+    Plan p = make_plan(L.max_q, L.H, L.R);
+    p.n_rb = (p.n_rb + 1) / 2;
+    return launch(L, p);
 }
 
 // Sets this translation unit's test controls (see ptx.cuh).
