@@ -38,8 +38,9 @@
 // end 3 apart.  64-row blocks: the tensor cores, whose M = 64 products run at half rate: a tile
 // takes 36 MMAs of 37 cycles and 16 of 47, 2080 in all, and comes by every 2600 to 3000, since
 // with 64 rows' Q the ring holds two tiles and a tile's chain (copy, S, softmax, PV) is 6000
-// long: 8 sequences of 4096, 128 heads, 27.0 us.  Many such blocks over long caches go to pairs of
-// CTAs instead (latent_pair.cu).
+// long: 8 sequences of 4096, 128 heads, 27.0 us; 1 to 4 drafts of 32 heads of 16 x 32768 tokens 140
+// us (89 at a copy's rate), tensor pipe 54%, DRAM 61%.  Many such blocks over long caches go to pairs
+// of CTAs instead (latent_pair.cu).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -681,12 +682,14 @@ size_t latent_attend_workspace(int max_q, int H, int R) { return make_plan(max_q
 attn_status launch_latent_attend(const LatentAttendLaunch& L) {
     const Plan p = make_plan(L.max_q, L.H, L.R);
     // Many blocks of 64 rows over long caches go to pairs of CTAs, which are faster a tile and slower to
-    // start and to end (one GB300, blocks of 64 rows here and in pairs: 32 sequences of 512 to 8192, 128 heads,
-    // 28 tiles an SM, 61.4 and 57.2 us; 256 of 1024, 54 tiles, 124 and 110; a chunk of 512 tokens on 4096,
-    // 597 and 473; 8 sequences of 4096, 7 tiles, 27.1 and 31.6; one of 3000 20.7 and 27.7; 256 latent values,
-    // 32 sequences of 4096: 33.7 and 41.6).  What the caches hold is not known here, only what they can.
+    // start and to end (one GB300, here and in pairs: 32 sequences of 512 to 8192, 128 heads, 28 tiles an SM,
+    // 61.4 and 57.3 us; 256 of 1024, 54 tiles, 124 and 110; a chunk of 512 tokens on 4096, 597 and 475; 8 sequences
+    // of 4096, 7 tiles, 27.0 and 31.6; one of 3000 20.7 and 27.7; 256 latent values, 32 sequences of 4096: 33.7
+    // and 41.6).  Not chunks of one or two blocks, of which the shorter ones fill half a pair's (1 to 4 drafts of
+    // 32 heads of 16 x 32768: 141.7 and 145.5).  What the caches hold is not known here, only what they can.
     const long long blocks = L.B * p.n_rb;
-    if (L.R == 512 && p.n_rb > 1 && blocks >= 32 && blocks * ((L.cache.capacity + BN - 1) / BN) >= 16 * kMaxCtas)
+    if (L.R == 512 && p.n_rb > (L.max_q == 1 ? 1 : 2) && blocks >= 32 &&
+        blocks * ((L.cache.capacity + BN - 1) / BN) >= 16 * kMaxCtas)
         return launch_latent_pair(L);
     return L.R == 256 ? launch_rows<2>(L, p) : launch_rows<4>(L, p);
 }

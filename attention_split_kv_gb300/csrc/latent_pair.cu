@@ -28,8 +28,8 @@
 // cores work 1150; with a quarter of the products, no exponentials and a quarter of the copies it is 1700.
 // Two tiles' P and S are under way at a time, and shared memory is full.  An owner's loop takes 2000 cycles
 // for 16 rows; 8 rows an owner (19 warps) made 128 heads 57 to 61 us, owners that take every second
-// tile 67.  32 sequences of 512 to 8192, 128 heads: 57.2 us, 660 TFLOP/s; 1 to 4 drafts of 32 heads of 16 x
-// 32768 tokens: 138.7 us, 4.4 TB/s.
+// tile 67.  32 sequences of 512 to 8192, 128 heads: 57.3 us, 660 TFLOP/s; a chunk of 512 tokens of 128 heads
+// on 4096: 475 us, 1180 TFLOP/s.
 //
 // Roles (15 warps): 4 owners, 4 senders, 4 that wait for the peer's P (and load Q into TMEM), a TMA warp,
 // a warp that issues S and one that issues the others.  The first 12 write a segment's rows.
@@ -259,7 +259,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
         // (The whole warp runs the code and one lane issues.)
         const uint32_t one = elect_one();
         // Row blocks taken side by side, or one, read the cache once: the lines are the first to leave L2,
-        // so that those of the partial rows stay (1 to 4 drafts of 16 x 32768: 141.8 to 139.0 us).
+        // so that those of the partial rows stay.
         const uint64_t policy = a.n_rb <= a.side ? l2_policy_evict_first() : l2_policy_evict_normal();
         const int log_nb = a.log_nb, nb = 1 << log_nb, box_rows = BN >> log_nb, P = 1 << a.log2P;
         uint32_t n_tile = 0, n_seg = 0, s = 0, phase = 1;   // (the first round waits for no release)

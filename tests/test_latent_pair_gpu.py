@@ -13,7 +13,8 @@ from latent_util import assert_lse, assert_within, attend_reference, starts
 
 pytestmark = pytest.mark.gpu
 
-ROOM, SEQS = 4864, 16   # tokens and sequences for which more than 64 rows a chunk are taken in pairs
+# tokens and sequences for which single tokens of more than 64 rows, and chunks of more than 128, are taken in pairs
+ROOM, SEQS = 4864, 16
 
 
 @pytest.fixture(autouse=True)
@@ -48,8 +49,8 @@ def _check(case, q, q_lens, what="", max_q=None):
 @pytest.mark.parametrize("q_lens,kv_lens,H", [
     ([1, 1], [2500, 3], 65), ([1], [900], 127), ([1, 1, 1], [64, 700, 0], 129), ([1, 1], [4864, 40], 300), ([1], [300], 1100),
     ([1] * 5, [1, 63, 64, 65, 128], 128), ([1] * 20, list(range(100, 2100, 100)), 128),
-    ([3, 1, 4], [700, 20, 3000], 32), ([9, 2], [1500, 2], 16), ([130], [130], 1), ([2, 3], [65, 1000], 100),
-    ([1, 0, 3, 1], [64, 0, 130, 5], 40), ([40, 7], [40, 555], 17),
+    ([3, 1, 4], [700, 20, 3000], 50), ([9, 2], [1500, 2], 16), ([130], [130], 1), ([2, 3], [65, 1000], 100),
+    ([1, 0, 3, 1], [64, 0, 130, 5], 50), ([40, 7], [40, 555], 17),
 ], ids=str)
 @pytest.mark.parametrize("page", [0, 8, 16, 64, 256])
 def test_against_the_formula(q_lens, kv_lens, H, page):
@@ -60,7 +61,7 @@ def test_against_the_formula(q_lens, kv_lens, H, page):
 def test_more_tokens_than_cached_and_a_chunk_that_is_cut():
     case, q, q_lens = _case([9, 4], [5, 300], 20, 16)
     _check(case, q, q_lens)
-    case, q, q_lens = _case([9, 4], [500, 300], 20, 16)
+    case, q, q_lens = _case([9, 4], [500, 300], 40, 16)
     _check(case, q, q_lens, max_q=6)
 
 
@@ -93,7 +94,7 @@ def test_page_ids_outside_the_pool_read_as_zeros_and_are_reported():
     assert_lse(lse, ref_lse)
 
 
-@pytest.mark.parametrize("H,n", [(128, 1), (40, 3)])
+@pytest.mark.parametrize("H,n", [(128, 1), (50, 3)])
 @pytest.mark.parametrize("step", [0.5, 12.0])
 def test_logits_that_keep_growing(H, n, step):
     # keys of one direction, growing along the sequence, and queries along it and against it in turn: the
@@ -167,7 +168,7 @@ def test_two_streams_at_once():
 
 
 def test_offsets_past_32_bits():
-    case, q, q_lens = _case([1, 2], [150, 70], 64, 64)
+    case, q, q_lens = _case([1, 2], [150, 70], 70, 64)
     pages = (1 << 32) // (64 * 576) + 8
     pool = torch.zeros(pages, 64, 576, dtype=torch.float16, device="cuda")
     far = case.page_table.clone()
@@ -198,10 +199,10 @@ import attention_split_kv_gb300 as attn
 import seeded_inputs as si
 from tests.latent_util import starts
 attn.load()
-for B, cap, H, R in ((16, 4864, 128, 512), (16, 4800, 128, 512), (15, 4864, 128, 512), (16, 4864, 128, 256), (32, 4864, 64, 512),
-                     (16, 4864, 300, 512)):
+for B, cap, H, R, n in ((16, 4864, 128, 512, 1), (16, 4800, 128, 512, 1), (15, 4864, 128, 512, 1), (16, 4864, 128, 256, 1),
+                        (32, 4864, 64, 512, 1), (16, 4864, 300, 512, 1), (16, 4864, 32, 512, 4), (16, 4864, 32, 512, 5)):
     case = si.make_latent_case([9] * B, R, 1, page_size=16, cap=cap, device="cuda")
-    attn.latent_attend(case, si.f16_normal((B, H, R + 64), 2, "cuda"), starts([1] * B, "cuda"), 1)
+    attn.latent_attend(case, si.f16_normal((B * n, H, R + 64), 2, "cuda"), starts([n] * B, "cuda"), n)
 torch.cuda.synchronize()
 assert attn.attn_device_status() == attn.ATTN_OK
 """
@@ -214,5 +215,5 @@ def test_trace_names_the_form():
                        text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
     lines = [x for x in r.stderr.splitlines() if x.startswith("[libattn]")]
-    assert ["latent_pair_kernel " in x for x in lines] == [True, False, False, False, False, True]
+    assert ["latent_pair_kernel " in x for x in lines] == [True, False, False, False, False, True, False, True]
     assert "side=1" in lines[0] and "side=3" in lines[5]
