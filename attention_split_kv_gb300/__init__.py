@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 __all__ = [
@@ -43,7 +44,8 @@ exported_symbols = ("attn_version", "attn_last_error", "attn_decode_workspace_si
                     "attn_decode_noalloc", "attn_prefill", "attn_prefill_paged", "attn_decode_validate",
                     "attn_device_status", "attn_testing_set_waits", "attn_prefill_paged_ex",
                     "attn_prefill_paged_workspace_size", "attn_append", "attn_kv_read", "attn_latent_append",
-                    "attn_latent_read", "attn_latent_workspace_size", "attn_latent_attend", "attn_latent_prefill")
+                    "attn_latent_read", "attn_latent_workspace_size", "attn_latent_attend", "attn_latent_prefill",
+                    "attn_latent_append_from", "attn_latent_read_from", "attn_latent_attend_from")
 
 
 class AttnLibraryMissing(RuntimeError):
@@ -112,10 +114,13 @@ def load():
     lib.attn_latent_append.restype = I
     lib.attn_latent_read.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, I, P]
     lib.attn_latent_read.restype = I
-    lib.attn_latent_workspace_size.argtypes = [I, I, I, I]
-    lib.attn_latent_workspace_size.restype = SZ
     lib.attn_latent_attend.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P]
     lib.attn_latent_attend.restype = I
+    for f in (lib.attn_latent_append_from, lib.attn_latent_read_from, lib.attn_latent_attend_from):
+        f.argtypes = [ctypes.c_char_p]   # (the bytes of an argument struct)
+        f.restype = I
+    lib.attn_latent_workspace_size.argtypes = [I, I, I, I]
+    lib.attn_latent_workspace_size.restype = SZ
     lib.attn_latent_prefill.argtypes = [P, P, P, P, LL, LL, LL, LL, LL, LL, P, P, I, I, I, I, I, I, I, I, F, P, P, P]
     lib.attn_latent_prefill.restype = I
     lib.attn_decode_validate.argtypes = [P, P, I, I, I, I, I, ctypes.POINTER(ctypes.c_int), P]
@@ -560,26 +565,44 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
 
 
 # ---------------------------------------------------------------- latent attention
+# The argument structs of the calls that serve single tokens, packed in one step: each argument on its own
+# costs a ctypes call 0.15 us and as much again in Python (32 of them: 13 us a call, packed 4).
+_LATENT_APPEND_ARGS = struct.Struct("@3Pi4qP2f2P2i4P9iP2qP")
+_LATENT_READ_ARGS = struct.Struct("@5P8i2PiP")
+_LATENT_ATTEND_ARGS = struct.Struct("@5P10if3PNP")
+
+
+def _addr(x) -> int:
+    if x is None:
+        return 0
+    return x if isinstance(x, int) else x.data_ptr()
+
+
+def _packed(layout, *args) -> bytes:
+    try:
+        return layout.pack(*args)
+    except (struct.error, OverflowError) as e:
+        raise AttnError(ATTN_EINVAL, "an argument that its type does not hold (%s)" % e) from None
+
+
 def attn_latent_append(c, k_rope, q_rope, in_dtype, c_stride, k_rope_stride, q_stride, q_head_stride, c_norm, norm_eps,
                        norm_offset, rope_cos, rope_sin, rope_positions, rope_interleaved, q_start, kv_len, cache,
                        page_table, page_size, max_pages, n_pages, max_kv, batch, total_q, n_heads, latent_dim,
                        rope_dim, q_out, q_out_stride, q_out_head_stride, stream=None) -> None:
-    _check(load().attn_latent_append(_ptr(c), _ptr(k_rope), _ptr(q_rope), int(in_dtype), int(c_stride),
-                                     int(k_rope_stride), int(q_stride), int(q_head_stride), _ptr(c_norm),
-                                     float(norm_eps), float(norm_offset), _ptr(rope_cos), _ptr(rope_sin),
-                                     int(rope_positions), int(bool(rope_interleaved)), _ptr(q_start), _ptr(kv_len),
-                                     _ptr(cache), _ptr(page_table), int(page_size), int(max_pages), int(n_pages),
-                                     int(max_kv), int(batch), int(total_q), int(n_heads), int(latent_dim),
-                                     int(rope_dim), _ptr(q_out), int(q_out_stride), int(q_out_head_stride),
-                                     _stream(stream)))
+    _check(load().attn_latent_append_from(_packed(
+        _LATENT_APPEND_ARGS, _addr(c), _addr(k_rope), _addr(q_rope), in_dtype, c_stride, k_rope_stride, q_stride,
+        q_head_stride, _addr(c_norm), norm_eps, norm_offset, _addr(rope_cos), _addr(rope_sin), rope_positions,
+        bool(rope_interleaved), _addr(q_start), _addr(kv_len), _addr(cache), _addr(page_table), page_size, max_pages,
+        n_pages, max_kv, batch, total_q, n_heads, latent_dim, rope_dim, _addr(q_out), q_out_stride, q_out_head_stride,
+        _stream(stream) or 0)))
 
 
 def attn_latent_read(cache, kv_len, first, out_start, page_table, page_size, max_pages, n_pages, max_kv, batch, total,
                      latent_dim, rope_dim, c_out, k_rope_out, out_dtype, stream=None) -> None:
-    _check(load().attn_latent_read(_ptr(cache), _ptr(kv_len), _ptr(first), _ptr(out_start), _ptr(page_table),
-                                   int(page_size), int(max_pages), int(n_pages), int(max_kv), int(batch), int(total),
-                                   int(latent_dim), int(rope_dim), _ptr(c_out), _ptr(k_rope_out), int(out_dtype),
-                                   _stream(stream)))
+    _check(load().attn_latent_read_from(_packed(
+        _LATENT_READ_ARGS, _addr(cache), _addr(kv_len), _addr(first), _addr(out_start), _addr(page_table), page_size,
+        max_pages, n_pages, max_kv, batch, total, latent_dim, rope_dim, _addr(c_out), _addr(k_rope_out), out_dtype,
+        _stream(stream) or 0)))
 
 
 def attn_latent_workspace_size(batch, max_q, n_heads, latent_dim) -> int:
@@ -589,11 +612,10 @@ def attn_latent_workspace_size(batch, max_q, n_heads, latent_dim) -> int:
 def attn_latent_attend(q, cache, q_start, kv_len, page_table, page_size, max_pages, n_pages, max_kv, batch, total_q,
                        max_q, n_heads, latent_dim, rope_dim, scale, out, lse_out, workspace, workspace_bytes,
                        stream=None) -> None:
-    _check(load().attn_latent_attend(_ptr(q), _ptr(cache), _ptr(q_start), _ptr(kv_len), _ptr(page_table),
-                                     int(page_size), int(max_pages), int(n_pages), int(max_kv), int(batch),
-                                     int(total_q), int(max_q), int(n_heads), int(latent_dim), int(rope_dim),
-                                     float(scale), _ptr(out), _ptr(lse_out), _ptr(workspace), int(workspace_bytes),
-                                     _stream(stream)))
+    _check(load().attn_latent_attend_from(_packed(
+        _LATENT_ATTEND_ARGS, _addr(q), _addr(cache), _addr(q_start), _addr(kv_len), _addr(page_table), page_size,
+        max_pages, n_pages, max_kv, batch, total_q, max_q, n_heads, latent_dim, rope_dim, scale, _addr(out),
+        _addr(lse_out), _addr(workspace), workspace_bytes, _stream(stream) or 0)))
 
 
 def attn_latent_prefill(q, k, v, k_rope, q_stride, k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride,

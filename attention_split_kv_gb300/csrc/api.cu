@@ -1012,6 +1012,31 @@ attn_status attn_latent_prefill(const void* q, const void* k, const void* v, con
     return launch_latent_prefill(L);
 }
 
+attn_status attn_latent_append_from(const attn_latent_append_args* a) {
+    if (!a) return set_error(ATTN_EINVAL, "attn_latent_append_from: args must be non-null");
+    return attn_latent_append(a->c, a->k_rope, a->q_rope, a->in_dtype, a->c_stride, a->k_rope_stride, a->q_stride,
+                              a->q_head_stride, a->c_norm, a->norm_eps, a->norm_offset, a->rope_cos, a->rope_sin,
+                              a->rope_positions, a->rope_interleaved, a->q_start, a->kv_len, a->cache, a->page_table,
+                              a->page_size, a->max_pages_per_seq, a->n_pages, a->max_kv, a->batch, a->total_q,
+                              a->n_heads, a->latent_dim, a->rope_dim, a->q_out, a->q_out_stride,
+                              a->q_out_head_stride, a->stream);
+}
+
+attn_status attn_latent_read_from(const attn_latent_read_args* a) {
+    if (!a) return set_error(ATTN_EINVAL, "attn_latent_read_from: args must be non-null");
+    return attn_latent_read(a->cache, a->kv_len, a->first, a->out_start, a->page_table, a->page_size,
+                            a->max_pages_per_seq, a->n_pages, a->max_kv, a->batch, a->total, a->latent_dim,
+                            a->rope_dim, a->c_out, a->k_rope_out, a->out_dtype, a->stream);
+}
+
+attn_status attn_latent_attend_from(const attn_latent_attend_args* a) {
+    if (!a) return set_error(ATTN_EINVAL, "attn_latent_attend_from: args must be non-null");
+    return attn_latent_attend(a->q, a->cache, a->q_start, a->kv_len, a->page_table, a->page_size,
+                              a->max_pages_per_seq, a->n_pages, a->max_kv, a->batch, a->total_q, a->max_q,
+                              a->n_heads, a->latent_dim, a->rope_dim, a->scale, a->out, a->lse_out, a->workspace,
+                              a->workspace_bytes, a->stream);
+}
+
 attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_table, int batch, int page_size,
                                  int max_pages_per_seq, int n_pages, int max_kv, int* bad_seq, void* stream) {
     if (!kv_len || batch <= 0 || max_kv <= 0)

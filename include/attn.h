@@ -527,6 +527,25 @@ attn_status attn_latent_append(const void* c, const void* k_rope, const void* q_
                                int n_heads, int latent_dim, int rope_dim, void* q_out, long long q_out_stride,
                                long long q_out_head_stride, void* stream);
 
+/* The same with its arguments in a struct, in their order: what a binding can fill in one step. */
+typedef struct attn_latent_append_args {
+    const void *c, *k_rope, *q_rope;
+    attn_dtype in_dtype;
+    long long c_stride, k_rope_stride, q_stride, q_head_stride;
+    const float* c_norm;
+    float norm_eps, norm_offset;
+    const float *rope_cos, *rope_sin;
+    int rope_positions, rope_interleaved;
+    const int32_t *q_start, *kv_len;
+    void* cache;
+    const int32_t* page_table;
+    int page_size, max_pages_per_seq, n_pages, max_kv, batch, total_q, n_heads, latent_dim, rope_dim;
+    void* q_out;
+    long long q_out_stride, q_out_head_stride;
+    void* stream;
+} attn_latent_append_args;
+attn_status attn_latent_append_from(const attn_latent_append_args* args);
+
 /*
  * attn_latent_read -- cached rows back as packed c and key-part rows.
  *
@@ -542,6 +561,17 @@ attn_status attn_latent_read(const void* cache, const int32_t* kv_len, const int
                              const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
                              int batch, int total, int latent_dim, int rope_dim, void* c_out, void* k_rope_out,
                              attn_dtype out_dtype, void* stream);
+
+/* The same with its arguments in a struct, in their order: what a binding can fill in one step. */
+typedef struct attn_latent_read_args {
+    const void* cache;
+    const int32_t *kv_len, *first, *out_start, *page_table;
+    int page_size, max_pages_per_seq, n_pages, max_kv, batch, total, latent_dim, rope_dim;
+    void *c_out, *k_rope_out;
+    attn_dtype out_dtype;
+    void* stream;
+} attn_latent_read_args;
+attn_status attn_latent_read_from(const attn_latent_read_args* args);
 
 /*
  * attn_latent_attend -- the absorbed form: the newest tokens of every sequence attend to
@@ -569,6 +599,20 @@ attn_status attn_latent_attend(const void* q, const void* cache, const int32_t* 
                                const int32_t* page_table, int page_size, int max_pages_per_seq, int n_pages, int max_kv,
                                int batch, int total_q, int max_q, int n_heads, int latent_dim, int rope_dim, float scale,
                                void* out, float* lse_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with its arguments in a struct, in their order: what a binding can fill in one step. */
+typedef struct attn_latent_attend_args {
+    const void *q, *cache;
+    const int32_t *q_start, *kv_len, *page_table;
+    int page_size, max_pages_per_seq, n_pages, max_kv, batch, total_q, max_q, n_heads, latent_dim, rope_dim;
+    float scale;
+    void* out;
+    float* lse_out;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+} attn_latent_attend_args;
+attn_status attn_latent_attend_from(const attn_latent_attend_args* args);
 
 /*
  * attn_latent_prefill -- the expanded form over packed sequences: the n_b queries of sequence b

@@ -222,3 +222,66 @@ def test_prefill_refuses_tensors_that_do_not_agree(kw, called):
                 max_q=3, scale=0.1)
     args.update(kw)
     _refuses(lambda: attn.latent_prefill(**args), called)
+
+
+# ------------------------------------------------------------------ argument structs
+def _fields(name):
+    """The header's struct of a call, as (name, ctypes type) in order."""
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "attn.h")).read()
+    body = re.search(r"typedef struct %s_args \{(.*?)\}" % name, text, re.S).group(1)
+    kinds = {"int": ctypes.c_int, "attn_dtype": ctypes.c_int, "float": ctypes.c_float, "long long": ctypes.c_longlong,
+             "size_t": ctypes.c_size_t}
+    out = []
+    for line in body.split(";")[:-1]:
+        line = " ".join(line.split()).replace("*", " * ")
+        first, *more = line.split(",")
+        kind = first.replace("*", " ").replace("const ", "").split()
+        for at, item in enumerate([first] + more):
+            out.append((item.split()[-1], ctypes.c_void_p if "*" in item else kinds[" ".join(kind[:-1])]))
+    return out
+
+
+@pytest.mark.parametrize("name", ["attn_latent_append", "attn_latent_read", "attn_latent_attend"])
+def test_argument_structs_lie_as_the_header_says(name, monkeypatch):
+    fields = _fields(name)
+    assert [f for f, _ in fields] == ORDER[name].split()
+    Args = type("Args", (ctypes.Structure,), {"_fields_": fields})
+    values = {f: (0.5 + i if t is ctypes.c_float else 64 * (i + 1)) for i, (f, t) in enumerate(fields)}
+    if "rope_interleaved" in values:
+        values["rope_interleaved"] = 1
+    seen = []
+
+    class Lib:
+        def __getattr__(self, what):
+            return lambda data: seen.append((what, data)) or attn.ATTN_OK
+    monkeypatch.setattr(attn, "load", Lib)
+    getattr(attn, name)(*[values[f] for f, _ in fields])
+    (what, data), = seen
+    assert what == name + "_from"
+    got = Args.from_buffer_copy(data.ljust(ctypes.sizeof(Args), b"\0"))
+    assert {f: getattr(got, f) for f, _ in fields} == values
+
+
+@pytest.mark.parametrize("name,kw,status", [
+    ("append", dict(c=None), EINVAL), ("append", dict(q_out_stride=576), EINVAL), ("append", dict(latent_dim=128), EUNSUPPORTED),
+    ("append", dict(total_q=1 << 40), EINVAL), ("append", dict(norm_eps=1e300), EINVAL), ("append", dict(n_heads=2.5), EINVAL),
+    ("read", dict(k_rope_out=FAKE + 8), EINVAL), ("read", dict(rope_dim=32), EUNSUPPORTED), ("read", dict(total=-1), EINVAL),
+    ("attend", dict(workspace=FAKE + 128), EINVAL), ("attend", dict(workspace_bytes=-1), EINVAL),
+    ("attend", dict(scale=float("nan")), EINVAL), ("attend", dict(max_q=-1), EINVAL),
+], ids=str)
+def test_the_binding_refuses_what_the_calls_refuse(name, kw, status):
+    name = "attn_latent_" + name
+    args = dict(GOOD[name], stream=0)
+    getattr(attn, name)(*[args[k] for k in ORDER[name].split()])
+    args.update(kw)
+    with pytest.raises(attn.AttnError) as e:
+        getattr(attn, name)(*[args[k] for k in ORDER[name].split()])
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("name", ["attn_latent_append", "attn_latent_read", "attn_latent_attend"])
+def test_a_missing_struct_is_refused(name):
+    assert getattr(attn.load(), name + "_from")(None) == EINVAL
