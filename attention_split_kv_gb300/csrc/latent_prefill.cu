@@ -25,7 +25,8 @@
 // A block of at most 128 queries has one row tile, which would wait for its own softmax.  Its even
 // and odd key tiles are two streams instead, in the places of the two row tiles, each with its own
 // maximum, sum and O; the first stream's warps join them at the end.  (100 queries of 16 heads over
-// 4096 keys 51.4 to 35.9 us, one query of 2 heads over 8000 keys 95 to 64.)
+// 4096 keys 51.4 to 35.9 us, one query of 2 heads over 8000 keys 95 to 64.)  Where blocks of 256 would
+// not fill the SMs, all blocks are of 128.
 //
 // What bounds it: a row tile's chain.  From S to the next S of the same row tile (430 cycles until
 // the softmax has it, 230 to load it, 1550 for its weights, 180 until PV is issued, 540 and 680 of
@@ -75,7 +76,8 @@ struct Args {
     float* lse;
     const int32_t *q_start, *kv_start;
     int total_q, total_kv, max_q, H, causal;
-    int B, blocks;   // sequences, blocks of 256 queries of the longest
+    int B, blocks;   // sequences, blocks of the longest
+    int rows;        // queries of a block: 128 or 256
     int ranked;      // the grid's CTAs take (sequence, block) pairs longest first
     float scale;
     int* err;
@@ -446,7 +448,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     auto bar = [&](int i) { return sbase + OFF_BAR + i * 8; };
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-    // Heads fastest, then blocks of 256 queries: of few sequences all of them ranked by the work
+    const int rows = STREAMS ? a.rows : 2 * BM;   // of a block
+    // Heads fastest, then blocks of 256 (or 128) queries: of few sequences all of them ranked by the work
     // they are, the most first (8 chunks of 33 to 700 tokens over 739 to 3900: 103 us in the
     // sequences' order), else sequence by sequence from the last block (the longest when causal).
     int h = blockIdx.x, b = blockIdx.z, block = static_cast<int>(gridDim.y - 1 - blockIdx.y);
@@ -455,11 +458,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const int n_pairs = a.B * a.blocks, want = static_cast<int>(blockIdx.x) / a.H;
         int mine = -1;                           // no queries: last
         if (tid < n_pairs) {
-            const int bb = tid / a.blocks, first = tid % a.blocks * 2 * BM;
+            const int bb = tid / a.blocks, first = tid % a.blocks * rows;
             const int all = max(a.q_start[bb + 1] - a.q_start[bb], 0), keys = max(a.kv_start[bb + 1] - a.kv_start[bb], 0);
             const int nq = min(all, a.max_q);
             if (first < nq) {
-                const int end = min(first + 2 * BM, nq);
+                const int end = min(first + rows, nq);
                 const int hi = a.causal ? max(min(keys, keys - all + end), 0) : keys;
                 mine = (hi / BN + 1) * (end - first > BM ? 2 : 1);   // (a key tile for one row tile: half the time)
             }
@@ -482,7 +485,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const int q_base = a.q_start[b], k_base = a.kv_start[b];
     const int n_all = max(a.q_start[b + 1] - q_base, 0), L = max(a.kv_start[b + 1] - k_base, 0);
     const int n_q = min(n_all, a.max_q);
-    const int q0 = block * 2 * BM;
+    const int q0 = block * rows;
     if (q0 >= n_q) return;                       // a shorter sequence: no queries for this CTA
     const int pos0 = L - n_all;                  // position of query 0
     // key tiles of each row tile (at least one where it has rows)
@@ -491,7 +494,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     for (int t = 0; t < 2; ++t) {
         const int first = q0 + t * BM, last = min(first + BM, n_q) - 1;
         const int hi = a.causal ? max(min(L, pos0 + last + 1), 0) : L;
-        n_tiles[t] = first < n_q ? max((hi + BN - 1) / BN, 1) : 0;
+        n_tiles[t] = first < n_q && t * BM < rows ? max((hi + BN - 1) / BN, 1) : 0;
     }
     const int n_keys = max(n_tiles[0], n_tiles[1]);
     const bool split = STREAMS && n_tiles[1] == 0 && n_keys > 1;
@@ -545,11 +548,15 @@ attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
     if ((st = rows_map(&tk, L.k, HD, L.H, L.total_kv, L.k_head_stride, L.k_stride)) != ATTN_OK) return st;
     if ((st = rows_map(&tv, L.v, HD, L.H, L.total_kv, L.v_head_stride, L.v_stride)) != ATTN_OK) return st;
     if ((st = rows_map(&tr, L.k_rope, RD, 1, L.total_kv, RD, L.k_rope_stride)) != ATTN_OK) return st;
-    // A lone sequence of more than a row tile has at most one short block, beside full ones that take
-    // longer, and runs faster without the streams' code (8192 tokens of 16 heads 217 us, with it 225; 300
-    // queries over 4096 keys 58 and 62).  All others with it: 8 ragged chunks 78.6 us, without 79.5; one
-    // sequence of 100 queries over 4096 keys 36 and 51, of one query over 8000 64 and 95.
-    const bool streams = L.B > 1 || L.max_q <= BM;
+    // Blocks of 256 queries that do not fill the SMs are halved, each half with its keys in two streams (one
+    // sequence of 16 heads: 300 queries over 4096 keys 61 to 37 us, a prompt of 1024 tokens 21 to 15, of 2048
+    // 36 to 28; of 3000, 192 blocks, 49 to 51, and 8 ragged chunks, 304 blocks, 69 to 71).
+    const long long most = (static_cast<long long>(L.total_q) / (2 * BM) + L.B) * L.H;
+    const int rows = most <= sm_count() ? BM : 2 * BM;
+    // A lone sequence of more blocks has at most one short one, beside full ones that take longer, and runs
+    // faster without the streams' code (8192 tokens of 16 heads 217 us, with it 225); several with it (8
+    // ragged chunks 78.6 us, without 79.5).
+    const bool streams = rows == BM || L.B > 1 || L.max_q <= BM;
     auto kernel = streams ? latent_prefill_kernel<true> : latent_prefill_kernel<false>;
     static bool attr_set[2][64] = {};
     int dev = 0;
@@ -572,12 +579,13 @@ attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
     a.scale = L.scale;
     a.err = L.err_word;
     a.B = L.B;
-    a.blocks = (L.max_q - 1) / (2 * BM) + 1;
+    a.rows = rows;
+    a.blocks = (L.max_q - 1) / rows + 1;
     a.ranked = L.B > 1 && static_cast<long long>(L.B) * a.blocks <= kMaxRanked;
     const dim3 grid = a.ranked ? dim3(L.B * a.blocks * L.H) : dim3(L.H, a.blocks, L.B);
     if (trace_enabled())
-        trace("latent_prefill_kernel grid=(%u,%u,%u) block=%d smem=%u tmem_cols=%u total_q=%d total_kv=%d H=%d causal=%d ranked=%d streams=%d",
-              grid.x, grid.y, grid.z, kThreads, SMEM_ALLOC, TMEM_COLS, L.total_q, L.total_kv, L.H, L.causal, a.ranked, (int)streams);
+        trace("latent_prefill_kernel grid=(%u,%u,%u) block=%d smem=%u tmem_cols=%u total_q=%d total_kv=%d H=%d causal=%d ranked=%d streams=%d rows=%d",
+              grid.x, grid.y, grid.z, kThreads, SMEM_ALLOC, TMEM_COLS, L.total_q, L.total_kv, L.H, L.causal, a.ranked, (int)streams, rows);
     kernel<<<grid, kThreads, SMEM_ALLOC, L.stream>>>(tq, tk, tr, tv, a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(ATTN_ECUDA, "latent prefill launch failed: %s", cudaGetErrorString(e));

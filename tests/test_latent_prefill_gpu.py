@@ -167,3 +167,66 @@ def test_a_nan_query_stays_in_its_row(n):
     good = torch.ones(n, 3, dtype=torch.bool)
     good[7, 1] = good[40, 2] = False
     assert_within(out[good], ref[good], bound[good])
+
+
+# Blocks of 256 queries are taken where they fill the SMs: sequences without tokens behind the others (ranked, and
+# too many to be ranked), or one sequence of many heads.
+WIDE = [
+    ([256], [256]), ([300], [700]), ([129, 1], [129, 400]), ([1, 0, 130, 257, 5], [1, 9, 130, 400, 128]),
+    ([513, 255], [513, 511]), ([700], [64]),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", WIDE, ids=str)
+@pytest.mark.parametrize("H,seqs", [(16, 12), (1, 200)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_blocks_of_256(q_lens, kv_lens, H, seqs, causal):
+    more = [0] * (seqs - len(q_lens))
+    _check(*_inputs(q_lens, kv_lens, H, tail=3), q_lens + more, kv_lens + more, causal=causal)
+
+
+@pytest.mark.parametrize("n,L", [(129, 129), (256, 300), (300, 700), (600, 513)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_blocks_of_256_of_one_sequence(n, L, causal):
+    _check(*_inputs([n], [L], 160, tail=2), [n], [L], causal=causal)
+
+
+@pytest.mark.parametrize("n,H", [(300, 160), (300, 20)])
+def test_logits_that_keep_growing_in_both_row_tiles(n, H):
+    q, k, v, r = _inputs([n], [900], H)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    d = torch.randn(192, generator=g, device="cuda")
+    d /= d.norm()
+    rows = torch.arange(900, device="cuda")[:, None] / 128.0 * 12.0 / (SCALE * 14.0) * d
+    k.copy_((rows[:, None, :128] + 0.3 * torch.randn(k.shape, generator=g, device="cuda")).half())
+    r.copy_((rows[:, 128:] + 0.3 * torch.randn(r.shape, generator=g, device="cuda")).half())
+    q.copy_((14.0 * d + 0.2 * torch.randn(q.shape, generator=g, device="cuda")).half())
+    _check(q, k, v, r, [n], [900])
+
+
+@pytest.mark.parametrize("n,H", [(300, 160), (300, 3)])
+def test_rows_behind_a_long_sequence_and_nan_queries(n, H):
+    q, k, v, r = _inputs([n], [700], H, tail=80)
+    ref, _, bound = prefill_reference(q[:n], k, v, r, [n], [700], SCALE)
+    for t in (k, v, r):
+        t[700:] = math.nan
+    q[7, 1, 5], q[260, 2, 150] = math.nan, math.inf
+    st = starts([n], "cuda"), starts([700], "cuda")
+    out = attn.latent_prefill(q, k, v, r, *st, n, SCALE)[:n]
+    assert bool(out[7, 1].isnan().all()) and bool(out[260, 2].isnan().all())
+    good = torch.ones(n, H, dtype=torch.bool)
+    good[7, 1] = good[260, 2] = False
+    assert_within(out[good], ref[good], bound[good])
+
+
+@pytest.mark.parametrize("n,H", [(300, 160), (300, 16)])
+def test_a_timeout_in_either_block_size(n, H):
+    q, k, v, r = _inputs([n], [n], H)
+    st = starts([n], "cuda")
+    assert attn.attn_testing_set_waits(20_000_000, 1) == attn.ATTN_OK
+    try:
+        attn.latent_prefill(q, k, v, r, st, st, n, SCALE)
+        assert attn.attn_device_status() == attn.ATTN_ETIMEOUT
+    finally:
+        assert attn.attn_testing_set_waits(0, 0) == attn.ATTN_OK
+    _check(q, k, v, r, [n], [n])
