@@ -217,3 +217,24 @@ def test_trace_names_the_form():
     lines = [x for x in r.stderr.splitlines() if x.startswith("[libattn]")]
     assert ["latent_pair_kernel " in x for x in lines] == [True, False, False, False, False, True, False, True]
     assert "side=1" in lines[0] and "side=3" in lines[5]
+
+
+def test_steps_of_append_and_attend():
+    # each step's q and cache rows are written by the append directly before, q in place of the last step's
+    H, B = 128, 16
+    lens = [3, 700, 64, 1500] * 4
+    room = si.make_latent_case([n + 8 for n in lens], 512, 3, page_size=32, cap=ROOM, device="cuda")
+    start = starts([1] * B, "cuda")
+    q = si.f16_normal((B, H, 576), 9, "cuda")
+    outs = []
+    for step in range(6):
+        c = si.f16_normal((B, 512), 20 + step, "cuda")
+        kr, qr = si.f16_normal((B, 64), 40 + step, "cuda"), si.f16_normal((B, H, 64), 60 + step, "cuda")
+        kv_len = torch.tensor([n + 1 + step for n in lens], dtype=torch.int32, device="cuda")
+        attn.latent_append(room, c, kr, start, kv_len=kv_len, q_rope=qr, q_out=q[..., 512:])
+        outs.append((attn.latent_attend(room, q, start, 1, kv_len=kv_len), q.clone(), kv_len, c, kr, qr))
+    for out, used, kv_len, c, kr, qr in outs:
+        assert torch.equal(used[..., 512:], qr)
+        room.kv_len = kv_len
+        ref, _, bound = attend_reference(room, used, [1] * B)
+        assert_within(out, ref, bound)
