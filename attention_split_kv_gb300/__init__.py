@@ -45,7 +45,8 @@ exported_symbols = ("attn_version", "attn_last_error", "attn_decode_workspace_si
                     "attn_device_status", "attn_testing_set_waits", "attn_prefill_paged_ex",
                     "attn_prefill_paged_workspace_size", "attn_append", "attn_kv_read", "attn_latent_append",
                     "attn_latent_read", "attn_latent_workspace_size", "attn_latent_attend", "attn_latent_prefill",
-                    "attn_latent_append_from", "attn_latent_read_from", "attn_latent_attend_from")
+                    "attn_latent_append_from", "attn_latent_read_from", "attn_latent_attend_from",
+                    "attn_latent_prefill_from")
 
 
 class AttnLibraryMissing(RuntimeError):
@@ -116,7 +117,8 @@ def load():
     lib.attn_latent_read.restype = I
     lib.attn_latent_attend.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, F, P, P, P, SZ, P]
     lib.attn_latent_attend.restype = I
-    for f in (lib.attn_latent_append_from, lib.attn_latent_read_from, lib.attn_latent_attend_from):
+    for f in (lib.attn_latent_append_from, lib.attn_latent_read_from, lib.attn_latent_attend_from,
+              lib.attn_latent_prefill_from):
         f.argtypes = [ctypes.c_char_p]   # (the bytes of an argument struct)
         f.restype = I
     lib.attn_latent_workspace_size.argtypes = [I, I, I, I]
@@ -565,11 +567,12 @@ def kv_read(case, out_start, total, first=None, kv_len=None, out_f32=False, stre
 
 
 # ---------------------------------------------------------------- latent attention
-# The argument structs of the calls that serve single tokens, packed in one step: each argument on its own
-# costs a ctypes call 0.15 us and as much again in Python (32 of them: 13 us a call, packed 4).
+# The calls' argument structs, packed in one step: each argument on its own costs a ctypes call 0.15 us and as
+# much again in Python (32 of them: 13 us a call, packed 3.6).
 _LATENT_APPEND_ARGS = struct.Struct("@3Pi4qP2f2P2i4P9iP2qP")
 _LATENT_READ_ARGS = struct.Struct("@5P8i2PiP")
 _LATENT_ATTEND_ARGS = struct.Struct("@5P10if3PNP")
+_LATENT_PREFILL_ARGS = struct.Struct("@4P6q2P8if3P")
 
 
 def _addr(x) -> int:
@@ -621,11 +624,10 @@ def attn_latent_attend(q, cache, q_start, kv_len, page_table, page_size, max_pag
 def attn_latent_prefill(q, k, v, k_rope, q_stride, k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride,
                         q_start, kv_start, batch, total_q, total_kv, max_q, n_heads, head_dim, rope_dim, causal, scale,
                         out, lse_out=None, stream=None) -> None:
-    _check(load().attn_latent_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(k_rope), int(q_stride), int(k_stride),
-                                      int(k_head_stride), int(v_stride), int(v_head_stride), int(k_rope_stride),
-                                      _ptr(q_start), _ptr(kv_start), int(batch), int(total_q), int(total_kv),
-                                      int(max_q), int(n_heads), int(head_dim), int(rope_dim), int(bool(causal)),
-                                      float(scale), _ptr(out), _ptr(lse_out), _stream(stream)))
+    _check(load().attn_latent_prefill_from(_packed(
+        _LATENT_PREFILL_ARGS, _addr(q), _addr(k), _addr(v), _addr(k_rope), q_stride, k_stride, k_head_stride, v_stride,
+        v_head_stride, k_rope_stride, _addr(q_start), _addr(kv_start), batch, total_q, total_kv, max_q, n_heads,
+        head_dim, rope_dim, bool(causal), scale, _addr(out), _addr(lse_out), _stream(stream) or 0)))
 
 
 _ROPE = 64   # values of the rotated part of a latent cache's rows

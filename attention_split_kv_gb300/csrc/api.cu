@@ -1037,6 +1037,14 @@ attn_status attn_latent_attend_from(const attn_latent_attend_args* a) {
                               a->workspace_bytes, a->stream);
 }
 
+attn_status attn_latent_prefill_from(const attn_latent_prefill_args* a) {
+    if (!a) return set_error(ATTN_EINVAL, "attn_latent_prefill_from: args must be non-null");
+    return attn_latent_prefill(a->q, a->k, a->v, a->k_rope, a->q_stride, a->k_stride, a->k_head_stride, a->v_stride,
+                               a->v_head_stride, a->k_rope_stride, a->q_start, a->kv_start, a->batch, a->total_q,
+                               a->total_kv, a->max_q, a->n_heads, a->head_dim, a->rope_dim, a->causal, a->scale,
+                               a->out, a->lse_out, a->stream);
+}
+
 attn_status attn_decode_validate(const int32_t* kv_len, const int32_t* page_table, int batch, int page_size,
                                  int max_pages_per_seq, int n_pages, int max_kv, int* bad_seq, void* stream) {
     if (!kv_len || batch <= 0 || max_kv <= 0)

@@ -644,6 +644,19 @@ attn_status attn_latent_prefill(const void* q, const void* k, const void* v, con
                                 int head_dim, int rope_dim, int causal, float scale, void* out, float* lse_out,
                                 void* stream);
 
+/* The same with its arguments in a struct, in their order: what a binding can fill in one step. */
+typedef struct attn_latent_prefill_args {
+    const void *q, *k, *v, *k_rope;
+    long long q_stride, k_stride, k_head_stride, v_stride, v_head_stride, k_rope_stride;
+    const int32_t *q_start, *kv_start;
+    int batch, total_q, total_kv, max_q, n_heads, head_dim, rope_dim, causal;
+    float scale;
+    void* out;
+    float* lse_out;
+    void* stream;
+} attn_latent_prefill_args;
+attn_status attn_latent_prefill_from(const attn_latent_prefill_args* args);
+
 /*
  * attn_decode_validate -- synchronous check of the device-side decode inputs:
  * every kv_len[b] in [1, capacity] and every page id a sequence uses in

@@ -244,14 +244,13 @@ def _fields(name):
     return out
 
 
-@pytest.mark.parametrize("name", ["attn_latent_append", "attn_latent_read", "attn_latent_attend"])
+@pytest.mark.parametrize("name", sorted(GOOD))
 def test_argument_structs_lie_as_the_header_says(name, monkeypatch):
     fields = _fields(name)
     assert [f for f, _ in fields] == ORDER[name].split()
     Args = type("Args", (ctypes.Structure,), {"_fields_": fields})
     values = {f: (0.5 + i if t is ctypes.c_float else 64 * (i + 1)) for i, (f, t) in enumerate(fields)}
-    if "rope_interleaved" in values:
-        values["rope_interleaved"] = 1
+    values.update((f, 1) for f in ("rope_interleaved", "causal") if f in values)   # flags
     seen = []
 
     class Lib:
@@ -271,6 +270,7 @@ def test_argument_structs_lie_as_the_header_says(name, monkeypatch):
     ("read", dict(k_rope_out=FAKE + 8), EINVAL), ("read", dict(rope_dim=32), EUNSUPPORTED), ("read", dict(total=-1), EINVAL),
     ("attend", dict(workspace=FAKE + 128), EINVAL), ("attend", dict(workspace_bytes=-1), EINVAL),
     ("attend", dict(scale=float("nan")), EINVAL), ("attend", dict(max_q=-1), EINVAL),
+    ("prefill", dict(k_stride=1 << 64), EINVAL), ("prefill", dict(kv_start=None), EINVAL), ("prefill", dict(head_dim=64), EUNSUPPORTED),
 ], ids=str)
 def test_the_binding_refuses_what_the_calls_refuse(name, kw, status):
     name = "attn_latent_" + name
@@ -282,6 +282,6 @@ def test_the_binding_refuses_what_the_calls_refuse(name, kw, status):
     assert e.value.status == status
 
 
-@pytest.mark.parametrize("name", ["attn_latent_append", "attn_latent_read", "attn_latent_attend"])
+@pytest.mark.parametrize("name", sorted(GOOD))
 def test_a_missing_struct_is_refused(name):
     assert getattr(attn.load(), name + "_from")(None) == EINVAL
