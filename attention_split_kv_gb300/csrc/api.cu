@@ -1002,7 +1002,8 @@ attn_status attn_latent_prefill(const void* q, const void* k, const void* v, con
     L.B = batch;
     L.total_q = total_q;
     L.total_kv = total_kv;
-    L.max_q = max_q;
+    // (no sequence has more than all queries: a loose bound costs no blocks, and the grid stays within its limits)
+    L.max_q = max_q < total_q ? max_q : total_q;
     L.H = n_heads;
     L.causal = causal;
     L.scale = scale;
