@@ -15,7 +15,7 @@
 // so a tile of 64 keys comes from memory once and serves both products, few rows (one token of
 // 16 heads) cost products of N = 16 and not of 128 padded rows, and O^T of 512 values fits TMEM
 // for up to 64 rows (4 x 64 columns) beside two S.  A row's logits lie in four threads, so its
-// maximum and sum stay there; O is rescaled lazily (m within 2^8 of the row's maximum), a
+// maximum and sum stay there; O is rescaled lazily (a weight is at most 2^15), a
 // column a row, by all softmax warps.
 //
 // The S of a tile is made while the one before is in the softmax.  Tiles lie in a ring of halves
@@ -438,7 +438,7 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // rows keep the keys below lim; no row of the warp drops a key below all_keep
             const int lim_a = key_end(a, w.c, row0 + ra + 1), lim_b = key_end(a, w.c, row0 + rb + 1);
             const int all_keep = key_end(a, w.c, row0 + warp * 16 + 1);
-            // maxima in log2 units; +inf for what is not a row of the block: no weight
+            // offsets in log2 units; +inf for what is not a row of the block: no weight
             float m_a = ra < live ? -INFINITY : INFINITY, m_b = rb < live ? -INFINITY : INFINITY;
             float2 l_a = make_float2(0.f, 0.f), l_b = make_float2(0.f, 0.f);
             for (int j = 0; j < w.n; ++j, ++n_tile) {
@@ -491,8 +491,8 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             *reinterpret_cast<uint32_t*>(line + u + 8 * 128) = pb;
                         }
                     };
-                    // First against the running maxima, without the tile's: weights of a thread that sum to
-                    // at most 2^8 are each at most that.  A warp with any other (or a NaN, or a row that
+                    // First against the running offsets, without the tile's maxima: weights of a thread that sum to
+                    // at most 2^15 are each at most that.  A warp with any other (or a NaN, or a row that
                     // has kept no key so far) takes the tile's maxima.
                     float2 s_a, s_b;
                     bool fast = __all_sync(0xffffffffu, m_a != -INFINITY && m_b != -INFINITY);
@@ -517,16 +517,16 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
                         }
                         float f_a = 1.f, f_b = 1.f;
-                        const bool need_a = ta > m_a + kRescaleThreshold, need_b = tb > m_b + kRescaleThreshold;
+                        const bool need_a = ta - m_a > kRescaleThreshold, need_b = tb - m_b > kRescaleThreshold;
                         if (need_a) {
-                            f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - ta);
+                            f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - (ta - kLift));
                             l_a = fmul2(l_a, make_float2(f_a, f_a));
-                            m_a = ta;
+                            m_a = ta - kLift;
                         }
                         if (need_b) {
-                            f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - tb);
+                            f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - (tb - kLift));
                             l_b = fmul2(l_b, make_float2(f_b, f_b));
-                            m_b = tb;
+                            m_b = tb - kLift;
                         }
                         if ((lane & 3) == 0) {
                             factors[(n_tile & 1) * NR + ra] = f_a;

@@ -14,7 +14,7 @@
 // A row belongs to one CTA: 16 of each 32 rows (of a warp's lanes of TMEM) to CTA 0, the others to CTA
 // 1, so that the four warps that own rows are on all four schedulers (on two: 2260 cycles a tile).
 // Four more send the other rows' part of S to the peer, and four take what concerns the other rows'
-// O: they wait for their P and rescale their O if their maximum moved.
+// O: they wait for their P and rescale their O if their offset moved.
 //
 // What crosses to the peer goes without a release (one costs 1500 to 2300 cycles): S by st.async, 16 lines
 // of P by a copy of 2 KB, both counted in bytes on the peer's barriers (a copy arrives 900 cycles later;
@@ -450,7 +450,7 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                 // rows keep the keys below lim; no row of the warp drops a key below all_keep
                 const int lim_a = key_end(a, w.c, row0 + ra + 1), lim_b = key_end(a, w.c, row0 + rb + 1);
                 const int all_keep = key_end(a, w.c, row0 + first_row + 1);
-                // maxima in log2 units; +inf for what is not a row of the block: no weight
+                // offsets in log2 units; +inf for what is not a row of the block: no weight
                 float m_a = ra < live ? -INFINITY : INFINITY, m_b = rb < live ? -INFINITY : INFINITY;
                 float2 l_a = make_float2(0.f, 0.f), l_b = make_float2(0.f, 0.f);
                 for (int j = 0; j < w.n; ++j, ++n_tile) {
@@ -522,8 +522,8 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                             *reinterpret_cast<uint32_t*>(line + u + 8 * 128) = pb;
                         }
                     };
-                    // First against the running maxima, without the tile's: weights of a thread that sum to
-                    // at most 2^8 are each at most that.  A warp with any other (or a NaN, or a row that
+                    // First against the running offsets, without the tile's maxima: weights of a thread that sum to
+                    // at most 2^15 are each at most that.  A warp with any other (or a NaN, or a row that
                     // has kept no key so far) takes the tile's maxima.
                     float2 s_a, s_b;
                     float f_a = 1.f, f_b = 1.f;
@@ -547,16 +547,16 @@ latent_pair_kernel(const __half* q, const __grid_constant__ CUtensorMap tm_qr, c
                             ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
                             tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
                         }
-                        const bool need_a = ta > m_a + kRescaleThreshold, need_b = tb > m_b + kRescaleThreshold;
+                        const bool need_a = ta - m_a > kRescaleThreshold, need_b = tb - m_b > kRescaleThreshold;
                         if (need_a) {
-                            f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - ta);
+                            f_a = m_a == -INFINITY ? 0.f : ex2_approx(m_a - (ta - kLift));
                             l_a = fmul2(l_a, make_float2(f_a, f_a));
-                            m_a = ta;
+                            m_a = ta - kLift;
                         }
                         if (need_b) {
-                            f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - tb);
+                            f_b = m_b == -INFINITY ? 0.f : ex2_approx(m_b - (tb - kLift));
                             l_b = fmul2(l_b, make_float2(f_b, f_b));
-                            m_b = tb;
+                            m_b = tb - kLift;
                         }
                         moved = __any_sync(0xffffffffu, need_a || need_b) && j > 0;
                         // (a row that has kept no key yet: all of its weights are 0)

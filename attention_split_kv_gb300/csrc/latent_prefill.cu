@@ -24,7 +24,7 @@
 //
 // A block of at most 128 queries has one row tile, which would wait for its own softmax.  Its even
 // and odd key tiles are two streams instead, in the places of the two row tiles, each with its own
-// maximum, sum and O; the first stream's warps join them at the end.  (100 queries of 16 heads over
+// offset, sum and O; the first stream's warps join them at the end.  (100 queries of 16 heads over
 // 4096 keys 51.4 to 35.9 us, one query of 2 heads over 8000 keys 95 to 64.)  Where blocks of 256 would
 // not fill the SMs, all blocks are of 128.
 //
@@ -49,8 +49,11 @@ namespace {
 constexpr int BM = 128, BN = 128;           // rows of a row tile, keys of a key tile
 constexpr int HD = 128, RD = 64;            // a head's values, the rotated part's
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
-constexpr float kFastSumLimit = 256.0f;     // a row whose p sum to at most this has every p <= 2^8
+// A row's weights are 2^(logit - its offset) in f16: the offset lies kLift below the row's maximum when it is
+// set, and is set again when a logit passes it by kRescaleThreshold (log2 units).  So the largest weight is 2^7
+// to 2^15 (f16 holds 65504), and of the others what is above 2^-25 is kept, 2^-32 or less of the largest.
+constexpr float kLift = 7.0f, kRescaleThreshold = 15.0f;
+constexpr float kFastSumLimit = 32768.0f;   // a row whose p sum to at most this has every p <= 2^15
 constexpr int kSoftmaxWarps = 8, kTmaWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1;
 // 3 warpgroups: 8 softmax warps, then the TMA warp, the MMA warp and two that only make up the
 // third, which leaves registers to the others (launch: 384 x 168)
@@ -65,7 +68,7 @@ constexpr uint32_t OFF_Q = 0, OFF_RING = 2 * K_CHUNKS * kChunk, OFF_BAR = OFF_RI
 // done; the second stream's rows are there
 enum : int { B_Q, B_K = B_Q + 2, B_V = B_K + 2, B_KFREE = B_V + 2, B_VFREE = B_KFREE + 2, B_S = B_VFREE + 2, B_P = B_S + 2,
              B_DONE = B_P + 2, B_JOIN = B_DONE + 2, B_TEARDOWN, N_BARS };
-constexpr uint32_t OFF_ML = (OFF_BAR + N_BARS * 8 + 15) / 16 * 16;   // the second stream's maxima and sums
+constexpr uint32_t OFF_ML = (OFF_BAR + N_BARS * 8 + 15) / 16 * 16;   // the second stream's offsets and sums
 constexpr uint32_t OFF_MISC = OFF_ML + BM * 8, SMEM_ALLOC = OFF_MISC + 8 + 1024;
 constexpr uint32_t COL_O = 2 * BN, TMEM_COLS = 512;
 static_assert(SMEM_ALLOC <= 232448, "shared memory budget");
@@ -280,7 +283,7 @@ __device__ __forceinline__ void run_roles(const CUtensorMap& tm_q, const CUtenso
         // logits are raw products times scale > 0 in the exponent; another scale goes in first
         const bool raw = a.scale > 0.f;
         const float to_log2 = raw ? a.scale * kLog2e : 1.f;
-        float m = -INFINITY, l = 0.f;      // m: of the products times to_log2
+        float m = -INFINITY, l = 0.f;      // m: the offset, of the products times to_log2
         bool ok = true;
         for (int i = 0; i < my_tiles; ++i) {
             const int j = key_tile(t, i);
@@ -327,8 +330,8 @@ __device__ __forceinline__ void run_roles(const CUtensorMap& tm_q, const CUtenso
                 }
                 return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
             };
-            // First against the running maximum, without the tile's: a warp with a row whose
-            // weights sum to more than 2^8 (or a NaN, or no key so far) takes the tile's maximum.
+            // First against the running offset, without the tile's maximum: a warp with a row whose
+            // weights sum to more than 2^15 (or a NaN, or no key so far) takes that.
             bool fast = false;
             if (__all_sync(0xffffffffu, m != -INFINITY)) {
                 const float s = exps(m);
@@ -337,13 +340,13 @@ __device__ __forceinline__ void run_roles(const CUtensorMap& tm_q, const CUtenso
             }
             if (!fast) {
                 const float top = row_max(x) * to_log2;
-                const bool need = top > m + kRescaleThreshold || (m == -INFINITY && top > -INFINITY);
+                const bool need = top - m > kRescaleThreshold;   // (no key so far: m -inf)
                 const bool rescale = __any_sync(0xffffffffu, need) && i > 0;
                 float alpha = 1.f;
                 if (need) {
-                    alpha = m == -INFINITY ? 0.f : ex2_approx(m - top);
+                    alpha = m == -INFINITY ? 0.f : ex2_approx(m - (top - kLift));
                     l *= alpha;
-                    m = top;
+                    m = top - kLift;
                 }
                 l += exps(m == -INFINITY ? 0.f : m);
                 if (rescale) {

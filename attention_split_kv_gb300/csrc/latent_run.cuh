@@ -17,8 +17,12 @@ namespace {
 
 constexpr int BN = 64;                      // keys of a tile
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;   // log2 units: P stays at most 2^8
-constexpr float kFastSumLimit = 256.0f;     // weights that sum to at most this are at most 2^8
+// A row's weights are 2^(logit - its offset), in f16 for the second product.  The offset lies kLift below the
+// row's maximum when it is set, and is set again when a logit passes it by kRescaleThreshold (log2 units): the
+// largest weight is 2^7 to 2^15 (f16 holds 65504), and of the others what is above 2^-25 is kept, 2^-32 or less
+// of the largest.  (At offset 0 it was 2^-25: one key beside 65 thousand of e^-18 each lost all of their 0.1%.)
+constexpr float kLift = 7.0f, kRescaleThreshold = 15.0f;
+constexpr float kFastSumLimit = 32768.0f;   // weights that sum to at most this are at most 2^15
 constexpr int kMaxCtas = 152;               // one CTA an SM
 constexpr int kWholeTiles = 4;              // items of at most this many tiles are not cut
 constexpr uint32_t kChunk = BN * 128;       // bytes of 64 values of a tile

@@ -592,7 +592,8 @@ attn_status attn_latent_read_from(const attn_latent_read_args* args);
  *  kv_len are never used, whatever they hold; a NaN or an infinity in a chunk's own token may
  *  reach the rows of the tokens before it.  The tokens of a page id outside the pool are zeros,
  *  and it is reported through attn_device_status (ATTN_EBOUNDS).  The weights are rounded to
- *  f16, relative to about their row's largest, and summed as rounded.
+ *  f16, 11 bits down to 2^-21 of their row's largest and to steps of 2^-31 of it below, and
+ *  summed as rounded.
  */
 size_t attn_latent_workspace_size(int batch, int max_q, int n_heads, int latent_dim);
 attn_status attn_latent_attend(const void* q, const void* cache, const int32_t* q_start, const int32_t* kv_len,
@@ -635,7 +636,7 @@ attn_status attn_latent_attend_from(const attn_latent_attend_args* args);
  *                left alone.
  *  A query that keeps no key is a row of zeros, lse -inf.  Rows behind a sequence's keys are
  *  never used for it, whatever they hold; a NaN or an infinity in a token may reach the rows of
- *  the tokens before it.
+ *  the tokens before it.  The weights are rounded as attn_latent_attend's are.
  */
 attn_status attn_latent_prefill(const void* q, const void* k, const void* v, const void* k_rope, long long q_stride,
                                 long long k_stride, long long k_head_stride, long long v_stride,
