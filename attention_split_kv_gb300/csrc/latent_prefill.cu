@@ -78,7 +78,7 @@ struct Args {
     __half* out;
     float* lse;
     const int32_t *q_start, *kv_start;
-    int total_q, total_kv, max_q, H, causal;
+    int total_q, max_q, H, causal;
     int B, blocks;   // sequences, blocks of the longest
     int rows;        // queries of a block: 128 or 256
     int ranked;      // the grid's CTAs take (sequence, block) pairs longest first
@@ -575,7 +575,6 @@ attn_status launch_latent_prefill(const LatentPrefillLaunch& L) {
     a.q_start = L.q_start;
     a.kv_start = L.kv_start;
     a.total_q = L.total_q;
-    a.total_kv = L.total_kv;
     a.max_q = L.max_q;
     a.H = L.H;
     a.causal = L.causal;
