@@ -19,8 +19,9 @@
 // column a row, by all softmax warps.
 //
 // The S of a tile is made while the one before is in the softmax.  Tiles lie in a ring of halves
-// that holds two or two and a half of them: a tile stays until its second product is done, so
-// with tiles of 128 keys the ring held one and the copies stood still meanwhile.
+// that holds four of them, or of 512 values two (64 or 32 rows) or two and a half (16): a tile stays
+// until its second product is done, so with tiles of 128 keys of 512 values the ring held one and the
+// copies stood still meanwhile.
 //
 // Persistent CTAs: the key tiles of all (sequence, row block) items, in that order, are cut
 // into equal runs, one a CTA; rows of items cut by a run's end go to the workspace and are
@@ -33,8 +34,9 @@
 // written by the softmax warps and 4 that do only that.
 //
 // What bounds it.  Few heads: memory.  One token of 32 sequences of 512 to 8192 (137 thousand
-// tokens of 576 values, 158 MB), 16 heads: 34.7 us with the join, 4.6 TB/s (23.3 us at a copy's
-// rate); of the rest about 4 us go by before the first tile is there, 4 in the join, and the CTAs
+// tokens of 576 values, 158 MB), 16 heads: 34.9 us with the join, 4.5 TB/s, of one cache again and again,
+// of which some stays in L2; 38.2 us, 4.1 TB/s, with eight caches in turn (23.3 us at a copy's rate).
+// Of the rest about 4 us go by before the first tile is there, 4 in the join, and the CTAs
 // end 3 apart.  64-row blocks: the tensor cores, whose M = 64 products run at half rate: a tile
 // takes 36 MMAs of 37 cycles and 16 of 47, 2080 in all, and comes by every 2600 to 3000, since
 // with 64 rows' Q the ring holds two tiles and a tile's chain (copy, S, softmax, PV) is 6000
@@ -220,9 +222,10 @@ latent_attend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         // chunk.  (The whole warp runs the code and one lane issues.)
         const uint32_t one = elect_one();
         // Row blocks taken side by side, or one, read the cache once: the lines are the first to leave L2,
-        // so that those of the partial rows stay, and some of the cache for the next step (32 sequences of
-        // 512 to 8192, 16 heads: 39.2 to 35.5 us; 128 heads: 65.0 to 61.8).  Row blocks that come by at other
-        // times want them longer (1 to 4 drafts of 16 x 32768: 139.5 to 141.3).
+        // so that those of the partial rows stay (32 sequences of 512 to 8192, eight caches in turn: 16 heads 38.6
+        // to 38.2 us, 128 heads, in pairs, 61.2 to 59.4), and some of a cache that the next call reads again (one
+        // cache: 38.5 to 36.9, 61.2 to 57.4).  Row blocks that come by at other times want them longer (1 to 4 drafts
+        // of 16 x 32768: 139.5 to 141.3).
         const uint64_t policy = a.n_rb <= a.side ? l2_policy_evict_first() : l2_policy_evict_normal();
         const int log_nb = a.log_nb, nb = 1 << log_nb, box_rows = BN >> log_nb, P = 1 << a.log2P;
         uint32_t n_half = 0, n_seg = 0, n_q = 0;   // (copies posted)
@@ -685,8 +688,12 @@ attn_status launch_latent_attend(const LatentAttendLaunch& L) {
     // start and to end (one GB300, here and in pairs: 32 sequences of 512 to 8192, 128 heads, 28 tiles an SM,
     // 61.4 and 57.3 us; 256 of 1024, 54 tiles, 124 and 110; a chunk of 512 tokens on 4096, 597 and 475; 8 sequences
     // of 4096, 7 tiles, 27.0 and 31.6; one of 3000 20.7 and 27.7; 256 latent values, 32 sequences of 4096: 33.7
-    // and 41.6).  Not chunks of one or two blocks, of which the shorter ones fill half a pair's (1 to 4 drafts of
-    // 32 heads of 16 x 32768: 141.7 and 145.5).  What the caches hold is not known here, only what they can.
+    // and 41.6).  The two cross at 16 to 18 tiles an SM (128 heads, equal lengths, four caches in turn; 10, 14, 18
+    // and 22 tiles: 32 sequences 35.7, 42.3, 48.1, 54.7 and 38.7, 43.3, 47.7, 52.3; 16 sequences 34.2, 40.3, 46.5, 52.8
+    // and 37.0, 42.0, 46.3, 50.8).  Not chunks of one or two blocks, of which the shorter ones fill half a pair's (1
+    // to 4 drafts of 32 heads of 16 x 32768: 141.7 and 145.5).  What the caches hold is not known here, only what
+    // they can: short sequences in a wide table take the pairs' longer start and end (32 of 512 tokens, 128 heads:
+    // 22.1 us in a table of 512, 26.4 in one of 32768).
     const long long blocks = L.B * p.n_rb;
     if (L.R == 512 && p.n_rb > (L.max_q == 1 ? 1 : 2) && blocks >= 32 &&
         blocks * ((L.cache.capacity + BN - 1) / BN) >= 16 * kMaxCtas)

@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(256) latent_append_kernel(const LatentAppendAr
 // ------------------------------------------------------------------ read back
 // A CTA takes `per` rows in a row: a lane each finds their places (a binary search over the
 // sequences), then all threads copy 16-byte pieces, several at a time before their stores.  Bound
-// by memory: 16 x 32768 tokens of 576 values to f16 178.6 us, 6.8 TB/s, what a copy takes; 37 tokens
-// 2.5 us.  Few rows (less than 8 CTAs an SM of 32) are spread, 4 a CTA.
+// by memory: 16 x 32768 tokens of 576 values to f16 179 us, 6.8 TB/s, what a copy takes, to f32 285 us,
+// 6.35 TB/s; 37 tokens 2.5 us.  Few rows (less than 8 CTAs an SM of 32) are spread, 4 a CTA.
 constexpr int kReadThreads = 256;
 constexpr int kReadMost = 32;    // rows of a CTA
 constexpr int kReadPieces = 4;   // pieces of a thread at a time

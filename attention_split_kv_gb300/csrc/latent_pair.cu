@@ -28,7 +28,8 @@
 // cores work 1150; with a quarter of the products, no exponentials and a quarter of the copies it is 1700.
 // Two tiles' P and S are under way at a time, and shared memory is full.  An owner's loop takes 2000 cycles
 // for 16 rows; 8 rows an owner (19 warps) made 128 heads 57 to 61 us, owners that take every second
-// tile 67.  32 sequences of 512 to 8192, 128 heads: 57.3 us, 660 TFLOP/s; a chunk of 512 tokens of 128 heads
+// tile 67.  32 sequences of 512 to 8192, 128 heads: 57.4 us, 660 TFLOP/s (59.4 with eight caches in turn, of which
+// nothing stays in L2 from call to call); a chunk of 512 tokens of 128 heads
 // on 4096: 475 us, 1180 TFLOP/s.
 //
 // Roles (15 warps): 4 owners, 4 senders, 4 that wait for the peer's P (and load Q into TMEM), a TMA warp,

@@ -31,7 +31,9 @@
 // What bounds it: a row tile's chain.  From S to the next S of the same row tile (430 cycles until
 // the softmax has it, 230 to load it, 1550 for its weights, 180 until PV is issued, 540 and 680 of
 // products) is 3600, for 2560 of products of both; 8192 tokens of 16 heads take 217 us, 1584
-// TFLOP/s (83% of what a library's large product reaches here), tensor pipe 68%.  Rows shared by
+// TFLOP/s (84% of what a library's large product reaches here), tensor pipe 68%, in runs of 20 calls; under
+// the power cap, which brings the SMs from 2070 to 1720 MHz, 237 us, 1450 TFLOP/s (86% of the library's there),
+// and 240 with six inputs in turn.  Rows shared by
 // two threads, 16 softmax warps, made it 243; a barrier a chunk instead of a tile (12 waits and 7
 // commits a turn, not 4 and 4) 231; waits with a suspend-time hint 226.
 //

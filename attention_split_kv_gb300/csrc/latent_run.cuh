@@ -361,8 +361,9 @@ void fill_args(const LatentAttendLaunch& L, const Plan& p, Args& a) {
     // finds the cache's rows in L2
     a.side = L.max_q == 1 && p.n_rb <= 8 ? static_cast<int>(p.n_rb) : 1;
     a.scale = L.scale;
-    // Short caches: items of few tiles are not cut, and nothing is to be joined (one token over 128
-    // keys 9.1 us, 6.9 without the second kernel)
+    // Short caches: items of few tiles are not cut, and nothing is to be joined.  That goes by what the cache
+    // can hold, since the lengths are not known here (one token over 128 keys: 6.7 us in a table of 256
+    // tokens, 9.6 with the second kernel in one of 32768)
     a.whole = a.capacity <= kWholeTiles * BN;
 }
 
